@@ -166,6 +166,67 @@ int moe_router(const moe_dims* dims, int32_t T, const void* x, const float* rout
                const float* pre_norm_gain, int32_t* topk_idx, float* topk_w,
                void* ws, size_t ws_bytes, void* stream);
 
+/* ---- Training the router -------------------------------------------------
+ *
+ * A training step calls moe_router_logits (the routing, with the logits kept),
+ * the experts and moe_combine as above, moe_balance_loss on the logits and the
+ * picks, moe_balance_loss_grad for the loss's gradient in the logits, and
+ * moe_router_grad with that gradient and the routing weights' (d_topk_w[t,k] =
+ * the gradient of the layer's output against expert k's output for token t).
+ * token_mask: uint8 [T], 0 for a token that does not count (padding), or NULL
+ * when all do; the rows of such tokens in every [T, ...] input may hold
+ * anything, NaN too, and their rows of every [T, ...] gradient are zero.
+ * A slot whose topk_idx lies outside [0, E) takes part in nothing; an id that
+ * occurs twice in a token's picks counts twice.  Logits of counted tokens are
+ * finite or -inf (an expert switched off for that token: probability and
+ * gradient 0; a row of -inf only contributes nothing but its count).
+ * T == 0 is not a no-op for what sums over tokens: losses, counts and parameter
+ * gradients are then written as zeros.  Sums run in fp32 in an order fixed by
+ * the sizes, without atomics on floats: results repeat bit for bit.
+ *
+ * moe_router_logits: moe_router, with its logits [T,E] (fp32) as an output.
+ * The routing is that of moe_router, bit for bit. */
+int moe_router_logits(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
+                      const float* router_scale, const float* per_expert_scale,
+                      const float* pre_norm_gain, int32_t* topk_idx, float* topk_w,
+                      float* logits, void* ws, size_t ws_bytes, void* stream);
+
+/* Balance loss, z-loss and per-expert counts of a batch.  With N the number of
+ * tokens that count, p_t = softmax(logits_t), n_e the counted slots of expert e:
+ *   balance = E * sum_e (n_e / (N K)) * (1/N sum_t p_te)   (1 when both are even)
+ *   z       = 1/N sum_t (log sum_e exp logits_te)^2
+ * Outputs: loss [4] fp32 = {balance_coef * balance + z_coef * z, balance, z, N},
+ * expert_counts [E] int32 = n_e, mean_probs [E] fp32 = 1/N sum_t p_te.  N = 0
+ * gives zeros.  Only num_experts and top_k of dims matter. */
+int moe_balance_loss(const moe_dims* dims, int32_t T, const float* logits,
+                     const int32_t* topk_idx, const uint8_t* token_mask, float balance_coef,
+                     float z_coef, float* loss, int32_t* expert_counts, float* mean_probs,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* Gradient of *d_loss * loss[0] in the logits (the counts are constants):
+ * d_logits [T,E] fp32.  logits, token_mask, the coefficients as in
+ * moe_balance_loss, expert_counts and loss its outputs; d_loss one fp32 on the
+ * device.  d_logits may be logits (each row is read before it is written). */
+int moe_balance_loss_grad(const moe_dims* dims, int32_t T, const float* logits,
+                          const uint8_t* token_mask, const int32_t* expert_counts,
+                          const float* loss, float balance_coef, float z_coef,
+                          const float* d_loss, float* d_logits, void* stream);
+
+/* Backward pass of moe_router_logits: from the gradients of its outputs,
+ * d_topk_w [T,K] and d_logits [T,E] (fp32; either may be NULL for zero, not
+ * both), those of its inputs: d_x [T,H] act dtype (NULL: not wanted),
+ * d_router_w [E,H], d_router_scale [H], d_per_expert_scale [E],
+ * d_pre_norm_gain [H] (exactly when pre_norm_gain is given), all fp32, all
+ * overwritten.  The picks are constants; x, the parameters, logits and
+ * topk_idx are the forward call's.  No output may overlap an input. */
+int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
+                    const float* router_scale, const float* per_expert_scale,
+                    const float* pre_norm_gain, const float* logits, const int32_t* topk_idx,
+                    const uint8_t* token_mask, const float* d_topk_w, const float* d_logits,
+                    void* d_x, float* d_router_w, float* d_router_scale,
+                    float* d_per_expert_scale, float* d_pre_norm_gain, void* ws,
+                    size_t ws_bytes, void* stream);
+
 /* moe_router followed by moe_dispatch of its result, in one call (for small
  * batches the dispatch runs inside the router's top-K kernel).  Outputs are
  * those of the two calls. */

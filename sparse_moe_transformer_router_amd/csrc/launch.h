@@ -34,6 +34,67 @@ struct RouterArgs {
 hipError_t launch_router(const RouterArgs& a, hipStream_t s);
 bool router_fuses_dispatch(int T, int H, int E, int K);
 
+// Balance loss and z-loss of a batch's logits (router_train.hip): first step
+// in balance_blocks(T) blocks, whose sums the second step adds.
+struct BalanceArgs {
+  int T, E, K;
+  float balance_coef, z_coef;
+  const float* logits;      // [T,E]
+  const int32_t* topk_idx;  // [T,K]
+  const uint8_t* mask;      // [T] or nullptr: 0 = the token does not count
+  float* loss;              // [4]
+  int32_t* counts;          // [E]
+  float* mean_p;            // [E]
+  float* ws_part_p;         // [blocks,E]
+  int32_t* ws_part_n;       // [blocks,E]
+  float* ws_part_z;         // [blocks]
+  int32_t* ws_part_live;    // [blocks]
+};
+int balance_blocks(int T);
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t s);
+
+struct BalanceGradArgs {
+  int T, E, K;
+  float balance_coef, z_coef;
+  const float* logits;
+  const uint8_t* mask;
+  const int32_t* counts;
+  const float* loss;    // loss[3]: tokens that count
+  const float* d_loss;  // [1]
+  float* d_logits;      // [T,E]
+};
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s);
+
+// Router backward.  T == 0 writes zero parameter gradients.
+struct RouterGradArgs {
+  int T, H, E, K;
+  float eps;
+  bool x_bf16;
+  const void* x;                  // [T,H]
+  const float* router_w;          // [E,H]
+  const float* router_scale;      // [H]
+  const float* per_expert_scale;  // [E]
+  const float* pre_gain;          // [H] or nullptr
+  const float* logits;            // [T,E]
+  const int32_t* topk_idx;        // [T,K]
+  const uint8_t* mask;            // [T] or nullptr
+  const float* d_topk_w;          // [T,K] or nullptr
+  const float* d_logits;          // [T,E] or nullptr
+  void* d_x;                      // [T,H] or nullptr
+  float* d_router_w;              // [E,H]
+  float* d_router_scale;          // [H]
+  float* d_per_expert_scale;      // [E]
+  float* d_pre_gain;              // [H] or nullptr
+  float* ws_dl;                   // [T,E]
+  float* ws_beta;                 // [T]
+  float* ws_part_g;               // [splits,E,H]
+  float* ws_part_b;               // [splits,H]
+  float* ws_part_pes;             // [row blocks,E]
+};
+int router_grad_splits(int T);
+int router_grad_row_blocks(int T);
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
+
 struct DispatchArgs {
   int T, E, K;
   const int32_t* topk_idx;   // [T*K]

@@ -94,6 +94,10 @@ struct Layout {
   size_t counter;                   // small-batch top-K completion counter
   size_t base_end;                  // end of the regions above (all but the MXFP8 ones)
   size_t xq, xs, hq, hs;            // MXFP8 activations of the 8-bit / 4-bit experts
+  // The training calls' scratch shares the bytes past base_end with the MXFP8
+  // activations: a workspace serves one call at a time.
+  size_t bal_p, bal_n, bal_z, bal_live;      // balance loss
+  size_t rg_dl, rg_beta, rg_g, rg_b, rg_pes; // router backward
   size_t total;
 };
 
@@ -131,6 +135,22 @@ Layout layout(const moe_dims* d, long long T) {
   L.hq = take((size_t)S * d->expert_inter);
   L.hs = take((size_t)S * (d->expert_inter / 32));
   L.total = o;
+  const size_t E = (size_t)d->num_experts, H = (size_t)d->hidden;
+  const size_t nb = (size_t)moe::balance_blocks((int)T);
+  o = L.base_end;
+  L.bal_p = take(4 * nb * E);
+  L.bal_n = take(4 * nb * E);
+  L.bal_z = take(4 * nb);
+  L.bal_live = take(4 * nb);
+  if (o > L.total) L.total = o;
+  const size_t splits = (size_t)moe::router_grad_splits((int)T);
+  o = L.base_end;
+  L.rg_dl = take(4 * (size_t)T * E);
+  L.rg_beta = take(4 * (size_t)T);
+  L.rg_g = take(4 * splits * E * H);
+  L.rg_b = take(4 * splits * H);
+  L.rg_pes = take(4 * (size_t)moe::router_grad_row_blocks((int)T) * E);
+  if (o > L.total) L.total = o;
   return L;
 }
 
@@ -220,7 +240,7 @@ int run_forward(const moe_dims* dims, int32_t T, const void* x, const float* rou
 int run_router(const moe_dims* d, int32_t T, const void* x, const float* router_w,
                const float* router_scale, const float* pes, const float* pre_gain,
                int32_t* idx, float* w, int32_t* counts, int32_t* offsets, int32_t* sorted,
-               void* ws, hipStream_t s) {
+               void* ws, hipStream_t s, float* logits = nullptr) {
   const Layout L = layout(d, T);
   moe::RouterArgs a{};
   a.T = T; a.H = d->hidden; a.E = d->num_experts; a.K = d->top_k; a.eps = d->eps;
@@ -228,7 +248,7 @@ int run_router(const moe_dims* d, int32_t T, const void* x, const float* router_
   a.x = x; a.pre_gain = pre_gain; a.router_w = router_w; a.router_scale = router_scale;
   a.per_expert_scale = pes; a.topk_idx = idx; a.topk_w = w;
   a.ws_r0 = at<float>(ws, L.r0); a.ws_r = at<float>(ws, L.r);
-  a.ws_logits = at<float>(ws, L.logits);
+  a.ws_logits = logits ? logits : at<float>(ws, L.logits);
   a.ws_counter = at<unsigned>(ws, L.counter);
   a.counts = counts; a.offsets = offsets; a.sorted_slots = sorted;
   a.ws_blk_counts = at<int32_t>(ws, L.blk_counts);
@@ -495,6 +515,108 @@ int moe_route(const moe_dims* dims, int32_t T, const void* x, const float* route
   return run_router(dims, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain,
                     topk_idx, topk_w, expert_counts, expert_offsets, sorted_slots, ws,
                     static_cast<hipStream_t>(stream));
+}
+
+int moe_router_logits(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
+                      const float* router_scale, const float* per_expert_scale,
+                      const float* pre_norm_gain, int32_t* topk_idx, float* topk_w,
+                      float* logits, void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(router_w); REQUIRE_PTR(router_scale);
+  REQUIRE_PTR(per_expert_scale); OPTIONAL_PTR(pre_norm_gain);
+  REQUIRE_PTR(topk_idx); REQUIRE_PTR(topk_w); REQUIRE_PTR(logits);
+  if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+  return run_router(dims, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain,
+                    topk_idx, topk_w, nullptr, nullptr, nullptr, ws,
+                    static_cast<hipStream_t>(stream), logits);
+}
+
+int moe_balance_loss(const moe_dims* dims, int32_t T, const float* logits,
+                     const int32_t* topk_idx, const uint8_t* token_mask, float balance_coef,
+                     float z_coef, float* loss, int32_t* expert_counts, float* mean_probs,
+                     void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  REQUIRE_PTR(loss); REQUIRE_PTR(expert_counts); REQUIRE_PTR(mean_probs);
+  if (T > 0) {
+    REQUIRE_PTR(logits); REQUIRE_PTR(topk_idx); OPTIONAL_PTR(token_mask);
+    if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+  }
+  const Layout L = layout(dims, T);
+  moe::BalanceArgs a{};
+  a.T = T; a.E = dims->num_experts; a.K = dims->top_k;
+  a.balance_coef = balance_coef; a.z_coef = z_coef;
+  a.logits = logits; a.topk_idx = topk_idx; a.mask = token_mask;
+  a.loss = loss; a.counts = expert_counts; a.mean_p = mean_probs;
+  a.ws_part_p = at<float>(ws, L.bal_p); a.ws_part_n = at<int32_t>(ws, L.bal_n);
+  a.ws_part_z = at<float>(ws, L.bal_z); a.ws_part_live = at<int32_t>(ws, L.bal_live);
+  hipError_t e = moe::launch_balance_loss(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_balance_loss");
+}
+
+int moe_balance_loss_grad(const moe_dims* dims, int32_t T, const float* logits,
+                          const uint8_t* token_mask, const int32_t* expert_counts,
+                          const float* loss, float balance_coef, float z_coef,
+                          const float* d_loss, float* d_logits, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(logits); OPTIONAL_PTR(token_mask); REQUIRE_PTR(expert_counts); REQUIRE_PTR(loss);
+  REQUIRE_PTR(d_loss); REQUIRE_PTR(d_logits);
+  moe::BalanceGradArgs a{};
+  a.T = T; a.E = dims->num_experts; a.K = dims->top_k;
+  a.balance_coef = balance_coef; a.z_coef = z_coef;
+  a.logits = logits; a.mask = token_mask; a.counts = expert_counts; a.loss = loss;
+  a.d_loss = d_loss; a.d_logits = d_logits;
+  hipError_t e = moe::launch_balance_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_balance_loss_grad");
+}
+
+int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
+                    const float* router_scale, const float* per_expert_scale,
+                    const float* pre_norm_gain, const float* logits, const int32_t* topk_idx,
+                    const uint8_t* token_mask, const float* d_topk_w, const float* d_logits,
+                    void* d_x, float* d_router_w, float* d_router_scale,
+                    float* d_per_expert_scale, float* d_pre_norm_gain, void* ws,
+                    size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  REQUIRE_PTR(router_w); REQUIRE_PTR(router_scale); OPTIONAL_PTR(pre_norm_gain);
+  REQUIRE_PTR(d_router_w); REQUIRE_PTR(d_router_scale); REQUIRE_PTR(d_per_expert_scale);
+  if (pre_norm_gain) {
+    REQUIRE_PTR(d_pre_norm_gain);
+  } else if (d_pre_norm_gain) {
+    return fail(MOE_ERR_ARG, "d_pre_norm_gain without pre_norm_gain");
+  }
+  if (T > 0) {
+    REQUIRE_PTR(x); REQUIRE_PTR(logits); OPTIONAL_PTR(token_mask); OPTIONAL_PTR(d_topk_w);
+    OPTIONAL_PTR(d_logits); OPTIONAL_PTR(d_x);
+    if (!d_topk_w && !d_logits) return fail(MOE_ERR_ARG, "d_topk_w and d_logits are both NULL");
+    if (d_topk_w) {
+      REQUIRE_PTR(topk_idx); REQUIRE_PTR(per_expert_scale);
+    }
+    if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+  }
+  const Layout L = layout(dims, T);
+  moe::RouterGradArgs a{};
+  a.T = T; a.H = dims->hidden; a.E = dims->num_experts; a.K = dims->top_k; a.eps = dims->eps;
+  a.x_bf16 = dims->act_dtype == MOE_BF16;
+  a.x = x; a.router_w = router_w; a.router_scale = router_scale;
+  a.per_expert_scale = per_expert_scale; a.pre_gain = pre_norm_gain; a.logits = logits;
+  a.topk_idx = topk_idx; a.mask = token_mask; a.d_topk_w = d_topk_w; a.d_logits = d_logits;
+  a.d_x = d_x; a.d_router_w = d_router_w; a.d_router_scale = d_router_scale;
+  a.d_per_expert_scale = d_per_expert_scale; a.d_pre_gain = d_pre_norm_gain;
+  a.ws_dl = at<float>(ws, L.rg_dl); a.ws_beta = at<float>(ws, L.rg_beta);
+  a.ws_part_g = at<float>(ws, L.rg_g); a.ws_part_b = at<float>(ws, L.rg_b);
+  a.ws_part_pes = at<float>(ws, L.rg_pes);
+  hipError_t e = moe::launch_router_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_router_grad");
 }
 
 int moe_dispatch(const moe_dims* dims, int32_t T, const int32_t* topk_idx,

@@ -1,0 +1,776 @@
+// Training side of the router (Gemma4TextRouter on the page "Porting a
+// 128-expert MoE (Gemma-4 26B-A4B) to AWS Inferentia2", section "The
+// architecture: a dual-path FFN nobody warned me about"): the balance loss and
+// z-loss of a batch with the tokens each expert received, the loss's gradient
+// in the logits, and the backward pass from the gradient of the routing
+// weights and logits to the router's input and parameters.
+//
+// Every sum runs in fp32 in an order fixed by the sizes alone (no
+// floating-point atomics), so results repeat bit for bit.  Counts are integers.
+#include <type_traits>
+
+#include "common.h"
+#include "launch.h"
+#include "route_dev.h"
+
+namespace moe {
+namespace {
+
+// ---------------------------------------------------------------------------
+// Reductions over the G = 8, 16, 32 or 64 lanes that share a token; every lane
+// of the group gets the result.  Within 16 lanes they are DPP moves (quad
+// permutes, then the mirrors of 8 and 16 lanes), past that lane shuffles.
+// ---------------------------------------------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp_f32(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+constexpr int kDppXor1 = 0xB1, kDppXor2 = 0x4E, kDppHalfMirror = 0x141, kDppMirror = 0x140;
+
+template <int G, typename F>
+__device__ __forceinline__ float group_reduce(float v, F f) {
+  static_assert(G == 8 || G == 16 || G == 32 || G == 64, "lanes per token");
+  v = f(v, dpp_f32<kDppXor1>(v));
+  v = f(v, dpp_f32<kDppXor2>(v));
+  v = f(v, dpp_f32<kDppHalfMirror>(v));
+  if constexpr (G >= 16) v = f(v, dpp_f32<kDppMirror>(v));
+  if constexpr (G >= 32) v = f(v, __shfl_xor(v, 16, kWave));
+  if constexpr (G >= 64) v = f(v, __shfl_xor(v, 32, kWave));
+  return v;
+}
+template <int G>
+__device__ __forceinline__ float group_sum(float v) {
+  return group_reduce<G>(v, [](float a, float b) { return a + b; });
+}
+template <int G>
+__device__ __forceinline__ float group_max(float v) {
+  return group_reduce<G>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// Four consecutive logits e0 .. e0 + 3 of a row; past the last expert -inf,
+// whose probability is 0.  VEC: E % 4 == 0, so every row is 16-byte aligned.
+template <bool VEC>
+__device__ __forceinline__ void load_logits4(const float* __restrict__ row, int e0, int E,
+                                             float (&l)[4]) {
+  if constexpr (VEC) {
+    if (e0 < E) {
+      const float4 v = *reinterpret_cast<const float4*>(row + e0);
+      l[0] = v.x; l[1] = v.y; l[2] = v.z; l[3] = v.w;
+      return;
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) l[j] = e0 + j < E ? row[e0 + j] : -INFINITY;
+}
+
+// Softmax numerators of a token's logits: l becomes exp(l - max), z their sum
+// over the group, lse the row's log-sum-exp.  A row of -inf only has no
+// probability anywhere: z is 0 and inv (1 / z) and lse are 0.
+template <int G>
+__device__ __forceinline__ void group_softmax(float (&l)[4], float& inv, float& lse) {
+  const float top = group_max<G>(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+  const bool none = top == -INFINITY;
+  float z = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    l[j] = none ? 0.0f : expf(l[j] - top);
+    z += l[j];
+  }
+  z = group_sum<G>(z);
+  inv = none ? 0.0f : 1.0f / z;
+  lse = none ? 0.0f : top + logf(z);
+}
+
+// ---------------------------------------------------------------------------
+// Balance loss, first step.  N live tokens (token_mask, or all of them):
+//   n_e = slots of live tokens routed to e,  f_e = n_e / (N K),
+//   P_e = 1/N sum_t softmax(l_t)_e,          lse_t = log sum_e exp l_te,
+//   balance = E sum_e f_e P_e,               z = 1/N sum_t lse_t^2.
+// Block b takes tokens [b * span, ...): G lanes a token, four experts a lane,
+// kept in registers over the block's tokens.  It writes its sums of P_e, its
+// counts, its sum of lse^2 and its number of live tokens; the second step adds
+// the blocks in order.  A batch of one block's size runs both steps in one
+// launch.
+// ---------------------------------------------------------------------------
+constexpr int kBalThreads = 512;
+constexpr int kBalWaves = kBalThreads / kWave;
+constexpr int kBalUnroll = 4;       // tokens a group loads before it adds the first
+constexpr int kBalOneBlock = 256;   // tokens that one block takes alone
+constexpr int kBalMaxBlocks = 256;  // one block per CU
+
+// loss[4] = {a * balance + b * z, balance, z, N}; mean_p = P.  Called by the
+// whole block with the summed values of expert tid (tid < E).
+__device__ __forceinline__ void balance_finish(int E, int K, float a, float b, float sum_p,
+                                               int count, float sum_z, int live,
+                                               float* __restrict__ loss,
+                                               int32_t* __restrict__ counts,
+                                               float* __restrict__ mean_p, float* red) {
+  const int tid = threadIdx.x;
+  const float inv = live > 0 ? 1.0f / (float)live : 0.0f;
+  float fp = 0.0f;
+  if (tid < E) {
+    const float p = sum_p * inv;
+    counts[tid] = count;
+    mean_p[tid] = p;
+    fp = ((float)count * (inv / (float)K)) * p;
+  }
+  fp = wave_sum(fp);  // E <= 256: the first four waves hold terms
+  if (lane_id() == 0) red[tid / kWave] = fp;
+  __syncthreads();
+  if (tid == 0) {
+    const float bal = (float)E * (((red[0] + red[1]) + red[2]) + red[3]);
+    const float z = sum_z * inv;
+    loss[0] = a * bal + b * z;
+    loss[1] = bal;
+    loss[2] = z;
+    loss[3] = (float)live;
+  }
+}
+
+template <int G, bool VEC>
+__global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
+    int T, int E, int K, int span, const float* __restrict__ logits,
+    const int32_t* __restrict__ topk_idx, const uint8_t* __restrict__ mask, float a, float b,
+    float* __restrict__ part_p, int32_t* __restrict__ part_n, float* __restrict__ part_z,
+    int32_t* __restrict__ part_live, float* __restrict__ loss, int32_t* __restrict__ counts,
+    float* __restrict__ mean_p) {
+  constexpr int TW = kWave / G;             // tokens per wave
+  constexpr int TB = TW * kBalWaves;        // tokens per block and round
+  __shared__ float sum_p[kBalWaves * TW][4 * G];
+  __shared__ int cnt[kBalWaves][kMaxE];
+  __shared__ float wave_z[kBalWaves];
+  __shared__ int wave_live[kBalWaves];
+  __shared__ float red[kBalWaves];
+  const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
+  const int gl = lane % G, grp = wave * TW + lane / G;
+  const int t0 = blockIdx.x * span, t1 = min(T, t0 + span);
+  for (int i = tid; i < kBalWaves * kMaxE; i += kBalThreads) (&cnt[0][0])[i] = 0;
+  __syncthreads();
+  // counts: the block's slots in order, one counter row per wave
+  for (int s = t0 * K + tid; s < t1 * K; s += kBalThreads) {
+    const int e = topk_idx[s];
+    if ((unsigned)e < (unsigned)E && (mask == nullptr || mask[s / K] != 0))
+      atomicAdd(&cnt[wave][e], 1);
+  }
+  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  float zsum = 0.0f;
+  int live = 0;
+  for (int t = t0 + grp; t < t1; t += TB * kBalUnroll) {
+    float l[kBalUnroll][4];
+    bool on[kBalUnroll];
+#pragma unroll
+    for (int u = 0; u < kBalUnroll; ++u) {
+      const int tu = min(t + u * TB, t1 - 1);
+      on[u] = t + u * TB < t1 && (mask == nullptr || mask[tu] != 0);
+      load_logits4<VEC>(logits + (size_t)tu * E, 4 * gl, E, l[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kBalUnroll; ++u) {
+      float inv, lse;
+      group_softmax<G>(l[u], inv, lse);
+      if (on[u]) {  // a masked row may hold anything
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += l[u][j] * inv;
+        zsum += lse * lse;
+        live += 1;
+      }
+    }
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j)
+    if (4 * gl + j < E) sum_p[grp][4 * gl + j] = acc[j];
+  // one lane of each group holds its tokens' sum
+  zsum = wave_sum(gl == 0 ? zsum : 0.0f);
+  live = wave_sum(gl == 0 ? live : 0);
+  if (lane == 0) {
+    wave_z[wave] = zsum;
+    wave_live[wave] = live;
+  }
+  __syncthreads();
+  float p = 0.0f, z = 0.0f;
+  int n = 0, nl = 0;
+  if (tid < E) {
+    for (int w = 0; w < kBalWaves * TW; ++w) p += sum_p[w][tid];
+    for (int w = 0; w < kBalWaves; ++w) n += cnt[w][tid];
+  }
+  for (int w = 0; w < kBalWaves; ++w) {
+    z += wave_z[w];
+    nl += wave_live[w];
+  }
+  if (gridDim.x == 1) {
+    balance_finish(E, K, a, b, p, n, z, nl, loss, counts, mean_p, red);
+    return;
+  }
+  if (tid < E) {
+    part_p[(size_t)blockIdx.x * E + tid] = p;
+    part_n[(size_t)blockIdx.x * E + tid] = n;
+  }
+  if (tid == 0) {
+    part_z[blockIdx.x] = z;
+    part_live[blockIdx.x] = nl;
+  }
+}
+
+// Second step: one block of 1024 threads adds the blocks' sums; expert e's nb
+// values are split over the thread rows, whose sums are added in order.
+constexpr int kBalFinThreads = 1024;
+__global__ __launch_bounds__(kBalFinThreads) void balance_final_kernel(
+    int nb, int E, int K, float a, float b, const float* __restrict__ part_p,
+    const int32_t* __restrict__ part_n, const float* __restrict__ part_z,
+    const int32_t* __restrict__ part_live, float* __restrict__ loss,
+    int32_t* __restrict__ counts, float* __restrict__ mean_p) {
+  __shared__ float sp[kBalFinThreads];
+  __shared__ int sn[kBalFinThreads];
+  __shared__ float wz[kBalFinThreads / kWave];
+  __shared__ int wl[kBalFinThreads / kWave];
+  __shared__ float red[kBalFinThreads / kWave];
+  const int tid = threadIdx.x;
+  const int rows = kBalFinThreads / E;  // E <= 256: four or more
+  const int e = tid % E, r = tid / E;
+  float p = 0.0f;
+  int n = 0;
+  if (r < rows)
+    for (int i = r; i < nb; i += rows) {
+      p += part_p[(size_t)i * E + e];
+      n += part_n[(size_t)i * E + e];
+    }
+  sp[tid] = p;
+  sn[tid] = n;
+  float z = tid < nb ? part_z[tid] : 0.0f;  // nb <= kBalMaxBlocks
+  int live = tid < nb ? part_live[tid] : 0;
+  z = wave_sum(z);
+  live = wave_sum(live);
+  if (lane_id() == 0) {
+    wz[tid / kWave] = z;
+    wl[tid / kWave] = live;
+  }
+  __syncthreads();
+  p = 0.0f;
+  n = 0;
+  if (tid < E)
+    for (int i = 0; i < rows; ++i) {
+      p += sp[i * E + tid];
+      n += sn[i * E + tid];
+    }
+  z = 0.0f;
+  live = 0;
+  for (int w = 0; w < kBalMaxBlocks / kWave; ++w) {
+    z += wz[w];
+    live += wl[w];
+  }
+  balance_finish(E, K, a, b, p, n, z, live, loss, counts, mean_p, red);
+}
+
+// Gradient of g * loss[0] in the logits, g = *d_loss:
+//   d l_tj = g [ a E / N p_tj (f_j - sum_e f_e p_te) + 2 b / N lse_t p_tj ],
+// 0 for masked tokens and for a row of -inf.  Memory-bound: the logits read
+// and the gradient written once; f_e of a lane's four experts in registers.
+constexpr int kGradUnroll = 2;
+template <int G, bool VEC>
+__global__ __launch_bounds__(256) void balance_grad_kernel(
+    int T, int E, int K, const float* logits, const uint8_t* __restrict__ mask,
+    const int32_t* __restrict__ counts, const float* __restrict__ loss, float a, float b,
+    const float* __restrict__ d_loss, float* d_logits) {  // d_logits may be logits
+  constexpr int TB = 256 / G;
+  const int gl = threadIdx.x % G, grp = threadIdx.x / G, e0 = 4 * gl;
+  const float n = loss[3];
+  const float inv_n = n > 0.0f ? 1.0f / n : 0.0f;
+  const float up = d_loss[0] * inv_n;
+  const float ca = up * a * (float)E, cb = 2.0f * up * b;
+  const float fs = inv_n / (float)K;
+  float f[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) f[j] = e0 + j < E ? (float)counts[e0 + j] * fs : 0.0f;
+  for (int t = blockIdx.x * TB * kGradUnroll + grp; t < T; t += gridDim.x * TB * kGradUnroll) {
+    float l[kGradUnroll][4];
+    bool on[kGradUnroll];
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      const int tu = min(t + u * TB, T - 1);
+      on[u] = mask == nullptr || mask[tu] != 0;
+      load_logits4<VEC>(logits + (size_t)tu * E, e0, E, l[u]);
+    }
+#pragma unroll
+    for (int u = 0; u < kGradUnroll; ++u) {
+      float inv, lse;
+      group_softmax<G>(l[u], inv, lse);
+      float pf = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        l[u][j] *= inv;
+        pf += l[u][j] * f[j];
+      }
+      pf = group_sum<G>(pf);
+      float d[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        d[j] = on[u] ? l[u][j] * (ca * (f[j] - pf) + cb * lse) : 0.0f;
+      if (t + u * TB < T && e0 < E) {
+        float* dst = d_logits + (size_t)(t + u * TB) * E + e0;
+        if constexpr (VEC) {
+          *reinterpret_cast<float4*>(dst) = make_float4(d[0], d[1], d[2], d[3]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (e0 + j < E) dst[j] = d[j];
+        }
+      }
+    }
+  }
+}
+
+// Calls go(G, VEC) for E experts.
+template <typename F>
+void by_group(int E, F go) {
+  auto vec = [&](auto g) {
+    if (E % 4 == 0) go(g, std::true_type{});
+    else go(g, std::false_type{});
+  };
+  if (E <= 32) vec(std::integral_constant<int, 8>{});
+  else if (E <= 64) vec(std::integral_constant<int, 16>{});
+  else if (E <= 128) vec(std::integral_constant<int, 32>{});
+  else vec(std::integral_constant<int, 64>{});
+}
+
+// ---------------------------------------------------------------------------
+// Router backward.  With r0 = 1/sqrt(mean x^2 + eps), v = x r0 g (pre-norm)
+// or x, r = 1/sqrt(mean v^2 + eps), vhat = v r c, l = W vhat, and the gradient
+// dl of the logits, the norm's own terms need no second pass over H: since
+// sum_h (c W^T dl)_h v_h = D / r with D = sum_e dl_e l_e,
+//   dl' = dl r0 r,   beta = r0^2 r^2 D / H   (r0 = 1 without a pre-norm)
+//   G = dl'^T x [E,H],   m_h = sum_e W_eh G_eh
+//   dW = G g c,   dc = g m,   dg = c m - g sum_t x^2 beta
+//   dx = g c (dl' W) - x beta (g^2 + eps)    with a pre-norm
+//   dx =   c (dl' W) - x beta                without (g = 1)
+// (the pre-norm's projection, sum_h g dv x, is D r^2 eps / r0).
+//
+// First kernel, a wave per token: the routing weights' gradient to the
+// logits (q = softmax over the K picked, dl_k = q_k (d_k - sum_j q_j d_j) with
+// d_k = d_topk_w_k * per_expert_scale), plus the given d_logits; the two
+// norms; dl', beta, and the block's sums of d_topk_w_k q_k per expert.
+// ---------------------------------------------------------------------------
+constexpr int kRgRowWaves = 4;
+
+__device__ __forceinline__ void load8f(const bf16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+
+template <typename XT>
+__global__ __launch_bounds__(64 * kRgRowWaves) void router_grad_rows_kernel(
+    int T, int H, int E, int K, float eps, const XT* __restrict__ x,
+    const float* __restrict__ pre_gain, const float* __restrict__ pes,
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const uint8_t* __restrict__ mask, const float* __restrict__ d_w,
+    const float* __restrict__ d_logits, float* __restrict__ dl_out, float* __restrict__ beta_out,
+    float* __restrict__ part_pes) {
+  __shared__ float sums[kRgRowWaves][kMaxE];
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  float dpes[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // experts lane + 64 j
+  for (int t = blockIdx.x * kRgRowWaves + wave; t < T; t += gridDim.x * kRgRowWaves) {
+    const bool live = mask == nullptr || mask[t] != 0;  // uniform over the wave
+    float dl[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float scale = 0.0f, beta = 0.0f;
+    if (live) {
+      float ss = 0.0f, sg = 0.0f;
+      const XT* xr = x + (size_t)t * H;
+      for (int h = 8 * lane; h < H; h += 8 * kWave) {
+        float v[8];
+        load8f(xr + h, v);
+#pragma unroll
+        for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+        if (pre_gain != nullptr) {
+          float g[8];
+          load8f(pre_gain + h, g);
+#pragma unroll
+          for (int i = 0; i < 8; ++i) sg = __builtin_fmaf(v[i] * g[i], v[i] * g[i], sg);
+        }
+      }
+      ss = wave_sum(ss);
+      float r0 = 1.0f, r;
+      if (pre_gain != nullptr) {
+        sg = wave_sum(sg);
+        r0 = 1.0f / sqrtf(ss / (float)H + eps);
+        r = 1.0f / sqrtf(r0 * r0 * sg / (float)H + eps);
+      } else {
+        r = 1.0f / sqrtf(ss / (float)H + eps);
+      }
+      float l[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int e = lane + kWave * j;
+        l[j] = e < E ? logits[(size_t)t * E + e] : 0.0f;
+        if (d_logits != nullptr && e < E) dl[j] = d_logits[(size_t)t * E + e];
+      }
+      if (d_w != nullptr) {
+        // lane k < K: slot k (an id outside [0, E) is no slot)
+        int e = -1;
+        float lk = -INFINITY, dw = 0.0f, s = 0.0f;
+        if (lane < K) {
+          e = topk_idx[(size_t)t * K + lane];
+          if ((unsigned)e < (unsigned)E) {
+            lk = logits[(size_t)t * E + e];
+            dw = d_w[(size_t)t * K + lane];
+            s = pes[e];
+          } else {
+            e = -1;
+          }
+        }
+        const float top = wave_max(lk);
+        float q = lk == -INFINITY ? 0.0f : expf(lk - top);
+        const float z = wave_sum(q);
+        q = z > 0.0f ? q / z : 0.0f;
+        const float d = dw * s;
+        const float qd = wave_sum(q * d);
+        const float dlk = q * (d - qd), dsk = dw * q;
+        for (int k = 0; k < K; ++k) {  // a repeated id adds up
+          const int ek = __builtin_amdgcn_readlane(e, k);
+          const float dk = lane_value(dlk, k), sk = lane_value(dsk, k);
+#pragma unroll
+          for (int j = 0; j < 4; ++j)
+            if (ek == lane + kWave * j) {
+              dl[j] += dk;
+              dpes[j] += sk;
+            }
+        }
+      }
+      float D = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) D += dl[j] != 0.0f ? dl[j] * l[j] : 0.0f;
+      D = wave_sum(D);
+      scale = r0 * r;
+      beta = scale * scale * (D / (float)H);
+    }
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int e = lane + kWave * j;
+      if (e < E) dl_out[(size_t)t * E + e] = dl[j] * scale;
+    }
+    if (lane == 0) beta_out[t] = beta;
+  }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sums[wave][lane + kWave * j] = dpes[j];
+  __syncthreads();
+  if ((int)threadIdx.x < E) {
+    float s = 0.0f;
+    for (int w = 0; w < kRgRowWaves; ++w) s += sums[w][threadIdx.x];
+    part_pes[(size_t)blockIdx.x * E + threadIdx.x] = s;
+  }
+}
+
+// fp32 matrix instruction 32x32x2: lane l holds A[l % 32][l / 32] and
+// B[l / 32][l % 32]; register q of lane l is D[8 (q / 4) + 4 (l / 32) + q % 4]
+// [l % 32].  One value of the contraction per lane and instruction: both
+// operands come straight from rows whose fast axis is not the contraction.
+__device__ __forceinline__ f32x16 mfma_f32(float a, float b, f32x16 c) {
+  return __builtin_amdgcn_mfma_f32_32x32x2f32(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ int mfma_row(int q, int g) { return 8 * (q / 4) + 4 * g + q % 4; }
+
+// G partial of one split of the tokens: a wave takes 32 MT experts x 64
+// columns of x, the block's four waves four quarters of the split's tokens,
+// added through LDS.  The wave also sums x^2 beta for its columns (experts'
+// tile 0 only).
+constexpr int kRgWaves = 4;
+template <typename XT, int MT>
+__global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
+    int T, int H, int E, int span, const XT* __restrict__ x, const uint8_t* __restrict__ mask,
+    const float* __restrict__ dl, const float* __restrict__ beta, float* __restrict__ part_g,
+    float* __restrict__ part_b) {
+  __shared__ float acc_s[kRgWaves][16 * 2][kWave];
+  __shared__ float b_s[kRgWaves][64];
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int c = lane % 32, g = lane / 32;
+  const int h0 = blockIdx.x * 64, e0 = blockIdx.y * 32 * MT, split = blockIdx.z;
+  const int s0 = split * span, s1 = min(T, s0 + span);
+  const int q4 = ((s1 - s0 + kRgWaves - 1) / kRgWaves + 1) / 2 * 2;
+  const int t0 = min(s1, s0 + wave * q4), t1 = min(s1, t0 + q4);
+  f32x16 acc[MT][2];
+#pragma unroll
+  for (int i = 0; i < MT; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  float bs[2] = {0.0f, 0.0f};
+  constexpr int U = 4;  // pairs of tokens loaded before the first is used
+  for (int t = t0; t < t1; t += 2 * U) {
+    float a[U][MT], b[U][2], be[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int tt = t + 2 * u + g, tc = min(tt, t1 - 1);
+      const bool on = tt < t1 && (mask == nullptr || mask[tc] != 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        const int e = e0 + 32 * i + c;
+        a[u][i] = on && e < E ? dl[(size_t)tc * E + min(e, E - 1)] : 0.0f;
+      }
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b[u][j] = on ? to_f32(x[(size_t)tc * H + h0 + 32 * j + c]) : 0.0f;
+      be[u] = on ? beta[tc] : 0.0f;
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+#pragma unroll
+      for (int i = 0; i < MT; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f32(a[u][i], b[u][j], acc[i][j]);
+#pragma unroll
+      for (int j = 0; j < 2; ++j) bs[j] = __builtin_fmaf(b[u][j] * b[u][j], be[u], bs[j]);
+    }
+  }
+  const bool want_b = blockIdx.y == 0;
+  if (want_b) {
+#pragma unroll
+    for (int j = 0; j < 2; ++j) {
+      const float v = bs[j] + __shfl_xor(bs[j], 32, kWave);
+      if (g == 0) b_s[wave][32 * j + c] = v;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) {
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc_s[wave][16 * j + q][lane] = acc[i][j][q];
+    __syncthreads();
+    // each wave adds a quarter of the 32 registers
+#pragma unroll
+    for (int k = 0; k < 32 / kRgWaves; ++k) {
+      const int r = wave * (32 / kRgWaves) + k;
+      float v = 0.0f;
+#pragma unroll
+      for (int w = 0; w < kRgWaves; ++w) v += acc_s[w][r][lane];
+      const int e = e0 + 32 * i + mfma_row(r % 16, g), h = h0 + 32 * (r / 16) + c;
+      if (e < E) part_g[((size_t)split * E + e) * H + h] = v;
+    }
+  }
+  if (want_b && threadIdx.x < 64) {
+    float v = 0.0f;
+    for (int w = 0; w < kRgWaves; ++w) v += b_s[w][threadIdx.x];
+    part_b[(size_t)split * H + h0 + threadIdx.x] = v;
+  }
+}
+
+// dx: a wave takes 64 tokens x 64 columns; the contraction runs over the
+// experts, four per lane and load (lanes 0-31 experts 8 s .. 8 s + 3, lanes
+// 32-63 the next four; W's rows in the same order).
+template <typename XT, bool VEC>
+__global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
+    int T, int H, int E, float eps, const XT* __restrict__ x, const uint8_t* __restrict__ mask,
+    const float* __restrict__ dl, const float* __restrict__ beta, const float* __restrict__ W,
+    const float* __restrict__ scale, const float* __restrict__ pre_gain, XT* __restrict__ dx) {
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int c = lane % 32, g = lane / 32;
+  const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgWaves + wave) * 64;
+  if (t0 >= T) return;  // no barrier below
+  f32x16 acc[2][2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
+#pragma unroll
+    for (int j = 0; j < 2; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+  for (int e0 = 0; e0 < E; e0 += 8) {
+    float a[2][4], b[4][2];
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const float* row = dl + (size_t)min(t0 + 32 * i + c, T - 1) * E;
+      const int e = e0 + 4 * g;
+      if (VEC && e + 3 < E) {
+        const float4 v = *reinterpret_cast<const float4*>(row + e);
+        a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
+      } else {
+#pragma unroll
+        for (int k = 0; k < 4; ++k) a[i][k] = e + k < E ? row[e + k] : 0.0f;
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const int e = e0 + 4 * g + k;
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+        b[k][j] = e < E ? W[(size_t)e * H + h0 + 32 * j + c] : 0.0f;
+    }
+#pragma unroll
+    for (int k = 0; k < 4; ++k)
+#pragma unroll
+      for (int i = 0; i < 2; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f32(a[i][k], b[k][j], acc[i][j]);
+  }
+#pragma unroll
+  for (int j = 0; j < 2; ++j) {
+    const int h = h0 + 32 * j + c;
+    const float gn = pre_gain != nullptr ? pre_gain[h] : 1.0f;
+    const float gc = gn * scale[h], ge = pre_gain != nullptr ? gn * gn + eps : 1.0f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int t = t0 + 32 * i + mfma_row(q, g);
+        if (t >= T) continue;
+        const bool live = mask == nullptr || mask[t] != 0;
+        const size_t at = (size_t)t * H + h;
+        const float v = live ? gc * acc[i][j][q] - to_f32(x[at]) * (beta[t] * ge) : 0.0f;
+        dx[at] = from_f32<XT>(v);
+      }
+  }
+}
+
+// Last kernel: adds the splits of G; dW, dc and dg of 16 columns per block
+// (16 groups of experts), and in the blocks past the columns the per-expert
+// scale's gradient from the first kernel's sums.
+constexpr int kRgCols = 16, kRgParts = 16;
+__global__ __launch_bounds__(kRgCols * kRgParts) void router_grad_finish_kernel(
+    int H, int E, int splits, int pes_blocks, const float* __restrict__ part_g,
+    const float* __restrict__ part_b, const float* __restrict__ part_pes,
+    const float* __restrict__ W, const float* __restrict__ scale,
+    const float* __restrict__ pre_gain, float* __restrict__ dW, float* __restrict__ d_scale,
+    float* __restrict__ d_pes, float* __restrict__ d_gain) {
+  __shared__ float red[kRgParts][kRgCols];
+  const int c = threadIdx.x % kRgCols, p = threadIdx.x / kRgCols;
+  const int col_blocks = H / kRgCols;
+  if ((int)blockIdx.x >= col_blocks) {
+    const int e = ((int)blockIdx.x - col_blocks) * kRgCols + c;
+    float s = 0.0f;
+    if (e < E)
+      for (int i = p; i < pes_blocks; i += kRgParts) s += part_pes[(size_t)i * E + e];
+    red[p][c] = s;
+    __syncthreads();
+    if (p == 0 && e < E) {
+      s = 0.0f;
+      for (int i = 0; i < kRgParts; ++i) s += red[i][c];
+      d_pes[e] = s;
+    }
+    return;
+  }
+  const int h = blockIdx.x * kRgCols + c;
+  const float gn = pre_gain != nullptr ? pre_gain[h] : 1.0f, cs = scale[h];
+  float m = 0.0f;
+  for (int e = p; e < E; e += kRgParts) {
+    float v = 0.0f;
+    for (int s = 0; s < splits; ++s) v += part_g[((size_t)s * E + e) * H + h];
+    dW[(size_t)e * H + h] = v * gn * cs;
+    m = __builtin_fmaf(W[(size_t)e * H + h], v, m);
+  }
+  red[p][c] = m;
+  __syncthreads();
+  if (p != 0) return;
+  m = 0.0f;
+  for (int i = 0; i < kRgParts; ++i) m += red[i][c];
+  d_scale[h] = gn * m;
+  if (d_gain != nullptr) {
+    float bsum = 0.0f;
+    for (int s = 0; s < splits; ++s) bsum += part_b[(size_t)s * H + h];
+    d_gain[h] = cs * m - gn * bsum;
+  }
+}
+
+// Splits of the tokens for G.
+constexpr int kRgMinSpan = 64;
+
+template <typename XT>
+hipError_t launch_router_grad_t(const RouterGradArgs& a, hipStream_t s) {
+  const XT* x = static_cast<const XT*>(a.x);
+  const int splits = router_grad_splits(a.T);
+  const int rb = router_grad_row_blocks(a.T);
+  if (a.T > 0) {
+    hipLaunchKernelGGL(router_grad_rows_kernel<XT>, dim3(rb), dim3(64 * kRgRowWaves), 0, s, a.T,
+                       a.H, a.E, a.K, a.eps, x, a.pre_gain, a.per_expert_scale, a.logits,
+                       a.topk_idx, a.mask, a.d_topk_w, a.d_logits, a.ws_dl, a.ws_beta,
+                       a.ws_part_pes);
+    const int span = (a.T + splits - 1) / splits;
+    auto gw = [&](auto mt) {
+      constexpr int MT = decltype(mt)::value;
+      hipLaunchKernelGGL((router_grad_w_kernel<XT, MT>),
+                         dim3(a.H / 64, (a.E + 32 * MT - 1) / (32 * MT), splits),
+                         dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, span, x, a.mask, a.ws_dl,
+                         a.ws_beta, a.ws_part_g, a.ws_part_b);
+    };
+    if (a.E <= 32) gw(std::integral_constant<int, 1>{});
+    else if (a.E <= 64) gw(std::integral_constant<int, 2>{});
+    else gw(std::integral_constant<int, 4>{});
+    if (a.d_x != nullptr) {
+      const dim3 grid(a.H / 64, (a.T + 64 * kRgWaves - 1) / (64 * kRgWaves));
+      XT* dx = static_cast<XT*>(a.d_x);
+      if (a.E % 4 == 0)
+        hipLaunchKernelGGL((router_grad_x_kernel<XT, true>), grid, dim3(64 * kRgWaves), 0, s, a.T,
+                           a.H, a.E, a.eps, x, a.mask, a.ws_dl, a.ws_beta, a.router_w,
+                           a.router_scale, a.pre_gain, dx);
+      else
+        hipLaunchKernelGGL((router_grad_x_kernel<XT, false>), grid, dim3(64 * kRgWaves), 0, s,
+                           a.T, a.H, a.E, a.eps, x, a.mask, a.ws_dl, a.ws_beta, a.router_w,
+                           a.router_scale, a.pre_gain, dx);
+    }
+  }
+  hipLaunchKernelGGL(router_grad_finish_kernel,
+                     dim3(a.H / kRgCols + (a.E + kRgCols - 1) / kRgCols),
+                     dim3(kRgCols * kRgParts), 0, s, a.H, a.E, a.T > 0 ? splits : 0,
+                     a.T > 0 ? rb : 0, a.ws_part_g, a.ws_part_b, a.ws_part_pes, a.router_w,
+                     a.router_scale, a.pre_gain, a.d_router_w, a.d_router_scale,
+                     a.d_per_expert_scale, a.d_pre_gain);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+int balance_blocks(int T) {
+  if (T <= kBalOneBlock) return 1;
+  const int nb = (T + 63) / 64;
+  return nb < kBalMaxBlocks ? nb : kBalMaxBlocks;
+}
+
+hipError_t launch_balance_loss(const BalanceArgs& a, hipStream_t s) {
+  const int nb = balance_blocks(a.T), span = a.T > 0 ? (a.T + nb - 1) / nb : 0;
+  by_group(a.E, [&](auto g, auto vec) {
+    hipLaunchKernelGGL((balance_partial_kernel<decltype(g)::value, decltype(vec)::value>),
+                       dim3(nb), dim3(kBalThreads), 0, s, a.T, a.E, a.K, span, a.logits,
+                       a.topk_idx, a.mask, a.balance_coef, a.z_coef, a.ws_part_p, a.ws_part_n,
+                       a.ws_part_z, a.ws_part_live, a.loss, a.counts, a.mean_p);
+  });
+  if (nb > 1)
+    hipLaunchKernelGGL(balance_final_kernel, dim3(1), dim3(kBalFinThreads), 0, s, nb, a.E, a.K,
+                       a.balance_coef, a.z_coef, a.ws_part_p, a.ws_part_n, a.ws_part_z,
+                       a.ws_part_live, a.loss, a.counts, a.mean_p);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
+  by_group(a.E, [&](auto g, auto vec) {
+    constexpr int per = 256 / decltype(g)::value * kGradUnroll;
+    const int nb = (a.T + per - 1) / per;
+    hipLaunchKernelGGL((balance_grad_kernel<decltype(g)::value, decltype(vec)::value>), dim3(nb),
+                       dim3(256), 0, s, a.T, a.E, a.K, a.logits, a.mask, a.counts, a.loss,
+                       a.balance_coef, a.z_coef, a.d_loss, a.d_logits);
+  });
+  return hipGetLastError();
+}
+
+int router_grad_splits(int T) {
+  const int n = (T + kRgMinSpan - 1) / kRgMinSpan;
+  return n < 1 ? 1 : n < 8 ? n : 8;
+}
+
+int router_grad_row_blocks(int T) {
+  const int n = (T + kRgRowWaves - 1) / kRgRowWaves;
+  return n < 512 ? n : 512;
+}
+
+hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
+  return a.x_bf16 ? launch_router_grad_t<bf16>(a, s) : launch_router_grad_t<float>(a, s);
+}
+
+}  // namespace moe

@@ -63,6 +63,11 @@ def _load():
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_router.argtypes = [D, I32] + [P] * 8 + [SZ, P]
+    F = ctypes.c_float
+    L.moe_router_logits.argtypes = [D, I32] + [P] * 9 + [SZ, P]
+    L.moe_balance_loss.argtypes = [D, I32] + [P] * 3 + [F, F] + [P] * 4 + [SZ, P]
+    L.moe_balance_loss_grad.argtypes = [D, I32] + [P] * 4 + [F, F] + [P] * 3
+    L.moe_router_grad.argtypes = [D, I32] + [P] * 16 + [SZ, P]
     L.moe_route.argtypes = [D, I32] + [P] * 11 + [SZ, P]
     L.moe_dispatch.argtypes = [D, I32] + [P] * 5 + [SZ, P]
     L.moe_expert_ffn.argtypes = [D, I32] + [P] * 8 + [SZ, P]
@@ -87,7 +92,9 @@ def _load():
               "moe_expert_down", "moe_combine", "moe_forward", "gemma4_ffn_block",
               "moe_quantize_int8", "moe_expert_ffn_int8", "moe_dense_mask_dispatch",
               "moe_quantize", "moe_dequantize", "moe_expert_ffn_q", "moe_expert_gate_up_timed",
-              "gemma4_ffn_block_q", "moe_forward_noalloc", "moe_expert_ffn_mx"):
+              "gemma4_ffn_block_q", "moe_forward_noalloc", "moe_expert_ffn_mx",
+              "moe_router_logits", "moe_balance_loss", "moe_balance_loss_grad",
+              "moe_router_grad"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -113,6 +120,30 @@ def _ptr(t: Optional[torch.Tensor]):
     if not t.is_contiguous():
         raise ValueError("tensors passed to libmoe must be contiguous")
     return ctypes.c_void_p(t.data_ptr())
+
+
+def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, optional: bool = False):
+    """Device pointer of an array argument, after its type and size: a tensor of
+    dtype (or of one of several) with at least numel elements, on the current
+    device, contiguous."""
+    if t is None:
+        if optional:
+            return None
+        raise ValueError(f"{name} is required")
+    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+        raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
+    if t.numel() < numel:
+        raise ValueError(f"{name} has {t.numel()} elements, {numel} needed")
+    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+        raise ValueError(f"{name} is on {t.device}, not on the current GPU")
+    return _ptr(t)
+
+
+_MASK = (torch.uint8, torch.bool)
+
+
+def _act(d: MoeDims):
+    return torch.bfloat16 if d.act_dtype == MOE_BF16 else torch.float32
 
 
 def _stream(stream):
@@ -148,6 +179,66 @@ def moe_router(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain,
                            _ptr(per_expert_scale), _ptr(pre_norm_gain), _ptr(topk_idx),
                            _ptr(topk_w), _ptr(ws), ws.numel() if ws is not None else 0,
                            _stream(stream)))
+
+
+def moe_router_logits(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx,
+                      topk_w, logits, ws, stream=None):
+    """moe_router, with the logits [T, E] as an output."""
+    E, H, K, f32 = d.num_experts, d.hidden, d.top_k, torch.float32
+    _check(_lib.moe_router_logits(
+        ctypes.byref(d), T, _arg("x", x, _act(d), T * H), _arg("router_w", router_w, f32, E * H),
+        _arg("router_scale", router_scale, f32, H),
+        _arg("per_expert_scale", per_expert_scale, f32, E),
+        _arg("pre_norm_gain", pre_norm_gain, f32, H, True),
+        _arg("topk_idx", topk_idx, torch.int32, T * K), _arg("topk_w", topk_w, f32, T * K),
+        _arg("logits", logits, f32, T * E), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
+
+
+def moe_balance_loss(d, T, logits, topk_idx, token_mask, balance_coef, z_coef, loss,
+                     expert_counts, mean_probs, ws, stream=None):
+    """Balance loss, z-loss, per-expert counts and mean probabilities of a batch."""
+    E, f32 = d.num_experts, torch.float32
+    _check(_lib.moe_balance_loss(
+        ctypes.byref(d), T, _arg("logits", logits, f32, T * E),
+        _arg("topk_idx", topk_idx, torch.int32, T * d.top_k),
+        _arg("token_mask", token_mask, _MASK, T, True), balance_coef, z_coef,
+        _arg("loss", loss, f32, 4), _arg("expert_counts", expert_counts, torch.int32, E),
+        _arg("mean_probs", mean_probs, f32, E), _ptr(ws), ws.numel() if ws is not None else 0,
+        _stream(stream)))
+
+
+def moe_balance_loss_grad(d, T, logits, token_mask, expert_counts, loss, balance_coef, z_coef,
+                          d_loss, d_logits, stream=None):
+    """Gradient of d_loss * loss[0] in the logits."""
+    E, f32 = d.num_experts, torch.float32
+    _check(_lib.moe_balance_loss_grad(
+        ctypes.byref(d), T, _arg("logits", logits, f32, T * E),
+        _arg("token_mask", token_mask, _MASK, T, True),
+        _arg("expert_counts", expert_counts, torch.int32, E), _arg("loss", loss, f32, 4),
+        balance_coef, z_coef, _arg("d_loss", d_loss, f32, 1),
+        _arg("d_logits", d_logits, f32, T * E), _stream(stream)))
+
+
+def moe_router_grad(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, logits,
+                    topk_idx, token_mask, d_topk_w, d_logits, d_x, d_router_w, d_router_scale,
+                    d_per_expert_scale, d_pre_norm_gain, ws, stream=None):
+    """Backward pass of moe_router_logits."""
+    E, H, K, f32 = d.num_experts, d.hidden, d.top_k, torch.float32
+    _check(_lib.moe_router_grad(
+        ctypes.byref(d), T, _arg("x", x, _act(d), T * H), _arg("router_w", router_w, f32, E * H),
+        _arg("router_scale", router_scale, f32, H),
+        _arg("per_expert_scale", per_expert_scale, f32, E, True),
+        _arg("pre_norm_gain", pre_norm_gain, f32, H, True), _arg("logits", logits, f32, T * E),
+        _arg("topk_idx", topk_idx, torch.int32, T * K, True),
+        _arg("token_mask", token_mask, _MASK, T, True),
+        _arg("d_topk_w", d_topk_w, f32, T * K, True),
+        _arg("d_logits", d_logits, f32, T * E, True), _arg("d_x", d_x, _act(d), T * H, True),
+        _arg("d_router_w", d_router_w, f32, E * H),
+        _arg("d_router_scale", d_router_scale, f32, H),
+        _arg("d_per_expert_scale", d_per_expert_scale, f32, E),
+        _arg("d_pre_norm_gain", d_pre_norm_gain, f32, H, True), _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def moe_route(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx, topk_w,

@@ -1,0 +1,412 @@
+"""The router's training calls against fp64 definitions (router_train_ref.py):
+balance loss, counts and gradient; the router's logits and backward pass; and a
+whole step of them through the experts, eager and from a graph.
+
+Tolerances: a chain of n fp32 roundings moves a sum by at most n * 2^-24 of
+the magnitudes it adds.  Balance: a lane adds at most 64 tokens, a block at
+most 64 rows, the second step 256 / rows + 64 values (1024 / E rows); exp, log and
+the division cost a few units, and exp of l - max inherits 2^-24 |l - max|, at
+most 64 units here: 640 covers it.  Backward: n_round below adds the chain over
+the tokens (or experts) to the two norms' chains (H / 512 + 8 each)."""
+import numpy as np
+import pytest
+import torch
+
+from sparse_moe_transformer_router_amd import synth
+from tests import router_train_ref as ref
+from tests.gpu_util import F32_TOL, dev_f32, dev_tensor, note, rel_max_err
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from sparse_moe_transformer_router_amd import lib
+else:
+    lib = None
+
+A, B, G = 0.7, 0.3, 1.25
+EPS = 1e-6
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _picks(g, T, E, K):
+    return torch.stack([torch.randperm(E, generator=g)[:K] for _ in range(max(T, 1))])[:T].to(
+        torch.int32)
+
+
+def _mask(g, T, kind):
+    if kind == "none":
+        return None
+    if kind == "all":
+        return torch.zeros(T, dtype=torch.uint8)
+    return (torch.rand(T, generator=g) < 0.6).to(torch.uint8)
+
+
+def _run_balance(lg, idx, mask, E, K):
+    T = len(lg)
+    d = lib.dims(64, E, K, 32)
+    ws = lib.workspace(d, T)
+    ws.fill_(0xFF)  # scratch holds NaN
+    out = dict(loss=torch.full((4,), np.nan, device="cuda"),
+               counts=torch.full((E,), -1, dtype=torch.int32, device="cuda"),
+               p=torch.full((E,), np.nan, device="cuda"),
+               d=torch.full((T, E), np.nan, device="cuda"))
+    lgd, idd = lg.float().cuda(), idx.cuda()
+    md = None if mask is None else mask.cuda()
+    lib.moe_balance_loss(d, T, lgd, idd, md, A, B, out["loss"], out["counts"], out["p"], ws)
+    lib.moe_balance_loss_grad(d, T, lgd, md, out["counts"], out["loss"], A, B,
+                              torch.tensor([G], device="cuda"), out["d"])
+    torch.cuda.synchronize()
+    return {k: v.cpu() for k, v in out.items()}
+
+
+def _check_balance(lg, idx, mask, got):
+    """lg: fp32 values in fp64."""
+    E = lg.shape[1]
+    clean = lg if mask is None else torch.where(mask.bool()[:, None], lg, torch.zeros_like(lg))
+    tot, bal, z, n, counts, p = ref.balance(clean, idx, mask, A, B)
+    assert torch.equal(got["counts"].long(), counts)
+    u = 640 * ref.U32
+    want = torch.stack([torch.as_tensor(v, dtype=torch.float64) for v in (tot, bal, z)])
+    assert got["loss"][3] == n
+    assert torch.all((got["loss"][:3].double() - want).abs() <= u * want.abs()), (got["loss"], want)
+    assert torch.all((got["p"].double() - p).abs() <= u * p)
+    d, mag = ref.balance_grad(clean, idx, mask, A, B, G)
+    err = (got["d"].double() - d).abs()
+    assert torch.all(err <= u * mag + 1e-38), float((err / (mag + 1e-38)).max())
+    if mask is not None:
+        assert torch.all(got["d"][mask == 0] == 0)
+    assert got["d"].shape == (len(lg), E)
+
+
+@pytest.mark.parametrize("E,K", [(1, 1), (7, 3), (8, 8), (33, 2), (60, 4), (64, 8), (128, 8),
+                                 (130, 5), (255, 8), (256, 32)])
+@pytest.mark.parametrize("T", [1, 2, 63, 256, 257, 1003])
+def test_balance(E, K, T):
+    g = _gen(100 * E + T)
+    lg = (2.0 * torch.randn(T, E, generator=g) + torch.randn(E, generator=g)).double()
+    idx = _picks(g, T, E, K)
+    kind = ("none", "some", "all")[(E + T) % 3]
+    mask = _mask(g, T, kind)
+    note(f"balance T={T} E={E} K={K} mask={kind}")
+    _check_balance(lg, idx, mask, _run_balance(lg, idx, mask, E, K))
+
+
+def test_balance_odd_values():
+    """NaN and infinities in masked rows, experts switched off (-inf), a row of
+    -inf only, picks outside [0, E) and a pick that occurs twice."""
+    g = _gen(3)
+    T, E, K = 300, 20, 4
+    lg = torch.randn(T, E, generator=g).double()
+    idx = _picks(g, T, E, K)
+    mask = _mask(g, T, "some")
+    mask[5], mask[6], mask[7] = 0, 1, 1
+    lg[5] = float("nan")
+    lg[mask == 0] = float("inf")
+    lg[6, 3:9] = -float("inf")
+    lg[7] = -float("inf")
+    lg[8] = torch.finfo(torch.float32).min
+    mask[8] = 0
+    idx[6, 0], idx[7, 1], idx[9] = -1, E, idx[9, 0]
+    note("balance, odd values")
+    got = _run_balance(lg, idx, mask, E, K)
+    _check_balance(lg, idx, mask, got)
+    assert torch.all(got["d"][7] == 0) and torch.all(got["d"][6, 3:9] == 0)
+
+
+def test_balance_lowest_value_mask():
+    """Experts masked with the type's lowest value have probability 0."""
+    g = _gen(4)
+    lg = torch.randn(70, 128, generator=g).double()
+    lg[:, 40:90] = torch.finfo(torch.float32).min
+    idx = _picks(g, 70, 128, 8)
+    note("balance, lowest-value masks")
+    got = _run_balance(lg, idx, None, 128, 8)
+    _check_balance(lg, idx, None, got)
+    assert torch.all(got["p"][40:90] == 0)
+
+
+def test_balance_largest_batch():
+    g = _gen(5)
+    T, E, K = 65536, 16, 2
+    lg = torch.randn(T, E, generator=g).double()
+    idx = torch.randint(0, E, (T, K), generator=g, dtype=torch.int32)
+    note("balance T=65536")
+    _check_balance(lg, idx, None, _run_balance(lg, idx, None, E, K))
+
+
+def test_balance_empty_batch_writes_zeros():
+    note("balance T=0")
+    d = lib.dims(64, 12, 2, 32)
+    loss = torch.full((4,), 7.0, device="cuda")
+    counts = torch.full((12,), 7, dtype=torch.int32, device="cuda")
+    p = torch.full((12,), 7.0, device="cuda")
+    e = torch.empty(0, 12, device="cuda")
+    lib.moe_balance_loss(d, 0, e, torch.empty(0, 2, dtype=torch.int32, device="cuda"), None, A, B,
+                         loss, counts, p, None)
+    torch.cuda.synchronize()
+    assert not loss.any() and not counts.any() and not p.any()
+
+
+# ---------------------------------------------------------------------------
+def _router_case(T, H, E, K, bf16, pre, aux, use_w, kind, seed):
+    g = _gen(seed)
+    n = lambda *s: torch.randn(*s, generator=g)  # noqa: E731
+    x = n(T, H) * (1 + 7 * (torch.rand(H, generator=g) < 0.05).float())
+    x = x.bfloat16().float() if bf16 else x
+    c = dict(x=x, W=n(E, H) * (1.5 / H ** 0.5), scale=1 + 0.1 * n(H), pes=1 + 0.1 * n(E),
+             gain=1 + 0.1 * n(H) if pre else None, idx=_picks(g, T, E, K), mask=_mask(g, T, kind),
+             d_w=n(T, K) if use_w else None, d_l=n(T, E) if aux else None)
+    return c
+
+
+def _logits(c):
+    return ref.router_outputs(*[ref.f64(c[k]) for k in ("x", "W", "scale", "pes", "gain")],
+                              c["idx"], EPS)[1].float()
+
+
+def _run_router_grad(c, bf16, want_x=True, spoil=False):
+    T, H = c["x"].shape
+    E, K = c["W"].shape[0], c["idx"].shape[1]
+    d = lib.dims(H, E, K, 32, 0, EPS, lib.MOE_BF16 if bf16 else lib.MOE_F32)
+    ws = lib.workspace(d, T)
+    ws.fill_(0xFF)
+    dt = torch.bfloat16 if bf16 else torch.float32
+    dev = {k: None if v is None else v.cuda() for k, v in c.items()}
+    x, lg = dev["x"].to(dt), _logits(c).cuda()
+    if spoil:  # what a padded row may hold
+        off = dev["mask"] == 0
+        x[off], lg[off] = float("nan"), float("inf")
+        for k in ("d_w", "d_l"):
+            if dev[k] is not None:
+                dev[k][off] = float("nan")
+    new = lambda *s, t=torch.float32: torch.full(s, np.nan, dtype=t, device="cuda")  # noqa: E731
+    out = dict(x=new(T, H, t=dt) if want_x else None, W=new(E, H), scale=new(H), pes=new(E),
+               gain=new(H) if c["gain"] is not None else None)
+    lib.moe_router_grad(d, T, x, dev["W"], dev["scale"], dev["pes"], dev["gain"], lg, dev["idx"],
+                        dev["mask"], dev["d_w"], dev["d_l"], out["x"], out["W"], out["scale"],
+                        out["pes"], out["gain"], ws)
+    torch.cuda.synchronize()
+    return {k: v.cpu() for k, v in out.items() if v is not None}
+
+
+def _check_router_grad(c, got, bf16):
+    T, H = c["x"].shape
+    E = c["W"].shape[0]
+    n = T + E + 2 * (H // 512 + 8) + 64
+    want, tol = ref.router_grad(*[ref.f64(c[k]) for k in ("x", "W", "scale", "pes", "gain")],
+                                c["idx"], c["mask"], ref.f64(c["d_w"]), ref.f64(c["d_l"]), EPS, n)
+    for k, v in got.items():
+        err = (v.double() - want[k]).abs()
+        t = tol[k] + 1e-37
+        if k == "x" and bf16:
+            t = t + 2.0 ** -8 * want[k].abs() * 1.001
+        assert torch.all(err <= t), (k, float((err / t).max()))
+
+
+@pytest.mark.parametrize("T,H,E,K", [(1, 64, 4, 1), (2, 64, 1, 1), (48, 192, 16, 3),
+                                     (63, 128, 7, 7), (65, 704, 33, 2), (130, 2816, 128, 8),
+                                     (301, 512, 130, 8), (257, 192, 256, 32), (600, 64, 60, 4)])
+@pytest.mark.parametrize("bf16", [False, True])
+def test_router_grad(T, H, E, K, bf16):
+    v = (T + H + bf16) % 6
+    pre, aux, use_w = v % 2 == 0, v < 4, v != 1
+    kind = ("none", "some")[T % 2]
+    c = _router_case(T, H, E, K, bf16, pre, aux, use_w, kind, 10 * T + E)
+    note(f"router grad T={T} H={H} E={E} K={K} bf16={bf16} pre={pre} aux={aux} w={use_w} {kind}")
+    _check_router_grad(c, _run_router_grad(c, bf16, spoil=c["mask"] is not None), bf16)
+
+
+@pytest.mark.parametrize("pre", [False, True])
+@pytest.mark.parametrize("aux,use_w", [(False, True), (True, False), (True, True)])
+def test_router_grad_inputs_given(pre, aux, use_w):
+    c = _router_case(70, 128, 24, 4, False, pre, aux, use_w, "none", 77)
+    note(f"router grad pre={pre} aux={aux} w={use_w}")
+    got = _run_router_grad(c, False)
+    _check_router_grad(c, got, False)
+    less = _run_router_grad(c, False, want_x=False)  # d_x not wanted: the rest is the same
+    for k, v in less.items():
+        assert torch.equal(v, got[k])
+
+
+def test_router_grad_odd_picks():
+    """Ids outside [0, E), an id picked twice, every token masked."""
+    c = _router_case(40, 64, 12, 3, False, True, True, True, "none", 8)
+    c["idx"][3, 0], c["idx"][4, 2] = -1, 12
+    c["idx"][5] = -7
+    c["idx"][6, 1] = c["idx"][6, 0]
+    note("router grad, odd picks")
+    _check_router_grad(c, _run_router_grad(c, False), False)
+    c["mask"] = torch.zeros(40, dtype=torch.uint8)
+    got = _run_router_grad(c, False, spoil=True)
+    assert all(not v.any() for v in got.values())
+
+
+def test_router_grad_against_differences():
+    c = _router_case(33, 128, 10, 3, False, True, True, True, "some", 9)
+    note("router grad against differences")
+    got = _run_router_grad(c, False)
+    a = {k: ref.f64(c[k]) for k in ("x", "W", "scale", "pes", "gain")}
+    rest = (c["idx"], c["mask"], ref.f64(c["d_w"]), ref.f64(c["d_l"]), EPS)
+    g, h = _gen(1), 1e-5
+    for k, v in a.items():
+        s = torch.randn(v.shape, generator=g, dtype=torch.float64)
+        f = lambda z: float(ref.router_objective(*{**a, k: v + z * h * s}.values(), *rest))  # noqa
+        # the fp32 gradient is within n 2^-24 of its terms, 1e-5 of the
+        # gradient's norm here; the step's norm carries that over
+        scale = float(got[k].double().norm() * s.norm())
+        assert abs(float((got[k].double() * s).sum()) - (f(1) - f(-1)) / (2 * h)) <= 2e-5 * scale
+
+
+def test_router_grad_empty_batch_writes_zeros():
+    note("router grad T=0")
+    c = _router_case(1, 64, 12, 3, False, True, True, True, "none", 8)
+    d = lib.dims(64, 12, 3, 32, 0, EPS, lib.MOE_F32)
+    z = lambda *s: torch.full(s, 3.0, device="cuda")  # noqa: E731
+    o = [z(12, 64), z(64), z(12), z(64)]
+    lib.moe_router_grad(d, 0, z(0, 64), c["W"].cuda(), c["scale"].cuda(), c["pes"].cuda(),
+                        c["gain"].cuda(), z(0, 12), torch.empty(0, 3, dtype=torch.int32).cuda(),
+                        None, z(0, 3), None, None, *o, None)
+    torch.cuda.synchronize()
+    assert all(not t.any() for t in o)
+
+
+@pytest.mark.parametrize("T", [1, 20, 300, 700])
+def test_router_logits_are_the_routers(T):
+    """Same picks and weights as moe_router, bit for bit; the logits it kept."""
+    c = _router_case(T, 2816, 128, 8, True, True, False, True, "none", T)
+    note(f"router logits T={T}")
+    d = lib.dims(2816, 128, 8, 704)
+    ws = lib.workspace(d, T)
+    x = c["x"].bfloat16().cuda()
+    args = [c[k].cuda() for k in ("W", "scale", "pes", "gain")]
+    idx, w = torch.empty(2, T, 8, dtype=torch.int32).cuda(), torch.empty(2, T, 8).cuda()
+    lg = torch.full((T, 128), np.nan, device="cuda")
+    lib.moe_router(d, T, x, *args, idx[0], w[0], ws)
+    lib.moe_router_logits(d, T, x, *args, idx[1], w[1], lg, ws)
+    torch.cuda.synchronize()
+    assert torch.equal(idx[0], idx[1]) and torch.equal(w[0], w[1])
+    want = _logits(c).double()
+    mag = c["W"].double().abs().sum(1).max() * 12  # |vhat| stays below 12
+    assert float((lg.cpu().double() - want).abs().max()) <= 200 * ref.U32 * float(mag)
+    assert torch.equal(torch.gather(lg, 1, idx[1].long()), torch.sort(lg, 1, True).values[:, :8])
+
+
+# ---------------------------------------------------------------------------
+class _Step:
+    """One training step of a router with frozen experts: routing, experts,
+    combine, balance loss, gradients.  fp32 throughout."""
+
+    def __init__(self, T, seed):
+        m = synth.tiny_case(seed=seed, T=T, H=128, E=12, K=3, I=64)
+        self.m, self.T = m, T
+        self.d = lib.dims(m.H, m.E, m.K, m.I, 0, m.eps, lib.MOE_F32)
+        self.ws = lib.workspace(self.d, T)
+        g = _gen(seed)
+        self.gain = (1 + 0.1 * torch.randn(m.H, generator=g)).cuda()
+        self.mask = (torch.rand(T, generator=g) < 0.8).to(torch.uint8).cuda()
+        self.up = torch.randn(T, m.H, generator=g).cuda() * self.mask[:, None]
+        self.x = dev_tensor(m.x, False)
+        self.W, self.scale, self.pes = map(dev_f32, (m.router_w, m.router_scale,
+                                                     m.per_expert_scale))
+        self.gu, self.dn = dev_tensor(m.gate_up, False), dev_tensor(m.down, False)
+        e = lambda *s: torch.empty(*s, device="cuda")  # noqa: E731
+        i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.idx, self.w, self.lg = i(T, m.K), e(T, m.K), e(T, m.E)
+        self.cnt, self.off, self.srt = i(m.E), i(m.E + 1), i(T * m.K)
+        self.ones = torch.ones(T, m.K, device="cuda")
+        self.y, self.dw = e(T, m.K, m.H), e(T, m.K)
+        self.loss, self.bc, self.p, self.dl = e(4), i(m.E), e(m.E), e(T, m.E)
+        self.one = torch.ones(1, device="cuda")
+        self.g = dict(x=e(T, m.H), W=e(m.E, m.H), scale=e(m.H), pes=e(m.E), gain=e(m.H))
+
+    def run(self):
+        s, d, T = self, self.d, self.T
+        lib.moe_router_logits(d, T, s.x, s.W, s.scale, s.pes, s.gain, s.idx, s.w, s.lg, s.ws)
+        lib.moe_dispatch(d, T, s.idx, s.cnt, s.off, s.srt, s.ws)
+        lib.moe_expert_ffn(d, T, s.x, s.gu, s.dn, s.ones, s.off, s.srt, s.y, s.ws)
+        s.dw.copy_((s.y * s.up[:, None]).sum(-1))
+        lib.moe_balance_loss(d, T, s.lg, s.idx, s.mask, A, B, s.loss, s.bc, s.p, s.ws)
+        lib.moe_balance_loss_grad(d, T, s.lg, s.mask, s.bc, s.loss, A, B, s.one, s.dl)
+        lib.moe_router_grad(d, T, s.x, s.W, s.scale, s.pes, s.gain, s.lg, s.idx, s.mask, s.dw,
+                            s.dl, *s.g.values(), s.ws)
+
+
+def test_training_step_together():
+    s = _Step(150, 11)
+    note("router training step")
+    s.run()
+    torch.cuda.synchronize()
+    a = [ref.f64(t).requires_grad_(True) for t in (s.x, s.W, s.scale, s.pes, s.gain)]
+    idx = s.idx.cpu()
+    w, lg = ref.router_outputs(*a, idx, s.m.eps)
+    x = a[0].detach()  # the experts are frozen and their input is a constant here
+    gu, dn = ref.f64(s.gu)[idx.long()], ref.f64(s.dn)[idx.long()]
+    z = torch.einsum("tkih,th->tki", gu, x)
+    I = s.m.I
+    y = torch.einsum("tkhi,tki->tkh", dn, torch.nn.functional.gelu(
+        z[..., :I], approximate="tanh") * z[..., I:])
+    out = (w[..., None] * y).sum(1)
+    total = (out * ref.f64(s.up)).sum() + ref.balance(lg, idx, s.mask.cpu(), A, B)[0]
+    want = torch.autograd.grad(total, a)
+    for (k, got), ex in zip(s.g.items(), want):
+        assert rel_max_err(got.cpu().numpy(), ex.numpy()) <= F32_TOL, k
+
+
+def test_training_step_in_a_graph():
+    """Two captured steps that share one workspace, replayed with eager steps
+    and other inputs in between: every replay gives the eager bits."""
+    st = torch.cuda.Stream()
+    steps = [_Step(150, 21), _Step(90, 22)]
+    steps[1].ws = steps[0].ws
+    want = []
+    for s in steps:
+        s.run()
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in s.g.items()})
+    graphs = []
+    for s in steps:
+        with torch.cuda.stream(st):
+            s.run()
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        note("capture a router training step")
+        with torch.cuda.graph(gr, stream=st):
+            s.run()
+        graphs.append(gr)
+    for r in range(4):
+        for s, gr, w in zip(steps, graphs, want):
+            for v in s.g.values():
+                v.fill_(np.nan)
+            gr.replay()
+            torch.cuda.synchronize()
+            for k, v in w.items():
+                assert torch.equal(s.g[k], v), (r, k)
+        keep = steps[r % 2].x.clone()
+        steps[r % 2].x.mul_(0.5)
+        steps[r % 2].run()
+        torch.cuda.synchronize()
+        steps[r % 2].x.copy_(keep)
+
+
+def test_on_a_side_stream_and_twice():
+    """Two steps on two streams with their own workspaces at once."""
+    steps = [_Step(200, 31), _Step(130, 32)]
+    want = []
+    for s in steps:
+        s.run()
+        torch.cuda.synchronize()
+        want.append({k: v.clone() for k, v in s.g.items()})
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    note("two router training steps at once")
+    for _ in range(3):
+        for s, st in zip(steps, streams):
+            with torch.cuda.stream(st):
+                s.run()
+    torch.cuda.synchronize()
+    for s, w in zip(steps, want):
+        for k, v in w.items():
+            assert torch.equal(s.g[k], v), k
