@@ -402,6 +402,56 @@ int moe_expert_ffn_mx(const moe_dims* dims, int32_t fmt, int32_t T, const void* 
                       const int32_t* expert_offsets, const int32_t* sorted_slots, void* y_slots,
                       void* ws, size_t ws_bytes, void* stream);
 
+/* ---- E4M3 with one fp32 scale per block of 128 ----------------------------
+ *
+ * The 8-bit option of the same page with scales along both axes.  Weights: one
+ * scale per 128 x 128 block of an [out, in] matrix, blocks counted from the
+ * matrix's first row and column, the last ones partial where an axis is no
+ * multiple of 128 (of each matrix of a batch: an expert's fused gate_up
+ * [2I, H] is one matrix, its blocks run over the boundary between the gate
+ * and the up rows).  Activations: one scale per 128 consecutive values of a
+ * row, counted from the row's start.  value = E4M3(code) * scale.
+ *
+ * moe_quantize_b128: w is bf16 [batch, rows, cols], cols a multiple of 16 in
+ * [16, 65536].  block_rows = 128: weights, scale [batch, ceil(rows / 128),
+ * ceil(cols / 128)]; block_rows = 1: activations, scale [batch, rows,
+ * ceil(cols / 128)].  scale = max |v| / 448 over the block, code = E4M3 nearest
+ * to v / scale (fp32 divisions, ties to the even mantissa, 448 at most); a block
+ * of zeros gets scale 0 and codes 0.
+ * moe_dequantize_b128: the values, fp32 [batch, rows, cols], each product
+ * rounded once.  MOE_ERR_ARG for another block_rows, bad sizes or pointers. */
+int moe_quantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,
+                      const void* w, uint8_t* q, float* scale, void* stream);
+int moe_dequantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,
+                        const uint8_t* q, const float* scale, float* out, void* stream);
+
+/* y[t, n] = sum_k X[t, k] W[n, k], X what moe_quantize_b128(1, ...) makes of x
+ * [T, in_features] bf16 (done inside the call), W the value of the weights
+ * w_q [out_features, in_features], w_scale as above.  y [T, out_features] in
+ * y_dtype.  Products of a 128-block accumulate inside the 8-bit matrix
+ * instruction (which keeps each block's sum to about 2^-15 of the sum of the
+ * magnitudes it adds), the blocks in fp32.  T up to 65536, out_features up to
+ * 262144, in_features a multiple of 16 up to 16384.  ws:
+ * moe_linear_b128_workspace_size(T, in_features) bytes, 256-byte aligned (0: the
+ * sizes are not supported). */
+size_t moe_linear_b128_workspace_size(int32_t max_tokens, int32_t in_features);
+int moe_linear_b128(int32_t T, int32_t out_features, int32_t in_features, const void* x,
+                    const uint8_t* w_q, const float* w_scale, void* y, int32_t y_dtype, void* ws,
+                    size_t ws_bytes, void* stream);
+
+/* The experts in this format: moe_expert_ffn with the expert input quantized
+ * per 128 values, h = gelu_tanh(gate) * up quantized per 128 columns from its
+ * fp32 value, and the weights (gate_up [E, 2I, H] with scales [E, ceil(2I / 128),
+ * ceil(H / 128)], down [E, H, I] with scales [E, ceil(H / 128), ceil(I / 128)])
+ * multiplied in 8 bits.  act dtype bf16; every dims and T that moe_expert_ffn
+ * takes.  Up to 256 tokens with at most 16 rows per expert on average the
+ * weights are streamed per row tile, larger batches take tiled grouped GEMMs. */
+int moe_expert_ffn_b128(const moe_dims* dims, int32_t T, const void* x,
+                        const uint8_t* w_gate_up_q, const float* w_gate_up_scale,
+                        const uint8_t* w_down_q, const float* w_down_scale, const float* topk_w,
+                        const int32_t* expert_offsets, const int32_t* sorted_slots,
+                        void* y_slots, void* ws, size_t ws_bytes, void* stream);
+
 /* The experts' scatter-add: out[t] = sum_{k=0..K-1} y_slots[t,k] (fp32, k
  * ascending, no atomics) + addend[t] (if addend is not NULL).
  * y_slots slot dtype; addend and out act dtype. */

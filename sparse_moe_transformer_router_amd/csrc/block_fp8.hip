@@ -1,0 +1,732 @@
+// Products in E4M3 with one fp32 scale per block of 128: weights per 128 x 128
+// block, activations per 128 consecutive values of a row (quantized on the way
+// in).  An 8-bit storage option as on the page "Porting a 128-expert MoE
+// (Gemma-4 26B-A4B) to AWS Inferentia2" (section "The fp4 rabbit hole (two of
+// them, both dead ends)"), with scales fine enough for both operands to stay
+// in 8 bits:
+//
+//   y_tn = sum_b sx[t, b] sw[n / 128, b] sum_{k in block b} xq_tk wq_nk
+//
+// The inner sum of a 128-block is one v_mfma_f32_16x16x128_f8f6f4 with a zero
+// addend; its four results per lane are scaled and added in fp32 registers.
+// The weights are the instruction's first operand, so a lane's results are four
+// consecutive output columns of ONE token: one scale product per token tile
+// and weight block, 4 fused multiply-adds per instruction (16 of its 32 cycles
+// on the vector unit, which runs beside the matrix unit).
+//
+// Operand layout (8-bit, 16 x 128): lane l holds row l % 16 and, with g = l /
+// 16, k = 16 g .. 16 g + 15 and k = 64 + 16 g .. 64 + 16 g + 15.  Result: lane
+// l, register r is row 4 g + r of the first operand, row l % 16 of the second.
+#include <type_traits>
+
+#include "common.h"
+#include "launch.h"
+#include "wformat.h"
+
+namespace moe {
+namespace {
+
+typedef int i32x8 __attribute__((ext_vector_type(8)));
+
+constexpr int kBlk = 128;              // values that share a scale
+constexpr float kE4m3Max = 448.0f;
+constexpr uint32_t kUnitScale = 127;   // E8M0 code of 1.0
+
+__host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
+
+// The sum of 128 products per result, from zero.
+__device__ __forceinline__ f32x4 mfma_blk(i32x8 w, i32x8 x) {
+  return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+      w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, (int)kUnitScale, 0, (int)kUnitScale);
+}
+
+// Maximum over the 16 lanes of a DPP row, in every lane.
+template <int CTRL>
+__device__ __forceinline__ float dpp_f(float v) {
+  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+}
+__device__ __forceinline__ float row16_max(float v) {
+  v = fmaxf(v, dpp_f<0xB1>(v));   // lane ^ 1
+  v = fmaxf(v, dpp_f<0x4E>(v));   // lane ^ 2
+  v = fmaxf(v, dpp_f<0x141>(v));  // mirror of 8
+  return fmaxf(v, dpp_f<0x140>(v));
+}
+
+// E4M3 codes of four values already divided by their scale: nearest, ties to
+// even; the quotient of the largest value may round past 448 and is clamped.
+__device__ __forceinline__ uint32_t encode4(float a, float b, float c, float d) {
+  auto cl = [](float v) { return fminf(fmaxf(v, -kE4m3Max), kE4m3Max); };
+  int w = __builtin_amdgcn_cvt_pk_fp8_f32(cl(a), cl(b), 0, false);
+  return (uint32_t)__builtin_amdgcn_cvt_pk_fp8_f32(cl(c), cl(d), w, true);
+}
+
+__device__ __forceinline__ void ld8(const bf16* p, float (&v)[8]) {
+  const uint4 u = *reinterpret_cast<const uint4*>(p);
+  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(w[i] << 16);
+    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
+  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
+  v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+  v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+}
+__device__ __forceinline__ float amax8(const float (&v)[8]) {
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  return m;
+}
+// 8 codes of v / s (s = 0: zeros).
+__device__ __forceinline__ uint2 encode8(const float (&v)[8], float s) {
+  float q[8];
+#pragma unroll
+  for (int i = 0; i < 8; ++i) q[i] = s > 0.0f ? v[i] / s : 0.0f;
+  return make_uint2(encode4(q[0], q[1], q[2], q[3]), encode4(q[4], q[5], q[6], q[7]));
+}
+
+// Rows: scale = max |v| / 448 per 128 values, code = E4M3 nearest to v / scale
+// (fp32 divisions).  16 lanes a group, 8 values a lane.
+template <typename XT>
+__global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, int cols,
+                                                               const XT* __restrict__ in,
+                                                               uint8_t* __restrict__ q,
+                                                               float* __restrict__ scale) {
+  const int nb = blocks_of(cols);
+  const long long grp = ((long long)blockIdx.x * 256 + threadIdx.x) / 16;
+  if (grp >= rows * nb) return;  // 16 lanes alike
+  const int l = threadIdx.x % 16;
+  const long long r = grp / nb;
+  const int c = (int)(grp % nb) * kBlk + 8 * l;
+  float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+  if (c < cols) ld8(in + r * cols + c, v);
+  const float s = row16_max(amax8(v)) / kE4m3Max;
+  if (l == 0) scale[grp] = s;
+  if (c < cols) *reinterpret_cast<uint2*>(q + r * cols + c) = encode8(v, s);
+}
+
+// 128 x 128 blocks of [batch, rows, cols]: one workgroup a block, 8 values of 8
+// rows a thread.
+__global__ __launch_bounds__(256) void quantize_blocks128_kernel(int rows, int cols,
+                                                                 const bf16* __restrict__ in,
+                                                                 uint8_t* __restrict__ q,
+                                                                 float* __restrict__ scale) {
+  __shared__ float red[4];
+  const int cb = blockIdx.x, rb = blockIdx.y;
+  const long long b = blockIdx.z;
+  const bf16* src = in + b * rows * cols;
+  uint8_t* dst = q + b * rows * cols;
+  const int c = cb * kBlk + 8 * (threadIdx.x % 16), r0 = rb * kBlk + threadIdx.x / 16;
+  float v[8][8];
+  float m = 0.0f;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
+    if (r < rows && c < cols) ld8(src + (long long)r * cols + c, v[i]);
+    m = fmaxf(m, amax8(v[i]));
+  }
+  m = wave_max(m);
+  if (lane_id() == 0) red[threadIdx.x / kWave] = m;
+  __syncthreads();
+  const float s = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / kE4m3Max;
+  if (threadIdx.x == 0) scale[(b * gridDim.y + rb) * gridDim.x + cb] = s;
+#pragma unroll
+  for (int i = 0; i < 8; ++i) {
+    const int r = r0 + 16 * i;
+    if (r < rows && c < cols)
+      *reinterpret_cast<uint2*>(dst + (long long)r * cols + c) = encode8(v[i], s);
+  }
+}
+
+// Codes times their scale, one rounding: 8 values a thread.
+__global__ __launch_bounds__(256) void dequantize_b128_kernel(long long total_rows, int rows,
+                                                              int cols, int block_rows,
+                                                              const uint8_t* __restrict__ q,
+                                                              const float* __restrict__ scale,
+                                                              float* __restrict__ out) {
+  const long long i = (long long)blockIdx.x * 256 + threadIdx.x;
+  const int per = cols / 8, nb = blocks_of(cols);
+  if (i >= total_rows * per) return;
+  const long long r = i / per;
+  const int c = 8 * (int)(i % per);
+  const long long b = r / rows;
+  const int sr = (rows + block_rows - 1) / block_rows;
+  const float s = scale[(b * sr + (int)(r % rows) / block_rows) * nb + c / kBlk];
+  const uint2 u = *reinterpret_cast<const uint2*>(q + r * cols + c);
+  float v[8];
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {
+    uint32_t lo, hi;
+    fp8x4_to_bf16(h == 0 ? u.x : u.y, lo, hi);
+    v[4 * h] = __uint_as_float(lo << 16) * s;
+    v[4 * h + 1] = __uint_as_float(lo & 0xffff0000u) * s;
+    v[4 * h + 2] = __uint_as_float(hi << 16) * s;
+    v[4 * h + 3] = __uint_as_float(hi & 0xffff0000u) * s;
+  }
+  float4* o = reinterpret_cast<float4*>(out + r * cols + c);
+  o[0] = make_float4(v[0], v[1], v[2], v[3]);
+  o[1] = make_float4(v[4], v[5], v[6], v[7]);
+}
+
+// ---------------------------------------------------------------------------
+// Shared by both products.
+// ---------------------------------------------------------------------------
+constexpr int kGateUp = 0, kPlain = 1;
+
+// Where lane group g's two 16-byte halves of k-block kb lie in a row of Kd
+// values, moved to the row's start where they pass its end (v0, v1: inside).
+__device__ __forceinline__ void spans(int kb, int g, int Kd, int& o0, int& o1, bool& v0,
+                                      bool& v1) {
+  const int a = kb * kBlk + 16 * g, b = a + 64;
+  v0 = a + 16 <= Kd;
+  v1 = b + 16 <= Kd;
+  o0 = v0 ? a : 0;
+  o1 = v1 ? b : 0;
+}
+__device__ __forceinline__ i32x8 pack8(uint4 a, uint4 b) {
+  return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
+}
+__device__ __forceinline__ i32x8 ld32(const uint8_t* row, int o0, int o1) {
+  return pack8(*reinterpret_cast<const uint4*>(row + o0),
+               *reinterpret_cast<const uint4*>(row + o1));
+}
+__device__ __forceinline__ i32x8 keep32(i32x8 v, bool v0, bool v1) {
+  return i32x8{v0 ? v[0] : 0, v0 ? v[1] : 0, v0 ? v[2] : 0, v0 ? v[3] : 0,
+               v1 ? v[4] : 0, v1 ? v[5] : 0, v1 ? v[6] : 0, v1 ? v[7] : 0};
+}
+
+// Four consecutive outputs of a row of N columns from column n.
+template <typename YT>
+__device__ __forceinline__ void store4(YT* __restrict__ row, int n, int N, f32x4 v) {
+  if (N % 4 == 0) {
+    if (n >= N) return;
+    if constexpr (std::is_same<YT, float>::value) {
+      *reinterpret_cast<f32x4*>(row + n) = v;
+    } else {
+      typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
+      *reinterpret_cast<bf16x4*>(row + n) =
+          bf16x4{(bf16)v[0], (bf16)v[1], (bf16)v[2], (bf16)v[3]};
+    }
+    return;
+  }
+#pragma unroll
+  for (int r = 0; r < 4; ++r)
+    if (n + r < N) row[n + r] = from_f32<YT>(v[r]);
+}
+
+// ---------------------------------------------------------------------------
+// Few rows per group: the weights streamed from HBM into registers once per
+// tile of 16 MB rows.  A block is one row tile x WN waves of NC tiles of 16
+// columns (gate_up: NC gate and the matching NC up tiles), times WK waves that
+// split the contraction in 128-blocks and are added through LDS.  Loads run
+// NS - 1 blocks ahead, unconditionally (addresses clamped into their rows), so
+// that a step waits for its own slot alone.
+// ---------------------------------------------------------------------------
+template <int MODE, int WK, int WN, int MB, int NC, int NS, typename YT>
+__global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
+  constexpr int NW = MODE == kGateUp ? 2 * NC : NC;  // weight tiles per wave
+  __shared__ f32x4 red[WK > 1 ? WK : 1][WN][MB][NW][WK > 1 ? kWave : 1];
+  int e, row0, row1, cg;
+  const int CG = (a.N + 16 * WN * NC - 1) / (16 * WN * NC);
+  if (!stream_item(a.ident, a.rows, a.offsets, a.E, 16 * MB, CG, e, row0, row1, cg)) return;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wk = wave % WK, wn = wave / WK;
+  const int fr = lane % 16, g = lane / 16;
+  const int Kd = a.Kd, KB = blocks_of(Kd);
+  const int NR = MODE == kGateUp ? 2 * a.N : a.N;
+  const int n0 = (cg * WN + wn) * 16 * NC;
+  const uint8_t* wrow[NW];
+  const float* wsc[NW];
+#pragma unroll
+  for (int c = 0; c < NW; ++c) {
+    const int first = n0 + 16 * (c % NC), up = c >= NC ? a.N : 0;
+    const int r = up + min(first + fr, a.N - 1);
+    wrow[c] = a.wq + ((long long)e * NR + r) * Kd;
+    wsc[c] = a.wscale +
+             ((long long)e * blocks_of(NR) + (up + min(first, a.N - 1)) / kBlk) * KB;
+  }
+  const int nmb = (row1 - row0 + 15) / 16;
+  const uint8_t* xrow[MB];
+  const float* xsc[MB];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    const int r = row0 + 16 * mb + fr;
+    long long t = r < row1 ? r : row0;
+    if (MODE == kGateUp) t = a.sorted_slots[t] / a.K;
+    xrow[mb] = a.xq + t * Kd;
+    xsc[mb] = a.xscale + t * KB;
+  }
+  const int kb0 = wk * KB / WK, kb1 = (wk + 1) * KB / WK;
+
+  f32x4 acc[MB][NW];
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+    for (int c = 0; c < NW; ++c) acc[mb][c] = f32x4{0, 0, 0, 0};
+  i32x8 rx[NS][MB], rw[NS][NW];
+  float sx[NS][MB], sw[NS][NW];
+  auto load = [&](int kb, int slot) {
+    int o0, o1;
+    bool v0, v1;
+    spans(kb, g, Kd, o0, o1, v0, v1);
+#pragma unroll
+    for (int c = 0; c < NW; ++c) rw[slot][c] = ld32(wrow[c], o0, o1);
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb) {
+      rx[slot][mb] = ld32(xrow[mb], o0, o1);
+      sx[slot][mb] = xsc[mb][kb];
+    }
+#pragma unroll
+    for (int c = 0; c < NW; ++c) sw[slot][c] = wsc[c][kb];
+  };
+  auto step = [&](int slot, int kb, auto checked) {
+    if (decltype(checked)::value && (kb + 1) * kBlk > Kd) {  // uniform
+      int o0, o1;
+      bool v0, v1;
+      spans(kb, g, Kd, o0, o1, v0, v1);
+#pragma unroll
+      for (int mb = 0; mb < MB; ++mb) rx[slot][mb] = keep32(rx[slot][mb], v0, v1);
+#pragma unroll
+      for (int c = 0; c < NW; ++c) rw[slot][c] = keep32(rw[slot][c], v0, v1);
+    }
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+      if (mb == 0 || mb < nmb) {
+        f32x4 d[NW];
+#pragma unroll
+        for (int c = 0; c < NW; ++c) d[c] = mfma_blk(rw[slot][c], rx[slot][mb]);
+#pragma unroll
+        for (int c = 0; c < NW; ++c) {
+          const float s = sx[slot][mb] * sw[slot][c];
+#pragma unroll
+          for (int r = 0; r < 4; ++r) acc[mb][c][r] = __builtin_fmaf(d[c][r], s, acc[mb][c][r]);
+        }
+      }
+  };
+#pragma unroll
+  for (int s = 0; s < NS - 1; ++s) {
+    load(max(min(kb0 + s, kb1 - 1), 0), s);
+    __builtin_amdgcn_sched_barrier(0);
+  }
+  int kb = kb0;
+  const int kbf = min(kb1, Kd / kBlk);
+  for (; kb + 2 * NS - 2 < kbf; kb += NS) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      load(kb + s + NS - 1, (s + NS - 1) % NS);
+      __builtin_amdgcn_sched_barrier(0);
+      step(s, kb + s, std::false_type{});
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  }
+  for (; kb < kb1; kb += NS) {
+#pragma unroll
+    for (int s = 0; s < NS; ++s) {
+      if (kb + s >= kb1) break;
+      if (kb + s + NS - 1 < kb1) load(kb + s + NS - 1, (s + NS - 1) % NS);
+      step(s, kb + s, std::true_type{});
+    }
+  }
+  if constexpr (WK > 1) {
+#pragma unroll
+    for (int mb = 0; mb < MB; ++mb)
+#pragma unroll
+      for (int c = 0; c < NW; ++c) red[wk][wn][mb][c][lane] = acc[mb][c];
+    __syncthreads();
+  }
+  // the WK waves of a column group take its tiles in turn
+#pragma unroll
+  for (int mb = 0; mb < MB; ++mb) {
+    if (mb >= nmb) break;
+    const int row = row0 + 16 * mb + fr;
+#pragma unroll
+    for (int c = 0; c < NC; ++c) {
+      if (WK > 1 && (mb * NC + c) % WK != wk) continue;
+      const int n = n0 + 16 * c + 4 * g;
+      f32x4 v = acc[mb][c], u = {0, 0, 0, 0};
+      if constexpr (MODE == kGateUp) u = acc[mb][NC + c];
+      if constexpr (WK > 1) {
+        v = red[0][wn][mb][c][lane];
+        if constexpr (MODE == kGateUp) u = red[0][wn][mb][NC + c][lane];
+#pragma unroll
+        for (int w = 1; w < WK; ++w) {
+          v += red[w][wn][mb][c][lane];
+          if constexpr (MODE == kGateUp) u += red[w][wn][mb][NC + c][lane];
+        }
+      }
+      if (row >= row1) continue;
+      if constexpr (MODE == kGateUp) {
+#pragma unroll
+        for (int r = 0; r < 4; ++r) v[r] = gelu_tanh(v[r]) * u[r];
+        store4(a.h + (size_t)row * a.N, n, a.N, v);
+      } else {
+        size_t to = row;
+        if (!a.ident) {
+          to = a.sorted_slots[row];
+          v *= a.topk_w[to];
+        }
+        store4(static_cast<YT*>(a.y) + to * a.N, n, a.N, v);
+      }
+    }
+  }
+}
+
+// ---------------------------------------------------------------------------
+// Many rows per group: tiles of 256 rows x 256 weight rows (gate_up: 128 gate
+// and the matching 128 up), 8 waves (2 x 4) of 128 x 64, on k-tiles of one
+// 128-block.  Both operands go global -> LDS directly into two stages of 64
+// KB: stage s is refilled once every wave has read it.  A line is a row's 128
+// bytes; its 16-byte chunk c sits at position c ^ (line % 8), so the 16 rows
+// that a fragment load touches spread over the banks.  The scales of up to
+// kTileBlocks k-blocks sit in LDS beside the ring, reloaded when those are
+// used up.  A wave multiplies one 16-row tile of activations by its four
+// weight tiles, and scales the previous tile's results meanwhile.
+// ---------------------------------------------------------------------------
+constexpr int kTM = 256, kTN = 256, kTileWaves = 8;
+constexpr int kTileBlocks = 23;
+constexpr int kStageBytes = (kTM + kTN) * kBlk;
+constexpr int kRingBytes = 2 * kStageBytes;
+constexpr int kScaleOff = kRingBytes;                               // [kTileBlocks][256]
+constexpr int kWScaleOff = kScaleOff + kTileBlocks * kTM * 4;       // [kTileBlocks][4]
+constexpr int kTabOff = kWScaleOff + kTileBlocks * 4 * 4;           // rtok, slot, weight
+constexpr int kTileLds = kTabOff + 3 * kTM * 4;
+constexpr int kHPitch = kTN / 2 + 4;                                // floats
+static_assert(kTM * kHPitch * 4 <= kTabOff, "h is staged over the ring and the scales");
+static_assert(kTileLds <= 160 * 1024, "LDS per CU");
+
+template <int MODE, typename YT>
+__global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args a) {
+  constexpr int TI = 8, TJ = 4;       // 16-row tiles of activations, weight tiles per wave
+  constexpr int COPIES = kStageBytes / (64 * kTileWaves * 16);
+  extern __shared__ __align__(16) unsigned char smem[];
+  const int Kd = a.Kd, KB = blocks_of(Kd), N = a.N;
+  const int NR = MODE == kGateUp ? 2 * N : N;
+  constexpr int COLS = MODE == kGateUp ? kTN / 2 : kTN;  // output columns per tile
+  const int NT = (N + COLS - 1) / COLS;
+  int e = 0, row0, row1, nt;
+  if (a.ident) {
+    const int RT = (a.rows + kTM - 1) / kTM;
+    const int item = xcd_item(blockIdx.x, RT * NT);
+    if (item < 0) return;  // uniform over the block
+    nt = item / RT;
+    row0 = item % RT * kTM;
+    row1 = min(row0 + kTM, a.rows);
+  } else {
+    RowTileScan sc;
+    row_tile_scan(a.offsets, a.E, kTM, sc);
+    const int item = xcd_item(blockIdx.x, sc.total * NT);
+    if (item < 0) return;
+    weight_major_item(sc, a.offsets, kTM, item, NT, e, row0, row1, nt);
+    e = __builtin_amdgcn_readfirstlane(e);
+    row0 = __builtin_amdgcn_readfirstlane(row0);
+    row1 = __builtin_amdgcn_readfirstlane(row1);
+    nt = __builtin_amdgcn_readfirstlane(nt);
+  }
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int wm = wave / 4, wn = wave % 4;
+  const int nbase = nt * COLS;
+  float* s_x = reinterpret_cast<float*>(smem + kScaleOff);
+  float* s_w = reinterpret_cast<float*>(smem + kWScaleOff);
+  int* rtok = reinterpret_cast<int*>(smem + kTabOff);
+  int* row_slot = rtok + kTM;
+  float* row_w = reinterpret_cast<float*>(row_slot + kTM);
+  if (tid < kTM) {
+    const int r = min(row0 + tid, row1 - 1);  // rows past the tile repeat its last: dropped
+    rtok[tid] = MODE == kGateUp ? a.sorted_slots[r] / a.K : r;
+    if constexpr (MODE == kPlain) {
+      const int slot = a.ident ? r : a.sorted_slots[r];
+      row_slot[tid] = slot;
+      row_w[tid] = a.ident ? 1.0f : a.topk_w[slot];
+    }
+  }
+  __syncthreads();
+  const uint8_t* wbase = a.wq + (long long)e * NR * Kd;
+  // tile row n of the weights: its row in the expert's matrix (past the last
+  // column a valid row, whose outputs are dropped)
+  auto wrow = [&](int n) {
+    const bool up = MODE == kGateUp && n >= kTN / 2;
+    const int col = min(nbase + n - (up ? kTN / 2 : 0), N - 1);
+    return col + (up ? N : 0);
+  };
+  // Copy j of wave w fills lines 8 (8 j + w) .. + 7 of a stage: activations for
+  // j < 4, weights past that.  Sources in 16-byte units (a tensor of 2^36
+  // bytes fits 32 bits).
+  unsigned src[COPIES];
+  const int chunk = (lane % 8) ^ (lane / 8);
+#pragma unroll
+  for (int j = 0; j < COPIES; ++j) {
+    const int line = 8 * (kTileWaves * j + wave) + lane / 8;
+    const unsigned row = j < COPIES / 2 ? (unsigned)rtok[line] : (unsigned)wrow(line - kTM);
+    src[j] = row * (unsigned)(Kd / 16);
+  }
+  auto copy = [&](int kt) {
+    const unsigned k16 = min(kt * 8 + chunk, Kd / 16 - 1);  // past the row: its last chunk
+#pragma unroll
+    for (int j = 0; j < COPIES; ++j) {
+      const uint8_t* base = j < COPIES / 2 ? a.xq : wbase;
+#if defined(__HIP_DEVICE_COMPILE__)
+      lds_copy16(base + (size_t)(src[j] + k16) * 16,
+                 smem + (kt & 1) * kStageBytes + (kTileWaves * j + wave) * 1024);
+#endif
+    }
+  };
+  // scales of k-blocks [kb0, kb0 + n): activations [kb][256], weights [kb][4]
+  // (gate_up: the gate block and the up rows' two; otherwise the two blocks)
+  const float* wsbase = a.wscale + (long long)e * blocks_of(NR) * KB;
+  const int wblk0 = nbase / kBlk, wblk_up = (N + nbase) / kBlk;
+  auto load_scales = [&](int kb0) {
+    const int n = min(kTileBlocks, KB - kb0);
+    for (int i = tid; i < n * kTM; i += 64 * kTileWaves) {
+      const int r = i % kTM, kb = i / kTM;
+      s_x[i] = a.xscale[(long long)rtok[r] * KB + kb0 + kb];
+    }
+    for (int i = tid; i < n * 4; i += 64 * kTileWaves) {
+      const int kb = i / 4, w = i % 4;
+      const int blk = MODE == kGateUp && w >= 2 ? wblk_up + w - 2 : wblk0 + w;
+      s_w[i] = wsbase[(long long)min(blk, blocks_of(NR) - 1) * KB + kb0 + kb];
+    }
+  };
+  // this wave's weight tiles: their scale slots (the two halves of a gate_up
+  // wave, else one), fragment offsets
+  const int fr = lane % 16, g = lane / 16;
+  int ws0, ws1;
+  if constexpr (MODE == kGateUp) {
+    ws0 = 0;  // 128 gate columns from a multiple of 128
+    ws1 = 2 + (N + min(nbase + 32 * wn, N - 32)) / kBlk - wblk_up;
+  } else {
+    ws0 = ws1 = wn / 2;
+  }
+  int woff[TJ];
+#pragma unroll
+  for (int j = 0; j < TJ; ++j) {
+    int n;
+    if constexpr (MODE == kGateUp) n = (j / 2) * (kTN / 2) + wn * 32 + (j % 2) * 16 + fr;
+    else n = wn * 64 + j * 16 + fr;
+    const int line = kTM + n;
+    woff[j] = line * kBlk + (g ^ (line & 7)) * 16;
+  }
+  const int xline = wm * 128 + fr;
+  const int xoff = xline * kBlk + (g ^ (xline & 7)) * 16;  // tile i: + i * 16 * kBlk
+  int nv = (row1 - row0 - wm * 128 + 15) / 16;             // tiles of this wave with rows
+  nv = __builtin_amdgcn_readfirstlane(max(0, min(TI, nv)));
+
+  f32x4 acc[TI][TJ];
+#pragma unroll
+  for (int i = 0; i < TI; ++i)
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+
+  copy(0);
+  if (KB > 1) copy(1);
+  else copy(0);  // the same bytes again: the waits below count on two stages
+  for (int kt = 0; kt < KB; ++kt) {
+    const int kl = kt % kTileBlocks;
+    if (kl == 0) {
+      __syncthreads();  // the scales of the blocks before are used up
+      load_scales(kt);
+    }
+    wait_vmem<COPIES>();  // tile kt landed (this wave's copies)
+    __syncthreads();      // ... everyone's, and the scales
+    const unsigned char* st = smem + (kt & 1) * kStageBytes;
+    auto rd = [&](int off) {
+      return pack8(*reinterpret_cast<const uint4*>(st + off),
+                   *reinterpret_cast<const uint4*>(st + (off ^ 64)));
+    };
+    const bool tail = (kt + 1) * kBlk > Kd;  // uniform
+    int o0, o1;
+    bool v0, v1;
+    spans(kt, g, Kd, o0, o1, v0, v1);
+    i32x8 fw[TJ];
+#pragma unroll
+    for (int j = 0; j < TJ; ++j) {
+      fw[j] = rd(woff[j]);
+      if (tail) fw[j] = keep32(fw[j], v0, v1);
+    }
+    const float sw0 = s_w[kl * 4 + ws0], sw1 = s_w[kl * 4 + ws1];
+    f32x4 d[2][TJ];
+    auto scale_add = [&](int i, int buf) {
+      const float sx = s_x[kl * kTM + xline + 16 * i];
+      const float s0 = sx * sw0, s1 = sx * sw1;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j) {
+        const float s = j < TJ / 2 ? s0 : s1;
+#pragma unroll
+        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[buf][j][r], s, acc[i][j][r]);
+      }
+    };
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      if (i < nv) {  // uniform: tiles past the group's rows are skipped
+        i32x8 fx = rd(xoff + i * 16 * kBlk);
+        if (tail) fx = keep32(fx, v0, v1);
+#pragma unroll
+        for (int j = 0; j < TJ; ++j) d[i & 1][j] = mfma_blk(fw[j], fx);
+      }
+      if (i > 0 && i - 1 < nv) scale_add(i - 1, (i - 1) & 1);
+    }
+    if (TI - 1 < nv) scale_add(TI - 1, (TI - 1) & 1);
+    wait_lds();
+    block_barrier();  // every wave has read stage kt: it can be refilled
+    copy(min(kt + 2, KB - 1) == kt + 2 ? kt + 2 : kt);
+  }
+  wait_vmem<0>();
+  __syncthreads();
+
+  if constexpr (MODE == kGateUp) {
+    // h = GELU(gate) * up in fp32, staged row-major; then 128 columns of a row
+    // share a scale: 4 lanes a row, 32 columns a lane
+    float* hs = reinterpret_cast<float*>(smem);
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      if (i >= nv) break;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) {
+        const int c = wn * 32 + 16 * j + 4 * g;
+        f32x4 v;
+#pragma unroll
+        for (int r = 0; r < 4; ++r)
+          v[r] = nbase + c + r < N ? gelu_tanh(acc[i][j][r]) * acc[i][2 + j][r] : 0.0f;
+        *reinterpret_cast<f32x4*>(hs + (xline + 16 * i) * kHPitch + c) = v;
+      }
+    }
+    __syncthreads();
+    const int nbh = blocks_of(N);
+#pragma unroll
+    for (int it = 0; it < kTM * 4 / (64 * kTileWaves); ++it) {
+      const int k = tid + it * 64 * kTileWaves, r = k / 4, c = 32 * (k % 4);
+      const bool on = row0 + r < row1;
+      float v[32];
+      float m = 0.0f;
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float4 f = *reinterpret_cast<const float4*>(hs + r * kHPitch + c + 4 * i);
+        v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
+      }
+#pragma unroll
+      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
+      m = fmaxf(m, dpp_f<0xB1>(m));
+      m = fmaxf(m, dpp_f<0x4E>(m));
+      const float s = m / kE4m3Max;
+      if (!on || nbase + c >= N) continue;
+      uint32_t q[8];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        float t[4];
+#pragma unroll
+        for (int u = 0; u < 4; ++u) t[u] = s > 0.0f ? v[4 * i + u] / s : 0.0f;
+        q[i] = encode4(t[0], t[1], t[2], t[3]);
+      }
+      uint4* dst = reinterpret_cast<uint4*>(a.hq + (size_t)(row0 + r) * N + nbase + c);
+      dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
+      dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
+      if (c == 0) a.hscale[(size_t)(row0 + r) * nbh + nbase / kBlk] = s;
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < TI; ++i) {
+      if (i >= nv) break;
+      const int r = xline + 16 * i;
+      if (row0 + r >= row1) continue;
+      const float w = row_w[r];
+      YT* out = static_cast<YT*>(a.y) + (size_t)row_slot[r] * N;
+#pragma unroll
+      for (int j = 0; j < TJ; ++j)
+        store4(out, nbase + wn * 64 + 16 * j + 4 * g, N, acc[i][j] * w);
+    }
+  }
+}
+
+template <int MODE, int WK, int WN, int MB, int NC, int NS, typename YT>
+hipError_t launch_stream(const B128Args& a, hipStream_t s) {
+  const long long cgs = (a.N + 16 * WN * NC - 1) / (16 * WN * NC);
+  const long long grid = cgs * tile_count_bound(a.ident, a.rows, a.T, a.E, 16 * MB);
+  hipLaunchKernelGGL((stream_b128_kernel<MODE, WK, WN, MB, NC, NS, YT>), dim3((unsigned)grid),
+                     dim3(64 * WK * WN), 0, s, a);
+  return hipGetLastError();
+}
+
+template <int MODE, typename YT>
+hipError_t launch_tile(const B128Args& a, hipStream_t s) {
+  auto kf = tile_b128_kernel<MODE, YT>;
+  // set on every call: the attribute belongs to the current device
+  const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kf),
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds);
+  if (e != hipSuccess) return e;
+  const int COLS = MODE == kGateUp ? kTN / 2 : kTN;
+  const long long grid = (long long)tile_count_bound(a.ident, a.rows, a.T, a.E, kTM) *
+                         ((a.N + COLS - 1) / COLS);
+  hipLaunchKernelGGL(kf, dim3((unsigned)grid), dim3(64 * kTileWaves), kTileLds, s, a);
+  return hipGetLastError();
+}
+
+template <typename XT>
+hipError_t quantize_rows(long long rows, int cols, const void* x, uint8_t* q, float* scale,
+                         hipStream_t s) {
+  const long long lanes = rows * blocks_of(cols) * 16;
+  hipLaunchKernelGGL(quantize_rows128_kernel<XT>, dim3((unsigned)((lanes + 255) / 256)), dim3(256),
+                     0, s, rows, cols, static_cast<const XT*>(x), q, scale);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_quantize_b128(int block_rows, long long batch, int rows, int cols, const void* w,
+                                uint8_t* q, float* scale, hipStream_t s) {
+  if (block_rows == 1) return quantize_rows<bf16>(batch * rows, cols, w, q, scale, s);
+  // the grid's z axis holds 65535 matrices at a time
+  const int rb = blocks_of(rows), cb = blocks_of(cols);
+  for (long long b = 0; b < batch; b += 65535) {
+    const unsigned nz = (unsigned)(batch - b < 65535 ? batch - b : 65535);
+    hipLaunchKernelGGL(quantize_blocks128_kernel, dim3(cb, rb, nz), dim3(256), 0, s, rows, cols,
+                       static_cast<const bf16*>(w) + b * rows * cols, q + b * rows * cols,
+                       scale + b * rb * cb);
+  }
+  return hipGetLastError();
+}
+
+hipError_t launch_dequantize_b128(int block_rows, long long batch, int rows, int cols,
+                                  const uint8_t* q, const float* scale, float* out,
+                                  hipStream_t s) {
+  const long long n = batch * rows * (cols / 8);
+  hipLaunchKernelGGL(dequantize_b128_kernel, dim3((unsigned)((n + 255) / 256)), dim3(256), 0, s,
+                     batch * rows, rows, cols, block_rows, q, scale, out);
+  return hipGetLastError();
+}
+
+bool b128_streams(int T, int rows, int E) { return T <= kB128StreamTokens && rows <= 16 * E; }
+
+// x quantized, y = x W^T.
+hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, float* xscale,
+                              bool y_bf16, hipStream_t s) {
+  hipError_t e = quantize_rows<bf16>(a.rows, a.Kd, x, xq, xscale, s);
+  if (e != hipSuccess) return e;
+  if (a.rows <= 128)
+    return y_bf16 ? launch_stream<kPlain, 4, 1, 1, 1, 2, bf16>(a, s)
+                  : launch_stream<kPlain, 4, 1, 1, 1, 2, float>(a, s);
+  return y_bf16 ? launch_tile<kPlain, bf16>(a, s) : launch_tile<kPlain, float>(a, s);
+}
+
+// x quantized; h = GELU(gate) * up, quantized; y = topk_w * down h.  gu and dn
+// are the two products' arguments.
+hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,
+                                  uint8_t* xq, float* xscale, bool y_bf16, hipStream_t s) {
+  hipError_t e = quantize_rows<bf16>(gu.T, gu.Kd, x, xq, xscale, s);
+  if (e != hipSuccess) return e;
+  if (b128_streams(gu.T, gu.rows, gu.E)) {
+    if ((e = launch_stream<kGateUp, 4, 1, 1, 2, 2, float>(gu, s)) != hipSuccess) return e;
+    if ((e = quantize_rows<float>(gu.rows, gu.N, gu.h, gu.hq, gu.hscale, s)) != hipSuccess)
+      return e;
+    return y_bf16 ? launch_stream<kPlain, 1, 4, 1, 1, 2, bf16>(dn, s)
+                  : launch_stream<kPlain, 1, 4, 1, 1, 2, float>(dn, s);
+  }
+  if ((e = launch_tile<kGateUp, float>(gu, s)) != hipSuccess) return e;
+  return y_bf16 ? launch_tile<kPlain, bf16>(dn, s) : launch_tile<kPlain, float>(dn, s);
+}
+
+}  // namespace moe

@@ -238,6 +238,39 @@ hipError_t launch_mx8_quantize(long long rows, int cols, const void* in, uint8_t
 hipError_t launch_mx8_dequantize(long long rows, int cols, const uint8_t* q, const uint8_t* e8,
                                  float* out, hipStream_t s);
 
+// E4M3 products with one fp32 scale per 128 x 128 weight block and per 128
+// activations (block_fp8.hip).  One group (ident: rows are the tokens) or E
+// groups of rows as in GateUpArgs.
+struct B128Args {
+  int T, rows, E, K;
+  int Kd;                      // contraction length, a multiple of 16
+  int N;                       // output columns (gate_up: the expert width)
+  bool ident;
+  const uint8_t* xq;           // [., Kd] codes of the input rows
+  const float* xscale;         // [., ceil(Kd / 128)]
+  const uint8_t* wq;           // [E, N or 2N, Kd]
+  const float* wscale;         // [E, ceil(N or 2N / 128), ceil(Kd / 128)]
+  const int32_t* offsets;      // [E+1] (unused when ident)
+  const int32_t* sorted_slots; // [rows] (unused when ident)
+  const float* topk_w;         // [rows] (down only)
+  float* h;                    // [rows, N] (gate_up, few rows per group)
+  uint8_t* hq;                 // [rows, N] codes of h (gate_up)
+  float* hscale;               // [rows, ceil(N / 128)]
+  void* y;                     // [rows, N] (down, linear)
+};
+// Few rows per group: the weight-streaming kernels; h then goes through fp32.
+constexpr int kB128StreamTokens = 256;
+bool b128_streams(int T, int rows, int E);
+hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, float* xscale,
+                              bool y_bf16, hipStream_t s);
+hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,
+                                  uint8_t* xq, float* xscale, bool y_bf16, hipStream_t s);
+hipError_t launch_quantize_b128(int block_rows, long long batch, int rows, int cols, const void* w,
+                                uint8_t* q, float* scale, hipStream_t s);
+hipError_t launch_dequantize_b128(int block_rows, long long batch, int rows, int cols,
+                                  const uint8_t* q, const float* scale, float* out,
+                                  hipStream_t s);
+
 struct CombineArgs {
   int T, H, K;
   bool y_bf16, act_bf16;

@@ -94,10 +94,12 @@ struct Layout {
   size_t counter;                   // small-batch top-K completion counter
   size_t base_end;                  // end of the regions above (all but the MXFP8 ones)
   size_t xq, xs, hq, hs;            // MXFP8 activations of the 8-bit / 4-bit experts
-  // The training calls' scratch shares the bytes past base_end with the MXFP8
-  // activations: a workspace serves one call at a time.
+  // The training calls' and the block-scaled experts' scratch shares the bytes
+  // past base_end with the MXFP8 activations: a workspace serves one call at a
+  // time.
   size_t bal_p, bal_n, bal_z, bal_live;      // balance loss
   size_t rg_dl, rg_beta, rg_g, rg_b, rg_pes; // router backward
+  size_t b_xq, b_xs, b_h, b_hq, b_hs;        // block-scaled E4M3 experts
   size_t total;
 };
 
@@ -150,6 +152,15 @@ Layout layout(const moe_dims* d, long long T) {
   L.rg_g = take(4 * splits * E * H);
   L.rg_b = take(4 * splits * H);
   L.rg_pes = take(4 * (size_t)moe::router_grad_row_blocks((int)T) * E);
+  if (o > L.total) L.total = o;
+  const size_t I = (size_t)d->expert_inter;
+  const size_t ts = (size_t)(T < moe::kB128StreamTokens ? T : moe::kB128StreamTokens);
+  o = L.base_end;
+  L.b_xq = take((size_t)T * H);
+  L.b_xs = take(4 * (size_t)T * ((H + 127) / 128));
+  L.b_h = take(4 * ts * d->top_k * I);  // fp32, the weight-streaming form only
+  L.b_hq = take((size_t)S * I);
+  L.b_hs = take(4 * (size_t)S * ((I + 127) / 128));
   if (o > L.total) L.total = o;
   return L;
 }
@@ -780,6 +791,129 @@ int moe_expert_ffn_mx(const moe_dims* dims, int32_t fmt, int32_t T, const void* 
   a.offsets = expert_offsets; a.sorted_slots = sorted_slots; a.topk_w = topk_w; a.y = y_slots;
   hipError_t e = moe::launch_expert_ffn_mx(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_mx");
+}
+
+namespace {
+
+// Shape of a block-scaled matrix batch.
+int check_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols) {
+  if (block_rows != 1 && block_rows != 128)
+    return fail(MOE_ERR_ARG, "block_rows=%d: need 1 or 128", block_rows);
+  if (batch < 0 || rows < 0 || batch > (int64_t)1 << 31 || rows > 1 << 21)
+    return fail(MOE_ERR_ARG, "batch or rows out of range");
+  if (cols < 16 || cols > 65536 || cols % 16)
+    return fail(MOE_ERR_ARG, "cols=%d: need a multiple of 16 in [16, 65536]", cols);
+  // a launch holds 2^31 groups of 16 values
+  if (batch * rows > ((int64_t)1 << 35) / cols)
+    return fail(MOE_ERR_UNSUPPORTED, "more than 2^35 values");
+  return MOE_OK;
+}
+
+int check_linear(int32_t T, int32_t out_features, int32_t in_features) {
+  if (T < 0 || T > 65536) return fail(MOE_ERR_ARG, "T=%d: need 0..65536", T);
+  if (out_features < 1 || out_features > 1 << 18)
+    return fail(MOE_ERR_UNSUPPORTED, "out_features=%d: need 1..262144", out_features);
+  if (in_features < 16 || in_features > 16384 || in_features % 16)
+    return fail(MOE_ERR_UNSUPPORTED, "in_features=%d: need a multiple of 16 in [16, 16384]",
+                in_features);
+  return MOE_OK;
+}
+
+size_t linear_scale_offset(int32_t T, int32_t in_features) {
+  return align256((size_t)T * in_features);
+}
+
+}  // namespace
+
+int moe_quantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,
+                      const void* w, uint8_t* q, float* scale, void* stream) {
+  int rc;
+  if ((rc = check_b128(block_rows, batch, rows, cols))) return rc;
+  g_err.clear();
+  if (batch == 0 || rows == 0) return MOE_OK;
+  REQUIRE_PTR(w); REQUIRE_PTR(q); REQUIRE_PTR(scale);
+  hipError_t e = moe::launch_quantize_b128(block_rows, batch, rows, cols, w, q, scale,
+                                           static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_quantize_b128");
+}
+
+int moe_dequantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,
+                        const uint8_t* q, const float* scale, float* out, void* stream) {
+  int rc;
+  if ((rc = check_b128(block_rows, batch, rows, cols))) return rc;
+  g_err.clear();
+  if (batch == 0 || rows == 0) return MOE_OK;
+  REQUIRE_PTR(q); REQUIRE_PTR(scale); REQUIRE_PTR(out);
+  hipError_t e = moe::launch_dequantize_b128(block_rows, batch, rows, cols, q, scale, out,
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_dequantize_b128");
+}
+
+size_t moe_linear_b128_workspace_size(int32_t max_tokens, int32_t in_features) {
+  if (check_linear(max_tokens, 1, in_features) != MOE_OK) return 0;
+  return linear_scale_offset(max_tokens, in_features) +
+         align256(4 * (size_t)max_tokens * ((in_features + 127) / 128)) + 256;
+}
+
+int moe_linear_b128(int32_t T, int32_t out_features, int32_t in_features, const void* x,
+                    const uint8_t* w_q, const float* w_scale, void* y, int32_t y_dtype, void* ws,
+                    size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_linear(T, out_features, in_features))) return rc;
+  if (y_dtype != MOE_F32 && y_dtype != MOE_BF16)
+    return fail(MOE_ERR_ARG, "y_dtype=%d unknown", y_dtype);
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(w_q); REQUIRE_PTR(w_scale); REQUIRE_PTR(y);
+  if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
+  if (reinterpret_cast<uintptr_t>(ws) & 255u)
+    return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
+  const size_t need = moe_linear_b128_workspace_size(T, in_features);
+  if (ws_bytes < need)
+    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed for T=%d", ws_bytes, need,
+                T);
+  moe::B128Args a{};
+  a.T = T; a.rows = T; a.E = 1; a.K = 1; a.Kd = in_features; a.N = out_features; a.ident = true;
+  uint8_t* xq = at<uint8_t>(ws, 0);
+  float* xs = at<float>(ws, linear_scale_offset(T, in_features));
+  a.xq = xq; a.xscale = xs; a.wq = w_q; a.wscale = w_scale; a.y = y;
+  hipError_t e = moe::launch_linear_b128(a, x, xq, xs, y_dtype == MOE_BF16,
+                                         static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_linear_b128");
+}
+
+int moe_expert_ffn_b128(const moe_dims* dims, int32_t T, const void* x,
+                        const uint8_t* w_gate_up_q, const float* w_gate_up_scale,
+                        const uint8_t* w_down_q, const float* w_down_scale, const float* topk_w,
+                        const int32_t* expert_offsets, const int32_t* sorted_slots,
+                        void* y_slots, void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  if (dims->act_dtype != MOE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "block-scaled E4M3 experts take bf16 activations");
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(w_gate_up_q); REQUIRE_PTR(w_gate_up_scale); REQUIRE_PTR(w_down_q);
+  REQUIRE_PTR(w_down_scale); REQUIRE_PTR(topk_w); REQUIRE_PTR(expert_offsets);
+  REQUIRE_PTR(sorted_slots); REQUIRE_PTR(y_slots);
+  if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+  const Layout L = layout(dims, T);
+  moe::B128Args gu{};
+  gu.T = T; gu.rows = T * dims->top_k; gu.E = dims->num_experts; gu.K = dims->top_k;
+  gu.offsets = expert_offsets; gu.sorted_slots = sorted_slots; gu.topk_w = topk_w;
+  moe::B128Args dn = gu;
+  gu.Kd = dims->hidden; gu.N = dims->expert_inter;
+  gu.xq = at<uint8_t>(ws, L.b_xq); gu.xscale = at<float>(ws, L.b_xs);
+  gu.wq = w_gate_up_q; gu.wscale = w_gate_up_scale;
+  gu.h = at<float>(ws, L.b_h); gu.hq = at<uint8_t>(ws, L.b_hq); gu.hscale = at<float>(ws, L.b_hs);
+  dn.Kd = dims->expert_inter; dn.N = dims->hidden;
+  dn.xq = gu.hq; dn.xscale = gu.hscale; dn.wq = w_down_q; dn.wscale = w_down_scale;
+  dn.y = y_slots;
+  hipError_t e = moe::launch_expert_ffn_b128(gu, dn, x, at<uint8_t>(ws, L.b_xq),
+                                             at<float>(ws, L.b_xs),
+                                             dims->slot_dtype == MOE_BF16,
+                                             static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_b128");
 }
 
 int moe_quantize_int8(int64_t rows, int32_t cols, const void* w, int8_t* q, float* scale,

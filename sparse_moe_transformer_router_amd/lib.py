@@ -68,6 +68,13 @@ def _load():
     L.moe_balance_loss.argtypes = [D, I32] + [P] * 3 + [F, F] + [P] * 4 + [SZ, P]
     L.moe_balance_loss_grad.argtypes = [D, I32] + [P] * 4 + [F, F] + [P] * 3
     L.moe_router_grad.argtypes = [D, I32] + [P] * 16 + [SZ, P]
+    I64 = ctypes.c_int64
+    L.moe_quantize_b128.argtypes = [I32, I64, I32, I32, P, P, P, P]
+    L.moe_dequantize_b128.argtypes = [I32, I64, I32, I32, P, P, P, P]
+    L.moe_linear_b128_workspace_size.argtypes = [I32, I32]
+    L.moe_linear_b128_workspace_size.restype = SZ
+    L.moe_linear_b128.argtypes = [I32, I32, I32] + [P] * 4 + [I32, P, SZ, P]
+    L.moe_expert_ffn_b128.argtypes = [D, I32] + [P] * 10 + [SZ, P]
     L.moe_route.argtypes = [D, I32] + [P] * 11 + [SZ, P]
     L.moe_dispatch.argtypes = [D, I32] + [P] * 5 + [SZ, P]
     L.moe_expert_ffn.argtypes = [D, I32] + [P] * 8 + [SZ, P]
@@ -94,7 +101,8 @@ def _load():
               "moe_quantize", "moe_dequantize", "moe_expert_ffn_q", "moe_expert_gate_up_timed",
               "gemma4_ffn_block_q", "moe_forward_noalloc", "moe_expert_ffn_mx",
               "moe_router_logits", "moe_balance_loss", "moe_balance_loss_grad",
-              "moe_router_grad"):
+              "moe_router_grad", "moe_quantize_b128", "moe_dequantize_b128", "moe_linear_b128",
+              "moe_expert_ffn_b128"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -140,6 +148,7 @@ def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, optional: bool
 
 
 _MASK = (torch.uint8, torch.bool)
+_CODE = (torch.uint8, torch.float8_e4m3fn)
 
 
 def _act(d: MoeDims):
@@ -316,6 +325,77 @@ def moe_expert_ffn_mx(d, fmt, T, x, w_gate_up_q, w_gate_up_scale, w_down_q, w_do
                                   _ptr(topk_w), _ptr(offsets), _ptr(sorted_slots),
                                   _ptr(y_slots), _ptr(ws), ws.numel() if ws is not None else 0,
                                   _stream(stream)))
+
+
+def _blocks(n: int) -> int:
+    return (n + 127) // 128
+
+
+def _b128_shape(block_rows, t, name):
+    if t.dim() < 2:
+        raise ValueError(f"{name} needs two axes or more")
+    rows, cols = t.shape[-2:]
+    batch = t.numel() // (rows * cols) if rows and cols else 0
+    nscale = batch * (rows if block_rows == 1 else _blocks(rows)) * _blocks(cols)
+    return batch, rows, cols, nscale
+
+
+def moe_quantize_b128(block_rows, w, q, scale, stream=None):
+    """E4M3 codes (uint8 or float8_e4m3fn) and fp32 scales of a bf16 [..., rows,
+    cols]: per 128 x 128 block (block_rows = 128, weights) or per 128 values of a
+    row (block_rows = 1, activations)."""
+    batch, rows, cols, ns = _b128_shape(block_rows, w, "w")
+    _check(_lib.moe_quantize_b128(block_rows, batch, rows, cols,
+                                  _arg("w", w, torch.bfloat16, w.numel()),
+                                  _arg("q", q, _CODE, w.numel()),
+                                  _arg("scale", scale, torch.float32, ns), _stream(stream)))
+
+
+def moe_dequantize_b128(block_rows, q, scale, out, stream=None):
+    batch, rows, cols, ns = _b128_shape(block_rows, q, "q")
+    _check(_lib.moe_dequantize_b128(block_rows, batch, rows, cols, _arg("q", q, _CODE, q.numel()),
+                                    _arg("scale", scale, torch.float32, ns),
+                                    _arg("out", out, torch.float32, q.numel()), _stream(stream)))
+
+
+def linear_b128_workspace(max_tokens: int, in_features: int, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of moe_linear_b128_workspace_size bytes."""
+    n = _lib.moe_linear_b128_workspace_size(max_tokens, in_features)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_linear_b128(T, x, w_q, w_scale, y, ws, stream=None):
+    """y [T, out] (fp32 or bf16) = x [T, in] (bf16) times the block-scaled weights
+    w_q [out, in]; x is quantized inside."""
+    if w_q.dim() != 2:
+        raise ValueError("w_q needs two axes")
+    n, k = w_q.shape
+    _check(_lib.moe_linear_b128(
+        T, n, k, _arg("x", x, torch.bfloat16, T * k), _arg("w_q", w_q, _CODE, n * k),
+        _arg("w_scale", w_scale, torch.float32, _blocks(n) * _blocks(k)),
+        _arg("y", y, (torch.bfloat16, torch.float32), T * n),
+        MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, _ptr(ws),
+        ws.numel() if ws is not None else 0, _stream(stream)))
+
+
+def moe_expert_ffn_b128(d, T, x, w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, topk_w,
+                        offsets, sorted_slots, y_slots, ws, stream=None):
+    """The experts with E4M3 weights scaled per 128 x 128 block, activations per
+    128 values."""
+    H, E, I, S = d.hidden, d.num_experts, d.expert_inter, T * d.top_k
+    f32, i32 = torch.float32, torch.int32
+    _check(_lib.moe_expert_ffn_b128(
+        ctypes.byref(d), T, _arg("x", x, torch.bfloat16, T * H),
+        _arg("w_gate_up_q", w_gate_up_q, _CODE, E * 2 * I * H),
+        _arg("w_gate_up_scale", w_gate_up_scale, f32, E * _blocks(2 * I) * _blocks(H)),
+        _arg("w_down_q", w_down_q, _CODE, E * H * I),
+        _arg("w_down_scale", w_down_scale, f32, E * _blocks(H) * _blocks(I)),
+        _arg("topk_w", topk_w, f32, S), _arg("offsets", offsets, i32, E + 1),
+        _arg("sorted_slots", sorted_slots, i32, S),
+        _arg("y_slots", y_slots, torch.bfloat16 if d.slot_dtype == MOE_BF16 else f32, S * H),
+        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
 
 
 def moe_expert_gate_up(d, T, x, w_gate_up, offsets, sorted_slots, h, stream=None):

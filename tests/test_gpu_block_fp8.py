@@ -1,0 +1,351 @@
+"""Block-scaled E4M3 on the GPU against tests/b128_ref.py: the quantizers bit
+for bit, the product and the experts within derived bounds.
+
+Product: the 8-bit instruction adds a block's 128 products to within ACC_REL
+of their magnitudes (b128_ref), the blocks are scaled and added in fp32 (K / 128
++ 4 roundings), and a bf16 output is rounded once (2^-8)."""
+import numpy as np
+import pytest
+import torch
+
+from tests import b128_ref as ref
+from tests.gpu_util import note
+
+pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from sparse_moe_transformer_router_amd import lib
+else:
+    lib = None
+
+
+def _gen(seed):
+    return torch.Generator().manual_seed(seed)
+
+
+def _x(g, T, K):
+    x = torch.randn(T, K, generator=g) * (1 + 7 * (torch.rand(K, generator=g) < 0.02).float())
+    return x.bfloat16().float()
+
+
+def _weights(g, *shape, std=0.05):
+    return ref.quantize((torch.randn(*shape, generator=g) * std).bfloat16().float(), 128)
+
+
+@pytest.mark.parametrize("br", [1, 128])
+@pytest.mark.parametrize("shape", [(1, 16), (3, 48), (130, 272), (2, 300, 2816), (3, 192, 96),
+                                   (128, 128), (257, 1040)])
+def test_quantizers_bit_for_bit(br, shape):
+    g = _gen(sum(shape))
+    v = torch.randn(*shape, generator=g) * torch.exp(3 * torch.randn(*shape[:-1], 1, generator=g))
+    v = v.bfloat16()
+    v[..., 0, :16] = 0
+    if shape[-1] >= 128:
+        v[..., -1, :128] = 0                       # a group of zeros
+    if shape[-2] > 2:
+        v[..., 1, :16] = 1e-40                     # below the smallest normal
+        v[..., 2, :16] = torch.tensor(3.0e38).bfloat16()
+    q, s = ref.quantize(v.float(), br)
+    note(f"quantize_b128 block_rows={br} {shape}")
+    vd = v.cuda()
+    qd = torch.full(shape, 0xAA, dtype=torch.uint8, device="cuda")
+    sd = torch.full(s.shape, np.nan, device="cuda")
+    lib.moe_quantize_b128(br, vd, qd, sd)
+    out = torch.full(shape, np.nan, device="cuda")
+    lib.moe_dequantize_b128(br, qd, sd, out)
+    torch.cuda.synchronize()
+    assert torch.equal(sd.cpu(), s)
+    # a zero has one value and two codes
+    diff = (qd.cpu() != q) & ~((qd.cpu() & 0x7F == 0) & (q & 0x7F == 0))
+    assert not diff.any(), int(diff.sum())
+    want = (ref.values(q, s, br)).float()
+    assert torch.equal(out.cpu(), want)
+
+
+def _linear(x, q, s, dt, guard=3):
+    T, K = x.shape
+    N = q.shape[0]
+    y = torch.full((T + guard, N), 77.0, dtype=dt, device="cuda")
+    ws = lib.linear_b128_workspace(T, K)
+    ws.fill_(0xFF)
+    lib.moe_linear_b128(T, x.bfloat16().cuda(), q.cuda(), s.cuda(), y, ws)
+    torch.cuda.synchronize()
+    y = y.cpu()
+    assert torch.all(y[T:] == 77.0)  # rows past the last stay
+    return y[:T]
+
+
+def _check_linear(x, q, s, y):
+    xv, wv = ref.values(*ref.quantize(x, 1), 1), ref.values(q, s, 128)
+    want = xv @ wv.t()
+    mag = xv.abs() @ wv.abs().t()
+    tol = ref.ACC_REL * mag + (ref.blocks(x.shape[1]) + 4) * 2.0 ** -24 * mag
+    if y.dtype == torch.bfloat16:
+        tol = tol + ref.BF16 * want.abs() * 1.001
+    err = (y.double() - want).abs()
+    assert torch.all(err <= tol + 1e-37), float((err / (tol + 1e-37)).max())
+
+
+@pytest.mark.parametrize("T,N,K", [
+    (1, 1, 16), (1, 2112, 2816), (2, 5, 48), (15, 255, 128), (16, 64, 144), (17, 257, 272),
+    (37, 1003, 1520), (64, 704, 2816), (127, 130, 704), (128, 96, 2960), (129, 97, 2960),
+    (200, 1003, 208), (257, 257, 128), (300, 513, 6016), (513, 1, 16), (640, 2816, 704),
+    (1025, 130, 2944)])
+def test_linear(T, N, K):
+    """One k-block and many (past the 23 whose scales a tile holds), partial
+    ones, single rows and columns, both forms."""
+    g = _gen(T * 7 + N + K)
+    x = _x(g, T, K)
+    q, s = _weights(g, N, K)
+    for dt in (torch.bfloat16, torch.float32):
+        note(f"linear_b128 T={T} N={N} K={K} {dt}")
+        _check_linear(x, q, s, _linear(x, q, s, dt))
+
+
+@pytest.mark.parametrize("T", [3, 150])
+def test_linear_zero_rows_and_blocks(T):
+    g = _gen(T)
+    x = _x(g, T, 400)
+    x[1], x[2, 128:256] = 0, 0
+    w = torch.randn(300, 400, generator=g)
+    w[128:256, 128:256] = 0
+    q, s = ref.quantize(w, 128)
+    note(f"linear_b128, zeros, T={T}")
+    y = _linear(x, q, s, torch.float32)
+    _check_linear(x, q, s, y)
+    assert not y[1].any()
+
+
+def test_linear_large_offsets():
+    """Outputs past 2^32 bytes."""
+    T, N, K = 65536, 40000, 16
+    g = _gen(5)
+    x = _x(g, T, K)
+    q, s = _weights(g, N, K)
+    note("linear_b128, 5 GB of output")
+    y = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+    ws = lib.linear_b128_workspace(T, K)
+    lib.moe_linear_b128(T, x.bfloat16().cuda(), q.cuda(), s.cuda(), y, ws)
+    rows = torch.tensor([0, 1, 300, 53687, 53688, 65535])
+    got = y[rows.cuda()].cpu()
+    _check_linear(x[rows], q, s, got)
+
+
+def _experts(x, guq, gus, dnq, dns, idx, w, slot=None, guard=2):
+    T, H = x.shape
+    E, K, I = guq.shape[0], idx.shape[1], guq.shape[1] // 2
+    d = lib.dims(H, E, K, I, 0, 1e-6, lib.MOE_BF16, lib.MOE_F32 if slot is None else slot)
+    ws = lib.workspace(d, T)
+    ws.fill_(0xFF)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cnt, off, srt = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T * K, **i32)
+    idd = idx.int().cuda()
+    lib.moe_dispatch(d, T, idd, cnt, off, srt, ws)
+    y = torch.zeros(T + guard, K, H, dtype=torch.float32 if slot is None else torch.bfloat16,
+                    device="cuda")
+    y[T:] = 77.0
+    lib.moe_expert_ffn_b128(d, T, x.bfloat16().cuda(), guq.cuda(), gus.cuda(), dnq.cuda(),
+                            dns.cuda(), w.float().cuda(), off, srt, y, ws)
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    lib.moe_combine(d, T, y, None, out)
+    torch.cuda.synchronize()
+    assert torch.all(y[T:] == 77.0)
+    return y[:T].cpu(), out.cpu()
+
+
+def _routing(g, T, E, K, skew=0.0):
+    lg = torch.randn(T, E, generator=g) + skew * torch.randn(E, generator=g)
+    v, idx = torch.topk(lg, K, dim=-1)
+    return idx, torch.softmax(v, -1)
+
+
+def _check_experts(x, guq, gus, dnq, dns, idx, w, y, out):
+    want, err = ref.experts(x, ref.values(guq, gus, 128), ref.values(dnq, dns, 128), idx, w)
+    d = (y.double().sum(1) - want).abs()
+    extra = 0.0 if y.dtype == torch.float32 else ref.BF16 * y.double().abs().sum(1) * 1.01
+    note(f"  max err / bound {float((d / (err + extra + 1e-30)).max()):.3f}")
+    assert torch.all(d <= err + extra + 1e-30)
+    d = (out.double() - want).abs()
+    assert torch.all(d <= err + extra + ref.BF16 * (want.abs() + err) * 1.01 + 1e-30)
+    rms = float((d ** 2).mean().sqrt() / (want ** 2).mean().sqrt().clamp(min=1e-30))
+    note(f"  RMS err / RMS {rms:.5f}")
+    return rms
+
+
+@pytest.mark.parametrize("T,H,E,K,I", [
+    (1, 64, 1, 1, 32), (1, 256, 8, 8, 160), (2, 128, 4, 1, 96), (5, 192, 16, 3, 96),
+    (37, 192, 16, 3, 96), (40, 320, 6, 2, 224), (200, 512, 128, 8, 64), (256, 64, 256, 16, 32),
+    (257, 64, 256, 4, 32), (90, 320, 2, 2, 160), (300, 256, 8, 2, 192), (700, 192, 5, 1, 96),
+    (1100, 2816, 3, 2, 704), (520, 8192, 2, 1, 288)])
+def test_experts(T, H, E, K, I):
+    """Both forms, ragged widths (up rows that start inside a block), one row to
+    many per expert, more k-blocks than a tile holds scales for."""
+    g = _gen(T + H + I)
+    x = _x(g, T, H)
+    guq, gus = _weights(g, E, 2 * I, H, std=1.0 / H ** 0.5)
+    dnq, dns = _weights(g, E, H, I, std=1.0 / I ** 0.5)
+    idx, w = _routing(g, T, E, K, 0.8)
+    for slot in (None, 1):
+        note(f"experts_b128 T={T} H={H} E={E} K={K} I={I} slot={slot}")
+        y, out = _experts(x, guq, gus, dnq, dns, idx, w, slot)
+        _check_experts(x, guq, gus, dnq, dns, idx, w, y, out)
+
+
+@pytest.mark.parametrize("T", [1, 8, 64, 256, 1024])
+def test_experts_26b(T):
+    g = _gen(T)
+    H, E, K, I = 2816, 128, 8, 704
+    x = _x(g, T, H)
+    guq, gus = _weights(g, 16, 2 * I, H, std=1.0 / H ** 0.5)
+    dnq, dns = _weights(g, 16, H, I, std=1.0 / I ** 0.5)
+    # 16 experts' weights repeated: the reference stays in memory
+    idx, w = _routing(g, T, E, K, 0.5)
+    note(f"experts_b128 26B T={T}")
+    rep = lambda t: t.repeat(8, 1, 1)  # noqa: E731
+    y, out = _experts(x, rep(guq), rep(gus), rep(dnq), rep(dns), idx, w)
+    rms = _check_experts(x, guq, gus, dnq, dns, idx % 16, w, y, out)
+    # one bf16 rounding is 1.7e-3; a wrong scale or layout is orders above
+    assert rms <= 5e-3
+
+
+@pytest.mark.parametrize("T", [9, 400])
+def test_experts_dropped_slots(T):
+    """Picks outside [0, E) take part in nothing; their slots stay as they were."""
+    g = _gen(T)
+    x = _x(g, T, 128)
+    guq, gus = _weights(g, 4, 128, 128)
+    dnq, dns = _weights(g, 4, 128, 64)
+    idx, w = _routing(g, T, 4, 2)
+    idx[0, 0], idx[1] = -1, 4
+    note(f"experts_b128 dropped slots T={T}")
+    y, out = _experts(x, guq, gus, dnq, dns, idx, w)
+    assert not y[0, 0].any() and not y[1].any()
+    _check_experts(x, guq, gus, dnq, dns, idx, w, y, out)
+
+
+@pytest.mark.parametrize("T", [4, 300])
+def test_experts_weights_past_32_bits(T):
+    """An expert whose weights start past 2^32 bytes."""
+    H, E, I = 8192, 256, 1024
+    g = _gen(T)
+    x = _x(g, T, H)
+    gq, gs = _weights(g, 1, 2 * I, H, std=1.0 / H ** 0.5)
+    dq, ds = _weights(g, 1, H, I, std=1.0 / I ** 0.5)
+    note(f"experts_b128, 6 GB of codes, T={T}")
+    d = lib.dims(H, E, 1, I)
+    ws = lib.workspace(d, T)
+    new = lambda *s, dt=torch.uint8: torch.zeros(*s, dtype=dt, device="cuda")  # noqa: E731
+    guq, dnq = new(E, 2 * I, H), new(E, H, I)
+    gus, dns = new(E, 16, 64, dt=torch.float32), new(E, 64, 8, dt=torch.float32)
+    guq[-1], gus[-1], dnq[-1], dns[-1] = gq[0].cuda(), gs[0].cuda(), dq[0].cuda(), ds[0].cuda()
+    idx = torch.full((T, 1), E - 1, dtype=torch.int32, device="cuda")
+    i32 = dict(dtype=torch.int32, device="cuda")
+    cnt, off, srt = torch.empty(E, **i32), torch.empty(E + 1, **i32), torch.empty(T, **i32)
+    w = torch.ones(T, 1, device="cuda")
+    y = torch.empty(T, 1, H, device="cuda")
+    out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+    lib.moe_dispatch(d, T, idx, cnt, off, srt, ws)
+    lib.moe_expert_ffn_b128(d, T, x.bfloat16().cuda(), guq, gus, dnq, dns, w, off, srt, y, ws)
+    lib.moe_combine(d, T, y, None, out)
+    torch.cuda.synchronize()
+    keep = torch.arange(min(T, 40))
+    _check_experts(x[keep], gq, gs, dq, ds, torch.zeros(len(keep), 1, dtype=torch.long),
+                   torch.ones(len(keep), 1), y.cpu()[keep], out.cpu()[keep])
+
+
+class _Layer:
+    """Route, experts, combine on block-scaled weights that the library quantized,
+    beside the dense projection."""
+
+    def __init__(self, T, seed, H=256, E=8, K=2, I=96, N=304):
+        g = torch.Generator(device="cuda").manual_seed(seed)
+        n = lambda *s: torch.randn(*s, generator=g, device="cuda")  # noqa: E731
+        self.T, self.d = T, lib.dims(H, E, K, I)
+        self.x = n(T, H).bfloat16()
+        self.W, self.scale, self.pes = n(E, H) / H ** 0.5, 1 + 0.1 * n(H), 1 + 0.1 * n(E)
+        self.w = {}
+        for name, shape in (("gu", (E, 2 * I, H)), ("dn", (E, H, I)), ("lin", (N, H))):
+            w = (n(*shape) / shape[-1] ** 0.5).bfloat16()
+            q = torch.empty(shape, dtype=torch.float8_e4m3fn, device="cuda")
+            s = torch.empty(*shape[:-2], -(-shape[-2] // 128), -(-shape[-1] // 128), device="cuda")
+            lib.moe_quantize_b128(128, w, q, s)
+            self.w[name] = (q, s)
+        i = lambda *s: torch.empty(*s, dtype=torch.int32, device="cuda")  # noqa: E731
+        self.idx, self.tw = i(T, K), torch.empty(T, K, device="cuda")
+        self.cnt, self.off, self.srt = i(E), i(E + 1), i(T * K)
+        self.y = torch.empty(T, K, H, device="cuda")
+        self.out = torch.empty(T, H, dtype=torch.bfloat16, device="cuda")
+        self.lin = torch.empty(T, N, dtype=torch.bfloat16, device="cuda")
+        self.ws, self.lws = lib.workspace(self.d, T), lib.linear_b128_workspace(T, H)
+
+    def run(self):
+        s = self
+        lib.moe_route(s.d, s.T, s.x, s.W, s.scale, s.pes, None, s.idx, s.tw, s.cnt, s.off, s.srt,
+                      s.ws)
+        lib.moe_expert_ffn_b128(s.d, s.T, s.x, *s.w["gu"], *s.w["dn"], s.tw, s.off, s.srt, s.y,
+                                s.ws)
+        lib.moe_combine(s.d, s.T, s.y, None, s.out)
+        lib.moe_linear_b128(s.T, s.x, *s.w["lin"], s.lin, s.lws)
+
+    def outputs(self):
+        return self.out.clone(), self.lin.clone()
+
+
+@pytest.mark.parametrize("T", [3, 320])
+def test_layer_together(T):
+    s = _Layer(T, 3)
+    note(f"block-scaled layer T={T}")
+    s.run()
+    torch.cuda.synchronize()
+    c = lambda t: t.view(torch.uint8).cpu() if t.dtype == torch.float8_e4m3fn else t.cpu()  # noqa
+    w = {k: (c(q), c(sc)) for k, (q, sc) in s.w.items()}
+    x = s.x.float().cpu()
+    _check_experts(x, *w["gu"], *w["dn"], s.idx.cpu().long(), s.tw.cpu(), s.y.cpu(), s.out.cpu())
+    _check_linear(x, *w["lin"], s.lin.cpu())
+
+
+@pytest.mark.parametrize("sizes", [(3, 40), (320, 280)])
+def test_layers_in_graphs_and_streams(sizes):
+    """Two captured layers that share their workspaces, replayed in turn with
+    eager runs between, and the same two at once on streams of their own."""
+    st = torch.cuda.Stream()
+    ls = [_Layer(t, 40 + t) for t in sizes]
+    big = max(ls, key=lambda s: s.T)
+    own = [(s.ws, s.lws) for s in ls]
+    want = []
+    for s in ls:
+        s.run()
+        torch.cuda.synchronize()
+        want.append(s.outputs())
+    graphs = []
+    for s in ls:
+        s.ws, s.lws = big.ws, big.lws
+        with torch.cuda.stream(st):
+            s.run()
+        torch.cuda.synchronize()
+        gr = torch.cuda.CUDAGraph()
+        note(f"capture a block-scaled layer T={s.T}")
+        with torch.cuda.graph(gr, stream=st):
+            s.run()
+        graphs.append(gr)
+    for r in range(4):
+        for s, gr, w in zip(ls, graphs, want):
+            s.out.fill_(np.nan)
+            s.lin.fill_(np.nan)
+            gr.replay()
+            torch.cuda.synchronize()
+            assert all(torch.equal(a, b) for a, b in zip(s.outputs(), w)), r
+        ls[r % 2].run()
+        torch.cuda.synchronize()
+    for s, (ws, lws) in zip(ls, own):
+        s.ws, s.lws = ws, lws
+    streams = [torch.cuda.Stream(), torch.cuda.Stream()]
+    torch.cuda.synchronize()
+    note("two block-scaled layers at once")
+    for _ in range(3):
+        for s, t in zip(ls, streams):
+            with torch.cuda.stream(t):
+                s.run()
+    torch.cuda.synchronize()
+    for s, w in zip(ls, want):
+        assert all(torch.equal(a, b) for a, b in zip(s.outputs(), w))
