@@ -415,9 +415,10 @@ int moe_expert_ffn_mx(const moe_dims* dims, int32_t fmt, int32_t T, const void* 
  * moe_quantize_b128: w is bf16 [batch, rows, cols], cols a multiple of 16 in
  * [16, 65536].  block_rows = 128: weights, scale [batch, ceil(rows / 128),
  * ceil(cols / 128)]; block_rows = 1: activations, scale [batch, rows,
- * ceil(cols / 128)].  scale = max |v| / 448 over the block, code = E4M3 nearest
- * to v / scale (fp32 divisions, ties to the even mantissa, 448 at most); a block
- * of zeros gets scale 0 and codes 0.
+ * ceil(cols / 128)].  scale = max |v| over the block times the fp32 number
+ * nearest to 1 / 448, in fp32; code = E4M3 nearest to the fp32 quotient v /
+ * scale (ties to the even mantissa, 448 at most); a block of zeros (or one so
+ * small that its scale underflows) gets scale 0 and codes 0.
  * moe_dequantize_b128: the values, fp32 [batch, rows, cols], each product
  * rounded once.  MOE_ERR_ARG for another block_rows, bad sizes or pointers. */
 int moe_quantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,
@@ -429,8 +430,8 @@ int moe_dequantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t
  * [T, in_features] bf16 (done inside the call), W the value of the weights
  * w_q [out_features, in_features], w_scale as above.  y [T, out_features] in
  * y_dtype.  Products of a 128-block accumulate inside the 8-bit matrix
- * instruction (which keeps each block's sum to about 2^-15 of the sum of the
- * magnitudes it adds), the blocks in fp32.  T up to 65536, out_features up to
+ * instruction (off by at most 2^-12 of the sum of the magnitudes it adds, some
+ * 2^-19 in the root mean square), the blocks in fp32.  T up to 65536, out_features up to
  * 262144, in_features a multiple of 16 up to 16384.  ws:
  * moe_linear_b128_workspace_size(T, in_features) bytes, 256-byte aligned (0: the
  * sizes are not supported). */

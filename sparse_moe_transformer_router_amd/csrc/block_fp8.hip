@@ -30,6 +30,7 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 
 constexpr int kBlk = 128;              // values that share a scale
 constexpr float kE4m3Max = 448.0f;
+constexpr float kInvE4m3Max = 1.0f / 448.0f;  // a block's scale is max |v| times this
 constexpr uint32_t kUnitScale = 127;   // E8M0 code of 1.0
 
 __host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
@@ -88,8 +89,10 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float s) {
   return make_uint2(encode4(q[0], q[1], q[2], q[3]), encode4(q[4], q[5], q[6], q[7]));
 }
 
-// Rows: scale = max |v| / 448 per 128 values, code = E4M3 nearest to v / scale
-// (fp32 divisions).  16 lanes a group, 8 values a lane.
+// Rows: scale = max |v| * (1 / 448) per 128 values, in fp32, code = E4M3 nearest
+// to v / scale (fp32 division: bf16 inputs put many quotients exactly on a
+// decision point, where a reciprocal would change the code).  16 lanes a group,
+// 8 values a lane.
 template <typename XT>
 __global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, int cols,
                                                                const XT* __restrict__ in,
@@ -103,7 +106,7 @@ __global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, i
   const int c = (int)(grp % nb) * kBlk + 8 * l;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < cols) ld8(in + r * cols + c, v);
-  const float s = row16_max(amax8(v)) / kE4m3Max;
+  const float s = row16_max(amax8(v)) * kInvE4m3Max;
   if (l == 0) scale[grp] = s;
   if (c < cols) *reinterpret_cast<uint2*>(q + r * cols + c) = encode8(v, s);
 }
@@ -133,7 +136,7 @@ __global__ __launch_bounds__(256) void quantize_blocks128_kernel(int rows, int c
   m = wave_max(m);
   if (lane_id() == 0) red[threadIdx.x / kWave] = m;
   __syncthreads();
-  const float s = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) / kE4m3Max;
+  const float s = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) * kInvE4m3Max;
   if (threadIdx.x == 0) scale[(b * gridDim.y + rb) * gridDim.x + cb] = s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -612,7 +615,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
       m = fmaxf(m, dpp_f<0xB1>(m));
       m = fmaxf(m, dpp_f<0x4E>(m));
-      const float s = m / kE4m3Max;
+      const float s = m * kInvE4m3Max;
       if (!on || nbase + c >= N) continue;
       uint32_t q[8];
 #pragma unroll

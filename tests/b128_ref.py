@@ -8,6 +8,7 @@ import math
 import torch
 
 E4M3_MAX = 448.0
+INV_MAX = torch.tensor(1.0 / 448.0, dtype=torch.float32)  # a scale is max |v| times this
 # Accumulation error of the 8-bit matrix instruction relative to the sum of the
 # magnitudes of the 128 products it adds (measured on the part against exact
 # host sums: at most 1.5e-4).
@@ -28,10 +29,11 @@ def _tiles(v, block_rows):
 
 
 def quantize(v, block_rows):
-    """(uint8 codes, fp32 scales) of fp32 v: fp32 divisions, ties to even."""
+    """(uint8 codes, fp32 scales) of fp32 v: the scale by the reciprocal of 448,
+    the quotients by fp32 division, ties to even."""
     rows, cols = v.shape[-2:]
     t = _tiles(v.float(), block_rows)
-    s = t.abs().amax((-3, -1)) / E4M3_MAX
+    s = t.abs().amax((-3, -1)) * INV_MAX
     d = s[..., :, None, :, None]
     q = torch.where(d > 0, t / torch.where(d > 0, d, torch.ones_like(d)), torch.zeros_like(t))
     q = q.clamp(-E4M3_MAX, E4M3_MAX).to(torch.float8_e4m3fn)
@@ -85,7 +87,7 @@ def experts(x, gu, dn, idx, w):
         m = torch.nn.functional.pad(h.abs(), (0, pad)).unflatten(-1, (-1, 128))
         me = torch.nn.functional.pad(he, (0, pad)).unflatten(-1, (-1, 128))
         rep = lambda v: v.repeat_interleave(128, -1)[:, :I]  # noqa: E731
-        s = rep((m.amax(-1).float() / E4M3_MAX).double())
+        s = rep((m.amax(-1).float() * INV_MAX).double())
         s_lo = rep((m - me).clamp(min=0).amax(-1)) / E4M3_MAX * (1 - 2.0 ** -22)
         s_hi = rep((m + me).amax(-1)) / E4M3_MAX * (1 + 2.0 ** -22)
         q = torch.where(s > 0, _e4m3(h / s.clamp(min=1e-300)) * s, torch.zeros_like(h))
