@@ -93,7 +93,7 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float s) {
 // to v / scale (fp32 division: bf16 inputs put many quotients exactly on a
 // decision point, where a reciprocal would change the code).  16 lanes a group,
 // 8 values a lane.
-template <typename XT>
+template <typename XT, bool PAD>
 __global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, int cols,
                                                                const XT* __restrict__ in,
                                                                uint8_t* __restrict__ q,
@@ -108,7 +108,8 @@ __global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, i
   if (c < cols) ld8(in + r * cols + c, v);
   const float s = row16_max(amax8(v)) * kInvE4m3Max;
   if (l == 0) scale[grp] = s;
-  if (c < cols) *reinterpret_cast<uint2*>(q + r * cols + c) = encode8(v, s);
+  const long long pitch = PAD ? (long long)nb * kBlk : cols;
+  if (PAD || c < cols) *reinterpret_cast<uint2*>(q + r * pitch + c) = encode8(v, s);
 }
 
 // 128 x 128 blocks of [batch, rows, cols]: one workgroup a block, 8 values of 8
@@ -261,7 +262,7 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
     const int r = row0 + 16 * mb + fr;
     long long t = r < row1 ? r : row0;
     if (MODE == kGateUp) t = a.sorted_slots[t] / a.K;
-    xrow[mb] = a.xq + t * Kd;
+    xrow[mb] = a.xq + t * (KB * kBlk);
     xsc[mb] = a.xscale + t * KB;
   }
   const int kb0 = wk * KB / WK, kb1 = (wk + 1) * KB / WK;
@@ -391,7 +392,8 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 // weight tiles, and scales the previous tile's results meanwhile.
 // ---------------------------------------------------------------------------
 constexpr int kTM = 256, kTN = 256, kTileWaves = 8;
-constexpr int kTileBlocks = 23;
+constexpr int kTileBlocks = 22;  // even: a run of k-blocks starts in stage 0
+constexpr int kRowGroup = 4;
 constexpr int kStageBytes = (kTM + kTN) * kBlk;
 constexpr int kRingBytes = 2 * kStageBytes;
 constexpr int kScaleOff = kRingBytes;                               // [kTileBlocks][256]
@@ -416,8 +418,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
     const int RT = (a.rows + kTM - 1) / kTM;
     const int item = xcd_item(blockIdx.x, RT * NT);
     if (item < 0) return;  // uniform over the block
-    nt = item / RT;
-    row0 = item % RT * kTM;
+    // four row tiles at a time, the row tiles fastest: an XCD's run of items
+    // then covers few rows and few columns, each read into its L2 once
+    const int first = item / (kRowGroup * NT) * kRowGroup, in = item % (kRowGroup * NT);
+    const int gr = min(kRowGroup, RT - first);
+    nt = in / gr;
+    row0 = (first + in % gr) * kTM;
     row1 = min(row0 + kTM, a.rows);
   } else {
     RowTileScan sc;
@@ -458,24 +464,33 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
     return col + (up ? N : 0);
   };
   // Copy j of wave w fills lines 8 (8 j + w) .. + 7 of a stage: activations for
-  // j < 4, weights past that.  Sources in 16-byte units (a tensor of 2^36
-  // bytes fits 32 bits).
+  // j < 4, weights past that.  Byte offsets from the tile's bases: below 2^32 (a
+  // batch's codes of x take 2^30 bytes at most, an expert's weights 2^32).
+  // Activation rows end in zeros up to a whole line, so what the weights' part
+  // of the last line holds past their row does not matter: their own last
+  // chunk, which is a finite number exactly when the output is to be one.
+  const int pitch = KB * kBlk;
+  const uint8_t* xbase = MODE == kGateUp ? a.xq : a.xq + (long long)row0 * pitch;
   unsigned src[COPIES];
   const int chunk = (lane % 8) ^ (lane / 8);
 #pragma unroll
   for (int j = 0; j < COPIES; ++j) {
     const int line = 8 * (kTileWaves * j + wave) + lane / 8;
-    const unsigned row = j < COPIES / 2 ? (unsigned)rtok[line] : (unsigned)wrow(line - kTM);
-    src[j] = row * (unsigned)(Kd / 16);
+    if (j < COPIES / 2) {
+      const int row = MODE == kGateUp ? rtok[line] : min(line, row1 - 1 - row0);
+      src[j] = (unsigned)row * (unsigned)pitch;
+    } else {
+      src[j] = (unsigned)wrow(line - kTM) * (unsigned)Kd;
+    }
   }
-  auto copy = [&](int kt) {
-    const unsigned k16 = min(kt * 8 + chunk, Kd / 16 - 1);  // past the row: its last chunk
+  auto copy = [&](int kt, int st) __attribute__((always_inline)) {
+    const unsigned kx = (kt * 8 + chunk) * 16, kw = min(kt * 8 + chunk, Kd / 16 - 1) * 16;
 #pragma unroll
     for (int j = 0; j < COPIES; ++j) {
-      const uint8_t* base = j < COPIES / 2 ? a.xq : wbase;
 #if defined(__HIP_DEVICE_COMPILE__)
-      lds_copy16(base + (size_t)(src[j] + k16) * 16,
-                 smem + (kt & 1) * kStageBytes + (kTileWaves * j + wave) * 1024);
+      unsigned char* to = smem + st * kStageBytes + (kTileWaves * j + wave) * 1024;
+      if (j < COPIES / 2) lds_copy16(xbase, src[j] + kx, to);
+      else lds_copy16(wbase, src[j] + kw, to);
 #endif
     }
   };
@@ -505,17 +520,15 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   } else {
     ws0 = ws1 = wn / 2;
   }
-  int woff[TJ];
-#pragma unroll
-  for (int j = 0; j < TJ; ++j) {
-    int n;
-    if constexpr (MODE == kGateUp) n = (j / 2) * (kTN / 2) + wn * 32 + (j % 2) * 16 + fr;
-    else n = wn * 64 + j * 16 + fr;
-    const int line = kTM + n;
-    woff[j] = line * kBlk + (g ^ (line & 7)) * 16;
-  }
+  // Lines 16 apart have the same swizzle, so a wave's tiles lie at constants
+  // from its first: activations i * 16 lines, weights as wtile().
   const int xline = wm * 128 + fr;
-  const int xoff = xline * kBlk + (g ^ (xline & 7)) * 16;  // tile i: + i * 16 * kBlk
+  const int xoff = xline * kBlk + (g ^ (xline & 7)) * 16;
+  const int wline = kTM + wn * (MODE == kGateUp ? 32 : 64) + fr;
+  const int woff = wline * kBlk + (g ^ (wline & 7)) * 16;
+  auto wtile = [](int j) {
+    return (MODE == kGateUp ? (j / 2) * (kTN / 2) + (j % 2) * 16 : j * 16) * kBlk;
+  };
   int nv = (row1 - row0 - wm * 128 + 15) / 16;             // tiles of this wave with rows
   nv = __builtin_amdgcn_readfirstlane(max(0, min(TI, nv)));
 
@@ -525,59 +538,90 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  copy(0);
-  if (KB > 1) copy(1);
-  else copy(0);  // the same bytes again: the waits below count on two stages
-  for (int kt = 0; kt < KB; ++kt) {
-    const int kl = kt % kTileBlocks;
-    if (kl == 0) {
-      __syncthreads();  // the scales of the blocks before are used up
-      load_scales(kt);
-    }
-    wait_vmem<COPIES>();  // tile kt landed (this wave's copies)
-    __syncthreads();      // ... everyone's, and the scales
-    const unsigned char* st = smem + (kt & 1) * kStageBytes;
-    auto rd = [&](int off) {
-      return pack8(*reinterpret_cast<const uint4*>(st + off),
-                   *reinterpret_cast<const uint4*>(st + (off ^ 64)));
-    };
-    const bool tail = (kt + 1) * kBlk > Kd;  // uniform
-    int o0, o1;
-    bool v0, v1;
-    spans(kt, g, Kd, o0, o1, v0, v1);
-    i32x8 fw[TJ];
+  // Fragment at a wave's first tile + at, of stage `st`.
+  auto rd = [&](int st, int off, int at) __attribute__((always_inline)) {
+    const unsigned char* p = smem + st * kStageBytes;
+    return pack8(*reinterpret_cast<const uint4*>(p + off + at),
+                 *reinterpret_cast<const uint4*>(p + (off ^ 64) + at));
+  };
+  i32x8 fw[TJ], fx[2];
+  f32x4 d[2][TJ];
+  float sx[2], sw[2];
+  // results of tile i (in d[i & 1]) times their scales
+  auto scale_add = [&](int i) __attribute__((always_inline)) {
+    const float s0 = sx[i & 1] * sw[0], s1 = sx[i & 1] * sw[1];
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) {
-      fw[j] = rd(woff[j]);
-      if (tail) fw[j] = keep32(fw[j], v0, v1);
-    }
-    const float sw0 = s_w[kl * 4 + ws0], sw1 = s_w[kl * 4 + ws1];
-    f32x4 d[2][TJ];
-    auto scale_add = [&](int i, int buf) {
-      const float sx = s_x[kl * kTM + xline + 16 * i];
-      const float s0 = sx * sw0, s1 = sx * sw1;
+    for (int j = 0; j < TJ; ++j)
 #pragma unroll
-      for (int j = 0; j < TJ; ++j) {
-        const float s = j < TJ / 2 ? s0 : s1;
+      for (int r = 0; r < 4; ++r)
+        acc[i][j][r] = __builtin_fmaf(d[i & 1][j][r], j < TJ / 2 ? s0 : s1, acc[i][j][r]);
+  };
+  auto read_first = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) acc[i][j][r] = __builtin_fmaf(d[buf][j][r], s, acc[i][j][r]);
+    for (int j = 0; j < TJ; ++j) fw[j] = rd(st, woff, wtile(j));
+    fx[0] = rd(st, xoff, 0);
+  };
+  // One k-block from stage `st`, its weight fragments in fw and its first
+  // activation tile in fx[0]; kl: its place among the staged scales.
+  // Activation tiles are read one ahead.  Before the last tile's products comes
+  // the block's barrier: past it the stage is free for k-block kt + 2 (every
+  // wave has its last fragments) and k-block kt + 1 has landed everywhere, so
+  // its first fragments are read behind those products.  No branch: one would
+  // let the compiler move products past it and their operands would pile up.
+  auto block = [&](int kt, int kl, auto st_tag, auto ti_tag) __attribute__((always_inline)) {
+    constexpr int st = decltype(st_tag)::value;
+    constexpr int TV = decltype(ti_tag)::value;
+    sw[0] = s_w[kl * 4 + ws0];
+    sw[1] = s_w[kl * 4 + ws1];
+#pragma unroll
+    for (int i = 0; i < TV; ++i) {
+      sx[i & 1] = s_x[kl * kTM + xline + 16 * i];
+      if (i + 1 < TV) {
+        fx[(i + 1) & 1] = rd(st, xoff, (i + 1) * 16 * kBlk);
+      } else {
+        wait_lds();
+        wait_vmem<0>();
+        block_barrier();
+        copy(min(kt + 2, KB - 1), st);  // past the end: bytes that are never read
+        __builtin_amdgcn_sched_barrier(0);
       }
-    };
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      if (i < nv) {  // uniform: tiles past the group's rows are skipped
-        i32x8 fx = rd(xoff + i * 16 * kBlk);
-        if (tail) fx = keep32(fx, v0, v1);
-#pragma unroll
-        for (int j = 0; j < TJ; ++j) d[i & 1][j] = mfma_blk(fw[j], fx);
+      for (int j = 0; j < TJ; ++j) d[i & 1][j] = mfma_blk(fw[j], fx[i & 1]);
+      if (i + 1 == TV) {
+        __builtin_amdgcn_sched_barrier(0);
+        read_first(1 - st);  // (past the end: never used)
+        __builtin_amdgcn_sched_barrier(0);
       }
-      if (i > 0 && i - 1 < nv) scale_add(i - 1, (i - 1) & 1);
+      if (i > 0) scale_add(i - 1);
+      __builtin_amdgcn_sched_barrier(0);  // no fragment is read further ahead
     }
-    if (TI - 1 < nv) scale_add(TI - 1, (TI - 1) & 1);
-    wait_lds();
-    block_barrier();  // every wave has read stage kt: it can be refilled
-    copy(min(kt + 2, KB - 1) == kt + 2 ? kt + 2 : kt);
-  }
+    scale_add(TV - 1);
+  };
+  auto loop = [&](auto ti_tag) __attribute__((always_inline)) {
+    for (int k0 = 0; k0 < KB; k0 += kTileBlocks) {
+      if (k0 > 0) {
+        __syncthreads();  // the scales of the k-blocks before are used up
+        load_scales(k0);
+        __syncthreads();
+      }
+      const int n = min(kTileBlocks, KB - k0);
+      for (int kl = 0; kl < n; kl += 2) {
+        block(k0 + kl, kl, std::integral_constant<int, 0>{}, ti_tag);
+        if (kl + 1 < n) block(k0 + kl + 1, kl + 1, std::integral_constant<int, 1>{}, ti_tag);
+      }
+    }
+  };
+  copy(0, 0);
+  load_scales(0);
+  wait_vmem<0>();
+  __syncthreads();
+  copy(min(1, KB - 1), 1);
+  read_first(0);
+  // as many tiles as hold the wave's rows (every wave takes part in the copies
+  // and barriers)
+  if (nv > 4) loop(std::integral_constant<int, 8>{});
+  else if (nv > 2) loop(std::integral_constant<int, 4>{});
+  else loop(std::integral_constant<int, 2>{});
   wait_vmem<0>();
   __syncthreads();
 
@@ -616,7 +660,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       m = fmaxf(m, dpp_f<0xB1>(m));
       m = fmaxf(m, dpp_f<0x4E>(m));
       const float s = m * kInvE4m3Max;
-      if (!on || nbase + c >= N) continue;
+      if (!on) continue;  // columns past the last are zeros: the row's padding
       uint32_t q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
@@ -625,7 +669,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
         for (int u = 0; u < 4; ++u) t[u] = s > 0.0f ? v[4 * i + u] / s : 0.0f;
         q[i] = encode4(t[0], t[1], t[2], t[3]);
       }
-      uint4* dst = reinterpret_cast<uint4*>(a.hq + (size_t)(row0 + r) * N + nbase + c);
+      uint4* dst = reinterpret_cast<uint4*>(a.hq + (size_t)(row0 + r) * (nbh * kBlk) + nbase + c);
       dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
       dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
       if (c == 0) a.hscale[(size_t)(row0 + r) * nbh + nbase / kBlk] = s;
@@ -668,11 +712,11 @@ hipError_t launch_tile(const B128Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <typename XT>
+template <typename XT, bool PAD>
 hipError_t quantize_rows(long long rows, int cols, const void* x, uint8_t* q, float* scale,
                          hipStream_t s) {
   const long long lanes = rows * blocks_of(cols) * 16;
-  hipLaunchKernelGGL(quantize_rows128_kernel<XT>, dim3((unsigned)((lanes + 255) / 256)), dim3(256),
+  hipLaunchKernelGGL((quantize_rows128_kernel<XT, PAD>), dim3((unsigned)((lanes + 255) / 256)), dim3(256),
                      0, s, rows, cols, static_cast<const XT*>(x), q, scale);
   return hipGetLastError();
 }
@@ -681,7 +725,7 @@ hipError_t quantize_rows(long long rows, int cols, const void* x, uint8_t* q, fl
 
 hipError_t launch_quantize_b128(int block_rows, long long batch, int rows, int cols, const void* w,
                                 uint8_t* q, float* scale, hipStream_t s) {
-  if (block_rows == 1) return quantize_rows<bf16>(batch * rows, cols, w, q, scale, s);
+  if (block_rows == 1) return quantize_rows<bf16, false>(batch * rows, cols, w, q, scale, s);
   // the grid's z axis holds 65535 matrices at a time
   const int rb = blocks_of(rows), cb = blocks_of(cols);
   for (long long b = 0; b < batch; b += 65535) {
@@ -707,7 +751,7 @@ bool b128_streams(int T, int rows, int E) { return T <= kB128StreamTokens && row
 // x quantized, y = x W^T.
 hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, float* xscale,
                               bool y_bf16, hipStream_t s) {
-  hipError_t e = quantize_rows<bf16>(a.rows, a.Kd, x, xq, xscale, s);
+  hipError_t e = quantize_rows<bf16, true>(a.rows, a.Kd, x, xq, xscale, s);
   if (e != hipSuccess) return e;
   if (a.rows <= 128)
     return y_bf16 ? launch_stream<kPlain, 4, 1, 1, 1, 2, bf16>(a, s)
@@ -719,11 +763,11 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
 // are the two products' arguments.
 hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,
                                   uint8_t* xq, float* xscale, bool y_bf16, hipStream_t s) {
-  hipError_t e = quantize_rows<bf16>(gu.T, gu.Kd, x, xq, xscale, s);
+  hipError_t e = quantize_rows<bf16, true>(gu.T, gu.Kd, x, xq, xscale, s);
   if (e != hipSuccess) return e;
   if (b128_streams(gu.T, gu.rows, gu.E)) {
     if ((e = launch_stream<kGateUp, 4, 1, 1, 2, 2, float>(gu, s)) != hipSuccess) return e;
-    if ((e = quantize_rows<float>(gu.rows, gu.N, gu.h, gu.hq, gu.hscale, s)) != hipSuccess)
+    if ((e = quantize_rows<float, true>(gu.rows, gu.N, gu.h, gu.hq, gu.hscale, s)) != hipSuccess)
       return e;
     return y_bf16 ? launch_stream<kPlain, 1, 4, 1, 1, 2, bf16>(dn, s)
                   : launch_stream<kPlain, 1, 4, 1, 1, 2, float>(dn, s);

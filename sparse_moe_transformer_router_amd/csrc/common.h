@@ -69,6 +69,15 @@ __device__ __forceinline__ void lds_copy16(const void* gsrc, const void* lds) {
                : "memory", "m0");
 }
 
+// The same from a base that all lanes share and a 32-bit byte offset per lane.
+__device__ __forceinline__ void lds_copy16(const void* base, unsigned off, const void* lds) {
+  const unsigned m0 = __builtin_amdgcn_readfirstlane((unsigned)(uintptr_t)lds);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(m0)
+               : "memory", "m0");
+}
+
 // s_barrier that the compiler may not move memory accesses across.
 __device__ __forceinline__ void block_barrier() {
   __builtin_amdgcn_s_barrier();

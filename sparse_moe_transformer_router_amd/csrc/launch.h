@@ -246,7 +246,7 @@ struct B128Args {
   int Kd;                      // contraction length, a multiple of 16
   int N;                       // output columns (gate_up: the expert width)
   bool ident;
-  const uint8_t* xq;           // [., Kd] codes of the input rows
+  const uint8_t* xq;           // [., Kd rounded up to 128] codes of the input rows, zeros past Kd
   const float* xscale;         // [., ceil(Kd / 128)]
   const uint8_t* wq;           // [E, N or 2N, Kd]
   const float* wscale;         // [E, ceil(N or 2N / 128), ceil(Kd / 128)]
@@ -254,7 +254,7 @@ struct B128Args {
   const int32_t* sorted_slots; // [rows] (unused when ident)
   const float* topk_w;         // [rows] (down only)
   float* h;                    // [rows, N] (gate_up, few rows per group)
-  uint8_t* hq;                 // [rows, N] codes of h (gate_up)
+  uint8_t* hq;                 // [rows, N rounded up to 128] codes of h (gate_up)
   float* hscale;               // [rows, ceil(N / 128)]
   void* y;                     // [rows, N] (down, linear)
 };

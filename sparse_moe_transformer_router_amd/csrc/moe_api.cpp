@@ -156,10 +156,10 @@ Layout layout(const moe_dims* d, long long T) {
   const size_t I = (size_t)d->expert_inter;
   const size_t ts = (size_t)(T < moe::kB128StreamTokens ? T : moe::kB128StreamTokens);
   o = L.base_end;
-  L.b_xq = take((size_t)T * H);
+  L.b_xq = take((size_t)T * ((H + 127) / 128 * 128));
   L.b_xs = take(4 * (size_t)T * ((H + 127) / 128));
   L.b_h = take(4 * ts * d->top_k * I);  // fp32, the weight-streaming form only
-  L.b_hq = take((size_t)S * I);
+  L.b_hq = take((size_t)S * ((I + 127) / 128 * 128));
   L.b_hs = take(4 * (size_t)S * ((I + 127) / 128));
   if (o > L.total) L.total = o;
   return L;
@@ -820,7 +820,7 @@ int check_linear(int32_t T, int32_t out_features, int32_t in_features) {
 }
 
 size_t linear_scale_offset(int32_t T, int32_t in_features) {
-  return align256((size_t)T * in_features);
+  return align256((size_t)T * ((in_features + 127) / 128 * 128));
 }
 
 }  // namespace

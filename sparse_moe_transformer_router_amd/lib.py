@@ -130,6 +130,12 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
+def _current_device() -> int:
+    """Index of the current GPU, -2 before torch has set one up (a CPU tensor's
+    device is -1)."""
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+
+
 def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, optional: bool = False):
     """Device pointer of an array argument, after its type and size: a tensor of
     dtype (or of one of several) with at least numel elements, on the current
@@ -138,13 +144,15 @@ def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, optional: bool
         if optional:
             return None
         raise ValueError(f"{name} is required")
-    if t.dtype != dtype and not (isinstance(dtype, tuple) and t.dtype in dtype):
+    if t.dtype is not dtype and not (type(dtype) is tuple and t.dtype in dtype):
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, {numel} needed")
-    if not t.is_cuda or t.get_device() != torch.cuda.current_device():
+    if t.get_device() != _current_device():
         raise ValueError(f"{name} is on {t.device}, not on the current GPU")
-    return _ptr(t)
+    if not t.is_contiguous():
+        raise ValueError("tensors passed to libmoe must be contiguous")
+    return t.data_ptr()
 
 
 _MASK = (torch.uint8, torch.bool)
@@ -156,9 +164,14 @@ def _act(d: MoeDims):
 
 
 def _stream(stream):
+    """The hipStream_t of a torch stream, the current one if none is given (asked
+    for by its raw handle: a torch.cuda.Stream object costs a few microseconds,
+    as much as a small call's launches)."""
     if stream is None:
-        stream = torch.cuda.current_stream()
-    return ctypes.c_void_p(stream.cuda_stream)
+        if not torch.cuda.is_initialized():
+            torch.cuda.init()
+        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
+    return stream.cuda_stream
 
 
 def _check(rc: int):

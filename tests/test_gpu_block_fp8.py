@@ -90,10 +90,11 @@ def _check_linear(x, q, s, y):
     (1, 1, 16), (1, 2112, 2816), (2, 5, 48), (15, 255, 128), (16, 64, 144), (17, 257, 272),
     (37, 1003, 1520), (64, 704, 2816), (127, 130, 704), (128, 96, 2960), (129, 97, 2960),
     (200, 1003, 208), (257, 257, 128), (300, 513, 6016), (513, 1, 16), (640, 2816, 704),
-    (1025, 130, 2944)])
+    (1025, 130, 2944),
+    (260, 130, 2816), (260, 130, 5632)])
 def test_linear(T, N, K):
-    """One k-block and many (past the 23 whose scales a tile holds), partial
-    ones, single rows and columns, both forms."""
+    """One k-block and many (up to, at and past the 22 whose scales a tile
+    holds), partial ones, single rows and columns, both forms."""
     g = _gen(T * 7 + N + K)
     x = _x(g, T, K)
     q, s = _weights(g, N, K)
