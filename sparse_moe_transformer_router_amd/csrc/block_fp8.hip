@@ -31,14 +31,15 @@ typedef int i32x8 __attribute__((ext_vector_type(8)));
 constexpr int kBlk = 128;              // values that share a scale
 constexpr float kE4m3Max = 448.0f;
 constexpr float kInvE4m3Max = 1.0f / 448.0f;  // a block's scale is max |v| times this
-constexpr uint32_t kUnitScale = 127;   // E8M0 code of 1.0
 
 __host__ __device__ constexpr int blocks_of(int n) { return (n + kBlk - 1) / kBlk; }
 
-// The sum of 128 products per result, from zero.
+// The sum of 128 products per result, from zero.  Scale operands of 0 select the
+// instruction without block scales (the scaled form, with unit scales, ran the
+// tiles' inner loop at 0.9 of its rate).
 __device__ __forceinline__ f32x4 mfma_blk(i32x8 w, i32x8 x) {
   return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-      w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, (int)kUnitScale, 0, (int)kUnitScale);
+      w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
 
 // Maximum over the 16 lanes of a DPP row, in every lane.
@@ -483,10 +484,13 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       src[j] = (unsigned)wrow(line - kTM) * (unsigned)Kd;
     }
   }
-  auto copy = [&](int kt, int st) __attribute__((always_inline)) {
-    const unsigned kx = (kt * 8 + chunk) * 16, kw = min(kt * 8 + chunk, Kd / 16 - 1) * 16;
+  // Copies 2 p and 2 p + 1 of k-block kt (past the last one the last again:
+  // bytes that are never read).
+  auto copy = [&](int kt, int st, int p) __attribute__((always_inline)) {
+    const int kc = min(kt, KB - 1) * 8 + chunk;
+    const unsigned kx = kc * 16, kw = min(kc, Kd / 16 - 1) * 16;
 #pragma unroll
-    for (int j = 0; j < COPIES; ++j) {
+    for (int j = 2 * p; j < 2 * p + 2; ++j) {
 #if defined(__HIP_DEVICE_COMPILE__)
       unsigned char* to = smem + st * kStageBytes + (kTileWaves * j + wave) * 1024;
       if (j < COPIES / 2) lds_copy16(xbase, src[j] + kx, to);
@@ -499,16 +503,21 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   const float* wsbase = a.wscale + (long long)e * blocks_of(NR) * KB;
   const int wblk0 = nbase / kBlk, wblk_up = (N + nbase) / kBlk;
   auto load_scales = [&](int kb0) {
+    // all of a thread's loads before the first store: one after the other they
+    // had cost 8 us a run
+    constexpr int NX = kTileBlocks * kTM / (64 * kTileWaves);
     const int n = min(kTileBlocks, KB - kb0);
-    for (int i = tid; i < n * kTM; i += 64 * kTileWaves) {
-      const int r = i % kTM, kb = i / kTM;
-      s_x[i] = a.xscale[(long long)rtok[r] * KB + kb0 + kb];
-    }
-    for (int i = tid; i < n * 4; i += 64 * kTileWaves) {
-      const int kb = i / 4, w = i % 4;
-      const int blk = MODE == kGateUp && w >= 2 ? wblk_up + w - 2 : wblk0 + w;
-      s_w[i] = wsbase[(long long)min(blk, blocks_of(NR) - 1) * KB + kb0 + kb];
-    }
+    const int r = tid % kTM, kr = tid / kTM, step = 64 * kTileWaves / kTM;
+    const float* row = a.xscale + (long long)rtok[r] * KB + kb0;
+    float v[NX];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) v[i] = row[min(kr + step * i, n - 1)];
+    const int kw = min(tid / 4, n - 1), w = tid % 4;
+    const int blk = MODE == kGateUp && w >= 2 ? wblk_up + w - 2 : wblk0 + w;
+    const float vw = wsbase[(long long)min(blk, blocks_of(NR) - 1) * KB + kb0 + kw];
+#pragma unroll
+    for (int i = 0; i < NX; ++i) s_x[(kr + step * i) * kTM + r] = v[i];
+    if (tid < kTileBlocks * 4) s_w[tid] = vw;
   };
   // this wave's weight tiles: their scale slots (the two halves of a gate_up
   // wave, else one), fragment offsets
@@ -582,7 +591,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
         wait_lds();
         wait_vmem<0>();
         block_barrier();
-        copy(min(kt + 2, KB - 1), st);  // past the end: bytes that are never read
+        copy(kt + 2, st, 0);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -592,6 +601,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
         read_first(1 - st);  // (past the end: never used)
         __builtin_amdgcn_sched_barrier(0);
       }
+#pragma unroll
+      for (int p = 1; p < 4; ++p)
+        if (i == (TV == 8 ? p - 1 : 0)) copy(kt + 1, 1 - st, p);
       if (i > 0) scale_add(i - 1);
       __builtin_amdgcn_sched_barrier(0);  // no fragment is read further ahead
     }
@@ -611,11 +623,12 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       }
     }
   };
-  copy(0, 0);
+#pragma unroll
+  for (int p = 0; p < 4; ++p) copy(0, 0, p);
   load_scales(0);
   wait_vmem<0>();
   __syncthreads();
-  copy(min(1, KB - 1), 1);
+  copy(1, 1, 0);
   read_first(0);
   // as many tiles as hold the wave's rows (every wave takes part in the copies
   // and barriers)
