@@ -183,6 +183,16 @@ __global__ __launch_bounds__(256) void dequantize_b128_kernel(long long total_ro
 // ---------------------------------------------------------------------------
 constexpr int kGateUp = 0, kPlain = 1;
 
+// The tanh form of GELU as z / (1 + exp(-2 u)), u = sqrt(2 / pi) (z + 0.044715
+// z^3), on the hardware's exponential and reciprocal (each within an ulp).  No
+// cancellation where tanh u nears -1; tanhf had taken half of a gate_up tile's
+// time past its products.
+__device__ __forceinline__ float gelu_sigmoid(float z) {
+  constexpr float c = -2.0f * 0.7978845608028654f * 1.4426950408889634f;  // in powers of 2
+  const float u = c * (z + 0.044715f * z * z * z);
+  return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u));
+}
+
 // Where lane group g's two 16-byte halves of k-block kb lie in a row of Kd
 // values, moved to the row's start where they pass its end (v0, v1: inside).
 __device__ __forceinline__ void spans(int kb, int g, int Kd, int& o0, int& o1, bool& v0,
@@ -205,13 +215,15 @@ __device__ __forceinline__ i32x8 keep32(i32x8 v, bool v0, bool v1) {
                v1 ? v[4] : 0, v1 ? v[5] : 0, v1 ? v[6] : 0, v1 ? v[7] : 0};
 }
 
-// Four consecutive outputs of a row of N columns from column n.
-template <typename YT>
+// Four consecutive outputs of a row of N columns from column n.  ONCE: fp32 in
+// streaming stores (slots, which the combine reads once).
+template <bool ONCE = false, typename YT>
 __device__ __forceinline__ void store4(YT* __restrict__ row, int n, int N, f32x4 v) {
   if (N % 4 == 0) {
     if (n >= N) return;
     if constexpr (std::is_same<YT, float>::value) {
-      *reinterpret_cast<f32x4*>(row + n) = v;
+      if constexpr (ONCE) __builtin_nontemporal_store(v, reinterpret_cast<f32x4*>(row + n));
+      else *reinterpret_cast<f32x4*>(row + n) = v;
     } else {
       typedef bf16 bf16x4 __attribute__((ext_vector_type(4)));
       *reinterpret_cast<bf16x4*>(row + n) =
@@ -367,7 +379,7 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
       if (row >= row1) continue;
       if constexpr (MODE == kGateUp) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = gelu_tanh(v[r]) * u[r];
+        for (int r = 0; r < 4; ++r) v[r] = gelu_sigmoid(v[r]) * u[r];
         store4(a.h + (size_t)row * a.N, n, a.N, v);
       } else {
         size_t to = row;
@@ -392,23 +404,36 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 // used up.  A wave multiplies one 16-row tile of activations by its four
 // weight tiles, and scales the previous tile's results meanwhile.
 // ---------------------------------------------------------------------------
-constexpr int kTM = 256, kTN = 256, kTileWaves = 8;
 constexpr int kTileBlocks = 22;  // even: a run of k-blocks starts in stage 0
 constexpr int kRowGroup = 4;
-constexpr int kStageBytes = (kTM + kTN) * kBlk;
-constexpr int kRingBytes = 2 * kStageBytes;
-constexpr int kScaleOff = kRingBytes;                               // [kTileBlocks][256]
-constexpr int kWScaleOff = kScaleOff + kTileBlocks * kTM * 4;       // [kTileBlocks][4]
-constexpr int kTabOff = kWScaleOff + kTileBlocks * 4 * 4;           // rtok, slot, weight
-constexpr int kTileLds = kTabOff + 3 * kTM * 4;
-constexpr int kHPitch = kTN / 2 + 4;                                // floats
-static_assert(kTM * kHPitch * 4 <= kTabOff, "h is staged over the ring and the scales");
-static_assert(kTileLds <= 160 * 1024, "LDS per CU");
 
-template <int MODE, typename YT>
-__global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args a) {
-  constexpr int TI = 8, TJ = 4;       // 16-row tiles of activations, weight tiles per wave
-  constexpr int COPIES = kStageBytes / (64 * kTileWaves * 16);
+// WM x WN waves of 16 TI x 64.
+template <int WM, int WN, int TI>
+struct TileShape {
+  static constexpr int TM = WM * TI * 16, TN = WN * 64, NW = WM * WN, THREADS = 64 * NW;
+  static constexpr int STAGE = (TM + TN) * kBlk;
+  static constexpr int COPIES = STAGE / (THREADS * 16);           // per wave and stage
+  static constexpr int XCOPIES = TM * kBlk / (THREADS * 16);      // of them activations
+  static constexpr int SX = 2 * STAGE;                            // [kTileBlocks][TM]
+  static constexpr int SW = SX + kTileBlocks * TM * 4;            // [kTileBlocks][4]
+  static constexpr int TAB = SW + kTileBlocks * 4 * 4;            // rtok, slot, weight
+  static constexpr int LDS = TAB + 3 * TM * 4;
+  static constexpr int HPITCH = TN / 2 + 4;                       // floats
+  static_assert(XCOPIES * THREADS * 16 == TM * kBlk && COPIES % 4 == 0, "copies cover a stage");
+  static_assert(LDS <= 160 * 1024, "LDS per CU");
+};
+typedef TileShape<2, 4, 8> WideTile;    // 256 x 256, one block per CU
+typedef TileShape<2, 2, 4> SmallTile;   // 128 x 128, two blocks per CU
+static_assert(WideTile::TM * WideTile::HPITCH * 4 <= WideTile::TAB,
+              "h is staged over the ring and the scales");
+static_assert(2 * SmallTile::LDS <= 160 * 1024, "two blocks share a CU");
+
+template <int MODE, int WM, int WN, int TI, typename YT>
+__global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) {
+  typedef TileShape<WM, WN, TI> S;
+  constexpr int TJ = 4;  // weight tiles of 16 rows per wave
+  constexpr int kTM = S::TM, kTN = S::TN, COPIES = S::COPIES;
+  static_assert(MODE != kGateUp || kTN == 256, "a gate_up tile makes one 128-block of h");
   extern __shared__ __align__(16) unsigned char smem[];
   const int Kd = a.Kd, KB = blocks_of(Kd), N = a.N;
   const int NR = MODE == kGateUp ? 2 * N : N;
@@ -439,11 +464,11 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   }
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
-  const int wm = wave / 4, wn = wave % 4;
+  const int wm = wave / WN, wn = wave % WN;
   const int nbase = nt * COLS;
-  float* s_x = reinterpret_cast<float*>(smem + kScaleOff);
-  float* s_w = reinterpret_cast<float*>(smem + kWScaleOff);
-  int* rtok = reinterpret_cast<int*>(smem + kTabOff);
+  float* s_x = reinterpret_cast<float*>(smem + S::SX);
+  float* s_w = reinterpret_cast<float*>(smem + S::SW);
+  int* rtok = reinterpret_cast<int*>(smem + S::TAB);
   int* row_slot = rtok + kTM;
   float* row_w = reinterpret_cast<float*>(row_slot + kTM);
   if (tid < kTM) {
@@ -464,8 +489,8 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
     const int col = min(nbase + n - (up ? kTN / 2 : 0), N - 1);
     return col + (up ? N : 0);
   };
-  // Copy j of wave w fills lines 8 (8 j + w) .. + 7 of a stage: activations for
-  // j < 4, weights past that.  Byte offsets from the tile's bases: below 2^32 (a
+  // Copy j of wave w fills lines 8 (NW j + w) .. + 7 of a stage: activations for
+  // j < XCOPIES, weights past that.  Byte offsets from the tile's bases: below 2^32 (a
   // batch's codes of x take 2^30 bytes at most, an expert's weights 2^32).
   // Activation rows end in zeros up to a whole line, so what the weights' part
   // of the last line holds past their row does not matter: their own last
@@ -476,24 +501,24 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   const int chunk = (lane % 8) ^ (lane / 8);
 #pragma unroll
   for (int j = 0; j < COPIES; ++j) {
-    const int line = 8 * (kTileWaves * j + wave) + lane / 8;
-    if (j < COPIES / 2) {
+    const int line = 8 * (S::NW * j + wave) + lane / 8;
+    if (j < S::XCOPIES) {
       const int row = MODE == kGateUp ? rtok[line] : min(line, row1 - 1 - row0);
       src[j] = (unsigned)row * (unsigned)pitch;
     } else {
       src[j] = (unsigned)wrow(line - kTM) * (unsigned)Kd;
     }
   }
-  // Copies 2 p and 2 p + 1 of k-block kt (past the last one the last again:
+  // Quarter p of the copies of k-block kt (past the last one the last again:
   // bytes that are never read).
   auto copy = [&](int kt, int st, int p) __attribute__((always_inline)) {
     const int kc = min(kt, KB - 1) * 8 + chunk;
     const unsigned kx = kc * 16, kw = min(kc, Kd / 16 - 1) * 16;
 #pragma unroll
-    for (int j = 2 * p; j < 2 * p + 2; ++j) {
+    for (int j = p * COPIES / 4; j < (p + 1) * COPIES / 4; ++j) {
 #if defined(__HIP_DEVICE_COMPILE__)
-      unsigned char* to = smem + st * kStageBytes + (kTileWaves * j + wave) * 1024;
-      if (j < COPIES / 2) lds_copy16(xbase, src[j] + kx, to);
+      unsigned char* to = smem + st * S::STAGE + (S::NW * j + wave) * 1024;
+      if (j < S::XCOPIES) lds_copy16(xbase, src[j] + kx, to);
       else lds_copy16(wbase, src[j] + kw, to);
 #endif
     }
@@ -505,9 +530,9 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   auto load_scales = [&](int kb0) {
     // all of a thread's loads before the first store: one after the other they
     // had cost 8 us a run
-    constexpr int NX = kTileBlocks * kTM / (64 * kTileWaves);
+    constexpr int NX = kTileBlocks * kTM / (S::THREADS);
     const int n = min(kTileBlocks, KB - kb0);
-    const int r = tid % kTM, kr = tid / kTM, step = 64 * kTileWaves / kTM;
+    const int r = tid % kTM, kr = tid / kTM, step = S::THREADS / kTM;
     const float* row = a.xscale + (long long)rtok[r] * KB + kb0;
     float v[NX];
 #pragma unroll
@@ -531,14 +556,14 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   }
   // Lines 16 apart have the same swizzle, so a wave's tiles lie at constants
   // from its first: activations i * 16 lines, weights as wtile().
-  const int xline = wm * 128 + fr;
+  const int xline = wm * TI * 16 + fr;
   const int xoff = xline * kBlk + (g ^ (xline & 7)) * 16;
   const int wline = kTM + wn * (MODE == kGateUp ? 32 : 64) + fr;
   const int woff = wline * kBlk + (g ^ (wline & 7)) * 16;
   auto wtile = [](int j) {
     return (MODE == kGateUp ? (j / 2) * (kTN / 2) + (j % 2) * 16 : j * 16) * kBlk;
   };
-  int nv = (row1 - row0 - wm * 128 + 15) / 16;             // tiles of this wave with rows
+  int nv = (row1 - row0 - wm * TI * 16 + 15) / 16;             // tiles of this wave with rows
   nv = __builtin_amdgcn_readfirstlane(max(0, min(TI, nv)));
 
   f32x4 acc[TI][TJ];
@@ -549,7 +574,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
 
   // Fragment at a wave's first tile + at, of stage `st`.
   auto rd = [&](int st, int off, int at) __attribute__((always_inline)) {
-    const unsigned char* p = smem + st * kStageBytes;
+    const unsigned char* p = smem + st * S::STAGE;
     return pack8(*reinterpret_cast<const uint4*>(p + off + at),
                  *reinterpret_cast<const uint4*>(p + (off ^ 64) + at));
   };
@@ -603,7 +628,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       }
 #pragma unroll
       for (int p = 1; p < 4; ++p)
-        if (i == (TV == 8 ? p - 1 : 0)) copy(kt + 1, 1 - st, p);
+        if (i == (TV >= 4 ? (p - 1) * TV / 8 : 0)) copy(kt + 1, 1 - st, p);
       if (i > 0) scale_add(i - 1);
       __builtin_amdgcn_sched_barrier(0);  // no fragment is read further ahead
     }
@@ -632,7 +657,7 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
   read_first(0);
   // as many tiles as hold the wave's rows (every wave takes part in the copies
   // and barriers)
-  if (nv > 4) loop(std::integral_constant<int, 8>{});
+  if (TI > 4 && nv > 4) loop(std::integral_constant<int, TI>{});
   else if (nv > 2) loop(std::integral_constant<int, 4>{});
   else loop(std::integral_constant<int, 2>{});
   wait_vmem<0>();
@@ -651,21 +676,21 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
         f32x4 v;
 #pragma unroll
         for (int r = 0; r < 4; ++r)
-          v[r] = nbase + c + r < N ? gelu_tanh(acc[i][j][r]) * acc[i][2 + j][r] : 0.0f;
-        *reinterpret_cast<f32x4*>(hs + (xline + 16 * i) * kHPitch + c) = v;
+          v[r] = nbase + c + r < N ? gelu_sigmoid(acc[i][j][r]) * acc[i][2 + j][r] : 0.0f;
+        *reinterpret_cast<f32x4*>(hs + (xline + 16 * i) * S::HPITCH + c) = v;
       }
     }
     __syncthreads();
     const int nbh = blocks_of(N);
 #pragma unroll
-    for (int it = 0; it < kTM * 4 / (64 * kTileWaves); ++it) {
-      const int k = tid + it * 64 * kTileWaves, r = k / 4, c = 32 * (k % 4);
+    for (int it = 0; it < kTM * 4 / (S::THREADS); ++it) {
+      const int k = tid + it * S::THREADS, r = k / 4, c = 32 * (k % 4);
       const bool on = row0 + r < row1;
       float v[32];
       float m = 0.0f;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
-        const float4 f = *reinterpret_cast<const float4*>(hs + r * kHPitch + c + 4 * i);
+        const float4 f = *reinterpret_cast<const float4*>(hs + r * S::HPITCH + c + 4 * i);
         v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
       }
 #pragma unroll
@@ -673,13 +698,16 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       m = fmaxf(m, dpp_f<0xB1>(m));
       m = fmaxf(m, dpp_f<0x4E>(m));
       const float s = m * kInvE4m3Max;
+      // one division a row: h is an fp32 sum already, no decision point is hit
+      // exactly, and an ulp of the quotient moves no more codes than one of h
+      const float inv = s > 0.0f ? 1.0f / s : 0.0f;
       if (!on) continue;  // columns past the last are zeros: the row's padding
       uint32_t q[8];
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         float t[4];
 #pragma unroll
-        for (int u = 0; u < 4; ++u) t[u] = s > 0.0f ? v[4 * i + u] / s : 0.0f;
+        for (int u = 0; u < 4; ++u) t[u] = v[4 * i + u] * inv;
         q[i] = encode4(t[0], t[1], t[2], t[3]);
       }
       uint4* dst = reinterpret_cast<uint4*>(a.hq + (size_t)(row0 + r) * (nbh * kBlk) + nbase + c);
@@ -688,16 +716,33 @@ __global__ __launch_bounds__(64 * kTileWaves, 1) void tile_b128_kernel(B128Args 
       if (c == 0) a.hscale[(size_t)(row0 + r) * nbh + nbase / kBlk] = s;
     }
   } else {
+    // through LDS, 128 rows at a time, so that a wave stores whole rows of the
+    // tile (as the results lie, 64 bytes of 16 rows: the stores of fp32 slots
+    // took twice the time)
+    constexpr int PITCH = kTN + 4, ROWS = 128, CH = kTN / 4;
+    static_assert(ROWS * PITCH * 4 <= S::TAB, "results are staged over the ring and the scales");
+    float* ys = reinterpret_cast<float*>(smem);
 #pragma unroll
-    for (int i = 0; i < TI; ++i) {
-      if (i >= nv) break;
-      const int r = xline + 16 * i;
-      if (row0 + r >= row1) continue;
-      const float w = row_w[r];
-      YT* out = static_cast<YT*>(a.y) + (size_t)row_slot[r] * N;
+    for (int pass = 0; pass < kTM / ROWS; ++pass) {
+      if (pass > 0) __syncthreads();
+      if (wm * TI * 16 / ROWS == pass) {
 #pragma unroll
-      for (int j = 0; j < TJ; ++j)
-        store4(out, nbase + wn * 64 + 16 * j + 4 * g, N, acc[i][j] * w);
+        for (int i = 0; i < TI; ++i) {
+          if (i >= nv) break;
+          float* row = ys + ((wm * TI * 16) % ROWS + 16 * i + fr) * PITCH + wn * 64 + 4 * g;
+#pragma unroll
+          for (int j = 0; j < TJ; ++j) *reinterpret_cast<f32x4*>(row + 16 * j) = acc[i][j];
+        }
+      }
+      __syncthreads();
+#pragma unroll 4
+      for (int k = tid; k < ROWS * CH; k += S::THREADS) {
+        const int r = k / CH, c = 4 * (k % CH), rr = pass * ROWS + r;
+        if (row0 + rr >= row1) break;
+        const f32x4 v = *reinterpret_cast<const f32x4*>(ys + r * PITCH + c);
+        store4<true>(static_cast<YT*>(a.y) + (size_t)row_slot[rr] * N, nbase + c, N,
+                     v * row_w[rr]);
+      }
     }
   }
 }
@@ -711,18 +756,27 @@ hipError_t launch_stream(const B128Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MODE, typename YT>
+template <int MODE, int WM, int WN, int TI, typename YT>
 hipError_t launch_tile(const B128Args& a, hipStream_t s) {
-  auto kf = tile_b128_kernel<MODE, YT>;
+  typedef TileShape<WM, WN, TI> S;
+  auto kf = tile_b128_kernel<MODE, WM, WN, TI, YT>;
   // set on every call: the attribute belongs to the current device
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kf),
-                                           hipFuncAttributeMaxDynamicSharedMemorySize, kTileLds);
+                                           hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
   if (e != hipSuccess) return e;
-  const int COLS = MODE == kGateUp ? kTN / 2 : kTN;
-  const long long grid = (long long)tile_count_bound(a.ident, a.rows, a.T, a.E, kTM) *
+  const int COLS = MODE == kGateUp ? S::TN / 2 : S::TN;
+  const long long grid = (long long)tile_count_bound(a.ident, a.rows, a.T, a.E, S::TM) *
                          ((a.N + COLS - 1) / COLS);
-  hipLaunchKernelGGL(kf, dim3((unsigned)grid), dim3(64 * kTileWaves), kTileLds, s, a);
+  hipLaunchKernelGGL(kf, dim3((unsigned)grid), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
+}
+template <int MODE, typename YT>
+hipError_t launch_wide(const B128Args& a, hipStream_t s) {
+  return launch_tile<MODE, 2, 4, 8, YT>(a, s);
+}
+template <typename YT>
+hipError_t launch_small(const B128Args& a, hipStream_t s) {
+  return launch_tile<kPlain, 2, 2, 4, YT>(a, s);
 }
 
 template <typename XT, bool PAD>
@@ -761,6 +815,19 @@ hipError_t launch_dequantize_b128(int block_rows, long long batch, int rows, int
 
 bool b128_streams(int T, int rows, int E) { return T <= kB128StreamTokens && rows <= 16 * E; }
 
+// Whether a product of one group takes the 128 x 128 tiles: by the rounds of
+// blocks that each shape needs.  A round of 256 wide tiles takes some 8 units, of
+// 512 small ones (two per CU) 5, and one of at most 256 small ones 3.3 (at
+// 2112-long rows, 2816 columns: 256 / 1024 / 2048 / 4096 / 8192 tokens 21 / 24 /
+// 32 / 51 / 84 us small, 38 / 41 / 44 / 49 / 86 us wide).
+static bool linear_takes_small(long long rows, long long cols) {
+  const long long small = (rows + 127) / 128 * ((cols + 127) / 128);
+  const long long wide = (rows + 255) / 256 * ((cols + 255) / 256);
+  const long long rest = small % 512;
+  const double s = 5.0 * (small / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 3.3 : 5.0);
+  return s < 8.0 * ((wide + 255) / 256);
+}
+
 // x quantized, y = x W^T.
 hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, float* xscale,
                               bool y_bf16, hipStream_t s) {
@@ -769,7 +836,9 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
   if (a.rows <= 128)
     return y_bf16 ? launch_stream<kPlain, 4, 1, 1, 1, 2, bf16>(a, s)
                   : launch_stream<kPlain, 4, 1, 1, 1, 2, float>(a, s);
-  return y_bf16 ? launch_tile<kPlain, bf16>(a, s) : launch_tile<kPlain, float>(a, s);
+  if (linear_takes_small(a.rows, a.N))
+    return y_bf16 ? launch_small<bf16>(a, s) : launch_small<float>(a, s);
+  return y_bf16 ? launch_wide<kPlain, bf16>(a, s) : launch_wide<kPlain, float>(a, s);
 }
 
 // x quantized; h = GELU(gate) * up, quantized; y = topk_w * down h.  gu and dn
@@ -785,8 +854,13 @@ hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const 
     return y_bf16 ? launch_stream<kPlain, 1, 4, 1, 1, 2, bf16>(dn, s)
                   : launch_stream<kPlain, 1, 4, 1, 1, 2, float>(dn, s);
   }
-  if ((e = launch_tile<kGateUp, float>(gu, s)) != hipSuccess) return e;
-  return y_bf16 ? launch_tile<kPlain, bf16>(dn, s) : launch_tile<kPlain, float>(dn, s);
+  if ((e = launch_wide<kGateUp, float>(gu, s)) != hipSuccess) return e;
+  // down: the small tiles while an expert has fewer than some 96 rows on average
+  // (26B-A4B experts and combine at 512 / 1024 / 2048 / 4096 tokens: 225 / 255 /
+  // 348 / 520 us small, 234 / 264 / 341 / 480 us wide)
+  if (dn.rows < 96LL * dn.E)
+    return y_bf16 ? launch_small<bf16>(dn, s) : launch_small<float>(dn, s);
+  return y_bf16 ? launch_wide<kPlain, bf16>(dn, s) : launch_wide<kPlain, float>(dn, s);
 }
 
 }  // namespace moe
