@@ -85,7 +85,7 @@ struct RouterGradArgs {
   float* d_router_scale;          // [H]
   float* d_per_expert_scale;      // [E]
   float* d_pre_gain;              // [H] or nullptr
-  float* ws_dl;                   // [T,E]
+  void* ws_dl;                    // router_grad_dl_bytes
   float* ws_beta;                 // [T]
   float* ws_part_g;               // [splits,E,H]
   float* ws_part_b;               // [splits,H]
@@ -93,6 +93,7 @@ struct RouterGradArgs {
 };
 int router_grad_splits(int T);
 int router_grad_row_blocks(int T);
+size_t router_grad_dl_bytes(int T, int H, int E);
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);
 
 struct DispatchArgs {

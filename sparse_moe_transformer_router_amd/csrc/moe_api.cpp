@@ -147,7 +147,7 @@ Layout layout(const moe_dims* d, long long T) {
   if (o > L.total) L.total = o;
   const size_t splits = (size_t)moe::router_grad_splits((int)T);
   o = L.base_end;
-  L.rg_dl = take(4 * (size_t)T * E);
+  L.rg_dl = take(moe::router_grad_dl_bytes((int)T, d->hidden, d->num_experts));
   L.rg_beta = take(4 * (size_t)T);
   L.rg_g = take(4 * splits * E * H);
   L.rg_b = take(4 * splits * H);
@@ -623,7 +623,7 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
   a.topk_idx = topk_idx; a.mask = token_mask; a.d_topk_w = d_topk_w; a.d_logits = d_logits;
   a.d_x = d_x; a.d_router_w = d_router_w; a.d_router_scale = d_router_scale;
   a.d_per_expert_scale = d_per_expert_scale; a.d_pre_gain = d_pre_norm_gain;
-  a.ws_dl = at<float>(ws, L.rg_dl); a.ws_beta = at<float>(ws, L.rg_beta);
+  a.ws_dl = at<void>(ws, L.rg_dl); a.ws_beta = at<float>(ws, L.rg_beta);
   a.ws_part_g = at<float>(ws, L.rg_g); a.ws_part_b = at<float>(ws, L.rg_b);
   a.ws_part_pes = at<float>(ws, L.rg_pes);
   hipError_t e = moe::launch_router_grad(a, static_cast<hipStream_t>(stream));

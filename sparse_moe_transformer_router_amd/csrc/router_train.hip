@@ -366,9 +366,110 @@ __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
 
+// One token's share, by a wave: dl (experts lane + 64 j) scaled by r0 r, beta,
+// and d_topk_w_k q_k added to dpes.  A masked token gives zeros.
 template <typename XT>
+__device__ __forceinline__ void router_grad_token(
+    int t, bool live, int H, int E, int K, float eps, const XT* __restrict__ x,
+    const float* __restrict__ pre_gain, const float* __restrict__ pes,
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const float* __restrict__ d_w, const float* __restrict__ d_logits, float (&dl)[4],
+    float& beta, float (&dpes)[4]) {
+  const int lane = lane_id();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dl[j] = 0.0f;
+  beta = 0.0f;
+  if (!live) return;  // uniform over the wave
+  // the token's small rows first: their latency passes behind x's
+  float l[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = lane + kWave * j;
+    l[j] = e < E ? logits[(size_t)t * E + e] : 0.0f;
+    if (d_logits != nullptr && e < E) dl[j] = d_logits[(size_t)t * E + e];
+  }
+  // lane k < K: slot k (an id outside [0, E) is no slot)
+  int e = -1;
+  float lk = -INFINITY, dw = 0.0f, pk = 0.0f;
+  if (d_w != nullptr && lane < K) {
+    e = topk_idx[(size_t)t * K + lane];
+    if ((unsigned)e < (unsigned)E) {
+      lk = logits[(size_t)t * E + e];
+      dw = d_w[(size_t)t * K + lane];
+      pk = pes[e];
+    } else {
+      e = -1;
+    }
+  }
+  float ss = 0.0f, sg = 0.0f;
+  const XT* xr = x + (size_t)t * H;
+  for (int h = 8 * lane; h < H; h += 8 * kWave) {
+    float v[8];
+    load8f(xr + h, v);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
+    if (pre_gain != nullptr) {
+      float g[8];
+      load8f(pre_gain + h, g);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) sg = __builtin_fmaf(v[i] * g[i], v[i] * g[i], sg);
+    }
+  }
+  ss = group_sum<kWave>(ss);
+  float r0 = 1.0f, r;
+  if (pre_gain != nullptr) {
+    sg = group_sum<kWave>(sg);
+    r0 = 1.0f / sqrtf(ss / (float)H + eps);
+    r = 1.0f / sqrtf(r0 * r0 * sg / (float)H + eps);
+  } else {
+    r = 1.0f / sqrtf(ss / (float)H + eps);
+  }
+  if (d_w != nullptr) {
+    const float top = group_max<kWave>(lk);
+    float q = lk == -INFINITY ? 0.0f : expf(lk - top);
+    const float z = group_sum<kWave>(q);
+    q = z > 0.0f ? q / z : 0.0f;
+    const float d = dw * pk;
+    const float qd = group_sum<kWave>(q * d);
+    const float dlk = q * (d - qd), dsk = dw * q;
+    for (int k = 0; k < K; ++k) {  // a repeated id adds up
+      const int ek = __builtin_amdgcn_readlane(e, k);
+      const float dk = lane_value(dlk, k), sk = lane_value(dsk, k);
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (ek == lane + kWave * j) {
+          dl[j] += dk;
+          dpes[j] += sk;
+        }
+    }
+  }
+  float D = 0.0f;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) D += dl[j] != 0.0f ? dl[j] * l[j] : 0.0f;
+  D = group_sum<kWave>(D);
+  const float scale = r0 * r;
+  beta = scale * scale * (D / (float)H);
+#pragma unroll
+  for (int j = 0; j < 4; ++j) dl[j] *= scale;
+}
+
+// The block's sums of dpes, added over its waves.
+__device__ __forceinline__ void store_pes_part(float (*sums)[kMaxE], int waves, int E,
+                                               const float (&dpes)[4], float* __restrict__ part) {
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+#pragma unroll
+  for (int j = 0; j < 4; ++j) sums[wave][lane + kWave * j] = dpes[j];
+  __syncthreads();
+  for (int e = threadIdx.x; e < E; e += blockDim.x) {
+    float s = 0.0f;
+    for (int w = 0; w < waves; ++w) s += sums[w][e];
+    part[(size_t)blockIdx.x * E + e] = s;
+  }
+}
+
+// fp32 inputs: dl' in fp32 [T, E].
 __global__ __launch_bounds__(64 * kRgRowWaves) void router_grad_rows_kernel(
-    int T, int H, int E, int K, float eps, const XT* __restrict__ x,
+    int T, int H, int E, int K, float eps, const float* __restrict__ x,
     const float* __restrict__ pre_gain, const float* __restrict__ pes,
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const uint8_t* __restrict__ mask, const float* __restrict__ d_w,
@@ -378,94 +479,17 @@ __global__ __launch_bounds__(64 * kRgRowWaves) void router_grad_rows_kernel(
   const int wave = threadIdx.x / kWave, lane = lane_id();
   float dpes[4] = {0.0f, 0.0f, 0.0f, 0.0f};  // experts lane + 64 j
   for (int t = blockIdx.x * kRgRowWaves + wave; t < T; t += gridDim.x * kRgRowWaves) {
-    const bool live = mask == nullptr || mask[t] != 0;  // uniform over the wave
-    float dl[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-    float scale = 0.0f, beta = 0.0f;
-    if (live) {
-      float ss = 0.0f, sg = 0.0f;
-      const XT* xr = x + (size_t)t * H;
-      for (int h = 8 * lane; h < H; h += 8 * kWave) {
-        float v[8];
-        load8f(xr + h, v);
-#pragma unroll
-        for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
-        if (pre_gain != nullptr) {
-          float g[8];
-          load8f(pre_gain + h, g);
-#pragma unroll
-          for (int i = 0; i < 8; ++i) sg = __builtin_fmaf(v[i] * g[i], v[i] * g[i], sg);
-        }
-      }
-      ss = wave_sum(ss);
-      float r0 = 1.0f, r;
-      if (pre_gain != nullptr) {
-        sg = wave_sum(sg);
-        r0 = 1.0f / sqrtf(ss / (float)H + eps);
-        r = 1.0f / sqrtf(r0 * r0 * sg / (float)H + eps);
-      } else {
-        r = 1.0f / sqrtf(ss / (float)H + eps);
-      }
-      float l[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int e = lane + kWave * j;
-        l[j] = e < E ? logits[(size_t)t * E + e] : 0.0f;
-        if (d_logits != nullptr && e < E) dl[j] = d_logits[(size_t)t * E + e];
-      }
-      if (d_w != nullptr) {
-        // lane k < K: slot k (an id outside [0, E) is no slot)
-        int e = -1;
-        float lk = -INFINITY, dw = 0.0f, s = 0.0f;
-        if (lane < K) {
-          e = topk_idx[(size_t)t * K + lane];
-          if ((unsigned)e < (unsigned)E) {
-            lk = logits[(size_t)t * E + e];
-            dw = d_w[(size_t)t * K + lane];
-            s = pes[e];
-          } else {
-            e = -1;
-          }
-        }
-        const float top = wave_max(lk);
-        float q = lk == -INFINITY ? 0.0f : expf(lk - top);
-        const float z = wave_sum(q);
-        q = z > 0.0f ? q / z : 0.0f;
-        const float d = dw * s;
-        const float qd = wave_sum(q * d);
-        const float dlk = q * (d - qd), dsk = dw * q;
-        for (int k = 0; k < K; ++k) {  // a repeated id adds up
-          const int ek = __builtin_amdgcn_readlane(e, k);
-          const float dk = lane_value(dlk, k), sk = lane_value(dsk, k);
-#pragma unroll
-          for (int j = 0; j < 4; ++j)
-            if (ek == lane + kWave * j) {
-              dl[j] += dk;
-              dpes[j] += sk;
-            }
-        }
-      }
-      float D = 0.0f;
-#pragma unroll
-      for (int j = 0; j < 4; ++j) D += dl[j] != 0.0f ? dl[j] * l[j] : 0.0f;
-      D = wave_sum(D);
-      scale = r0 * r;
-      beta = scale * scale * (D / (float)H);
-    }
+    float dl[4], beta;
+    router_grad_token(t, mask == nullptr || mask[t] != 0, H, E, K, eps, x, pre_gain, pes, logits,
+                      topk_idx, d_w, d_logits, dl, beta, dpes);
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       const int e = lane + kWave * j;
-      if (e < E) dl_out[(size_t)t * E + e] = dl[j] * scale;
+      if (e < E) dl_out[(size_t)t * E + e] = dl[j];
     }
     if (lane == 0) beta_out[t] = beta;
   }
-#pragma unroll
-  for (int j = 0; j < 4; ++j) sums[wave][lane + kWave * j] = dpes[j];
-  __syncthreads();
-  if ((int)threadIdx.x < E) {
-    float s = 0.0f;
-    for (int w = 0; w < kRgRowWaves; ++w) s += sums[w][threadIdx.x];
-    part_pes[(size_t)blockIdx.x * E + threadIdx.x] = s;
-  }
+  store_pes_part(sums, kRgRowWaves, E, dpes, part_pes);
 }
 
 // fp32 matrix instruction 32x32x2: lane l holds A[l % 32][l / 32] and
@@ -482,9 +506,9 @@ __device__ __forceinline__ int mfma_row(int q, int g) { return 8 * (q / 4) + 4 *
 // added through LDS.  The wave also sums x^2 beta for its columns (experts'
 // tile 0 only).
 constexpr int kRgWaves = 4;
-template <typename XT, int MT>
+template <int MT>
 __global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
-    int T, int H, int E, int span, const XT* __restrict__ x, const uint8_t* __restrict__ mask,
+    int T, int H, int E, int span, const float* __restrict__ x, const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, float* __restrict__ part_g,
     float* __restrict__ part_b) {
   __shared__ float acc_s[kRgWaves][16 * 2][kWave];
@@ -517,7 +541,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
       }
 #pragma unroll
       for (int j = 0; j < 2; ++j)
-        b[u][j] = on ? to_f32(x[(size_t)tc * H + h0 + 32 * j + c]) : 0.0f;
+        b[u][j] = on ? x[(size_t)tc * H + h0 + 32 * j + c] : 0.0f;
       be[u] = on ? beta[tc] : 0.0f;
     }
 #pragma unroll
@@ -567,11 +591,11 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
 // dx: a wave takes 64 tokens x 64 columns; the contraction runs over the
 // experts, four per lane and load (lanes 0-31 experts 8 s .. 8 s + 3, lanes
 // 32-63 the next four; W's rows in the same order).
-template <typename XT, bool VEC>
+template <bool VEC>
 __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
-    int T, int H, int E, float eps, const XT* __restrict__ x, const uint8_t* __restrict__ mask,
+    int T, int H, int E, float eps, const float* __restrict__ x, const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, const float* __restrict__ W,
-    const float* __restrict__ scale, const float* __restrict__ pre_gain, XT* __restrict__ dx) {
+    const float* __restrict__ scale, const float* __restrict__ pre_gain, float* __restrict__ dx) {
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int c = lane % 32, g = lane / 32;
   const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgWaves + wave) * 64;
@@ -624,105 +648,452 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
         if (t >= T) continue;
         const bool live = mask == nullptr || mask[t] != 0;
         const size_t at = (size_t)t * H + h;
-        const float v = live ? gc * acc[i][j][q] - to_f32(x[at]) * (beta[t] * ge) : 0.0f;
-        dx[at] = from_f32<XT>(v);
+        dx[at] = live ? gc * acc[i][j][q] - x[at] * (beta[t] * ge) : 0.0f;
       }
   }
 }
 
-// Last kernel: adds the splits of G; dW, dc and dg of 16 columns per block
-// (16 groups of experts), and in the blocks past the columns the per-expert
-// scale's gradient from the first kernel's sums.
-constexpr int kRgCols = 16, kRgParts = 16;
-__global__ __launch_bounds__(kRgCols * kRgParts) void router_grad_finish_kernel(
+// Splits of the tokens for G: one per 64 tokens, 8 at most.
+constexpr int kRgMinSpan = 64;
+
+// ---------------------------------------------------------------------------
+// bf16 inputs: both products on bf16 matrix instructions (16x16x32: lane l holds
+// row l % 16 of each operand, k = 8 (l / 16) .. + 7; register r of the result
+// is row 4 (l / 16) + r of the first operand, row l % 16 of the second).  x is
+// bf16 already; dl' and W are cut into bf16 parts, v = v0 + v1 + v2 with v0 the
+// value rounded and v1, v2 the rest rounded: three parts hold all 24 bits, two
+// hold 16.  G = dl'^T x takes the three parts (an fp32 result); dx, rounded to
+// bf16 at the end, the products v0 w0 + v0 w1 + v1 w0, which leave out 2^-16.
+// A third of the fp32 instruction's time and less (it takes 16 times as long
+// for the same product).
+//
+// The rows kernel stores dl' as two row-major parts [T, Ep] for dx and as three
+// transposed parts [Ep, Tp] for G (Ep, Tp: rounded up to 32, zeros past the
+// end); blocks past the tokens do the same for W, [H, Ep].
+// ---------------------------------------------------------------------------
+constexpr int kRgTok = 16;   // tokens per rows block, four per wave
+constexpr int kRgWCols = 32; // columns of W per block past those
+
+__device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
+  a = (bf16)v;
+  const float r = v - (float)a;
+  b = (bf16)r;
+  c = (bf16)(r - (float)b);
+}
+
+__global__ __launch_bounds__(256) void router_grad_rows_bf16_kernel(
+    int T, int H, int E, int K, float eps, const bf16* __restrict__ x,
+    const float* __restrict__ pre_gain, const float* __restrict__ pes,
+    const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
+    const uint8_t* __restrict__ mask, const float* __restrict__ d_w,
+    const float* __restrict__ d_logits, const float* __restrict__ W, int tok_blocks,
+    bf16* __restrict__ rows_out, bf16* __restrict__ cols_out, bf16* __restrict__ wt_out,
+    float* __restrict__ beta_out, float* __restrict__ part_pes) {
+  __shared__ float tile[kRgWCols][kMaxE + 1];  // W^T's columns, or kRgTok tokens' dl'
+  __shared__ float sums[4][kMaxE];
+  const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
+  const int Ep = (E + 31) / 32 * 32;
+  if ((int)blockIdx.x >= tok_blocks) {  // columns of W, transposed
+    const int h0 = ((int)blockIdx.x - tok_blocks) * kRgWCols;
+    const int c = tid % kRgWCols;
+#pragma unroll 8
+    for (int e = tid / kRgWCols; e < Ep; e += 256 / kRgWCols)
+      tile[c][e] = e < E ? W[(size_t)e * H + h0 + c] : 0.0f;
+    __syncthreads();
+    const size_t plane = (size_t)H * Ep;
+    for (int k = tid; k < kRgWCols * Ep / 8; k += 256) {
+      const int h = k / (Ep / 8), e0 = 8 * (k % (Ep / 8));
+      bf16x8 p[2];
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        bf16 a, b, c;
+        split3(tile[h][e0 + i], a, b, c);
+        p[0][i] = a;
+        p[1][i] = b;
+      }
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        *reinterpret_cast<bf16x8*>(wt_out + q * plane + (size_t)(h0 + h) * Ep + e0) = p[q];
+    }
+    return;
+  }
+  const int t0 = blockIdx.x * kRgTok;
+  float dpes[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  for (int i = 0; i < kRgTok / 4; ++i) {
+    const int tl = wave * (kRgTok / 4) + i, t = t0 + tl;
+    float dl[4], beta;
+    router_grad_token(t, t < T && (mask == nullptr || mask[t] != 0), H, E, K, eps, x, pre_gain,
+                      pes, logits, topk_idx, d_w, d_logits, dl, beta, dpes);
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+      if (lane + kWave * j < Ep) tile[tl][lane + kWave * j] = dl[j];
+    if (lane == 0 && t < T) beta_out[t] = beta;
+  }
+  store_pes_part(sums, 4, E, dpes, part_pes);  // (its barrier covers the tile)
+  const size_t rplane = (size_t)T * Ep;
+  for (int k = tid; k < kRgTok * Ep / 8; k += 256) {
+    const int tl = k / (Ep / 8), e0 = 8 * (k % (Ep / 8));
+    if (t0 + tl >= T) break;
+    bf16x8 p[2];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bf16 a, b, c;
+      split3(tile[tl][e0 + i], a, b, c);
+      p[0][i] = a;
+      p[1][i] = b;
+    }
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+      *reinterpret_cast<bf16x8*>(rows_out + q * rplane + (size_t)(t0 + tl) * Ep + e0) = p[q];
+  }
+  const int Tp = (T + 31) / 32 * 32;
+  const size_t cplane = (size_t)Ep * Tp;
+  for (int k = tid; k < Ep * (kRgTok / 8); k += 256) {
+    const int e = k / (kRgTok / 8), tl = 8 * (k % (kRgTok / 8));
+    bf16x8 p[3];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      bf16 a, b, c;
+      split3(tile[tl + i][e], a, b, c);
+      p[0][i] = a;
+      p[1][i] = b;
+      p[2][i] = c;
+    }
+#pragma unroll
+    for (int q = 0; q < 3; ++q)
+      *reinterpret_cast<bf16x8*>(cols_out + q * cplane + (size_t)e * Tp + t0 + tl) = p[q];
+  }
+}
+
+__device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
+  return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+
+// G partial: a wave takes 16 MT experts x 64 columns of x over a quarter of the
+// split's 32-token steps.  x rows are loaded as they lie, four columns of eight
+// tokens a lane, and regrouped in registers: fragment i holds columns 4 (l % 16)
+// + i, so a lane's four results of a row are consecutive columns.
+template <int MT, bool MASK>
+__global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
+    int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ mask,
+    const bf16* __restrict__ cols, const float* __restrict__ beta, bool want_beta,
+    float* __restrict__ part_g, float* __restrict__ part_b) {
+  __shared__ f32x4 acc_s[kRgWaves][4][kWave];
+  __shared__ float b_s[kRgWaves][4][64];
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int c = lane % 16, g = lane / 16;
+  const int h0 = blockIdx.x * 64, m0 = blockIdx.y * MT, split = blockIdx.z;
+  const int Ep = (E + 31) / 32 * 32, Tp = (T + 31) / 32 * 32, all = Tp / 32;
+  const size_t cplane = (size_t)Ep * Tp;
+  const int s0 = min(all, split * steps), s1 = min(all, s0 + steps);
+  const int n = s1 - s0, a0 = s0 + wave * n / kRgWaves, a1 = s0 + (wave + 1) * n / kRgWaves;
+  const bool beta_here = want_beta && blockIdx.y == 0;
+  f32x4 acc[MT][4];
+#pragma unroll
+  for (int m = 0; m < MT; ++m)
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc[m][i] = f32x4{0, 0, 0, 0};
+  float bs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+  uint2 raw[8];
+  auto load_x = [&](int s) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      const int t = min(32 * s + 8 * g + j, T - 1);
+      raw[j] = *reinterpret_cast<const uint2*>(x + (size_t)t * H + h0 + 4 * c);
+    }
+  };
+  if (a0 < a1) load_x(a0);
+  for (int s = a0; s < a1; ++s) {
+    uint2 cur[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      cur[j] = raw[j];
+      if constexpr (MASK) {  // a masked row may hold anything
+        const int t = min(32 * s + 8 * g + j, T - 1);
+        if (mask[t] == 0) cur[j] = make_uint2(0u, 0u);
+      }
+    }
+    if (s + 1 < a1) load_x(s + 1);
+    if (beta_here) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int t = 32 * s + 8 * g + j;
+        const float be = t < T ? beta[t] : 0.0f;
+        const float v[4] = {__uint_as_float(cur[j].x << 16),
+                            __uint_as_float(cur[j].x & 0xffff0000u),
+                            __uint_as_float(cur[j].y << 16),
+                            __uint_as_float(cur[j].y & 0xffff0000u)};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) bs[i] = __builtin_fmaf(v[i] * v[i], be, bs[i]);
+      }
+    }
+    // columns 4 c + i of the eight tokens: halves of eight words
+    bf16x8 fb[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      uint4 w;
+      uint32_t* wp = &w.x;
+#pragma unroll
+      for (int p = 0; p < 4; ++p) {
+        const uint32_t lo = i < 2 ? cur[2 * p].x : cur[2 * p].y;
+        const uint32_t hi = i < 2 ? cur[2 * p + 1].x : cur[2 * p + 1].y;
+        wp[p] = i % 2 == 0 ? __builtin_amdgcn_perm(hi, lo, 0x05040100u)
+                           : __builtin_amdgcn_perm(hi, lo, 0x07060302u);
+      }
+      fb[i] = __builtin_bit_cast(bf16x8, w);
+    }
+#pragma unroll
+    for (int m = 0; m < MT; ++m) {
+      const int e = min(16 * (m0 + m) + c, Ep - 1);
+      const bf16* p = cols + (size_t)e * Tp + 32 * s + 8 * g;
+      bf16x8 fa[3];
+#pragma unroll
+      for (int q = 0; q < 3; ++q) fa[q] = *reinterpret_cast<const bf16x8*>(p + q * cplane);
+#pragma unroll
+      for (int q = 0; q < 3; ++q)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(fa[q], fb[i], acc[m][i]);
+    }
+  }
+  if (beta_here) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) b_s[wave][g][4 * c + i] = bs[i];
+  }
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    __syncthreads();
+#pragma unroll
+    for (int i = 0; i < 4; ++i) acc_s[wave][i][lane] = acc[m][i];
+    __syncthreads();
+    // wave w adds result register w of every lane: row 4 g + w, columns 4 c .. + 3
+    f32x4 v;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[i] = 0.0f;
+#pragma unroll
+      for (int u = 0; u < kRgWaves; ++u) v[i] += acc_s[u][i][lane][wave];
+    }
+    const int e = 16 * (m0 + m) + 4 * g + wave;
+    if (e < E)
+      *reinterpret_cast<f32x4*>(part_g + ((size_t)split * E + e) * H + h0 + 4 * c) = v;
+  }
+  if (beta_here && threadIdx.x < 64) {
+    float v = 0.0f;
+    for (int w = 0; w < kRgWaves; ++w)
+      for (int i = 0; i < 4; ++i) v += b_s[w][i][threadIdx.x];
+    part_b[(size_t)split * H + h0 + threadIdx.x] = v;
+  }
+}
+
+// dx: a wave takes 64 tokens x 64 columns.  W^T is the first operand, its tile
+// j's row m being column 16 (m / 4) + 4 j + m % 4, so that a lane's 16 results of
+// a token are consecutive columns: 32-byte loads of x and stores of dx, four
+// lanes to a 128-byte line.
+__global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
+    int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ mask,
+    const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
+    const float* __restrict__ scale, const float* __restrict__ pre_gain, bf16* __restrict__ dx) {
+  const int wave = threadIdx.x / kWave, lane = lane_id();
+  const int c = lane % 16, g = lane / 16;
+  const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgWaves + wave) * 64;
+  if (t0 >= T) return;  // no barrier below
+  const int Ep = (E + 31) / 32 * 32;
+  const size_t rplane = (size_t)T * Ep, wplane = (size_t)H * Ep;
+  f32x4 acc[4][4];  // token tile, column tile
+#pragma unroll
+  for (int i = 0; i < 4; ++i)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
+  const bf16* wr[4];
+  const bf16* tr[4];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    wr[j] = wt + (size_t)(h0 + 16 * (c / 4) + 4 * j + c % 4) * Ep + 8 * g;
+    tr[j] = rows + (size_t)min(t0 + 16 * j + c, T - 1) * Ep + 8 * g;
+  }
+  for (int k = 0; k < Ep; k += 32) {
+    bf16x8 fw[2][4], ft[2][4];
+#pragma unroll
+    for (int q = 0; q < 2; ++q)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        fw[q][j] = *reinterpret_cast<const bf16x8*>(wr[j] + q * wplane + k);
+        ft[q][j] = *reinterpret_cast<const bf16x8*>(tr[j] + q * rplane + k);
+      }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        acc[i][j] = mfma_bf16(fw[0][j], ft[1][i], acc[i][j]);
+        acc[i][j] = mfma_bf16(fw[1][j], ft[0][i], acc[i][j]);
+        acc[i][j] = mfma_bf16(fw[0][j], ft[0][i], acc[i][j]);
+      }
+  }
+  // columns h0 + 16 g .. + 15
+  const int h = h0 + 16 * g;
+  float gc[16], ge[16];
+#pragma unroll
+  for (int j = 0; j < 16; j += 8) {
+    float sc[8], gn[8];
+    load8f(scale + h + j, sc);
+    if (pre_gain != nullptr) load8f(pre_gain + h + j, gn);
+#pragma unroll
+    for (int u = 0; u < 8; ++u) {
+      gc[j + u] = pre_gain != nullptr ? gn[u] * sc[u] : sc[u];
+      ge[j + u] = pre_gain != nullptr ? gn[u] * gn[u] + eps : 1.0f;
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int t = t0 + 16 * i + c;
+    if (t >= T) continue;
+    const bool live = mask == nullptr || mask[t] != 0;
+    const float be = beta[t];
+    const bf16* xr = x + (size_t)t * H + h;
+    bf16* dr = dx + (size_t)t * H + h;
+#pragma unroll
+    for (int j = 0; j < 16; j += 8) {
+      float xv[8];
+      load8f(xr + j, xv);
+      bf16x8 o;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float v = gc[j + u] * acc[i][(j + u) / 4][u % 4] - xv[u] * (be * ge[j + u]);
+        o[u] = (bf16)(live ? v : 0.0f);
+      }
+      *reinterpret_cast<bf16x8*>(dr + j) = o;
+    }
+  }
+}
+
+// Last kernel: adds the splits of G; dW, dc and dg of 32 columns per block, four
+// columns a thread and 32 groups of experts; in the blocks past the columns the
+// per-expert scale's gradient from the first kernel's sums.
+constexpr int kRgCols = 32, kRgParts = 32, kRgFinThreads = kRgCols / 4 * kRgParts;
+constexpr int kRgMaxSplits = 8;
+__global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
     int H, int E, int splits, int pes_blocks, const float* __restrict__ part_g,
     const float* __restrict__ part_b, const float* __restrict__ part_pes,
     const float* __restrict__ W, const float* __restrict__ scale,
     const float* __restrict__ pre_gain, float* __restrict__ dW, float* __restrict__ d_scale,
     float* __restrict__ d_pes, float* __restrict__ d_gain) {
-  __shared__ float red[kRgParts][kRgCols];
-  const int c = threadIdx.x % kRgCols, p = threadIdx.x / kRgCols;
+  __shared__ f32x4 red[kRgParts][kRgCols / 4];
+  const int c = threadIdx.x % (kRgCols / 4), p = threadIdx.x / (kRgCols / 4);
   const int col_blocks = H / kRgCols;
   if ((int)blockIdx.x >= col_blocks) {
-    const int e = ((int)blockIdx.x - col_blocks) * kRgCols + c;
+    // eight experts a block, a lane group each
+    const int e = ((int)blockIdx.x - col_blocks) * (kRgCols / 4) + c;
     float s = 0.0f;
-    if (e < E)
+    if (e < E) {
+#pragma unroll 8
       for (int i = p; i < pes_blocks; i += kRgParts) s += part_pes[(size_t)i * E + e];
-    red[p][c] = s;
+    }
+    red[p][c][0] = s;
     __syncthreads();
     if (p == 0 && e < E) {
       s = 0.0f;
-      for (int i = 0; i < kRgParts; ++i) s += red[i][c];
+      for (int i = 0; i < kRgParts; ++i) s += red[i][c][0];
       d_pes[e] = s;
     }
     return;
   }
-  const int h = blockIdx.x * kRgCols + c;
-  const float gn = pre_gain != nullptr ? pre_gain[h] : 1.0f, cs = scale[h];
-  float m = 0.0f;
+  const int h = blockIdx.x * kRgCols + 4 * c;
+  const f32x4 one = {1.0f, 1.0f, 1.0f, 1.0f};
+  const f32x4 gn = pre_gain != nullptr ? *reinterpret_cast<const f32x4*>(pre_gain + h) : one;
+  const f32x4 cs = *reinterpret_cast<const f32x4*>(scale + h);
+  f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll 2
   for (int e = p; e < E; e += kRgParts) {
-    float v = 0.0f;
-    for (int s = 0; s < splits; ++s) v += part_g[((size_t)s * E + e) * H + h];
-    dW[(size_t)e * H + h] = v * gn * cs;
-    m = __builtin_fmaf(W[(size_t)e * H + h], v, m);
+    f32x4 v[kRgMaxSplits];
+#pragma unroll
+    for (int s = 0; s < kRgMaxSplits; ++s)
+      v[s] = s < splits ? *reinterpret_cast<const f32x4*>(part_g + ((size_t)s * E + e) * H + h)
+                        : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+    f32x4 sum = v[0];
+#pragma unroll
+    for (int s = 1; s < kRgMaxSplits; ++s) sum += v[s];
+    *reinterpret_cast<f32x4*>(dW + (size_t)e * H + h) = sum * gn * cs;
+    m += *reinterpret_cast<const f32x4*>(W + (size_t)e * H + h) * sum;
   }
   red[p][c] = m;
   __syncthreads();
   if (p != 0) return;
-  m = 0.0f;
-  for (int i = 0; i < kRgParts; ++i) m += red[i][c];
-  d_scale[h] = gn * m;
+  m = red[0][c];
+  for (int i = 1; i < kRgParts; ++i) m += red[i][c];
+  *reinterpret_cast<f32x4*>(d_scale + h) = gn * m;
   if (d_gain != nullptr) {
-    float bsum = 0.0f;
-    for (int s = 0; s < splits; ++s) bsum += part_b[(size_t)s * H + h];
-    d_gain[h] = cs * m - gn * bsum;
+    f32x4 bsum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s = 0; s < splits; ++s)
+      bsum += *reinterpret_cast<const f32x4*>(part_b + (size_t)s * H + h);
+    *reinterpret_cast<f32x4*>(d_gain + h) = cs * m - gn * bsum;
   }
 }
 
-// Splits of the tokens for G.
-constexpr int kRgMinSpan = 64;
-
-template <typename XT>
-hipError_t launch_router_grad_t(const RouterGradArgs& a, hipStream_t s) {
-  const XT* x = static_cast<const XT*>(a.x);
+// fp32 inputs.
+void launch_grad_f32(const RouterGradArgs& a, hipStream_t s) {
+  const float* x = static_cast<const float*>(a.x);
+  float* dl = static_cast<float*>(a.ws_dl);
   const int splits = router_grad_splits(a.T);
-  const int rb = router_grad_row_blocks(a.T);
-  if (a.T > 0) {
-    hipLaunchKernelGGL(router_grad_rows_kernel<XT>, dim3(rb), dim3(64 * kRgRowWaves), 0, s, a.T,
-                       a.H, a.E, a.K, a.eps, x, a.pre_gain, a.per_expert_scale, a.logits,
-                       a.topk_idx, a.mask, a.d_topk_w, a.d_logits, a.ws_dl, a.ws_beta,
-                       a.ws_part_pes);
-    const int span = (a.T + splits - 1) / splits;
-    auto gw = [&](auto mt) {
-      constexpr int MT = decltype(mt)::value;
-      hipLaunchKernelGGL((router_grad_w_kernel<XT, MT>),
-                         dim3(a.H / 64, (a.E + 32 * MT - 1) / (32 * MT), splits),
-                         dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, span, x, a.mask, a.ws_dl,
-                         a.ws_beta, a.ws_part_g, a.ws_part_b);
-    };
-    if (a.E <= 32) gw(std::integral_constant<int, 1>{});
-    else if (a.E <= 64) gw(std::integral_constant<int, 2>{});
-    else gw(std::integral_constant<int, 4>{});
-    if (a.d_x != nullptr) {
-      const dim3 grid(a.H / 64, (a.T + 64 * kRgWaves - 1) / (64 * kRgWaves));
-      XT* dx = static_cast<XT*>(a.d_x);
-      if (a.E % 4 == 0)
-        hipLaunchKernelGGL((router_grad_x_kernel<XT, true>), grid, dim3(64 * kRgWaves), 0, s, a.T,
-                           a.H, a.E, a.eps, x, a.mask, a.ws_dl, a.ws_beta, a.router_w,
-                           a.router_scale, a.pre_gain, dx);
-      else
-        hipLaunchKernelGGL((router_grad_x_kernel<XT, false>), grid, dim3(64 * kRgWaves), 0, s,
-                           a.T, a.H, a.E, a.eps, x, a.mask, a.ws_dl, a.ws_beta, a.router_w,
-                           a.router_scale, a.pre_gain, dx);
-    }
-  }
-  hipLaunchKernelGGL(router_grad_finish_kernel,
-                     dim3(a.H / kRgCols + (a.E + kRgCols - 1) / kRgCols),
-                     dim3(kRgCols * kRgParts), 0, s, a.H, a.E, a.T > 0 ? splits : 0,
-                     a.T > 0 ? rb : 0, a.ws_part_g, a.ws_part_b, a.ws_part_pes, a.router_w,
-                     a.router_scale, a.pre_gain, a.d_router_w, a.d_router_scale,
-                     a.d_per_expert_scale, a.d_pre_gain);
-  return hipGetLastError();
+  hipLaunchKernelGGL(router_grad_rows_kernel, dim3(router_grad_row_blocks(a.T)),
+                     dim3(64 * kRgRowWaves), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
+                     a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits, dl,
+                     a.ws_beta, a.ws_part_pes);
+  const int span = (a.T + splits - 1) / splits;
+  auto gw = [&](auto mt) {
+    constexpr int MT = decltype(mt)::value;
+    hipLaunchKernelGGL((router_grad_w_kernel<MT>),
+                       dim3(a.H / 64, (a.E + 32 * MT - 1) / (32 * MT), splits),
+                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, span, x, a.mask, dl, a.ws_beta,
+                       a.ws_part_g, a.ws_part_b);
+  };
+  if (a.E <= 32) gw(std::integral_constant<int, 1>{});
+  else if (a.E <= 64) gw(std::integral_constant<int, 2>{});
+  else gw(std::integral_constant<int, 4>{});
+  if (a.d_x == nullptr) return;
+  const dim3 grid(a.H / 64, (a.T + 64 * kRgWaves - 1) / (64 * kRgWaves));
+  float* dx = static_cast<float*>(a.d_x);
+  if (a.E % 4 == 0)
+    hipLaunchKernelGGL((router_grad_x_kernel<true>), grid, dim3(64 * kRgWaves), 0, s, a.T, a.H,
+                       a.E, a.eps, x, a.mask, dl, a.ws_beta, a.router_w, a.router_scale,
+                       a.pre_gain, dx);
+  else
+    hipLaunchKernelGGL((router_grad_x_kernel<false>), grid, dim3(64 * kRgWaves), 0, s, a.T, a.H,
+                       a.E, a.eps, x, a.mask, dl, a.ws_beta, a.router_w, a.router_scale,
+                       a.pre_gain, dx);
+}
+
+// bf16 inputs.
+void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
+  const bf16* x = static_cast<const bf16*>(a.x);
+  const long long Ep = (a.E + 31) / 32 * 32, Tp = (a.T + 31) / 32 * 32;
+  bf16* rows = static_cast<bf16*>(a.ws_dl);
+  bf16* cols = rows + 2 * a.T * Ep;
+  bf16* wt = cols + 3 * Ep * Tp;
+  const int splits = router_grad_splits(a.T), tb = router_grad_row_blocks(a.T);
+  hipLaunchKernelGGL(router_grad_rows_bf16_kernel, dim3(tb + (a.d_x != nullptr ? a.H / kRgWCols : 0)),
+                     dim3(256), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
+                     a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits,
+                     a.router_w, tb, rows, cols, wt, a.ws_beta, a.ws_part_pes);
+  const int steps = ((int)(Tp / 32) + splits - 1) / splits;
+  auto gw = [&](auto mt, auto masked) {
+    constexpr int MT = decltype(mt)::value;
+    hipLaunchKernelGGL((router_grad_w_bf16_kernel<MT, decltype(masked)::value>),
+                       dim3(a.H / 64, (a.E + 16 * MT - 1) / (16 * MT), splits),
+                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, steps, x, a.mask, cols,
+                       a.ws_beta, a.pre_gain != nullptr, a.ws_part_g, a.ws_part_b);
+  };
+  auto by_mask = [&](auto mt) {
+    if (a.mask != nullptr) gw(mt, std::true_type{});
+    else gw(mt, std::false_type{});
+  };
+  if (a.E <= 32) by_mask(std::integral_constant<int, 2>{});
+  else if (a.E <= 64) by_mask(std::integral_constant<int, 4>{});
+  else by_mask(std::integral_constant<int, 8>{});
+  if (a.d_x != nullptr)
+    hipLaunchKernelGGL(router_grad_x_bf16_kernel,
+                       dim3(a.H / 64, (a.T + 64 * kRgWaves - 1) / (64 * kRgWaves)),
+                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, a.eps, x, a.mask, rows,
+                       a.ws_beta, wt, a.router_scale, a.pre_gain, static_cast<bf16*>(a.d_x));
 }
 
 }  // namespace
@@ -761,16 +1132,28 @@ hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
 
 int router_grad_splits(int T) {
   const int n = (T + kRgMinSpan - 1) / kRgMinSpan;
-  return n < 1 ? 1 : n < 8 ? n : 8;
+  return n < 1 ? 1 : n < kRgMaxSplits ? n : kRgMaxSplits;
 }
 
-int router_grad_row_blocks(int T) {
-  const int n = (T + kRgRowWaves - 1) / kRgRowWaves;
-  return n < 512 ? n : 512;
+int router_grad_row_blocks(int T) { return (T + 31) / 32 * 32 / kRgTok; }
+
+size_t router_grad_dl_bytes(int T, int H, int E) {
+  const size_t Ep = (E + 31) / 32 * 32, Tp = (T + 31) / 32 * 32;
+  return 2 * (2 * T * Ep + 3 * Ep * Tp + 2 * H * Ep);  // more than the 4 T E of fp32
 }
 
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
-  return a.x_bf16 ? launch_router_grad_t<bf16>(a, s) : launch_router_grad_t<float>(a, s);
+  if (a.T > 0) {
+    if (a.x_bf16) launch_grad_bf16(a, s);
+    else launch_grad_f32(a, s);
+  }
+  constexpr int per = kRgCols / 4;
+  hipLaunchKernelGGL(router_grad_finish_kernel, dim3(a.H / kRgCols + (a.E + per - 1) / per),
+                     dim3(kRgFinThreads), 0, s, a.H, a.E, a.T > 0 ? router_grad_splits(a.T) : 0,
+                     a.T > 0 ? router_grad_row_blocks(a.T) : 0, a.ws_part_g, a.ws_part_b,
+                     a.ws_part_pes, a.router_w, a.router_scale, a.pre_gain, a.d_router_w,
+                     a.d_router_scale, a.d_per_expert_scale, a.d_pre_gain);
+  return hipGetLastError();
 }
 
 }  // namespace moe
