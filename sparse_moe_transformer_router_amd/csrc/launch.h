@@ -86,7 +86,7 @@ struct RouterGradArgs {
   float* d_per_expert_scale;      // [E]
   float* d_pre_gain;              // [H] or nullptr
   void* ws_dl;                    // router_grad_dl_bytes
-  float* ws_beta;                 // [T]
+  float* ws_beta;                 // [T rounded up to 32]
   float* ws_part_g;               // [splits,E,H]
   float* ws_part_b;               // [splits,H]
   float* ws_part_pes;             // [row blocks,E]

@@ -148,7 +148,7 @@ Layout layout(const moe_dims* d, long long T) {
   const size_t splits = (size_t)moe::router_grad_splits((int)T);
   o = L.base_end;
   L.rg_dl = take(moe::router_grad_dl_bytes((int)T, d->hidden, d->num_experts));
-  L.rg_beta = take(4 * (size_t)T);
+  L.rg_beta = take(4 * (((size_t)T + 31) / 32 * 32));
   L.rg_g = take(4 * splits * E * H);
   L.rg_b = take(4 * splits * H);
   L.rg_pes = take(4 * (size_t)moe::router_grad_row_blocks((int)T) * E);

@@ -671,7 +671,8 @@ constexpr int kRgMinSpan = 64;
 // transposed parts [Ep, Tp] for G (Ep, Tp: rounded up to 32, zeros past the
 // end); blocks past the tokens do the same for W, [H, Ep].
 // ---------------------------------------------------------------------------
-constexpr int kRgTok = 16;   // tokens per rows block, four per wave
+constexpr int kRgTok = 16;   // tokens per rows block, one per wave
+constexpr int kRgRowThreads = kRgTok * kWave;
 constexpr int kRgWCols = 32; // columns of W per block past those
 
 __device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
@@ -681,27 +682,27 @@ __device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
   c = (bf16)(r - (float)b);
 }
 
-__global__ __launch_bounds__(256) void router_grad_rows_bf16_kernel(
+__global__ __launch_bounds__(kRgRowThreads) void router_grad_rows_bf16_kernel(
     int T, int H, int E, int K, float eps, const bf16* __restrict__ x,
     const float* __restrict__ pre_gain, const float* __restrict__ pes,
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
     const uint8_t* __restrict__ mask, const float* __restrict__ d_w,
     const float* __restrict__ d_logits, const float* __restrict__ W, int tok_blocks,
     bf16* __restrict__ rows_out, bf16* __restrict__ cols_out, bf16* __restrict__ wt_out,
-    float* __restrict__ beta_out, float* __restrict__ part_pes) {
+    float* __restrict__ beta_out, uint8_t* __restrict__ live_out, float* __restrict__ part_pes) {
   __shared__ float tile[kRgWCols][kMaxE + 1];  // W^T's columns, or kRgTok tokens' dl'
-  __shared__ float sums[4][kMaxE];
+  __shared__ float sums[kRgTok][kMaxE];
   const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
   const int Ep = (E + 31) / 32 * 32;
   if ((int)blockIdx.x >= tok_blocks) {  // columns of W, transposed
     const int h0 = ((int)blockIdx.x - tok_blocks) * kRgWCols;
     const int c = tid % kRgWCols;
 #pragma unroll 8
-    for (int e = tid / kRgWCols; e < Ep; e += 256 / kRgWCols)
+    for (int e = tid / kRgWCols; e < Ep; e += kRgRowThreads / kRgWCols)
       tile[c][e] = e < E ? W[(size_t)e * H + h0 + c] : 0.0f;
     __syncthreads();
     const size_t plane = (size_t)H * Ep;
-    for (int k = tid; k < kRgWCols * Ep / 8; k += 256) {
+    for (int k = tid; k < kRgWCols * Ep / 8; k += kRgRowThreads) {
       const int h = k / (Ep / 8), e0 = 8 * (k % (Ep / 8));
       bf16x8 p[2];
 #pragma unroll
@@ -719,19 +720,23 @@ __global__ __launch_bounds__(256) void router_grad_rows_bf16_kernel(
   }
   const int t0 = blockIdx.x * kRgTok;
   float dpes[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  for (int i = 0; i < kRgTok / 4; ++i) {
-    const int tl = wave * (kRgTok / 4) + i, t = t0 + tl;
+  {
+    const int t = t0 + wave;
+    const bool live = t < T && (mask == nullptr || mask[t] != 0);
     float dl[4], beta;
-    router_grad_token(t, t < T && (mask == nullptr || mask[t] != 0), H, E, K, eps, x, pre_gain,
-                      pes, logits, topk_idx, d_w, d_logits, dl, beta, dpes);
+    router_grad_token(t, live, H, E, K, eps, x, pre_gain, pes, logits, topk_idx, d_w, d_logits,
+                      dl, beta, dpes);
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      if (lane + kWave * j < Ep) tile[tl][lane + kWave * j] = dl[j];
-    if (lane == 0 && t < T) beta_out[t] = beta;
+      if (lane + kWave * j < Ep) tile[wave][lane + kWave * j] = dl[j];
+    if (lane == 0) {  // [Tp]: zeros past the last token
+      beta_out[t] = beta;
+      live_out[t] = live ? 1 : 0;
+    }
   }
-  store_pes_part(sums, 4, E, dpes, part_pes);  // (its barrier covers the tile)
+  store_pes_part(sums, kRgTok, E, dpes, part_pes);  // (its barrier covers the tile)
   const size_t rplane = (size_t)T * Ep;
-  for (int k = tid; k < kRgTok * Ep / 8; k += 256) {
+  for (int k = tid; k < kRgTok * Ep / 8; k += kRgRowThreads) {
     const int tl = k / (Ep / 8), e0 = 8 * (k % (Ep / 8));
     if (t0 + tl >= T) break;
     bf16x8 p[2];
@@ -748,7 +753,7 @@ __global__ __launch_bounds__(256) void router_grad_rows_bf16_kernel(
   }
   const int Tp = (T + 31) / 32 * 32;
   const size_t cplane = (size_t)Ep * Tp;
-  for (int k = tid; k < Ep * (kRgTok / 8); k += 256) {
+  for (int k = tid; k < Ep * (kRgTok / 8); k += kRgRowThreads) {
     const int e = k / (kRgTok / 8), tl = 8 * (k % (kRgTok / 8));
     bf16x8 p[3];
 #pragma unroll
@@ -775,7 +780,7 @@ __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
 // + i, so a lane's four results of a row are consecutive columns.
 template <int MT, bool MASK>
 __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
-    int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ mask,
+    int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
     const bf16* __restrict__ cols, const float* __restrict__ beta, bool want_beta,
     float* __restrict__ part_g, float* __restrict__ part_b) {
   __shared__ f32x4 acc_s[kRgWaves][4][kWave];
@@ -794,31 +799,50 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
 #pragma unroll
     for (int i = 0; i < 4; ++i) acc[m][i] = f32x4{0, 0, 0, 0};
   float bs[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  uint2 raw[8];
+  uint2 raw[8], on = {0u, 0u};
+  float4 be4[2] = {};
+  // (steps past the wave's last load that one again)
   auto load_x = [&](int s) {
+    if constexpr (MASK) on = *reinterpret_cast<const uint2*>(live + 32 * s + 8 * g);
+    if (beta_here) {
+      be4[0] = *reinterpret_cast<const float4*>(beta + 32 * s + 8 * g);
+      be4[1] = *reinterpret_cast<const float4*>(beta + 32 * s + 8 * g + 4);
+    }
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       const int t = min(32 * s + 8 * g + j, T - 1);
       raw[j] = *reinterpret_cast<const uint2*>(x + (size_t)t * H + h0 + 4 * c);
     }
   };
-  if (a0 < a1) load_x(a0);
+  bf16x8 fa[2][3];
+  auto load_a = [&](int s, int m, bf16x8 (&f)[3]) {
+    const int e = min(16 * (m0 + m) + c, Ep - 1);
+    const bf16* p = cols + (size_t)e * Tp + 32 * s + 8 * g;
+#pragma unroll
+    for (int q = 0; q < 3; ++q) f[q] = *reinterpret_cast<const bf16x8*>(p + q * cplane);
+  };
+  if (a0 < a1) {
+    load_x(a0);
+    load_a(a0, 0, fa[0]);
+  }
   for (int s = a0; s < a1; ++s) {
+    const int next = min(s + 1, a1 - 1);
     uint2 cur[8];
 #pragma unroll
     for (int j = 0; j < 8; ++j) {
       cur[j] = raw[j];
       if constexpr (MASK) {  // a masked row may hold anything
-        const int t = min(32 * s + 8 * g + j, T - 1);
-        if (mask[t] == 0) cur[j] = make_uint2(0u, 0u);
+        const uint32_t w = j < 4 ? on.x : on.y;
+        if (((w >> (8 * (j % 4))) & 255u) == 0) cur[j] = make_uint2(0u, 0u);
       }
     }
-    if (s + 1 < a1) load_x(s + 1);
+    const float4 b0 = be4[0], b1 = be4[1];
+    load_x(next);
     if (beta_here) {
+      const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
       for (int j = 0; j < 8; ++j) {
-        const int t = 32 * s + 8 * g + j;
-        const float be = t < T ? beta[t] : 0.0f;
+        const float be = bb[j];
         const float v[4] = {__uint_as_float(cur[j].x << 16),
                             __uint_as_float(cur[j].x & 0xffff0000u),
                             __uint_as_float(cur[j].y << 16),
@@ -844,15 +868,16 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      const int e = min(16 * (m0 + m) + c, Ep - 1);
-      const bf16* p = cols + (size_t)e * Tp + 32 * s + 8 * g;
-      bf16x8 fa[3];
-#pragma unroll
-      for (int q = 0; q < 3; ++q) fa[q] = *reinterpret_cast<const bf16x8*>(p + q * cplane);
+      // the next tile's parts are on their way during this one's products
+      if (m + 1 < MT) load_a(s, m + 1, fa[(m + 1) & 1]);
+      else load_a(next, 0, fa[0]);
+      static_assert(MT % 2 == 0, "a step's first tile is in fa[0]");
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(fa[q], fb[i], acc[m][i]);
+        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(fa[m & 1][q], fb[i], acc[m][i]);
+      __builtin_amdgcn_sched_barrier(0);
     }
   }
   if (beta_here) {
@@ -886,9 +911,9 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
 }
 
 // dx: a wave takes 64 tokens x 64 columns.  W^T is the first operand, its tile
-// j's row m being column 16 (m / 4) + 4 j + m % 4, so that a lane's 16 results of
-// a token are consecutive columns: 32-byte loads of x and stores of dx, four
-// lanes to a 128-byte line.
+// j's row m being column 32 (j / 2) + 8 (m / 4) + 4 (j % 2) + m % 4, so that a
+// lane's results of two tiles are eight consecutive columns of a token: 16-byte
+// loads of x and stores of dx, four lanes to 64 bytes.
 __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
     int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ mask,
     const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
@@ -908,7 +933,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
   const bf16* tr[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    wr[j] = wt + (size_t)(h0 + 16 * (c / 4) + 4 * j + c % 4) * Ep + 8 * g;
+    wr[j] = wt + (size_t)(h0 + 32 * (j / 2) + 8 * (c / 4) + 4 * (j % 2) + c % 4) * Ep + 8 * g;
     tr[j] = rows + (size_t)min(t0 + 16 * j + c, T - 1) * Ep + 8 * g;
   }
   for (int k = 0; k < Ep; k += 32) {
@@ -929,18 +954,17 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
         acc[i][j] = mfma_bf16(fw[0][j], ft[0][i], acc[i][j]);
       }
   }
-  // columns h0 + 16 g .. + 15
-  const int h = h0 + 16 * g;
-  float gc[16], ge[16];
+  // pair p of tiles: columns h0 + 32 p + 8 g .. + 7
+  float gc[2][8], ge[2][8];
 #pragma unroll
-  for (int j = 0; j < 16; j += 8) {
+  for (int p = 0; p < 2; ++p) {
     float sc[8], gn[8];
-    load8f(scale + h + j, sc);
-    if (pre_gain != nullptr) load8f(pre_gain + h + j, gn);
+    load8f(scale + h0 + 32 * p + 8 * g, sc);
+    if (pre_gain != nullptr) load8f(pre_gain + h0 + 32 * p + 8 * g, gn);
 #pragma unroll
     for (int u = 0; u < 8; ++u) {
-      gc[j + u] = pre_gain != nullptr ? gn[u] * sc[u] : sc[u];
-      ge[j + u] = pre_gain != nullptr ? gn[u] * gn[u] + eps : 1.0f;
+      gc[p][u] = pre_gain != nullptr ? gn[u] * sc[u] : sc[u];
+      ge[p][u] = pre_gain != nullptr ? gn[u] * gn[u] + eps : 1.0f;
     }
   }
 #pragma unroll
@@ -949,19 +973,18 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
     if (t >= T) continue;
     const bool live = mask == nullptr || mask[t] != 0;
     const float be = beta[t];
-    const bf16* xr = x + (size_t)t * H + h;
-    bf16* dr = dx + (size_t)t * H + h;
 #pragma unroll
-    for (int j = 0; j < 16; j += 8) {
+    for (int p = 0; p < 2; ++p) {
+      const size_t at = (size_t)t * H + h0 + 32 * p + 8 * g;
       float xv[8];
-      load8f(xr + j, xv);
+      load8f(x + at, xv);
       bf16x8 o;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float v = gc[j + u] * acc[i][(j + u) / 4][u % 4] - xv[u] * (be * ge[j + u]);
+        const float v = gc[p][u] * acc[i][2 * p + u / 4][u % 4] - xv[u] * (be * ge[p][u]);
         o[u] = (bf16)(live ? v : 0.0f);
       }
-      *reinterpret_cast<bf16x8*>(dr + j) = o;
+      *reinterpret_cast<bf16x8*>(dx + at) = o;
     }
   }
 }
@@ -1069,17 +1092,18 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   bf16* rows = static_cast<bf16*>(a.ws_dl);
   bf16* cols = rows + 2 * a.T * Ep;
   bf16* wt = cols + 3 * Ep * Tp;
+  uint8_t* live = reinterpret_cast<uint8_t*>(wt + 2 * a.H * Ep);
   const int splits = router_grad_splits(a.T), tb = router_grad_row_blocks(a.T);
   hipLaunchKernelGGL(router_grad_rows_bf16_kernel, dim3(tb + (a.d_x != nullptr ? a.H / kRgWCols : 0)),
-                     dim3(256), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
+                     dim3(kRgRowThreads), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
                      a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits,
-                     a.router_w, tb, rows, cols, wt, a.ws_beta, a.ws_part_pes);
+                     a.router_w, tb, rows, cols, wt, a.ws_beta, live, a.ws_part_pes);
   const int steps = ((int)(Tp / 32) + splits - 1) / splits;
   auto gw = [&](auto mt, auto masked) {
     constexpr int MT = decltype(mt)::value;
     hipLaunchKernelGGL((router_grad_w_bf16_kernel<MT, decltype(masked)::value>),
                        dim3(a.H / 64, (a.E + 16 * MT - 1) / (16 * MT), splits),
-                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, steps, x, a.mask, cols,
+                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, steps, x, live, cols,
                        a.ws_beta, a.pre_gain != nullptr, a.ws_part_g, a.ws_part_b);
   };
   auto by_mask = [&](auto mt) {
@@ -1139,7 +1163,7 @@ int router_grad_row_blocks(int T) { return (T + 31) / 32 * 32 / kRgTok; }
 
 size_t router_grad_dl_bytes(int T, int H, int E) {
   const size_t Ep = (E + 31) / 32 * 32, Tp = (T + 31) / 32 * 32;
-  return 2 * (2 * T * Ep + 3 * Ep * Tp + 2 * H * Ep);  // more than the 4 T E of fp32
+  return 2 * (2 * T * Ep + 3 * Ep * Tp + 2 * H * Ep) + Tp;  // more than the 4 T E of fp32
 }
 
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
