@@ -667,13 +667,27 @@ constexpr int kRgMinSpan = 64;
 // A third of the fp32 instruction's time and less (it takes 16 times as long
 // for the same product).
 //
-// The rows kernel stores dl' as two row-major parts [T, Ep] for dx and as three
-// transposed parts [Ep, Tp] for G (Ep, Tp: rounded up to 32, zeros past the
-// end); blocks past the tokens do the same for W, [H, Ep].
+// The rows kernel stores every operand in the order in which a wave loads it, a
+// fragment of 64 lanes x 16 bytes at a time (row-major parts, whose loads touch
+// 64 bytes of 16 rows, took the products 28 of 42 us at 4096 tokens).  Ep and Tp:
+// experts and tokens rounded up to 32, zeros past the end.
+//   dl' for dx  [Tp / 16][Ep / 32][2 parts][lane]   token 16 i + l % 16, experts
+//                                                   32 k + 8 (l / 16) .. + 7
+//   dl' for G   [Tp / 32][Ep / 16][3 parts][lane]   expert 16 m + l % 16, tokens
+//                                                   32 s + 8 (l / 16) .. + 7
+//   W for dx    [H / 16][Ep / 32][2 parts][lane]    column wt_col(l % 16) of the
+//                                                   tile, experts as in dl'
 // ---------------------------------------------------------------------------
 constexpr int kRgTok = 16;   // tokens per rows block, one per wave
 constexpr int kRgRowThreads = kRgTok * kWave;
 constexpr int kRgWCols = 32; // columns of W per block past those
+
+constexpr int kFrag = kWave * 8;  // values of a fragment
+
+// Column of row m of the 16-column tile i of W^T, counted from the first of the
+// 32 columns of tiles i and i + 1 (i even): a lane's results of the two tiles
+// (rows 4 g .. 4 g + 3 of each) are then eight consecutive columns.
+__device__ __forceinline__ int wt_col(int i, int m) { return 8 * (m / 4) + 4 * (i % 2) + m % 4; }
 
 __device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
   a = (bf16)v;
@@ -701,20 +715,22 @@ __global__ __launch_bounds__(kRgRowThreads) void router_grad_rows_bf16_kernel(
     for (int e = tid / kRgWCols; e < Ep; e += kRgRowThreads / kRgWCols)
       tile[c][e] = e < E ? W[(size_t)e * H + h0 + c] : 0.0f;
     __syncthreads();
-    const size_t plane = (size_t)H * Ep;
-    for (int k = tid; k < kRgWCols * Ep / 8; k += kRgRowThreads) {
-      const int h = k / (Ep / 8), e0 = 8 * (k % (Ep / 8));
+    const int KS = Ep / 32;
+    // tiles h0 / 16 and h0 / 16 + 1
+    for (int k = tid; k < 2 * KS * kWave; k += kRgRowThreads) {
+      const int l = k % kWave, ks = k / kWave % KS, i = k / kWave / KS;
+      const int col = wt_col(i, l % 16), e0 = 32 * ks + 8 * (l / 16);
       bf16x8 p[2];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
+      for (int u = 0; u < 8; ++u) {
         bf16 a, b, c;
-        split3(tile[h][e0 + i], a, b, c);
-        p[0][i] = a;
-        p[1][i] = b;
+        split3(tile[col][e0 + u], a, b, c);
+        p[0][u] = a;
+        p[1][u] = b;
       }
-#pragma unroll
-      for (int q = 0; q < 2; ++q)
-        *reinterpret_cast<bf16x8*>(wt_out + q * plane + (size_t)(h0 + h) * Ep + e0) = p[q];
+      bf16* dst = wt_out + ((size_t)(h0 / 16 + i) * KS + ks) * 2 * kFrag + 8 * l;
+      *reinterpret_cast<bf16x8*>(dst) = p[0];
+      *reinterpret_cast<bf16x8*>(dst + kFrag) = p[1];
     }
     return;
   }
@@ -735,38 +751,37 @@ __global__ __launch_bounds__(kRgRowThreads) void router_grad_rows_bf16_kernel(
     }
   }
   store_pes_part(sums, kRgTok, E, dpes, part_pes);  // (its barrier covers the tile)
-  const size_t rplane = (size_t)T * Ep;
-  for (int k = tid; k < kRgTok * Ep / 8; k += kRgRowThreads) {
-    const int tl = k / (Ep / 8), e0 = 8 * (k % (Ep / 8));
-    if (t0 + tl >= T) break;
+  const int KS = Ep / 32, MS = Ep / 16;
+  for (int k = tid; k < KS * kWave; k += kRgRowThreads) {
+    const int l = k % kWave, ks = k / kWave, tl = l % 16, e0 = 32 * ks + 8 * (l / 16);
     bf16x8 p[2];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int u = 0; u < 8; ++u) {
       bf16 a, b, c;
-      split3(tile[tl][e0 + i], a, b, c);
-      p[0][i] = a;
-      p[1][i] = b;
+      split3(tile[tl][e0 + u], a, b, c);
+      p[0][u] = a;
+      p[1][u] = b;
     }
-#pragma unroll
-    for (int q = 0; q < 2; ++q)
-      *reinterpret_cast<bf16x8*>(rows_out + q * rplane + (size_t)(t0 + tl) * Ep + e0) = p[q];
+    bf16* dst = rows_out + ((size_t)blockIdx.x * KS + ks) * 2 * kFrag + 8 * l;
+    *reinterpret_cast<bf16x8*>(dst) = p[0];
+    *reinterpret_cast<bf16x8*>(dst + kFrag) = p[1];
   }
-  const int Tp = (T + 31) / 32 * 32;
-  const size_t cplane = (size_t)Ep * Tp;
-  for (int k = tid; k < Ep * (kRgTok / 8); k += kRgRowThreads) {
-    const int e = k / (kRgTok / 8), tl = 8 * (k % (kRgTok / 8));
+  // the block's 16 tokens are half a step: lane groups 0, 1 or 2, 3
+  for (int k = tid; k < MS * 32; k += kRgRowThreads) {
+    const int l = k % 32, m = k / 32, e = 16 * m + l % 16, tl = 8 * (l / 16);
     bf16x8 p[3];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
+    for (int u = 0; u < 8; ++u) {
       bf16 a, b, c;
-      split3(tile[tl + i][e], a, b, c);
-      p[0][i] = a;
-      p[1][i] = b;
-      p[2][i] = c;
+      split3(tile[tl + u][e], a, b, c);
+      p[0][u] = a;
+      p[1][u] = b;
+      p[2][u] = c;
     }
+    bf16* dst = cols_out + ((size_t)(blockIdx.x / 2) * MS + m) * 3 * kFrag +
+                8 * (l + 32 * (blockIdx.x % 2));
 #pragma unroll
-    for (int q = 0; q < 3; ++q)
-      *reinterpret_cast<bf16x8*>(cols_out + q * cplane + (size_t)e * Tp + t0 + tl) = p[q];
+    for (int q = 0; q < 3; ++q) *reinterpret_cast<bf16x8*>(dst + q * kFrag) = p[q];
   }
 }
 
@@ -788,8 +803,7 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int c = lane % 16, g = lane / 16;
   const int h0 = blockIdx.x * 64, m0 = blockIdx.y * MT, split = blockIdx.z;
-  const int Ep = (E + 31) / 32 * 32, Tp = (T + 31) / 32 * 32, all = Tp / 32;
-  const size_t cplane = (size_t)Ep * Tp;
+  const int MS = (E + 31) / 32 * 2, all = (T + 31) / 32;
   const int s0 = min(all, split * steps), s1 = min(all, s0 + steps);
   const int n = s1 - s0, a0 = s0 + wave * n / kRgWaves, a1 = s0 + (wave + 1) * n / kRgWaves;
   const bool beta_here = want_beta && blockIdx.y == 0;
@@ -816,10 +830,9 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
   };
   bf16x8 fa[2][3];
   auto load_a = [&](int s, int m, bf16x8 (&f)[3]) {
-    const int e = min(16 * (m0 + m) + c, Ep - 1);
-    const bf16* p = cols + (size_t)e * Tp + 32 * s + 8 * g;
+    const bf16* p = cols + ((size_t)s * MS + min(m0 + m, MS - 1)) * 3 * kFrag + 8 * lane;
 #pragma unroll
-    for (int q = 0; q < 3; ++q) f[q] = *reinterpret_cast<const bf16x8*>(p + q * cplane);
+    for (int q = 0; q < 3; ++q) f[q] = *reinterpret_cast<const bf16x8*>(p + q * kFrag);
   };
   if (a0 < a1) {
     load_x(a0);
@@ -910,10 +923,9 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
   }
 }
 
-// dx: a wave takes 64 tokens x 64 columns.  W^T is the first operand, its tile
-// j's row m being column 32 (j / 2) + 8 (m / 4) + 4 (j % 2) + m % 4, so that a
-// lane's results of two tiles are eight consecutive columns of a token: 16-byte
-// loads of x and stores of dx, four lanes to 64 bytes.
+// dx: a wave takes 64 tokens x 64 columns.  W^T is the first operand: with its
+// column order (wt_col) a lane's results of two tiles are eight consecutive
+// columns of a token, 16-byte loads of x and stores of dx.
 __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
     int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ mask,
     const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
@@ -922,8 +934,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
   const int c = lane % 16, g = lane / 16;
   const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgWaves + wave) * 64;
   if (t0 >= T) return;  // no barrier below
-  const int Ep = (E + 31) / 32 * 32;
-  const size_t rplane = (size_t)T * Ep, wplane = (size_t)H * Ep;
+  const int KS = (E + 31) / 32, tiles = (T + 31) / 32 * 2;
   f32x4 acc[4][4];  // token tile, column tile
 #pragma unroll
   for (int i = 0; i < 4; ++i)
@@ -933,17 +944,17 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
   const bf16* tr[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    wr[j] = wt + (size_t)(h0 + 32 * (j / 2) + 8 * (c / 4) + 4 * (j % 2) + c % 4) * Ep + 8 * g;
-    tr[j] = rows + (size_t)min(t0 + 16 * j + c, T - 1) * Ep + 8 * g;
+    wr[j] = wt + (size_t)(h0 / 16 + j) * KS * 2 * kFrag + 8 * lane;
+    tr[j] = rows + (size_t)min(t0 / 16 + j, tiles - 1) * KS * 2 * kFrag + 8 * lane;
   }
-  for (int k = 0; k < Ep; k += 32) {
+  for (int k = 0; k < KS; ++k) {
     bf16x8 fw[2][4], ft[2][4];
 #pragma unroll
     for (int q = 0; q < 2; ++q)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        fw[q][j] = *reinterpret_cast<const bf16x8*>(wr[j] + q * wplane + k);
-        ft[q][j] = *reinterpret_cast<const bf16x8*>(tr[j] + q * rplane + k);
+        fw[q][j] = *reinterpret_cast<const bf16x8*>(wr[j] + (2 * k + q) * kFrag);
+        ft[q][j] = *reinterpret_cast<const bf16x8*>(tr[j] + (2 * k + q) * kFrag);
       }
 #pragma unroll
     for (int i = 0; i < 4; ++i)
@@ -1090,7 +1101,7 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   const bf16* x = static_cast<const bf16*>(a.x);
   const long long Ep = (a.E + 31) / 32 * 32, Tp = (a.T + 31) / 32 * 32;
   bf16* rows = static_cast<bf16*>(a.ws_dl);
-  bf16* cols = rows + 2 * a.T * Ep;
+  bf16* cols = rows + 2 * Tp * Ep;
   bf16* wt = cols + 3 * Ep * Tp;
   uint8_t* live = reinterpret_cast<uint8_t*>(wt + 2 * a.H * Ep);
   const int splits = router_grad_splits(a.T), tb = router_grad_row_blocks(a.T);
@@ -1163,7 +1174,7 @@ int router_grad_row_blocks(int T) { return (T + 31) / 32 * 32 / kRgTok; }
 
 size_t router_grad_dl_bytes(int T, int H, int E) {
   const size_t Ep = (E + 31) / 32 * 32, Tp = (T + 31) / 32 * 32;
-  return 2 * (2 * T * Ep + 3 * Ep * Tp + 2 * H * Ep) + Tp;  // more than the 4 T E of fp32
+  return 2 * (5 * Tp * Ep + 2 * H * Ep) + Tp;  // more than the 4 T E of fp32
 }
 
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
