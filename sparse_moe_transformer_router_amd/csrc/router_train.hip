@@ -351,20 +351,37 @@ void by_group(int E, F go) {
 // ---------------------------------------------------------------------------
 constexpr int kRgRowWaves = 4;
 
-__device__ __forceinline__ void load8f(const bf16* p, float (&v)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    v[2 * i] = __uint_as_float(w[i] << 16);
-    v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
-  }
-}
 __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
+
+// Eight values as loaded.
+template <typename XT> struct Piece;
+template <> struct Piece<bf16> {
+  uint4 u;
+  __device__ __forceinline__ void load(const bf16* p) { u = *reinterpret_cast<const uint4*>(p); }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      v[2 * i] = __uint_as_float(w[i] << 16);
+      v[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+    }
+  }
+};
+template <> struct Piece<float> {
+  float4 a, b;
+  __device__ __forceinline__ void load(const float* p) {
+    a = reinterpret_cast<const float4*>(p)[0];
+    b = reinterpret_cast<const float4*>(p)[1];
+  }
+  __device__ __forceinline__ void get(float (&v)[8]) const {
+    v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
+    v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
+  }
+};
 
 // One token's share, by a wave: dl (experts lane + 64 j) scaled by r0 r, beta,
 // and d_topk_w_k q_k added to dpes.  A masked token gives zeros.
@@ -380,40 +397,48 @@ __device__ __forceinline__ void router_grad_token(
   for (int j = 0; j < 4; ++j) dl[j] = 0.0f;
   beta = 0.0f;
   if (!live) return;  // uniform over the wave
-  // the token's small rows first: their latency passes behind x's
+  // in the order of what has to wait: the picks, x's row (6 pieces a lane at a
+  // time), the logits, then what the picks point at
+  int e = d_w != nullptr && lane < K ? topk_idx[(size_t)t * K + lane] : -1;
+  const float dw = d_w != nullptr && lane < K ? d_w[(size_t)t * K + lane] : 0.0f;
+  constexpr int XP = 6, XSTEP = 8 * kWave;
+  const XT* xr = x + (size_t)t * H;
+  Piece<XT> xp[XP];
+  auto load_x = [&](int h0) {
+#pragma unroll
+    for (int i = 0; i < XP; ++i) xp[i].load(xr + min(h0 + i * XSTEP, H - 8));
+  };
+  load_x(8 * lane);
   float l[4];
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    const int e = lane + kWave * j;
-    l[j] = e < E ? logits[(size_t)t * E + e] : 0.0f;
-    if (d_logits != nullptr && e < E) dl[j] = d_logits[(size_t)t * E + e];
+    const int ej = lane + kWave * j;
+    l[j] = ej < E ? logits[(size_t)t * E + ej] : 0.0f;
+    if (d_logits != nullptr && ej < E) dl[j] = d_logits[(size_t)t * E + ej];
   }
   // lane k < K: slot k (an id outside [0, E) is no slot)
-  int e = -1;
-  float lk = -INFINITY, dw = 0.0f, pk = 0.0f;
-  if (d_w != nullptr && lane < K) {
-    e = topk_idx[(size_t)t * K + lane];
-    if ((unsigned)e < (unsigned)E) {
-      lk = logits[(size_t)t * E + e];
-      dw = d_w[(size_t)t * K + lane];
-      pk = pes[e];
-    } else {
-      e = -1;
-    }
-  }
+  if ((unsigned)e >= (unsigned)E) e = -1;
+  const float lk = e >= 0 ? logits[(size_t)t * E + e] : -INFINITY;
+  const float pk = e >= 0 ? pes[e] : 0.0f;
   float ss = 0.0f, sg = 0.0f;
-  const XT* xr = x + (size_t)t * H;
-  for (int h = 8 * lane; h < H; h += 8 * kWave) {
-    float v[8];
-    load8f(xr + h, v);
+  for (int h0 = 8 * lane;; h0 += XP * XSTEP) {
 #pragma unroll
-    for (int i = 0; i < 8; ++i) ss = __builtin_fmaf(v[i], v[i], ss);
-    if (pre_gain != nullptr) {
-      float g[8];
-      load8f(pre_gain + h, g);
+    for (int i = 0; i < XP; ++i) {
+      const int h = h0 + i * XSTEP;
+      if (h >= H) break;
+      float v[8];
+      xp[i].get(v);
 #pragma unroll
-      for (int i = 0; i < 8; ++i) sg = __builtin_fmaf(v[i] * g[i], v[i] * g[i], sg);
+      for (int u = 0; u < 8; ++u) ss = __builtin_fmaf(v[u], v[u], ss);
+      if (pre_gain != nullptr) {
+        float g[8];
+        load8f(pre_gain + h, g);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) sg = __builtin_fmaf(v[u] * g[u], v[u] * g[u], sg);
+      }
     }
+    if (h0 - 8 * lane + XP * XSTEP >= H) break;  // uniform
+    load_x(h0 + XP * XSTEP);
   }
   ss = group_sum<kWave>(ss);
   float r0 = 1.0f, r;
@@ -429,9 +454,9 @@ __device__ __forceinline__ void router_grad_token(
     float q = lk == -INFINITY ? 0.0f : expf(lk - top);
     const float z = group_sum<kWave>(q);
     q = z > 0.0f ? q / z : 0.0f;
-    const float d = dw * pk;
+    const float d = e >= 0 ? dw * pk : 0.0f;
     const float qd = group_sum<kWave>(q * d);
-    const float dlk = q * (d - qd), dsk = dw * q;
+    const float dlk = q * (d - qd), dsk = e >= 0 ? dw * q : 0.0f;
     for (int k = 0; k < K; ++k) {  // a repeated id adds up
       const int ek = __builtin_amdgcn_readlane(e, k);
       const float dk = lane_value(dlk, k), sk = lane_value(dsk, k);
@@ -798,7 +823,7 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
     int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
     const bf16* __restrict__ cols, const float* __restrict__ beta, bool want_beta,
     float* __restrict__ part_g, float* __restrict__ part_b) {
-  __shared__ f32x4 acc_s[kRgWaves][4][kWave];
+  __shared__ f32x4 acc_s[2][kRgWaves][4][kWave];
   __shared__ float b_s[kRgWaves][4][64];
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int c = lane % 16, g = lane / 16;
@@ -898,22 +923,27 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
     for (int i = 0; i < 4; ++i) b_s[wave][g][4 * c + i] = bs[i];
   }
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
+  for (int m = 0; m < MT; m += 2) {
     __syncthreads();
 #pragma unroll
-    for (int i = 0; i < 4; ++i) acc_s[wave][i][lane] = acc[m][i];
+    for (int d = 0; d < 2; ++d)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) acc_s[d][wave][i][lane] = acc[m + d][i];
     __syncthreads();
     // wave w adds result register w of every lane: row 4 g + w, columns 4 c .. + 3
-    f32x4 v;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      v[i] = 0.0f;
+    for (int d = 0; d < 2; ++d) {
+      f32x4 v;
 #pragma unroll
-      for (int u = 0; u < kRgWaves; ++u) v[i] += acc_s[u][i][lane][wave];
+      for (int i = 0; i < 4; ++i) {
+        v[i] = 0.0f;
+#pragma unroll
+        for (int u = 0; u < kRgWaves; ++u) v[i] += acc_s[d][u][i][lane][wave];
+      }
+      const int e = 16 * (m0 + m + d) + 4 * g + wave;
+      if (e < E)
+        *reinterpret_cast<f32x4*>(part_g + ((size_t)split * E + e) * H + h0 + 4 * c) = v;
     }
-    const int e = 16 * (m0 + m) + 4 * g + wave;
-    if (e < E)
-      *reinterpret_cast<f32x4*>(part_g + ((size_t)split * E + e) * H + h0 + 4 * c) = v;
   }
   if (beta_here && threadIdx.x < 64) {
     float v = 0.0f;
@@ -923,79 +953,99 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
   }
 }
 
-// dx: a wave takes 64 tokens x 64 columns.  W^T is the first operand: with its
-// column order (wt_col) a lane's results of two tiles are eight consecutive
-// columns of a token, 16-byte loads of x and stores of dx.
-__global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_bf16_kernel(
-    int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ mask,
+// dx: a block takes 64 columns x 256 tokens, a wave 32 of the tokens.  The columns'
+// W^T fragments go to LDS once (32 KB at 128 experts), the tokens' fragments and
+// the rows of x come straight from memory, one step ahead.  W^T is the first
+// operand: with its column order (wt_col) a lane's results of two tiles are eight
+// consecutive columns of a token, 16-byte loads of x and stores of dx.
+constexpr int kRgXWaves = 8, kRgXTok = 32;
+__global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
+    int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
     const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
     const float* __restrict__ scale, const float* __restrict__ pre_gain, bf16* __restrict__ dx) {
-  const int wave = threadIdx.x / kWave, lane = lane_id();
+  extern __shared__ __align__(16) unsigned char smem[];
+  bf16x8* ws = reinterpret_cast<bf16x8*>(smem);  // [4 tiles][KS][2][lane]
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, g = lane / 16;
-  const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgWaves + wave) * 64;
-  if (t0 >= T) return;  // no barrier below
+  const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgXWaves + wave) * kRgXTok;
   const int KS = (E + 31) / 32, tiles = (T + 31) / 32 * 2;
-  f32x4 acc[4][4];  // token tile, column tile
+  const bf16* tr[2];
 #pragma unroll
-  for (int i = 0; i < 4; ++i)
+  for (int i = 0; i < 2; ++i)
+    tr[i] = rows + (size_t)min(t0 / 16 + i, tiles - 1) * KS * 2 * kFrag + 8 * lane;
+  bf16x8 ft[2][2];  // [token tile][part]
+  auto load_t = [&](int k) {
+#pragma unroll
+    for (int i = 0; i < 2; ++i)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        ft[i][q] = *reinterpret_cast<const bf16x8*>(tr[i] + (2 * k + q) * kFrag);
+  };
+  load_t(0);
+  Piece<bf16> xp[2][2];  // [token tile][column pair]
+  float be[2];
+  bool on[2];
+#pragma unroll
+  for (int i = 0; i < 2; ++i) {
+    const int t = min(t0 + 16 * i + c, T - 1);
+    be[i] = beta[t];
+    on[i] = live[t] != 0;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) xp[i][p].load(x + (size_t)t * H + h0 + 32 * p + 8 * g);
+  }
+  const bf16x8* src = reinterpret_cast<const bf16x8*>(wt + (size_t)h0 / 16 * KS * 2 * kFrag);
+#pragma unroll 4
+  for (int k = tid; k < 4 * KS * 2 * kWave; k += 64 * kRgXWaves) ws[k] = src[k];
+  __syncthreads();
+  f32x4 acc[2][4];  // token tile, column tile
+#pragma unroll
+  for (int i = 0; i < 2; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
-  const bf16* wr[4];
-  const bf16* tr[4];
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    wr[j] = wt + (size_t)(h0 / 16 + j) * KS * 2 * kFrag + 8 * lane;
-    tr[j] = rows + (size_t)min(t0 / 16 + j, tiles - 1) * KS * 2 * kFrag + 8 * lane;
-  }
   for (int k = 0; k < KS; ++k) {
-    bf16x8 fw[2][4], ft[2][4];
+    bf16x8 cur[2][2];
 #pragma unroll
-    for (int q = 0; q < 2; ++q)
+    for (int i = 0; i < 2; ++i)
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        fw[q][j] = *reinterpret_cast<const bf16x8*>(wr[j] + (2 * k + q) * kFrag);
-        ft[q][j] = *reinterpret_cast<const bf16x8*>(tr[j] + (2 * k + q) * kFrag);
+      for (int q = 0; q < 2; ++q) cur[i][q] = ft[i][q];
+    load_t(min(k + 1, KS - 1));
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const bf16x8 w0 = ws[((j * KS + k) * 2) * kWave + lane];
+      const bf16x8 w1 = ws[((j * KS + k) * 2 + 1) * kWave + lane];
+#pragma unroll
+      for (int i = 0; i < 2; ++i) {
+        acc[i][j] = mfma_bf16(w0, cur[i][1], acc[i][j]);
+        acc[i][j] = mfma_bf16(w1, cur[i][0], acc[i][j]);
+        acc[i][j] = mfma_bf16(w0, cur[i][0], acc[i][j]);
       }
-#pragma unroll
-    for (int i = 0; i < 4; ++i)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        acc[i][j] = mfma_bf16(fw[0][j], ft[1][i], acc[i][j]);
-        acc[i][j] = mfma_bf16(fw[1][j], ft[0][i], acc[i][j]);
-        acc[i][j] = mfma_bf16(fw[0][j], ft[0][i], acc[i][j]);
-      }
-  }
-  // pair p of tiles: columns h0 + 32 p + 8 g .. + 7
-  float gc[2][8], ge[2][8];
-#pragma unroll
-  for (int p = 0; p < 2; ++p) {
-    float sc[8], gn[8];
-    load8f(scale + h0 + 32 * p + 8 * g, sc);
-    if (pre_gain != nullptr) load8f(pre_gain + h0 + 32 * p + 8 * g, gn);
-#pragma unroll
-    for (int u = 0; u < 8; ++u) {
-      gc[p][u] = pre_gain != nullptr ? gn[u] * sc[u] : sc[u];
-      ge[p][u] = pre_gain != nullptr ? gn[u] * gn[u] + eps : 1.0f;
     }
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int t = t0 + 16 * i + c;
-    if (t >= T) continue;
-    const bool live = mask == nullptr || mask[t] != 0;
-    const float be = beta[t];
+  for (int p = 0; p < 2; ++p) {  // columns h .. h + 7
+    const int h = h0 + 32 * p + 8 * g;
+    float gc[8], gn[8], ge[8];
+    load8f(scale + h, gc);
+    if (pre_gain != nullptr) load8f(pre_gain + h, gn);
 #pragma unroll
-    for (int p = 0; p < 2; ++p) {
-      const size_t at = (size_t)t * H + h0 + 32 * p + 8 * g;
+    for (int u = 0; u < 8; ++u) {
+      ge[u] = pre_gain != nullptr ? gn[u] * gn[u] + eps : 1.0f;
+      if (pre_gain != nullptr) gc[u] *= gn[u];
+    }
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+      const int t = t0 + 16 * i + c;
+      if (t >= T) continue;
       float xv[8];
-      load8f(x + at, xv);
+      xp[i][p].get(xv);
       bf16x8 o;
 #pragma unroll
       for (int u = 0; u < 8; ++u) {
-        const float v = gc[p][u] * acc[i][2 * p + u / 4][u % 4] - xv[u] * (be * ge[p][u]);
-        o[u] = (bf16)(live ? v : 0.0f);
+        const float v = gc[u] * acc[i][2 * p + u / 4][u % 4] - xv[u] * (be[i] * ge[u]);
+        o[u] = (bf16)(on[i] ? v : 0.0f);
       }
-      *reinterpret_cast<bf16x8*>(dx + at) = o;
+      *reinterpret_cast<bf16x8*>(dx + (size_t)t * H + h) = o;
     }
   }
 }
@@ -1124,11 +1174,12 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   if (a.E <= 32) by_mask(std::integral_constant<int, 2>{});
   else if (a.E <= 64) by_mask(std::integral_constant<int, 4>{});
   else by_mask(std::integral_constant<int, 8>{});
-  if (a.d_x != nullptr)
-    hipLaunchKernelGGL(router_grad_x_bf16_kernel,
-                       dim3(a.H / 64, (a.T + 64 * kRgWaves - 1) / (64 * kRgWaves)),
-                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, a.eps, x, a.mask, rows,
+  if (a.d_x != nullptr) {
+    constexpr int tok = kRgXWaves * kRgXTok;  // per block
+    hipLaunchKernelGGL(router_grad_x_bf16_kernel, dim3(a.H / 64, (a.T + tok - 1) / tok),
+                       dim3(64 * kRgXWaves), 64 * Ep * 4, s, a.T, a.H, a.E, a.eps, x, live, rows,
                        a.ws_beta, wt, a.router_scale, a.pre_gain, static_cast<bf16*>(a.d_x));
+  }
 }
 
 }  // namespace
