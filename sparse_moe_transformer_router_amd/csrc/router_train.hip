@@ -87,13 +87,14 @@ __device__ __forceinline__ void group_softmax(float (&l)[4], float& inv, float& 
 //   P_e = 1/N sum_t softmax(l_t)_e,          lse_t = log sum_e exp l_te,
 //   balance = E sum_e f_e P_e,               z = 1/N sum_t lse_t^2.
 // Block b takes tokens [b * span, ...): G lanes a token, four experts a lane,
-// kept in registers over the block's tokens.  It writes its sums of P_e, its
-// counts, its sum of lse^2 and its number of live tokens; the second step adds
-// the blocks in order.  A batch of one block's size runs both steps in one
-// launch.
+// kept in registers over the block's tokens, while four more waves count the
+// block's slots.  It writes its sums of P_e, its counts, its sum of lse^2 and its
+// number of live tokens; the second step adds the blocks in order.  A batch of
+// one block's size runs both steps in one launch.
 // ---------------------------------------------------------------------------
-constexpr int kBalThreads = 512;
-constexpr int kBalWaves = kBalThreads / kWave;
+constexpr int kBalWaves = 8, kBalCountWaves = 4;  // softmax, counts
+constexpr int kBalThreads = (kBalWaves + kBalCountWaves) * kWave;
+constexpr int kBalCountThreads = kBalCountWaves * kWave;
 constexpr int kBalUnroll = 4;       // tokens a group loads before it adds the first
 constexpr int kBalOneBlock = 256;   // tokens that one block takes alone
 constexpr int kBalMaxBlocks = 256;  // one block per CU
@@ -137,61 +138,72 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
   constexpr int TW = kWave / G;             // tokens per wave
   constexpr int TB = TW * kBalWaves;        // tokens per block and round
   __shared__ float sum_p[kBalWaves * TW][4 * G];
-  __shared__ int cnt[kBalWaves][kMaxE];
+  __shared__ int cnt[kBalCountWaves][kMaxE];
   __shared__ float wave_z[kBalWaves];
   __shared__ int wave_live[kBalWaves];
-  __shared__ float red[kBalWaves];
+  __shared__ float red[kBalThreads / kWave];
   const int tid = threadIdx.x, wave = tid / kWave, lane = lane_id();
-  const int gl = lane % G, grp = wave * TW + lane / G;
   const int t0 = blockIdx.x * span, t1 = min(T, t0 + span);
-  for (int i = tid; i < kBalWaves * kMaxE; i += kBalThreads) (&cnt[0][0])[i] = 0;
-  __syncthreads();
-  // counts: the block's slots in order, one counter row per wave
-  for (int s = t0 * K + tid; s < t1 * K; s += kBalThreads) {
-    const int e = topk_idx[s];
-    if ((unsigned)e < (unsigned)E && (mask == nullptr || mask[s / K] != 0))
-      atomicAdd(&cnt[wave][e], 1);
-  }
-  float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-  float zsum = 0.0f;
-  int live = 0;
-  for (int t = t0 + grp; t < t1; t += TB * kBalUnroll) {
-    float l[kBalUnroll][4];
-    bool on[kBalUnroll];
+  if (wave >= kBalWaves) {
+    // one counter row per wave, cleared and used by that wave alone
+    int* mine = cnt[wave - kBalWaves];
+    for (int e = lane; e < kMaxE; e += kWave) mine[e] = 0;
+    constexpr int U = 8;  // slots a lane loads before it counts the first
+    for (int s0 = t0 * K + tid - kBalWaves * kWave; s0 < t1 * K; s0 += U * kBalCountThreads) {
+      int e[U];
+      bool on[U];
 #pragma unroll
-    for (int u = 0; u < kBalUnroll; ++u) {
-      const int tu = min(t + u * TB, t1 - 1);
-      on[u] = t + u * TB < t1 && (mask == nullptr || mask[tu] != 0);
-      load_logits4<VEC>(logits + (size_t)tu * E, 4 * gl, E, l[u]);
+      for (int u = 0; u < U; ++u) {
+        const int s = s0 + u * kBalCountThreads, sc = min(s, t1 * K - 1);
+        e[u] = topk_idx[sc];
+        on[u] = s < t1 * K && (mask == nullptr || mask[sc / K] != 0);
+      }
+#pragma unroll
+      for (int u = 0; u < U; ++u)
+        if (on[u] && (unsigned)e[u] < (unsigned)E) atomicAdd(&mine[e[u]], 1);
     }
+  } else {
+    const int gl = lane % G, grp = wave * TW + lane / G;
+    float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+    float zsum = 0.0f;
+    int live = 0;
+    for (int t = t0 + grp; t < t1; t += TB * kBalUnroll) {
+      float l[kBalUnroll][4];
+      bool on[kBalUnroll];
 #pragma unroll
-    for (int u = 0; u < kBalUnroll; ++u) {
-      float inv, lse;
-      group_softmax<G>(l[u], inv, lse);
-      if (on[u]) {  // a masked row may hold anything
+      for (int u = 0; u < kBalUnroll; ++u) {
+        const int tu = min(t + u * TB, t1 - 1);
+        on[u] = t + u * TB < t1 && (mask == nullptr || mask[tu] != 0);
+        load_logits4<VEC>(logits + (size_t)tu * E, 4 * gl, E, l[u]);
+      }
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += l[u][j] * inv;
-        zsum += lse * lse;
-        live += 1;
+      for (int u = 0; u < kBalUnroll; ++u) {
+        float inv, lse;
+        group_softmax<G>(l[u], inv, lse);
+        if (on[u]) {  // a masked row may hold anything
+#pragma unroll
+          for (int j = 0; j < 4; ++j) acc[j] += l[u][j] * inv;
+          zsum += lse * lse;
+          live += 1;
+        }
       }
     }
-  }
 #pragma unroll
-  for (int j = 0; j < 4; ++j)
-    if (4 * gl + j < E) sum_p[grp][4 * gl + j] = acc[j];
-  // one lane of each group holds its tokens' sum
-  zsum = wave_sum(gl == 0 ? zsum : 0.0f);
-  live = wave_sum(gl == 0 ? live : 0);
-  if (lane == 0) {
-    wave_z[wave] = zsum;
-    wave_live[wave] = live;
+    for (int j = 0; j < 4; ++j) sum_p[grp][4 * gl + j] = acc[j];
+    // one lane of each group holds its tokens' sum
+    zsum = wave_sum(gl == 0 ? zsum : 0.0f);
+    live = wave_sum(gl == 0 ? live : 0);
+    if (lane == 0) {
+      wave_z[wave] = zsum;
+      wave_live[wave] = live;
+    }
   }
   __syncthreads();
   float p = 0.0f, z = 0.0f;
   int n = 0, nl = 0;
   if (tid < E) {
     for (int w = 0; w < kBalWaves * TW; ++w) p += sum_p[w][tid];
-    for (int w = 0; w < kBalWaves; ++w) n += cnt[w][tid];
+    for (int w = 0; w < kBalCountWaves; ++w) n += cnt[w][tid];
   }
   for (int w = 0; w < kBalWaves; ++w) {
     z += wave_z[w];
@@ -229,11 +241,13 @@ __global__ __launch_bounds__(kBalFinThreads) void balance_final_kernel(
   const int e = tid % E, r = tid / E;
   float p = 0.0f;
   int n = 0;
-  if (r < rows)
+  if (r < rows) {
+#pragma unroll 8
     for (int i = r; i < nb; i += rows) {
       p += part_p[(size_t)i * E + e];
       n += part_n[(size_t)i * E + e];
     }
+  }
   sp[tid] = p;
   sn[tid] = n;
   float z = tid < nb ? part_z[tid] : 0.0f;  // nb <= kBalMaxBlocks
@@ -721,7 +735,7 @@ __device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
   c = (bf16)(r - (float)b);
 }
 
-__global__ __launch_bounds__(kRgRowThreads) void router_grad_rows_bf16_kernel(
+__global__ __launch_bounds__(kRgRowThreads, 8) void router_grad_rows_bf16_kernel(
     int T, int H, int E, int K, float eps, const bf16* __restrict__ x,
     const float* __restrict__ pre_gain, const float* __restrict__ pes,
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,

@@ -130,16 +130,17 @@ def _ptr(t: Optional[torch.Tensor]):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _current_device() -> int:
+def _device() -> int:
     """Index of the current GPU, -2 before torch has set one up (a CPU tensor's
     device is -1)."""
     return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
-def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, optional: bool = False):
-    """Device pointer of an array argument, after its type and size: a tensor of
-    dtype (or of one of several) with at least numel elements, on the current
-    device, contiguous."""
+def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, dev: int,
+         optional: bool = False):
+    """Device pointer of an array argument, after its type and size: a contiguous
+    tensor of dtype (or of one of several) with at least numel elements, on
+    device dev."""
     if t is None:
         if optional:
             return None
@@ -148,11 +149,18 @@ def _arg(name: str, t: Optional[torch.Tensor], dtype, numel: int, optional: bool
         raise TypeError(f"{name} is {t.dtype}, expected {dtype}")
     if t.numel() < numel:
         raise ValueError(f"{name} has {t.numel()} elements, {numel} needed")
-    if t.get_device() != _current_device():
+    if t.get_device() != dev:
         raise ValueError(f"{name} is on {t.device}, not on the current GPU")
     if not t.is_contiguous():
         raise ValueError("tensors passed to libmoe must be contiguous")
     return t.data_ptr()
+
+
+def _work(ws: Optional[torch.Tensor], dev: int):
+    """Pointer and size of a workspace (its size is the library's to check)."""
+    if ws is None:
+        return None, 0
+    return _arg("ws", ws, torch.uint8, 0, dev), ws.numel()
 
 
 _MASK = (torch.uint8, torch.bool)
@@ -206,61 +214,64 @@ def moe_router(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain,
 def moe_router_logits(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx,
                       topk_w, logits, ws, stream=None):
     """moe_router, with the logits [T, E] as an output."""
-    E, H, K, f32 = d.num_experts, d.hidden, d.top_k, torch.float32
+    E, H, K, f32, dev = d.num_experts, d.hidden, d.top_k, torch.float32, _device()
     _check(_lib.moe_router_logits(
-        ctypes.byref(d), T, _arg("x", x, _act(d), T * H), _arg("router_w", router_w, f32, E * H),
-        _arg("router_scale", router_scale, f32, H),
-        _arg("per_expert_scale", per_expert_scale, f32, E),
-        _arg("pre_norm_gain", pre_norm_gain, f32, H, True),
-        _arg("topk_idx", topk_idx, torch.int32, T * K), _arg("topk_w", topk_w, f32, T * K),
-        _arg("logits", logits, f32, T * E), _ptr(ws), ws.numel() if ws is not None else 0,
-        _stream(stream)))
+        ctypes.byref(d), T, _arg("x", x, _act(d), T * H, dev),
+        _arg("router_w", router_w, f32, E * H, dev),
+        _arg("router_scale", router_scale, f32, H, dev),
+        _arg("per_expert_scale", per_expert_scale, f32, E, dev),
+        _arg("pre_norm_gain", pre_norm_gain, f32, H, dev, True),
+        _arg("topk_idx", topk_idx, torch.int32, T * K, dev),
+        _arg("topk_w", topk_w, f32, T * K, dev),
+        _arg("logits", logits, f32, T * E, dev), *_work(ws, dev), _stream(stream)))
 
 
 def moe_balance_loss(d, T, logits, topk_idx, token_mask, balance_coef, z_coef, loss,
                      expert_counts, mean_probs, ws, stream=None):
     """Balance loss, z-loss, per-expert counts and mean probabilities of a batch."""
-    E, f32 = d.num_experts, torch.float32
+    E, f32, dev = d.num_experts, torch.float32, _device()
     _check(_lib.moe_balance_loss(
-        ctypes.byref(d), T, _arg("logits", logits, f32, T * E),
-        _arg("topk_idx", topk_idx, torch.int32, T * d.top_k),
-        _arg("token_mask", token_mask, _MASK, T, True), balance_coef, z_coef,
-        _arg("loss", loss, f32, 4), _arg("expert_counts", expert_counts, torch.int32, E),
-        _arg("mean_probs", mean_probs, f32, E), _ptr(ws), ws.numel() if ws is not None else 0,
-        _stream(stream)))
+        ctypes.byref(d), T, _arg("logits", logits, f32, T * E, dev),
+        _arg("topk_idx", topk_idx, torch.int32, T * d.top_k, dev),
+        _arg("token_mask", token_mask, _MASK, T, dev, True), balance_coef, z_coef,
+        _arg("loss", loss, f32, 4, dev), _arg("expert_counts", expert_counts, torch.int32, E, dev),
+        _arg("mean_probs", mean_probs, f32, E, dev), *_work(ws, dev), _stream(stream)))
 
 
 def moe_balance_loss_grad(d, T, logits, token_mask, expert_counts, loss, balance_coef, z_coef,
                           d_loss, d_logits, stream=None):
     """Gradient of d_loss * loss[0] in the logits."""
-    E, f32 = d.num_experts, torch.float32
+    E, f32, dev = d.num_experts, torch.float32, _device()
     _check(_lib.moe_balance_loss_grad(
-        ctypes.byref(d), T, _arg("logits", logits, f32, T * E),
-        _arg("token_mask", token_mask, _MASK, T, True),
-        _arg("expert_counts", expert_counts, torch.int32, E), _arg("loss", loss, f32, 4),
-        balance_coef, z_coef, _arg("d_loss", d_loss, f32, 1),
-        _arg("d_logits", d_logits, f32, T * E), _stream(stream)))
+        ctypes.byref(d), T, _arg("logits", logits, f32, T * E, dev),
+        _arg("token_mask", token_mask, _MASK, T, dev, True),
+        _arg("expert_counts", expert_counts, torch.int32, E, dev), _arg("loss", loss, f32, 4, dev),
+        balance_coef, z_coef, _arg("d_loss", d_loss, f32, 1, dev),
+        _arg("d_logits", d_logits, f32, T * E, dev), _stream(stream)))
 
 
 def moe_router_grad(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, logits,
                     topk_idx, token_mask, d_topk_w, d_logits, d_x, d_router_w, d_router_scale,
                     d_per_expert_scale, d_pre_norm_gain, ws, stream=None):
     """Backward pass of moe_router_logits."""
-    E, H, K, f32 = d.num_experts, d.hidden, d.top_k, torch.float32
+    E, H, K, f32, dev = d.num_experts, d.hidden, d.top_k, torch.float32, _device()
     _check(_lib.moe_router_grad(
-        ctypes.byref(d), T, _arg("x", x, _act(d), T * H), _arg("router_w", router_w, f32, E * H),
-        _arg("router_scale", router_scale, f32, H),
-        _arg("per_expert_scale", per_expert_scale, f32, E, True),
-        _arg("pre_norm_gain", pre_norm_gain, f32, H, True), _arg("logits", logits, f32, T * E),
-        _arg("topk_idx", topk_idx, torch.int32, T * K, True),
-        _arg("token_mask", token_mask, _MASK, T, True),
-        _arg("d_topk_w", d_topk_w, f32, T * K, True),
-        _arg("d_logits", d_logits, f32, T * E, True), _arg("d_x", d_x, _act(d), T * H, True),
-        _arg("d_router_w", d_router_w, f32, E * H),
-        _arg("d_router_scale", d_router_scale, f32, H),
-        _arg("d_per_expert_scale", d_per_expert_scale, f32, E),
-        _arg("d_pre_norm_gain", d_pre_norm_gain, f32, H, True), _ptr(ws),
-        ws.numel() if ws is not None else 0, _stream(stream)))
+        ctypes.byref(d), T, _arg("x", x, _act(d), T * H, dev),
+        _arg("router_w", router_w, f32, E * H, dev),
+        _arg("router_scale", router_scale, f32, H, dev),
+        _arg("per_expert_scale", per_expert_scale, f32, E, dev, True),
+        _arg("pre_norm_gain", pre_norm_gain, f32, H, dev, True),
+        _arg("logits", logits, f32, T * E, dev),
+        _arg("topk_idx", topk_idx, torch.int32, T * K, dev, True),
+        _arg("token_mask", token_mask, _MASK, T, dev, True),
+        _arg("d_topk_w", d_topk_w, f32, T * K, dev, True),
+        _arg("d_logits", d_logits, f32, T * E, dev, True),
+        _arg("d_x", d_x, _act(d), T * H, dev, True),
+        _arg("d_router_w", d_router_w, f32, E * H, dev),
+        _arg("d_router_scale", d_router_scale, f32, H, dev),
+        _arg("d_per_expert_scale", d_per_expert_scale, f32, E, dev),
+        _arg("d_pre_norm_gain", d_pre_norm_gain, f32, H, dev, True), *_work(ws, dev),
+        _stream(stream)))
 
 
 def moe_route(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx, topk_w,
@@ -358,17 +369,19 @@ def moe_quantize_b128(block_rows, w, q, scale, stream=None):
     cols]: per 128 x 128 block (block_rows = 128, weights) or per 128 values of a
     row (block_rows = 1, activations)."""
     batch, rows, cols, ns = _b128_shape(block_rows, w, "w")
+    dev = _device()
     _check(_lib.moe_quantize_b128(block_rows, batch, rows, cols,
-                                  _arg("w", w, torch.bfloat16, w.numel()),
-                                  _arg("q", q, _CODE, w.numel()),
-                                  _arg("scale", scale, torch.float32, ns), _stream(stream)))
+                                  _arg("w", w, torch.bfloat16, w.numel(), dev),
+                                  _arg("q", q, _CODE, w.numel(), dev),
+                                  _arg("scale", scale, torch.float32, ns, dev), _stream(stream)))
 
 
 def moe_dequantize_b128(block_rows, q, scale, out, stream=None):
     batch, rows, cols, ns = _b128_shape(block_rows, q, "q")
-    _check(_lib.moe_dequantize_b128(block_rows, batch, rows, cols, _arg("q", q, _CODE, q.numel()),
-                                    _arg("scale", scale, torch.float32, ns),
-                                    _arg("out", out, torch.float32, q.numel()), _stream(stream)))
+    dev = _device()
+    _check(_lib.moe_dequantize_b128(block_rows, batch, rows, cols, _arg("q", q, _CODE, q.numel(), dev),
+                                    _arg("scale", scale, torch.float32, ns, dev),
+                                    _arg("out", out, torch.float32, q.numel(), dev), _stream(stream)))
 
 
 def linear_b128_workspace(max_tokens: int, in_features: int, device="cuda") -> torch.Tensor:
@@ -384,13 +397,12 @@ def moe_linear_b128(T, x, w_q, w_scale, y, ws, stream=None):
     w_q [out, in]; x is quantized inside."""
     if w_q.dim() != 2:
         raise ValueError("w_q needs two axes")
-    n, k = w_q.shape
+    (n, k), dev = w_q.shape, _device()
     _check(_lib.moe_linear_b128(
-        T, n, k, _arg("x", x, torch.bfloat16, T * k), _arg("w_q", w_q, _CODE, n * k),
-        _arg("w_scale", w_scale, torch.float32, _blocks(n) * _blocks(k)),
-        _arg("y", y, (torch.bfloat16, torch.float32), T * n),
-        MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, _ptr(ws),
-        ws.numel() if ws is not None else 0, _stream(stream)))
+        T, n, k, _arg("x", x, torch.bfloat16, T * k, dev), _arg("w_q", w_q, _CODE, n * k, dev),
+        _arg("w_scale", w_scale, torch.float32, _blocks(n) * _blocks(k), dev),
+        _arg("y", y, (torch.bfloat16, torch.float32), T * n, dev),
+        MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, *_work(ws, dev), _stream(stream)))
 
 
 def moe_expert_ffn_b128(d, T, x, w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, topk_w,
@@ -398,17 +410,17 @@ def moe_expert_ffn_b128(d, T, x, w_gate_up_q, w_gate_up_scale, w_down_q, w_down_
     """The experts with E4M3 weights scaled per 128 x 128 block, activations per
     128 values."""
     H, E, I, S = d.hidden, d.num_experts, d.expert_inter, T * d.top_k
-    f32, i32 = torch.float32, torch.int32
+    f32, i32, dev = torch.float32, torch.int32, _device()
     _check(_lib.moe_expert_ffn_b128(
-        ctypes.byref(d), T, _arg("x", x, torch.bfloat16, T * H),
-        _arg("w_gate_up_q", w_gate_up_q, _CODE, E * 2 * I * H),
-        _arg("w_gate_up_scale", w_gate_up_scale, f32, E * _blocks(2 * I) * _blocks(H)),
-        _arg("w_down_q", w_down_q, _CODE, E * H * I),
-        _arg("w_down_scale", w_down_scale, f32, E * _blocks(H) * _blocks(I)),
-        _arg("topk_w", topk_w, f32, S), _arg("offsets", offsets, i32, E + 1),
-        _arg("sorted_slots", sorted_slots, i32, S),
-        _arg("y_slots", y_slots, torch.bfloat16 if d.slot_dtype == MOE_BF16 else f32, S * H),
-        _ptr(ws), ws.numel() if ws is not None else 0, _stream(stream)))
+        ctypes.byref(d), T, _arg("x", x, torch.bfloat16, T * H, dev),
+        _arg("w_gate_up_q", w_gate_up_q, _CODE, E * 2 * I * H, dev),
+        _arg("w_gate_up_scale", w_gate_up_scale, f32, E * _blocks(2 * I) * _blocks(H), dev),
+        _arg("w_down_q", w_down_q, _CODE, E * H * I, dev),
+        _arg("w_down_scale", w_down_scale, f32, E * _blocks(H) * _blocks(I), dev),
+        _arg("topk_w", topk_w, f32, S, dev), _arg("offsets", offsets, i32, E + 1, dev),
+        _arg("sorted_slots", sorted_slots, i32, S, dev),
+        _arg("y_slots", y_slots, torch.bfloat16 if d.slot_dtype == MOE_BF16 else f32, S * H, dev),
+        *_work(ws, dev), _stream(stream)))
 
 
 def moe_expert_gate_up(d, T, x, w_gate_up, offsets, sorted_slots, h, stream=None):

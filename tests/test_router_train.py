@@ -118,12 +118,12 @@ def test_binding_checks_types_and_sizes():
     d = dims()
     cpu = torch.zeros(4, 128)
     with pytest.raises(ValueError, match="not on the current GPU"):
-        lib._arg("logits", cpu, torch.float32, 4)
+        lib._arg("logits", cpu, torch.float32, 4, 0)
     with pytest.raises(TypeError, match="logits"):
-        lib._arg("logits", cpu.double(), torch.float32, 4)
+        lib._arg("logits", cpu.double(), torch.float32, 4, 0)
     with pytest.raises(ValueError, match="needed"):
-        lib._arg("logits", cpu, torch.float32, 4096)
+        lib._arg("logits", cpu, torch.float32, 4096, 0)
     with pytest.raises(ValueError, match="required"):
-        lib._arg("logits", None, torch.float32, 4)
-    assert lib._arg("token_mask", None, lib._MASK, 4, True) is None
+        lib._arg("logits", None, torch.float32, 4, 0)
+    assert lib._arg("token_mask", None, lib._MASK, 4, 0, True) is None
     assert d.num_experts == 128
