@@ -193,26 +193,8 @@ __device__ __forceinline__ float gelu_sigmoid(float z) {
   return z * __builtin_amdgcn_rcpf(1.0f + __builtin_amdgcn_exp2f(u));
 }
 
-// Where lane group g's two 16-byte halves of k-block kb lie in a row of Kd
-// values, moved to the row's start where they pass its end (v0, v1: inside).
-__device__ __forceinline__ void spans(int kb, int g, int Kd, int& o0, int& o1, bool& v0,
-                                      bool& v1) {
-  const int a = kb * kBlk + 16 * g, b = a + 64;
-  v0 = a + 16 <= Kd;
-  v1 = b + 16 <= Kd;
-  o0 = v0 ? a : 0;
-  o1 = v1 ? b : 0;
-}
 __device__ __forceinline__ i32x8 pack8(uint4 a, uint4 b) {
   return i32x8{(int)a.x, (int)a.y, (int)a.z, (int)a.w, (int)b.x, (int)b.y, (int)b.z, (int)b.w};
-}
-__device__ __forceinline__ i32x8 ld32(const uint8_t* row, int o0, int o1) {
-  return pack8(*reinterpret_cast<const uint4*>(row + o0),
-               *reinterpret_cast<const uint4*>(row + o1));
-}
-__device__ __forceinline__ i32x8 keep32(i32x8 v, bool v0, bool v1) {
-  return i32x8{v0 ? v[0] : 0, v0 ? v[1] : 0, v0 ? v[2] : 0, v0 ? v[3] : 0,
-               v1 ? v[4] : 0, v1 ? v[5] : 0, v1 ? v[6] : 0, v1 ? v[7] : 0};
 }
 
 // Four consecutive outputs of a row of N columns from column n.  ONCE: fp32 in
@@ -238,23 +220,63 @@ __device__ __forceinline__ void store4(YT* __restrict__ row, int n, int N, f32x4
 
 // ---------------------------------------------------------------------------
 // Few rows per group: the weights streamed from HBM into registers once per
-// tile of 16 MB rows.  A block is one row tile x WN waves of NC tiles of 16
-// columns (gate_up: NC gate and the matching NC up tiles), times WK waves that
-// split the contraction in 128-blocks and are added through LDS.  Loads run
-// NS - 1 blocks ahead, unconditionally (addresses clamped into their rows), so
-// that a step waits for its own slot alone.
+// tile of 16 rows.  A block is one row tile x WN waves of NC tiles of 16 columns
+// (gate_up: NC gate and the matching NC up tiles), times WK waves that split the
+// contraction in 128-blocks and are added through LDS.  Weight loads run NS - 1
+// blocks ahead, unconditionally (addresses clamped into their rows), so that a
+// step waits for its own slot alone.
+//
+// The codes are widened to bf16 in registers and multiplied by the bf16
+// instruction: the weight stream bounds these kernels, and that instruction adds
+// its products to 2^-25 of their magnitudes where the 8-bit one rounds to about
+// 2^-17 (an E4M3 code of h whose sum lies that near a decision point changes).
+//
+// FUSE: the block quantizes its own rows of x (bf16) or h (fp32) into LDS behind
+// the first weight loads, which saves a launch; otherwise their codes and scales
+// come from memory with the weights.
 // ---------------------------------------------------------------------------
-template <int MODE, int WK, int WN, int MB, int NC, int NS, typename YT>
+__device__ __forceinline__ bf16x8 widen8(uint32_t lo, uint32_t hi) {
+  uint4 w;
+  fp8x4_to_bf16(lo, w.x, w.y);
+  fp8x4_to_bf16(hi, w.z, w.w);
+  return __builtin_bit_cast(bf16x8, w);
+}
+// A lane's 32 codes of a k-block, as loaded: k = 16 g .. + 15, then 64 + 16 g.
+struct Codes {
+  uint4 a, b;
+  __device__ __forceinline__ void load(const uint8_t* row, int kb, int g, int Kd) {
+    // (past the row: its first chunk; the other operand is 0 there)
+    const int o0 = kb * kBlk + 16 * g, o1 = o0 + 64;
+    a = *reinterpret_cast<const uint4*>(row + (o0 < Kd ? o0 : 0));
+    b = *reinterpret_cast<const uint4*>(row + (o1 < Kd ? o1 : 0));
+  }
+  __device__ __forceinline__ void widen(bf16x8 (&v)[4]) const {
+    v[0] = widen8(a.x, a.y);
+    v[1] = widen8(a.z, a.w);
+    v[2] = widen8(b.x, b.y);
+    v[3] = widen8(b.z, b.w);
+  }
+};
+
+constexpr int kFusePad = 16;  // bytes between rows of codes in LDS
+__host__ __device__ constexpr int fuse_bytes(int rows, int KB) {
+  return rows * (KB * kBlk + kFusePad + 4 * KB);
+}
+
+// XT: the type of the rows that FUSE quantizes (void: not fused).
+template <int MODE, int WK, int WN, int NC, int NS, typename XT, typename YT>
 __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
+  constexpr bool FUSE = !std::is_same<XT, void>::value;
   constexpr int NW = MODE == kGateUp ? 2 * NC : NC;  // weight tiles per wave
-  __shared__ f32x4 red[WK > 1 ? WK : 1][WN][MB][NW][WK > 1 ? kWave : 1];
+  __shared__ f32x4 red[WK][WN][NW][WK > 1 ? kWave : 1];
+  extern __shared__ __align__(16) unsigned char smem[];
   int e, row0, row1, cg;
   const int CG = (a.N + 16 * WN * NC - 1) / (16 * WN * NC);
-  if (!stream_item(a.ident, a.rows, a.offsets, a.E, 16 * MB, CG, e, row0, row1, cg)) return;
+  if (!stream_item(a.ident, a.rows, a.offsets, a.E, 16, CG, e, row0, row1, cg)) return;
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
   const int wk = wave % WK, wn = wave / WK;
   const int fr = lane % 16, g = lane / 16;
-  const int Kd = a.Kd, KB = blocks_of(Kd);
+  const int Kd = a.Kd, KB = blocks_of(Kd), pitch = KB * kBlk;
   const int NR = MODE == kGateUp ? 2 * a.N : a.N;
   const int n0 = (cg * WN + wn) * 16 * NC;
   const uint8_t* wrow[NW];
@@ -267,77 +289,92 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
     wsc[c] = a.wscale +
              ((long long)e * blocks_of(NR) + (up + min(first, a.N - 1)) / kBlk) * KB;
   }
-  const int nmb = (row1 - row0 + 15) / 16;
-  const uint8_t* xrow[MB];
-  const float* xsc[MB];
+  const int kb0 = wk * KB / WK, kb1 = (wk + 1) * KB / WK, last = max(kb1 - 1, 0);
+  Codes rw[NS][NW], rx[NS];
+  float sw[NS][NW], sx[NS];
+  auto load_w = [&](int kb, int slot) {
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    const int r = row0 + 16 * mb + fr;
-    long long t = r < row1 ? r : row0;
-    if (MODE == kGateUp) t = a.sorted_slots[t] / a.K;
-    xrow[mb] = a.xq + t * (KB * kBlk);
-    xsc[mb] = a.xscale + t * KB;
-  }
-  const int kb0 = wk * KB / WK, kb1 = (wk + 1) * KB / WK;
-
-  f32x4 acc[MB][NW];
-#pragma unroll
-  for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-    for (int c = 0; c < NW; ++c) acc[mb][c] = f32x4{0, 0, 0, 0};
-  i32x8 rx[NS][MB], rw[NS][NW];
-  float sx[NS][MB], sw[NS][NW];
-  auto load = [&](int kb, int slot) {
-    int o0, o1;
-    bool v0, v1;
-    spans(kb, g, Kd, o0, o1, v0, v1);
-#pragma unroll
-    for (int c = 0; c < NW; ++c) rw[slot][c] = ld32(wrow[c], o0, o1);
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-      rx[slot][mb] = ld32(xrow[mb], o0, o1);
-      sx[slot][mb] = xsc[mb][kb];
-    }
+    for (int c = 0; c < NW; ++c) rw[slot][c].load(wrow[c], kb, g, Kd);
 #pragma unroll
     for (int c = 0; c < NW; ++c) sw[slot][c] = wsc[c][kb];
   };
-  auto step = [&](int slot, int kb, auto checked) {
-    if (decltype(checked)::value && (kb + 1) * kBlk > Kd) {  // uniform
-      int o0, o1;
-      bool v0, v1;
-      spans(kb, g, Kd, o0, o1, v0, v1);
-#pragma unroll
-      for (int mb = 0; mb < MB; ++mb) rx[slot][mb] = keep32(rx[slot][mb], v0, v1);
-#pragma unroll
-      for (int c = 0; c < NW; ++c) rw[slot][c] = keep32(rw[slot][c], v0, v1);
-    }
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-      if (mb == 0 || mb < nmb) {
-        f32x4 d[NW];
-#pragma unroll
-        for (int c = 0; c < NW; ++c) d[c] = mfma_blk(rw[slot][c], rx[slot][mb]);
-#pragma unroll
-        for (int c = 0; c < NW; ++c) {
-          const float s = sx[slot][mb] * sw[slot][c];
-#pragma unroll
-          for (int r = 0; r < 4; ++r) acc[mb][c][r] = __builtin_fmaf(d[c][r], s, acc[mb][c][r]);
-        }
-      }
-  };
+  // a wave without a k-block loads a valid one and never uses it
 #pragma unroll
   for (int s = 0; s < NS - 1; ++s) {
-    load(max(min(kb0 + s, kb1 - 1), 0), s);
+    load_w(min(kb0 + s, last), s);
     __builtin_amdgcn_sched_barrier(0);
   }
+
+  const int nrow = row1 - row0;
+  const uint8_t* xrow;
+  const float* xsc;
+  if constexpr (FUSE) {
+    uint8_t* xl = smem;
+    float* sl = reinterpret_cast<float*>(smem + nrow * (pitch + kFusePad));
+    const int l = threadIdx.x % 16;
+    for (int k = threadIdx.x / 16; k < nrow * KB; k += 4 * WK * WN) {  // 16 lanes alike
+      const int r = k / KB, kb = k % KB, c = kb * kBlk + 8 * l;
+      long long t = row0 + r;
+      if (MODE == kGateUp) t = a.sorted_slots[t] / a.K;
+      float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+      if (c < Kd) ld8(static_cast<const XT*>(a.x) + t * Kd + c, v);
+      const float s = row16_max(amax8(v)) * kInvE4m3Max;
+      if (l == 0) sl[r * KB + kb] = s;
+      *reinterpret_cast<uint2*>(xl + r * (pitch + kFusePad) + c) = encode8(v, s);
+    }
+    __syncthreads();
+    xrow = xl + min(fr, nrow - 1) * (pitch + kFusePad);
+    xsc = sl + min(fr, nrow - 1) * KB;
+  } else {
+    long long t = row0 + min(fr, nrow - 1);
+    if (MODE == kGateUp) t = a.sorted_slots[t] / a.K;
+    xrow = a.xq + t * pitch;
+    xsc = a.xscale + t * KB;
+#pragma unroll
+    for (int s = 0; s < NS - 1; ++s) {
+      rx[s].load(xrow, min(kb0 + s, last), g, pitch);
+      sx[s] = xsc[min(kb0 + s, last)];
+    }
+  }
+
+  f32x4 acc[NW];
+#pragma unroll
+  for (int c = 0; c < NW; ++c) acc[c] = f32x4{0, 0, 0, 0};
+  auto load = [&](int kb, int slot) __attribute__((always_inline)) {
+    load_w(kb, slot);
+    if constexpr (!FUSE) {
+      rx[slot].load(xrow, kb, g, pitch);
+      sx[slot] = xsc[kb];
+    }
+  };
+  auto step = [&](int kb, int slot) __attribute__((always_inline)) {
+    if constexpr (FUSE) {
+      rx[slot].load(xrow, kb, g, pitch);
+      sx[slot] = xsc[kb];
+    }
+    bf16x8 xv[4];
+    rx[slot].widen(xv);
+#pragma unroll
+    for (int c = 0; c < NW; ++c) {
+      bf16x8 wv[4];
+      rw[slot][c].widen(wv);
+      f32x4 d = {0, 0, 0, 0};
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+        d = __builtin_amdgcn_mfma_f32_16x16x32_bf16(wv[q], xv[q], d, 0, 0, 0);
+      const float sc = sx[slot] * sw[slot][c];
+#pragma unroll
+      for (int r = 0; r < 4; ++r) acc[c][r] = __builtin_fmaf(d[r], sc, acc[c][r]);
+    }
+  };
   int kb = kb0;
-  const int kbf = min(kb1, Kd / kBlk);
-  for (; kb + 2 * NS - 2 < kbf; kb += NS) {
+  // every load of the unrolled NS steps lies inside the wave's range
+  for (; kb + 2 * NS - 2 < kb1; kb += NS) {
 #pragma unroll
     for (int s = 0; s < NS; ++s) {
       load(kb + s + NS - 1, (s + NS - 1) % NS);
       __builtin_amdgcn_sched_barrier(0);
-      step(s, kb + s, std::false_type{});
+      step(kb + s, s);
       __builtin_amdgcn_sched_barrier(0);
     }
   }
@@ -346,49 +383,43 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
     for (int s = 0; s < NS; ++s) {
       if (kb + s >= kb1) break;
       if (kb + s + NS - 1 < kb1) load(kb + s + NS - 1, (s + NS - 1) % NS);
-      step(s, kb + s, std::true_type{});
+      step(kb + s, s);
     }
   }
   if constexpr (WK > 1) {
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-      for (int c = 0; c < NW; ++c) red[wk][wn][mb][c][lane] = acc[mb][c];
+    for (int c = 0; c < NW; ++c) red[wk][wn][c][lane] = acc[c];
     __syncthreads();
   }
   // the WK waves of a column group take its tiles in turn
+  const int row = row0 + fr;
 #pragma unroll
-  for (int mb = 0; mb < MB; ++mb) {
-    if (mb >= nmb) break;
-    const int row = row0 + 16 * mb + fr;
+  for (int c = 0; c < NC; ++c) {
+    if (WK > 1 && c % WK != wk) continue;
+    const int n = n0 + 16 * c + 4 * g;
+    f32x4 v = acc[c], u = {0, 0, 0, 0};
+    if constexpr (MODE == kGateUp) u = acc[NC + c];
+    if constexpr (WK > 1) {
+      v = red[0][wn][c][lane];
+      if constexpr (MODE == kGateUp) u = red[0][wn][NC + c][lane];
 #pragma unroll
-    for (int c = 0; c < NC; ++c) {
-      if (WK > 1 && (mb * NC + c) % WK != wk) continue;
-      const int n = n0 + 16 * c + 4 * g;
-      f32x4 v = acc[mb][c], u = {0, 0, 0, 0};
-      if constexpr (MODE == kGateUp) u = acc[mb][NC + c];
-      if constexpr (WK > 1) {
-        v = red[0][wn][mb][c][lane];
-        if constexpr (MODE == kGateUp) u = red[0][wn][mb][NC + c][lane];
-#pragma unroll
-        for (int w = 1; w < WK; ++w) {
-          v += red[w][wn][mb][c][lane];
-          if constexpr (MODE == kGateUp) u += red[w][wn][mb][NC + c][lane];
-        }
+      for (int w = 1; w < WK; ++w) {
+        v += red[w][wn][c][lane];
+        if constexpr (MODE == kGateUp) u += red[w][wn][NC + c][lane];
       }
-      if (row >= row1) continue;
-      if constexpr (MODE == kGateUp) {
+    }
+    if (row >= row1) continue;
+    if constexpr (MODE == kGateUp) {
 #pragma unroll
-        for (int r = 0; r < 4; ++r) v[r] = gelu_sigmoid(v[r]) * u[r];
-        store4(a.h + (size_t)row * a.N, n, a.N, v);
-      } else {
-        size_t to = row;
-        if (!a.ident) {
-          to = a.sorted_slots[row];
-          v *= a.topk_w[to];
-        }
-        store4(static_cast<YT*>(a.y) + to * a.N, n, a.N, v);
+      for (int r = 0; r < 4; ++r) v[r] = gelu_sigmoid(v[r]) * u[r];
+      store4(a.h + (size_t)row * a.N, n, a.N, v);
+    } else {
+      size_t to = row;
+      if (!a.ident) {
+        to = a.sorted_slots[row];
+        v *= a.topk_w[to];
       }
+      store4(static_cast<YT*>(a.y) + to * a.N, n, a.N, v);
     }
   }
 }
@@ -747,12 +778,14 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
   }
 }
 
-template <int MODE, int WK, int WN, int MB, int NC, int NS, typename YT>
+template <int MODE, int WK, int WN, int NC, int NS, typename XT, typename YT>
 hipError_t launch_stream(const B128Args& a, hipStream_t s) {
   const long long cgs = (a.N + 16 * WN * NC - 1) / (16 * WN * NC);
-  const long long grid = cgs * tile_count_bound(a.ident, a.rows, a.T, a.E, 16 * MB);
-  hipLaunchKernelGGL((stream_b128_kernel<MODE, WK, WN, MB, NC, NS, YT>), dim3((unsigned)grid),
-                     dim3(64 * WK * WN), 0, s, a);
+  const long long grid = cgs * tile_count_bound(a.ident, a.rows, a.T, a.E, 16);
+  const int lds = std::is_same<XT, void>::value
+                      ? 0 : fuse_bytes(a.T < 16 ? a.T : 16, blocks_of(a.Kd));
+  hipLaunchKernelGGL((stream_b128_kernel<MODE, WK, WN, NC, NS, XT, YT>), dim3((unsigned)grid),
+                     dim3(64 * WK * WN), lds, s, a);
   return hipGetLastError();
 }
 
@@ -828,14 +861,35 @@ static bool linear_takes_small(long long rows, long long cols) {
   return s < 8.0 * ((wide + 255) / 256);
 }
 
+// Whether the streaming blocks quantize their own rows: few enough of them that
+// the repeated work costs less than the launch it saves (T <= most), and their
+// codes fit in LDS beside the partial sums (48 KB).  26B-A4B gate_up: experts at
+// 4 / 8 / 16 tokens 44 / 67 / 101 us fused, 51 / 67 / 94 us not; a 2112 x 2816
+// product at 8 / 16 tokens 11.1 / 17.5 and 11.3 / 10.8 us.  down's rows are short
+// (704 values): fused at every streamed size (64 tokens 60 -> 55 us with the
+// quantizer).
+constexpr int kFuseGateUpTokens = 4, kFuseLinearTokens = 8;
+static bool fuses(int T, int Kd, int most) {
+  return T <= most && fuse_bytes(T < 16 ? T : 16, blocks_of(Kd)) <= 48 * 1024;
+}
+
+template <typename XT>
+static hipError_t stream_linear(const B128Args& a, bool y_bf16, hipStream_t s) {
+  return y_bf16 ? launch_stream<kPlain, 4, 1, 1, 3, XT, bf16>(a, s)
+                : launch_stream<kPlain, 4, 1, 1, 3, XT, float>(a, s);
+}
+
 // x quantized, y = x W^T.
 hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, float* xscale,
                               bool y_bf16, hipStream_t s) {
+  if (fuses(a.rows, a.Kd, kFuseLinearTokens)) {
+    B128Args f = a;
+    f.x = x;
+    return stream_linear<bf16>(f, y_bf16, s);
+  }
   hipError_t e = quantize_rows<bf16, true>(a.rows, a.Kd, x, xq, xscale, s);
   if (e != hipSuccess) return e;
-  if (a.rows <= 128)
-    return y_bf16 ? launch_stream<kPlain, 4, 1, 1, 1, 2, bf16>(a, s)
-                  : launch_stream<kPlain, 4, 1, 1, 1, 2, float>(a, s);
+  if (a.rows <= 128) return stream_linear<void>(a, y_bf16, s);
   if (linear_takes_small(a.rows, a.N))
     return y_bf16 ? launch_small<bf16>(a, s) : launch_small<float>(a, s);
   return y_bf16 ? launch_wide<kPlain, bf16>(a, s) : launch_wide<kPlain, float>(a, s);
@@ -843,17 +897,42 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
 
 // x quantized; h = GELU(gate) * up, quantized; y = topk_w * down h.  gu and dn
 // are the two products' arguments.
+// Four waves of one column tile, two k-blocks deep (26B-A4B at 64 tokens: 54.6
+// us; two tiles a wave 54.4, deeper rings 55 to 60, eight waves 55.9).
+template <typename XT>
+static hipError_t stream_down(const B128Args& a, bool y_bf16, hipStream_t s) {
+  return y_bf16 ? launch_stream<kPlain, 1, 4, 1, 2, XT, bf16>(a, s)
+                : launch_stream<kPlain, 1, 4, 1, 2, XT, float>(a, s);
+}
+
 hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,
                                   uint8_t* xq, float* xscale, bool y_bf16, hipStream_t s) {
-  hipError_t e = quantize_rows<bf16, true>(gu.T, gu.Kd, x, xq, xscale, s);
-  if (e != hipSuccess) return e;
+  hipError_t e;
   if (b128_streams(gu.T, gu.rows, gu.E)) {
-    if ((e = launch_stream<kGateUp, 4, 1, 1, 2, 2, float>(gu, s)) != hipSuccess) return e;
+    B128Args f = gu;
+    f.x = x;
+    if (fuses(gu.T, gu.Kd, kFuseGateUpTokens)) {
+      // eight waves a block where the blocks do not fill the CUs (1 token: 13.4 ->
+      // 11.7 us), else four (4 tokens: 51 -> 44 us with down and combine)
+      const long long blocks = (long long)tile_count_bound(false, gu.rows, gu.T, gu.E, 16) *
+                               ((gu.N + 31) / 32);
+      e = blocks <= 256 ? launch_stream<kGateUp, 8, 1, 2, 3, bf16, float>(f, s)
+                        : launch_stream<kGateUp, 4, 1, 2, 2, bf16, float>(f, s);
+    } else {
+      if ((e = quantize_rows<bf16, true>(gu.T, gu.Kd, x, xq, xscale, s)) != hipSuccess) return e;
+      e = launch_stream<kGateUp, 4, 1, 2, 2, void, float>(gu, s);
+    }
+    if (e != hipSuccess) return e;
+    if (fuses(dn.T, dn.Kd, kB128StreamTokens)) {
+      B128Args h = dn;
+      h.x = gu.h;
+      return stream_down<float>(h, y_bf16, s);
+    }
     if ((e = quantize_rows<float, true>(gu.rows, gu.N, gu.h, gu.hq, gu.hscale, s)) != hipSuccess)
       return e;
-    return y_bf16 ? launch_stream<kPlain, 1, 4, 1, 1, 2, bf16>(dn, s)
-                  : launch_stream<kPlain, 1, 4, 1, 1, 2, float>(dn, s);
+    return stream_down<void>(dn, y_bf16, s);
   }
+  if ((e = quantize_rows<bf16, true>(gu.T, gu.Kd, x, xq, xscale, s)) != hipSuccess) return e;
   if ((e = launch_wide<kGateUp, float>(gu, s)) != hipSuccess) return e;
   // down: the small tiles while an expert has fewer than some 96 rows on average
   // (26B-A4B experts and combine at 512 / 1024 / 2048 / 4096 tokens: 225 / 255 /

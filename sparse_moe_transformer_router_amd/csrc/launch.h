@@ -247,6 +247,7 @@ struct B128Args {
   int Kd;                      // contraction length, a multiple of 16
   int N;                       // output columns (gate_up: the expert width)
   bool ident;
+  const void* x;               // [., Kd] rows to quantize in the kernel: bf16, or fp32 h (down)
   const uint8_t* xq;           // [., Kd rounded up to 128] codes of the input rows, zeros past Kd
   const float* xscale;         // [., ceil(Kd / 128)]
   const uint8_t* wq;           // [E, N or 2N, Kd]
