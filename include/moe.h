@@ -429,9 +429,9 @@ int moe_dequantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t
 /* y[t, n] = sum_k X[t, k] W[n, k], X what moe_quantize_b128(1, ...) makes of x
  * [T, in_features] bf16 (done inside the call), W the value of the weights
  * w_q [out_features, in_features], w_scale as above.  y [T, out_features] in
- * y_dtype.  Products of a 128-block accumulate inside the 8-bit matrix
- * instruction (off by at most 2^-12 of the sum of the magnitudes it adds, some
- * 2^-19 in the root mean square), the blocks in fp32.  T up to 65536, out_features up to
+ * y_dtype.  Blocks add up in fp32; a block's 128 products, in large
+ * batches, inside the 8-bit matrix instruction (off by at most 2^-12 of the sum
+ * of their magnitudes, some 2^-19 in the root mean square).  T up to 65536, out_features up to
  * 262144, in_features a multiple of 16 up to 16384.  ws:
  * moe_linear_b128_workspace_size(T, in_features) bytes, 256-byte aligned (0: the
  * sizes are not supported). */
@@ -445,8 +445,11 @@ int moe_linear_b128(int32_t T, int32_t out_features, int32_t in_features, const 
  * fp32 value, and the weights (gate_up [E, 2I, H] with scales [E, ceil(2I / 128),
  * ceil(H / 128)], down [E, H, I] with scales [E, ceil(H / 128), ceil(I / 128)])
  * multiplied in 8 bits.  act dtype bf16; every dims and T that moe_expert_ffn
- * takes.  Up to 256 tokens with at most 16 rows per expert on average the
- * weights are streamed per row tile, larger batches take tiled grouped GEMMs. */
+ * takes.  Up to 256 tokens the weights are streamed per tile of 16 rows, while
+ * experts have one tile on average or few bytes to read again, and widened to
+ * bf16 for the products; larger batches take tiled grouped GEMMs on the 8-bit
+ * instruction, whose sums of 128 products are off by at most 2^-12 of their
+ * magnitudes. */
 int moe_expert_ffn_b128(const moe_dims* dims, int32_t T, const void* x,
                         const uint8_t* w_gate_up_q, const float* w_gate_up_scale,
                         const uint8_t* w_down_q, const float* w_down_scale, const float* topk_w,

@@ -846,7 +846,14 @@ hipError_t launch_dequantize_b128(int block_rows, long long batch, int rows, int
   return hipGetLastError();
 }
 
-bool b128_streams(int T, int rows, int E) { return T <= kB128StreamTokens && rows <= 16 * E; }
+// Streaming where an expert's rows fill one 16-row tile on average, or where
+// reading the weights again for every further tile costs little: at most 96 MB
+// (8 experts of 2816 x 704, top 8: 24 tokens 35 us streamed, 43 tiled; 64 tokens
+// 51 and 45; of 1024 x 256, top 4: 256 tokens 27 and 34).
+bool b128_streams(int T, int rows, int E, int H, int I) {
+  const long long again = (long long)E * ((rows + 16 * E - 1) / (16 * E) - 1) * 3 * H * I;
+  return T <= kB128StreamTokens && again <= 96LL << 20;
+}
 
 // Whether a product of one group takes the 128 x 128 tiles: by the rounds of
 // blocks that each shape needs.  A round of 256 wide tiles takes some 8 units, of
@@ -889,7 +896,10 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
   }
   hipError_t e = quantize_rows<bf16, true>(a.rows, a.Kd, x, xq, xscale, s);
   if (e != hipSuccess) return e;
-  if (a.rows <= 128) return stream_linear<void>(a, y_bf16, s);
+  // streamed while all the row tiles together read at most 48 MB of weights
+  // (2112 x 2816: 128 tokens 19.5 us streamed, 24.6 tiled, 256 tokens 30.4 and
+  // 25.0; 704 x 704: 512 tokens 10.0 and 13.1, 1024 tokens 14.0 and 13.4)
+  if ((a.rows + 15LL) / 16 * a.N * a.Kd <= 48LL << 20) return stream_linear<void>(a, y_bf16, s);
   if (linear_takes_small(a.rows, a.N))
     return y_bf16 ? launch_small<bf16>(a, s) : launch_small<float>(a, s);
   return y_bf16 ? launch_wide<kPlain, bf16>(a, s) : launch_wide<kPlain, float>(a, s);
@@ -908,7 +918,7 @@ static hipError_t stream_down(const B128Args& a, bool y_bf16, hipStream_t s) {
 hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,
                                   uint8_t* xq, float* xscale, bool y_bf16, hipStream_t s) {
   hipError_t e;
-  if (b128_streams(gu.T, gu.rows, gu.E)) {
+  if (b128_streams(gu.T, gu.rows, gu.E, gu.Kd, gu.N)) {
     B128Args f = gu;
     f.x = x;
     if (fuses(gu.T, gu.Kd, kFuseGateUpTokens)) {

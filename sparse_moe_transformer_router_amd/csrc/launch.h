@@ -262,7 +262,7 @@ struct B128Args {
 };
 // Few rows per group: the weight-streaming kernels; h then goes through fp32.
 constexpr int kB128StreamTokens = 256;
-bool b128_streams(int T, int rows, int E);
+bool b128_streams(int T, int rows, int E, int H, int I);
 hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, float* xscale,
                               bool y_bf16, hipStream_t s);
 hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,

@@ -91,7 +91,8 @@ def _check_linear(x, q, s, y):
     (37, 1003, 1520), (64, 704, 2816), (127, 130, 704), (128, 96, 2960), (129, 97, 2960),
     (200, 1003, 208), (257, 257, 128), (300, 513, 6016), (513, 1, 16), (640, 2816, 704),
     (1025, 130, 2944),
-    (260, 130, 2816), (260, 130, 5632)])
+    (260, 130, 2816), (260, 130, 5632), (2, 40, 16384), (3, 40, 16384), (5, 70, 6016),
+    (8, 70, 6016), (9, 70, 512), (2500, 65, 64), (700, 1408, 1408)])
 def test_linear(T, N, K):
     """One k-block and many (up to, at and past the 22 whose scales a tile
     holds), partial ones, single rows and columns, both forms."""
@@ -177,10 +178,12 @@ def _check_experts(x, guq, gus, dnq, dns, idx, w, y, out):
     (1, 64, 1, 1, 32), (1, 256, 8, 8, 160), (2, 128, 4, 1, 96), (5, 192, 16, 3, 96),
     (37, 192, 16, 3, 96), (40, 320, 6, 2, 224), (200, 512, 128, 8, 64), (256, 64, 256, 16, 32),
     (257, 64, 256, 4, 32), (90, 320, 2, 2, 160), (300, 256, 8, 2, 192), (700, 192, 5, 1, 96),
-    (1100, 2816, 3, 2, 704), (520, 8192, 2, 1, 288)])
+    (1100, 2816, 3, 2, 704), (520, 8192, 2, 1, 288), (200, 2816, 3, 3, 704),
+    (20, 64, 4, 2, 3200), (4, 8192, 3, 2, 32), (3, 2816, 4, 4, 704)])
 def test_experts(T, H, E, K, I):
-    """Both forms, ragged widths (up rows that start inside a block), one row to
-    many per expert, more k-blocks than a tile holds scales for."""
+    """Both forms, with the quantizers inside the products and before them, ragged
+    widths (up rows that start inside a block), one row to many per expert, more
+    k-blocks than a tile holds scales for."""
     g = _gen(T + H + I)
     x = _x(g, T, H)
     guq, gus = _weights(g, E, 2 * I, H, std=1.0 / H ** 0.5)
