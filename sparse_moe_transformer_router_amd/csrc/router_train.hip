@@ -63,6 +63,12 @@ __device__ __forceinline__ void load_logits4(const float* __restrict__ row, int 
   for (int j = 0; j < 4; ++j) l[j] = e0 + j < E ? row[e0 + j] : -INFINITY;
 }
 
+// exp(x), x <= 0, on the hardware's power of two: the product's rounding moves the
+// result by |x| 2^-24, as much as the rounding of l - max did.
+__device__ __forceinline__ float exp_neg(float x) {
+  return __builtin_amdgcn_exp2f(x * 1.4426950408889634f);
+}
+
 // Softmax numerators of a token's logits: l becomes exp(l - max), z their sum
 // over the group, lse the row's log-sum-exp.  A row of -inf only has no
 // probability anywhere: z is 0 and inv (1 / z) and lse are 0.
@@ -73,7 +79,7 @@ __device__ __forceinline__ void group_softmax(float (&l)[4], float& inv, float& 
   float z = 0.0f;
 #pragma unroll
   for (int j = 0; j < 4; ++j) {
-    l[j] = none ? 0.0f : expf(l[j] - top);
+    l[j] = none ? 0.0f : exp_neg(l[j] - top);
     z += l[j];
   }
   z = group_sum<G>(z);
@@ -167,6 +173,13 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
     float acc[4] = {0.0f, 0.0f, 0.0f, 0.0f};
     float zsum = 0.0f;
     int live = 0;
+    float next[kBalUnroll][4];
+    auto load = [&](int t) {
+#pragma unroll
+      for (int u = 0; u < kBalUnroll; ++u)
+        load_logits4<VEC>(logits + (size_t)min(t + u * TB, t1 - 1) * E, 4 * gl, E, next[u]);
+    };
+    if (t0 + grp < t1) load(t0 + grp);
     for (int t = t0 + grp; t < t1; t += TB * kBalUnroll) {
       float l[kBalUnroll][4];
       bool on[kBalUnroll];
@@ -174,8 +187,10 @@ __global__ __launch_bounds__(kBalThreads) void balance_partial_kernel(
       for (int u = 0; u < kBalUnroll; ++u) {
         const int tu = min(t + u * TB, t1 - 1);
         on[u] = t + u * TB < t1 && (mask == nullptr || mask[tu] != 0);
-        load_logits4<VEC>(logits + (size_t)tu * E, 4 * gl, E, l[u]);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) l[u][j] = next[u][j];
       }
+      if (t + TB * kBalUnroll < t1) load(t + TB * kBalUnroll);
 #pragma unroll
       for (int u = 0; u < kBalUnroll; ++u) {
         float inv, lse;
@@ -363,7 +378,7 @@ void by_group(int E, F go) {
 // d_k = d_topk_w_k * per_expert_scale), plus the given d_logits; the two
 // norms; dl', beta, and the block's sums of d_topk_w_k q_k per expert.
 // ---------------------------------------------------------------------------
-constexpr int kRgRowWaves = 4;
+constexpr int kRgRowWaves = 16;  // a token each
 
 __device__ __forceinline__ void load8f(const float* p, float (&v)[8]) {
   const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
@@ -465,7 +480,7 @@ __device__ __forceinline__ void router_grad_token(
   }
   if (d_w != nullptr) {
     const float top = group_max<kWave>(lk);
-    float q = lk == -INFINITY ? 0.0f : expf(lk - top);
+    float q = lk == -INFINITY ? 0.0f : exp_neg(lk - top);
     const float z = group_sum<kWave>(q);
     q = z > 0.0f ? q / z : 0.0f;
     const float d = e >= 0 ? dw * pk : 0.0f;
@@ -674,26 +689,32 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f32(a[i][k], b[k][j], acc[i][j]);
   }
+  // a tile's loads all before its first store
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int h = h0 + 32 * j + c;
     const float gn = pre_gain != nullptr ? pre_gain[h] : 1.0f;
     const float gc = gn * scale[h], ge = pre_gain != nullptr ? gn * gn + eps : 1.0f;
 #pragma unroll
-    for (int i = 0; i < 2; ++i)
+    for (int i = 0; i < 2; ++i) {
+      float xv[16], be[16];
+      bool on[16];
+#pragma unroll
+      for (int q = 0; q < 16; ++q) {
+        const int t = min(t0 + 32 * i + mfma_row(q, g), T - 1);
+        on[q] = mask == nullptr || mask[t] != 0;
+        be[q] = beta[t];
+        xv[q] = x[(size_t)t * H + h];
+      }
 #pragma unroll
       for (int q = 0; q < 16; ++q) {
         const int t = t0 + 32 * i + mfma_row(q, g);
-        if (t >= T) continue;
-        const bool live = mask == nullptr || mask[t] != 0;
-        const size_t at = (size_t)t * H + h;
-        dx[at] = live ? gc * acc[i][j][q] - x[at] * (beta[t] * ge) : 0.0f;
+        if (t < T)
+          dx[(size_t)t * H + h] = on[q] ? gc * acc[i][j][q] - xv[q] * (be[q] * ge) : 0.0f;
       }
+    }
   }
 }
-
-// Splits of the tokens for G: one per 64 tokens, 8 at most.
-constexpr int kRgMinSpan = 64;
 
 // ---------------------------------------------------------------------------
 // bf16 inputs: both products on bf16 matrix instructions (16x16x32: lane l holds
@@ -735,7 +756,7 @@ __device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
   c = (bf16)(r - (float)b);
 }
 
-__global__ __launch_bounds__(kRgRowThreads, 8) void router_grad_rows_bf16_kernel(
+__global__ __launch_bounds__(kRgRowThreads) void router_grad_rows_bf16_kernel(
     int T, int H, int E, int K, float eps, const bf16* __restrict__ x,
     const float* __restrict__ pre_gain, const float* __restrict__ pes,
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
@@ -831,7 +852,10 @@ __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
 // G partial: a wave takes 16 MT experts x 64 columns of x over a quarter of the
 // split's 32-token steps.  x rows are loaded as they lie, four columns of eight
 // tokens a lane, and regrouped in registers: fragment i holds columns 4 (l % 16)
-// + i, so a lane's four results of a row are consecutive columns.
+// + i, so a lane's four results of a row are consecutive columns.  The next
+// step's x and parts of dl' are fetched during a step's products; what is left
+// is their latency (two column groups a block, which halves what L2 delivers,
+// took as long).
 template <int MT, bool MASK>
 __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
     int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
@@ -867,17 +891,23 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
       raw[j] = *reinterpret_cast<const uint2*>(x + (size_t)t * H + h0 + 4 * c);
     }
   };
-  bf16x8 fa[2][3];
-  auto load_a = [&](int s, int m, bf16x8 (&f)[3]) {
-    const bf16* p = cols + ((size_t)s * MS + min(m0 + m, MS - 1)) * 3 * kFrag + 8 * lane;
+  bf16x8 fa[2][MT][3];
+  auto load_a = [&](int s, bf16x8 (&f)[MT][3]) __attribute__((always_inline)) {
 #pragma unroll
-    for (int q = 0; q < 3; ++q) f[q] = *reinterpret_cast<const bf16x8*>(p + q * kFrag);
+    for (int m = 0; m < MT; ++m) {
+      const bf16* p = cols + ((size_t)s * MS + min(m0 + m, MS - 1)) * 3 * kFrag + 8 * lane;
+#pragma unroll
+      for (int q = 0; q < 3; ++q) f[m][q] = *reinterpret_cast<const bf16x8*>(p + q * kFrag);
+    }
   };
   if (a0 < a1) {
     load_x(a0);
-    load_a(a0, 0, fa[0]);
+    load_a(a0, fa[0]);
   }
-  for (int s = a0; s < a1; ++s) {
+  // one step, its parts in fa[cur]; the next step's x and parts are on their way
+  // during its products
+  auto step = [&](int s, auto cur_tag) __attribute__((always_inline)) {
+    constexpr int now = decltype(cur_tag)::value;
     const int next = min(s + 1, a1 - 1);
     uint2 cur[8];
 #pragma unroll
@@ -890,6 +920,8 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
     }
     const float4 b0 = be4[0], b1 = be4[1];
     load_x(next);
+    load_a(next, fa[1 - now]);
+    __builtin_amdgcn_sched_barrier(0);
     if (beta_here) {
       const float bb[8] = {b0.x, b0.y, b0.z, b0.w, b1.x, b1.y, b1.z, b1.w};
 #pragma unroll
@@ -920,17 +952,16 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
     }
 #pragma unroll
     for (int m = 0; m < MT; ++m) {
-      // the next tile's parts are on their way during this one's products
-      if (m + 1 < MT) load_a(s, m + 1, fa[(m + 1) & 1]);
-      else load_a(next, 0, fa[0]);
-      static_assert(MT % 2 == 0, "a step's first tile is in fa[0]");
-      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int q = 0; q < 3; ++q)
 #pragma unroll
-        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(fa[m & 1][q], fb[i], acc[m][i]);
-      __builtin_amdgcn_sched_barrier(0);
+        for (int i = 0; i < 4; ++i) acc[m][i] = mfma_bf16(fa[now][m][q], fb[i], acc[m][i]);
     }
+    __builtin_amdgcn_sched_barrier(0);
+  };
+  for (int s = a0; s < a1; s += 2) {
+    step(s, std::integral_constant<int, 0>{});
+    if (s + 1 < a1) step(s + 1, std::integral_constant<int, 1>{});
   }
   if (beta_here) {
 #pragma unroll
@@ -1068,7 +1099,6 @@ __global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
 // columns a thread and 32 groups of experts; in the blocks past the columns the
 // per-expert scale's gradient from the first kernel's sums.
 constexpr int kRgCols = 32, kRgParts = 32, kRgFinThreads = kRgCols / 4 * kRgParts;
-constexpr int kRgMaxSplits = 8;
 __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
     int H, int E, int splits, int pes_blocks, const float* __restrict__ part_g,
     const float* __restrict__ part_b, const float* __restrict__ part_pes,
@@ -1079,7 +1109,7 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
   const int c = threadIdx.x % (kRgCols / 4), p = threadIdx.x / (kRgCols / 4);
   const int col_blocks = H / kRgCols;
   if ((int)blockIdx.x >= col_blocks) {
-    // eight experts a block, a lane group each
+    // eight experts a block
     const int e = ((int)blockIdx.x - col_blocks) * (kRgCols / 4) + c;
     float s = 0.0f;
     if (e < E) {
@@ -1100,16 +1130,20 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
   const f32x4 gn = pre_gain != nullptr ? *reinterpret_cast<const f32x4*>(pre_gain + h) : one;
   const f32x4 cs = *reinterpret_cast<const f32x4*>(scale + h);
   f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
+  constexpr int U = 5;  // splits loaded before the first is added
 #pragma unroll 2
   for (int e = p; e < E; e += kRgParts) {
-    f32x4 v[kRgMaxSplits];
+    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
+    for (int s0 = 0; s0 < splits; s0 += U) {
+      f32x4 v[U];
 #pragma unroll
-    for (int s = 0; s < kRgMaxSplits; ++s)
-      v[s] = s < splits ? *reinterpret_cast<const f32x4*>(part_g + ((size_t)s * E + e) * H + h)
-                        : f32x4{0.0f, 0.0f, 0.0f, 0.0f};
-    f32x4 sum = v[0];
+      for (int u = 0; u < U; ++u)
+        v[u] = *reinterpret_cast<const f32x4*>(
+            part_g + ((size_t)min(s0 + u, splits - 1) * E + e) * H + h);
 #pragma unroll
-    for (int s = 1; s < kRgMaxSplits; ++s) sum += v[s];
+      for (int u = 0; u < U; ++u)
+        if (s0 + u < splits) sum += v[u];
+    }
     *reinterpret_cast<f32x4*>(dW + (size_t)e * H + h) = sum * gn * cs;
     m += *reinterpret_cast<const f32x4*>(W + (size_t)e * H + h) * sum;
   }
@@ -1117,6 +1151,7 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
   __syncthreads();
   if (p != 0) return;
   m = red[0][c];
+#pragma unroll 8
   for (int i = 1; i < kRgParts; ++i) m += red[i][c];
   *reinterpret_cast<f32x4*>(d_scale + h) = gn * m;
   if (d_gain != nullptr) {
@@ -1131,7 +1166,7 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
 void launch_grad_f32(const RouterGradArgs& a, hipStream_t s) {
   const float* x = static_cast<const float*>(a.x);
   float* dl = static_cast<float*>(a.ws_dl);
-  const int splits = router_grad_splits(a.T);
+  const int splits = router_grad_splits(a.T, a.H, a.E);
   hipLaunchKernelGGL(router_grad_rows_kernel, dim3(router_grad_row_blocks(a.T)),
                      dim3(64 * kRgRowWaves), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
                      a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits, dl,
@@ -1168,7 +1203,7 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   bf16* cols = rows + 2 * Tp * Ep;
   bf16* wt = cols + 3 * Ep * Tp;
   uint8_t* live = reinterpret_cast<uint8_t*>(wt + 2 * a.H * Ep);
-  const int splits = router_grad_splits(a.T), tb = router_grad_row_blocks(a.T);
+  const int splits = router_grad_splits(a.T, a.H, a.E), tb = router_grad_row_blocks(a.T);
   hipLaunchKernelGGL(router_grad_rows_bf16_kernel, dim3(tb + (a.d_x != nullptr ? a.H / kRgWCols : 0)),
                      dim3(kRgRowThreads), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
                      a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits,
@@ -1185,9 +1220,10 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
     if (a.mask != nullptr) gw(mt, std::true_type{});
     else gw(mt, std::false_type{});
   };
+  // 64 experts a wave: with 128 the parts could be fetched one tile ahead only
+  // (20 us at 4096 tokens)
   if (a.E <= 32) by_mask(std::integral_constant<int, 2>{});
-  else if (a.E <= 64) by_mask(std::integral_constant<int, 4>{});
-  else by_mask(std::integral_constant<int, 8>{});
+  else by_mask(std::integral_constant<int, 4>{});
   if (a.d_x != nullptr) {
     constexpr int tok = kRgXWaves * kRgXTok;  // per block
     hipLaunchKernelGGL(router_grad_x_bf16_kernel, dim3(a.H / 64, (a.T + tok - 1) / tok),
@@ -1230,9 +1266,13 @@ hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-int router_grad_splits(int T) {
-  const int n = (T + kRgMinSpan - 1) / kRgMinSpan;
-  return n < 1 ? 1 : n < kRgMaxSplits ? n : kRgMaxSplits;
+// Splits of the tokens for G: one per 64 tokens, as many as two blocks a CU take
+// in one round (26B-A4B shapes: 5), 32 at most.
+int router_grad_splits(int T, int H, int E) {
+  const int blocks = H / 64 * ((E + 63) / 64);
+  const int by_cus = blocks >= 512 ? 1 : 512 / blocks, by_tokens = (T + 63) / 64;
+  const int n = by_cus < by_tokens ? by_cus : by_tokens;
+  return n < 1 ? 1 : n < 32 ? n : 32;
 }
 
 int router_grad_row_blocks(int T) { return (T + 31) / 32 * 32 / kRgTok; }
@@ -1249,7 +1289,7 @@ hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
   }
   constexpr int per = kRgCols / 4;
   hipLaunchKernelGGL(router_grad_finish_kernel, dim3(a.H / kRgCols + (a.E + per - 1) / per),
-                     dim3(kRgFinThreads), 0, s, a.H, a.E, a.T > 0 ? router_grad_splits(a.T) : 0,
+                     dim3(kRgFinThreads), 0, s, a.H, a.E, a.T > 0 ? router_grad_splits(a.T, a.H, a.E) : 0,
                      a.T > 0 ? router_grad_row_blocks(a.T) : 0, a.ws_part_g, a.ws_part_b,
                      a.ws_part_pes, a.router_w, a.router_scale, a.pre_gain, a.d_router_w,
                      a.d_router_scale, a.d_per_expert_scale, a.d_pre_gain);
