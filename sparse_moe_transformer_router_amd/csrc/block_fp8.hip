@@ -425,45 +425,60 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 }
 
 // ---------------------------------------------------------------------------
-// Many rows per group: tiles of 256 rows x 256 weight rows (gate_up: 128 gate
-// and the matching 128 up), 8 waves (2 x 4) of 128 x 64, on k-tiles of one
-// 128-block.  Both operands go global -> LDS directly into two stages of 64
-// KB: stage s is refilled once every wave has read it.  A line is a row's 128
+// Many rows per group: tiles of TM rows x TN weight rows (gate_up: half gate,
+// half the matching up rows), WM x WN waves of 16 TI x 64, on k-tiles of one
+// 128-block.  Both operands go global -> LDS directly, a line being a row's 128
 // bytes; its 16-byte chunk c sits at position c ^ (line % 8), so the 16 rows
-// that a fragment load touches spread over the banks.  The scales of up to
-// kTileBlocks k-blocks sit in LDS beside the ring, reloaded when those are
-// used up.  A wave multiplies one 16-row tile of activations by its four
-// weight tiles, and scales the previous tile's results meanwhile.
+// that a fragment load touches spread over the banks.  The activations have two
+// stages: one is refilled once every wave has read it.  The weights have two as
+// well where waves share them; where none does (WM = 1) a wave copies its own 64
+// rows again as soon as it holds their fragments, into the same lines, and two
+// blocks of 256 columns fit into a CU.  The scales of up to KBS k-blocks sit in
+// LDS beside the ring, reloaded when those are used up.  A wave multiplies one
+// 16-row tile of activations by its four weight tiles, and scales the previous
+// tile's results meanwhile.
+//
+// Bound by the matrix cores' power: at 4096 x 4096 x 16384 a k-block of a 256 x
+// 256 tile takes 1.7 to 1.9 us on every CU at 1.93 GHz; its products alone take
+// 1.1 us (random codes), with the scaling 1.26, and a k-block of a plain E4M3
+// library product of 8192^3 1.64.  At 26B-A4B's 4096 tokens gate_up takes 201 us
+// (1290 TF/s; weights 507 MB) and down 193 us (254 MB of weights, 369 MB of
+// fp32 slots: 3.2 TB/s).
 // ---------------------------------------------------------------------------
-constexpr int kTileBlocks = 22;  // even: a run of k-blocks starts in stage 0
 constexpr int kRowGroup = 4;
 
-// WM x WN waves of 16 TI x 64.
 template <int WM, int WN, int TI>
 struct TileShape {
   static constexpr int TM = WM * TI * 16, TN = WN * 64, NW = WM * WN, THREADS = 64 * NW;
-  static constexpr int STAGE = (TM + TN) * kBlk;
-  static constexpr int COPIES = STAGE / (THREADS * 16);           // per wave and stage
-  static constexpr int XCOPIES = TM * kBlk / (THREADS * 16);      // of them activations
-  static constexpr int SX = 2 * STAGE;                            // [kTileBlocks][TM]
-  static constexpr int SW = SX + kTileBlocks * TM * 4;            // [kTileBlocks][4]
-  static constexpr int TAB = SW + kTileBlocks * 4 * 4;            // rtok, slot, weight
+  static constexpr bool OWN_W = WM == 1;                     // no wave shares its weights
+  static constexpr int XSTAGE = TM * kBlk, WSTAGE = TN * kBlk;
+  static constexpr int XCOPIES = XSTAGE / (THREADS * 16);    // per wave and stage
+  static constexpr int WCOPIES = WSTAGE / (THREADS * 16);
+  static constexpr int KBS = OWN_W ? 16 : 22;                // even: a run starts in stage 0
+  static constexpr int W0 = 2 * XSTAGE;                      // the weights' first line
+  static constexpr int SX = W0 + (OWN_W ? 1 : 2) * WSTAGE;   // [KBS][TM]
+  static constexpr int SW = SX + KBS * TM * 4;               // [KBS][4]
+  static constexpr int TAB = SW + KBS * 4 * 4;               // rtok, slot, weight
   static constexpr int LDS = TAB + 3 * TM * 4;
-  static constexpr int HPITCH = TN / 2 + 4;                       // floats
-  static_assert(XCOPIES * THREADS * 16 == TM * kBlk && COPIES % 4 == 0, "copies cover a stage");
+  static constexpr int HPITCH = TN / 2 + 4;                  // floats
+  static_assert(XCOPIES * THREADS * 16 == XSTAGE && WCOPIES * THREADS * 16 == WSTAGE,
+                "copies cover a stage");
   static_assert(LDS <= 160 * 1024, "LDS per CU");
 };
 typedef TileShape<2, 4, 8> WideTile;    // 256 x 256, one block per CU
+typedef TileShape<1, 4, 8> PairTile;    // 128 x 256, two blocks per CU
 typedef TileShape<2, 2, 4> SmallTile;   // 128 x 128, two blocks per CU
-static_assert(WideTile::TM * WideTile::HPITCH * 4 <= WideTile::TAB,
+static_assert(PairTile::TM * PairTile::HPITCH * 4 <= PairTile::TAB,
               "h is staged over the ring and the scales");
-static_assert(2 * SmallTile::LDS <= 160 * 1024, "two blocks share a CU");
+static_assert(2 * SmallTile::LDS <= 160 * 1024 && 2 * PairTile::LDS <= 160 * 1024,
+              "two blocks share a CU");
 
 template <int MODE, int WM, int WN, int TI, typename YT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) {
   typedef TileShape<WM, WN, TI> S;
   constexpr int TJ = 4;  // weight tiles of 16 rows per wave
-  constexpr int kTM = S::TM, kTN = S::TN, COPIES = S::COPIES;
+  constexpr int kTM = S::TM, kTN = S::TN, XC = S::XCOPIES, WC = S::WCOPIES;
+  constexpr int KBS = S::KBS;
   static_assert(MODE != kGateUp || kTN == 256, "a gate_up tile makes one 128-block of h");
   extern __shared__ __align__(16) unsigned char smem[];
   const int Kd = a.Kd, KB = blocks_of(Kd), N = a.N;
@@ -520,40 +535,45 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
     const int col = min(nbase + n - (up ? kTN / 2 : 0), N - 1);
     return col + (up ? N : 0);
   };
-  // Copy j of wave w fills lines 8 (NW j + w) .. + 7 of a stage: activations for
-  // j < XCOPIES, weights past that.  Byte offsets from the tile's bases: below 2^32 (a
-  // batch's codes of x take 2^30 bytes at most, an expert's weights 2^32).
+  // Copy j of wave w fills lines 8 (NW j + w) .. + 7 of the activations for j <
+  // XC, past that 8 lines of the weights from wl(j - XC) on.  Byte offsets from the
+  // tile's bases: below 2^32 (a batch's codes of x take 2^30 bytes at most, an
+  // expert's weights 2^32).
   // Activation rows end in zeros up to a whole line, so what the weights' part
   // of the last line holds past their row does not matter: their own last
   // chunk, which is a finite number exactly when the output is to be one.
   const int pitch = KB * kBlk;
   const uint8_t* xbase = MODE == kGateUp ? a.xq : a.xq + (long long)row0 * pitch;
-  unsigned src[COPIES];
+  unsigned xsrc[XC], wsrc[WC];
   const int chunk = (lane % 8) ^ (lane / 8);
+  // (with one buffer the wave's own)
+  auto wl = [&](int j) {
+    if (!S::OWN_W) return 8 * (S::NW * j + wave);
+    return MODE == kGateUp ? (j / 4) * (kTN / 2) + wn * 32 + 8 * (j % 4) : wn * 64 + 8 * j;
+  };
 #pragma unroll
-  for (int j = 0; j < COPIES; ++j) {
+  for (int j = 0; j < XC; ++j) {
     const int line = 8 * (S::NW * j + wave) + lane / 8;
-    if (j < S::XCOPIES) {
-      const int row = MODE == kGateUp ? rtok[line] : min(line, row1 - 1 - row0);
-      src[j] = (unsigned)row * (unsigned)pitch;
-    } else {
-      src[j] = (unsigned)wrow(line - kTM) * (unsigned)Kd;
-    }
+    const int row = MODE == kGateUp ? rtok[line] : min(line, row1 - 1 - row0);
+    xsrc[j] = (unsigned)row * (unsigned)pitch;
   }
-  // Quarter p of the copies of k-block kt (past the last one the last again:
-  // bytes that are never read).
-  auto copy = [&](int kt, int st, int p) __attribute__((always_inline)) {
+#pragma unroll
+  for (int j = 0; j < WC; ++j) wsrc[j] = (unsigned)wrow(wl(j) + lane / 8) * (unsigned)Kd;
+  // Copies [j0, j1) of k-block kt, the activations' first (past the last one the
+  // last again: bytes that are never read).
+  auto copy = [&](int kt, int st, int j0, int j1) __attribute__((always_inline)) {
     const int kc = min(kt, KB - 1) * 8 + chunk;
     const unsigned kx = kc * 16, kw = min(kc, Kd / 16 - 1) * 16;
 #pragma unroll
-    for (int j = p * COPIES / 4; j < (p + 1) * COPIES / 4; ++j) {
-#if defined(__HIP_DEVICE_COMPILE__)
-      unsigned char* to = smem + st * S::STAGE + (S::NW * j + wave) * 1024;
-      if (j < S::XCOPIES) lds_copy16(xbase, src[j] + kx, to);
-      else lds_copy16(wbase, src[j] + kw, to);
-#endif
+    for (int j = j0; j < j1; ++j) {
+      if (j < XC)
+        lds_copy16(xbase, xsrc[j] + kx, smem + st * S::XSTAGE + (S::NW * j + wave) * 1024);
+      else
+        lds_copy16(wbase, wsrc[j - XC] + kw,
+                   smem + S::W0 + (S::OWN_W ? 0 : st * S::WSTAGE) + wl(j - XC) * kBlk);
     }
   };
+  constexpr int AHEAD = 2;  // copies of a k-block issued before the one before it is done
   // scales of k-blocks [kb0, kb0 + n): activations [kb][256], weights [kb][4]
   // (gate_up: the gate block and the up rows' two; otherwise the two blocks)
   const float* wsbase = a.wscale + (long long)e * blocks_of(NR) * KB;
@@ -561,8 +581,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
   auto load_scales = [&](int kb0) {
     // all of a thread's loads before the first store: one after the other they
     // had cost 8 us a run
-    constexpr int NX = kTileBlocks * kTM / (S::THREADS);
-    const int n = min(kTileBlocks, KB - kb0);
+    constexpr int NX = KBS * kTM / (S::THREADS);
+    const int n = min(KBS, KB - kb0);
     const int r = tid % kTM, kr = tid / kTM, step = S::THREADS / kTM;
     const float* row = a.xscale + (long long)rtok[r] * KB + kb0;
     float v[NX];
@@ -573,7 +593,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
     const float vw = wsbase[(long long)min(blk, blocks_of(NR) - 1) * KB + kb0 + kw];
 #pragma unroll
     for (int i = 0; i < NX; ++i) s_x[(kr + step * i) * kTM + r] = v[i];
-    if (tid < kTileBlocks * 4) s_w[tid] = vw;
+    if (tid < KBS * 4) s_w[tid] = vw;
   };
   // this wave's weight tiles: their scale slots (the two halves of a gate_up
   // wave, else one), fragment offsets
@@ -589,7 +609,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
   // from its first: activations i * 16 lines, weights as wtile().
   const int xline = wm * TI * 16 + fr;
   const int xoff = xline * kBlk + (g ^ (xline & 7)) * 16;
-  const int wline = kTM + wn * (MODE == kGateUp ? 32 : 64) + fr;
+  const int wline = wn * (MODE == kGateUp ? 32 : 64) + fr;
   const int woff = wline * kBlk + (g ^ (wline & 7)) * 16;
   auto wtile = [](int j) {
     return (MODE == kGateUp ? (j / 2) * (kTN / 2) + (j % 2) * 16 : j * 16) * kBlk;
@@ -603,9 +623,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
 #pragma unroll
     for (int j = 0; j < TJ; ++j) acc[i][j] = f32x4{0, 0, 0, 0};
 
-  // Fragment at a wave's first tile + at, of stage `st`.
-  auto rd = [&](int st, int off, int at) __attribute__((always_inline)) {
-    const unsigned char* p = smem + st * S::STAGE;
+  // Fragment at a wave's first tile + at, of the stage at p.
+  auto rd = [&](const unsigned char* p, int off, int at) __attribute__((always_inline)) {
     return pack8(*reinterpret_cast<const uint4*>(p + off + at),
                  *reinterpret_cast<const uint4*>(p + (off ^ 64) + at));
   };
@@ -623,8 +642,9 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
   };
   auto read_first = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
-    for (int j = 0; j < TJ; ++j) fw[j] = rd(st, woff, wtile(j));
-    fx[0] = rd(st, xoff, 0);
+    for (int j = 0; j < TJ; ++j)
+      fw[j] = rd(smem + S::W0 + (S::OWN_W ? 0 : st * S::WSTAGE), woff, wtile(j));
+    fx[0] = rd(smem + st * S::XSTAGE, xoff, 0);
   };
   // One k-block from stage `st`, its weight fragments in fw and its first
   // activation tile in fx[0]; kl: its place among the staged scales.
@@ -642,12 +662,12 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
     for (int i = 0; i < TV; ++i) {
       sx[i & 1] = s_x[kl * kTM + xline + 16 * i];
       if (i + 1 < TV) {
-        fx[(i + 1) & 1] = rd(st, xoff, (i + 1) * 16 * kBlk);
+        fx[(i + 1) & 1] = rd(smem + st * S::XSTAGE, xoff, (i + 1) * 16 * kBlk);
       } else {
         wait_lds();
         wait_vmem<0>();
         block_barrier();
-        copy(kt + 2, st, 0);
+        copy(kt + 2, st, 0, AHEAD);
         __builtin_amdgcn_sched_barrier(0);
       }
 #pragma unroll
@@ -657,34 +677,38 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
         read_first(1 - st);  // (past the end: never used)
         __builtin_amdgcn_sched_barrier(0);
       }
+      // the other copies in three parts; the products above have waited for the
+      // weights' fragments, so a wave's own lines are free
+      if (S::OWN_W && i == 0) __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
-      for (int p = 1; p < 4; ++p)
-        if (i == (TV >= 4 ? (p - 1) * TV / 8 : 0)) copy(kt + 1, 1 - st, p);
+      for (int p = 0; p < 3; ++p)
+        if (i == (TV >= 4 ? p * TV / 8 : 0))
+          copy(kt + 1, 1 - st, AHEAD + p * (XC + WC - AHEAD) / 3,
+               AHEAD + (p + 1) * (XC + WC - AHEAD) / 3);
       if (i > 0) scale_add(i - 1);
       __builtin_amdgcn_sched_barrier(0);  // no fragment is read further ahead
     }
     scale_add(TV - 1);
   };
   auto loop = [&](auto ti_tag) __attribute__((always_inline)) {
-    for (int k0 = 0; k0 < KB; k0 += kTileBlocks) {
+    for (int k0 = 0; k0 < KB; k0 += KBS) {
       if (k0 > 0) {
         __syncthreads();  // the scales of the k-blocks before are used up
         load_scales(k0);
         __syncthreads();
       }
-      const int n = min(kTileBlocks, KB - k0);
+      const int n = min(KBS, KB - k0);
       for (int kl = 0; kl < n; kl += 2) {
         block(k0 + kl, kl, std::integral_constant<int, 0>{}, ti_tag);
         if (kl + 1 < n) block(k0 + kl + 1, kl + 1, std::integral_constant<int, 1>{}, ti_tag);
       }
     }
   };
-#pragma unroll
-  for (int p = 0; p < 4; ++p) copy(0, 0, p);
+  copy(0, 0, 0, XC + WC);
   load_scales(0);
   wait_vmem<0>();
   __syncthreads();
-  copy(1, 1, 0);
+  copy(1, 1, 0, AHEAD);
   read_first(0);
   // as many tiles as hold the wave's rows (every wave takes part in the copies
   // and barriers)
@@ -750,17 +774,16 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
     // through LDS, 128 rows at a time, so that a wave stores whole rows of the
     // tile (as the results lie, 64 bytes of 16 rows: the stores of fp32 slots
     // took twice the time)
-    constexpr int PITCH = kTN + 4, ROWS = 128, CH = kTN / 4;
+    constexpr int PITCH = kTN + 4, ROWS = S::OWN_W ? 64 : 128, CH = kTN / 4;
     static_assert(ROWS * PITCH * 4 <= S::TAB, "results are staged over the ring and the scales");
     float* ys = reinterpret_cast<float*>(smem);
 #pragma unroll
     for (int pass = 0; pass < kTM / ROWS; ++pass) {
       if (pass > 0) __syncthreads();
-      if (wm * TI * 16 / ROWS == pass) {
 #pragma unroll
-        for (int i = 0; i < TI; ++i) {
-          if (i >= nv) break;
-          float* row = ys + ((wm * TI * 16) % ROWS + 16 * i + fr) * PITCH + wn * 64 + 4 * g;
+      for (int i = 0; i < TI; ++i) {
+        if (i < nv && (wm * TI + i) * 16 / ROWS == pass) {
+          float* row = ys + ((wm * TI + i) * 16 % ROWS + fr) * PITCH + wn * 64 + 4 * g;
 #pragma unroll
           for (int j = 0; j < TJ; ++j) *reinterpret_cast<f32x4*>(row + 16 * j) = acc[i][j];
         }
@@ -803,14 +826,18 @@ hipError_t launch_tile(const B128Args& a, hipStream_t s) {
   hipLaunchKernelGGL(kf, dim3((unsigned)grid), dim3(S::THREADS), S::LDS, s, a);
   return hipGetLastError();
 }
-template <int MODE, typename YT>
-hipError_t launch_wide(const B128Args& a, hipStream_t s) {
-  return launch_tile<MODE, 2, 4, 8, YT>(a, s);
-}
-template <typename YT>
-hipError_t launch_small(const B128Args& a, hipStream_t s) {
-  return launch_tile<kPlain, 2, 2, 4, YT>(a, s);
-}
+template <typename S>
+struct Launch;
+template <int WM, int WN, int TI>
+struct Launch<TileShape<WM, WN, TI>> {
+  static hipError_t plain(const B128Args& a, bool y_bf16, hipStream_t s) {
+    return y_bf16 ? launch_tile<kPlain, WM, WN, TI, bf16>(a, s)
+                  : launch_tile<kPlain, WM, WN, TI, float>(a, s);
+  }
+  static hipError_t gate_up(const B128Args& a, hipStream_t s) {
+    return launch_tile<kGateUp, WM, WN, TI, float>(a, s);
+  }
+};
 
 template <typename XT, bool PAD>
 hipError_t quantize_rows(long long rows, int cols, const void* x, uint8_t* q, float* scale,
@@ -900,13 +927,10 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
   // (2112 x 2816: 128 tokens 19.5 us streamed, 24.6 tiled, 256 tokens 30.4 and
   // 25.0; 704 x 704: 512 tokens 10.0 and 13.1, 1024 tokens 14.0 and 13.4)
   if ((a.rows + 15LL) / 16 * a.N * a.Kd <= 48LL << 20) return stream_linear<void>(a, y_bf16, s);
-  if (linear_takes_small(a.rows, a.N))
-    return y_bf16 ? launch_small<bf16>(a, s) : launch_small<float>(a, s);
-  return y_bf16 ? launch_wide<kPlain, bf16>(a, s) : launch_wide<kPlain, float>(a, s);
+  return linear_takes_small(a.rows, a.N) ? Launch<SmallTile>::plain(a, y_bf16, s)
+                                         : Launch<WideTile>::plain(a, y_bf16, s);
 }
 
-// x quantized; h = GELU(gate) * up, quantized; y = topk_w * down h.  gu and dn
-// are the two products' arguments.
 // Four waves of one column tile, two k-blocks deep (26B-A4B at 64 tokens: 54.6
 // us; two tiles a wave 54.4, deeper rings 55 to 60, eight waves 55.9).
 template <typename XT>
@@ -915,6 +939,8 @@ static hipError_t stream_down(const B128Args& a, bool y_bf16, hipStream_t s) {
                 : launch_stream<kPlain, 1, 4, 1, 2, XT, float>(a, s);
 }
 
+// x quantized; h = GELU(gate) * up, quantized; y = topk_w * down h.  gu and dn
+// are the two products' arguments.
 hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const void* x,
                                   uint8_t* xq, float* xscale, bool y_bf16, hipStream_t s) {
   hipError_t e;
@@ -943,13 +969,15 @@ hipError_t launch_expert_ffn_b128(const B128Args& gu, const B128Args& dn, const 
     return stream_down<void>(dn, y_bf16, s);
   }
   if ((e = quantize_rows<bf16, true>(gu.T, gu.Kd, x, xq, xscale, s)) != hipSuccess) return e;
-  if ((e = launch_wide<kGateUp, float>(gu, s)) != hipSuccess) return e;
-  // down: the small tiles while an expert has fewer than some 96 rows on average
-  // (26B-A4B experts and combine at 512 / 1024 / 2048 / 4096 tokens: 225 / 255 /
-  // 348 / 520 us small, 234 / 264 / 341 / 480 us wide)
-  if (dn.rows < 96LL * dn.E)
-    return y_bf16 ? launch_small<bf16>(dn, s) : launch_small<float>(dn, s);
-  return y_bf16 ? launch_wide<kPlain, bf16>(dn, s) : launch_wide<kPlain, float>(dn, s);
+  // tiles of 128 rows: an expert's last one wastes less than of 256 (experts and
+  // combine at 300 / 1024 / 2048 / 4096 / 8192 tokens 194 / 242 / 324 / 472 / 820
+  // us, with 256 rows 209 / 257 / 342 / 483 / 833, down alike)
+  if ((e = Launch<PairTile>::gate_up(gu, s)) != hipSuccess) return e;
+  // down: 256 rows a tile once an expert has some 192 on average (experts and
+  // combine at 512 / 1024 / 2560 / 4096 / 8192 tokens 224 / 250 / 353 / 470 / 820 us,
+  // with 128 rows 206 / 239 / 343 / 481 / 851)
+  return dn.rows < 192LL * dn.E ? Launch<PairTile>::plain(dn, y_bf16, s)
+                                : Launch<WideTile>::plain(dn, y_bf16, s);
 }
 
 }  // namespace moe
