@@ -418,9 +418,12 @@ int moe_expert_ffn_mx(const moe_dims* dims, int32_t fmt, int32_t T, const void* 
  * ceil(cols / 128)].  scale = max |v| over the block times the fp32 number
  * nearest to 1 / 448, in fp32; code = E4M3 nearest to the fp32 quotient v /
  * scale (ties to the even mantissa, 448 at most); a block of zeros (or one so
- * small that its scale underflows) gets scale 0 and codes 0.
+ * small that its scale underflows) gets scale 0 and codes 0, one that holds a NaN
+ * or an infinity scale NaN (its values are NaN, no other block's).
  * moe_dequantize_b128: the values, fp32 [batch, rows, cols], each product
- * rounded once.  MOE_ERR_ARG for another block_rows, bad sizes or pointers. */
+ * rounded once.  MOE_ERR_ARG for another block_rows, bad sizes or pointers;
+ * MOE_ERR_UNSUPPORTED from 2^28 row pieces of 128 values on (batch * rows *
+ * ceil(cols / 128)). */
 int moe_quantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,
                       const void* w, uint8_t* q, float* scale, void* stream);
 int moe_dequantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols,

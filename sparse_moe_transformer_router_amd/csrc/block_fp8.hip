@@ -42,16 +42,26 @@ __device__ __forceinline__ f32x4 mfma_blk(i32x8 w, i32x8 x) {
       w, x, f32x4{0.0f, 0.0f, 0.0f, 0.0f}, 0, 0, 0, 0, 0, 0);
 }
 
-// Maximum over the 16 lanes of a DPP row, in every lane.
+// Magnitudes are compared as their bit patterns: the order is that of the
+// numbers, with an infinity and then every NaN above them, so neither is lost as
+// in a maximum of floats.
+__device__ __forceinline__ unsigned mag(float v) { return __float_as_uint(v) & 0x7fffffffu; }
 template <int CTRL>
-__device__ __forceinline__ float dpp_f(float v) {
-  return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, 0xf, 0xf, true));
+__device__ __forceinline__ unsigned dpp_max(unsigned v) {
+  return max(v, (unsigned)__builtin_amdgcn_update_dpp(0, (int)v, CTRL, 0xf, 0xf, true));
 }
-__device__ __forceinline__ float row16_max(float v) {
-  v = fmaxf(v, dpp_f<0xB1>(v));   // lane ^ 1
-  v = fmaxf(v, dpp_f<0x4E>(v));   // lane ^ 2
-  v = fmaxf(v, dpp_f<0x141>(v));  // mirror of 8
-  return fmaxf(v, dpp_f<0x140>(v));
+// Maximum over the 16 lanes of a DPP row, in every lane.
+__device__ __forceinline__ unsigned row16_max(unsigned v) {
+  v = dpp_max<0xB1>(v);     // lane ^ 1
+  v = dpp_max<0x4E>(v);     // lane ^ 2
+  v = dpp_max<0x141>(v);    // mirror of 8
+  return dpp_max<0x140>(v);
+}
+// The scale of a block whose largest magnitude is m: NaN, and with it every value
+// of the block, where the block holds an infinity or a NaN (an infinite scale
+// would leave the others' sign to 448 of either sign).
+__device__ __forceinline__ float scale_of(unsigned m) {
+  return m < 0x7f800000u ? __uint_as_float(m) * kInvE4m3Max : __uint_as_float(0x7fc00000u);
 }
 
 // E4M3 codes of four values already divided by their scale: nearest, ties to
@@ -76,13 +86,13 @@ __device__ __forceinline__ void ld8(const float* p, float (&v)[8]) {
   v[0] = a.x; v[1] = a.y; v[2] = a.z; v[3] = a.w;
   v[4] = b.x; v[5] = b.y; v[6] = b.z; v[7] = b.w;
 }
-__device__ __forceinline__ float amax8(const float (&v)[8]) {
-  float m = 0.0f;
+__device__ __forceinline__ unsigned amax8(const float (&v)[8]) {
+  unsigned m = 0;
 #pragma unroll
-  for (int i = 0; i < 8; ++i) m = fmaxf(m, fabsf(v[i]));
+  for (int i = 0; i < 8; ++i) m = max(m, mag(v[i]));
   return m;
 }
-// 8 codes of v / s (s = 0: zeros).
+// 8 codes of v / s (s = 0 or NaN: zeros).
 __device__ __forceinline__ uint2 encode8(const float (&v)[8], float s) {
   float q[8];
 #pragma unroll
@@ -107,7 +117,7 @@ __global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, i
   const int c = (int)(grp % nb) * kBlk + 8 * l;
   float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
   if (c < cols) ld8(in + r * cols + c, v);
-  const float s = row16_max(amax8(v)) * kInvE4m3Max;
+  const float s = scale_of(row16_max(amax8(v)));
   if (l == 0) scale[grp] = s;
   const long long pitch = PAD ? (long long)nb * kBlk : cols;
   if (PAD || c < cols) *reinterpret_cast<uint2*>(q + r * pitch + c) = encode8(v, s);
@@ -119,26 +129,28 @@ __global__ __launch_bounds__(256) void quantize_blocks128_kernel(int rows, int c
                                                                  const bf16* __restrict__ in,
                                                                  uint8_t* __restrict__ q,
                                                                  float* __restrict__ scale) {
-  __shared__ float red[4];
+  __shared__ unsigned red[4];
   const int cb = blockIdx.x, rb = blockIdx.y;
   const long long b = blockIdx.z;
   const bf16* src = in + b * rows * cols;
   uint8_t* dst = q + b * rows * cols;
   const int c = cb * kBlk + 8 * (threadIdx.x % 16), r0 = rb * kBlk + threadIdx.x / 16;
   float v[8][8];
-  float m = 0.0f;
+  unsigned m = 0;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
     const int r = r0 + 16 * i;
 #pragma unroll
     for (int j = 0; j < 8; ++j) v[i][j] = 0.0f;
     if (r < rows && c < cols) ld8(src + (long long)r * cols + c, v[i]);
-    m = fmaxf(m, amax8(v[i]));
+    m = max(m, amax8(v[i]));
   }
-  m = wave_max(m);
+  m = row16_max(m);
+  m = max(m, (unsigned)__shfl_xor((int)m, 16));
+  m = max(m, (unsigned)__shfl_xor((int)m, 32));
   if (lane_id() == 0) red[threadIdx.x / kWave] = m;
   __syncthreads();
-  const float s = fmaxf(fmaxf(red[0], red[1]), fmaxf(red[2], red[3])) * kInvE4m3Max;
+  const float s = scale_of(max(max(red[0], red[1]), max(red[2], red[3])));
   if (threadIdx.x == 0) scale[(b * gridDim.y + rb) * gridDim.x + cb] = s;
 #pragma unroll
   for (int i = 0; i < 8; ++i) {
@@ -318,7 +330,7 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
       if (MODE == kGateUp) t = a.sorted_slots[t] / a.K;
       float v[8] = {0, 0, 0, 0, 0, 0, 0, 0};
       if (c < Kd) ld8(static_cast<const XT*>(a.x) + t * Kd + c, v);
-      const float s = row16_max(amax8(v)) * kInvE4m3Max;
+      const float s = scale_of(row16_max(amax8(v)));
       if (l == 0) sl[r * KB + kb] = s;
       *reinterpret_cast<uint2*>(xl + r * (pitch + kFusePad) + c) = encode8(v, s);
     }
@@ -742,17 +754,15 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
       const int k = tid + it * S::THREADS, r = k / 4, c = 32 * (k % 4);
       const bool on = row0 + r < row1;
       float v[32];
-      float m = 0.0f;
+      unsigned m = 0;
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float4 f = *reinterpret_cast<const float4*>(hs + r * S::HPITCH + c + 4 * i);
         v[4 * i] = f.x; v[4 * i + 1] = f.y; v[4 * i + 2] = f.z; v[4 * i + 3] = f.w;
       }
 #pragma unroll
-      for (int i = 0; i < 32; ++i) m = fmaxf(m, fabsf(v[i]));
-      m = fmaxf(m, dpp_f<0xB1>(m));
-      m = fmaxf(m, dpp_f<0x4E>(m));
-      const float s = m * kInvE4m3Max;
+      for (int i = 0; i < 32; ++i) m = max(m, mag(v[i]));
+      const float s = scale_of(dpp_max<0x4E>(dpp_max<0xB1>(m)));
       // one division a row: h is an fp32 sum already, no decision point is hit
       // exactly, and an ulp of the quotient moves no more codes than one of h
       const float inv = s > 0.0f ? 1.0f / s : 0.0f;

@@ -803,9 +803,9 @@ int check_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t cols) {
     return fail(MOE_ERR_ARG, "batch or rows out of range");
   if (cols < 16 || cols > 65536 || cols % 16)
     return fail(MOE_ERR_ARG, "cols=%d: need a multiple of 16 in [16, 65536]", cols);
-  // a launch holds 2^31 groups of 16 values
-  if (batch * rows > ((int64_t)1 << 35) / cols)
-    return fail(MOE_ERR_UNSUPPORTED, "more than 2^35 values");
+  // a launch counts its lanes in 32 bits: 16 for the 128 values that share a scale
+  if (batch * rows >= ((int64_t)1 << 28) / ((cols + 127) / 128))
+    return fail(MOE_ERR_UNSUPPORTED, "2^28 or more pieces of 128 values");
   return MOE_OK;
 }
 

@@ -54,6 +54,9 @@ def test_quantize_refusals(f):
     assert f(cols=0) == lib.MOE_ERR_ARG and f(cols=65552) == lib.MOE_ERR_ARG
     assert f(rows=-1) == lib.MOE_ERR_ARG and f(batch=-1) == lib.MOE_ERR_ARG
     assert f(batch=1 << 30, rows=1 << 20) == lib.MOE_ERR_UNSUPPORTED
+    # a launch's lanes are counted in 32 bits: 16 of them per row and 128 columns
+    assert f(batch=1 << 8, rows=1 << 20, cols=16) == lib.MOE_ERR_UNSUPPORTED
+    assert f(batch=1 << 7, rows=1 << 20, cols=256) == lib.MOE_ERR_UNSUPPORTED
     assert f(batch=0) == lib.MOE_OK and f(rows=0) == lib.MOE_OK
     for k in ("w", "q", "s", "o"):
         if k in f.__code__.co_varnames:

@@ -118,6 +118,65 @@ def test_linear_zero_rows_and_blocks(T):
     assert not y[1].any()
 
 
+@pytest.mark.parametrize("br", [1, 128])
+def test_quantizer_not_finite(br):
+    """A NaN or an infinity makes its own block NaN, and no other."""
+    g = _gen(br)
+    v = torch.randn(300, 400, generator=g).bfloat16()
+    q, s = ref.quantize(v.float(), br)
+    at = [(5, 7, float("nan")), (130, 399, float("inf")), (299, 130, -float("inf"))]
+    hit = torch.zeros(300, 400, dtype=torch.bool)
+    for r, c, val in at:
+        v[r, c] = val
+        hit[r // br * br:(r // br + 1) * br, c // 128 * 128:(c // 128 + 1) * 128] = True
+    qd = torch.empty(300, 400, dtype=torch.uint8, device="cuda")
+    sd = torch.empty(s.shape, device="cuda")
+    out = torch.empty(300, 400, device="cuda")
+    note(f"quantize_b128, not finite, block_rows={br}")
+    lib.moe_quantize_b128(br, v.cuda(), qd, sd)
+    lib.moe_dequantize_b128(br, qd, sd, out)
+    torch.cuda.synchronize()
+    out = out.cpu()
+    assert torch.all(out[hit].isnan())
+    assert torch.equal(out[~hit], ref.values(q, s, br).float()[~hit])
+
+
+@pytest.mark.parametrize("T", [3, 12, 150, 3000])
+def test_linear_not_finite(T):
+    """A NaN or an infinity in a row of x makes that row of y NaN, a NaN among the
+    weights' codes its column; nothing else changes."""
+    g = _gen(T)
+    x = _x(g, T, 400)
+    q, s = _weights(g, 300, 400)
+    note(f"linear_b128, not finite, T={T}")
+    want = _linear(x, q, s, torch.float32)
+    x[1, 399], x[2, 5] = float("nan"), -float("inf")
+    q[77, 130], q[299, 399] = 0x7F, 0xFF
+    y = _linear(x, q, s, torch.float32)
+    bad = torch.zeros(T, 300, dtype=torch.bool)
+    bad[1:3], bad[:, 77], bad[:, 299] = True, True, True
+    assert torch.all(y[bad].isnan())
+    assert torch.equal(y[~bad], want[~bad])
+
+
+@pytest.mark.parametrize("T", [3, 40, 700])
+def test_experts_not_finite(T):
+    """A token's NaN or infinity reaches its own slots alone."""
+    g = _gen(T)
+    x = _x(g, T, 192)
+    guq, gus = _weights(g, 4, 192, 192)
+    dnq, dns = _weights(g, 4, 192, 96)
+    idx, w = _routing(g, T, 4, 2)
+    note(f"experts_b128, not finite, T={T}")
+    want, _ = _experts(x, guq, gus, dnq, dns, idx, w)
+    x[0, 191], x[2, 0] = float("nan"), float("inf")
+    y, out = _experts(x, guq, gus, dnq, dns, idx, w)
+    bad = torch.zeros(T, dtype=torch.bool)
+    bad[0], bad[2] = True, True
+    assert torch.all(y[bad].isnan()) and torch.all(out[bad].isnan())
+    assert torch.equal(y[~bad], want[~bad])
+
+
 def test_linear_large_offsets():
     """Outputs past 2^32 bytes."""
     T, N, K = 65536, 40000, 16
@@ -179,7 +238,7 @@ def _check_experts(x, guq, gus, dnq, dns, idx, w, y, out):
     (37, 192, 16, 3, 96), (40, 320, 6, 2, 224), (200, 512, 128, 8, 64), (256, 64, 256, 16, 32),
     (257, 64, 256, 4, 32), (90, 320, 2, 2, 160), (300, 256, 8, 2, 192), (700, 192, 5, 1, 96),
     (1100, 2816, 3, 2, 704), (520, 8192, 2, 1, 288), (200, 2816, 3, 3, 704),
-    (20, 64, 4, 2, 3200), (4, 8192, 3, 2, 32), (3, 2816, 4, 4, 704)])
+    (20, 64, 4, 2, 3200), (300, 64, 4, 2, 3200), (4, 8192, 3, 2, 32), (3, 2816, 4, 4, 704)])
 def test_experts(T, H, E, K, I):
     """Both forms, with the quantizers inside the products and before them, ragged
     widths (up rows that start inside a block), one row to many per expert, more
