@@ -933,10 +933,12 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
   }
   hipError_t e = quantize_rows<bf16, true>(a.rows, a.Kd, x, xq, xscale, s);
   if (e != hipSuccess) return e;
-  // streamed while all the row tiles together read at most 48 MB of weights
-  // (2112 x 2816: 128 tokens 19.5 us streamed, 24.6 tiled, 256 tokens 30.4 and
-  // 25.0; 704 x 704: 512 tokens 10.0 and 13.1, 1024 tokens 14.0 and 13.4)
-  if ((a.rows + 15LL) / 16 * a.N * a.Kd <= 48LL << 20) return stream_linear<void>(a, y_bf16, s);
+  // streamed while there is one row tile, or all of them together read at most 64
+  // MB of weights (2112 x 2816: 128 tokens 16.4 us streamed, 20.8 tiled, 256 tokens
+  // 30.4 and 25.0; 4096 x 4096: 64 tokens 23.9 and 26.6; 4096 x 16384: 16 tokens
+  // 24.4 and 30.6, 32 tokens 41.8 and 31.2; 8192 x 8192: 16 tokens 23.5 and 52.6)
+  if (a.rows <= 16 || (a.rows + 15LL) / 16 * a.N * a.Kd <= 64LL << 20)
+    return stream_linear<void>(a, y_bf16, s);
   return linear_takes_small(a.rows, a.N) ? Launch<SmallTile>::plain(a, y_bf16, s)
                                          : Launch<WideTile>::plain(a, y_bf16, s);
 }

@@ -128,6 +128,51 @@ def test_balance_lowest_value_mask():
     assert torch.all(got["p"][40:90] == 0)
 
 
+@pytest.mark.parametrize("T,E", [(1, 7), (70, 128), (1001, 33), (20000, 256)])
+def test_balance_grad_in_place(T, E):
+    """The gradient written over the logits."""
+    g = _gen(T + E)
+    d = lib.dims(64, E, 2, 32)
+    ws = lib.workspace(d, T)
+    lg, idx = torch.randn(T, E, generator=g).cuda(), _picks(g, T, E, 2).cuda()
+    mask = _mask(g, T, "some").cuda()
+    new = lambda *s, t=torch.float32: torch.empty(*s, dtype=t, device="cuda")  # noqa: E731
+    loss, counts, p, d_l = new(4), new(E, t=torch.int32), new(E), new(T, E)
+    one = torch.tensor([G], device="cuda")
+    note(f"balance gradient in place T={T} E={E}")
+    lib.moe_balance_loss(d, T, lg, idx, mask, A, B, loss, counts, p, ws)
+    lib.moe_balance_loss_grad(d, T, lg, mask, counts, loss, A, B, one, d_l)
+    lib.moe_balance_loss_grad(d, T, lg, mask, counts, loss, A, B, one, lg)
+    torch.cuda.synchronize()
+    assert torch.equal(lg, d_l)
+
+
+def test_refuses_tensors_it_cannot_read():
+    """Strided, misaligned and host tensors: an error, and nothing written."""
+    E, T = 8, 16
+    d = lib.dims(64, E, 2, 32)
+    ws = lib.workspace(d, T)
+    idx = torch.zeros(T, 2, dtype=torch.int32, device="cuda")
+    out = [torch.full((4,), 7.0, device="cuda"), torch.full((E,), 7, dtype=torch.int32,
+                                                            device="cuda"),
+           torch.full((E,), 7.0, device="cuda")]
+    good = torch.zeros(T, E, device="cuda")
+    wide, long = torch.zeros(T, 2 * E, device="cuda"), torch.zeros(T * E + 1, device="cuda")
+    run = lambda lg, m=None, o=out: lib.moe_balance_loss(  # noqa: E731
+        d, T, lg, idx, m, A, B, *o, ws)
+    for lg in (wide[:, :E], torch.zeros(E, T, device="cuda").t(), torch.zeros(T, E)):
+        with pytest.raises(ValueError):
+            run(lg)
+    with pytest.raises(lib.MoeError):
+        run(long[1:].view(T, E))
+    with pytest.raises(ValueError):
+        run(good, torch.ones(2 * T, dtype=torch.uint8, device="cuda")[::2])
+    with pytest.raises(ValueError):
+        run(good, None, [out[0][:3], out[1], out[2]])
+    torch.cuda.synchronize()
+    assert all(torch.all(o == 7) for o in out)
+
+
 def test_balance_largest_batch():
     g = _gen(5)
     T, E, K = 65536, 16, 2
@@ -229,6 +274,14 @@ def test_router_grad_inputs_given(pre, aux, use_w):
     less = _run_router_grad(c, False, want_x=False)  # d_x not wanted: the rest is the same
     for k, v in less.items():
         assert torch.equal(v, got[k])
+
+
+@pytest.mark.parametrize("T,H,E,K,bf16", [(5000, 2816, 128, 8, True), (5000, 2816, 128, 8, False),
+                                          (65536, 192, 16, 2, True), (65536, 64, 7, 2, False)])
+def test_router_grad_large(T, H, E, K, bf16):
+    c = _router_case(T, H, E, K, bf16, True, True, True, "some", T + H)
+    note(f"router grad, large, T={T} H={H} E={E} bf16={bf16}")
+    _check_router_grad(c, _run_router_grad(c, bf16, spoil=True), bf16)
 
 
 def test_router_grad_odd_picks():
