@@ -91,7 +91,7 @@ struct RouterGradArgs {
   float* ws_part_b;               // [splits,H]
   float* ws_part_pes;             // [row blocks,E]
 };
-int router_grad_splits(int T, int H, int E);
+int router_grad_max_splits(int T, int H, int E);
 int router_grad_row_blocks(int T);
 size_t router_grad_dl_bytes(int T, int H, int E);
 hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s);

@@ -145,7 +145,7 @@ Layout layout(const moe_dims* d, long long T) {
   L.bal_z = take(4 * nb);
   L.bal_live = take(4 * nb);
   if (o > L.total) L.total = o;
-  const size_t splits = (size_t)moe::router_grad_splits((int)T, d->hidden, d->num_experts);
+  const size_t splits = (size_t)moe::router_grad_max_splits((int)T, d->hidden, d->num_experts);
   o = L.base_end;
   L.rg_dl = take(moe::router_grad_dl_bytes((int)T, d->hidden, d->num_experts));
   L.rg_beta = take(4 * (((size_t)T + 31) / 32 * 32));

@@ -560,16 +560,30 @@ __device__ __forceinline__ int mfma_row(int q, int g) { return 8 * (q / 4) + 4 *
 // added through LDS.  The wave also sums x^2 beta for its columns (experts'
 // tile 0 only).
 constexpr int kRgWaves = 4;
+struct BlockAt { int col, y, z; };  // 64 columns; experts or tokens; split
+
+// A launch of wb blocks that make G's partials and the rest dx, which need nothing
+// of each other, spread evenly.  True for a block of G.
+__device__ __forceinline__ bool grad_block(int wb, int H, int ey, BlockAt& at) {
+  const long long n = gridDim.x, b = blockIdx.x, w = b * wb / n;
+  const bool is_w = (b + 1) * wb / n != w;
+  const int i = (int)(is_w ? w : b - w), cols = H / 64;
+  at.col = i % cols;
+  at.y = is_w ? i / cols % ey : i / cols;
+  at.z = is_w ? i / cols / ey : 0;
+  return is_w;
+}
+
 template <int MT>
-__global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
-    int T, int H, int E, int span, const float* __restrict__ x, const uint8_t* __restrict__ mask,
+__device__ __forceinline__ void router_grad_w(
+    BlockAt at, int T, int H, int E, int span, const float* __restrict__ x, const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, float* __restrict__ part_g,
     float* __restrict__ part_b) {
   __shared__ float acc_s[kRgWaves][16 * 2][kWave];
   __shared__ float b_s[kRgWaves][64];
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int c = lane % 32, g = lane / 32;
-  const int h0 = blockIdx.x * 64, e0 = blockIdx.y * 32 * MT, split = blockIdx.z;
+  const int h0 = at.col * 64, e0 = at.y * 32 * MT, split = at.z;
   const int s0 = split * span, s1 = min(T, s0 + span);
   const int q4 = ((s1 - s0 + kRgWaves - 1) / kRgWaves + 1) / 2 * 2;
   const int t0 = min(s1, s0 + wave * q4), t1 = min(s1, t0 + q4);
@@ -608,7 +622,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
       for (int j = 0; j < 2; ++j) bs[j] = __builtin_fmaf(b[u][j] * b[u][j], be[u], bs[j]);
     }
   }
-  const bool want_b = blockIdx.y == 0;
+  const bool want_b = at.y == 0;
   if (want_b) {
 #pragma unroll
     for (int j = 0; j < 2; ++j) {
@@ -645,14 +659,13 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_w_kernel(
 // dx: a wave takes 64 tokens x 64 columns; the contraction runs over the
 // experts, four per lane and load (lanes 0-31 experts 8 s .. 8 s + 3, lanes
 // 32-63 the next four; W's rows in the same order).
-template <bool VEC>
-__global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
-    int T, int H, int E, float eps, const float* __restrict__ x, const uint8_t* __restrict__ mask,
+__device__ __forceinline__ void router_grad_x(
+    BlockAt at, bool vec, int T, int H, int E, float eps, const float* __restrict__ x, const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, const float* __restrict__ W,
     const float* __restrict__ scale, const float* __restrict__ pre_gain, float* __restrict__ dx) {
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int c = lane % 32, g = lane / 32;
-  const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgWaves + wave) * 64;
+  const int h0 = at.col * 64, t0 = (at.y * kRgWaves + wave) * 64;
   if (t0 >= T) return;  // no barrier below
   f32x16 acc[2][2];
 #pragma unroll
@@ -667,7 +680,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
     for (int i = 0; i < 2; ++i) {
       const float* row = dl + (size_t)min(t0 + 32 * i + c, T - 1) * E;
       const int e = e0 + 4 * g;
-      if (VEC && e + 3 < E) {
+      if (vec && e + 3 < E) {
         const float4 v = *reinterpret_cast<const float4*>(row + e);
         a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
       } else {
@@ -716,6 +729,29 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
   }
 }
 
+template <int MT>
+__global__ __launch_bounds__(64 * kRgWaves) void router_grad_wx_kernel(
+    int wb, int ey, int T, int H, int E, int span, float eps, const float* __restrict__ x,
+    const uint8_t* __restrict__ mask, const float* __restrict__ dl,
+    const float* __restrict__ beta, const float* __restrict__ W, const float* __restrict__ scale,
+    const float* __restrict__ pre_gain, float* __restrict__ part_g, float* __restrict__ part_b,
+    float* __restrict__ dx) {
+  BlockAt at;
+  if (grad_block(wb, H, ey, at))
+    router_grad_w<MT>(at, T, H, E, span, x, mask, dl, beta, part_g, part_b);
+  else
+    router_grad_x(at, E % 4 == 0, T, H, E, eps, x, mask, dl, beta, W, scale, pre_gain, dx);
+}
+
+__global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
+    int T, int H, int E, float eps, const float* __restrict__ x, const uint8_t* __restrict__ mask,
+    const float* __restrict__ dl, const float* __restrict__ beta, const float* __restrict__ W,
+    const float* __restrict__ scale, const float* __restrict__ pre_gain, float* __restrict__ dx) {
+  BlockAt at;
+  grad_block(0, H, 1, at);
+  router_grad_x(at, E % 4 == 0, T, H, E, eps, x, mask, dl, beta, W, scale, pre_gain, dx);
+}
+
 // ---------------------------------------------------------------------------
 // bf16 inputs: both products on bf16 matrix instructions (16x16x32: lane l holds
 // row l % 16 of each operand, k = 8 (l / 16) .. + 7; register r of the result
@@ -738,6 +774,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
 //   W for dx    [H / 16][Ep / 32][2 parts][lane]    column wt_col(l % 16) of the
 //                                                   tile, experts as in dl'
 // ---------------------------------------------------------------------------
+constexpr int kRgSumBytes = 2 * kRgWaves * 4 * kWave * 16;  // two tiles' results per wave
 constexpr int kRgTok = 16;   // tokens per rows block, one per wave
 constexpr int kRgRowThreads = kRgTok * kWave;
 constexpr int kRgWCols = 32; // columns of W per block past those
@@ -857,19 +894,19 @@ __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
 // is their latency (two column groups a block, which halves what L2 delivers,
 // took as long).
 template <int MT, bool MASK>
-__global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
-    int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
+__device__ __forceinline__ void router_grad_w_bf16(
+    BlockAt at, unsigned char* smem, int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
     const bf16* __restrict__ cols, const float* __restrict__ beta, bool want_beta,
     float* __restrict__ part_g, float* __restrict__ part_b) {
-  __shared__ f32x4 acc_s[2][kRgWaves][4][kWave];
-  __shared__ float b_s[kRgWaves][4][64];
+  auto acc_s = reinterpret_cast<f32x4 (*)[kRgWaves][4][kWave]>(smem);  // [2]
+  auto b_s = reinterpret_cast<float (*)[4][64]>(smem + kRgSumBytes);   // [kRgWaves]
   const int wave = threadIdx.x / kWave, lane = lane_id();
   const int c = lane % 16, g = lane / 16;
-  const int h0 = blockIdx.x * 64, m0 = blockIdx.y * MT, split = blockIdx.z;
+  const int h0 = at.col * 64, m0 = at.y * MT, split = at.z;
   const int MS = (E + 31) / 32 * 2, all = (T + 31) / 32;
   const int s0 = min(all, split * steps), s1 = min(all, s0 + steps);
   const int n = s1 - s0, a0 = s0 + wave * n / kRgWaves, a1 = s0 + (wave + 1) * n / kRgWaves;
-  const bool beta_here = want_beta && blockIdx.y == 0;
+  const bool beta_here = want_beta && at.y == 0;
   f32x4 acc[MT][4];
 #pragma unroll
   for (int m = 0; m < MT; ++m)
@@ -1003,17 +1040,17 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_w_bf16_kernel(
 // the rows of x come straight from memory, one step ahead.  W^T is the first
 // operand: with its column order (wt_col) a lane's results of two tiles are eight
 // consecutive columns of a token, 16-byte loads of x and stores of dx.
-constexpr int kRgXWaves = 8, kRgXTok = 32;
-__global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
-    int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
+constexpr int kRgXTok = 32;
+template <int WAVES>
+__device__ __forceinline__ void router_grad_x_bf16(
+    BlockAt at, unsigned char* smem, int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
     const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
     const float* __restrict__ scale, const float* __restrict__ pre_gain, bf16* __restrict__ dx) {
-  extern __shared__ __align__(16) unsigned char smem[];
   bf16x8* ws = reinterpret_cast<bf16x8*>(smem);  // [4 tiles][KS][2][lane]
   const int tid = threadIdx.x, lane = lane_id();
   const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
   const int c = lane % 16, g = lane / 16;
-  const int h0 = blockIdx.x * 64, t0 = (blockIdx.y * kRgXWaves + wave) * kRgXTok;
+  const int h0 = at.col * 64, t0 = (at.y * WAVES + wave) * kRgXTok;
   const int KS = (E + 31) / 32, tiles = (T + 31) / 32 * 2;
   const bf16* tr[2];
 #pragma unroll
@@ -1041,7 +1078,7 @@ __global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
   }
   const bf16x8* src = reinterpret_cast<const bf16x8*>(wt + (size_t)h0 / 16 * KS * 2 * kFrag);
 #pragma unroll 4
-  for (int k = tid; k < 4 * KS * 2 * kWave; k += 64 * kRgXWaves) ws[k] = src[k];
+  for (int k = tid; k < 4 * KS * 2 * kWave; k += 64 * WAVES) ws[k] = src[k];
   __syncthreads();
   f32x4 acc[2][4];  // token tile, column tile
 #pragma unroll
@@ -1095,17 +1132,47 @@ __global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
   }
 }
 
+constexpr int kRgWBytes = kRgSumBytes + kRgWaves * 4 * 64 * 4;
+template <int MT, bool MASK>
+__global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_wx_bf16_kernel(
+    int wb, int ey, int T, int H, int E, int steps, float eps, const bf16* __restrict__ x,
+    const uint8_t* __restrict__ live, const bf16* __restrict__ rows,
+    const bf16* __restrict__ cols, const float* __restrict__ beta, const bf16* __restrict__ wt,
+    const float* __restrict__ scale, const float* __restrict__ pre_gain,
+    float* __restrict__ part_g, float* __restrict__ part_b, bf16* __restrict__ dx) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  BlockAt at;
+  if (grad_block(wb, H, ey, at))
+    router_grad_w_bf16<MT, MASK>(at, smem, T, H, E, steps, x, live, cols, beta,
+                                 pre_gain != nullptr, part_g, part_b);
+  else
+    router_grad_x_bf16<kRgWaves>(at, smem, T, H, E, eps, x, live, rows, beta, wt, scale, pre_gain, dx);
+}
+
+constexpr int kRgXWaves = 8;
+__global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
+    int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
+    const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
+    const float* __restrict__ scale, const float* __restrict__ pre_gain, bf16* __restrict__ dx) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  router_grad_x_bf16<kRgXWaves>(BlockAt{(int)blockIdx.x, (int)blockIdx.y, 0}, smem, T, H, E, eps,
+                                x, live, rows, beta, wt, scale, pre_gain, dx);
+}
+
 // Last kernel: adds the splits of G; dW, dc and dg of 32 columns per block, four
 // columns a thread and 32 groups of experts; in the blocks past the columns the
-// per-expert scale's gradient from the first kernel's sums.
-constexpr int kRgCols = 32, kRgParts = 32, kRgFinThreads = kRgCols / 4 * kRgParts;
+// per-expert scale's gradient from the first kernel's sums.  Its few blocks wait for
+// memory: all the loads of a thread's EU experts go out before the first is added
+// (128 experts, 2816 columns, 5 splits: 7.4 -> 5.5 us).
+constexpr int kRgCols = 32, kRgParts = 32 /* >= the splits */, kRgFinThreads = kRgCols / 4 * kRgParts;
+template <int EU>
 __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
     int H, int E, int splits, int pes_blocks, const float* __restrict__ part_g,
     const float* __restrict__ part_b, const float* __restrict__ part_pes,
     const float* __restrict__ W, const float* __restrict__ scale,
     const float* __restrict__ pre_gain, float* __restrict__ dW, float* __restrict__ d_scale,
     float* __restrict__ d_pes, float* __restrict__ d_gain) {
-  __shared__ f32x4 red[kRgParts][kRgCols / 4];
+  __shared__ f32x4 red[kRgParts][kRgCols / 4], red_b[kRgParts][kRgCols / 4];
   const int c = threadIdx.x % (kRgCols / 4), p = threadIdx.x / (kRgCols / 4);
   const int col_blocks = H / kRgCols;
   if ((int)blockIdx.x >= col_blocks) {
@@ -1130,24 +1197,43 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
   const f32x4 gn = pre_gain != nullptr ? *reinterpret_cast<const f32x4*>(pre_gain + h) : one;
   const f32x4 cs = *reinterpret_cast<const f32x4*>(scale + h);
   f32x4 m = {0.0f, 0.0f, 0.0f, 0.0f};
+  // thread row p adds split p's sum of x^2 beta (at most kRgParts splits)
+  f32x4 bsum = m;
+  if (d_gain != nullptr && p < splits)
+    bsum = *reinterpret_cast<const f32x4*>(part_b + (size_t)p * H + h);
   constexpr int U = 5;  // splits loaded before the first is added
-#pragma unroll 2
-  for (int e = p; e < E; e += kRgParts) {
-    f32x4 sum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s0 = 0; s0 < splits; s0 += U) {
-      f32x4 v[U];
+  for (int e0 = p; e0 < E; e0 += EU * kRgParts) {
+    f32x4 sum[EU], w[EU];
 #pragma unroll
-      for (int u = 0; u < U; ++u)
-        v[u] = *reinterpret_cast<const f32x4*>(
-            part_g + ((size_t)min(s0 + u, splits - 1) * E + e) * H + h);
-#pragma unroll
-      for (int u = 0; u < U; ++u)
-        if (s0 + u < splits) sum += v[u];
+    for (int i = 0; i < EU; ++i) {
+      sum[i] = f32x4{0.0f, 0.0f, 0.0f, 0.0f};
+      w[i] = *reinterpret_cast<const f32x4*>(W + (size_t)min(e0 + i * kRgParts, E - 1) * H + h);
     }
-    *reinterpret_cast<f32x4*>(dW + (size_t)e * H + h) = sum * gn * cs;
-    m += *reinterpret_cast<const f32x4*>(W + (size_t)e * H + h) * sum;
+    for (int s0 = 0; s0 < splits; s0 += U) {
+      f32x4 v[EU][U];
+#pragma unroll
+      for (int i = 0; i < EU; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          v[i][u] = *reinterpret_cast<const f32x4*>(
+              part_g +
+              ((size_t)min(s0 + u, splits - 1) * E + min(e0 + i * kRgParts, E - 1)) * H + h);
+#pragma unroll
+      for (int i = 0; i < EU; ++i)
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+          if (s0 + u < splits) sum[i] += v[i][u];
+    }
+#pragma unroll
+    for (int i = 0; i < EU; ++i) {
+      const int e = e0 + i * kRgParts;
+      if (e >= E) break;
+      *reinterpret_cast<f32x4*>(dW + (size_t)e * H + h) = sum[i] * gn * cs;
+      m += w[i] * sum[i];
+    }
   }
   red[p][c] = m;
+  red_b[p][c] = bsum;
   __syncthreads();
   if (p != 0) return;
   m = red[0][c];
@@ -1155,18 +1241,40 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
   for (int i = 1; i < kRgParts; ++i) m += red[i][c];
   *reinterpret_cast<f32x4*>(d_scale + h) = gn * m;
   if (d_gain != nullptr) {
-    f32x4 bsum = {0.0f, 0.0f, 0.0f, 0.0f};
-    for (int s = 0; s < splits; ++s)
-      bsum += *reinterpret_cast<const f32x4*>(part_b + (size_t)s * H + h);
+    for (int i = 1; i < splits; ++i) bsum += red_b[i][c];
     *reinterpret_cast<f32x4*>(d_gain + h) = cs * m - gn * bsum;
   }
+}
+
+// G's partials and dx take one launch where dx and one split of G fit into one
+// round of blocks: two a CU with bf16 inputs, one with fp32 (whose G needs the
+// registers of two).  At 26B-A4B's shape, all of the router's backward and the
+// balance loss: bf16 48 / 301 / 1024 / 2048 tokens 24.9 / 32.1 / 35.5 / 43.5 us in
+// two launches, 20.0 / 25.8 / 31.4 / 43.5 in one; fp32 48 / 301 / 1024 tokens 47.2 /
+// 70.2 / 84.5 and 36.6 / 56.4 / 110.8.
+constexpr int kRgRound = 512;
+int grad_round(bool bf16_in) { return bf16_in ? kRgRound : kRgRound / 2; }
+int grad_w_blocks(int H, int E) { return H / 64 * ((E + 63) / 64); }  // of a split
+int grad_x_blocks(int T, int H, bool bf16_in) {
+  const int tok = kRgWaves * (bf16_in ? kRgXTok : 64);
+  return H / 64 * ((T + tok - 1) / tok);
+}
+bool grad_one_launch(int T, int H, int E, bool bf16_in) {
+  return grad_x_blocks(T, H, bf16_in) + grad_w_blocks(H, E) <= grad_round(bf16_in);
+}
+int grad_splits(int T, int H, int E, bool bf16_in) {
+  const int most = router_grad_max_splits(T, H, E);
+  if (!grad_one_launch(T, H, E, bf16_in)) return most;
+  const int n = (grad_round(bf16_in) - grad_x_blocks(T, H, bf16_in)) / grad_w_blocks(H, E);
+  return n < 1 ? 1 : n < most ? n : most;
 }
 
 // fp32 inputs.
 void launch_grad_f32(const RouterGradArgs& a, hipStream_t s) {
   const float* x = static_cast<const float*>(a.x);
   float* dl = static_cast<float*>(a.ws_dl);
-  const int splits = router_grad_splits(a.T, a.H, a.E);
+  const int splits = grad_splits(a.T, a.H, a.E, false);
+  const bool one = a.d_x != nullptr && grad_one_launch(a.T, a.H, a.E, false);
   hipLaunchKernelGGL(router_grad_rows_kernel, dim3(router_grad_row_blocks(a.T)),
                      dim3(64 * kRgRowWaves), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
                      a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits, dl,
@@ -1174,25 +1282,20 @@ void launch_grad_f32(const RouterGradArgs& a, hipStream_t s) {
   const int span = (a.T + splits - 1) / splits;
   auto gw = [&](auto mt) {
     constexpr int MT = decltype(mt)::value;
-    hipLaunchKernelGGL((router_grad_w_kernel<MT>),
-                       dim3(a.H / 64, (a.E + 32 * MT - 1) / (32 * MT), splits),
-                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, span, x, a.mask, dl, a.ws_beta,
-                       a.ws_part_g, a.ws_part_b);
+    const int cols = a.H / 64, ey = (a.E + 32 * MT - 1) / (32 * MT), wb = cols * ey * splits;
+    const int xb = one ? grad_x_blocks(a.T, a.H, false) : 0;
+    hipLaunchKernelGGL((router_grad_wx_kernel<MT>), dim3(wb + xb), dim3(64 * kRgWaves), 0, s, wb,
+                       ey, a.T, a.H, a.E, span, a.eps, x, a.mask, dl, a.ws_beta, a.router_w,
+                       a.router_scale, a.pre_gain, a.ws_part_g, a.ws_part_b,
+                       static_cast<float*>(a.d_x));
   };
   if (a.E <= 32) gw(std::integral_constant<int, 1>{});
   else if (a.E <= 64) gw(std::integral_constant<int, 2>{});
   else gw(std::integral_constant<int, 4>{});
-  if (a.d_x == nullptr) return;
-  const dim3 grid(a.H / 64, (a.T + 64 * kRgWaves - 1) / (64 * kRgWaves));
-  float* dx = static_cast<float*>(a.d_x);
-  if (a.E % 4 == 0)
-    hipLaunchKernelGGL((router_grad_x_kernel<true>), grid, dim3(64 * kRgWaves), 0, s, a.T, a.H,
-                       a.E, a.eps, x, a.mask, dl, a.ws_beta, a.router_w, a.router_scale,
-                       a.pre_gain, dx);
-  else
-    hipLaunchKernelGGL((router_grad_x_kernel<false>), grid, dim3(64 * kRgWaves), 0, s, a.T, a.H,
-                       a.E, a.eps, x, a.mask, dl, a.ws_beta, a.router_w, a.router_scale,
-                       a.pre_gain, dx);
+  if (a.d_x != nullptr && !one)
+    hipLaunchKernelGGL(router_grad_x_kernel, dim3(grad_x_blocks(a.T, a.H, false)),
+                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, a.eps, x, a.mask, dl, a.ws_beta,
+                       a.router_w, a.router_scale, a.pre_gain, static_cast<float*>(a.d_x));
 }
 
 // bf16 inputs.
@@ -1203,18 +1306,23 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   bf16* cols = rows + 2 * Tp * Ep;
   bf16* wt = cols + 3 * Ep * Tp;
   uint8_t* live = reinterpret_cast<uint8_t*>(wt + 2 * a.H * Ep);
-  const int splits = router_grad_splits(a.T, a.H, a.E), tb = router_grad_row_blocks(a.T);
+  const int splits = grad_splits(a.T, a.H, a.E, true), tb = router_grad_row_blocks(a.T);
   hipLaunchKernelGGL(router_grad_rows_bf16_kernel, dim3(tb + (a.d_x != nullptr ? a.H / kRgWCols : 0)),
                      dim3(kRgRowThreads), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
                      a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits,
                      a.router_w, tb, rows, cols, wt, a.ws_beta, live, a.ws_part_pes);
   const int steps = ((int)(Tp / 32) + splits - 1) / splits;
+  const int x_lds = (int)(64 * Ep * 4);
+  const bool one = a.d_x != nullptr && grad_one_launch(a.T, a.H, a.E, true);
   auto gw = [&](auto mt, auto masked) {
     constexpr int MT = decltype(mt)::value;
-    hipLaunchKernelGGL((router_grad_w_bf16_kernel<MT, decltype(masked)::value>),
-                       dim3(a.H / 64, (a.E + 16 * MT - 1) / (16 * MT), splits),
-                       dim3(64 * kRgWaves), 0, s, a.T, a.H, a.E, steps, x, live, cols,
-                       a.ws_beta, a.pre_gain != nullptr, a.ws_part_g, a.ws_part_b);
+    const int cb = a.H / 64, ey = (a.E + 16 * MT - 1) / (16 * MT), wb = cb * ey * splits;
+    const int xb = one ? grad_x_blocks(a.T, a.H, true) : 0;
+    const int lds = xb > 0 && x_lds > kRgWBytes ? x_lds : kRgWBytes;
+    hipLaunchKernelGGL((router_grad_wx_bf16_kernel<MT, decltype(masked)::value>), dim3(wb + xb),
+                       dim3(64 * kRgWaves), lds, s, wb, ey, a.T, a.H, a.E, steps, a.eps, x, live,
+                       rows, cols, a.ws_beta, wt, a.router_scale, a.pre_gain, a.ws_part_g,
+                       a.ws_part_b, static_cast<bf16*>(a.d_x));
   };
   auto by_mask = [&](auto mt) {
     if (a.mask != nullptr) gw(mt, std::true_type{});
@@ -1224,10 +1332,10 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   // (20 us at 4096 tokens)
   if (a.E <= 32) by_mask(std::integral_constant<int, 2>{});
   else by_mask(std::integral_constant<int, 4>{});
-  if (a.d_x != nullptr) {
-    constexpr int tok = kRgXWaves * kRgXTok;  // per block
+  if (a.d_x != nullptr && !one) {
+    constexpr int tok = kRgXWaves * kRgXTok;
     hipLaunchKernelGGL(router_grad_x_bf16_kernel, dim3(a.H / 64, (a.T + tok - 1) / tok),
-                       dim3(64 * kRgXWaves), 64 * Ep * 4, s, a.T, a.H, a.E, a.eps, x, live, rows,
+                       dim3(64 * kRgXWaves), x_lds, s, a.T, a.H, a.E, a.eps, x, live, rows,
                        a.ws_beta, wt, a.router_scale, a.pre_gain, static_cast<bf16*>(a.d_x));
   }
 }
@@ -1267,14 +1375,13 @@ hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
 }
 
 // Splits of the tokens for G: one per 64 tokens, as many as two blocks a CU take
-// in one round (26B-A4B shapes: 5), 32 at most.
-int router_grad_splits(int T, int H, int E) {
-  const int blocks = H / 64 * ((E + 63) / 64);
-  const int by_cus = blocks >= 512 ? 1 : 512 / blocks, by_tokens = (T + 63) / 64;
+// in one round (26B-A4B shapes: 5), 32 at most; beside dx in one launch, what dx
+// leaves of a round.
+int router_grad_max_splits(int T, int H, int E) {
+  const int by_cus = kRgRound / grad_w_blocks(H, E), by_tokens = (T + 63) / 64;
   const int n = by_cus < by_tokens ? by_cus : by_tokens;
   return n < 1 ? 1 : n < 32 ? n : 32;
 }
-
 int router_grad_row_blocks(int T) { return (T + 31) / 32 * 32 / kRgTok; }
 
 size_t router_grad_dl_bytes(int T, int H, int E) {
@@ -1288,11 +1395,18 @@ hipError_t launch_router_grad(const RouterGradArgs& a, hipStream_t s) {
     else launch_grad_f32(a, s);
   }
   constexpr int per = kRgCols / 4;
-  hipLaunchKernelGGL(router_grad_finish_kernel, dim3(a.H / kRgCols + (a.E + per - 1) / per),
-                     dim3(kRgFinThreads), 0, s, a.H, a.E, a.T > 0 ? router_grad_splits(a.T, a.H, a.E) : 0,
-                     a.T > 0 ? router_grad_row_blocks(a.T) : 0, a.ws_part_g, a.ws_part_b,
-                     a.ws_part_pes, a.router_w, a.router_scale, a.pre_gain, a.d_router_w,
-                     a.d_router_scale, a.d_per_expert_scale, a.d_pre_gain);
+  const int splits = a.T > 0 ? grad_splits(a.T, a.H, a.E, a.x_bf16) : 0;
+  const int row_blocks = a.T > 0 ? router_grad_row_blocks(a.T) : 0;
+  auto finish = [&](auto eu) {
+    hipLaunchKernelGGL((router_grad_finish_kernel<decltype(eu)::value>),
+                       dim3(a.H / kRgCols + (a.E + per - 1) / per), dim3(kRgFinThreads), 0, s,
+                       a.H, a.E, splits, row_blocks, a.ws_part_g, a.ws_part_b, a.ws_part_pes,
+                       a.router_w, a.router_scale, a.pre_gain, a.d_router_w, a.d_router_scale,
+                       a.d_per_expert_scale, a.d_pre_gain);
+  };
+  if (a.E <= kRgParts) finish(std::integral_constant<int, 1>{});
+  else if (a.E <= 2 * kRgParts) finish(std::integral_constant<int, 2>{});
+  else finish(std::integral_constant<int, 4>{});
   return hipGetLastError();
 }
 
