@@ -438,7 +438,7 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 
 // ---------------------------------------------------------------------------
 // Many rows per group: tiles of TM rows x TN weight rows (gate_up: half gate,
-// half the matching up rows), WM x WN waves of 16 TI x 64, on k-tiles of one
+// half the matching up rows), WM x WN waves of 16 TI x 16 TJ, on k-tiles of one
 // 128-block.  Both operands go global -> LDS directly, a line being a row's 128
 // bytes; its 16-byte chunk c sits at position c ^ (line % 8), so the 16 rows
 // that a fragment load touches spread over the banks.  The activations have two
@@ -447,7 +447,7 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 // rows again as soon as it holds their fragments, into the same lines, and two
 // blocks of 256 columns fit into a CU.  The scales of up to KBS k-blocks sit in
 // LDS beside the ring, reloaded when those are used up.  A wave multiplies one
-// 16-row tile of activations by its four weight tiles, and scales the previous
+// 16-row tile of activations by its TJ weight tiles, and scales the previous
 // tile's results meanwhile.
 //
 // Bound by the matrix cores' power: at 4096 x 4096 x 16384 a k-block of a 256 x
@@ -459,9 +459,9 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 // ---------------------------------------------------------------------------
 constexpr int kRowGroup = 4;
 
-template <int WM, int WN, int TI>
+template <int WM, int WN, int TI, int TJ>
 struct TileShape {
-  static constexpr int TM = WM * TI * 16, TN = WN * 64, NW = WM * WN, THREADS = 64 * NW;
+  static constexpr int TM = WM * TI * 16, TN = WN * TJ * 16, NW = WM * WN, THREADS = 64 * NW;
   static constexpr bool OWN_W = WM == 1;                     // no wave shares its weights
   static constexpr int XSTAGE = TM * kBlk, WSTAGE = TN * kBlk;
   static constexpr int XCOPIES = XSTAGE / (THREADS * 16);    // per wave and stage
@@ -477,18 +477,19 @@ struct TileShape {
                 "copies cover a stage");
   static_assert(LDS <= 160 * 1024, "LDS per CU");
 };
-typedef TileShape<2, 4, 8> WideTile;    // 256 x 256, one block per CU
-typedef TileShape<1, 4, 8> PairTile;    // 128 x 256, two blocks per CU
-typedef TileShape<2, 2, 4> SmallTile;   // 128 x 128, two blocks per CU
+typedef TileShape<2, 4, 8, 4> WideTile;   // 256 x 256, one block per CU
+typedef TileShape<2, 4, 8, 3> Tile192;    // 256 x 192, one block per CU
+typedef TileShape<1, 4, 8, 4> PairTile;   // 128 x 256, two blocks per CU
+typedef TileShape<2, 2, 4, 4> SmallTile;  // 128 x 128, two blocks per CU
 static_assert(PairTile::TM * PairTile::HPITCH * 4 <= PairTile::TAB,
               "h is staged over the ring and the scales");
 static_assert(2 * SmallTile::LDS <= 160 * 1024 && 2 * PairTile::LDS <= 160 * 1024,
               "two blocks share a CU");
 
-template <int MODE, int WM, int WN, int TI, typename YT>
+template <int MODE, int WM, int WN, int TI, int TJ, typename YT>
 __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) {
-  typedef TileShape<WM, WN, TI> S;
-  constexpr int TJ = 4;  // weight tiles of 16 rows per wave
+  typedef TileShape<WM, WN, TI, TJ> S;
+  constexpr int NS = TJ == 4 ? 2 : TJ;  // weight scales of a wave and k-block
   constexpr int kTM = S::TM, kTN = S::TN, XC = S::XCOPIES, WC = S::WCOPIES;
   constexpr int KBS = S::KBS;
   static_assert(MODE != kGateUp || kTN == 256, "a gate_up tile makes one 128-block of h");
@@ -607,21 +608,23 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
     for (int i = 0; i < NX; ++i) s_x[(kr + step * i) * kTM + r] = v[i];
     if (tid < KBS * 4) s_w[tid] = vw;
   };
-  // this wave's weight tiles: their scale slots (the two halves of a gate_up
-  // wave, else one), fragment offsets
+  // this wave's weight tiles: the slots of their scales (of a gate_up wave's two
+  // halves; else of its 16-column tiles, none of which crosses a block of 128),
+  // fragment offsets
   const int fr = lane % 16, g = lane / 16;
-  int ws0, ws1;
+  int ws[NS];
   if constexpr (MODE == kGateUp) {
-    ws0 = 0;  // 128 gate columns from a multiple of 128
-    ws1 = 2 + (N + min(nbase + 32 * wn, N - 32)) / kBlk - wblk_up;
+    ws[0] = 0;  // 128 gate columns from a multiple of 128
+    ws[1] = 2 + (N + min(nbase + 32 * wn, N - 32)) / kBlk - wblk_up;
   } else {
-    ws0 = ws1 = wn / 2;
+#pragma unroll
+    for (int i = 0; i < NS; ++i) ws[i] = (nbase + 16 * (TJ * wn + i * TJ / NS)) / kBlk - wblk0;
   }
   // Lines 16 apart have the same swizzle, so a wave's tiles lie at constants
   // from its first: activations i * 16 lines, weights as wtile().
   const int xline = wm * TI * 16 + fr;
   const int xoff = xline * kBlk + (g ^ (xline & 7)) * 16;
-  const int wline = wn * (MODE == kGateUp ? 32 : 64) + fr;
+  const int wline = wn * (MODE == kGateUp ? 32 : 16 * TJ) + fr;
   const int woff = wline * kBlk + (g ^ (wline & 7)) * 16;
   auto wtile = [](int j) {
     return (MODE == kGateUp ? (j / 2) * (kTN / 2) + (j % 2) * 16 : j * 16) * kBlk;
@@ -642,15 +645,17 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
   };
   i32x8 fw[TJ], fx[2];
   f32x4 d[2][TJ];
-  float sx[2], sw[2];
+  float sx[2], sw[NS];
   // results of tile i (in d[i & 1]) times their scales
   auto scale_add = [&](int i) __attribute__((always_inline)) {
-    const float s0 = sx[i & 1] * sw[0], s1 = sx[i & 1] * sw[1];
+    float s[NS];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) s[n] = sx[i & 1] * sw[n];
 #pragma unroll
     for (int j = 0; j < TJ; ++j)
 #pragma unroll
       for (int r = 0; r < 4; ++r)
-        acc[i][j][r] = __builtin_fmaf(d[i & 1][j][r], j < TJ / 2 ? s0 : s1, acc[i][j][r]);
+        acc[i][j][r] = __builtin_fmaf(d[i & 1][j][r], s[j * NS / TJ], acc[i][j][r]);
   };
   auto read_first = [&](int st) __attribute__((always_inline)) {
 #pragma unroll
@@ -668,8 +673,8 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
   auto block = [&](int kt, int kl, auto st_tag, auto ti_tag) __attribute__((always_inline)) {
     constexpr int st = decltype(st_tag)::value;
     constexpr int TV = decltype(ti_tag)::value;
-    sw[0] = s_w[kl * 4 + ws0];
-    sw[1] = s_w[kl * 4 + ws1];
+#pragma unroll
+    for (int n = 0; n < NS; ++n) sw[n] = s_w[kl * 4 + ws[n]];
 #pragma unroll
     for (int i = 0; i < TV; ++i) {
       sx[i & 1] = s_x[kl * kTM + xline + 16 * i];
@@ -793,7 +798,7 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
 #pragma unroll
       for (int i = 0; i < TI; ++i) {
         if (i < nv && (wm * TI + i) * 16 / ROWS == pass) {
-          float* row = ys + ((wm * TI + i) * 16 % ROWS + fr) * PITCH + wn * 64 + 4 * g;
+          float* row = ys + ((wm * TI + i) * 16 % ROWS + fr) * PITCH + wn * 16 * TJ + 4 * g;
 #pragma unroll
           for (int j = 0; j < TJ; ++j) *reinterpret_cast<f32x4*>(row + 16 * j) = acc[i][j];
         }
@@ -822,10 +827,10 @@ hipError_t launch_stream(const B128Args& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int MODE, int WM, int WN, int TI, typename YT>
+template <int MODE, int WM, int WN, int TI, int TJ, typename YT>
 hipError_t launch_tile(const B128Args& a, hipStream_t s) {
-  typedef TileShape<WM, WN, TI> S;
-  auto kf = tile_b128_kernel<MODE, WM, WN, TI, YT>;
+  typedef TileShape<WM, WN, TI, TJ> S;
+  auto kf = tile_b128_kernel<MODE, WM, WN, TI, TJ, YT>;
   // set on every call: the attribute belongs to the current device
   const hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(kf),
                                            hipFuncAttributeMaxDynamicSharedMemorySize, S::LDS);
@@ -838,14 +843,14 @@ hipError_t launch_tile(const B128Args& a, hipStream_t s) {
 }
 template <typename S>
 struct Launch;
-template <int WM, int WN, int TI>
-struct Launch<TileShape<WM, WN, TI>> {
+template <int WM, int WN, int TI, int TJ>
+struct Launch<TileShape<WM, WN, TI, TJ>> {
   static hipError_t plain(const B128Args& a, bool y_bf16, hipStream_t s) {
-    return y_bf16 ? launch_tile<kPlain, WM, WN, TI, bf16>(a, s)
-                  : launch_tile<kPlain, WM, WN, TI, float>(a, s);
+    return y_bf16 ? launch_tile<kPlain, WM, WN, TI, TJ, bf16>(a, s)
+                  : launch_tile<kPlain, WM, WN, TI, TJ, float>(a, s);
   }
   static hipError_t gate_up(const B128Args& a, hipStream_t s) {
-    return launch_tile<kGateUp, WM, WN, TI, float>(a, s);
+    return launch_tile<kGateUp, WM, WN, TI, TJ, float>(a, s);
   }
 };
 
@@ -892,17 +897,20 @@ bool b128_streams(int T, int rows, int E, int H, int I) {
   return T <= kB128StreamTokens && again <= 96LL << 20;
 }
 
-// Whether a product of one group takes the 128 x 128 tiles: by the rounds of
-// blocks that each shape needs.  A round of 256 wide tiles takes some 8 units, of
-// 512 small ones (two per CU) 5, and one of at most 256 small ones 3.3 (at
-// 2112-long rows, 2816 columns: 256 / 1024 / 2048 / 4096 / 8192 tokens 21 / 24 /
-// 32 / 51 / 84 us small, 38 / 41 / 44 / 49 / 86 us wide).
-static bool linear_takes_small(long long rows, long long cols) {
-  const long long small = (rows + 127) / 128 * ((cols + 127) / 128);
-  const long long wide = (rows + 255) / 256 * ((cols + 255) / 256);
-  const long long rest = small % 512;
+// The tiles of a product of one group, by the rounds of blocks that each shape
+// needs.  A round of 256 tiles of 256 x 256 takes some 8 units, of 256 x 192 6.4, of
+// 512 small ones (two per CU) 5, and one of at most 256 small ones 3.3 (2112-long
+// rows, 2816 columns, 1024 / 2048 / 4096 / 8192 tokens: small 25 / 33 / 53 / 82 us,
+// 192 columns 33 / 35 / 40 / 73, 256 columns 38 / 41 / 46 / 82; 4096 x 4096 x 4096
+// 94, 109, 80).
+enum class Tile { kSmall, k192, kWide };
+static Tile linear_tile(long long rows, long long cols) {
+  auto tiles = [&](int tm, int tn) { return (rows + tm - 1) / tm * ((cols + tn - 1) / tn); };
+  const long long small = tiles(128, 128), rest = small % 512;
   const double s = 5.0 * (small / 512) + (rest == 0 ? 0.0 : rest <= 256 ? 3.3 : 5.0);
-  return s < 8.0 * ((wide + 255) / 256);
+  const double m = 6.4 * ((tiles(256, 192) + 255) / 256);
+  const double w = 8.0 * ((tiles(256, 256) + 255) / 256);
+  return s < m && s < w ? Tile::kSmall : m < w ? Tile::k192 : Tile::kWide;
 }
 
 // Whether the streaming blocks quantize their own rows: few enough of them that
@@ -939,8 +947,11 @@ hipError_t launch_linear_b128(const B128Args& a, const void* x, uint8_t* xq, flo
   // 24.4 and 30.6, 32 tokens 41.8 and 31.2; 8192 x 8192: 16 tokens 23.5 and 52.6)
   if (a.rows <= 16 || (a.rows + 15LL) / 16 * a.N * a.Kd <= 64LL << 20)
     return stream_linear<void>(a, y_bf16, s);
-  return linear_takes_small(a.rows, a.N) ? Launch<SmallTile>::plain(a, y_bf16, s)
-                                         : Launch<WideTile>::plain(a, y_bf16, s);
+  switch (linear_tile(a.rows, a.N)) {
+    case Tile::kSmall: return Launch<SmallTile>::plain(a, y_bf16, s);
+    case Tile::k192: return Launch<Tile192>::plain(a, y_bf16, s);
+    default: return Launch<WideTile>::plain(a, y_bf16, s);
+  }
 }
 
 // Four waves of one column tile, two k-blocks deep (26B-A4B at 64 tokens: 54.6

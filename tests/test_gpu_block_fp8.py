@@ -91,7 +91,8 @@ def _check_linear(x, q, s, y):
     (37, 1003, 1520), (64, 704, 2816), (127, 130, 704), (128, 96, 2960), (129, 97, 2960),
     (200, 1003, 208), (257, 257, 128), (300, 513, 6016), (513, 1, 16), (640, 2816, 704),
     (1025, 130, 2944),
-    (260, 130, 2816), (260, 130, 5632), (2, 40, 16384), (3, 40, 16384), (5, 70, 6016),
+    (260, 130, 2816), (260, 130, 5632), (4096, 2112, 272), (3001, 5632, 144),
+    (8192, 2816, 128), (4090, 2107, 3200), (2, 40, 16384), (3, 40, 16384), (5, 70, 6016),
     (8, 70, 6016), (9, 70, 512), (2500, 65, 64), (700, 1408, 1408)])
 def test_linear(T, N, K):
     """One k-block and many (up to, at and past the 22 whose scales a tile
