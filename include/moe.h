@@ -432,10 +432,11 @@ int moe_dequantize_b128(int32_t block_rows, int64_t batch, int32_t rows, int32_t
 /* y[t, n] = sum_k X[t, k] W[n, k], X what moe_quantize_b128(1, ...) makes of x
  * [T, in_features] bf16 (done inside the call), W the value of the weights
  * w_q [out_features, in_features], w_scale as above.  y [T, out_features] in
- * y_dtype.  Blocks add up in fp32; a block's 128 products, in large
- * batches, inside the 8-bit matrix instruction (off by at most 2^-12 of the sum
- * of their magnitudes, some 2^-19 in the root mean square).  T up to 65536, out_features up to
- * 262144, in_features a multiple of 16 up to 16384.  ws:
+ * y_dtype.  Blocks add up in fp32; a block's 128 products, in large batches,
+ * inside the 8-bit matrix instruction (off by at most 2^-12 of the sum of their
+ * magnitudes, some 2^-19 in the root mean square).  A NaN or an infinity in a row
+ * of x makes that row of y NaN.  T up to 65536, out_features up to 262144,
+ * in_features a multiple of 16 up to 16384.  ws:
  * moe_linear_b128_workspace_size(T, in_features) bytes, 256-byte aligned (0: the
  * sizes are not supported). */
 size_t moe_linear_b128_workspace_size(int32_t max_tokens, int32_t in_features);

@@ -103,7 +103,7 @@ __device__ __forceinline__ uint2 encode8(const float (&v)[8], float s) {
 // Rows: scale = max |v| * (1 / 448) per 128 values, in fp32, code = E4M3 nearest
 // to v / scale (fp32 division: bf16 inputs put many quotients exactly on a
 // decision point, where a reciprocal would change the code).  16 lanes a group,
-// 8 values a lane.
+// 8 values a lane.  Memory-bound: 4096 x 2816 in 10.5 us (3.3 TB/s).
 template <typename XT, bool PAD>
 __global__ __launch_bounds__(256) void quantize_rows128_kernel(long long rows, int cols,
                                                                const XT* __restrict__ in,
@@ -242,6 +242,10 @@ __device__ __forceinline__ void store4(YT* __restrict__ row, int n, int N, f32x4
 // instruction: the weight stream bounds these kernels, and that instruction adds
 // its products to 2^-25 of their magnitudes where the 8-bit one rounds to about
 // 2^-17 (an E4M3 code of h whose sum lies that near a decision point changes).
+//
+// 26B-A4B at 64 tokens: gate_up 81 us (507 MB of weights, 6.2 TB/s), down 55 us (254
+// MB and 5.8 MB of slots, 4.8 TB/s); at 1 token 11.7 and 6.4 us, the latency of one
+// pass over a row.
 //
 // FUSE: the block quantizes its own rows of x (bf16) or h (fp32) into LDS behind
 // the first weight loads, which saves a launch; otherwise their codes and scales
@@ -858,8 +862,8 @@ template <typename XT, bool PAD>
 hipError_t quantize_rows(long long rows, int cols, const void* x, uint8_t* q, float* scale,
                          hipStream_t s) {
   const long long lanes = rows * blocks_of(cols) * 16;
-  hipLaunchKernelGGL((quantize_rows128_kernel<XT, PAD>), dim3((unsigned)((lanes + 255) / 256)), dim3(256),
-                     0, s, rows, cols, static_cast<const XT*>(x), q, scale);
+  hipLaunchKernelGGL((quantize_rows128_kernel<XT, PAD>), dim3((unsigned)((lanes + 255) / 256)),
+                     dim3(256), 0, s, rows, cols, static_cast<const XT*>(x), q, scale);
   return hipGetLastError();
 }
 

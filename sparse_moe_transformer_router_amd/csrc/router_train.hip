@@ -97,6 +97,10 @@ __device__ __forceinline__ void group_softmax(float (&l)[4], float& inv, float& 
 // block's slots.  It writes its sums of P_e, its counts, its sum of lse^2 and its
 // number of live tokens; the second step adds the blocks in order.  A batch of
 // one block's size runs both steps in one launch.
+//
+// Reads the logits once: 65536 x 128 in 12.6 us (2.8 TB/s; 12 softmax waves a block
+// 12.2, 512 blocks 12.0 but a second step of 7.6 us instead of 4.7), 4096 x 128 in
+// 5.0 us, 64 in 4.1: there a launch and one round trip to memory.
 // ---------------------------------------------------------------------------
 constexpr int kBalWaves = 8, kBalCountWaves = 4;  // softmax, counts
 constexpr int kBalThreads = (kBalWaves + kBalCountWaves) * kWave;
@@ -293,7 +297,9 @@ __global__ __launch_bounds__(kBalFinThreads) void balance_final_kernel(
 // Gradient of g * loss[0] in the logits, g = *d_loss:
 //   d l_tj = g [ a E / N p_tj (f_j - sum_e f_e p_te) + 2 b / N lse_t p_tj ],
 // 0 for masked tokens and for a row of -inf.  Memory-bound: the logits read
-// and the gradient written once; f_e of a lane's four experts in registers.
+// and the gradient written once; f_e of a lane's four experts in registers
+// (65536 x 128: 17.3 us, 3.9 TB/s; 4096: 4.7 us; four tokens a group and step
+// instead of two 16.8 and 5.9).
 constexpr int kGradUnroll = 2;
 template <int G, bool VEC>
 __global__ __launch_bounds__(256) void balance_grad_kernel(
@@ -376,7 +382,9 @@ void by_group(int E, F go) {
 // First kernel, a wave per token: the routing weights' gradient to the
 // logits (q = softmax over the K picked, dl_k = q_k (d_k - sum_j q_j d_j) with
 // d_k = d_topk_w_k * per_expert_scale), plus the given d_logits; the two
-// norms; dl', beta, and the block's sums of d_topk_w_k q_k per expert.
+// norms; dl', beta, and the block's sums of d_topk_w_k q_k per expert.  Bound by
+// the latency of a token's chain (picks, logits, x, sums over 64 lanes): 9 us for
+// 301 tokens, 13 for 4096 of 2816 bf16 values (1.8 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kRgRowWaves = 16;  // a token each
 
@@ -576,7 +584,8 @@ __device__ __forceinline__ bool grad_block(int wb, int H, int ey, BlockAt& at) {
 
 template <int MT>
 __device__ __forceinline__ void router_grad_w(
-    BlockAt at, int T, int H, int E, int span, const float* __restrict__ x, const uint8_t* __restrict__ mask,
+    BlockAt at, int T, int H, int E, int span, const float* __restrict__ x,
+    const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, float* __restrict__ part_g,
     float* __restrict__ part_b) {
   __shared__ float acc_s[kRgWaves][16 * 2][kWave];
@@ -660,7 +669,8 @@ __device__ __forceinline__ void router_grad_w(
 // experts, four per lane and load (lanes 0-31 experts 8 s .. 8 s + 3, lanes
 // 32-63 the next four; W's rows in the same order).
 __device__ __forceinline__ void router_grad_x(
-    BlockAt at, bool vec, int T, int H, int E, float eps, const float* __restrict__ x, const uint8_t* __restrict__ mask,
+    BlockAt at, bool vec, int T, int H, int E, float eps, const float* __restrict__ x,
+    const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, const float* __restrict__ W,
     const float* __restrict__ scale, const float* __restrict__ pre_gain, float* __restrict__ dx) {
   const int wave = threadIdx.x / kWave, lane = lane_id();
@@ -891,11 +901,12 @@ __device__ __forceinline__ f32x4 mfma_bf16(bf16x8 a, bf16x8 b, f32x4 c) {
 // tokens a lane, and regrouped in registers: fragment i holds columns 4 (l % 16)
 // + i, so a lane's four results of a row are consecutive columns.  The next
 // step's x and parts of dl' are fetched during a step's products; what is left
-// is their latency (two column groups a block, which halves what L2 delivers,
-// took as long).
+// is their latency (19.8 us at 4096 tokens of 2816, 128 experts; two column groups
+// a block, which halves what L2 delivers, took as long).
 template <int MT, bool MASK>
 __device__ __forceinline__ void router_grad_w_bf16(
-    BlockAt at, unsigned char* smem, int T, int H, int E, int steps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
+    BlockAt at, unsigned char* smem, int T, int H, int E, int steps, const bf16* __restrict__ x,
+    const uint8_t* __restrict__ live,
     const bf16* __restrict__ cols, const float* __restrict__ beta, bool want_beta,
     float* __restrict__ part_g, float* __restrict__ part_b) {
   auto acc_s = reinterpret_cast<f32x4 (*)[kRgWaves][4][kWave]>(smem);  // [2]
@@ -1039,11 +1050,13 @@ __device__ __forceinline__ void router_grad_w_bf16(
 // W^T fragments go to LDS once (32 KB at 128 experts), the tokens' fragments and
 // the rows of x come straight from memory, one step ahead.  W^T is the first
 // operand: with its column order (wt_col) a lane's results of two tiles are eight
-// consecutive columns of a token, 16-byte loads of x and stores of dx.
+// consecutive columns of a token, 16-byte loads of x and stores of dx (18.4 us at
+// 4096 tokens, 46 MB of x and dx: 2.5 TB/s; 128 columns a block 22 us).
 constexpr int kRgXTok = 32;
 template <int WAVES>
 __device__ __forceinline__ void router_grad_x_bf16(
-    BlockAt at, unsigned char* smem, int T, int H, int E, float eps, const bf16* __restrict__ x, const uint8_t* __restrict__ live,
+    BlockAt at, unsigned char* smem, int T, int H, int E, float eps, const bf16* __restrict__ x,
+    const uint8_t* __restrict__ live,
     const bf16* __restrict__ rows, const float* __restrict__ beta, const bf16* __restrict__ wt,
     const float* __restrict__ scale, const float* __restrict__ pre_gain, bf16* __restrict__ dx) {
   bf16x8* ws = reinterpret_cast<bf16x8*>(smem);  // [4 tiles][KS][2][lane]
@@ -1146,7 +1159,8 @@ __global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_wx_bf16_kernel(
     router_grad_w_bf16<MT, MASK>(at, smem, T, H, E, steps, x, live, cols, beta,
                                  pre_gain != nullptr, part_g, part_b);
   else
-    router_grad_x_bf16<kRgWaves>(at, smem, T, H, E, eps, x, live, rows, beta, wt, scale, pre_gain, dx);
+    router_grad_x_bf16<kRgWaves>(at, smem, T, H, E, eps, x, live, rows, beta, wt, scale, pre_gain,
+                                 dx);
 }
 
 constexpr int kRgXWaves = 8;
@@ -1164,7 +1178,8 @@ __global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
 // per-expert scale's gradient from the first kernel's sums.  Its few blocks wait for
 // memory: all the loads of a thread's EU experts go out before the first is added
 // (128 experts, 2816 columns, 5 splits: 7.4 -> 5.5 us).
-constexpr int kRgCols = 32, kRgParts = 32 /* >= the splits */, kRgFinThreads = kRgCols / 4 * kRgParts;
+constexpr int kRgCols = 32, kRgParts = 32;  // thread rows, as many as splits or more
+constexpr int kRgFinThreads = kRgCols / 4 * kRgParts;
 template <int EU>
 __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
     int H, int E, int splits, int pes_blocks, const float* __restrict__ part_g,
@@ -1307,10 +1322,11 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   bf16* wt = cols + 3 * Ep * Tp;
   uint8_t* live = reinterpret_cast<uint8_t*>(wt + 2 * a.H * Ep);
   const int splits = grad_splits(a.T, a.H, a.E, true), tb = router_grad_row_blocks(a.T);
-  hipLaunchKernelGGL(router_grad_rows_bf16_kernel, dim3(tb + (a.d_x != nullptr ? a.H / kRgWCols : 0)),
-                     dim3(kRgRowThreads), 0, s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain,
-                     a.per_expert_scale, a.logits, a.topk_idx, a.mask, a.d_topk_w, a.d_logits,
-                     a.router_w, tb, rows, cols, wt, a.ws_beta, live, a.ws_part_pes);
+  const int wt_blocks = a.d_x != nullptr ? a.H / kRgWCols : 0;
+  hipLaunchKernelGGL(router_grad_rows_bf16_kernel, dim3(tb + wt_blocks), dim3(kRgRowThreads), 0,
+                     s, a.T, a.H, a.E, a.K, a.eps, x, a.pre_gain, a.per_expert_scale, a.logits,
+                     a.topk_idx, a.mask, a.d_topk_w, a.d_logits, a.router_w, tb, rows, cols, wt,
+                     a.ws_beta, live, a.ws_part_pes);
   const int steps = ((int)(Tp / 32) + splits - 1) / splits;
   const int x_lds = (int)(64 * Ep * 4);
   const bool one = a.d_x != nullptr && grad_one_launch(a.T, a.H, a.E, true);
@@ -1329,7 +1345,6 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
     else gw(mt, std::false_type{});
   };
   // 64 experts a wave: with 128 the parts could be fetched one tile ahead only
-  // (20 us at 4096 tokens)
   if (a.E <= 32) by_mask(std::integral_constant<int, 2>{});
   else by_mask(std::integral_constant<int, 4>{});
   if (a.d_x != nullptr && !one) {

@@ -379,9 +379,11 @@ def moe_quantize_b128(block_rows, w, q, scale, stream=None):
 def moe_dequantize_b128(block_rows, q, scale, out, stream=None):
     batch, rows, cols, ns = _b128_shape(block_rows, q, "q")
     dev = _device()
-    _check(_lib.moe_dequantize_b128(block_rows, batch, rows, cols, _arg("q", q, _CODE, q.numel(), dev),
+    _check(_lib.moe_dequantize_b128(block_rows, batch, rows, cols,
+                                    _arg("q", q, _CODE, q.numel(), dev),
                                     _arg("scale", scale, torch.float32, ns, dev),
-                                    _arg("out", out, torch.float32, q.numel(), dev), _stream(stream)))
+                                    _arg("out", out, torch.float32, q.numel(), dev),
+                                    _stream(stream)))
 
 
 def linear_b128_workspace(max_tokens: int, in_features: int, device="cuda") -> torch.Tensor:
