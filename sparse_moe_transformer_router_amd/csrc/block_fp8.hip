@@ -243,9 +243,9 @@ __device__ __forceinline__ void store4(YT* __restrict__ row, int n, int N, f32x4
 // its products to 2^-25 of their magnitudes where the 8-bit one rounds to about
 // 2^-17 (an E4M3 code of h whose sum lies that near a decision point changes).
 //
-// 26B-A4B at 64 tokens: gate_up 81 us (507 MB of weights, 6.2 TB/s), down 55 us (254
-// MB and 5.8 MB of slots, 4.8 TB/s); at 1 token 11.7 and 6.4 us, the latency of one
-// pass over a row.
+// 26B-A4B at 64 tokens, 113 experts with rows: gate_up 80 us (448 MB, 5.6 TB/s), down
+// 55 us (262 MB and 5.8 MB of slots, 4.8 TB/s); at 1 token 11.7 and 6.4 us, the
+// latency of one pass over a row.
 //
 // FUSE: the block quantizes its own rows of x (bf16) or h (fp32) into LDS behind
 // the first weight loads, which saves a launch; otherwise their codes and scales
