@@ -171,15 +171,18 @@ def _act(d: MoeDims):
     return torch.bfloat16 if d.act_dtype == MOE_BF16 else torch.float32
 
 
-def _stream(stream):
-    """The hipStream_t of a torch stream, the current one if none is given (asked
-    for by its raw handle: a torch.cuda.Stream object costs a few microseconds,
-    as much as a small call's launches)."""
-    if stream is None:
+def _stream(stream, dev: int = -1):
+    """The hipStream_t of a torch stream, the current one (of device dev, if the
+    caller knows it) if none is given: asked for by its raw handle, a
+    torch.cuda.Stream object costs a few microseconds, as much as a small call's
+    launches."""
+    if stream is not None:
+        return stream.cuda_stream
+    if dev < 0:
         if not torch.cuda.is_initialized():
             torch.cuda.init()
-        return torch._C._cuda_getCurrentRawStream(torch._C._cuda_getDevice())
-    return stream.cuda_stream
+        dev = torch._C._cuda_getDevice()
+    return torch._C._cuda_getCurrentRawStream(dev)
 
 
 def _check(rc: int):
@@ -223,7 +226,7 @@ def moe_router_logits(d, T, x, router_w, router_scale, per_expert_scale, pre_nor
         _arg("pre_norm_gain", pre_norm_gain, f32, H, dev, True),
         _arg("topk_idx", topk_idx, torch.int32, T * K, dev),
         _arg("topk_w", topk_w, f32, T * K, dev),
-        _arg("logits", logits, f32, T * E, dev), *_work(ws, dev), _stream(stream)))
+        _arg("logits", logits, f32, T * E, dev), *_work(ws, dev), _stream(stream, dev)))
 
 
 def moe_balance_loss(d, T, logits, topk_idx, token_mask, balance_coef, z_coef, loss,
@@ -235,7 +238,7 @@ def moe_balance_loss(d, T, logits, topk_idx, token_mask, balance_coef, z_coef, l
         _arg("topk_idx", topk_idx, torch.int32, T * d.top_k, dev),
         _arg("token_mask", token_mask, _MASK, T, dev, True), balance_coef, z_coef,
         _arg("loss", loss, f32, 4, dev), _arg("expert_counts", expert_counts, torch.int32, E, dev),
-        _arg("mean_probs", mean_probs, f32, E, dev), *_work(ws, dev), _stream(stream)))
+        _arg("mean_probs", mean_probs, f32, E, dev), *_work(ws, dev), _stream(stream, dev)))
 
 
 def moe_balance_loss_grad(d, T, logits, token_mask, expert_counts, loss, balance_coef, z_coef,
@@ -247,7 +250,7 @@ def moe_balance_loss_grad(d, T, logits, token_mask, expert_counts, loss, balance
         _arg("token_mask", token_mask, _MASK, T, dev, True),
         _arg("expert_counts", expert_counts, torch.int32, E, dev), _arg("loss", loss, f32, 4, dev),
         balance_coef, z_coef, _arg("d_loss", d_loss, f32, 1, dev),
-        _arg("d_logits", d_logits, f32, T * E, dev), _stream(stream)))
+        _arg("d_logits", d_logits, f32, T * E, dev), _stream(stream, dev)))
 
 
 def moe_router_grad(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, logits,
@@ -271,7 +274,7 @@ def moe_router_grad(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_
         _arg("d_router_scale", d_router_scale, f32, H, dev),
         _arg("d_per_expert_scale", d_per_expert_scale, f32, E, dev),
         _arg("d_pre_norm_gain", d_pre_norm_gain, f32, H, dev, True), *_work(ws, dev),
-        _stream(stream)))
+        _stream(stream, dev)))
 
 
 def moe_route(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx, topk_w,
@@ -373,7 +376,8 @@ def moe_quantize_b128(block_rows, w, q, scale, stream=None):
     _check(_lib.moe_quantize_b128(block_rows, batch, rows, cols,
                                   _arg("w", w, torch.bfloat16, w.numel(), dev),
                                   _arg("q", q, _CODE, w.numel(), dev),
-                                  _arg("scale", scale, torch.float32, ns, dev), _stream(stream)))
+                                  _arg("scale", scale, torch.float32, ns, dev),
+                                  _stream(stream, dev)))
 
 
 def moe_dequantize_b128(block_rows, q, scale, out, stream=None):
@@ -383,7 +387,7 @@ def moe_dequantize_b128(block_rows, q, scale, out, stream=None):
                                     _arg("q", q, _CODE, q.numel(), dev),
                                     _arg("scale", scale, torch.float32, ns, dev),
                                     _arg("out", out, torch.float32, q.numel(), dev),
-                                    _stream(stream)))
+                                    _stream(stream, dev)))
 
 
 def linear_b128_workspace(max_tokens: int, in_features: int, device="cuda") -> torch.Tensor:
@@ -404,7 +408,7 @@ def moe_linear_b128(T, x, w_q, w_scale, y, ws, stream=None):
         T, n, k, _arg("x", x, torch.bfloat16, T * k, dev), _arg("w_q", w_q, _CODE, n * k, dev),
         _arg("w_scale", w_scale, torch.float32, _blocks(n) * _blocks(k), dev),
         _arg("y", y, (torch.bfloat16, torch.float32), T * n, dev),
-        MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, *_work(ws, dev), _stream(stream)))
+        MOE_BF16 if y.dtype == torch.bfloat16 else MOE_F32, *_work(ws, dev), _stream(stream, dev)))
 
 
 def moe_expert_ffn_b128(d, T, x, w_gate_up_q, w_gate_up_scale, w_down_q, w_down_scale, topk_w,
@@ -422,7 +426,7 @@ def moe_expert_ffn_b128(d, T, x, w_gate_up_q, w_gate_up_scale, w_down_q, w_down_
         _arg("topk_w", topk_w, f32, S, dev), _arg("offsets", offsets, i32, E + 1, dev),
         _arg("sorted_slots", sorted_slots, i32, S, dev),
         _arg("y_slots", y_slots, torch.bfloat16 if d.slot_dtype == MOE_BF16 else f32, S * H, dev),
-        *_work(ws, dev), _stream(stream)))
+        *_work(ws, dev), _stream(stream, dev)))
 
 
 def moe_expert_gate_up(d, T, x, w_gate_up, offsets, sorted_slots, h, stream=None):

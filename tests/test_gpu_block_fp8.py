@@ -234,12 +234,32 @@ def _check_experts(x, guq, gus, dnq, dns, idx, w, y, out):
     return rms
 
 
+@pytest.mark.parametrize("T", [3, 20, 300])
+def test_linear_largest_weights(T):
+    """The widest matrix: codes up to the last of 2^32 bytes."""
+    N, K, n = 262144, 16384, 96
+    g = _gen(T)
+    x = _x(g, T, K)
+    q, s = _weights(g, 128, K, std=1.0 / K ** 0.5)
+    note(f"linear_b128, 4 GB of codes, T={T}")
+    qd = torch.zeros(N, K, dtype=torch.uint8, device="cuda")
+    sd = torch.zeros(N // 128, K // 128, device="cuda")
+    qd[-128:], sd[-1] = q.cuda(), s[0].cuda()
+    y = torch.full((T, N), 7.0, dtype=torch.bfloat16, device="cuda")
+    ws = lib.linear_b128_workspace(T, K)
+    lib.moe_linear_b128(T, x.bfloat16().cuda(), qd, sd, y, ws)
+    torch.cuda.synchronize()
+    assert not y[:, :-128].any()
+    keep = torch.arange(min(T, n))
+    _check_linear(x[keep], q, s, y[:, -128:].cpu()[keep])
+
+
 @pytest.mark.parametrize("T,H,E,K,I", [
     (1, 64, 1, 1, 32), (1, 256, 8, 8, 160), (2, 128, 4, 1, 96), (5, 192, 16, 3, 96),
     (37, 192, 16, 3, 96), (40, 320, 6, 2, 224), (200, 512, 128, 8, 64), (256, 64, 256, 16, 32),
     (257, 64, 256, 4, 32), (90, 320, 2, 2, 160), (300, 256, 8, 2, 192), (700, 192, 5, 1, 96),
     (1100, 2816, 3, 2, 704), (520, 8192, 2, 1, 288), (200, 2816, 3, 3, 704),
-    (20, 64, 4, 2, 3200), (300, 64, 4, 2, 3200), (4, 8192, 3, 2, 32), (3, 2816, 4, 4, 704)])
+    (20, 64, 4, 2, 3200), (300, 64, 4, 2, 3200), (65536, 64, 4, 2, 32), (4, 8192, 3, 2, 32), (3, 2816, 4, 4, 704)])
 def test_experts(T, H, E, K, I):
     """Both forms, with the quantizers inside the products and before them, ragged
     widths (up rows that start inside a block), one row to many per expert, more
