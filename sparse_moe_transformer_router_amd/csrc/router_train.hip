@@ -384,7 +384,7 @@ void by_group(int E, F go) {
 // d_k = d_topk_w_k * per_expert_scale), plus the given d_logits; the two
 // norms; dl', beta, and the block's sums of d_topk_w_k q_k per expert.  Bound by
 // the latency of a token's chain (picks, logits, x, sums over 64 lanes): 9 us for
-// 301 tokens, 13 for 4096 of 2816 bf16 values (1.8 TB/s).
+// 301 tokens, 12 for 4096 of 2816 bf16 values (1.9 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kRgRowWaves = 16;  // a token each
 
@@ -434,11 +434,12 @@ __device__ __forceinline__ void router_grad_token(
   for (int j = 0; j < 4; ++j) dl[j] = 0.0f;
   beta = 0.0f;
   if (!live) return;  // uniform over the wave
-  // in the order of what has to wait: the picks, x's row (6 pieces a lane at a
-  // time), the logits, then what the picks point at
+  // in the order of what has to wait: the picks, x's row (3 pieces a lane at a
+  // time: six took 104 registers and one block a CU, 8192 tokens 94 us in all
+  // instead of 87), the logits, then what the picks point at
   int e = d_w != nullptr && lane < K ? topk_idx[(size_t)t * K + lane] : -1;
   const float dw = d_w != nullptr && lane < K ? d_w[(size_t)t * K + lane] : 0.0f;
-  constexpr int XP = 6, XSTEP = 8 * kWave;
+  constexpr int XP = 3, XSTEP = 8 * kWave;
   const XT* xr = x + (size_t)t * H;
   Piece<XT> xp[XP];
   auto load_x = [&](int h0) {
@@ -803,7 +804,7 @@ __device__ __forceinline__ void split3(float v, bf16& a, bf16& b, bf16& c) {
   c = (bf16)(r - (float)b);
 }
 
-__global__ __launch_bounds__(kRgRowThreads) void router_grad_rows_bf16_kernel(
+__global__ __launch_bounds__(kRgRowThreads, 8) void router_grad_rows_bf16_kernel(
     int T, int H, int E, int K, float eps, const bf16* __restrict__ x,
     const float* __restrict__ pre_gain, const float* __restrict__ pes,
     const float* __restrict__ logits, const int32_t* __restrict__ topk_idx,
@@ -1046,12 +1047,11 @@ __device__ __forceinline__ void router_grad_w_bf16(
   }
 }
 
-// dx: a block takes 64 columns x 256 tokens, a wave 32 of the tokens.  The columns'
+// dx: a block takes 64 columns x 32 WAVES tokens, a wave 32 of the tokens.  The columns'
 // W^T fragments go to LDS once (32 KB at 128 experts), the tokens' fragments and
 // the rows of x come straight from memory, one step ahead.  W^T is the first
 // operand: with its column order (wt_col) a lane's results of two tiles are eight
-// consecutive columns of a token, 16-byte loads of x and stores of dx (18.4 us at
-// 4096 tokens, 46 MB of x and dx: 2.5 TB/s; 128 columns a block 22 us).
+// consecutive columns of a token, 16-byte loads of x and stores of dx.
 constexpr int kRgXTok = 32;
 template <int WAVES>
 __device__ __forceinline__ void router_grad_x_bf16(
@@ -1171,6 +1171,100 @@ __global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_bf16_kernel(
   extern __shared__ __align__(16) unsigned char smem[];
   router_grad_x_bf16<kRgXWaves>(BlockAt{(int)blockIdx.x, (int)blockIdx.y, 0}, smem, T, H, E, eps,
                                 x, live, rows, beta, wt, scale, pre_gain, dx);
+}
+
+// dx for many tokens, up to 128 experts: a block keeps the W^T of its 64 columns in
+// LDS and its waves go through tiles of 16 tokens, the next tile's fragments, all of
+// them, and rows of x on their way during a tile's products.  As many blocks as one
+// round holds.  The whole backward of 4096 / 8192 tokens, 2816 x 128, 58.1 / 92.3 us
+// with the kernel above, 55.1 / 81.9 with this one (and 3 pieces of x a lane in the
+// first kernel); 256 experts, whose fragments take twice the registers, 79.6 and
+// 81.7 at 4096 tokens.
+constexpr int kRgXSteps = 4;  // of 32 experts, at most
+__global__ __launch_bounds__(64 * kRgXWaves, 4) void router_grad_x_loop_kernel(
+    int T, int H, int E, int span, float eps, const bf16* __restrict__ x,
+    const uint8_t* __restrict__ live, const bf16* __restrict__ rows,
+    const float* __restrict__ beta, const bf16* __restrict__ wt,
+    const float* __restrict__ scale, const float* __restrict__ pre_gain, bf16* __restrict__ dx) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  bf16x8* ws = reinterpret_cast<bf16x8*>(smem);  // [4 tiles][KS][2][lane]
+  const int tid = threadIdx.x, lane = lane_id();
+  const int wave = __builtin_amdgcn_readfirstlane(tid / kWave);
+  const int c = lane % 16, g = lane / 16, h0 = blockIdx.x * 64;
+  const int KS = (E + 31) / 32, tiles = (T + 15) / 16;
+  const int i0 = blockIdx.y * span, i1 = min(tiles, i0 + span);
+  bf16x8 ft[kRgXSteps][2];
+  Piece<bf16> xp[2];
+  float be = 0.0f;
+  bool on = false;
+  auto load = [&](int i) __attribute__((always_inline)) {
+    const bf16* p = rows + (size_t)i * KS * 2 * kFrag + 8 * lane;
+#pragma unroll
+    for (int k = 0; k < kRgXSteps; ++k)
+#pragma unroll
+      for (int q = 0; q < 2; ++q)
+        ft[k][q] = *reinterpret_cast<const bf16x8*>(p + (2 * min(k, KS - 1) + q) * kFrag);
+    const int t = min(16 * i + c, T - 1);
+#pragma unroll
+    for (int p2 = 0; p2 < 2; ++p2) xp[p2].load(x + (size_t)t * H + h0 + 32 * p2 + 8 * g);
+    be = beta[t];
+    on = live[t] != 0;
+  };
+  int i = i0 + wave;
+  if (i < i1) load(i);
+  const bf16x8* src = reinterpret_cast<const bf16x8*>(wt + (size_t)h0 / 16 * KS * 2 * kFrag);
+#pragma unroll 4
+  for (int k = tid; k < 4 * KS * 2 * kWave; k += 64 * kRgXWaves) ws[k] = src[k];
+  // [2][64]: the columns' factors
+  float* gs = reinterpret_cast<float*>(smem + 64 * kRgXSteps * 32 * 4);
+  if (tid < 64) {
+    const float gn = pre_gain != nullptr ? pre_gain[h0 + tid] : 1.0f;
+    gs[tid] = gn * scale[h0 + tid];
+    gs[64 + tid] = pre_gain != nullptr ? gn * gn + eps : 1.0f;
+  }
+  __syncthreads();
+  for (; i < i1; i += kRgXWaves) {
+    bf16x8 f[kRgXSteps][2];
+#pragma unroll
+    for (int k = 0; k < kRgXSteps; ++k)
+#pragma unroll
+      for (int q = 0; q < 2; ++q) f[k][q] = ft[k][q];
+    const Piece<bf16> x0 = xp[0], x1 = xp[1];
+    const float b = be;
+    const bool live_t = on;
+    const int t = 16 * i + c;
+    if (i + kRgXWaves < i1) load(i + kRgXWaves);
+    f32x4 acc[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0, 0, 0, 0};
+#pragma unroll
+    for (int k = 0; k < kRgXSteps; ++k) {
+      if (k >= KS) break;  // uniform
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const bf16x8 w0 = ws[((j * KS + k) * 2) * kWave + lane];
+        const bf16x8 w1 = ws[((j * KS + k) * 2 + 1) * kWave + lane];
+        acc[j] = mfma_bf16(w0, f[k][1], acc[j]);
+        acc[j] = mfma_bf16(w1, f[k][0], acc[j]);
+        acc[j] = mfma_bf16(w0, f[k][0], acc[j]);
+      }
+    }
+    if (t >= T) continue;
+#pragma unroll
+    for (int p = 0; p < 2; ++p) {  // columns h0 + 32 p + 8 g .. + 7
+      float xv[8], gc[8], ge[8];
+      (p == 0 ? x0 : x1).get(xv);
+      load8f(gs + 32 * p + 8 * g, gc);
+      load8f(gs + 64 + 32 * p + 8 * g, ge);
+      bf16x8 o;
+#pragma unroll
+      for (int u = 0; u < 8; ++u) {
+        const float v = gc[u] * acc[2 * p + u / 4][u % 4] - xv[u] * (b * ge[u]);
+        o[u] = (bf16)(live_t ? v : 0.0f);
+      }
+      *reinterpret_cast<bf16x8*>(dx + (size_t)t * H + h0 + 32 * p + 8 * g) = o;
+    }
+  }
 }
 
 // Last kernel: adds the splits of G; dW, dc and dg of 32 columns per block, four
@@ -1348,10 +1442,21 @@ void launch_grad_bf16(const RouterGradArgs& a, hipStream_t s) {
   if (a.E <= 32) by_mask(std::integral_constant<int, 2>{});
   else by_mask(std::integral_constant<int, 4>{});
   if (a.d_x != nullptr && !one) {
-    constexpr int tok = kRgXWaves * kRgXTok;
-    hipLaunchKernelGGL(router_grad_x_bf16_kernel, dim3(a.H / 64, (a.T + tok - 1) / tok),
-                       dim3(64 * kRgXWaves), x_lds, s, a.T, a.H, a.E, a.eps, x, live, rows,
-                       a.ws_beta, wt, a.router_scale, a.pre_gain, static_cast<bf16*>(a.d_x));
+    const int cb = a.H / 64;
+    if (a.E <= 32 * kRgXSteps) {
+      const int tiles = (a.T + 15) / 16, want = cb < kRgRound ? kRgRound / cb : 1;
+      const int each = (tiles + want - 1) / want;
+      const int span = (each + kRgXWaves - 1) / kRgXWaves * kRgXWaves;
+      hipLaunchKernelGGL(router_grad_x_loop_kernel, dim3(cb, (tiles + span - 1) / span),
+                         dim3(64 * kRgXWaves), 64 * 32 * kRgXSteps * 4 + 512, s, a.T, a.H, a.E,
+                         span, a.eps, x, live, rows, a.ws_beta, wt, a.router_scale, a.pre_gain,
+                         static_cast<bf16*>(a.d_x));
+    } else {
+      constexpr int tok = kRgXWaves * kRgXTok;
+      hipLaunchKernelGGL(router_grad_x_bf16_kernel, dim3(cb, (a.T + tok - 1) / tok),
+                         dim3(64 * kRgXWaves), x_lds, s, a.T, a.H, a.E, a.eps, x, live, rows,
+                         a.ws_beta, wt, a.router_scale, a.pre_gain, static_cast<bf16*>(a.d_x));
+    }
   }
 }
 

@@ -277,7 +277,8 @@ def test_router_grad_inputs_given(pre, aux, use_w):
 
 
 @pytest.mark.parametrize("T,H,E,K,bf16", [(5000, 2816, 128, 8, True), (5000, 2816, 128, 8, False),
-                                          (65536, 192, 16, 2, True), (65536, 64, 7, 2, False)])
+                                          (65536, 192, 16, 2, True), (65536, 64, 7, 2, False),
+                                          (2003, 2816, 200, 8, True), (3001, 1408, 60, 4, True)])
 def test_router_grad_large(T, H, E, K, bf16):
     c = _router_case(T, H, E, K, bf16, True, True, True, "some", T + H)
     note(f"router grad, large, T={T} H={H} E={E} bf16={bf16}")
