@@ -605,23 +605,37 @@ __device__ __forceinline__ void router_grad_w(
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
   float bs[2] = {0.0f, 0.0f};
-  constexpr int U = 4;  // pairs of tokens loaded before the first is used
+  // U pairs of tokens at a time, the next ones' loads on their way during a group's
+  // products; a token past the last or a masked one counts as zeros, whatever its
+  // rows hold
+  constexpr int U = 2;
+  float na[U][MT], nb[U][2], nbe[U];
+  bool non[U];
+  auto load = [&](int t) __attribute__((always_inline)) {
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int tt = t + 2 * u + g, tc = min(tt, t1 - 1);
+      non[u] = tt < t1 && (mask == nullptr || mask[tc] != 0);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) na[u][i] = dl[(size_t)tc * E + min(e0 + 32 * i + c, E - 1)];
+#pragma unroll
+      for (int j = 0; j < 2; ++j) nb[u][j] = x[(size_t)tc * H + h0 + 32 * j + c];
+      nbe[u] = beta[tc];
+    }
+  };
+  if (t0 < t1) load(t0);
   for (int t = t0; t < t1; t += 2 * U) {
     float a[U][MT], b[U][2], be[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int tt = t + 2 * u + g, tc = min(tt, t1 - 1);
-      const bool on = tt < t1 && (mask == nullptr || mask[tc] != 0);
 #pragma unroll
-      for (int i = 0; i < MT; ++i) {
-        const int e = e0 + 32 * i + c;
-        a[u][i] = on && e < E ? dl[(size_t)tc * E + min(e, E - 1)] : 0.0f;
-      }
+      for (int i = 0; i < MT; ++i) a[u][i] = non[u] && e0 + 32 * i + c < E ? na[u][i] : 0.0f;
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        b[u][j] = on ? x[(size_t)tc * H + h0 + 32 * j + c] : 0.0f;
-      be[u] = on ? beta[tc] : 0.0f;
+      for (int j = 0; j < 2; ++j) b[u][j] = non[u] ? nb[u][j] : 0.0f;
+      be[u] = non[u] ? nbe[u] : 0.0f;
     }
+    load(min(t + 2 * U, t1 - 1));
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
 #pragma unroll
@@ -631,6 +645,7 @@ __device__ __forceinline__ void router_grad_w(
 #pragma unroll
       for (int j = 0; j < 2; ++j) bs[j] = __builtin_fmaf(b[u][j] * b[u][j], be[u], bs[j]);
     }
+    __builtin_amdgcn_sched_barrier(0);
   }
   const bool want_b = at.y == 0;
   if (want_b) {
@@ -685,63 +700,82 @@ __device__ __forceinline__ void router_grad_x(
     for (int j = 0; j < 2; ++j)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-  for (int e0 = 0; e0 < E; e0 += 8) {
-    float a[2][4], b[4][2];
+  float na[2][4], nb[4][2];  // of the next step
+  auto load = [&](int e0) __attribute__((always_inline)) {
+    const int e = e0 + 4 * g;
 #pragma unroll
     for (int i = 0; i < 2; ++i) {
       const float* row = dl + (size_t)min(t0 + 32 * i + c, T - 1) * E;
-      const int e = e0 + 4 * g;
-      if (vec && e + 3 < E) {
-        const float4 v = *reinterpret_cast<const float4*>(row + e);
-        a[i][0] = v.x; a[i][1] = v.y; a[i][2] = v.z; a[i][3] = v.w;
+      if (vec) {  // E % 4 == 0: all four exist or none
+        const float4 v = *reinterpret_cast<const float4*>(row + min(e, E - 4));
+        na[i][0] = v.x; na[i][1] = v.y; na[i][2] = v.z; na[i][3] = v.w;
       } else {
 #pragma unroll
-        for (int k = 0; k < 4; ++k) a[i][k] = e + k < E ? row[e + k] : 0.0f;
+        for (int k = 0; k < 4; ++k) na[i][k] = row[min(e + k, E - 1)];
       }
     }
 #pragma unroll
-    for (int k = 0; k < 4; ++k) {
-      const int e = e0 + 4 * g + k;
+    for (int k = 0; k < 4; ++k)
 #pragma unroll
-      for (int j = 0; j < 2; ++j)
-        b[k][j] = e < E ? W[(size_t)e * H + h0 + 32 * j + c] : 0.0f;
+      for (int j = 0; j < 2; ++j) nb[k][j] = W[(size_t)min(e + k, E - 1) * H + h0 + 32 * j + c];
+  };
+  load(0);
+  for (int e0 = 0; e0 < E; e0 += 8) {
+    float a[2][4], b[4][2];
+#pragma unroll
+    for (int k = 0; k < 4; ++k) {
+      const bool on = e0 + 4 * g + k < E;
+#pragma unroll
+      for (int i = 0; i < 2; ++i) a[i][k] = on ? na[i][k] : 0.0f;
+#pragma unroll
+      for (int j = 0; j < 2; ++j) b[k][j] = on ? nb[k][j] : 0.0f;
     }
+    load(min(e0 + 8, E - 1));
+    __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
     for (int k = 0; k < 4; ++k)
 #pragma unroll
       for (int i = 0; i < 2; ++i)
 #pragma unroll
         for (int j = 0; j < 2; ++j) acc[i][j] = mfma_f32(a[i][k], b[k][j], acc[i][j]);
+    __builtin_amdgcn_sched_barrier(0);
   }
-  // a tile's loads all before its first store
+  float gc[2], ge[2];
 #pragma unroll
   for (int j = 0; j < 2; ++j) {
     const int h = h0 + 32 * j + c;
     const float gn = pre_gain != nullptr ? pre_gain[h] : 1.0f;
-    const float gc = gn * scale[h], ge = pre_gain != nullptr ? gn * gn + eps : 1.0f;
+    gc[j] = gn * scale[h];
+    ge[j] = pre_gain != nullptr ? gn * gn + eps : 1.0f;
+  }
+  // 32 tokens' loads all before their first store
 #pragma unroll
-    for (int i = 0; i < 2; ++i) {
-      float xv[16], be[16];
-      bool on[16];
+  for (int i = 0; i < 2; ++i) {
+    float xv[2][16], be[16];
+    bool on[16];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int t = min(t0 + 32 * i + mfma_row(q, g), T - 1);
-        on[q] = mask == nullptr || mask[t] != 0;
-        be[q] = beta[t];
-        xv[q] = x[(size_t)t * H + h];
-      }
+    for (int q = 0; q < 16; ++q) {
+      const int t = min(t0 + 32 * i + mfma_row(q, g), T - 1);
+      on[q] = mask == nullptr || mask[t] != 0;
+      be[q] = beta[t];
 #pragma unroll
-      for (int q = 0; q < 16; ++q) {
-        const int t = t0 + 32 * i + mfma_row(q, g);
-        if (t < T)
-          dx[(size_t)t * H + h] = on[q] ? gc * acc[i][j][q] - xv[q] * (be[q] * ge) : 0.0f;
-      }
+      for (int j = 0; j < 2; ++j) xv[j][q] = x[(size_t)t * H + h0 + 32 * j + c];
     }
+#pragma unroll
+    for (int q = 0; q < 16; ++q) {
+      const int t = t0 + 32 * i + mfma_row(q, g);
+      if (t < T)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+          dx[(size_t)t * H + h0 + 32 * j + c] =
+              on[q] ? gc[j] * acc[i][j][q] - xv[j][q] * (be[q] * ge[j]) : 0.0f;
+    }
+    __builtin_amdgcn_sched_barrier(0);
   }
 }
 
 template <int MT>
-__global__ __launch_bounds__(64 * kRgWaves) void router_grad_wx_kernel(
+__global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_wx_kernel(
     int wb, int ey, int T, int H, int E, int span, float eps, const float* __restrict__ x,
     const uint8_t* __restrict__ mask, const float* __restrict__ dl,
     const float* __restrict__ beta, const float* __restrict__ W, const float* __restrict__ scale,
@@ -754,7 +788,7 @@ __global__ __launch_bounds__(64 * kRgWaves) void router_grad_wx_kernel(
     router_grad_x(at, E % 4 == 0, T, H, E, eps, x, mask, dl, beta, W, scale, pre_gain, dx);
 }
 
-__global__ __launch_bounds__(64 * kRgWaves) void router_grad_x_kernel(
+__global__ __launch_bounds__(64 * kRgWaves, 2) void router_grad_x_kernel(
     int T, int H, int E, float eps, const float* __restrict__ x, const uint8_t* __restrict__ mask,
     const float* __restrict__ dl, const float* __restrict__ beta, const float* __restrict__ W,
     const float* __restrict__ scale, const float* __restrict__ pre_gain, float* __restrict__ dx) {
@@ -1355,26 +1389,38 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
   }
 }
 
-// G's partials and dx take one launch where dx and one split of G fit into one
-// round of blocks: two a CU with bf16 inputs, one with fp32 (whose G needs the
-// registers of two).  At 26B-A4B's shape, all of the router's backward and the
-// balance loss: bf16 48 / 301 / 1024 / 2048 tokens 24.9 / 32.1 / 35.5 / 43.5 us in
-// two launches, 20.0 / 25.8 / 31.4 / 43.5 in one; fp32 48 / 301 / 1024 tokens 47.2 /
-// 70.2 / 84.5 and 36.6 / 56.4 / 110.8.
+// G's partials and dx take one launch where dx and a split of G (fp32, whose G takes
+// longer: two) fit into one round of blocks, two a CU with bf16 inputs, one with
+// fp32.  At 26B-A4B's shape, all of the router's backward: bf16 48 / 301 / 1024 /
+// 2048 tokens 24.9 / 32.1 / 35.5 / 43.5 us in two launches, 20.0 / 25.8 / 31.4 / 43.5
+// in one; fp32 48 / 512 / 1024 tokens 47.2 / 72.9 / 70.6 and 36.6 / 46.7 / 93.6.
 constexpr int kRgRound = 512;
 int grad_round(bool bf16_in) { return bf16_in ? kRgRound : kRgRound / 2; }
-int grad_w_blocks(int H, int E) { return H / 64 * ((E + 63) / 64); }  // of a split
+int grad_w_blocks(int H, int E, bool bf16_in) {  // of a split
+  const int experts = bf16_in ? 64 : 128;        // of a block
+  return H / 64 * ((E + experts - 1) / experts);
+}
+// Splits of the tokens for G: one per 64 tokens, as many as two blocks a CU take in
+// one round (26B-A4B's shape: bf16 5, fp32 11), 32 at most; beside dx in one launch
+// what dx leaves of a round.
+int grad_max_splits(int T, int H, int E, bool bf16_in) {
+  const int by_cus = kRgRound / grad_w_blocks(H, E, bf16_in), by_tokens = (T + 63) / 64;
+  const int n = by_cus < by_tokens ? by_cus : by_tokens;
+  return n < 1 ? 1 : n < 32 ? n : 32;
+}
 int grad_x_blocks(int T, int H, bool bf16_in) {
   const int tok = kRgWaves * (bf16_in ? kRgXTok : 64);
   return H / 64 * ((T + tok - 1) / tok);
 }
 bool grad_one_launch(int T, int H, int E, bool bf16_in) {
-  return grad_x_blocks(T, H, bf16_in) + grad_w_blocks(H, E) <= grad_round(bf16_in);
+  return grad_x_blocks(T, H, bf16_in) + grad_w_blocks(H, E, bf16_in) * (bf16_in ? 1 : 2) <=
+         grad_round(bf16_in);
 }
 int grad_splits(int T, int H, int E, bool bf16_in) {
-  const int most = router_grad_max_splits(T, H, E);
+  const int most = grad_max_splits(T, H, E, bf16_in);
   if (!grad_one_launch(T, H, E, bf16_in)) return most;
-  const int n = (grad_round(bf16_in) - grad_x_blocks(T, H, bf16_in)) / grad_w_blocks(H, E);
+  const int n = (grad_round(bf16_in) - grad_x_blocks(T, H, bf16_in)) /
+                grad_w_blocks(H, E, bf16_in);
   return n < 1 ? 1 : n < most ? n : most;
 }
 
@@ -1494,14 +1540,10 @@ hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-// Splits of the tokens for G: one per 64 tokens, as many as two blocks a CU take
-// in one round (26B-A4B shapes: 5), 32 at most; beside dx in one launch, what dx
-// leaves of a round.
-int router_grad_max_splits(int T, int H, int E) {
-  const int by_cus = kRgRound / grad_w_blocks(H, E), by_tokens = (T + 63) / 64;
-  const int n = by_cus < by_tokens ? by_cus : by_tokens;
-  return n < 1 ? 1 : n < 32 ? n : 32;
-}
+// Workspaces hold as many splits as either type takes: fp32, whose blocks take more
+// experts.
+int router_grad_max_splits(int T, int H, int E) { return grad_max_splits(T, H, E, false); }
+
 int router_grad_row_blocks(int T) { return (T + 31) / 32 * 32 / kRgTok; }
 
 size_t router_grad_dl_bytes(int T, int H, int E) {
