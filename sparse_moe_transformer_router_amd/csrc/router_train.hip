@@ -1391,9 +1391,10 @@ __global__ __launch_bounds__(kRgFinThreads) void router_grad_finish_kernel(
 
 // G's partials and dx take one launch where dx and a split of G (fp32, whose G takes
 // longer: two) fit into one round of blocks, two a CU with bf16 inputs, one with
-// fp32.  At 26B-A4B's shape, all of the router's backward: bf16 48 / 301 / 1024 /
-// 2048 tokens 24.9 / 32.1 / 35.5 / 43.5 us in two launches, 20.0 / 25.8 / 31.4 / 43.5
-// in one; fp32 48 / 512 / 1024 tokens 47.2 / 72.9 / 70.6 and 36.6 / 46.7 / 93.6.
+// fp32.  At 26B-A4B's shape, all of the router's backward: bf16 48 / 301 / 1024
+// tokens 22.6 / 28.9 / 34.2 us in two launches, 19.0 / 24.4 / 31.0 in one (2048, forced:
+// 43.5 in both); fp32 48 / 301 / 768 tokens 39.3 / 56.7 / 66.9 and 30.1 / 45.8 / 48.9
+// (1024, forced: 70.6 and 93.6).
 constexpr int kRgRound = 512;
 int grad_round(bool bf16_in) { return bf16_in ? kRgRound : kRgRound / 2; }
 int grad_w_blocks(int H, int E, bool bf16_in) {  // of a split
