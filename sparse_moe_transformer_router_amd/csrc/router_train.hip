@@ -567,7 +567,8 @@ __device__ __forceinline__ int mfma_row(int q, int g) { return 8 * (q / 4) + 4 *
 // G partial of one split of the tokens: a wave takes 32 MT experts x 64
 // columns of x, the block's four waves four quarters of the split's tokens,
 // added through LDS.  The wave also sums x^2 beta for its columns (experts'
-// tile 0 only).
+// tile 0 only).  4096 tokens, 2816 x 128: 51 us (58 TF/s), the latency of loads that
+// run one step ahead at two waves a SIMD; without that step and a wave a SIMD 81.
 constexpr int kRgWaves = 4;
 struct BlockAt { int col, y, z; };  // 64 columns; experts or tokens; split
 
@@ -586,9 +587,8 @@ __device__ __forceinline__ bool grad_block(int wb, int H, int ey, BlockAt& at) {
 template <int MT>
 __device__ __forceinline__ void router_grad_w(
     BlockAt at, int T, int H, int E, int span, const float* __restrict__ x,
-    const uint8_t* __restrict__ mask,
-    const float* __restrict__ dl, const float* __restrict__ beta, float* __restrict__ part_g,
-    float* __restrict__ part_b) {
+    const uint8_t* __restrict__ mask, const float* __restrict__ dl,
+    const float* __restrict__ beta, float* __restrict__ part_g, float* __restrict__ part_b) {
   __shared__ float acc_s[kRgWaves][16 * 2][kWave];
   __shared__ float b_s[kRgWaves][64];
   const int wave = threadIdx.x / kWave, lane = lane_id();
@@ -683,7 +683,9 @@ __device__ __forceinline__ void router_grad_w(
 
 // dx: a wave takes 64 tokens x 64 columns; the contraction runs over the
 // experts, four per lane and load (lanes 0-31 experts 8 s .. 8 s + 3, lanes
-// 32-63 the next four; W's rows in the same order).
+// 32-63 the next four; W's rows in the same order).  4096 tokens, 2816 x 128: 82 us
+// (36 TF/s), 32 lines of dl' and 8 of W a step of 16 products; with no step ahead and
+// the tokens' factors loaded again for every 32 columns 123.
 __device__ __forceinline__ void router_grad_x(
     BlockAt at, bool vec, int T, int H, int E, float eps, const float* __restrict__ x,
     const uint8_t* __restrict__ mask,
