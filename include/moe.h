@@ -31,7 +31,9 @@
  *     MOE_ERR_HIP.
  *   - T = 0 is a valid no-op.
  *   - No call allocates device memory.  Calls that need scratch take a
- *     workspace `ws` of at least moe_workspace_size() bytes, 256-byte aligned.
+ *     workspace `ws` of at least moe_workspace_size() bytes, 256-byte aligned;
+ *     moe_balance_loss, moe_router_grad, moe_expert_ffn_b128 and
+ *     moe_linear_b128 have size functions of their own.
  *     Two calls in flight must not share a workspace.
  *   - Pointers must be 16-byte aligned.
  *   - Preconditions that are not checked: inputs are finite; topk_idx given to
@@ -143,9 +145,14 @@ typedef struct gemma4_ffn_weights {
   float layer_scalar;      /* multiplies (FFN + residual) */
 } gemma4_ffn_weights;
 
-/* Bytes of workspace sufficient for every call below with T <= max_tokens.
- * Returns 0 if the dimensions are unsupported (moe_last_error() says why). */
+/* Bytes of workspace sufficient for T <= max_tokens: for every call below that
+ * has no size function of its own, and for each of the three that follow.  A
+ * buffer of the largest of them serves all.  Returns 0 if the dimensions are
+ * unsupported (moe_last_error() says why). */
 size_t moe_workspace_size(const moe_dims* dims, int32_t max_tokens);
+size_t moe_balance_loss_workspace_size(const moe_dims* dims, int32_t max_tokens);
+size_t moe_router_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
+size_t moe_expert_ffn_b128_workspace_size(const moe_dims* dims, int32_t max_tokens);
 
 /* Message of the last failure on the calling thread ("" if none). */
 const char* moe_last_error(void);

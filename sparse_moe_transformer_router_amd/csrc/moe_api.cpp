@@ -83,6 +83,13 @@ int check_tokens(const moe_dims* d, int32_t T) {
     if ((p) && !aligned16(p)) return fail(MOE_ERR_ARG, "%s is not 16-byte aligned", #p); \
   } while (0)
 
+// The next region of a workspace: its offset, with `o` moved past it.
+size_t region(size_t& o, size_t bytes) {
+  const size_t at = o;
+  o += align256(bytes);
+  return at;
+}
+
 // Workspace regions (byte offsets), all 256-byte aligned, monotone in T so
 // that a workspace sized for max_tokens serves every T <= max_tokens.
 struct Layout {
@@ -94,12 +101,6 @@ struct Layout {
   size_t counter;                   // small-batch top-K completion counter
   size_t base_end;                  // end of the regions above (all but the MXFP8 ones)
   size_t xq, xs, hq, hs;            // MXFP8 activations of the 8-bit / 4-bit experts
-  // The training calls' and the block-scaled experts' scratch shares the bytes
-  // past base_end with the MXFP8 activations: a workspace serves one call at a
-  // time.
-  size_t bal_p, bal_n, bal_z, bal_live;      // balance loss
-  size_t rg_dl, rg_beta, rg_g, rg_b, rg_pes; // router backward
-  size_t b_xq, b_xs, b_h, b_hq, b_hs;        // block-scaled E4M3 experts
   size_t total;
 };
 
@@ -109,11 +110,7 @@ Layout layout(const moe_dims* d, long long T) {
   const long long nblk = (S + 1023) / 1024;
   const size_t act = dtype_size(d->act_dtype), slot = dtype_size(d->slot_dtype);
   size_t o = 0;
-  auto take = [&](size_t bytes) {
-    size_t at = o;
-    o += align256(bytes);
-    return at;
-  };
+  auto take = [&](size_t bytes) { return region(o, bytes); };
   L.r0 = take(4 * T);
   L.r = take(4 * T);
   L.logits = take(4 * T * d->num_experts);
@@ -137,31 +134,53 @@ Layout layout(const moe_dims* d, long long T) {
   L.hq = take((size_t)S * d->expert_inter);
   L.hs = take((size_t)S * (d->expert_inter / 32));
   L.total = o;
+  return L;
+}
+
+// The training calls and the block-scaled experts have workspaces of sizes of
+// their own: part of the layout above, their scratch would be asked of every
+// call (at 26B-A4B and one token 3.1 MB instead of 0.14).  Their regions come
+// after the layer's, whose bytes they do not touch.
+struct BalanceLayout { size_t p, n, z, live, total; };
+BalanceLayout balance_layout(const moe_dims* d, long long T) {
+  BalanceLayout L{};
+  const size_t E = (size_t)d->num_experts, nb = (size_t)moe::balance_blocks((int)T);
+  size_t o = layout(d, T).base_end;
+  L.p = region(o, 4 * nb * E);
+  L.n = region(o, 4 * nb * E);
+  L.z = region(o, 4 * nb);
+  L.live = region(o, 4 * nb);
+  L.total = o;
+  return L;
+}
+
+struct RouterGradLayout { size_t dl, beta, g, b, pes, total; };
+RouterGradLayout router_grad_layout(const moe_dims* d, long long T) {
+  RouterGradLayout L{};
   const size_t E = (size_t)d->num_experts, H = (size_t)d->hidden;
-  const size_t nb = (size_t)moe::balance_blocks((int)T);
-  o = L.base_end;
-  L.bal_p = take(4 * nb * E);
-  L.bal_n = take(4 * nb * E);
-  L.bal_z = take(4 * nb);
-  L.bal_live = take(4 * nb);
-  if (o > L.total) L.total = o;
   const size_t splits = (size_t)moe::router_grad_max_splits((int)T, d->hidden, d->num_experts);
-  o = L.base_end;
-  L.rg_dl = take(moe::router_grad_dl_bytes((int)T, d->hidden, d->num_experts));
-  L.rg_beta = take(4 * (((size_t)T + 31) / 32 * 32));
-  L.rg_g = take(4 * splits * E * H);
-  L.rg_b = take(4 * splits * H);
-  L.rg_pes = take(4 * (size_t)moe::router_grad_row_blocks((int)T) * E);
-  if (o > L.total) L.total = o;
-  const size_t I = (size_t)d->expert_inter;
+  size_t o = layout(d, T).base_end;
+  L.dl = region(o, moe::router_grad_dl_bytes((int)T, d->hidden, d->num_experts));
+  L.beta = region(o, 4 * (((size_t)T + 31) / 32 * 32));
+  L.g = region(o, 4 * splits * E * H);
+  L.b = region(o, 4 * splits * H);
+  L.pes = region(o, 4 * (size_t)moe::router_grad_row_blocks((int)T) * E);
+  L.total = o;
+  return L;
+}
+
+struct B128Layout { size_t xq, xs, h, hq, hs, total; };
+B128Layout b128_layout(const moe_dims* d, long long T) {
+  B128Layout L{};
+  const size_t H = (size_t)d->hidden, I = (size_t)d->expert_inter, S = (size_t)T * d->top_k;
   const size_t ts = (size_t)(T < moe::kB128StreamTokens ? T : moe::kB128StreamTokens);
-  o = L.base_end;
-  L.b_xq = take((size_t)T * ((H + 127) / 128 * 128));
-  L.b_xs = take(4 * (size_t)T * ((H + 127) / 128));
-  L.b_h = take(4 * ts * d->top_k * I);  // fp32, the weight-streaming form only
-  L.b_hq = take((size_t)S * ((I + 127) / 128 * 128));
-  L.b_hs = take(4 * (size_t)S * ((I + 127) / 128));
-  if (o > L.total) L.total = o;
+  size_t o = layout(d, T).base_end;
+  L.xq = region(o, (size_t)T * ((H + 127) / 128 * 128));
+  L.xs = region(o, 4 * (size_t)T * ((H + 127) / 128));
+  L.h = region(o, 4 * ts * d->top_k * I);  // fp32, the weight-streaming form only
+  L.hq = region(o, S * ((I + 127) / 128 * 128));
+  L.hs = region(o, 4 * S * ((I + 127) / 128));
+  L.total = o;
   return L;
 }
 
@@ -196,8 +215,7 @@ P* at(void* ws, size_t off) {
   return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
 }
 
-int check_ws(const moe_dims* d, int32_t T, const void* ws, size_t ws_bytes) {
-  const size_t need = layout(d, T).total;
+int check_ws(size_t need, int32_t T, const void* ws, size_t ws_bytes) {
   if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(ws) & 255u)
     return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
@@ -205,6 +223,9 @@ int check_ws(const moe_dims* d, int32_t T, const void* ws, size_t ws_bytes) {
     return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed for T=%d", ws_bytes, need,
                 T);
   return MOE_OK;
+}
+int check_ws(const moe_dims* d, int32_t T, const void* ws, size_t ws_bytes) {
+  return check_ws(layout(d, T).total, T, ws, ws_bytes);
 }
 
 // ---- scratch of the entry point that allocates nothing --------------------
@@ -490,6 +511,21 @@ size_t moe_workspace_size(const moe_dims* dims, int32_t max_tokens) {
   return layout(dims, max_tokens).total;
 }
 
+size_t moe_balance_loss_workspace_size(const moe_dims* dims, int32_t max_tokens) {
+  if (check_dims(dims, true) != MOE_OK || check_tokens(dims, max_tokens) != MOE_OK) return 0;
+  return balance_layout(dims, max_tokens).total;
+}
+
+size_t moe_router_grad_workspace_size(const moe_dims* dims, int32_t max_tokens) {
+  if (check_dims(dims, true) != MOE_OK || check_tokens(dims, max_tokens) != MOE_OK) return 0;
+  return router_grad_layout(dims, max_tokens).total;
+}
+
+size_t moe_expert_ffn_b128_workspace_size(const moe_dims* dims, int32_t max_tokens) {
+  if (check_dims(dims, true) != MOE_OK || check_tokens(dims, max_tokens) != MOE_OK) return 0;
+  return b128_layout(dims, max_tokens).total;
+}
+
 const char* moe_last_error(void) { return g_err.c_str(); }
 
 int moe_router(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
@@ -552,19 +588,19 @@ int moe_balance_loss(const moe_dims* dims, int32_t T, const float* logits,
   int rc;
   if ((rc = check_dims(dims)) || (rc = check_tokens(dims, T))) return rc;
   g_err.clear();
+  const auto L = balance_layout(dims, T);
   REQUIRE_PTR(loss); REQUIRE_PTR(expert_counts); REQUIRE_PTR(mean_probs);
   if (T > 0) {
     REQUIRE_PTR(logits); REQUIRE_PTR(topk_idx); OPTIONAL_PTR(token_mask);
-    if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+    if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
   }
-  const Layout L = layout(dims, T);
   moe::BalanceArgs a{};
   a.T = T; a.E = dims->num_experts; a.K = dims->top_k;
   a.balance_coef = balance_coef; a.z_coef = z_coef;
   a.logits = logits; a.topk_idx = topk_idx; a.mask = token_mask;
   a.loss = loss; a.counts = expert_counts; a.mean_p = mean_probs;
-  a.ws_part_p = at<float>(ws, L.bal_p); a.ws_part_n = at<int32_t>(ws, L.bal_n);
-  a.ws_part_z = at<float>(ws, L.bal_z); a.ws_part_live = at<int32_t>(ws, L.bal_live);
+  a.ws_part_p = at<float>(ws, L.p); a.ws_part_n = at<int32_t>(ws, L.n);
+  a.ws_part_z = at<float>(ws, L.z); a.ws_part_live = at<int32_t>(ws, L.live);
   hipError_t e = moe::launch_balance_loss(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_balance_loss");
 }
@@ -598,6 +634,7 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
   int rc;
   if ((rc = check_dims(dims)) || (rc = check_tokens(dims, T))) return rc;
   g_err.clear();
+  const auto L = router_grad_layout(dims, T);
   REQUIRE_PTR(router_w); REQUIRE_PTR(router_scale); OPTIONAL_PTR(pre_norm_gain);
   REQUIRE_PTR(d_router_w); REQUIRE_PTR(d_router_scale); REQUIRE_PTR(d_per_expert_scale);
   if (pre_norm_gain) {
@@ -612,9 +649,8 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
     if (d_topk_w) {
       REQUIRE_PTR(topk_idx); REQUIRE_PTR(per_expert_scale);
     }
-    if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+    if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
   }
-  const Layout L = layout(dims, T);
   moe::RouterGradArgs a{};
   a.T = T; a.H = dims->hidden; a.E = dims->num_experts; a.K = dims->top_k; a.eps = dims->eps;
   a.x_bf16 = dims->act_dtype == MOE_BF16;
@@ -623,9 +659,9 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
   a.topk_idx = topk_idx; a.mask = token_mask; a.d_topk_w = d_topk_w; a.d_logits = d_logits;
   a.d_x = d_x; a.d_router_w = d_router_w; a.d_router_scale = d_router_scale;
   a.d_per_expert_scale = d_per_expert_scale; a.d_pre_gain = d_pre_norm_gain;
-  a.ws_dl = at<void>(ws, L.rg_dl); a.ws_beta = at<float>(ws, L.rg_beta);
-  a.ws_part_g = at<float>(ws, L.rg_g); a.ws_part_b = at<float>(ws, L.rg_b);
-  a.ws_part_pes = at<float>(ws, L.rg_pes);
+  a.ws_dl = at<void>(ws, L.dl); a.ws_beta = at<float>(ws, L.beta);
+  a.ws_part_g = at<float>(ws, L.g); a.ws_part_b = at<float>(ws, L.b);
+  a.ws_part_pes = at<float>(ws, L.pes);
   hipError_t e = moe::launch_router_grad(a, static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_router_grad");
 }
@@ -890,27 +926,27 @@ int moe_expert_ffn_b128(const moe_dims* dims, int32_t T, const void* x,
   int rc;
   if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
   g_err.clear();
+  const auto L = b128_layout(dims, T);
   if (dims->act_dtype != MOE_BF16)
     return fail(MOE_ERR_UNSUPPORTED, "block-scaled E4M3 experts take bf16 activations");
   if (T == 0) return MOE_OK;
   REQUIRE_PTR(x); REQUIRE_PTR(w_gate_up_q); REQUIRE_PTR(w_gate_up_scale); REQUIRE_PTR(w_down_q);
   REQUIRE_PTR(w_down_scale); REQUIRE_PTR(topk_w); REQUIRE_PTR(expert_offsets);
   REQUIRE_PTR(sorted_slots); REQUIRE_PTR(y_slots);
-  if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
-  const Layout L = layout(dims, T);
+  if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
   moe::B128Args gu{};
   gu.T = T; gu.rows = T * dims->top_k; gu.E = dims->num_experts; gu.K = dims->top_k;
   gu.offsets = expert_offsets; gu.sorted_slots = sorted_slots; gu.topk_w = topk_w;
   moe::B128Args dn = gu;
   gu.Kd = dims->hidden; gu.N = dims->expert_inter;
-  gu.xq = at<uint8_t>(ws, L.b_xq); gu.xscale = at<float>(ws, L.b_xs);
+  gu.xq = at<uint8_t>(ws, L.xq); gu.xscale = at<float>(ws, L.xs);
   gu.wq = w_gate_up_q; gu.wscale = w_gate_up_scale;
-  gu.h = at<float>(ws, L.b_h); gu.hq = at<uint8_t>(ws, L.b_hq); gu.hscale = at<float>(ws, L.b_hs);
+  gu.h = at<float>(ws, L.h); gu.hq = at<uint8_t>(ws, L.hq); gu.hscale = at<float>(ws, L.hs);
   dn.Kd = dims->expert_inter; dn.N = dims->hidden;
   dn.xq = gu.hq; dn.xscale = gu.hscale; dn.wq = w_down_q; dn.wscale = w_down_scale;
   dn.y = y_slots;
-  hipError_t e = moe::launch_expert_ffn_b128(gu, dn, x, at<uint8_t>(ws, L.b_xq),
-                                             at<float>(ws, L.b_xs),
+  hipError_t e = moe::launch_expert_ffn_b128(gu, dn, x, at<uint8_t>(ws, L.xq),
+                                             at<float>(ws, L.xs),
                                              dims->slot_dtype == MOE_BF16,
                                              static_cast<hipStream_t>(stream));
   return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_b128");

@@ -51,6 +51,12 @@ class MoeError(RuntimeError):
         self.code = code
 
 
+# Size functions of the workspaces: of the calls named, of all others ("layer").
+_WS_SIZES = {"layer": "moe_workspace_size", "balance_loss": "moe_balance_loss_workspace_size",
+             "router_grad": "moe_router_grad_workspace_size",
+             "expert_ffn_b128": "moe_expert_ffn_b128_workspace_size"}
+
+
 def _load():
     if not os.path.exists(LIB_PATH):
         raise ImportError(f"{LIB_PATH} is missing: build it with "
@@ -58,8 +64,9 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     D = ctypes.POINTER(MoeDims)
-    L.moe_workspace_size.argtypes = [D, I32]
-    L.moe_workspace_size.restype = SZ
+    for f in _WS_SIZES.values():
+        getattr(L, f).argtypes = [D, I32]
+        getattr(L, f).restype = SZ
     L.moe_last_error.argtypes = []
     L.moe_last_error.restype = ctypes.c_char_p
     L.moe_router.argtypes = [D, I32] + [P] * 8 + [SZ, P]
@@ -194,16 +201,24 @@ def last_error() -> str:
     return _lib.moe_last_error().decode()
 
 
-def workspace_size(d: MoeDims, max_tokens: int) -> int:
-    n = _lib.moe_workspace_size(ctypes.byref(d), max_tokens)
-    if n == 0:
-        raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
-    return n
+def workspace_size(d: MoeDims, max_tokens: int, calls=tuple(_WS_SIZES)) -> int:
+    """Bytes that serve the calls named (any of "layer", "balance_loss", "router_grad",
+    "expert_ffn_b128", where "layer" is every call but the other three), all of
+    them by default."""
+    need = 0
+    for c in calls:
+        if c not in _WS_SIZES:
+            raise ValueError(f"calls names {c!r}, expected some of {tuple(_WS_SIZES)}")
+        n = getattr(_lib, _WS_SIZES[c])(ctypes.byref(d), max_tokens)
+        if n == 0:
+            raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
+        need = max(need, n)
+    return need
 
 
-def workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
-    """A uint8 device buffer of moe_workspace_size bytes (256-byte aligned)."""
-    return torch.empty(workspace_size(d, max_tokens), dtype=torch.uint8, device=device)
+def workspace(d: MoeDims, max_tokens: int, device="cuda", calls=tuple(_WS_SIZES)) -> torch.Tensor:
+    """A uint8 device buffer of workspace_size bytes (256-byte aligned)."""
+    return torch.empty(workspace_size(d, max_tokens, calls), dtype=torch.uint8, device=device)
 
 
 def moe_router(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx,
