@@ -204,7 +204,8 @@ int moe_router_logits(const moe_dims* dims, int32_t T, const void* x, const floa
  *   z       = 1/N sum_t (log sum_e exp logits_te)^2
  * Outputs: loss [4] fp32 = {balance_coef * balance + z_coef * z, balance, z, N},
  * expert_counts [E] int32 = n_e, mean_probs [E] fp32 = 1/N sum_t p_te.  N = 0
- * gives zeros.  Only num_experts and top_k of dims matter. */
+ * gives zeros.  Of dims only num_experts and top_k enter the result, and only
+ * num_experts the workspace; the others have to be valid. */
 int moe_balance_loss(const moe_dims* dims, int32_t T, const float* logits,
                      const int32_t* topk_idx, const uint8_t* token_mask, float balance_coef,
                      float z_coef, float* loss, int32_t* expert_counts, float* mean_probs,

@@ -139,13 +139,14 @@ Layout layout(const moe_dims* d, long long T) {
 
 // The training calls and the block-scaled experts have workspaces of sizes of
 // their own: part of the layout above, their scratch would be asked of every
-// call (at 26B-A4B and one token 3.1 MB instead of 0.14).  Their regions come
-// after the layer's, whose bytes they do not touch.
+// call (at 26B-A4B and one token 3.1 MB instead of 0.14).  Their regions start
+// at the workspace's first byte and hold nothing between calls, so a balance
+// loss of 65536 tokens asks for 0.3 MB, not for a layer's 9 GB beside it.
 struct BalanceLayout { size_t p, n, z, live, total; };
 BalanceLayout balance_layout(const moe_dims* d, long long T) {
   BalanceLayout L{};
   const size_t E = (size_t)d->num_experts, nb = (size_t)moe::balance_blocks((int)T);
-  size_t o = layout(d, T).base_end;
+  size_t o = 0;
   L.p = region(o, 4 * nb * E);
   L.n = region(o, 4 * nb * E);
   L.z = region(o, 4 * nb);
@@ -159,7 +160,7 @@ RouterGradLayout router_grad_layout(const moe_dims* d, long long T) {
   RouterGradLayout L{};
   const size_t E = (size_t)d->num_experts, H = (size_t)d->hidden;
   const size_t splits = (size_t)moe::router_grad_max_splits((int)T, d->hidden, d->num_experts);
-  size_t o = layout(d, T).base_end;
+  size_t o = 0;
   L.dl = region(o, moe::router_grad_dl_bytes((int)T, d->hidden, d->num_experts));
   L.beta = region(o, 4 * (((size_t)T + 31) / 32 * 32));
   L.g = region(o, 4 * splits * E * H);
@@ -174,7 +175,7 @@ B128Layout b128_layout(const moe_dims* d, long long T) {
   B128Layout L{};
   const size_t H = (size_t)d->hidden, I = (size_t)d->expert_inter, S = (size_t)T * d->top_k;
   const size_t ts = (size_t)(T < moe::kB128StreamTokens ? T : moe::kB128StreamTokens);
-  size_t o = layout(d, T).base_end;
+  size_t o = 0;
   L.xq = region(o, (size_t)T * ((H + 127) / 128 * 128));
   L.xs = region(o, 4 * (size_t)T * ((H + 127) / 128));
   L.h = region(o, 4 * ts * d->top_k * I);  // fp32, the weight-streaming form only

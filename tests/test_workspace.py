@@ -64,6 +64,20 @@ def test_size_functions_are_what_the_calls_ask_for(sizes):
         assert lib.workspace_size(d, T) == max(asks.values())
 
 
+def test_training_scratch_does_not_contain_a_layers():
+    """The balance loss: two values per expert and two more from each of at most 256
+    blocks, whatever the layer around it."""
+    a = lambda n: (n + 255) // 256 * 256  # noqa: E731
+    want = 2 * a(4 * 256 * 128) + 2 * a(4 * 256)
+    for sizes in ((2816, 128, 8, 704, 2112), (64, 128, 1, 32, 0), (8192, 128, 16, 8192, 0)):
+        d = lib.dims(*sizes)
+        assert lib.workspace_size(d, 65536, ("balance_loss",)) == want
+        assert _asks(d, 65536)["moe_balance_loss"] == want
+    # the router's backward does not know the experts' width
+    assert len({lib.workspace_size(lib.dims(2816, 128, 8, i, 0), 4096, ("router_grad",))
+                for i in (32, 704, 8192)}) == 1
+
+
 def test_refusals():
     for f in lib._WS_SIZES.values():
         size = getattr(L, f)
