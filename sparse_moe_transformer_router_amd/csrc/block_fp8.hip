@@ -773,17 +773,22 @@ __global__ __launch_bounds__(64 * WM * WN, 2) void tile_b128_kernel(B128Args a) 
       for (int i = 0; i < 32; ++i) m = max(m, mag(v[i]));
       const float s = scale_of(dpp_max<0x4E>(dpp_max<0xB1>(m)));
       // one division a row: h is an fp32 sum already, no decision point is hit
-      // exactly, and an ulp of the quotient moves no more codes than one of h
-      const float inv = s > 0.0f ? 1.0f / s : 0.0f;
+      // exactly, and an ulp of the quotient moves no more codes than one of h.  A
+      // scale that is no normal number has no reciprocal in fp32 (0 times infinity
+      // would make a NaN of every zero): there the quotients themselves
+      if (s >= 0x1p-126f) {
+        const float inv = 1.0f / s;
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] *= inv;
+      } else {
+#pragma unroll
+        for (int i = 0; i < 32; ++i) v[i] = s > 0.0f ? v[i] / s : 0.0f;
+      }
       if (!on) continue;  // columns past the last are zeros: the row's padding
       uint32_t q[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        float t[4];
-#pragma unroll
-        for (int u = 0; u < 4; ++u) t[u] = v[4 * i + u] * inv;
-        q[i] = encode4(t[0], t[1], t[2], t[3]);
-      }
+      for (int i = 0; i < 8; ++i)
+        q[i] = encode4(v[4 * i], v[4 * i + 1], v[4 * i + 2], v[4 * i + 3]);
       uint4* dst = reinterpret_cast<uint4*>(a.hq + (size_t)(row0 + r) * (nbh * kBlk) + nbase + c);
       dst[0] = make_uint4(q[0], q[1], q[2], q[3]);
       dst[1] = make_uint4(q[4], q[5], q[6], q[7]);
