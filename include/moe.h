@@ -226,7 +226,9 @@ int moe_balance_loss_grad(const moe_dims* dims, int32_t T, const float* logits,
  * d_router_w [E,H], d_router_scale [H], d_per_expert_scale [E],
  * d_pre_norm_gain [H] (exactly when pre_norm_gain is given), all fp32, all
  * overwritten.  The picks are constants; x, the parameters, logits and
- * topk_idx are the forward call's.  No output may overlap an input. */
+ * topk_idx are the forward call's.  Where a logit is -inf (an expert switched
+ * off), d_logits counts as 0, whatever it holds, and a pick takes part in
+ * nothing.  No output may overlap an input. */
 int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
                     const float* router_scale, const float* per_expert_scale,
                     const float* pre_norm_gain, const float* logits, const int32_t* topk_idx,

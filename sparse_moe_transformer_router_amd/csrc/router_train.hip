@@ -453,11 +453,13 @@ __device__ __forceinline__ void router_grad_token(
     const int ej = lane + kWave * j;
     l[j] = ej < E ? logits[(size_t)t * E + ej] : 0.0f;
     if (d_logits != nullptr && ej < E) dl[j] = d_logits[(size_t)t * E + ej];
+    if (l[j] == -INFINITY) dl[j] = 0.0f;  // an expert switched off
   }
-  // lane k < K: slot k (an id outside [0, E) is no slot)
+  // lane k < K: slot k (an id outside [0, E) or of an expert switched off is no slot)
   if ((unsigned)e >= (unsigned)E) e = -1;
   const float lk = e >= 0 ? logits[(size_t)t * E + e] : -INFINITY;
   const float pk = e >= 0 ? pes[e] : 0.0f;
+  if (lk == -INFINITY) e = -1;
   float ss = 0.0f, sg = 0.0f;
   for (int h0 = 8 * lane;; h0 += XP * XSTEP) {
 #pragma unroll
