@@ -176,15 +176,19 @@ int moe_router(const moe_dims* dims, int32_t T, const void* x, const float* rout
 /* ---- Training the router -------------------------------------------------
  *
  * A training step calls moe_router_logits (the routing, with the logits kept),
- * the experts and moe_combine as above, moe_balance_loss on the logits and the
- * picks, moe_balance_loss_grad for the loss's gradient in the logits, and
- * moe_router_grad with that gradient and the routing weights' (d_topk_w[t,k] =
- * the gradient of the layer's output against expert k's output for token t).
+ * moe_dispatch, the experts with weights of one (y_slots[t,k] is then expert k's
+ * output for token t), moe_combine on those slots times topk_w, moe_balance_loss
+ * on the logits and the picks, moe_balance_loss_grad for the loss's gradient in
+ * the logits, and moe_router_grad with that gradient and the routing weights'.
+ * Two steps are the caller's, no call here makes them: d_topk_w[t,k] = sum_h
+ * d_out[t,h] y_slots[t,k,h], d_out the gradient of the layer's output, and the
+ * slots' product with topk_w before moe_combine.
  * token_mask: uint8 [T], 0 for a token that does not count (padding), or NULL
  * when all do; the rows of such tokens in every [T, ...] input may hold
  * anything, NaN too, and their rows of every [T, ...] gradient are zero.
  * A slot whose topk_idx lies outside [0, E) takes part in nothing; an id that
- * occurs twice in a token's picks counts twice.  Logits of counted tokens are
+ * occurs twice in a token's picks counts twice (here; the experts' calls need
+ * distinct ones).  Logits of counted tokens are
  * finite or -inf (an expert switched off for that token: probability and
  * gradient 0; a row of -inf only contributes nothing but its count).
  * T == 0 is not a no-op for what sums over tokens: losses, counts and parameter
