@@ -131,3 +131,20 @@ def router_grad(x, W, scale, pes, gain, idx, mask, d_w, d_l, eps, n_round):
     if gain is not None:
         tol["gain"] = u * (scale.abs() * m + g.abs() * (x * x * beta).sum(0))
     return got, tol
+
+
+def rms_error(got, want):
+    """Root mean square of the error over that of the values."""
+    want = want.double()
+    return float(((got.double() - want) ** 2).mean().sqrt() / (want ** 2).mean().sqrt())
+
+
+# Limit of rms_error for an fp32 result of the router's backward.  A token's factors
+# (norms of H / 512 + 8 roundings each, softmax, D: at most 100 of them together, as
+# if all pointed one way) move its terms by 100 * 2^-24 = 6e-6; sums over T tokens add
+# their roundings with either sign: a chain of n terms of size s, whose partial sums
+# grow as sqrt(k) s, ends with an error near 0.41 n 2^-24 s where the sum is sqrt(n) s,
+# 0.41 sqrt(n) 2^-24 of it: for a wave's 512 tokens 6e-7, and the parts' sums add less.
+GRAD_RMS = 1e-5
+# and of d_x rounded to bf16: half a step, as if every value lost all of it
+GRAD_RMS_BF16 = 2.0 ** -8
