@@ -467,8 +467,8 @@ __global__ __launch_bounds__(64 * WK * WN) void stream_b128_kernel(B128Args a) {
 // 256 tile takes 1.7 to 1.9 us on every CU at 1.93 GHz; its products alone take
 // 1.1 us (random codes), with the scaling 1.26, and a k-block of a plain E4M3
 // library product of 8192^3 1.64.  At 26B-A4B's 4096 tokens gate_up takes 201 us
-// (1290 TF/s; weights 507 MB) and down 193 us (254 MB of weights, 369 MB of
-// fp32 slots: 3.2 TB/s).
+// (1290 TF/s; weights 507 MB) and down 191 us (254 MB of weights, 369 MB of
+// fp32 slots: 3.3 TB/s).
 // ---------------------------------------------------------------------------
 constexpr int kRowGroup = 4;
 
@@ -909,7 +909,15 @@ hipError_t launch_dequantize_b128(int block_rows, long long batch, int rows, int
 // Streaming where an expert's rows fill one 16-row tile on average, or where
 // reading the weights again for every further tile costs little: at most 96 MB
 // (8 experts of 2816 x 704, top 8: 24 tokens 35 us streamed, 43 tiled; 64 tokens
-// 51 and 45; of 1024 x 256, top 4: 256 tokens 27 and 34).
+// 51 and 45; of 1024 x 256, top 4: 256 tokens 27 and 34).  What decides is the rows
+// per expert, which the limit of 256 tokens stands for: experts of 2816 x 704, us
+// streamed and tiled,
+//   128, top 8: 32 tokens 106 138, 64 135 161, 128 (8 rows an expert) 157 166, 160
+//     177 174, 200 191 176, 256 (16 rows) 209 177;
+//   128, top 2: 256 tokens (4 rows) 132 157, 400 140 158, 600 (9 rows) 168 170;
+//   256, top 4: 256 tokens (4 rows) 240 258, 400 270 269, 512 (8 rows) 311 284.
+// Past eight rows an expert the limit is late, below it early for few slots a token:
+// up to 18 % of the call.
 bool b128_streams(int T, int rows, int E, int H, int I) {
   const long long again = (long long)E * ((rows + 16 * E - 1) / (16 * E) - 1) * 3 * H * I;
   return T <= kB128StreamTokens && again <= 96LL << 20;
@@ -920,7 +928,9 @@ bool b128_streams(int T, int rows, int E, int H, int I) {
 // 512 small ones (two per CU) 5, and one of at most 256 small ones 3.3 (2112-long
 // rows, 2816 columns, 1024 / 2048 / 4096 / 8192 tokens: small 25 / 33 / 53 / 82 us,
 // 192 columns 33 / 35 / 40 / 73, 256 columns 38 / 41 / 46 / 82; 4096 x 4096 x 4096
-// 94, 109, 80).
+// 94, 109, 80).  The order hardly depends on the contraction: of the three shapes
+// forced on 60 products (rows of 512, 1408, 2112, 5632, 16384 values; 2112, 2816,
+// 4096 columns; 1024 to 8192 tokens) the one chosen was the fastest or within 3 %.
 enum class Tile { kSmall, k192, kWide };
 static Tile linear_tile(long long rows, long long cols) {
   auto tiles = [&](int tm, int tn) { return (rows + tm - 1) / tm * ((cols + tn - 1) / tn); };
