@@ -181,7 +181,7 @@ B128Layout b128_layout(const moe_dims* d, long long T) {
   L.h = region(o, 4 * ts * d->top_k * I);  // fp32, the weight-streaming form only
   L.hq = region(o, S * ((I + 127) / 128 * 128));
   L.hs = region(o, 4 * S * ((I + 127) / 128));
-  L.total = o;
+  L.total = o + 256;  // never 0, which says that the sizes are not supported
   return L;
 }
 

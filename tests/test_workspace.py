@@ -78,6 +78,14 @@ def test_training_scratch_does_not_contain_a_layers():
                 for i in (32, 704, 8192)}) == 1
 
 
+@pytest.mark.parametrize("calls", [("layer",), ("balance_loss",), ("router_grad",),
+                                   ("expert_ffn_b128",), tuple(lib._WS_SIZES)])
+def test_no_tokens(calls):
+    """An empty batch is a size like any other (0 bytes would say unsupported)."""
+    d = lib.dims(64, 4, 2, 32)
+    assert 0 < lib.workspace_size(d, 0, calls) <= lib.workspace_size(d, 1, calls)
+
+
 def test_refusals():
     for f in lib._WS_SIZES.values():
         size = getattr(L, f)
