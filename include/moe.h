@@ -241,6 +241,137 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
                     float* d_per_expert_scale, float* d_pre_norm_gain, void* ws,
                     size_t ws_bytes, void* stream);
 
+/* ---- Training the rest of the layer --------------------------------------
+ *
+ * The layer's own calls for a training step, forward and backward.  Forward:
+ * gemma4_pre_norms, moe_router_logits (with pre_norm_gain = g_pre2),
+ * moe_dispatch, moe_expert_ffn_keep, gemma4_dense_mlp, gemma4_post_norms (which
+ * also sums the slots).  Backward, from d_out, the gradient of the layer's
+ * output: gemma4_post_norms_grad, gemma4_dense_mlp_grad, moe_expert_ffn_grad
+ * (which also gives the routing weights' gradient), the balance loss's calls,
+ * moe_router_grad, and gemma4_pre_norms_grad, which adds the router's and the
+ * residual's gradient of x to its own.  Then moe_grad_norm and moe_grad_clip.
+ * token_mask and T == 0 are as in the router's training calls above; sums run in
+ * fp32 or more in an order fixed by the sizes; no output may overlap an input
+ * unless it says so.
+ *
+ * moe_expert_ffn_keep: moe_expert_ffn, with the projections as an output: row r
+ * of gate_up [T*K, 2I] (act dtype) belongs to slot sorted_slots[r] of expert e
+ * and holds gate[e] x_t, then up[e] x_t, rounded to act dtype; rows from
+ * expert_offsets[E] on are left alone.  y_slots is that of moe_expert_ffn, bit
+ * for bit.  Workspace: moe_workspace_size. */
+int moe_expert_ffn_keep(const moe_dims* dims, int32_t T, const void* x, const void* w_gate_up,
+                        const void* w_down, const float* topk_w, const int32_t* expert_offsets,
+                        const int32_t* sorted_slots, void* gate_up, void* y_slots, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* Backward pass of moe_expert_ffn_keep and the slots' sum, from d_out [T,H] (act
+ * dtype), the gradient of sum_k y_slots[t,k]; x, the weights, topk_w and the
+ * dispatch are the forward call's, gate_up its output.  With g, u the two halves
+ * of a row of gate_up, h = gelu_tanh(g) u, v = down[e]^T d_out_t:
+ *   d_topk_w[t,k] = <v, h>                                   fp32 [T,K]
+ *   d_gate = w v u gelu_tanh'(g), d_up = w v gelu_tanh(g)    w = topk_w[t,k]
+ *   d_x[t] = sum_k gate_up[e]^T [d_gate, d_up]               act dtype [T,H]
+ *   d_w_gate_up[e] = sum_r [d_gate, d_up]_r x_t^T            [E,2I,H]
+ *   d_w_down[e] = sum_r d_out_t (w h)_r^T                    [E,H,I]
+ * The weights' gradients are stored in d_weights_dtype (MOE_F32, or MOE_BF16
+ * where act_dtype is), overwritten, zero for an expert without rows.  Each output
+ * may be NULL (not wanted), not all.  A slot that the dispatch dropped has a zero
+ * in d_topk_w and takes part in nothing.  bf16 path: v, <v, h> and every sum in
+ * fp32; [d_gate, d_up], w h and the slots' parts of d_x are rounded to bf16 in
+ * between.  Workspace of its own size, as is every call's below that has one. */
+size_t moe_expert_ffn_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
+int moe_expert_ffn_grad(const moe_dims* dims, int32_t T, const void* x, const void* w_gate_up,
+                        const void* w_down, const float* topk_w, const int32_t* expert_offsets,
+                        const int32_t* sorted_slots, const void* gate_up,
+                        const uint8_t* token_mask, const void* d_out, void* d_x, float* d_topk_w,
+                        int32_t d_weights_dtype, void* d_w_gate_up, void* d_w_down, void* ws,
+                        size_t ws_bytes, void* stream);
+
+/* The dense MLP: y = dense_down (gelu_tanh(dense_gate x) * (dense_up x)), y [T,H]
+ * slot dtype, as gemma4_ffn_block computes it; gate_up [T, 2D] (act dtype, the
+ * gate's projections, then the up ones) kept for the backward pass, or NULL.
+ * Requires dims->dense_inter > 0.  Workspace: moe_workspace_size. */
+int gemma4_dense_mlp(const moe_dims* dims, int32_t T, const void* x, const void* dense_gate,
+                     const void* dense_up, const void* dense_down, void* gate_up, void* y,
+                     void* ws, size_t ws_bytes, void* stream);
+
+/* Its backward pass from d_y [T,H] (act dtype): d_x [T,H] act dtype, d_gate and
+ * d_up [D,H], d_down [H,D] in d_weights_dtype, as for moe_expert_ffn_grad with a
+ * routing weight of one.  NULL: not wanted (d_gate and d_up together). */
+size_t gemma4_dense_mlp_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
+int gemma4_dense_mlp_grad(const moe_dims* dims, int32_t T, const void* x, const void* dense_gate,
+                          const void* dense_up, const void* dense_down, const void* gate_up,
+                          const uint8_t* token_mask, const void* d_y, void* d_x,
+                          int32_t d_weights_dtype, void* d_gate, void* d_up, void* d_down,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* The norms before the branches: xd = RMSNorm(x) * g_pre, xm = RMSNorm(x) *
+ * g_pre2, [T,H] act dtype. */
+int gemma4_pre_norms(const moe_dims* dims, int32_t T, const void* x, const float* g_pre,
+                     const float* g_pre2, void* xd, void* xm, void* stream);
+
+/* The layer's end, behind the branches: moe_sum[t] = sum_k y_slots[t,k] (k
+ * ascending, fp32; [T,H] slot dtype, NULL: not wanted),
+ *   o = RMSNorm_post(RMSNorm_post1(dn) + RMSNorm_post2(moe_sum)),
+ *   out = (o + x) * layer_scalar,
+ * dn [T,H] slot dtype, out [T,H] act dtype, ffn_out [T,H] fp32 receives o (NULL:
+ * not wanted).  The norms see the sum before it is rounded to the slot dtype. */
+int gemma4_post_norms(const moe_dims* dims, int32_t T, const void* x, const void* y_slots,
+                      const void* dn, const float* g_post1, const float* g_post2,
+                      const float* g_post, float layer_scalar, void* out, void* moe_sum,
+                      float* ffn_out, void* stream);
+
+/* Backward pass of gemma4_pre_norms, from d_xd and d_xm: d_x = the norms' gradient
+ * + d_x_add (another branch's gradient of x, the router's; NULL: none) +
+ * layer_scalar * d_out (the residual's; d_out NULL: none), all [T,H] act dtype;
+ * d_g_pre, d_g_pre2 [H] fp32.  A token that does not count gets a zero row of
+ * d_x whatever d_x_add and d_out hold.  d_x may be any of the [T,H] inputs (each
+ * row is read before it is written). */
+size_t gemma4_norms_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
+int gemma4_pre_norms_grad(const moe_dims* dims, int32_t T, const void* x, const float* g_pre,
+                          const float* g_pre2, const uint8_t* token_mask, const void* d_xd,
+                          const void* d_xm, const void* d_x_add, const void* d_out,
+                          float layer_scalar, void* d_x, float* d_g_pre, float* d_g_pre2,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* Backward pass of gemma4_post_norms, from d_out [T,H] (act dtype): d_dn and d_moe
+ * [T,H] act dtype (d_moe that of the slots' sum, the same for each of a token's
+ * slots), the gains' gradients [H] fp32, d_layer_scalar [1] fp32 (NULL: not
+ * wanted; x, the residual, is read for it alone and may be NULL without it).  dn
+ * and moe_sum [T,H] slot dtype.  The residual's gradient, layer_scalar * d_out, is
+ * gemma4_pre_norms_grad's to add.  Workspace: gemma4_norms_grad_workspace_size. */
+int gemma4_post_norms_grad(const moe_dims* dims, int32_t T, const void* x, const void* dn,
+                           const void* moe_sum, const float* g_post1, const float* g_post2,
+                           const float* g_post, float layer_scalar, const uint8_t* token_mask,
+                           const void* d_out, void* d_dn, void* d_moe, float* d_g_post1,
+                           float* d_g_post2, float* d_g_post, float* d_layer_scalar, void* ws,
+                           size_t ws_bytes, void* stream);
+
+/* A tensor of a list: numel elements (0 is fine) at a device address aligned to
+ * its type (16 bytes where it should be fast), dtype a moe_dtype.  The list itself
+ * is HOST memory, read before the call returns. */
+typedef struct moe_tensor {
+  void* data;
+  int64_t numel;
+  int32_t dtype;
+} moe_tensor;
+
+/* Global norm of n gradients (up to 65536 tensors, 2^40 elements):
+ * norm [2] fp32 = {sqrt(sum of all squares), min(1, max_norm / (that + 1e-6))}.
+ * Squares and sums in fp64.  max_norm > 0, an infinity to measure only.  A NaN or
+ * an infinity among the gradients makes the norm one; the coefficient is then a
+ * NaN or 0.  A tensor listed twice counts twice. */
+size_t moe_grad_norm_workspace_size(int32_t n, const moe_tensor* grads);
+int moe_grad_norm(int32_t n, const moe_tensor* grads, float max_norm, float* norm, void* ws,
+                  size_t ws_bytes, void* stream);
+
+/* out[i] = grads[i] * norm[1], norm as moe_grad_norm left it on the device; out
+ * NULL: in place.  An out tensor may have another dtype than its gradient; it is
+ * its gradient (same address and dtype) or overlaps nothing in either list. */
+int moe_grad_clip(int32_t n, const moe_tensor* grads, const float* norm, const moe_tensor* out,
+                  void* stream);
+
 /* moe_router followed by moe_dispatch of its result, in one call (for small
  * batches the dispatch runs inside the router's top-K kernel).  Outputs are
  * those of the two calls. */

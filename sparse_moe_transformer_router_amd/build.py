@@ -16,7 +16,8 @@ OBJ = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe.so")
 PROBE_LIB = os.path.join(PKG, "libmoe_probe.so")
 SOURCES = ["router.hip", "dispatch.hip", "expert_ffn.hip", "expert_stream.hip", "expert_mx.hip",
-           "block_fp8.hip", "combine.hip", "quant.hip", "router_train.hip", "moe_api.cpp"]
+           "block_fp8.hip", "combine.hip", "quant.hip", "router_train.hip",
+           "ffn_grad.hip", "norms_grad.hip", "grad_norm.hip", "moe_api.cpp"]
 # Measurement probes (achievable read and MFMA rates), a library of their own.
 PROBE_SOURCES = ["probe.hip"]
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")

@@ -139,7 +139,7 @@ __global__ __launch_bounds__(kThreads) void block_epilogue_kernel(
     int H, int K, float eps, float layer_scalar, const YT* __restrict__ y,
     const YT* __restrict__ dn, const XT* __restrict__ x, const float* __restrict__ g_post1,
     const float* __restrict__ g_post2, const float* __restrict__ g_post, XT* __restrict__ out,
-    float* __restrict__ ffn_out) {
+    float* __restrict__ ffn_out, YT* __restrict__ moe_sum) {
   extern __shared__ float row[];
   float* ms = row;      // [H] sum_k y
   float* ds = row + H;  // [H] dense
@@ -157,6 +157,7 @@ __global__ __launch_bounds__(kThreads) void block_epilogue_kernel(
     }
     st8(ms + c, acc);
     st8(ds + c, d);
+    if (moe_sum) st8(moe_sum + (size_t)t * H + c, acc);
   }
   const float rm = 1.0f / sqrtf(block_sum(ssm, red) / (float)H + eps);
   const float rd = 1.0f / sqrtf(block_sum(ssd, red) / (float)H + eps);
@@ -235,17 +236,20 @@ hipError_t launch_block_epilogue(const EpilogueArgs& a, hipStream_t s) {
       hipLaunchKernelGGL((block_epilogue_kernel<bf16, bf16>), dim3(a.T), dim3(kThreads), lds, s,
                          a.H, a.K, a.eps, a.layer_scalar, static_cast<const bf16*>(a.y),
                          static_cast<const bf16*>(a.dn), static_cast<const bf16*>(a.x),
-                         a.g_post1, a.g_post2, a.g_post, static_cast<bf16*>(a.out), a.ffn_out);
+                         a.g_post1, a.g_post2, a.g_post, static_cast<bf16*>(a.out), a.ffn_out,
+                         static_cast<bf16*>(a.moe_sum));
     else
       hipLaunchKernelGGL((block_epilogue_kernel<float, bf16>), dim3(a.T), dim3(kThreads), lds, s,
                          a.H, a.K, a.eps, a.layer_scalar, static_cast<const float*>(a.y),
                          static_cast<const float*>(a.dn), static_cast<const bf16*>(a.x),
-                         a.g_post1, a.g_post2, a.g_post, static_cast<bf16*>(a.out), a.ffn_out);
+                         a.g_post1, a.g_post2, a.g_post, static_cast<bf16*>(a.out), a.ffn_out,
+                         static_cast<float*>(a.moe_sum));
   } else {
     hipLaunchKernelGGL((block_epilogue_kernel<float, float>), dim3(a.T), dim3(kThreads), lds, s,
                        a.H, a.K, a.eps, a.layer_scalar, static_cast<const float*>(a.y),
                        static_cast<const float*>(a.dn), static_cast<const float*>(a.x),
-                       a.g_post1, a.g_post2, a.g_post, static_cast<float*>(a.out), a.ffn_out);
+                       a.g_post1, a.g_post2, a.g_post, static_cast<float*>(a.out), a.ffn_out,
+                       static_cast<float*>(a.moe_sum));
   }
   return hipGetLastError();
 }

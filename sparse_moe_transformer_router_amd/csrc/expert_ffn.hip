@@ -134,13 +134,14 @@ __device__ __forceinline__ bf16x8 widen_half(const uint4& c, int s, float scale)
 // W0 / W1 hold the weights in the form WF; S0 / S1 their scales (int8, E4M3:
 // fp32 per output channel n at e * s_stride + n; MXFP4: E8M0 rows of Kd / 32
 // at e * s_stride + n * Kd / 32), w_stride counts weights between groups.
-template <bool GU, int BM, int WM, int WN, int NSTAGE, typename YT, int WF>
+template <bool GU, int BM, int WM, int WN, int NSTAGE, typename YT, int WF, bool KEEP>
 __global__ __launch_bounds__(64 * WM * WN, 1) void grouped_gemm_kernel(
     int Kd, int Nout, int E, int K, int rows, int ident, int NT, const bf16* __restrict__ A,
     const void* __restrict__ W0v, const void* __restrict__ W1v, long long w_stride,
     const void* __restrict__ S0v, const void* __restrict__ S1v, long long s_stride,
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ sorted_slots,
-    const float* __restrict__ topk_w, bf16* __restrict__ hout, YT* __restrict__ yout) {
+    const float* __restrict__ topk_w, bf16* __restrict__ hout, YT* __restrict__ yout,
+    bf16* __restrict__ keep) {
   constexpr bool NARROW = WF != kWfBF16;
   constexpr int SB = stage_bytes<BM, WF>();
   constexpr int NW = WM * WN, ROWS = BM + GN, LPW = ROWS / 16 / NW;
@@ -512,6 +513,35 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void grouped_gemm_kernel(
         *reinterpret_cast<uint4*>(hout + (size_t)(row0 + r) * Nout + col) =
             *reinterpret_cast<const uint4*>(stg + r * kGuStride + ch * 8);
     }
+    // KEEP: the projections themselves leave the same way, gate then up
+    if constexpr (KEEP) {
+#pragma unroll
+      for (int part = 0; part < 2; ++part) {
+        __syncthreads();
+#pragma unroll
+        for (int i = 0; i < TM; ++i) {
+          if (i >= nv) break;
+#pragma unroll
+          for (int j = 0; j < half; ++j)
+#pragma unroll
+            for (int q = 0; q < 16; ++q) {
+              const int r = wm * WR + i * 32 + 8 * (q / 4) + 4 * fq + (q % 4);
+              const int c = wn * (WC / 2) + j * 32 + fr;
+              stg[r * kGuStride + c] = (bf16)acc[i][j + part * half][q];
+            }
+        }
+        __syncthreads();
+#pragma unroll
+        for (int it = 0; it < BM * CH / NT_; ++it) {
+          const int k = tid + it * NT_;
+          const int r = k / CH, ch = k % CH;
+          const int col = nbase + ch * 8;
+          if (row0 + r < row1 && col < Nout)
+            *reinterpret_cast<uint4*>(keep + (size_t)(row0 + r) * 2 * Nout + part * Nout + col) =
+                *reinterpret_cast<const uint4*>(stg + r * kGuStride + ch * 8);
+        }
+      }
+    }
   } else {
     float sd[TN];
 #pragma unroll
@@ -588,7 +618,7 @@ __global__ __launch_bounds__(256) void gate_up_f32_kernel(
     int H, int N, int E, int K, int rows, int ident, const float* __restrict__ x,
     const float* __restrict__ wg, const float* __restrict__ wu, long long w_stride,
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ sorted_slots,
-    float* __restrict__ h) {
+    float* __restrict__ h, float* __restrict__ keep) {
   __shared__ float As[kFT][kFT + 1], Gs[kFT][kFT + 1], Us[kFT][kFT + 1];
   RowTile rt;
   if (!get_row_tile(ident, rows, offsets, E, kFT, rt)) return;
@@ -628,7 +658,13 @@ __global__ __launch_bounds__(256) void gate_up_f32_kernel(
 #pragma unroll
     for (int b = 0; b < 2; ++b) {
       const int row = rt.row0 + 2 * tr + a, col = n0 + 2 * tc + b;
-      if (row < rt.row1 && col < N) h[(size_t)row * N + col] = gelu_tanh(ag[a][b]) * au[a][b];
+      if (row < rt.row1 && col < N) {
+        h[(size_t)row * N + col] = gelu_tanh(ag[a][b]) * au[a][b];
+        if (keep) {
+          keep[(size_t)row * 2 * N + col] = ag[a][b];
+          keep[(size_t)row * 2 * N + N + col] = au[a][b];
+        }
+      }
     }
 }
 
@@ -685,14 +721,15 @@ __global__ __launch_bounds__(256) void down_f32_kernel(
 
 namespace {
 
-template <bool GU, int BM, int WM, int WN, int NSTAGE, typename YT, int WF>
+template <bool GU, int BM, int WM, int WN, int NSTAGE, typename YT, int WF, bool KEEP = false>
 hipError_t launch_grouped(int Kd, int Nout, int E, int K, int rows, bool ident, int RT, int NT,
                           const bf16* A, const void* W0, const void* W1, long long w_stride,
                           const void* S0, const void* S1, long long s_stride,
                           const int32_t* offsets, const int32_t* sorted_slots,
                           const float* topk_w, bf16* hout, YT* yout, hipStream_t s,
-                          hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr) {
-  auto kf = grouped_gemm_kernel<GU, BM, WM, WN, NSTAGE, YT, WF>;
+                          hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr,
+                          bf16* keep = nullptr) {
+  auto kf = grouped_gemm_kernel<GU, BM, WM, WN, NSTAGE, YT, WF, KEEP>;
   // ring (+ MXFP4 scale rows) or staging (+ row slots, weights)
   const int lds = gemm_lds_bytes<GU, BM, NSTAGE, WF>();
   static const hipError_t attr = hipFuncSetAttribute(
@@ -700,7 +737,7 @@ hipError_t launch_grouped(int Kd, int Nout, int E, int K, int rows, bool ident, 
   if (attr != hipSuccess) return attr;
   launch_maybe_timed(kf, dim3(RT * NT), dim3(64 * WM * WN), lds, s, ev_start, ev_stop, Kd, Nout, E,
                      K, rows, (int)ident, NT, A, W0, W1, w_stride, S0, S1, s_stride, offsets,
-                     sorted_slots, topk_w, hout, yout);
+                     sorted_slots, topk_w, hout, yout, keep);
   return hipSuccess;
 }
 
@@ -712,7 +749,7 @@ hipError_t launch_grouped(int Kd, int Nout, int E, int K, int rows, bool ident, 
 template <int WF>
 constexpr int gate_up_stages() { return WF == kWfBF16 ? 5 : WF == kWfMXFP4 ? 4 : 6; }
 
-template <int WF>
+template <int WF, bool KEEP = false>
 hipError_t launch_gate_up_tiled(const GateUpArgs& a, hipStream_t s) {
   const int NT = (a.N + GN / 2 - 1) / (GN / 2);
   // bf16 expert groups of 256 rows or more on average: 8 waves of 128 x 64
@@ -723,17 +760,17 @@ hipError_t launch_gate_up_tiled(const GateUpArgs& a, hipStream_t s) {
   // win (2048 tokens 306 against 318 us); the dense branch keeps them too.
   if constexpr (WF == kWfBF16) {
     if (!a.ident && (long long)a.rows >= 256LL * a.E)
-      return launch_grouped<true, 256, 2, 4, gate_up_stages<WF>(), float, WF>(
+      return launch_grouped<true, 256, 2, 4, gate_up_stages<WF>(), float, WF, KEEP>(
           a.H, a.N, a.E, a.K, a.rows, a.ident, tile_count_bound(a.ident, a.rows, a.T, a.E, 256),
           NT, static_cast<const bf16*>(a.x), a.w_gate, a.w_up, a.w_stride, a.s_gate, a.s_up,
           a.s_stride, a.offsets, a.sorted_slots, nullptr, static_cast<bf16*>(a.h),
-          static_cast<float*>(nullptr), s, a.ev_start, a.ev_stop);
+          static_cast<float*>(nullptr), s, a.ev_start, a.ev_stop, static_cast<bf16*>(a.keep));
   }
-  return launch_grouped<true, 256, 4, 4, gate_up_stages<WF>(), float, WF>(
+  return launch_grouped<true, 256, 4, 4, gate_up_stages<WF>(), float, WF, KEEP>(
       a.H, a.N, a.E, a.K, a.rows, a.ident, tile_count_bound(a.ident, a.rows, a.T, a.E, 256), NT,
       static_cast<const bf16*>(a.x), a.w_gate, a.w_up, a.w_stride, a.s_gate, a.s_up, a.s_stride,
       a.offsets, a.sorted_slots, nullptr, static_cast<bf16*>(a.h), static_cast<float*>(nullptr),
-      s, a.ev_start, a.ev_stop);
+      s, a.ev_start, a.ev_stop, static_cast<bf16*>(a.keep));
 }
 
 template <typename YT, int WF>
@@ -774,14 +811,16 @@ hipError_t launch_gate_up(const GateUpArgs& a, hipStream_t s) {
   }
   if (a.bf16 && use_stream_kernels(a.T, a.rows, a.E, a.ident)) return launch_gate_up_stream(a, s);
   if (a.bf16) {
-    const hipError_t e = launch_gate_up_tiled<kWfBF16>(a, s);
+    const hipError_t e = a.keep ? launch_gate_up_tiled<kWfBF16, true>(a, s)
+                                : launch_gate_up_tiled<kWfBF16>(a, s);
     if (e != hipSuccess) return e;
   } else {
     dim3 grid(tile_count_bound(a.ident, a.rows, a.T, a.E, kFT), (a.N + kFT - 1) / kFT);
     launch_maybe_timed(gate_up_f32_kernel, grid, dim3(256), 0, s, a.ev_start, a.ev_stop, a.H, a.N,
                        a.E, a.K, a.rows, (int)a.ident, static_cast<const float*>(a.x),
                        static_cast<const float*>(a.w_gate), static_cast<const float*>(a.w_up),
-                       a.w_stride, a.offsets, a.sorted_slots, static_cast<float*>(a.h));
+                       a.w_stride, a.offsets, a.sorted_slots, static_cast<float*>(a.h),
+                       static_cast<float*>(a.keep));
   }
   return hipGetLastError();
 }

@@ -74,13 +74,13 @@ __device__ __forceinline__ f32x4 mfma16(bf16x8 a, bf16x8 b, f32x4 c) {
 // gate_up: one block = one row tile (<= 16 * MB rows) x NC groups of 16 gate
 // + 16 up columns; its WK waves split H.  A wave's activation fragments serve
 // all NC groups, so narrow weight formats stream more bytes per wave.
-template <typename WQ, int WK, int MB, int NS, int NC>
+template <typename WQ, int WK, int MB, int NS, int NC, bool KEEP>
 __global__ __launch_bounds__(64 * WK) void gate_up_stream_kernel(
     int H, int N, int E, int K, int rows, int ident, const bf16* __restrict__ x,
     const WQ* __restrict__ wg, const WQ* __restrict__ wu, long long w_stride,
     const void* __restrict__ sg, const void* __restrict__ su, long long s_stride,
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ sorted_slots,
-    bf16* __restrict__ h) {
+    bf16* __restrict__ h, bf16* __restrict__ keep) {
   typedef WFmt<WQ> F;
   static_assert(NS >= 2, "the load ring needs two slots or more");
   __shared__ f32x4 red[WK][MB][NC][2][kWave];
@@ -244,7 +244,13 @@ __global__ __launch_bounds__(64 * WK) void gate_up_stream_kernel(
 #pragma unroll
       for (int r = 0; r < 4; ++r) {
         const int row = row0 + 16 * mb + 4 * fg + r;
-        if (row < row1 && nvalid) h[(size_t)row * N + n] = (bf16)(gelu_tanh(g[r]) * u[r]);
+        if (row < row1 && nvalid) {
+          h[(size_t)row * N + n] = (bf16)(gelu_tanh(g[r]) * u[r]);
+          if constexpr (KEEP) {
+            keep[(size_t)row * 2 * N + n] = (bf16)g[r];
+            keep[(size_t)row * 2 * N + N + n] = (bf16)u[r];
+          }
+        }
       }
     }
   }
@@ -473,15 +479,23 @@ __global__ __launch_bounds__(64 * WN * WK) void down_stream_kernel(
   }
 }
 
-template <typename WQ, int WK, int MB, int NS, int NC>
+template <typename WQ, int WK, int MB, int NS, int NC, bool KEEP = false>
 void launch_gu(const GateUpArgs& a, hipStream_t s) {
   const long long cgs = (a.N + 16 * NC - 1) / (16 * NC);
   dim3 grid((unsigned)(tile_count_bound(a.ident, a.rows, a.T, a.E, 16 * MB) * cgs));
-  launch_maybe_timed(gate_up_stream_kernel<WQ, WK, MB, NS, NC>, grid, dim3(64 * WK), 0, s,
+  launch_maybe_timed(gate_up_stream_kernel<WQ, WK, MB, NS, NC, KEEP>, grid, dim3(64 * WK), 0, s,
                      a.ev_start, a.ev_stop, a.H, a.N, a.E, a.K, a.rows, (int)a.ident,
                      static_cast<const bf16*>(a.x), static_cast<const WQ*>(a.w_gate),
                      static_cast<const WQ*>(a.w_up), a.w_stride, a.s_gate, a.s_up, a.s_stride,
-                     a.offsets, a.sorted_slots, static_cast<bf16*>(a.h));
+                     a.offsets, a.sorted_slots, static_cast<bf16*>(a.h),
+                     static_cast<bf16*>(a.keep));
+}
+
+// The bf16 form, with the projections kept where a.keep asks for them.
+template <int WK, int MB, int NS, int NC>
+void launch_gu_bf16(const GateUpArgs& a, hipStream_t s) {
+  if (a.keep) launch_gu<bf16, WK, MB, NS, NC, true>(a, s);
+  else launch_gu<bf16, WK, MB, NS, NC>(a, s);
 }
 
 // Activation rows of a down tile staged in LDS while they and the block's
@@ -570,9 +584,9 @@ hipError_t launch_gate_up_stream(const GateUpArgs& a, hipStream_t s) {
       else launch_gu<fp4x2, 1, 2, 2, 1>(a, s);
       break;
     case WFormat::kBF16:
-      if (a.ident) launch_gu<bf16, 8, 2, 2, 1>(a, s);
-      else if (a.T <= 64) launch_gu<bf16, 4, 1, 4, 1>(a, s);
-      else launch_gu<bf16, 4, 2, 3, 1>(a, s);  // 16 rows per expert at 128 tokens
+      if (a.ident) launch_gu_bf16<8, 2, 2, 1>(a, s);
+      else if (a.T <= 64) launch_gu_bf16<4, 1, 4, 1>(a, s);
+      else launch_gu_bf16<4, 2, 3, 1>(a, s);  // 16 rows per expert at 128 tokens
       break;
   }
   return hipGetLastError();

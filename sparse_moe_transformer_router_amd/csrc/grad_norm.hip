@@ -1,0 +1,227 @@
+// Global norm of a list of gradients, and their clipping.
+//
+//   norm = sqrt(sum over all tensors and elements of g^2)
+//   coef = min(1, max_norm / (norm + 1e-6)),   g <- coef g
+//
+// Bound by memory: one read of every gradient for the norm; a second read and a
+// write for the clipping, which cannot begin before the norm is known.  The list
+// of tensors travels in the kernels' arguments (no copy to the device, nothing
+// that a captured graph could find changed), kTable of them a launch.  A tensor
+// is cut into chunks of kChunk elements, dealt out to the blocks in turn; each block adds
+// its chunks' squares in fp64 (an fp32 square overflows from 2^64 on and
+// vanishes below 2^-75) and writes one partial sum, added in order by a last block:
+// results repeat bit for bit.
+#include "common.h"
+#include "launch.h"
+#include "moe.h"
+
+namespace moe {
+namespace {
+
+constexpr int kTable = 128;              // tensors a launch
+constexpr int kChunk = 16384;            // elements
+constexpr int kThreads = 256;
+constexpr int kNormBlocks = 2048;        // blocks of a norm launch at most
+
+struct Table {
+  const void* src[kTable];
+  void* dst[kTable];
+  long long numel[kTable];
+  int first[kTable + 1];                 // first chunk of each tensor
+  unsigned char src_bf16[kTable], dst_bf16[kTable];
+  int n;
+};
+static_assert(sizeof(Table) <= 3968, "kernel arguments");
+
+// Tensor that chunk c belongs to.
+__device__ __forceinline__ int find(const Table& t, int c) {
+  int lo = 0, hi = t.n - 1;
+  while (lo < hi) {
+    const int mid = (lo + hi + 1) / 2;
+    if (t.first[mid] <= c) lo = mid;
+    else hi = mid - 1;
+  }
+  return lo;
+}
+
+__device__ __forceinline__ bool aligned16(const void* p) {
+  return (reinterpret_cast<uintptr_t>(p) & 15u) == 0;
+}
+
+template <typename T>
+__device__ __forceinline__ double chunk_squares(const T* __restrict__ p, int n) {
+  double s = 0.0;
+  constexpr int V = 16 / (int)sizeof(T);
+  if (aligned16(p)) {
+    const int nv = n / V;
+    for (int i = threadIdx.x; i < nv; i += kThreads) {
+      T v[V];
+      *reinterpret_cast<uint4*>(v) = reinterpret_cast<const uint4*>(p)[i];
+#pragma unroll
+      for (int j = 0; j < V; ++j) {
+        const double d = (double)to_f32(v[j]);
+        s = fma(d, d, s);
+      }
+    }
+    for (int i = nv * V + threadIdx.x; i < n; i += kThreads) {
+      const double d = (double)to_f32(p[i]);
+      s = fma(d, d, s);
+    }
+  } else {
+    for (int i = threadIdx.x; i < n; i += kThreads) {
+      const double d = (double)to_f32(p[i]);
+      s = fma(d, d, s);
+    }
+  }
+  return s;
+}
+
+__device__ __forceinline__ double block_sum(double v) {
+  __shared__ double red[kThreads / kWave];
+  v = wave_sum(v);
+  if (lane_id() == 0) red[threadIdx.x / kWave] = v;
+  __syncthreads();
+  v = 0.0;
+#pragma unroll
+  for (int w = 0; w < kThreads / kWave; ++w) v += red[w];
+  return v;
+}
+
+__global__ __launch_bounds__(kThreads) void norm_kernel(const Table t, double* __restrict__ part) {
+  double s = 0.0;
+  for (int c = blockIdx.x; c < t.first[t.n]; c += gridDim.x) {
+    const int i = find(t, c);
+    const long long at = (long long)(c - t.first[i]) * kChunk;
+    const int n = (int)min((long long)kChunk, t.numel[i] - at);
+    if (t.src_bf16[i]) s += chunk_squares(static_cast<const bf16*>(t.src[i]) + at, n);
+    else s += chunk_squares(static_cast<const float*>(t.src[i]) + at, n);
+  }
+  s = block_sum(s);
+  if (threadIdx.x == 0) part[blockIdx.x] = s;
+}
+
+__global__ __launch_bounds__(kThreads) void norm_end_kernel(int nparts, float max_norm,
+                                                            const double* __restrict__ part,
+                                                            float* __restrict__ norm) {
+  double s = 0.0;
+  for (int i = threadIdx.x; i < nparts; i += kThreads) s += part[i];
+  s = block_sum(s);
+  if (threadIdx.x == 0) {
+    const float v = (float)sqrt(s);
+    const float c = max_norm / (v + 1e-6f);
+    norm[0] = v;
+    norm[1] = c > 1.0f ? 1.0f : c;  // a NaN stays one
+  }
+}
+
+template <typename S, typename D>
+__device__ __forceinline__ void chunk_scale(const S* p, D* q, int n, float coef) {
+  if (aligned16(p) && aligned16(q)) {
+    const int nv = n / 8;
+    for (int i = threadIdx.x; i < nv; i += kThreads) {
+      S v[8];
+      D o[8];
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(S) / 2; ++j)
+        reinterpret_cast<uint4*>(v)[j] = reinterpret_cast<const uint4*>(p + 8 * (size_t)i)[j];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) o[j] = from_f32<D>(to_f32(v[j]) * coef);
+#pragma unroll
+      for (int j = 0; j < (int)sizeof(D) / 2; ++j)
+        reinterpret_cast<uint4*>(q + 8 * (size_t)i)[j] = reinterpret_cast<uint4*>(o)[j];
+    }
+    for (int i = nv * 8 + threadIdx.x; i < n; i += kThreads)
+      q[i] = from_f32<D>(to_f32(p[i]) * coef);
+  } else {
+    for (int i = threadIdx.x; i < n; i += kThreads) q[i] = from_f32<D>(to_f32(p[i]) * coef);
+  }
+}
+
+// Chunks from the last to the first: the norm's pass read the last ones last, so
+// they are the likeliest to be in the caches still.
+__global__ __launch_bounds__(kThreads) void clip_kernel(const Table t,
+                                                        const float* __restrict__ norm) {
+  const float coef = norm[1];
+  const int total = t.first[t.n];
+  for (int k = blockIdx.x; k < total; k += gridDim.x) {
+    const int c = total - 1 - k, i = find(t, c);
+    if (coef == 1.0f && t.dst[i] == t.src[i] && t.src_bf16[i] == t.dst_bf16[i]) continue;
+    const long long at = (long long)(c - t.first[i]) * kChunk;
+    const int n = (int)min((long long)kChunk, t.numel[i] - at);
+    if (t.src_bf16[i]) {
+      const bf16* p = static_cast<const bf16*>(t.src[i]) + at;
+      if (t.dst_bf16[i]) chunk_scale(p, static_cast<bf16*>(t.dst[i]) + at, n, coef);
+      else chunk_scale(p, static_cast<float*>(t.dst[i]) + at, n, coef);
+    } else {
+      const float* p = static_cast<const float*>(t.src[i]) + at;
+      if (t.dst_bf16[i]) chunk_scale(p, static_cast<bf16*>(t.dst[i]) + at, n, coef);
+      else chunk_scale(p, static_cast<float*>(t.dst[i]) + at, n, coef);
+    }
+  }
+}
+
+// The next tensors of a list, from `at` on, as a launch's table: at most kTable
+// tensors with elements and at most 2^30 chunks.
+void fill(Table& tb, int n, const moe_tensor* t, const moe_tensor* out, int& at) {
+  tb.n = 0;
+  tb.first[0] = 0;
+  for (; at < n && tb.n < kTable; ++at) {
+    if (t[at].numel == 0) continue;
+    const int i = tb.n++;
+    tb.src[i] = t[at].data;
+    tb.src_bf16[i] = t[at].dtype == MOE_BF16;
+    tb.dst[i] = out ? out[at].data : t[at].data;
+    tb.dst_bf16[i] = (out ? out : t)[at].dtype == MOE_BF16;
+    tb.numel[i] = t[at].numel;
+    tb.first[i + 1] = tb.first[i] + (int)((t[at].numel + kChunk - 1) / kChunk);
+  }
+}
+
+}  // namespace
+
+long long grad_norm_parts(int n, const moe_tensor* t) {
+  long long parts = 0;
+  int at = 0;
+  while (at < n) {
+    Table tb;
+    fill(tb, n, t, nullptr, at);
+    parts += tb.first[tb.n] < kNormBlocks ? tb.first[tb.n] : kNormBlocks;
+  }
+  return parts;
+}
+
+hipError_t launch_grad_norm(int n, const moe_tensor* t, float max_norm, float* norm,
+                            double* ws_part, hipStream_t s) {
+  int parts = 0, at = 0;
+  while (at < n) {
+    Table tb;
+    fill(tb, n, t, nullptr, at);
+    const int blocks = tb.first[tb.n] < kNormBlocks ? tb.first[tb.n] : kNormBlocks;
+    if (blocks == 0) continue;
+    hipLaunchKernelGGL(norm_kernel, dim3(blocks), dim3(kThreads), 0, s, tb, ws_part + parts);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    parts += blocks;
+  }
+  hipLaunchKernelGGL(norm_end_kernel, dim3(1), dim3(kThreads), 0, s, parts, max_norm, ws_part,
+                     norm);
+  return hipGetLastError();
+}
+
+hipError_t launch_grad_clip(int n, const moe_tensor* t, const float* norm, const moe_tensor* out,
+                            hipStream_t s) {
+  int at = 0;
+  while (at < n) {
+    Table tb;
+    fill(tb, n, t, out, at);
+    const int chunks = tb.first[tb.n];
+    if (chunks == 0) continue;
+    hipLaunchKernelGGL(clip_kernel, dim3(chunks < 8192 ? chunks : 8192), dim3(kThreads), 0, s, tb,
+                       norm);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return hipSuccess;
+}
+
+}  // namespace moe

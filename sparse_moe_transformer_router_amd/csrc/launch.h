@@ -7,6 +7,8 @@
 #include <hip/hip_runtime.h>
 #include <stdint.h>
 
+struct moe_tensor;
+
 namespace moe {
 
 struct RouterArgs {
@@ -133,6 +135,7 @@ struct GateUpArgs {
   const int32_t* offsets;      // [E+1] (unused when ident)
   const int32_t* sorted_slots; // [rows] (unused when ident)
   void* h;                     // [rows, N] act dtype, sorted order
+  void* keep;                  // [rows, 2N] act dtype or nullptr: the gate projections, then the up ones
   // Weights below bf16: w_gate / w_up hold codes; int8 and E4M3 rows n of
   // group e are scaled by the fp32 s_gate / s_up[e * s_stride + n]; MXFP4
   // rows carry E8M0 block scales at s_gate / s_up + e * s_stride + n * (H /
@@ -307,7 +310,93 @@ struct EpilogueArgs {
   const float* g_post;
   void* out;           // [T,H] act
   float* ffn_out;      // [T,H] fp32 or nullptr
+  void* moe_sum;       // [T,H] slot dtype or nullptr: sum over k of y
 };
 hipError_t launch_block_epilogue(const EpilogueArgs& a, hipStream_t s);
+
+// Backward pass of the gated block (ffn_grad.hip): of the experts (rows = T K,
+// sorted slots) or of the dense MLP (ident: rows = T, d_x written directly).
+// rows == 0 writes zero weight gradients.
+struct FfnGradArgs {
+  int T, H, I, E, K, rows;
+  bool ident, bf16, wgrad_bf16;  // wgrad_bf16: type of the weight gradients (bf16 path)
+  const void* x;                 // [T,H]
+  const void* w_gate;            // group 0's [I,H] gate rows
+  const void* w_up;
+  long long gu_stride;           // elements between groups, of the gradients too
+  const void* w_down;            // group 0's [H,I]
+  long long dn_stride;
+  const float* topk_w;
+  const int32_t* offsets;
+  const int32_t* sorted_slots;
+  const void* kept;              // [rows,2I] gate and up projections
+  const uint8_t* mask;           // [T] or nullptr
+  const void* d_out;             // [T,H]
+  void* d_x;                     // [T,H] or nullptr
+  float* d_topk_w;               // [T,K] or nullptr
+  void* d_gate;                  // or nullptr (with d_up)
+  void* d_up;
+  void* d_down;                  // or nullptr
+  int32_t* ws_row_tok;           // [rows]
+  int32_t* ws_slot_row;          // [rows]
+  void* ws_d_gu;                 // [rows,2I]
+  void* ws_hw;                   // [rows,I]
+  void* ws_d_xs;                 // [rows,H] (experts)
+  float* ws_part;                // [ffn_grad_parts,rows]
+};
+int ffn_grad_parts(int I, bool bf16);
+hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s);
+
+// Backward passes of the layer's norms (norms_grad.hip), in norms_grad_blocks(T)
+// blocks whose sums over tokens a last kernel adds.
+struct PreNormGradArgs {
+  int T, H;
+  float eps, scalar;
+  bool bf16;
+  const void* x;         // [T,H]
+  const float* g1;
+  const float* g2;
+  const uint8_t* mask;   // [T] or nullptr
+  const void* d_xd;      // [T,H]
+  const void* d_xm;      // [T,H]
+  const void* d_add;     // [T,H] or nullptr
+  const void* d_out;     // [T,H] or nullptr
+  void* d_x;             // [T,H]
+  float* d_g1;           // [H]
+  float* d_g2;
+  float* ws_part;        // [blocks,2,H]
+};
+struct PostNormGradArgs {
+  int T, H;
+  float eps, scalar;
+  bool bf16, y_bf16;
+  const void* x;         // [T,H] act, or nullptr (with d_scalar)
+  const void* dn;        // [T,H] slot dtype
+  const void* moe_sum;   // [T,H] slot dtype
+  const float* g1;
+  const float* g2;
+  const float* g3;
+  const uint8_t* mask;
+  const void* d_out;     // [T,H] act
+  void* d_dn;            // [T,H] act
+  void* d_moe;           // [T,H] act
+  float* d_g1;
+  float* d_g2;
+  float* d_g3;
+  float* d_scalar;       // [1] or nullptr
+  float* ws_part;        // [blocks,3,H]
+  double* ws_scalar;     // [blocks]
+};
+int norms_grad_blocks(int T);
+hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s);
+hipError_t launch_post_norms_grad(const PostNormGradArgs& a, hipStream_t s);
+
+// Global norm of a list of gradients and their clipping (grad_norm.hip).
+// The lists are host arrays of include/moe.h's moe_tensor.
+long long grad_norm_parts(int n, const moe_tensor* t);  // doubles of scratch
+hipError_t launch_grad_norm(int n, const moe_tensor* t, float max_norm, float* norm,
+                            double* ws_part, hipStream_t s);
+hipError_t launch_grad_clip(int n, const moe_tensor* t, const float* norm, const moe_tensor* out,
+                            hipStream_t s);
 
 }  // namespace moe

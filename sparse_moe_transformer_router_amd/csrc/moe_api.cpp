@@ -33,6 +33,9 @@ int hip_fail(hipError_t e, const char* where) {
   return fail(MOE_ERR_HIP, "%s: %s", where, hipGetErrorString(e));
 }
 
+constexpr int32_t kMaxGradTensors = 1 << 16;
+constexpr int64_t kMaxGradElements = (int64_t)1 << 40;
+
 size_t align256(size_t v) { return (v + 255) & ~size_t(255); }
 
 size_t dtype_size(int32_t dt) { return dt == MOE_BF16 ? 2 : 4; }
@@ -185,6 +188,34 @@ B128Layout b128_layout(const moe_dims* d, long long T) {
   return L;
 }
 
+// Backward pass of the gated block over `rows` rows of width I.
+struct FfnGradLayout { size_t row_tok, slot_row, d_gu, hw, d_xs, part, total; };
+FfnGradLayout ffn_grad_layout(const moe_dims* d, long long rows, long long I, bool experts) {
+  FfnGradLayout L{};
+  const bool bf = d->act_dtype == MOE_BF16;
+  const size_t act = dtype_size(d->act_dtype), S = (size_t)rows;
+  size_t o = 0;
+  L.row_tok = region(o, 4 * S);
+  L.slot_row = region(o, experts ? 4 * S : 0);
+  L.d_gu = region(o, act * S * 2 * I);
+  L.hw = region(o, act * S * I);
+  L.d_xs = region(o, experts ? act * S * d->hidden : 0);
+  L.part = region(o, experts ? 4 * S * moe::ffn_grad_parts((int)I, bf) : 0);
+  L.total = o + 256;  // never 0, which says that the sizes are not supported
+  return L;
+}
+
+struct NormsGradLayout { size_t scalar, part, total; };
+NormsGradLayout norms_grad_layout(const moe_dims* d, long long T) {
+  NormsGradLayout L{};
+  const size_t nb = (size_t)moe::norms_grad_blocks((int)T);
+  size_t o = 0;
+  L.scalar = region(o, 8 * nb);
+  L.part = region(o, 4 * nb * 3 * d->hidden);
+  L.total = o + 256;
+  return L;
+}
+
 // The block's dense branch runs on a library-owned side stream (one per
 // device, default priority, created on first use and kept), forked from and
 // joined back into the caller's stream with two events.  A mutex keeps one
@@ -216,14 +247,19 @@ P* at(void* ws, size_t off) {
   return reinterpret_cast<P*>(static_cast<char*>(ws) + off);
 }
 
-int check_ws(size_t need, int32_t T, const void* ws, size_t ws_bytes) {
+int check_ws(size_t need, const char* what, const void* ws, size_t ws_bytes) {
   if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace is NULL");
   if (reinterpret_cast<uintptr_t>(ws) & 255u)
     return fail(MOE_ERR_WORKSPACE, "workspace is not 256-byte aligned");
   if (ws_bytes < need)
-    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed for T=%d", ws_bytes, need,
-                T);
+    return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, %zu needed for %s", ws_bytes, need,
+                what);
   return MOE_OK;
+}
+int check_ws(size_t need, int32_t T, const void* ws, size_t ws_bytes) {
+  char what[24];
+  snprintf(what, sizeof(what), "T=%d", T);
+  return check_ws(need, what, ws, ws_bytes);
 }
 int check_ws(const moe_dims* d, int32_t T, const void* ws, size_t ws_bytes) {
   return check_ws(layout(d, T).total, T, ws, ws_bytes);
@@ -304,7 +340,8 @@ int run_dispatch(const moe_dims* d, int32_t T, const int32_t* idx, int32_t* coun
 
 int run_gate_up(const moe_dims* d, int32_t T, const void* x, const void* w_gate_up,
                 const int32_t* offsets, const int32_t* sorted, void* h, hipStream_t s,
-                hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr) {
+                hipEvent_t ev_start = nullptr, hipEvent_t ev_stop = nullptr,
+                void* keep = nullptr) {
   const size_t act = dtype_size(d->act_dtype);
   const long long H = d->hidden, I = d->expert_inter;
   moe::GateUpArgs g{};
@@ -314,7 +351,7 @@ int run_gate_up(const moe_dims* d, int32_t T, const void* x, const void* w_gate_
   g.w_gate = w_gate_up;
   g.w_up = static_cast<const char*>(w_gate_up) + act * I * H;
   g.w_stride = 2 * I * H;
-  g.offsets = offsets; g.sorted_slots = sorted; g.h = h;
+  g.offsets = offsets; g.sorted_slots = sorted; g.h = h; g.keep = keep;
   g.ev_start = ev_start; g.ev_stop = ev_stop;
   hipError_t e = moe::launch_gate_up(g, s);
   return e == hipSuccess ? MOE_OK : hip_fail(e, "expert gate_up");
@@ -335,9 +372,10 @@ int run_down(const moe_dims* d, int32_t T, const void* h, const void* w_down,
 
 int run_expert_ffn(const moe_dims* d, int32_t T, const void* x, const void* w_gate_up,
                    const void* w_down, const float* topk_w, const int32_t* offsets,
-                   const int32_t* sorted, void* y, void* ws, hipStream_t s) {
+                   const int32_t* sorted, void* y, void* ws, hipStream_t s,
+                   void* keep = nullptr) {
   void* h = at<void>(ws, layout(d, T).h);
-  int rc = run_gate_up(d, T, x, w_gate_up, offsets, sorted, h, s);
+  int rc = run_gate_up(d, T, x, w_gate_up, offsets, sorted, h, s, nullptr, nullptr, keep);
   if (rc) return rc;
   return run_down(d, T, h, w_down, topk_w, offsets, sorted, y, s);
 }
@@ -421,6 +459,19 @@ struct LayerW {
   const void *gu, *gus, *dn, *dns;             // experts' gate_up, down (and scales)
 };
 
+// The dense MLP as one group whose rows are the tokens.
+void dense_args(const moe_dims* d, int32_t T, const void* x, const void* gate, const void* up,
+                const void* down, void* h, void* y, moe::GateUpArgs& g, moe::DownArgs& dd) {
+  const bool bf = d->act_dtype == MOE_BF16;
+  g.T = T; g.H = d->hidden; g.N = d->dense_inter; g.E = 1; g.K = 1; g.rows = T;
+  g.ident = true; g.bf16 = bf; g.x = x; g.w_gate = gate; g.w_up = up;
+  g.w_stride = 0; g.offsets = nullptr; g.sorted_slots = nullptr; g.h = h;
+  dd.T = T; dd.H = d->hidden; dd.N = d->dense_inter; dd.E = 1; dd.K = 1; dd.rows = T;
+  dd.ident = true; dd.bf16 = bf; dd.y_bf16 = d->slot_dtype == MOE_BF16; dd.h = h;
+  dd.w_down = down; dd.w_stride = 0; dd.offsets = nullptr; dd.sorted_slots = nullptr;
+  dd.topk_w = nullptr; dd.y = y;
+}
+
 // One dual-path layer: pre-norms; the dense branch on the side stream; router,
 // dispatch and experts on the caller's stream; the epilogue after the join.
 int run_layer(const moe_dims* dims, int32_t T, const void* residual, const LayerW& lw,
@@ -456,14 +507,8 @@ int run_layer(const moe_dims* dims, int32_t T, const void* residual, const Layer
     return hip_fail(e, "ffn layer (fork)");
 
   moe::GateUpArgs g{};
-  g.T = T; g.H = dims->hidden; g.N = dims->dense_inter; g.E = 1; g.K = 1; g.rows = T;
-  g.ident = true; g.bf16 = bf; g.x = xd; g.w_gate = lw.dg; g.w_up = lw.du;
-  g.w_stride = 0; g.offsets = nullptr; g.sorted_slots = nullptr; g.h = hd;
   moe::DownArgs dd{};
-  dd.T = T; dd.H = dims->hidden; dd.N = dims->dense_inter; dd.E = 1; dd.K = 1; dd.rows = T;
-  dd.ident = true; dd.bf16 = bf; dd.y_bf16 = dims->slot_dtype == MOE_BF16; dd.h = hd;
-  dd.w_down = lw.dd; dd.w_stride = 0; dd.offsets = nullptr; dd.sorted_slots = nullptr;
-  dd.topk_w = nullptr; dd.y = dnb;
+  dense_args(dims, T, xd, lw.dg, lw.du, lw.dd, hd, dnb, g, dd);
   if (lw.quant) {
     // one group: the per-expert strides are never applied
     g.w_fmt = lw.fmt; g.s_gate = lw.dgs; g.s_up = lw.dus; g.s_stride = 0;
@@ -499,6 +544,46 @@ int run_layer(const moe_dims* dims, int32_t T, const void* residual, const Layer
   ep.g_post = lw.g_post; ep.out = out; ep.ffn_out = ffn_out;
   if ((e = moe::launch_block_epilogue(ep, s)) != hipSuccess)
     return hip_fail(e, "ffn layer (epilogue)");
+  return MOE_OK;
+}
+
+int check_dense(const moe_dims* d) {
+  return d->dense_inter > 0 ? MOE_OK
+                            : fail(MOE_ERR_UNSUPPORTED, "the dense MLP needs dense_inter > 0");
+}
+
+int check_wgrad(const moe_dims* d, int32_t dt) {
+  if (dt != MOE_F32 && dt != MOE_BF16)
+    return fail(MOE_ERR_ARG, "d_weights_dtype=%d unknown", dt);
+  if (d->act_dtype == MOE_F32 && dt != MOE_F32)
+    return fail(MOE_ERR_UNSUPPORTED, "act_dtype F32 requires d_weights_dtype F32");
+  return MOE_OK;
+}
+
+void set_ffn_grad_ws(moe::FfnGradArgs& a, const FfnGradLayout& L, void* ws) {
+  a.ws_row_tok = at<int32_t>(ws, L.row_tok); a.ws_slot_row = at<int32_t>(ws, L.slot_row);
+  a.ws_d_gu = at<void>(ws, L.d_gu); a.ws_hw = at<void>(ws, L.hw);
+  a.ws_d_xs = at<void>(ws, L.d_xs); a.ws_part = at<float>(ws, L.part);
+}
+
+// A caller's list of gradients.
+int check_grads(const char* name, int32_t n, const moe_tensor* t) {
+  if (n < 0 || n > kMaxGradTensors)
+    return fail(MOE_ERR_ARG, "n=%d: need 0..%d", n, kMaxGradTensors);
+  if (n > 0 && !t) return fail(MOE_ERR_ARG, "%s is NULL", name);
+  int64_t total = 0;
+  for (int32_t i = 0; i < n; ++i) {
+    if (t[i].dtype != MOE_F32 && t[i].dtype != MOE_BF16)
+      return fail(MOE_ERR_ARG, "%s[%d].dtype=%d unknown", name, i, t[i].dtype);
+    if (t[i].numel < 0 || t[i].numel > kMaxGradElements ||
+        (total += t[i].numel) > kMaxGradElements)
+      return fail(MOE_ERR_UNSUPPORTED, "%s: more than 2^40 elements, or fewer than 0", name);
+    if (t[i].numel > 0) {
+      if (!t[i].data) return fail(MOE_ERR_ARG, "%s[%d].data is NULL", name, i);
+      if (reinterpret_cast<uintptr_t>(t[i].data) % dtype_size(t[i].dtype))
+        return fail(MOE_ERR_ARG, "%s[%d].data is not aligned to its type", name, i);
+    }
+  }
   return MOE_OK;
 }
 
@@ -1163,6 +1248,261 @@ int gemma4_ffn_block_q(const moe_dims* dims, int32_t T, const void* residual,
   lw.dn = wt->down_q; lw.dns = wt->down_scale;
   return run_layer(dims, T, residual, lw, out, ffn_out, topk_idx, topk_w, ws,
                    static_cast<hipStream_t>(stream));
+}
+
+// ---- the rest of the layer's training step ---------------------------------
+
+int moe_expert_ffn_keep(const moe_dims* dims, int32_t T, const void* x, const void* w_gate_up,
+                        const void* w_down, const float* topk_w, const int32_t* expert_offsets,
+                        const int32_t* sorted_slots, void* gate_up, void* y_slots, void* ws,
+                        size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(w_gate_up); REQUIRE_PTR(w_down); REQUIRE_PTR(topk_w);
+  REQUIRE_PTR(expert_offsets); REQUIRE_PTR(sorted_slots); REQUIRE_PTR(gate_up);
+  REQUIRE_PTR(y_slots);
+  if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+  return run_expert_ffn(dims, T, x, w_gate_up, w_down, topk_w, expert_offsets, sorted_slots,
+                        y_slots, ws, static_cast<hipStream_t>(stream), gate_up);
+}
+
+size_t moe_expert_ffn_grad_workspace_size(const moe_dims* dims, int32_t max_tokens) {
+  if (check_dims(dims, true) != MOE_OK || check_tokens(dims, max_tokens) != MOE_OK) return 0;
+  return ffn_grad_layout(dims, (long long)max_tokens * dims->top_k, dims->expert_inter, true)
+      .total;
+}
+
+int moe_expert_ffn_grad(const moe_dims* dims, int32_t T, const void* x, const void* w_gate_up,
+                        const void* w_down, const float* topk_w, const int32_t* expert_offsets,
+                        const int32_t* sorted_slots, const void* gate_up,
+                        const uint8_t* token_mask, const void* d_out, void* d_x, float* d_topk_w,
+                        int32_t d_weights_dtype, void* d_w_gate_up, void* d_w_down, void* ws,
+                        size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T)) ||
+      (rc = check_wgrad(dims, d_weights_dtype)))
+    return rc;
+  g_err.clear();
+  OPTIONAL_PTR(d_x); OPTIONAL_PTR(d_topk_w); OPTIONAL_PTR(d_w_gate_up); OPTIONAL_PTR(d_w_down);
+  if (!d_x && !d_topk_w && !d_w_gate_up && !d_w_down)
+    return fail(MOE_ERR_ARG, "every output is NULL");
+  const long long H = dims->hidden, I = dims->expert_inter;
+  const FfnGradLayout L = ffn_grad_layout(dims, (long long)T * dims->top_k, I, true);
+  if (T > 0) {
+    REQUIRE_PTR(x); REQUIRE_PTR(w_gate_up); REQUIRE_PTR(w_down); REQUIRE_PTR(topk_w);
+    REQUIRE_PTR(expert_offsets); REQUIRE_PTR(sorted_slots); REQUIRE_PTR(gate_up);
+    OPTIONAL_PTR(token_mask); REQUIRE_PTR(d_out);
+    if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
+  }
+  const size_t act = dtype_size(dims->act_dtype), wg = dtype_size(d_weights_dtype);
+  moe::FfnGradArgs a{};
+  a.T = T; a.H = dims->hidden; a.I = dims->expert_inter; a.E = dims->num_experts;
+  a.K = dims->top_k; a.rows = T * dims->top_k; a.ident = false;
+  a.bf16 = dims->act_dtype == MOE_BF16; a.wgrad_bf16 = d_weights_dtype == MOE_BF16;
+  a.x = x; a.w_gate = w_gate_up;
+  a.w_up = w_gate_up ? static_cast<const char*>(w_gate_up) + act * I * H : nullptr;
+  a.gu_stride = 2 * I * H; a.w_down = w_down; a.dn_stride = H * I;
+  a.topk_w = topk_w; a.offsets = expert_offsets; a.sorted_slots = sorted_slots;
+  a.kept = gate_up; a.mask = token_mask; a.d_out = d_out; a.d_x = d_x; a.d_topk_w = d_topk_w;
+  a.d_gate = d_w_gate_up;
+  a.d_up = d_w_gate_up ? static_cast<char*>(d_w_gate_up) + wg * I * H : nullptr;
+  a.d_down = d_w_down;
+  set_ffn_grad_ws(a, L, ws);
+  hipError_t e = moe::launch_ffn_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_expert_ffn_grad");
+}
+
+int gemma4_dense_mlp(const moe_dims* dims, int32_t T, const void* x, const void* dense_gate,
+                     const void* dense_up, const void* dense_down, void* gate_up, void* y,
+                     void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T)) || (rc = check_dense(dims)))
+    return rc;
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(dense_gate); REQUIRE_PTR(dense_up); REQUIRE_PTR(dense_down);
+  OPTIONAL_PTR(gate_up); REQUIRE_PTR(y);
+  if ((rc = check_ws(dims, T, ws, ws_bytes))) return rc;
+  moe::GateUpArgs g{};
+  moe::DownArgs dd{};
+  dense_args(dims, T, x, dense_gate, dense_up, dense_down, at<void>(ws, layout(dims, T).hd), y, g,
+             dd);
+  g.keep = gate_up;
+  const hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = moe::launch_gate_up(g, s);
+  if (e == hipSuccess) e = moe::launch_down(dd, s);
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "gemma4_dense_mlp");
+}
+
+size_t gemma4_dense_mlp_grad_workspace_size(const moe_dims* dims, int32_t max_tokens) {
+  if (check_dims(dims, true) != MOE_OK || check_tokens(dims, max_tokens) != MOE_OK ||
+      check_dense(dims) != MOE_OK)
+    return 0;
+  return ffn_grad_layout(dims, max_tokens, dims->dense_inter, false).total;
+}
+
+int gemma4_dense_mlp_grad(const moe_dims* dims, int32_t T, const void* x, const void* dense_gate,
+                          const void* dense_up, const void* dense_down, const void* gate_up,
+                          const uint8_t* token_mask, const void* d_y, void* d_x,
+                          int32_t d_weights_dtype, void* d_gate, void* d_up, void* d_down,
+                          void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T)) || (rc = check_dense(dims)) ||
+      (rc = check_wgrad(dims, d_weights_dtype)))
+    return rc;
+  g_err.clear();
+  OPTIONAL_PTR(d_x); OPTIONAL_PTR(d_gate); OPTIONAL_PTR(d_up); OPTIONAL_PTR(d_down);
+  if (!d_gate != !d_up) return fail(MOE_ERR_ARG, "d_gate and d_up go together");
+  if (!d_x && !d_gate && !d_down) return fail(MOE_ERR_ARG, "every output is NULL");
+  const FfnGradLayout L = ffn_grad_layout(dims, T, dims->dense_inter, false);
+  if (T > 0) {
+    REQUIRE_PTR(x); REQUIRE_PTR(dense_gate); REQUIRE_PTR(dense_up); REQUIRE_PTR(dense_down);
+    REQUIRE_PTR(gate_up); OPTIONAL_PTR(token_mask); REQUIRE_PTR(d_y);
+    if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
+  }
+  moe::FfnGradArgs a{};
+  a.T = T; a.H = dims->hidden; a.I = dims->dense_inter; a.E = 1; a.K = 1; a.rows = T;
+  a.ident = true; a.bf16 = dims->act_dtype == MOE_BF16;
+  a.wgrad_bf16 = d_weights_dtype == MOE_BF16;
+  a.x = x; a.w_gate = dense_gate; a.w_up = dense_up; a.w_down = dense_down;
+  a.kept = gate_up; a.mask = token_mask; a.d_out = d_y; a.d_x = d_x;
+  a.d_gate = d_gate; a.d_up = d_up; a.d_down = d_down;
+  set_ffn_grad_ws(a, L, ws);
+  hipError_t e = moe::launch_ffn_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "gemma4_dense_mlp_grad");
+}
+
+int gemma4_pre_norms(const moe_dims* dims, int32_t T, const void* x, const float* g_pre,
+                     const float* g_pre2, void* xd, void* xm, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(g_pre); REQUIRE_PTR(g_pre2); REQUIRE_PTR(xd); REQUIRE_PTR(xm);
+  moe::PreNormArgs a{};
+  a.T = T; a.H = dims->hidden; a.eps = dims->eps; a.bf16 = dims->act_dtype == MOE_BF16;
+  a.x = x; a.g_pre = g_pre; a.g_pre2 = g_pre2; a.xd = xd; a.xm = xm;
+  hipError_t e = moe::launch_prenorm(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "gemma4_pre_norms");
+}
+
+int gemma4_post_norms(const moe_dims* dims, int32_t T, const void* x, const void* y_slots,
+                      const void* dn, const float* g_post1, const float* g_post2,
+                      const float* g_post, float layer_scalar, void* out, void* moe_sum,
+                      float* ffn_out, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  if (T == 0) return MOE_OK;
+  REQUIRE_PTR(x); REQUIRE_PTR(y_slots); REQUIRE_PTR(dn); REQUIRE_PTR(g_post1);
+  REQUIRE_PTR(g_post2); REQUIRE_PTR(g_post); REQUIRE_PTR(out); OPTIONAL_PTR(moe_sum);
+  OPTIONAL_PTR(ffn_out);
+  moe::EpilogueArgs a{};
+  a.T = T; a.H = dims->hidden; a.K = dims->top_k; a.eps = dims->eps;
+  a.layer_scalar = layer_scalar; a.y_bf16 = dims->slot_dtype == MOE_BF16;
+  a.act_bf16 = dims->act_dtype == MOE_BF16; a.y = y_slots; a.dn = dn; a.x = x;
+  a.g_post1 = g_post1; a.g_post2 = g_post2; a.g_post = g_post; a.out = out; a.ffn_out = ffn_out;
+  a.moe_sum = moe_sum;
+  hipError_t e = moe::launch_block_epilogue(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "gemma4_post_norms");
+}
+
+size_t gemma4_norms_grad_workspace_size(const moe_dims* dims, int32_t max_tokens) {
+  if (check_dims(dims, true) != MOE_OK || check_tokens(dims, max_tokens) != MOE_OK) return 0;
+  return norms_grad_layout(dims, max_tokens).total;
+}
+
+int gemma4_pre_norms_grad(const moe_dims* dims, int32_t T, const void* x, const float* g_pre,
+                          const float* g_pre2, const uint8_t* token_mask, const void* d_xd,
+                          const void* d_xm, const void* d_x_add, const void* d_out,
+                          float layer_scalar, void* d_x, float* d_g_pre, float* d_g_pre2,
+                          void* ws, size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  REQUIRE_PTR(d_g_pre); REQUIRE_PTR(d_g_pre2);
+  const NormsGradLayout L = norms_grad_layout(dims, T);
+  if (T > 0) {
+    REQUIRE_PTR(x); REQUIRE_PTR(g_pre); REQUIRE_PTR(g_pre2); OPTIONAL_PTR(token_mask);
+    REQUIRE_PTR(d_xd); REQUIRE_PTR(d_xm); OPTIONAL_PTR(d_x_add); OPTIONAL_PTR(d_out);
+    REQUIRE_PTR(d_x);
+    if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
+  }
+  moe::PreNormGradArgs a{};
+  a.T = T; a.H = dims->hidden; a.eps = dims->eps; a.scalar = layer_scalar;
+  a.bf16 = dims->act_dtype == MOE_BF16;
+  a.x = x; a.g1 = g_pre; a.g2 = g_pre2; a.mask = token_mask; a.d_xd = d_xd; a.d_xm = d_xm;
+  a.d_add = d_x_add; a.d_out = d_out; a.d_x = d_x; a.d_g1 = d_g_pre; a.d_g2 = d_g_pre2;
+  a.ws_part = at<float>(ws, L.part);
+  hipError_t e = moe::launch_pre_norms_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "gemma4_pre_norms_grad");
+}
+
+int gemma4_post_norms_grad(const moe_dims* dims, int32_t T, const void* x, const void* dn,
+                           const void* moe_sum, const float* g_post1, const float* g_post2,
+                           const float* g_post, float layer_scalar, const uint8_t* token_mask,
+                           const void* d_out, void* d_dn, void* d_moe, float* d_g_post1,
+                           float* d_g_post2, float* d_g_post, float* d_layer_scalar, void* ws,
+                           size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_dims(dims, true)) || (rc = check_tokens(dims, T))) return rc;
+  g_err.clear();
+  REQUIRE_PTR(d_g_post1); REQUIRE_PTR(d_g_post2); REQUIRE_PTR(d_g_post);
+  OPTIONAL_PTR(d_layer_scalar);
+  const NormsGradLayout L = norms_grad_layout(dims, T);
+  if (T > 0) {
+    if (d_layer_scalar) REQUIRE_PTR(x);
+    REQUIRE_PTR(dn); REQUIRE_PTR(moe_sum); REQUIRE_PTR(g_post1); REQUIRE_PTR(g_post2);
+    REQUIRE_PTR(g_post); OPTIONAL_PTR(token_mask); REQUIRE_PTR(d_out); REQUIRE_PTR(d_dn);
+    REQUIRE_PTR(d_moe);
+    if ((rc = check_ws(L.total, T, ws, ws_bytes))) return rc;
+  }
+  moe::PostNormGradArgs a{};
+  a.T = T; a.H = dims->hidden; a.eps = dims->eps; a.scalar = layer_scalar;
+  a.bf16 = dims->act_dtype == MOE_BF16; a.y_bf16 = dims->slot_dtype == MOE_BF16;
+  a.x = x; a.dn = dn; a.moe_sum = moe_sum; a.g1 = g_post1; a.g2 = g_post2; a.g3 = g_post;
+  a.mask = token_mask; a.d_out = d_out; a.d_dn = d_dn; a.d_moe = d_moe;
+  a.d_g1 = d_g_post1; a.d_g2 = d_g_post2; a.d_g3 = d_g_post; a.d_scalar = d_layer_scalar;
+  a.ws_part = at<float>(ws, L.part); a.ws_scalar = at<double>(ws, L.scalar);
+  hipError_t e = moe::launch_post_norms_grad(a, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "gemma4_post_norms_grad");
+}
+
+size_t moe_grad_norm_workspace_size(int32_t n, const moe_tensor* grads) {
+  if (check_grads("grads", n, grads) != MOE_OK) return 0;
+  return align256(8 * (size_t)moe::grad_norm_parts(n, grads)) + 256;
+}
+
+int moe_grad_norm(int32_t n, const moe_tensor* grads, float max_norm, float* norm, void* ws,
+                  size_t ws_bytes, void* stream) {
+  int rc;
+  if ((rc = check_grads("grads", n, grads))) return rc;
+  if (!(max_norm > 0.0f)) return fail(MOE_ERR_ARG, "max_norm must be > 0");
+  g_err.clear();
+  REQUIRE_PTR(norm);
+  const size_t need = align256(8 * (size_t)moe::grad_norm_parts(n, grads)) + 256;
+  if ((rc = check_ws(need, "this list", ws, ws_bytes))) return rc;
+  hipError_t e = moe::launch_grad_norm(n, grads, max_norm, norm, static_cast<double*>(ws),
+                                       static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_grad_norm");
+}
+
+int moe_grad_clip(int32_t n, const moe_tensor* grads, const float* norm, const moe_tensor* out,
+                  void* stream) {
+  int rc;
+  if ((rc = check_grads("grads", n, grads)) || (out && (rc = check_grads("out", n, out))))
+    return rc;
+  for (int32_t i = 0; out && i < n; ++i)
+    if (grads[i].numel != out[i].numel)
+      return fail(MOE_ERR_ARG, "out[%d] has %lld elements, grads[%d] %lld", i,
+                  (long long)out[i].numel, i, (long long)grads[i].numel);
+  g_err.clear();
+  if (n == 0) return MOE_OK;
+  REQUIRE_PTR(norm);
+  hipError_t e = moe::launch_grad_clip(n, grads, norm, out, static_cast<hipStream_t>(stream));
+  return e == hipSuccess ? MOE_OK : hip_fail(e, "moe_grad_clip");
 }
 
 }  // extern "C"

@@ -45,6 +45,10 @@ class Gemma4FfnWeightsQ(ctypes.Structure):
         "down_scale")] + [("layer_scalar", ctypes.c_float)]
 
 
+class MoeTensor(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("numel", ctypes.c_int64), ("dtype", ctypes.c_int32)]
+
+
 class MoeError(RuntimeError):
     def __init__(self, code: int, msg: str):
         super().__init__(f"libmoe error {code}: {msg}")
@@ -55,6 +59,11 @@ class MoeError(RuntimeError):
 _WS_SIZES = {"layer": "moe_workspace_size", "balance_loss": "moe_balance_loss_workspace_size",
              "router_grad": "moe_router_grad_workspace_size",
              "expert_ffn_b128": "moe_expert_ffn_b128_workspace_size"}
+
+
+# Size functions of the calls whose workspace is asked for by a function of its own.
+_OWN_WS_SIZES = ("moe_expert_ffn_grad_workspace_size", "gemma4_dense_mlp_grad_workspace_size",
+                 "gemma4_norms_grad_workspace_size")
 
 
 def _load():
@@ -82,6 +91,22 @@ def _load():
     L.moe_linear_b128_workspace_size.restype = SZ
     L.moe_linear_b128.argtypes = [I32, I32, I32] + [P] * 4 + [I32, P, SZ, P]
     L.moe_expert_ffn_b128.argtypes = [D, I32] + [P] * 10 + [SZ, P]
+    TN = ctypes.POINTER(MoeTensor)
+    for f in _OWN_WS_SIZES:
+        getattr(L, f).argtypes = [D, I32]
+        getattr(L, f).restype = SZ
+    L.moe_grad_norm_workspace_size.argtypes = [I32, TN]
+    L.moe_grad_norm_workspace_size.restype = SZ
+    L.moe_expert_ffn_keep.argtypes = [D, I32] + [P] * 9 + [SZ, P]
+    L.moe_expert_ffn_grad.argtypes = [D, I32] + [P] * 11 + [I32] + [P] * 3 + [SZ, P]
+    L.gemma4_dense_mlp.argtypes = [D, I32] + [P] * 7 + [SZ, P]
+    L.gemma4_dense_mlp_grad.argtypes = [D, I32] + [P] * 8 + [I32] + [P] * 4 + [SZ, P]
+    L.gemma4_pre_norms.argtypes = [D, I32] + [P] * 6
+    L.gemma4_post_norms.argtypes = [D, I32] + [P] * 6 + [F] + [P] * 4
+    L.gemma4_pre_norms_grad.argtypes = [D, I32] + [P] * 8 + [F] + [P] * 4 + [SZ, P]
+    L.gemma4_post_norms_grad.argtypes = [D, I32] + [P] * 6 + [F] + [P] * 9 + [SZ, P]
+    L.moe_grad_norm.argtypes = [I32, TN, F, P, P, SZ, P]
+    L.moe_grad_clip.argtypes = [I32, TN, P, TN, P]
     L.moe_route.argtypes = [D, I32] + [P] * 11 + [SZ, P]
     L.moe_dispatch.argtypes = [D, I32] + [P] * 5 + [SZ, P]
     L.moe_expert_ffn.argtypes = [D, I32] + [P] * 8 + [SZ, P]
@@ -109,7 +134,10 @@ def _load():
               "gemma4_ffn_block_q", "moe_forward_noalloc", "moe_expert_ffn_mx",
               "moe_router_logits", "moe_balance_loss", "moe_balance_loss_grad",
               "moe_router_grad", "moe_quantize_b128", "moe_dequantize_b128", "moe_linear_b128",
-              "moe_expert_ffn_b128"):
+              "moe_expert_ffn_b128", "moe_expert_ffn_keep", "moe_expert_ffn_grad",
+              "gemma4_dense_mlp", "gemma4_dense_mlp_grad", "gemma4_pre_norms",
+              "gemma4_post_norms", "gemma4_pre_norms_grad", "gemma4_post_norms_grad",
+              "moe_grad_norm", "moe_grad_clip"):
         getattr(L, f).restype = ctypes.c_int
     return L
 
@@ -290,6 +318,219 @@ def moe_router_grad(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_
         _arg("d_per_expert_scale", d_per_expert_scale, f32, E, dev),
         _arg("d_pre_norm_gain", d_pre_norm_gain, f32, H, dev, True), *_work(ws, dev),
         _stream(stream, dev)))
+
+
+def _slot(d: MoeDims):
+    return torch.bfloat16 if d.slot_dtype == MOE_BF16 else torch.float32
+
+
+_FLOAT = (torch.bfloat16, torch.float32)
+
+
+def _dtype(*tensors):
+    """moe_dtype code that the tensors given share (MOE_F32 where none is)."""
+    kinds = {t.dtype for t in tensors if t is not None}
+    if len(kinds) > 1:
+        raise TypeError(f"weight gradients of several types: {sorted(map(str, kinds))}")
+    return MOE_BF16 if kinds == {torch.bfloat16} else MOE_F32
+
+
+def _own_workspace(size, d, max_tokens, device):
+    n = getattr(_lib, size)(ctypes.byref(d), max_tokens)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def expert_ffn_grad_workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of moe_expert_ffn_grad_workspace_size bytes."""
+    return _own_workspace("moe_expert_ffn_grad_workspace_size", d, max_tokens, device)
+
+
+def dense_mlp_grad_workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of gemma4_dense_mlp_grad_workspace_size bytes."""
+    return _own_workspace("gemma4_dense_mlp_grad_workspace_size", d, max_tokens, device)
+
+
+def norms_grad_workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of gemma4_norms_grad_workspace_size bytes."""
+    return _own_workspace("gemma4_norms_grad_workspace_size", d, max_tokens, device)
+
+
+def moe_expert_ffn_keep(d, T, x, w_gate_up, w_down, topk_w, offsets, sorted_slots, gate_up,
+                        y_slots, ws, stream=None):
+    """moe_expert_ffn, with the projections gate_up [T * K, 2I] as an output."""
+    H, E, I, S, a = d.hidden, d.num_experts, d.expert_inter, T * d.top_k, _act(d)
+    f32, i32, dev = torch.float32, torch.int32, _device()
+    _check(_lib.moe_expert_ffn_keep(
+        ctypes.byref(d), T, _arg("x", x, a, T * H, dev),
+        _arg("w_gate_up", w_gate_up, a, E * 2 * I * H, dev),
+        _arg("w_down", w_down, a, E * H * I, dev), _arg("topk_w", topk_w, f32, S, dev),
+        _arg("offsets", offsets, i32, E + 1, dev),
+        _arg("sorted_slots", sorted_slots, i32, S, dev),
+        _arg("gate_up", gate_up, a, S * 2 * I, dev),
+        _arg("y_slots", y_slots, _slot(d), S * H, dev), *_work(ws, dev), _stream(stream, dev)))
+
+
+def moe_expert_ffn_grad(d, T, x, w_gate_up, w_down, topk_w, offsets, sorted_slots, gate_up,
+                        token_mask, d_out, d_x, d_topk_w, d_w_gate_up, d_w_down, ws,
+                        stream=None):
+    """Backward pass of moe_expert_ffn_keep and the slots' sum.  The weights' gradients
+    are both fp32 or both of the activations' type."""
+    H, E, I, S, a = d.hidden, d.num_experts, d.expert_inter, T * d.top_k, _act(d)
+    f32, i32, dev = torch.float32, torch.int32, _device()
+    _check(_lib.moe_expert_ffn_grad(
+        ctypes.byref(d), T, _arg("x", x, a, T * H, dev),
+        _arg("w_gate_up", w_gate_up, a, E * 2 * I * H, dev),
+        _arg("w_down", w_down, a, E * H * I, dev), _arg("topk_w", topk_w, f32, S, dev),
+        _arg("offsets", offsets, i32, E + 1, dev),
+        _arg("sorted_slots", sorted_slots, i32, S, dev),
+        _arg("gate_up", gate_up, a, S * 2 * I, dev),
+        _arg("token_mask", token_mask, _MASK, T, dev, True), _arg("d_out", d_out, a, T * H, dev),
+        _arg("d_x", d_x, a, T * H, dev, True), _arg("d_topk_w", d_topk_w, f32, S, dev, True),
+        _dtype(d_w_gate_up, d_w_down),
+        _arg("d_w_gate_up", d_w_gate_up, _FLOAT, E * 2 * I * H, dev, True),
+        _arg("d_w_down", d_w_down, _FLOAT, E * H * I, dev, True), *_work(ws, dev),
+        _stream(stream, dev)))
+
+
+def gemma4_dense_mlp(d, T, x, dense_gate, dense_up, dense_down, gate_up, y, ws, stream=None):
+    """The dense MLP; gate_up [T, 2D] or None receives its projections."""
+    H, D, a, dev = d.hidden, d.dense_inter, _act(d), _device()
+    _check(_lib.gemma4_dense_mlp(
+        ctypes.byref(d), T, _arg("x", x, a, T * H, dev),
+        _arg("dense_gate", dense_gate, a, D * H, dev), _arg("dense_up", dense_up, a, D * H, dev),
+        _arg("dense_down", dense_down, a, H * D, dev),
+        _arg("gate_up", gate_up, a, T * 2 * D, dev, True), _arg("y", y, _slot(d), T * H, dev),
+        *_work(ws, dev), _stream(stream, dev)))
+
+
+def gemma4_dense_mlp_grad(d, T, x, dense_gate, dense_up, dense_down, gate_up, token_mask, d_y,
+                          d_x, d_gate, d_up, d_down, ws, stream=None):
+    """Backward pass of gemma4_dense_mlp.  The weights' gradients are all fp32 or all of
+    the activations' type."""
+    H, D, a, dev = d.hidden, d.dense_inter, _act(d), _device()
+    _check(_lib.gemma4_dense_mlp_grad(
+        ctypes.byref(d), T, _arg("x", x, a, T * H, dev),
+        _arg("dense_gate", dense_gate, a, D * H, dev), _arg("dense_up", dense_up, a, D * H, dev),
+        _arg("dense_down", dense_down, a, H * D, dev), _arg("gate_up", gate_up, a, T * 2 * D, dev),
+        _arg("token_mask", token_mask, _MASK, T, dev, True), _arg("d_y", d_y, a, T * H, dev),
+        _arg("d_x", d_x, a, T * H, dev, True), _dtype(d_gate, d_up, d_down),
+        _arg("d_gate", d_gate, _FLOAT, D * H, dev, True),
+        _arg("d_up", d_up, _FLOAT, D * H, dev, True),
+        _arg("d_down", d_down, _FLOAT, H * D, dev, True), *_work(ws, dev), _stream(stream, dev)))
+
+
+def gemma4_pre_norms(d, T, x, g_pre, g_pre2, xd, xm, stream=None):
+    """xd, xm: the two pre-norms of x."""
+    n, H, a, f32, dev = T * d.hidden, d.hidden, _act(d), torch.float32, _device()
+    _check(_lib.gemma4_pre_norms(
+        ctypes.byref(d), T, _arg("x", x, a, n, dev), _arg("g_pre", g_pre, f32, H, dev),
+        _arg("g_pre2", g_pre2, f32, H, dev), _arg("xd", xd, a, n, dev),
+        _arg("xm", xm, a, n, dev), _stream(stream, dev)))
+
+
+def gemma4_post_norms(d, T, x, y_slots, dn, g_post1, g_post2, g_post, layer_scalar, out, moe_sum,
+                      ffn_out, stream=None):
+    """The layer's end: the slots' sum (to moe_sum unless None), the post-norms, the
+    residual and layer_scalar."""
+    n, H, a, f32, dev = T * d.hidden, d.hidden, _act(d), torch.float32, _device()
+    _check(_lib.gemma4_post_norms(
+        ctypes.byref(d), T, _arg("x", x, a, n, dev),
+        _arg("y_slots", y_slots, _slot(d), n * d.top_k, dev), _arg("dn", dn, _slot(d), n, dev),
+        _arg("g_post1", g_post1, f32, H, dev), _arg("g_post2", g_post2, f32, H, dev),
+        _arg("g_post", g_post, f32, H, dev), layer_scalar, _arg("out", out, a, n, dev),
+        _arg("moe_sum", moe_sum, _slot(d), n, dev, True),
+        _arg("ffn_out", ffn_out, f32, n, dev, True), _stream(stream, dev)))
+
+
+def gemma4_pre_norms_grad(d, T, x, g_pre, g_pre2, token_mask, d_xd, d_xm, d_x_add, d_out,
+                          layer_scalar, d_x, d_g_pre, d_g_pre2, ws, stream=None):
+    """Backward pass of gemma4_pre_norms, plus d_x_add and layer_scalar * d_out."""
+    n, H, a, f32, dev = T * d.hidden, d.hidden, _act(d), torch.float32, _device()
+    _check(_lib.gemma4_pre_norms_grad(
+        ctypes.byref(d), T, _arg("x", x, a, n, dev), _arg("g_pre", g_pre, f32, H, dev),
+        _arg("g_pre2", g_pre2, f32, H, dev), _arg("token_mask", token_mask, _MASK, T, dev, True),
+        _arg("d_xd", d_xd, a, n, dev), _arg("d_xm", d_xm, a, n, dev),
+        _arg("d_x_add", d_x_add, a, n, dev, True), _arg("d_out", d_out, a, n, dev, True),
+        layer_scalar, _arg("d_x", d_x, a, n, dev), _arg("d_g_pre", d_g_pre, f32, H, dev),
+        _arg("d_g_pre2", d_g_pre2, f32, H, dev), *_work(ws, dev), _stream(stream, dev)))
+
+
+def gemma4_post_norms_grad(d, T, x, dn, moe_sum, g_post1, g_post2, g_post, layer_scalar,
+                           token_mask, d_out, d_dn, d_moe, d_g_post1, d_g_post2, d_g_post,
+                           d_layer_scalar, ws, stream=None):
+    """Backward pass of gemma4_post_norms; x and d_layer_scalar may both be None."""
+    n, H, a, f32, dev = T * d.hidden, d.hidden, _act(d), torch.float32, _device()
+    _check(_lib.gemma4_post_norms_grad(
+        ctypes.byref(d), T, _arg("x", x, a, n, dev, True), _arg("dn", dn, _slot(d), n, dev),
+        _arg("moe_sum", moe_sum, _slot(d), n, dev), _arg("g_post1", g_post1, f32, H, dev),
+        _arg("g_post2", g_post2, f32, H, dev), _arg("g_post", g_post, f32, H, dev), layer_scalar,
+        _arg("token_mask", token_mask, _MASK, T, dev, True), _arg("d_out", d_out, a, n, dev),
+        _arg("d_dn", d_dn, a, n, dev), _arg("d_moe", d_moe, a, n, dev),
+        _arg("d_g_post1", d_g_post1, f32, H, dev), _arg("d_g_post2", d_g_post2, f32, H, dev),
+        _arg("d_g_post", d_g_post, f32, H, dev),
+        _arg("d_layer_scalar", d_layer_scalar, f32, 1, dev, True), *_work(ws, dev),
+        _stream(stream, dev)))
+
+
+class GradList:
+    """A list of gradients for moe_grad_norm and moe_grad_clip: made once, used as long
+    as the tensors keep their memory (it holds them)."""
+
+    def __init__(self, tensors):
+        self.tensors = list(tensors)
+        self.device = _device()
+        spans = []
+        for i, t in enumerate(self.tensors):
+            _arg(f"tensor {i}", t, _FLOAT, 0, self.device)
+            if t.numel():
+                spans.append((t.data_ptr(), t.data_ptr() + t.numel() * t.element_size(), i))
+        spans.sort()
+        for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
+            if start < end:
+                raise ValueError(f"tensors {i} and {j} overlap")
+        self.n = len(self.tensors)
+        self.array = (MoeTensor * self.n)(*[
+            (t.data_ptr(), t.numel(), MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32)
+            for t in self.tensors])
+
+    def _on(self, dev):
+        if self.device != dev:
+            raise ValueError("the list's tensors are not on the current GPU")
+        return self.array
+
+
+def grad_list(tensors) -> GradList:
+    """The gradients (contiguous, fp32 or bf16, of any sizes, none overlapping another)
+    that moe_grad_norm and moe_grad_clip take."""
+    return GradList(tensors)
+
+
+def grad_norm_workspace(grads: GradList, device="cuda") -> torch.Tensor:
+    """A uint8 device buffer of moe_grad_norm_workspace_size bytes."""
+    n = _lib.moe_grad_norm_workspace_size(grads.n, grads.array)
+    if n == 0:
+        raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def moe_grad_norm(grads: GradList, max_norm, norm, ws, stream=None):
+    """norm [2] = {global norm, factor that brings it to max_norm at most}."""
+    dev = _device()
+    _check(_lib.moe_grad_norm(grads.n, grads._on(dev), max_norm,
+                              _arg("norm", norm, torch.float32, 2, dev), *_work(ws, dev),
+                              _stream(stream, dev)))
+
+
+def moe_grad_clip(grads: GradList, norm, out: Optional[GradList] = None, stream=None):
+    """out (None: grads themselves) = grads * norm[1]."""
+    dev = _device()
+    if out is not None and out.n != grads.n:
+        raise ValueError(f"out has {out.n} tensors, grads {grads.n}")
+    _check(_lib.moe_grad_clip(grads.n, grads._on(dev),
+                              _arg("norm", norm, torch.float32, 2, dev),
+                              None if out is None else out._on(dev), _stream(stream, dev)))
 
 
 def moe_route(d, T, x, router_w, router_scale, per_expert_scale, pre_norm_gain, topk_idx, topk_w,
