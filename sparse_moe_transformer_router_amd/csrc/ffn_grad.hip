@@ -18,7 +18,7 @@
 // d_w comes from <v, h>, not from <d, W_d h>: it needs no expert output kept.
 // Rows are the expert-sorted slots of the dispatch; row_tok maps a row to its
 // token, -1 where the token does not count: such a row enters every product as
-// zeros (read from a page of zeros), whatever its token's data hold.
+// zeros, whatever its token's data hold.
 #include <type_traits>
 
 #include "common.h"
@@ -30,10 +30,9 @@ namespace {
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef __bf16 bf16x4 __attribute__((ext_vector_type(4)));
 
-enum Kind { kDU = 0, kDX = 1, kDWGU = 2, kDWDN = 3 };
+constexpr unsigned kNowhere = 0xF0000000u;  // an offset past every buffer here
 
-// A row of zeros as long as the widest operand row.
-__device__ const uint4 zero_row[8192 * 2 / 16] = {};
+enum Kind { kDU = 0, kDX = 1, kDWGU = 2, kDWDN = 3 };
 
 // h, and with v = W_d^T d the gradients of the gate and of the up projection
 // (without the routing weight).  gelu(z) = z s(z), s the logistic function of
@@ -55,14 +54,16 @@ __device__ __forceinline__ void act_grad(float z, float up, float v, float& h, f
   du = v * gelu;
 }
 
-// Row r of the sorted order -> its token, -1 if the token does not count; slot ->
-// its row.  A slot that the dispatch dropped keeps whatever the workspace held:
+// Row r of the sorted order -> its token, -1 if the token does not count, and that
+// token's byte offset in a bf16 [T, H], kNowhere if it does not; slot -> its row.  A slot that the dispatch dropped keeps whatever the workspace held:
 // readers of slot_row check that sorted_slots points back.
 __global__ __launch_bounds__(256) void rows_kernel(int rows, int ident, int E, int K,
                                                    const int32_t* __restrict__ offsets,
                                                    const int32_t* __restrict__ sorted_slots,
                                                    const uint8_t* __restrict__ mask,
+                                                   unsigned row_bytes,
                                                    int32_t* __restrict__ row_tok,
+                                                   unsigned* __restrict__ row_off,
                                                    int32_t* __restrict__ slot_row) {
   const int r = blockIdx.x * 256 + threadIdx.x;
   if (r >= (ident ? rows : offsets[E])) return;
@@ -72,16 +73,18 @@ __global__ __launch_bounds__(256) void rows_kernel(int rows, int ident, int E, i
     slot_row[slot] = r;
     tok = slot / K;
   }
-  row_tok[r] = mask && !mask[tok] ? -1 : tok;
+  if (mask && !mask[tok]) tok = -1;
+  row_tok[r] = tok;
+  row_off[r] = tok < 0 ? kNowhere : (unsigned)tok * row_bytes;
 }
 
 // d_x[t] = sum over t's slots (k ascending) of their rows of d_xs, in fp32;
 // d_topk_w[t, k] = the sum of its row's partial sums (column tiles ascending).
-template <typename XT>
+template <typename XT, typename ST>
 __global__ __launch_bounds__(256) void combine_grad_kernel(
     int T, int H, int K, int E, int parts, long long part_stride,
     const int32_t* __restrict__ offsets, const int32_t* __restrict__ sorted_slots,
-    const int32_t* __restrict__ slot_row, const XT* __restrict__ d_xs,
+    const int32_t* __restrict__ slot_row, const ST* __restrict__ d_xs,
     const float* __restrict__ part, XT* __restrict__ d_x, float* __restrict__ d_topk_w) {
   __shared__ int row_of[256];
   const int t = blockIdx.x;
@@ -103,18 +106,18 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
   for (int c = threadIdx.x * 8; c < H; c += 256 * 8) {
     float acc[8] = {0, 0, 0, 0, 0, 0, 0, 0};
     for (int k0 = 0; k0 < K; k0 += 8) {
-      XT v[8][8];
+      ST v[8][8];
 #pragma unroll
       for (int kk = 0; kk < 8; ++kk) {
         const int r = k0 + kk < K ? row_of[k0 + kk] : -1;
         if (r >= 0) {
           const uint4* q = reinterpret_cast<const uint4*>(d_xs + (size_t)r * H + c);
 #pragma unroll
-          for (int i = 0; i < (int)(sizeof(XT) / 2); ++i)
+          for (int i = 0; i < (int)(sizeof(ST) / 2); ++i)
             reinterpret_cast<uint4*>(v[kk])[i] = q[i];
         } else {
 #pragma unroll
-          for (int j = 0; j < 8; ++j) v[kk][j] = (XT)0.0f;
+          for (int j = 0; j < 8; ++j) v[kk][j] = (ST)0.0f;
         }
       }
 #pragma unroll
@@ -133,9 +136,10 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
 
 // Operands of one product; which are used depends on the kind.
 struct Operands {
-  int H, I, E, K, rows, ident;
+  int T, H, I, E, K, rows, ident;
   const int32_t* offsets;
   const int32_t* row_tok;
+  const unsigned* row_off;
   const int32_t* sorted_slots;
   const float* topk_w;
   const void* x;        // [T, H]
@@ -155,271 +159,357 @@ struct Operands {
 };
 
 // ---------------------------------------------------------------------------
-// bf16: tiles of 256 x 256 on v_mfma_f32_32x32x16_bf16
+// bf16: tiles on v_mfma_f32_32x32x16_bf16
 // ---------------------------------------------------------------------------
 // Two forms of an operand in LDS, per k-tile of 32:
-//  - "row": memory rows run along k (the gathered rows of DU and DX).  256 rows
-//    of 64 B, 16-B chunk c of row r at position c ^ ((r >> 2) & 3); a fragment is
-//    one 16-B read.
+//  - "row": memory rows run along k (the gathered rows of DU and DX).  64 B a row,
+//    16-B chunk c of row r at position c ^ ((r >> 2) & 3); a fragment is one 16-B
+//    read.
 //  - "col": memory rows are the k index (weights of DU and DX, both operands of
-//    the weight gradients).  32 rows of 512 B, 32-B piece p of row k at position
-//    p ^ (2 (k & 3)); a fragment is two transposing 8-B reads
+//    the weight gradients).  32 rows as wide as the tile, 32-B piece p of row k at
+//    position p ^ (2 (k & 3)); a fragment is two transposing 8-B reads
 //    (ds_read_b64_tr_b16: each group of 16 lanes reads four k of 16 columns, lane
 //    i gets column i).  The four k of a group lie in four pieces and the next
 //    group's four in the other four of the same 256 B: no bank twice.
 // Both come in by direct global -> LDS copies into a ring of stages.  The B
 // columns are the instruction's first operand, so a lane's results are runs of
 // four consecutive columns of one row.
-constexpr int BT = 256, GK = 32;
-constexpr int kOpBytes = BT * GK * 2;         // one operand's k-tile
-constexpr int kStageBytes = 2 * kOpBytes;
-constexpr int kStages = 4;
-constexpr int kTab = 2048;                    // rows whose tokens are in LDS at a time
-constexpr int kStageRows = 128, kF32Pitch = BT + 4, kBfPitch = BT + 8;
-constexpr int kStagingBytes = kStageRows * kF32Pitch * 4;
-constexpr int kRingBytes = kStages * kStageBytes > kStagingBytes ? kStages * kStageBytes
-                                                                 : kStagingBytes;
-constexpr int kLdsBytes = kRingBytes + kTab * 4;
-static_assert(BT * kBfPitch * 2 <= kLdsBytes && kLdsBytes <= 160 * 1024, "LDS");
+constexpr int GK = 32;
 
 __device__ __forceinline__ int rswz(int r, int c) { return c ^ ((r >> 2) & 3); }
 __device__ __forceinline__ int cswz(int k, int p) { return p ^ ((k & 3) << 1); }
 
-template <int KIND, typename WT>
-__global__ __launch_bounds__(512, 1) void grad_gemm_kernel(Operands o, int MT, int NT) {
-  constexpr bool DW = KIND == kDWGU || KIND == kDWDN;
-  constexpr int WN = 4, NW = 8, LPW = kStageBytes / 1024 / NW;  // copies a wave and k-tile
-  constexpr int TM = 4, TN = 2, NF = TM + TN, NMF = TM * TN;
-  constexpr int WR = 32 * TM, WC = 32 * TN;
+// BM x BN tile, WM x WN waves, ST stages, blocks that share a CU.
+template <int BM_, int BN_, int WM_, int WN_, int ST_, int BLOCKS_>
+struct Tile {
+  static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, NW = WM * WN;
+  static constexpr int BLOCKS = BLOCKS_, WAVES_EU = BLOCKS_ * NW / 4;  // waves a SIMD
+  static constexpr int A_BYTES = BM * GK * 2, B_BYTES = BN * GK * 2, STAGE = A_BYTES + B_BYTES;
+  static constexpr int RING = ST * STAGE;
+  static constexpr int WR = BM / WM, WC = BN / WN, TM = WR / 32, TN = WC / 32;
+  // LDS of a block that stages its results over the ring: WR rows of fp32 or BM of bf16
+  static constexpr int F32_PITCH = BN + 4, BF_PITCH = BN + 8;
+  static constexpr int STAGED = WR * F32_PITCH * 4 > BM * BF_PITCH * 2 ? WR * F32_PITCH * 4
+                                                                       : BM * BF_PITCH * 2;
+  static constexpr int ROWS_LDS = RING > STAGED ? RING : STAGED;
+  // LDS through which a wave's results leave: 32 rows of SJ 32-column sub-tiles
+  static constexpr int SJ = BLOCKS * (RING + NW * 4096) <= 160 * 1024 ? 2 : 1;
+  static constexpr int WAVE_STAGING = SJ * 2048;
+  static constexpr int NF = TM + TN, NMF = TM * TN;  // fragments, products a half k-tile
+  static constexpr int CA = A_BYTES / 1024 / NW, CB = B_BYTES / 1024 / NW;  // copies a wave
+  static constexpr int LPW = CA + CB;
+  // col form: lanes a k row, k rows a copy, copies after which the swizzle repeats
+  static constexpr int LA = BM / 8, LB = BN / 8, SA = 64 / LA, SB = 64 / LB;
+  static constexpr int PA = SA >= 4 ? 1 : (4 / SA < CA ? 4 / SA : CA);
+  static constexpr int PB = SB >= 4 ? 1 : (4 / SB < CB ? 4 / SB : CB);
+  static_assert(CA * NW * 1024 == A_BYTES && CB * NW * 1024 == B_BYTES, "whole copies");
+  static_assert(BM >= 128 && BN >= 128, "the col form's swizzle needs 8 pieces a row");
+  static_assert(ST >= 2, "waits");
+};
+
+typedef int i32x4 __attribute__((ext_vector_type(4)));
+typedef __attribute__((address_space(3))) bf16x8 lds_bf16x8;
+typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
+typedef __attribute__((address_space(4))) const int const_int;
+
+// LDS offset of a shared array.
+__device__ __forceinline__ unsigned lds_offset(unsigned char* p) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return (unsigned)(uintptr_t)(__attribute__((address_space(3))) unsigned char*)p;
+#else
+  return (unsigned)(uintptr_t)p;
+#endif
+}
+
+// A fragment of the row form at LDS offset a; of the col form, its k rows 0..3 at a
+// and 4..7 `step` bytes on.
+__device__ __forceinline__ bf16x8 frag_row(unsigned a) {
+#if defined(__HIP_DEVICE_COMPILE__)
+  return *(lds_bf16x8*)a;
+#else
+  return bf16x8{};
+#endif
+}
+__device__ __forceinline__ bf16x8 frag_col(unsigned a, int step) {
+  union {
+    s16x4 h[2];
+    bf16x8 v;
+  } u = {};
+#if defined(__HIP_DEVICE_COMPILE__)
+  u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)a);
+  u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(a + step));
+#endif
+  return u.v;
+}
+
+// Descriptor of `bytes` bytes at p: loads past them give zeros, stores past them
+// are dropped.  Uniform over the wave.
+__device__ __forceinline__ i32x4 buffer_of(const void* p, unsigned bytes) {
+  const uint64_t a = (uint64_t)(uintptr_t)p;
+  i32x4 d;
+  d[0] = __builtin_amdgcn_readfirstlane((int)(uint32_t)a);
+  d[1] = __builtin_amdgcn_readfirstlane((int)((uint32_t)(a >> 32) & 0xffffu));
+  d[2] = __builtin_amdgcn_readfirstlane((int)bytes);
+  d[3] = 0x00020000;
+  return d;
+}
+
+// Copies and stores through descriptors, in inline asm for the reason given at
+// lds_copy16 and so that the waits below count them exactly.  The compiler does not
+// see these instructions, so their wait states are here: five after a vector
+// instruction that wrote a scalar register they read (readfirstlane), two before a
+// vector instruction that overwrites a store's data.
+__device__ __forceinline__ void buffer_copy16(i32x4 buf, unsigned off, unsigned lds) {
+  const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tbuffer_load_dwordx4 %0, %1, 0 offen lds"
+               :
+               : "v"(off), "s"(buf), "s"(m0)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void global_copy16(const void* base, unsigned off, unsigned lds) {
+  const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1"
+               :
+               : "v"(off), "s"(base), "s"(m0)
+               : "memory", "m0");
+}
+__device__ __forceinline__ void buffer_store16(i32x4 buf, unsigned off, i32x4 v) {
+  asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1" : : "v"(v), "v"(off), "s"(buf)
+               : "memory");
+}
+
+// Fragment offsets of a wave within a stage.
+template <typename TL, bool ROW_A>
+struct FragOffsets {
+  unsigned a[ROW_A ? 1 : TL::TM], b[TL::TN];
+  __device__ __forceinline__ FragOffsets(int lane, int wm, int wn) {
+    // row form: lane -> row lane % 32, chunk lane / 32 (+ 2 for the second half)
+    const int fr = lane % 32, fq = lane / 32;
+    // col form: k = 8 fq + (lane % 16) / 4, columns c .. c + 3 of the lane's address
+    const int tk = 8 * fq + (lane % 16) / 4, tc = 16 * ((lane / 16) % 2) + 4 * (lane % 4);
+    auto col = [&](int c, int width) {
+      c += tc;
+      return (unsigned)(tk * width * 2 + cswz(tk, c / 16) * 32 + (c % 16) * 2);
+    };
+    if constexpr (ROW_A) {
+      const int r = wm * TL::WR + fr;  // 32 rows on, the swizzle is the same
+      a[0] = r * 64 + rswz(r, fq) * 16;
+    } else {
+#pragma unroll
+      for (int i = 0; i < TL::TM; ++i) a[i] = col(wm * TL::WR + i * 32, TL::BM);
+    }
+#pragma unroll
+    for (int j = 0; j < TL::TN; ++j) b[j] = TL::A_BYTES + col(wn * TL::WC + j * 32, TL::BN);
+  }
+  // fragment f (A's TM, then B's TN) of half s of the stage at offset st
+  __device__ __forceinline__ bf16x8 read(unsigned st, int s, int f) const {
+    if (f >= TL::TM)
+      return frag_col(b[f - TL::TM] + st + s * 16 * TL::BN * 2, 4 * TL::BN * 2);
+    if constexpr (ROW_A) return frag_row((a[0] ^ (s * 32)) + st + f * 32 * 64);
+    else return frag_col(a[f] + st + s * 16 * TL::BM * 2, 4 * TL::BM * 2);
+  }
+};
+
+template <typename TL>
+__device__ __forceinline__ void clear(f32x16 (&acc)[TL::TM][TL::TN]) {
+#pragma unroll
+  for (int i = 0; i < TL::TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TL::TN; ++j)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
+}
+
+// DU and DX: a block takes one row tile of one expert and one column tile.
+template <int KIND, typename WT, typename TL>
+__global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Operands o, int NT) {
+  constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, ST = TL::ST, WN = TL::WN;
+  constexpr int TM = TL::TM, TN = TL::TN, NF = TL::NF, NMF = TL::NMF, WR = TL::WR, WC = TL::WC;
+  constexpr int CA = TL::CA, LPW = TL::LPW;
   extern __shared__ __align__(16) unsigned char smem[];
-  int* tab = reinterpret_cast<int*>(smem + kRingBytes);
+  const unsigned base = lds_offset(smem);
 
   const int H = o.H, I = o.I;
-  const int Nout = KIND == kDU || KIND == kDWDN ? I : H;
-  int e = 0, row0, row1, mt = 0, nt;
-  if constexpr (DW) {
-    const int item = xcd_item(blockIdx.x, o.E * MT * NT);
-    if (item < 0) return;  // uniform over the block
-    e = item / (MT * NT);
-    mt = item / NT % MT;
-    nt = item % NT;
-    const bool all = o.ident || o.rows == 0;  // no rows: the offsets may not exist
-    row0 = all ? 0 : o.offsets[e];
-    row1 = all ? o.rows : o.offsets[e + 1];
-  } else {
+  const int Nout = KIND == kDU ? I : H;
+  int e = 0, row0, row1, nt;
+  {
     RowTileScan sc;
     int R;
     if (o.ident) {
-      R = (o.rows + BT - 1) / BT;
+      R = (o.rows + BM - 1) / BM;
     } else {
-      row_tile_scan(o.offsets, o.E, BT, sc);
+      row_tile_scan(o.offsets, o.E, BM, sc);
       R = sc.total;
     }
     const int item = xcd_item(blockIdx.x, R * NT);
-    if (item < 0) return;
+    if (item < 0) return;  // uniform over the block
     if (o.ident) {
       nt = item % NT;
-      row0 = item / NT * BT;
-      row1 = min(row0 + BT, o.rows);
+      row0 = item / NT * BM;
+      row1 = min(row0 + BM, o.rows);
     } else {
-      weight_major_item(sc, o.offsets, BT, item, NT, e, row0, row1, nt);
+      weight_major_item(sc, o.offsets, BM, item, NT, e, row0, row1, nt);
     }
   }
+  e = __builtin_amdgcn_readfirstlane(e);
+  nt = __builtin_amdgcn_readfirstlane(nt);
+  row0 = __builtin_amdgcn_readfirstlane(row0);
+  row1 = __builtin_amdgcn_readfirstlane(row1);
   const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
-  const int wm = wave / WN, wn = wave % WN;
-  const int m0 = mt * BT, n0 = nt * BT;
-  const bf16* zeros = reinterpret_cast<const bf16*>(zero_row);
+  const int wm = wave / WN, wn = wave % WN, fr = lane % 32, fq = lane / 32;
+  const int n0 = nt * BN;
 
-  // Sources of this lane's copies.  Copies 0 .. 15 of a stage are A, 16 .. 31 B.
-  const bf16* src[LPW];   // row form: + 32 per k-tile; col form: the first k row
-  int kr[LPW];            // col form: this lane's k row of the tile
-  const int M = KIND == kDWGU ? 2 * I : H;  // DW: rows of the output
-  const bool waveA = wave < NW / 2;
+  // This lane's copies of a k-tile, CA of A and CB of B: byte offsets from bases
+  // that all lanes share.  A row past the tile reads a valid one, a token that does
+  // not count reads token 0: outputs dropped and replaced in the epilogue.
+  unsigned off[LPW];
+  const bf16 *pA, *pB, *pU = nullptr;
+  if constexpr (KIND == kDU) {
+    pA = static_cast<const bf16*>(o.d_out);
+    pB = static_cast<const bf16*>(o.w_down) + (size_t)e * o.dn_stride;
+  } else {
+    pA = static_cast<const bf16*>(o.d_gu) + (size_t)row0 * 2 * I;
+    pB = static_cast<const bf16*>(o.w_gate) + (size_t)e * o.gu_stride;
+    pU = static_cast<const bf16*>(o.w_up) + (size_t)e * o.gu_stride;
+  }
 #pragma unroll
   for (int j = 0; j < LPW; ++j) {
-    const int q = (wave * LPW + j) % (NW * LPW / 2);
-    if (!DW && waveA) {
-      const int r = 16 * q + lane / 4;
-      int gr = row0 + r;
-      if (gr >= row1) gr = row0;  // past the tile: a valid row, output dropped
-      const bf16* p;
-      if constexpr (KIND == kDU) {
-        const int tok = o.row_tok[gr];
-        p = tok < 0 ? zeros : static_cast<const bf16*>(o.d_out) + (size_t)tok * H;
-      } else {
-        p = static_cast<const bf16*>(o.d_gu) + (size_t)gr * 2 * I;
-      }
-      src[j] = p + rswz(r, lane % 4) * 8;
-      kr[j] = 0;
+    if (j < CA) {
+      const int r = 16 * (wave * CA + j) + lane / 4;
+      const int gr = row0 + r < row1 ? r : 0;
+      const unsigned at = KIND == kDU ? (unsigned)max(o.row_tok[row0 + gr], 0) * (unsigned)(2 * H)
+                                      : (unsigned)gr * (unsigned)(4 * I);
+      off[j] = at + rswz(r, lane % 4) * 16;
     } else {
-      kr[j] = 2 * q + lane / 32;
-      const int piece = cswz(kr[j], (lane % 32) / 2);
-      int c = (DW && waveA ? m0 : n0) + piece * 16 + (lane & 1) * 8;
-      if (c >= (DW && waveA ? M : Nout)) c = 0;  // a valid column, output dropped
-      if constexpr (KIND == kDU) {
-        src[j] = static_cast<const bf16*>(o.w_down) + (size_t)e * o.dn_stride +
-                 (size_t)kr[j] * I + c;
-      } else if constexpr (KIND == kDX) {
-        src[j] = static_cast<const bf16*>(o.w_gate) + (size_t)e * o.gu_stride +
-                 (size_t)kr[j] * H + c;
-      } else if constexpr (KIND == kDWGU) {
-        src[j] = (waveA ? static_cast<const bf16*>(o.d_gu) : static_cast<const bf16*>(o.x)) + c;
-      } else {
-        src[j] = (waveA ? static_cast<const bf16*>(o.d_out) : static_cast<const bf16*>(o.hw)) + c;
-      }
+      const int k = TL::SB * (wave * TL::CB + j - CA) + lane / TL::LB;
+      const int c = n0 + cswz(k, lane % TL::LB / 2) * 16 + (lane & 1) * 8;
+      off[j] = ((unsigned)k * (unsigned)Nout + (unsigned)(c < Nout ? c : 0)) * 2u;
     }
   }
-  // the up rows' distance from where the gate rows would go on
-  const long long up_shift =
-      KIND == kDX ? static_cast<const bf16*>(o.w_up) -
-                        (static_cast<const bf16*>(o.w_gate) + (size_t)I * H)
-                  : 0;
-
-  // Fragment byte offsets within a stage, per k16 half s.
-  const int fr = lane % 32, fq = lane / 32;
-  auto row_off = [&](int r, int s) { return r * 64 + rswz(r, 2 * s + fq) * 16; };
-  // col form: k = 16 s + 8 fq + (lane % 16) / 4 (+ 4 for the second read),
-  // columns c .. c + 3 of the lane's address
-  const int tk = 8 * fq + (lane % 16) / 4, tc = 16 * ((lane / 16) % 2) + 4 * (lane % 4);
-  auto col_off = [&](int c, int k) {
-    c += tc;
-    return k * (BT * 2) + cswz(k, c / 16) * 32 + (c % 16) * 2;
+  const int nk = (KIND == kDU ? H : 2 * I) / GK;
+  // pA, pB: the k-tile that is being copied; `turn` k-tiles before pB goes on to the
+  // up rows
+  int turn = KIND == kDX ? I / GK : -1;
+  const unsigned ldsA = base + wave * CA * 1024, ldsB = base + TL::A_BYTES + wave * TL::CB * 1024;
+  auto copy = [&](int j, unsigned st) {
+    if (j < CA) global_copy16(pA, off[j], ldsA + st + j * 1024);
+    else global_copy16(pB, off[j], ldsB + st + (j - CA) * 1024);
   };
-
+  auto copied = [&]() {
+    pA += GK;
+    pB += (size_t)GK * Nout;
+    if (KIND == kDX && --turn == 0) pB = pU;
+  };
+  // 32-row sub-tiles of this wave that hold rows
+  int nv;
+  {
+    const int left = row1 - row0 - wm * WR;
+    nv = left <= 0 ? 0 : min(TM, (left + 31) / 32);
+  }
+  const FragOffsets<TL, true> fo(lane, wm, wn);
   f32x16 acc[TM][TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-#pragma unroll
-    for (int j = 0; j < TN; ++j)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
-  bf16x8 f0[NF], f1[NF];
-  int offA[TM], offB[TN];
-#pragma unroll
-  for (int i = 0; i < TM; ++i)
-    offA[i] = DW ? col_off(wm * WR + i * 32, tk) : row_off(wm * WR + i * 32 + fr, 0);
-#pragma unroll
-  for (int j = 0; j < TN; ++j) offB[j] = kOpBytes + col_off(wn * WC + j * 32, tk);
-  typedef __attribute__((address_space(3))) s16x4 lds_s16x4;
-  auto rd_col = [&](const unsigned char* p) {
-    union {
-      s16x4 h[2];
-      bf16x8 v;
-    } u;
-#if defined(__HIP_DEVICE_COMPILE__)
-    u.h[0] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p));
-    u.h[1] = __builtin_amdgcn_ds_read_tr16_b64_v4i16((lds_s16x4*)(p + 4 * BT * 2));
-#else
-    u.v = bf16x8{};
-#endif
-    return u.v;
-  };
-  // k rows 16 s + tk: the swizzle depends on k & 3 = tk & 3 alone, so half s is
-  // 16 rows further on; the row form's half 1 flips chunk bit 1
-  auto rd = [&](const unsigned char* st, int s, int f, bf16x8 (&d)[NF]) {
-    if (f < TM) {
-      if constexpr (DW)
-        d[f] = rd_col(st + offA[f] + s * 16 * BT * 2);
-      else
-        d[f] = *reinterpret_cast<const bf16x8*>(st + (offA[f] ^ (s * 32)));
-    } else {
-      d[f] = rd_col(st + offB[f - TM] + s * 16 * BT * 2);
-    }
-  };
-  auto mf = [&](int m, bf16x8 (&c)[NF]) {
-    const int i = m / TN, j = m % TN;
-    acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[TM + j], c[i], acc[i][j], 0, 0, 0);
-  };
+  clear<TL>(acc);
 
-  // One segment of the contraction: nk k-tiles; DW: rows seg0 .. of the sorted
-  // order, whose tokens are in tab.
-  const int ld = waveA ? (KIND == kDWGU ? 2 * I : H) : (KIND == kDWGU ? H : I);
-  auto run = [&](int nk, int seg0, int segn) {
-    auto copy = [&](int kt, int j, int tok) {
-      const int ktc = min(kt, nk - 1);  // past the last: copied again, never used
-      const bf16* p;
-      if constexpr (DW) {
-        p = tok < 0 ? zeros : src[j] + (size_t)tok * ld;
-      } else {
-        if (waveA) {
-          p = src[j] + ktc * GK;
-        } else if constexpr (KIND == kDU) {
-          p = src[j] + (size_t)ktc * GK * I;
-        } else {
-          p = src[j] + (size_t)ktc * GK * H + (ktc * GK >= I ? up_shift : 0);
-        }
+  auto run = [&](auto nv_tag) {
+    constexpr int NV = decltype(nv_tag)::value;  // sub-tiles of rows to multiply
+    bf16x8 f0[NF], f1[NF];
+    auto rd = [&](unsigned st, int s, int f, bf16x8 (&d)[NF]) {
+      if (NV > 0 && (f >= TM || f < NV)) d[f] = fo.read(base + st, s, f);
+    };
+    auto mf = [&](int m, bf16x8 (&c)[NF]) {
+      const int i = m / TN, j = m % TN;
+      if (i < NV)
+        acc[i][j] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(c[TM + j], c[i], acc[i][j], 0, 0, 0);
+    };
+    // waits until all but the last `tiles` tiles' copies have landed
+    auto wait_tiles = [&](int tiles) {
+      if (tiles >= ST - 1) wait_vmem<(ST - 1) * LPW>();
+      else if (tiles == ST - 2) wait_vmem<(ST - 2) * LPW>();
+      else if (ST > 3 && tiles == 1) wait_vmem<LPW>();
+      else wait_vmem<0>();
+    };
+    // The copies of tile kt + ST go to tile kt's slot: the first P1 of them in the
+    // second half of tile kt, when no wave reads it any more, the others in the first
+    // half of tile kt + 1, so that the copy path is never idle for half of the time.
+    constexpr int P1 = LPW / 2, P2 = LPW - P1;
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+      if (s < nk) {
+#pragma unroll
+        for (int j = 0; j < LPW; ++j)
+          if (s < ST - 1 || j < P1) copy(j, s * TL::STAGE);
+        if (s < ST - 1) copied();
       }
-      lds_copy16(p, smem + (kt % kStages) * kStageBytes + (wave * LPW + j) * 1024);
-    };
-    // DW: the row of the source that k row kr of tile kt is, -1 for zeros
-    constexpr bool gatherA = KIND == kDWDN;
-    auto source_row = [&](int kt, int j) {
-      if constexpr (!DW) return 0;
-      const int r = min(kt, nk - 1) * GK + kr[j];
-      const int tok = tab[r];
-      return waveA == gatherA ? tok : (r < segn ? seg0 + r : -1);
-    };
-    int nx[LPW];
-#pragma unroll
-    for (int s = 0; s < kStages; ++s)
-#pragma unroll
-      for (int j = 0; j < LPW; ++j) copy(s, j, source_row(s, j));
-    wait_vmem<(kStages - 1) * LPW>();
+    if (nk >= ST) wait_vmem<(ST - 2) * LPW>();
+    else wait_tiles(nk - 1);
     block_barrier();
 #pragma unroll
-    for (int f = 0; f < NF; ++f) rd(smem, 0, f, f0);
+    for (int f = 0; f < NF; ++f) rd(0, 0, f, f0);
     wait_lds();
     __builtin_amdgcn_sched_barrier(0);
-    for (int kt = 0; kt < nk; ++kt) {
-      const unsigned char* st = smem + (kt % kStages) * kStageBytes;
-      const unsigned char* sn = smem + ((kt + 1) % kStages) * kStageBytes;
+    unsigned cur = 0, prv = TL::RING - TL::STAGE;
+    auto tile = [&](int kt, auto first_tag, auto second_tag) {
+      constexpr bool FIRST = decltype(first_tag)::value;    // tile kt - 1 + ST exists
+      constexpr bool SECOND = decltype(second_tag)::value;  // tile kt + ST exists
+      const unsigned nxt = cur + TL::STAGE == TL::RING ? 0 : cur + TL::STAGE;
       // first half: products on f0, reads of the second half's fragments
 #pragma unroll
       for (int m = 0; m < NMF; ++m) {
-        if (m < NF) rd(st, 1, m, f1);
+#pragma unroll
+        for (int f = m * NF / NMF; f < (m + 1) * NF / NMF; ++f) rd(cur, 1, f, f1);
         mf(m, f0);
-        if (m < LPW) nx[m] = source_row(kt + kStages, m);
+        if constexpr (FIRST) {
+#pragma unroll
+          for (int j = m * P2 / NMF; j < (m + 1) * P2 / NMF; ++j) copy(P1 + j, prv);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
+      if constexpr (FIRST) copied();
       wait_lds();
-      // tile kt + 1 has landed for every wave; no wave reads tile kt after this,
-      // so its slot takes tile kt + kStages
-      wait_vmem<(kStages - 2) * LPW>();
+      // tile kt + 1 has landed for every wave; no wave reads tile kt after this
+      if constexpr (FIRST) wait_vmem<(ST - 2) * LPW>();
+      else wait_tiles(nk - 2 - kt);
       block_barrier();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < NMF; ++m) {
-        if (m < NF) rd(sn, 0, m, f0);
+#pragma unroll
+        for (int f = m * NF / NMF; f < (m + 1) * NF / NMF; ++f) rd(nxt, 0, f, f0);
         mf(m, f1);
-        if (m >= NMF - LPW) copy(kt + kStages, m - (NMF - LPW), nx[m - (NMF - LPW)]);
+        if constexpr (SECOND) {
+#pragma unroll
+          for (int j = m * P1 / NMF; j < (m + 1) * P1 / NMF; ++j) copy(j, cur);
+        }
         __builtin_amdgcn_sched_barrier(0);
       }
       wait_lds();
-    }
-    wait_vmem<0>();
+      prv = cur;
+      cur = nxt;
+    };
+    int kt = 0;
+    for (; kt + ST < nk; ++kt) tile(kt, std::true_type{}, std::true_type{});
+    if (kt + ST == nk) tile(kt++, std::true_type{}, std::false_type{});
+    for (; kt < nk; ++kt) tile(kt, std::false_type{}, std::false_type{});
     __syncthreads();
   };
-  if constexpr (DW) {
-    for (int seg0 = row0; seg0 < row1; seg0 += kTab) {
-      const int segn = min(kTab, row1 - seg0);
-      for (int r = threadIdx.x; r < (segn + GK - 1) / GK * GK; r += 512)
-        tab[r] = r < segn ? o.row_tok[seg0 + r] : -1;
-      __syncthreads();
-      run((segn + GK - 1) / GK, seg0, segn);
-    }
-  } else {
-    run((KIND == kDU ? H : 2 * I) / GK, 0, 0);
-  }
+  static_assert(TM == 2, "the cases below");
+  if (nv == 2) run(std::integral_constant<int, 2>{});
+  else if (nv == 1) run(std::integral_constant<int, 1>{});
+  else run(std::integral_constant<int, 0>{});
 
   // Epilogue through LDS (the ring's, free now), so that whole rows are read and
   // written in 16-B pieces.
   const int tid = threadIdx.x;
-  if constexpr (KIND == kDU) {
+  constexpr int F32_PITCH = TL::F32_PITCH, BF_PITCH = TL::BF_PITCH;
+  constexpr bool F32 = KIND == kDU || std::is_same<WT, float>::value;
+  if constexpr (F32) {
     float* stg = reinterpret_cast<float*>(smem);
     const bf16* kept = static_cast<const bf16*>(o.kept);
     bf16* d_gu = static_cast<bf16*>(o.d_gu);
     bf16* hw = static_cast<bf16*>(o.hw);
-    for (int pass = 0; pass < BT / kStageRows; ++pass) {
+    constexpr int LPR = BN / 8, RPI = 64 * NW / LPR;  // lanes a row, rows an iteration
+    static_assert(LPR <= kWave && WR % RPI == 0, "rows of the epilogue");
+    for (int pass = 0; pass < TL::WM; ++pass) {
       if (wm == pass) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
@@ -429,93 +519,410 @@ __global__ __launch_bounds__(512, 1) void grad_gemm_kernel(Operands o, int MT, i
             for (int q = 0; q < 4; ++q) {
               const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                                acc[i][j][4 * q + 3]};
-              *reinterpret_cast<f32x4*>(stg + (i * 32 + fr) * kF32Pitch + wn * WC + j * 32 +
+              *reinterpret_cast<f32x4*>(stg + (i * 32 + fr) * F32_PITCH + wn * WC + j * 32 +
                                         8 * q + 4 * fq) = v;
             }
       }
       __syncthreads();
-      // 32 lanes a row, 8 columns each
 #pragma unroll 2
-      for (int it = 0; it < kStageRows / 16; ++it) {
-        const int rl = it * 16 + tid / 32, c = (tid % 32) * 8;
-        const int row = row0 + pass * kStageRows + rl, col = n0 + c;
-        float dot = 0.0f;
-        if (row < row1 && col < I) {
-          const bool live = o.row_tok[row] >= 0;
-          const float w = o.ident ? 1.0f : o.topk_w[o.sorted_slots[row]];
-          const bf16x8 g = *reinterpret_cast<const bf16x8*>(kept + (size_t)row * 2 * I + col);
-          const bf16x8 u = *reinterpret_cast<const bf16x8*>(kept + (size_t)row * 2 * I + I + col);
-          bf16x8 og, ou, oh;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) {
-            float h, dg, du;
-            const float v = stg[rl * kF32Pitch + c + j];
-            act_grad<true>((float)g[j], (float)u[j], v, h, dg, du);
-            dot += v * h;
-            og[j] = (bf16)(live ? w * dg : 0.0f);
-            ou[j] = (bf16)(live ? w * du : 0.0f);
-            oh[j] = (bf16)(live ? w * h : 0.0f);
+      for (int it = 0; it < WR / RPI; ++it) {
+        const int rl = it * RPI + tid / LPR, c = (tid % LPR) * 8;
+        const int row = row0 + pass * WR + rl, col = n0 + c;
+        if constexpr (KIND == kDX) {
+          if (row < row1 && col < Nout) {
+            const float* v = stg + rl * F32_PITCH + c;
+            float* d = static_cast<float*>(o.d_xs) + (size_t)row * H + col;
+            *reinterpret_cast<f32x4*>(d) = *reinterpret_cast<const f32x4*>(v);
+            *reinterpret_cast<f32x4*>(d + 4) = *reinterpret_cast<const f32x4*>(v + 4);
           }
-          if (!live) dot = 0.0f;
-          *reinterpret_cast<bf16x8*>(d_gu + (size_t)row * 2 * I + col) = og;
-          *reinterpret_cast<bf16x8*>(d_gu + (size_t)row * 2 * I + I + col) = ou;
-          *reinterpret_cast<bf16x8*>(hw + (size_t)row * I + col) = oh;
-        }
-        if (o.part) {
+        } else {
+          float dot = 0.0f;
+          if (row < row1 && col < I) {
+            const bool live = o.row_tok[row] >= 0;
+            const float w = o.ident ? 1.0f : o.topk_w[o.sorted_slots[row]];
+            const bf16x8 g = *reinterpret_cast<const bf16x8*>(kept + (size_t)row * 2 * I + col);
+            const bf16x8 u =
+                *reinterpret_cast<const bf16x8*>(kept + (size_t)row * 2 * I + I + col);
+            bf16x8 og, ou, oh;
 #pragma unroll
-          for (int s = 16; s > 0; s >>= 1) dot += __shfl_xor(dot, s, kWave);
-          if (tid % 32 == 0 && row < row1) o.part[(size_t)nt * o.rows + row] = dot;
+            for (int j = 0; j < 8; ++j) {
+              float h, dg, du;
+              const float v = stg[rl * F32_PITCH + c + j];
+              act_grad<true>((float)g[j], (float)u[j], v, h, dg, du);
+              dot += v * h;
+              og[j] = (bf16)(live ? w * dg : 0.0f);
+              ou[j] = (bf16)(live ? w * du : 0.0f);
+              oh[j] = (bf16)(live ? w * h : 0.0f);
+            }
+            if (!live) dot = 0.0f;
+            *reinterpret_cast<bf16x8*>(d_gu + (size_t)row * 2 * I + col) = og;
+            *reinterpret_cast<bf16x8*>(d_gu + (size_t)row * 2 * I + I + col) = ou;
+            *reinterpret_cast<bf16x8*>(hw + (size_t)row * I + col) = oh;
+          }
+          if (o.part) {
+#pragma unroll
+            for (int s = LPR / 2; s > 0; s >>= 1) dot += __shfl_xor(dot, s, kWave);
+            if (tid % LPR == 0 && row < row1) o.part[(size_t)nt * o.rows + row] = dot;
+          }
         }
       }
       __syncthreads();
     }
   } else {
-    // output rows: DX the sorted rows; DW the weight's rows
-    auto out_row = [&](int r) -> WT* {
-      if constexpr (KIND == kDX) {
-        return row0 + r < row1 ? static_cast<WT*>(o.d_xs) + (size_t)(row0 + r) * H : nullptr;
-      } else if constexpr (KIND == kDWGU) {
-        const int m = m0 + r;
-        if (m >= 2 * I) return nullptr;
-        return (m < I ? static_cast<WT*>(o.d_gate) + (size_t)m * H
-                      : static_cast<WT*>(o.d_up) + (size_t)(m - I) * H) +
-               (size_t)e * o.gu_stride;
-      } else {
-        const int m = m0 + r;
-        return m < H ? static_cast<WT*>(o.d_down) + (size_t)e * o.dn_stride + (size_t)m * I
-                     : nullptr;
-      }
-    };
-    constexpr bool F32 = std::is_same<WT, float>::value;
-    constexpr int SR = F32 ? kStageRows : BT, PITCH = F32 ? kF32Pitch : kBfPitch;
-    constexpr int PER = 16 / (int)sizeof(WT), CH = BT / PER;
-    WT* stg = reinterpret_cast<WT*>(smem);
-    for (int pass = 0; pass < BT / SR; ++pass) {
-      if (!F32 || wm == pass) {
+    bf16* stg = reinterpret_cast<bf16*>(smem);
 #pragma unroll
-        for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
-          for (int j = 0; j < TN; ++j)
+      for (int j = 0; j < TN; ++j)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-              typedef WT wx4 __attribute__((ext_vector_type(4)));
-              const wx4 v = {from_f32<WT>(acc[i][j][4 * q]), from_f32<WT>(acc[i][j][4 * q + 1]),
-                             from_f32<WT>(acc[i][j][4 * q + 2]),
-                             from_f32<WT>(acc[i][j][4 * q + 3])};
-              const int r = (F32 ? 0 : wm * WR) + i * 32 + fr;
-              *reinterpret_cast<wx4*>(stg + r * PITCH + wn * WC + j * 32 + 8 * q + 4 * fq) = v;
-            }
-      }
-      __syncthreads();
-      for (int k = tid; k < SR * CH; k += 512) {
-        const int r = k / CH, c = (k % CH) * PER;
-        WT* dst = out_row(pass * SR + r);
-        if (dst && n0 + c < Nout)
-          *reinterpret_cast<uint4*>(dst + n0 + c) =
-              *reinterpret_cast<const uint4*>(stg + r * PITCH + c);
-      }
-      __syncthreads();
+        for (int q = 0; q < 4; ++q) {
+          const bf16x4 v = {(bf16)acc[i][j][4 * q], (bf16)acc[i][j][4 * q + 1],
+                            (bf16)acc[i][j][4 * q + 2], (bf16)acc[i][j][4 * q + 3]};
+          *reinterpret_cast<bf16x4*>(stg + (wm * WR + i * 32 + fr) * BF_PITCH + wn * WC + j * 32 +
+                                     8 * q + 4 * fq) = v;
+        }
+    __syncthreads();
+    constexpr int CH = BN / 8;
+#pragma unroll 4
+    for (int k = tid; k < BM * CH; k += 64 * NW) {
+      const int r = k / CH, c = (k % CH) * 8;
+      if (row0 + r < row1 && n0 + c < Nout)
+        *reinterpret_cast<uint4*>(static_cast<bf16*>(o.d_xs) + (size_t)(row0 + r) * H + n0 + c) =
+            *reinterpret_cast<const uint4*>(stg + r * BF_PITCH + c);
     }
+  }
+}
+
+// First tile of the weights' gradients (tpe an expert) that XCD x takes, x = 8: all
+// of them.  A tile costs its k-tiles and kTileEnds more for its ends; XCD x starts at
+// the first tile that x / 8 of the whole cost lies before.
+constexpr int kTileEnds = 3;
+__device__ __forceinline__ int first_tile(const Operands& o, int tpe, int x) {
+  if (o.ident || o.rows == 0) return (int)((long long)o.E * tpe * x / 8);
+  const int lane = lane_id(), per = (o.E + kWave - 1) / kWave;  // experts a lane, <= 4
+  int cost[4], mine = 0;
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    const int e = lane * per + j;
+    cost[j] = j < per && e < o.E ? (o.offsets[e + 1] - o.offsets[e] + GK - 1) / GK + kTileEnds : 0;
+    mine += cost[j];
+  }
+  int upto = mine;
+#pragma unroll
+  for (int d = 1; d < kWave; d <<= 1) {
+    const int t = __shfl_up(upto, d, kWave);
+    if (lane >= d) upto += t;
+  }
+  const int total = __shfl(upto, kWave - 1, kWave);
+  // in units of an expert's tiles: cost before the target, of E experts at most
+  const long long target = (long long)total * x * tpe / 8;
+  long long before = (long long)(upto - mine) * tpe;
+  int first = 0;  // tiles of this lane's experts that lie before the target
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    if (cost[j] > 0 && before < target) {
+      const long long n = (target - before + cost[j] - 1) / cost[j];
+      first += n < tpe ? (int)n : tpe;
+    }
+    before += (long long)cost[j] * tpe;
+  }
+#pragma unroll
+  for (int d = kWave / 2; d > 0; d >>= 1) first += __shfl_xor(first, d, kWave);
+  return __builtin_amdgcn_readfirstlane(first);
+}
+
+// DWGU and DWDN: the gradients of the weights.  The contraction runs over an
+// expert's rows, some 256 of them: 8 k-tiles for a tile that writes 64 KB.  So a
+// block goes through many tiles as ONE stream of k-tiles: the copies run ST
+// k-tiles ahead of the products, across the tiles' ends, and the results leave from
+// the registers (through 4 KB of LDS a wave) while the next tile's copies are under
+// way.  (One tile a block, its ring filled and drained each time, ran at 427
+// TFLOP/s at 4096 tokens, the matrix unit busy for 0.24 of the time.)
+// An operand is "regular" (rows of the sorted order: d_gu, w h) or "gathered" (by
+// the rows' tokens: x, d_out).  Both are copied through descriptors, whose range
+// check gives zeros for rows past the expert's and for tokens that do not count.
+template <int KIND, typename WT, typename TL>
+__global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_weights_kernel(Operands o, int MT,
+                                                                                 int NT) {
+  constexpr int ST = TL::ST, WN = TL::WN, NW = TL::NW;
+  constexpr int TM = TL::TM, TN = TL::TN, NF = TL::NF, NMF = TL::NMF, WR = TL::WR, WC = TL::WC;
+  constexpr int CA = TL::CA, CB = TL::CB, LPW = TL::LPW;
+  constexpr bool GB = KIND == kDWGU;  // B is the gathered operand, else A
+  constexpr bool F32 = std::is_same<WT, float>::value;
+  constexpr int NS = TM * TN * (F32 ? 4 : 2);  // stores of a tile's results a wave
+  constexpr int KW = GK / NW;         // k rows that a wave copies of each operand
+  static_assert(TL::SA * CA == KW && TL::SB * CB == KW && (KW & (KW - 1)) == 0, "k rows a wave");
+  extern __shared__ __align__(16) unsigned char smem[];
+  const unsigned base = lds_offset(smem);
+  const int H = o.H, I = o.I;
+  const int M = KIND == kDWGU ? 2 * I : H, N = KIND == kDWGU ? H : I;
+  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int wm = wave / WN, wn = wave % WN, fr = lane % 32, fq = lane / 32;
+
+  // This block's tiles: every nb-th of its XCD's range (neighbours share operands).
+  // The ranges split the tiles by their k-tiles, not by their number: experts differ
+  // by more than ten in their rows, sixteen of them together by a fifth.
+  const int nb = gridDim.x / 8;
+  const int end = first_tile(o, MT * NT, blockIdx.x % 8 + 1);
+  int c_it = first_tile(o, MT * NT, blockIdx.x % 8) + blockIdx.x / 8;
+
+  const_int* offsets = (const_int*)o.offsets;
+  const_int* row_off_tab = (const_int*)o.row_off;
+  auto rows_of = [&](int it, int& row0, int& n) {
+    if (o.ident || o.rows == 0) {  // no rows: the offsets may not exist
+      row0 = 0;
+      n = o.rows;
+    } else {
+      const int e = it / (MT * NT);
+      row0 = offsets[e];
+      n = offsets[e + 1] - row0;
+    }
+  };
+
+  // Copies: the k rows of a wave are KW wave .. KW wave + KW - 1 of a k-tile, in CA
+  // (CB) copies of SA (SB) rows.  Lane offsets within a k-tile, from the tile's first
+  // column: whole ones for the regular operand, the column's part for the gathered.
+  constexpr int CR = GB ? CA : CB, CG = GB ? CB : CA;      // copies
+  constexpr int SR = GB ? TL::SA : TL::SB, SG = GB ? TL::SB : TL::SA;
+  constexpr int LR = GB ? TL::LA : TL::LB, LG = GB ? TL::LB : TL::LA;
+  constexpr int PG = GB ? TL::PB : TL::PA;
+  const char* Rp = static_cast<const char*>(GB ? o.d_gu : o.hw);
+  const char* Gp = static_cast<const char*>(GB ? o.x : o.d_out);
+  const unsigned ldr = 2u * (unsigned)(GB ? 2 * I : I), ldg = 2u * (unsigned)H;  // bytes
+  auto piece = [&](int k, int lpr) {
+    return (unsigned)(cswz(k, lane % lpr / 2) * 32 + (lane & 1) * 16);
+  };
+  unsigned offR[CR], colG[PG];
+#pragma unroll
+  for (int j = 0; j < CR; ++j) {
+    const int k = KW * wave + SR * j + lane / LR;
+    offR[j] = (unsigned)k * ldr + piece(k, LR);
+  }
+#pragma unroll
+  for (int j = 0; j < PG; ++j) colG[j] = piece(KW * wave + SG * j + lane / LG, LG);
+  const unsigned ldsR = base + (GB ? 0 : TL::A_BYTES) + wave * CR * 1024;
+  const unsigned ldsG = base + (GB ? TL::A_BYTES : 0) + wave * CG * 1024;
+
+  // The producer: the tile whose k-tiles are being copied.
+  int p_it = c_it, p_row0 = 0, p_n = 0, p_k = 0;
+  unsigned p_colR = 0;         // bytes of the tile's first column
+  const char* p_R = Rp;        // the regular operand's k-tile
+  i32x4 bufR = buffer_of(Rp, 0), bufG = buffer_of(Gp, 0);
+  auto uni = [](int v) { return __builtin_amdgcn_readfirstlane(v); };
+  int q_it = c_it, q_row0 = 0, q_n = 0;  // the tile after it, fetched ahead
+  if (q_it < end) rows_of(q_it, q_row0, q_n);
+  auto p_open = [&]() {  // to the next tile with rows
+    do {
+      p_it = q_it;
+      p_row0 = uni(q_row0);
+      p_n = uni(q_n);
+      q_it += nb;
+      if (q_it < end) rows_of(q_it, q_row0, q_n);
+    } while (p_it < end && p_n == 0);
+    if (p_it < end) {
+      const int mt = p_it / NT % MT, nt = p_it % NT;
+      p_colR = (unsigned)uni(2 * (GB ? mt * TL::BM : nt * TL::BN));
+      const unsigned cg = (unsigned)uni(2 * (GB ? nt * TL::BN : mt * TL::BM));
+      p_R = Rp + (size_t)p_row0 * ldr + p_colR;
+      bufG = buffer_of(Gp + cg, (unsigned)o.T * ldg - cg);
+      p_k = 0;
+    }
+  };
+  unsigned row_off[KW];  // gathered: byte offsets of this wave's k rows
+  auto p_rows = [&]() {
+    const int left = p_n - p_k;
+    bufR = buffer_of(p_R, (unsigned)min(GK, left) * ldr - p_colR);
+    const const_int* t = row_off_tab + p_row0 + p_k + KW * wave;  // 32 entries past the last exist
+#pragma unroll
+    for (int i = 0; i < KW; ++i) row_off[i] = (unsigned)t[i];
+    if (left < GK) {  // the rows past the expert's: another's, or none
+#pragma unroll
+      for (int i = 0; i < KW; ++i)
+        if (KW * wave + i >= left) row_off[i] = kNowhere;
+    }
+  };
+  auto p_copy = [&](int j, unsigned st) {  // copy j of a k-tile: the regular ones first
+    if (j < CR) {
+      buffer_copy16(bufR, offR[j], ldsR + st + j * 1024);
+    } else {
+      const int g = j - CR;
+      unsigned at;
+      if constexpr (SG == 2) {
+        at = lane < 32 ? row_off[(2 * g) & (KW - 1)] : row_off[(2 * g + 1) & (KW - 1)];
+      } else {
+        const unsigned lo = lane & 16 ? row_off[(4 * g + 1) & (KW - 1)] : row_off[(4 * g) & (KW - 1)];
+        const unsigned hi =
+            lane & 16 ? row_off[(4 * g + 3) & (KW - 1)] : row_off[(4 * g + 2) & (KW - 1)];
+        at = lane & 32 ? hi : lo;
+      }
+      buffer_copy16(bufG, at + colG[(g < 0 ? 0 : g) % PG], ldsG + st + g * 1024);
+    }
+  };
+  auto p_next = [&]() {
+    p_k += GK;
+    p_R += (size_t)GK * ldr;
+    if (p_k >= p_n) p_open();
+  };
+  static_assert(SG == 2 || SG == 4, "rows of a gathered copy");
+
+  const FragOffsets<TL, false> fo(lane, wm, wn);
+  f32x16 acc[TM][TN];
+  bf16x8 f0[NF], f1[NF];
+  unsigned cur = 0, prv = TL::RING - TL::STAGE;
+  // As in DU and DX, the copies of a k-tile are issued in two parts: the regular
+  // operand's in the second half of the k-tile ST before it, while its tokens are on
+  // their way, the gathered one's in the first half of the next; `open`: the
+  // producer's k-tile has its first part under way.
+  constexpr int P1 = CR, P2 = CG;
+  bool open = false;
+  p_open();
+  {  // the stream's first ST k-tiles
+#pragma unroll
+    for (int s = 0; s < ST; ++s)
+      if (p_it < end) {
+        p_rows();
+#pragma unroll
+        for (int j = 0; j < LPW; ++j)
+          if (s < ST - 1 || j < P1) p_copy(j, s * TL::STAGE);
+        if (s < ST - 1) p_next();
+        else open = true;
+      }
+    wait_vmem<0>();
+    block_barrier();
+#pragma unroll
+    for (int f = 0; f < NF; ++f) f0[f] = fo.read(base, 0, f);
+    wait_lds();
+  }
+  // k-tiles since the last stores: for ST - 2 of them the copies waited for are
+  // older than those stores, which may then be outstanding too
+  int since = ST;
+  for (; c_it < end; c_it += nb) {
+    int row0, n;
+    rows_of(c_it, row0, n);
+    clear<TL>(acc);
+    auto tile = [&](auto steady_tag) {
+      // the producer's k-tile has its first part under way and the tile has another
+      constexpr bool STEADY = decltype(steady_tag)::value;
+      const unsigned nxt = cur + TL::STAGE == TL::RING ? 0 : cur + TL::STAGE;
+      const bool was_open = STEADY || open;
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < NMF; ++m) {
+#pragma unroll
+        for (int f = m * NF / NMF; f < (m + 1) * NF / NMF; ++f) f1[f] = fo.read(base + cur, 1, f);
+        acc[m / TN][m % TN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            f0[TM + m % TN], f0[m / TN], acc[m / TN][m % TN], 0, 0, 0);
+        if (was_open) {
+#pragma unroll
+          for (int j = m * P2 / NMF; j < (m + 1) * P2 / NMF; ++j) p_copy(P1 + j, prv);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      if constexpr (STEADY) {
+        p_k += GK;
+        p_R += (size_t)GK * ldr;
+      } else if (was_open) {
+        p_next();
+        open = p_it < end;
+      }
+      wait_lds();
+      // the next k-tile has landed for every wave; no wave reads this one after the
+      // barrier, so its slot takes the one ST further on
+      if (!was_open) wait_vmem<0>();
+      else if (since < ST - 2) wait_vmem<(ST - 2) * LPW + NS < 63 ? (ST - 2) * LPW + NS : 63>();
+      else wait_vmem<(ST - 2) * LPW>();
+      block_barrier();
+      const bool now_open = STEADY || open;
+      if (now_open) p_rows();
+      __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+      for (int m = 0; m < NMF; ++m) {
+#pragma unroll
+        for (int f = m * NF / NMF; f < (m + 1) * NF / NMF; ++f) f0[f] = fo.read(base + nxt, 0, f);
+        acc[m / TN][m % TN] = __builtin_amdgcn_mfma_f32_32x32x16_bf16(
+            f1[TM + m % TN], f1[m / TN], acc[m / TN][m % TN], 0, 0, 0);
+        if (now_open) {
+#pragma unroll
+          for (int j = m * P1 / NMF; j < (m + 1) * P1 / NMF; ++j) p_copy(j, cur);
+        }
+        __builtin_amdgcn_sched_barrier(0);
+      }
+      wait_lds();
+      prv = cur;
+      cur = nxt;
+      ++since;
+    };
+    // k-tiles left, and the steady ones among the next
+    for (int left = (n + GK - 1) / GK; left > 0;) {
+      int steady = open ? min(left, (p_n - p_k - 1) / GK) : 0;
+      left -= steady;
+      for (; steady > 0; --steady) tile(std::true_type{});
+      if (left > 0) {
+        tile(std::false_type{});
+        --left;
+      }
+    }
+    // the results: 32 rows at a time lie in one matrix (I is a multiple of 32)
+    const int e = c_it / (MT * NT), mt = c_it / NT % MT, nt = c_it % NT;
+    const int n0 = nt * TL::BN;
+    const unsigned ldo = (unsigned)N * sizeof(WT);
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      const int r = mt * TL::BM + wm * WR + i * 32;
+      char* p;
+      int rows;  // of the matrix, from r on
+      if constexpr (KIND == kDWGU) {
+        const bool up = r >= I;
+        p = static_cast<char*>(up ? o.d_up : o.d_gate) + (size_t)(up ? r - I : r) * ldo +
+            (size_t)e * o.gu_stride * sizeof(WT);
+        rows = (up ? 2 * I : I) - r;
+      } else {
+        p = static_cast<char*>(o.d_down) + (size_t)r * ldo +
+            (size_t)e * o.dn_stride * sizeof(WT);
+        rows = H - r;
+      }
+      const unsigned first = (unsigned)n0 * sizeof(WT);
+      const i32x4 buf = buffer_of(p + first, rows > 0 ? (unsigned)rows * ldo - first : 0u);
+#pragma unroll
+      for (int j = 0; j < TN; ++j) {
+        const int c = wn * WC + j * 32;  // from n0
+        if constexpr (F32) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const int cc = c + 8 * q + 4 * fq;
+            const unsigned at = n0 + cc < N ? fr * ldo + cc * 4u : kNowhere;
+            const i32x4 v = {__float_as_int(acc[i][j][4 * q]), __float_as_int(acc[i][j][4 * q + 1]),
+                             __float_as_int(acc[i][j][4 * q + 2]),
+                             __float_as_int(acc[i][j][4 * q + 3])};
+            buffer_store16(buf, at, v);
+          }
+        } else {
+          // 32 rows of SJ x 32 columns through the wave's own LDS, 16-B chunk q of row r
+          // at q ^ f(r), so that 4 SJ lanes store 64 SJ B of a row
+          constexpr int SJ = TL::SJ, CPR = 4 * SJ, RPS = 64 / CPR;
+          auto place = [](int r, int q) { return r * (CPR * 16) + (q ^ (r / (4 / SJ) % CPR)) * 16; };
+          unsigned char* stg = smem + TL::RING + wave * TL::WAVE_STAGING;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) {
+            const bf16x4 v = {(bf16)acc[i][j][4 * q], (bf16)acc[i][j][4 * q + 1],
+                              (bf16)acc[i][j][4 * q + 2], (bf16)acc[i][j][4 * q + 3]};
+            *reinterpret_cast<bf16x4*>(stg + place(fr, j % SJ * 4 + q) + fq * 8) = v;
+          }
+          asm volatile("" ::: "memory");  // the wave's LDS accesses run in order
+          if (j % SJ == SJ - 1) {
+#pragma unroll
+            for (int h = 0; h < 32 / RPS; ++h) {
+              const int rr = RPS * h + lane / CPR, ch = lane % CPR;
+              const i32x4 v = *reinterpret_cast<const i32x4*>(stg + place(rr, ch));
+              const int cc = c - 32 * (SJ - 1) + ch * 8;
+              buffer_store16(buf, n0 + cc < N ? rr * ldo + cc * 2u : kNowhere, v);
+            }
+            asm volatile("" ::: "memory");
+          }
+        }
+      }
+    }
+    since = 0;
   }
 }
 
@@ -649,36 +1056,65 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
   }
 }
 
+// DU and DX: 128 x 256, two blocks of 8 waves a CU; DW: 256 x 256, one block of 8
+// waves, four stages (4096 tokens, DWGU / DWDN: 471 / 261 us; 128 x 256 in two blocks
+// of 4 waves a CU 484 / 277, waves of 64 x 128 496 / 269).
+typedef Tile<128, 256, 2, 4, 3, 2> RowsTile;
+typedef Tile<256, 256, 2, 4, 4, 1> WeightsTile;
+constexpr int kCUs = 256;
+
 template <int KIND, typename WT>
 hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   constexpr bool DW = KIND == kDWGU || KIND == kDWDN;
+  typedef typename std::conditional<DW, WeightsTile, RowsTile>::type TL;
   const int N = KIND == kDU || KIND == kDWDN ? a.I : a.H;
   const int M = KIND == kDWGU ? 2 * a.I : a.H;
-  const int bt = a.bf16 ? BT : FT;
-  const int NT = (N + bt - 1) / bt, MT = (M + bt - 1) / bt;
-  const int E = a.ident ? 1 : a.E;
-  const int blocks = DW ? E * MT * NT : tile_count_bound(a.ident, a.rows, a.T, a.E, bt) * NT;
-  if (blocks == 0) return hipSuccess;
-  if (a.bf16) {
-    auto kf = grad_gemm_kernel<KIND, WT>;
+  const int bm = a.bf16 ? TL::BM : FT, bn = a.bf16 ? TL::BN : FT;
+  const int NT = (N + bn - 1) / bn, MT = (M + bm - 1) / bm;
+  const int tiles = DW ? o.E * MT * NT : tile_count_bound(a.ident, a.rows, a.T, a.E, bm) * NT;
+  if (tiles == 0) return hipSuccess;
+  if (!a.bf16) {
+    hipLaunchKernelGGL(grad_gemm_f32_kernel<KIND>, dim3(tiles), dim3(256), 0, s, o, MT, NT);
+  } else if constexpr (DW) {
+    auto kf = grad_weights_kernel<KIND, WT, TL>;
+    constexpr int lds = TL::RING + TL::NW * TL::WAVE_STAGING;
+    static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
     static const hipError_t attr = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, kLdsBytes);
+        reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
     if (attr != hipSuccess) return attr;
-    hipLaunchKernelGGL(kf, dim3(blocks), dim3(512), kLdsBytes, s, o, MT, NT);
+    const int most = kCUs * TL::BLOCKS, blocks = tiles < most ? (tiles + 7) / 8 * 8 : most;
+    hipLaunchKernelGGL(kf, dim3(blocks), dim3(64 * TL::NW), lds, s, o, MT, NT);
   } else {
-    hipLaunchKernelGGL(grad_gemm_f32_kernel<KIND>, dim3(blocks), dim3(256), 0, s, o, MT, NT);
+    auto kf = grad_rows_kernel<KIND, WT, TL>;
+    constexpr int lds = TL::ROWS_LDS;
+    static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
+    static const hipError_t attr = hipFuncSetAttribute(
+        reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+    if (attr != hipSuccess) return attr;
+    hipLaunchKernelGGL(kf, dim3(tiles), dim3(64 * TL::NW), lds, s, o, NT);
   }
   return hipGetLastError();
 }
 
+template <typename XT, typename ST>
+void launch_combine_grad(const FfnGradArgs& a, int parts, hipStream_t s) {
+  hipLaunchKernelGGL((combine_grad_kernel<XT, ST>), dim3(a.T), dim3(256), 0, s, a.T, a.H, a.K, a.E,
+                     parts, (long long)a.rows, a.offsets, a.sorted_slots, a.ws_slot_row,
+                     static_cast<const ST*>(a.ws_d_xs), a.ws_part, static_cast<XT*>(a.d_x),
+                     a.d_topk_w);
+}
+
 }  // namespace
 
-int ffn_grad_parts(int I, bool bf16) { return bf16 ? (I + BT - 1) / BT : (I + FT - 1) / FT; }
+int ffn_grad_parts(int I, bool bf16) {
+  return bf16 ? (I + RowsTile::BN - 1) / RowsTile::BN : (I + FT - 1) / FT;
+}
 
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   Operands o{};
-  o.H = a.H; o.I = a.I; o.E = a.ident ? 1 : a.E; o.K = a.K; o.rows = a.rows; o.ident = a.ident;
-  o.offsets = a.offsets; o.row_tok = a.ws_row_tok; o.sorted_slots = a.sorted_slots;
+  o.T = a.T; o.H = a.H; o.I = a.I; o.E = a.ident ? 1 : a.E; o.K = a.K; o.rows = a.rows; o.ident = a.ident;
+  o.offsets = a.offsets; o.row_tok = a.ws_row_tok;
+  o.row_off = a.ws_row_off; o.sorted_slots = a.sorted_slots;
   o.topk_w = a.topk_w; o.x = a.x; o.d_out = a.d_out; o.kept = a.kept;
   o.w_gate = a.w_gate; o.w_up = a.w_up; o.w_down = a.w_down;
   o.gu_stride = a.gu_stride; o.dn_stride = a.dn_stride;
@@ -688,23 +1124,19 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   hipError_t e;
   if (a.rows > 0) {
     hipLaunchKernelGGL(rows_kernel, dim3((a.rows + 255) / 256), dim3(256), 0, s, a.rows,
-                       (int)a.ident, a.E, a.K, a.offsets, a.sorted_slots, a.mask, a.ws_row_tok,
-                       a.ws_slot_row);
+                       (int)a.ident, a.E, a.K, a.offsets, a.sorted_slots, a.mask, 2u * (unsigned)a.H, a.ws_row_tok,
+                       a.ws_row_off, a.ws_slot_row);
     if ((e = hipGetLastError()) != hipSuccess) return e;
     if ((e = launch_gemm<kDU, bf16>(a, o, s)) != hipSuccess) return e;
-    if (a.d_x && (e = launch_gemm<kDX, bf16>(a, o, s)) != hipSuccess) return e;
+    if (a.d_x) {
+      e = a.ident || a.xs_bf16 ? launch_gemm<kDX, bf16>(a, o, s) : launch_gemm<kDX, float>(a, o, s);
+      if (e != hipSuccess) return e;
+    }
     if (!a.ident && (a.d_x || a.d_topk_w)) {
       const int parts = ffn_grad_parts(a.I, a.bf16);
-      if (a.bf16)
-        hipLaunchKernelGGL(combine_grad_kernel<bf16>, dim3(a.T), dim3(256), 0, s, a.T, a.H, a.K,
-                           a.E, parts, (long long)a.rows, a.offsets, a.sorted_slots,
-                           a.ws_slot_row, static_cast<const bf16*>(a.ws_d_xs), a.ws_part,
-                           static_cast<bf16*>(a.d_x), a.d_topk_w);
-      else
-        hipLaunchKernelGGL(combine_grad_kernel<float>, dim3(a.T), dim3(256), 0, s, a.T, a.H, a.K,
-                           a.E, parts, (long long)a.rows, a.offsets, a.sorted_slots,
-                           a.ws_slot_row, static_cast<const float*>(a.ws_d_xs), a.ws_part,
-                           static_cast<float*>(a.d_x), a.d_topk_w);
+      if (!a.bf16) launch_combine_grad<float, float>(a, parts, s);
+      else if (a.xs_bf16) launch_combine_grad<bf16, bf16>(a, parts, s);
+      else launch_combine_grad<bf16, float>(a, parts, s);
       if ((e = hipGetLastError()) != hipSuccess) return e;
     }
   }

@@ -319,7 +319,8 @@ hipError_t launch_block_epilogue(const EpilogueArgs& a, hipStream_t s);
 // rows == 0 writes zero weight gradients.
 struct FfnGradArgs {
   int T, H, I, E, K, rows;
-  bool ident, bf16, wgrad_bf16;  // wgrad_bf16: type of the weight gradients (bf16 path)
+  bool ident, bf16;
+  bool wgrad_bf16, xs_bf16;      // bf16 path: types of the weight gradients, of ws_d_xs
   const void* x;                 // [T,H]
   const void* w_gate;            // group 0's [I,H] gate rows
   const void* w_up;
@@ -338,6 +339,7 @@ struct FfnGradArgs {
   void* d_up;
   void* d_down;                  // or nullptr
   int32_t* ws_row_tok;           // [rows]
+  unsigned* ws_row_off;          // [rows + 32]
   int32_t* ws_slot_row;          // [rows]
   void* ws_d_gu;                 // [rows,2I]
   void* ws_hw;                   // [rows,I]

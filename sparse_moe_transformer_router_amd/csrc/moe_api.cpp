@@ -189,17 +189,18 @@ B128Layout b128_layout(const moe_dims* d, long long T) {
 }
 
 // Backward pass of the gated block over `rows` rows of width I.
-struct FfnGradLayout { size_t row_tok, slot_row, d_gu, hw, d_xs, part, total; };
+struct FfnGradLayout { size_t row_tok, row_off, slot_row, d_gu, hw, d_xs, part, total; };
 FfnGradLayout ffn_grad_layout(const moe_dims* d, long long rows, long long I, bool experts) {
   FfnGradLayout L{};
   const bool bf = d->act_dtype == MOE_BF16;
   const size_t act = dtype_size(d->act_dtype), S = (size_t)rows;
   size_t o = 0;
   L.row_tok = region(o, 4 * S);
+  L.row_off = region(o, 4 * (S + 32));
   L.slot_row = region(o, experts ? 4 * S : 0);
   L.d_gu = region(o, act * S * 2 * I);
   L.hw = region(o, act * S * I);
-  L.d_xs = region(o, experts ? act * S * d->hidden : 0);
+  L.d_xs = region(o, experts ? dtype_size(d->slot_dtype) * S * d->hidden : 0);
   L.part = region(o, experts ? 4 * S * moe::ffn_grad_parts((int)I, bf) : 0);
   L.total = o + 256;  // never 0, which says that the sizes are not supported
   return L;
@@ -561,7 +562,8 @@ int check_wgrad(const moe_dims* d, int32_t dt) {
 }
 
 void set_ffn_grad_ws(moe::FfnGradArgs& a, const FfnGradLayout& L, void* ws) {
-  a.ws_row_tok = at<int32_t>(ws, L.row_tok); a.ws_slot_row = at<int32_t>(ws, L.slot_row);
+  a.ws_row_tok = at<int32_t>(ws, L.row_tok); a.ws_row_off = at<unsigned>(ws, L.row_off);
+  a.ws_slot_row = at<int32_t>(ws, L.slot_row);
   a.ws_d_gu = at<void>(ws, L.d_gu); a.ws_hw = at<void>(ws, L.hw);
   a.ws_d_xs = at<void>(ws, L.d_xs); a.ws_part = at<float>(ws, L.part);
 }
@@ -1301,6 +1303,7 @@ int moe_expert_ffn_grad(const moe_dims* dims, int32_t T, const void* x, const vo
   a.T = T; a.H = dims->hidden; a.I = dims->expert_inter; a.E = dims->num_experts;
   a.K = dims->top_k; a.rows = T * dims->top_k; a.ident = false;
   a.bf16 = dims->act_dtype == MOE_BF16; a.wgrad_bf16 = d_weights_dtype == MOE_BF16;
+  a.xs_bf16 = dims->slot_dtype == MOE_BF16;
   a.x = x; a.w_gate = w_gate_up;
   a.w_up = w_gate_up ? static_cast<const char*>(w_gate_up) + act * I * H : nullptr;
   a.gu_stride = 2 * I * H; a.w_down = w_down; a.dn_stride = H * I;
