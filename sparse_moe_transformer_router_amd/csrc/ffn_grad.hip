@@ -167,7 +167,8 @@ struct Operands {
 //    read.
 //  - "col": memory rows are the k index (weights of DU and DX, both operands of
 //    the weight gradients).  32 rows as wide as the tile, 32-B piece p of row k at
-//    position p ^ (2 (k & 3)); a fragment is two transposing 8-B reads
+//    position p ^ (2 (k & 3)), p ^ (k & 3) in rows of 64 columns; a fragment is two
+//    transposing 8-B reads
 //    (ds_read_b64_tr_b16: each group of 16 lanes reads four k of 16 columns, lane
 //    i gets column i).  The four k of a group lie in four pieces and the next
 //    group's four in the other four of the same 256 B: no bank twice.
@@ -177,13 +178,15 @@ struct Operands {
 constexpr int GK = 32;
 
 __device__ __forceinline__ int rswz(int r, int c) { return c ^ ((r >> 2) & 3); }
-__device__ __forceinline__ int cswz(int k, int p) { return p ^ ((k & 3) << 1); }
+__device__ __forceinline__ int cswz(int k, int p, int width) {
+  return p ^ (width >= 128 ? (k & 3) << 1 : k & 3);
+}
 
 // BM x BN tile, WM x WN waves, ST stages, blocks that share a CU.
 template <int BM_, int BN_, int WM_, int WN_, int ST_, int BLOCKS_>
 struct Tile {
   static constexpr int BM = BM_, BN = BN_, WM = WM_, WN = WN_, ST = ST_, NW = WM * WN;
-  static constexpr int BLOCKS = BLOCKS_, WAVES_EU = BLOCKS_ * NW / 4;  // waves a SIMD
+  static constexpr int BLOCKS = BLOCKS_, WAVES_EU = (BLOCKS_ * NW + 3) / 4;  // waves a SIMD
   static constexpr int A_BYTES = BM * GK * 2, B_BYTES = BN * GK * 2, STAGE = A_BYTES + B_BYTES;
   static constexpr int RING = ST * STAGE;
   static constexpr int WR = BM / WM, WC = BN / WN, TM = WR / 32, TN = WC / 32;
@@ -191,7 +194,12 @@ struct Tile {
   static constexpr int F32_PITCH = BN + 4, BF_PITCH = BN + 8;
   static constexpr int STAGED = WR * F32_PITCH * 4 > BM * BF_PITCH * 2 ? WR * F32_PITCH * 4
                                                                        : BM * BF_PITCH * 2;
-  static constexpr int ROWS_LDS = RING > STAGED ? RING : STAGED;
+  // (and, with the contraction split over KS groups, their sums on the way)
+  template <int KS>
+  static constexpr int rows_lds() {
+    const int sums = KS / 2 * BM * F32_PITCH * 4, most = KS * RING > STAGED ? KS * RING : STAGED;
+    return most > sums ? most : sums;
+  }
   // LDS through which a wave's results leave: 32 rows of SJ 32-column sub-tiles
   static constexpr int SJ = BLOCKS * (RING + NW * 4096) <= 160 * 1024 ? 2 : 1;
   static constexpr int WAVE_STAGING = SJ * 2048;
@@ -203,7 +211,7 @@ struct Tile {
   static constexpr int PA = SA >= 4 ? 1 : (4 / SA < CA ? 4 / SA : CA);
   static constexpr int PB = SB >= 4 ? 1 : (4 / SB < CB ? 4 / SB : CB);
   static_assert(CA * NW * 1024 == A_BYTES && CB * NW * 1024 == B_BYTES, "whole copies");
-  static_assert(BM >= 128 && BN >= 128, "the col form's swizzle needs 8 pieces a row");
+  static_assert(BN >= 64, "the col form's swizzle needs 4 pieces a row");
   static_assert(ST >= 2, "waits");
 };
 
@@ -289,7 +297,7 @@ struct FragOffsets {
     const int tk = 8 * fq + (lane % 16) / 4, tc = 16 * ((lane / 16) % 2) + 4 * (lane % 4);
     auto col = [&](int c, int width) {
       c += tc;
-      return (unsigned)(tk * width * 2 + cswz(tk, c / 16) * 32 + (c % 16) * 2);
+      return (unsigned)(tk * width * 2 + cswz(tk, c / 16, width) * 32 + (c % 16) * 2);
     };
     if constexpr (ROW_A) {
       const int r = wm * TL::WR + fr;  // 32 rows on, the swizzle is the same
@@ -320,14 +328,16 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TL::TM][TL::TN]) {
       for (int q = 0; q < 16; ++q) acc[i][j][q] = 0.0f;
 }
 
-// DU and DX: a block takes one row tile of one expert and one column tile.
-template <int KIND, typename WT, typename TL>
-__global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Operands o, int NT) {
+// DU and DX: a block takes one row tile of one expert and one column tile.  Its KS
+// groups of waves split the contraction, each with a ring of its own; their sums meet
+// in LDS, always in the same order.
+template <int KIND, typename WT, typename TL, int KS>
+__global__ __launch_bounds__(64 * TL::NW * KS, (TL::BLOCKS * TL::NW * KS + 3) / 4) void grad_rows_kernel(Operands o,
+                                                                                        int NT) {
   constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, ST = TL::ST, WN = TL::WN;
   constexpr int TM = TL::TM, TN = TL::TN, NF = TL::NF, NMF = TL::NMF, WR = TL::WR, WC = TL::WC;
   constexpr int CA = TL::CA, LPW = TL::LPW;
   extern __shared__ __align__(16) unsigned char smem[];
-  const unsigned base = lds_offset(smem);
 
   const int H = o.H, I = o.I;
   const int Nout = KIND == kDU ? I : H;
@@ -355,7 +365,9 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
   nt = __builtin_amdgcn_readfirstlane(nt);
   row0 = __builtin_amdgcn_readfirstlane(row0);
   row1 = __builtin_amdgcn_readfirstlane(row1);
-  const int lane = lane_id(), wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int lane = lane_id(), block_wave = __builtin_amdgcn_readfirstlane(threadIdx.x / kWave);
+  const int grp = block_wave / NW, wave = block_wave % NW;
+  const unsigned base = lds_offset(smem) + grp * TL::RING;
   const int wm = wave / WN, wn = wave % WN, fr = lane % 32, fq = lane / 32;
   const int n0 = nt * BN;
 
@@ -382,14 +394,19 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
       off[j] = at + rswz(r, lane % 4) * 16;
     } else {
       const int k = TL::SB * (wave * TL::CB + j - CA) + lane / TL::LB;
-      const int c = n0 + cswz(k, lane % TL::LB / 2) * 16 + (lane & 1) * 8;
+      const int c = n0 + cswz(k, lane % TL::LB / 2, BN) * 16 + (lane & 1) * 8;
       off[j] = ((unsigned)k * (unsigned)Nout + (unsigned)(c < Nout ? c : 0)) * 2u;
     }
   }
-  const int nk = (KIND == kDU ? H : 2 * I) / GK;
+  // this group's k-tiles, and the most that a group has
+  const int nk_all = (KIND == kDU ? H : 2 * I) / GK, first = grp * nk_all / KS;
+  const int nk = (grp + 1) * nk_all / KS - first, nk_most = (nk_all + KS - 1) / KS;
   // pA, pB: the k-tile that is being copied; `turn` k-tiles before pB goes on to the
   // up rows
-  int turn = KIND == kDX ? I / GK : -1;
+  int turn = KIND == kDX ? I / GK - first : -1;
+  pA += first * GK;
+  if (KIND == kDX && turn <= 0) pB = pU + (size_t)(-turn) * GK * Nout;
+  else pB += (size_t)first * GK * Nout;
   const unsigned ldsA = base + wave * CA * 1024, ldsB = base + TL::A_BYTES + wave * TL::CB * 1024;
   auto copy = [&](int j, unsigned st) {
     if (j < CA) global_copy16(pA, off[j], ldsA + st + j * 1024);
@@ -409,6 +426,12 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
   const FragOffsets<TL, true> fo(lane, wm, wn);
   f32x16 acc[TM][TN];
   clear<TL>(acc);
+
+  // a group of one wave has its ring for itself and waits for nobody
+  auto group_barrier = [&]() {
+    if constexpr (NW > 1) block_barrier();
+    else asm volatile("" ::: "memory");
+  };
 
   auto run = [&](auto nv_tag) {
     constexpr int NV = decltype(nv_tag)::value;  // sub-tiles of rows to multiply
@@ -430,8 +453,9 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
     };
     // The copies of tile kt + ST go to tile kt's slot: the first P1 of them in the
     // second half of tile kt, when no wave reads it any more, the others in the first
-    // half of tile kt + 1, so that the copy path is never idle for half of the time.
-    constexpr int P1 = LPW / 2, P2 = LPW - P1;
+    // half of tile kt + 1, so that the copy path is never idle for half of the time
+    // (with two stages all at once: they have a tile less to arrive).
+    constexpr int P1 = ST == 2 ? LPW : LPW / 2, P2 = LPW - P1;
 #pragma unroll
     for (int s = 0; s < ST; ++s)
       if (s < nk) {
@@ -442,7 +466,7 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
       }
     if (nk >= ST) wait_vmem<(ST - 2) * LPW>();
     else wait_tiles(nk - 1);
-    block_barrier();
+    group_barrier();
 #pragma unroll
     for (int f = 0; f < NF; ++f) rd(0, 0, f, f0);
     wait_lds();
@@ -469,7 +493,7 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
       // tile kt + 1 has landed for every wave; no wave reads tile kt after this
       if constexpr (FIRST) wait_vmem<(ST - 2) * LPW>();
       else wait_tiles(nk - 2 - kt);
-      block_barrier();
+      group_barrier();
       __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int m = 0; m < NMF; ++m) {
@@ -490,12 +514,49 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
     for (; kt + ST < nk; ++kt) tile(kt, std::true_type{}, std::true_type{});
     if (kt + ST == nk) tile(kt++, std::true_type{}, std::false_type{});
     for (; kt < nk; ++kt) tile(kt, std::false_type{}, std::false_type{});
+    for (; kt < nk_most; ++kt) group_barrier();  // the other groups'
     __syncthreads();
   };
   static_assert(TM == 2, "the cases below");
   if (nv == 2) run(std::integral_constant<int, 2>{});
   else if (nv == 1) run(std::integral_constant<int, 1>{});
   else run(std::integral_constant<int, 0>{});
+
+  // the groups' sums: the upper half of them to LDS, the lower half adds, and again
+#pragma unroll
+  for (int half = KS / 2; half > 0; half /= 2) {
+    float* part = reinterpret_cast<float*>(smem) +
+                  (size_t)(grp % half) * BM * TL::F32_PITCH + (wm * WR + fr) * TL::F32_PITCH +
+                  wn * WC + 4 * fq;
+    if (grp >= half && grp < 2 * half) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (i < nv)
+              *reinterpret_cast<f32x4*>(part + i * 32 * TL::F32_PITCH + j * 32 + 8 * q) =
+                  f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
+                        acc[i][j][4 * q + 3]};
+    }
+    __syncthreads();
+    if (grp < half) {
+#pragma unroll
+      for (int i = 0; i < TM; ++i)
+#pragma unroll
+        for (int j = 0; j < TN; ++j)
+#pragma unroll
+          for (int q = 0; q < 4; ++q)
+            if (i < nv) {
+              const f32x4 v =
+                  *reinterpret_cast<const f32x4*>(part + i * 32 * TL::F32_PITCH + j * 32 + 8 * q);
+#pragma unroll
+              for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
+            }
+    }
+    __syncthreads();
+  }
 
   // Epilogue through LDS (the ring's, free now), so that whole rows are read and
   // written in 16-B pieces.
@@ -507,10 +568,10 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
     const bf16* kept = static_cast<const bf16*>(o.kept);
     bf16* d_gu = static_cast<bf16*>(o.d_gu);
     bf16* hw = static_cast<bf16*>(o.hw);
-    constexpr int LPR = BN / 8, RPI = 64 * NW / LPR;  // lanes a row, rows an iteration
+    constexpr int LPR = BN / 8, RPI = 64 * NW * KS / LPR;  // lanes a row, rows an iteration
     static_assert(LPR <= kWave && WR % RPI == 0, "rows of the epilogue");
     for (int pass = 0; pass < TL::WM; ++pass) {
-      if (wm == pass) {
+      if (grp == 0 && wm == pass) {
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -571,7 +632,7 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
   } else {
     bf16* stg = reinterpret_cast<bf16*>(smem);
 #pragma unroll
-    for (int i = 0; i < TM; ++i)
+    for (int i = 0; i < TM && grp == 0; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
@@ -584,7 +645,7 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_rows_kernel(Op
     __syncthreads();
     constexpr int CH = BN / 8;
 #pragma unroll 4
-    for (int k = tid; k < BM * CH; k += 64 * NW) {
+    for (int k = tid; k < BM * CH; k += 64 * NW * KS) {
       const int r = k / CH, c = (k % CH) * 8;
       if (row0 + r < row1 && n0 + c < Nout)
         *reinterpret_cast<uint4*>(static_cast<bf16*>(o.d_xs) + (size_t)(row0 + r) * H + n0 + c) =
@@ -690,7 +751,7 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_weights_kernel
   const char* Gp = static_cast<const char*>(GB ? o.x : o.d_out);
   const unsigned ldr = 2u * (unsigned)(GB ? 2 * I : I), ldg = 2u * (unsigned)H;  // bytes
   auto piece = [&](int k, int lpr) {
-    return (unsigned)(cswz(k, lane % lpr / 2) * 32 + (lane & 1) * 16);
+    return (unsigned)(cswz(k, lane % lpr / 2, lpr * 8) * 32 + (lane & 1) * 16);
   };
   unsigned offR[CR], colG[PG];
 #pragma unroll
@@ -927,30 +988,35 @@ __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_weights_kernel
 }
 
 // ---------------------------------------------------------------------------
-// fp32 (debug path): 64 x 64 tiles on the vector ALUs
+// fp32 (debug path): BM x 64 tiles on the vector ALUs
 // ---------------------------------------------------------------------------
-constexpr int FT = 64, FK = 16;
+// k-steps of 32, the next one's loads under way while a thread multiplies its
+// (BM / 16) x 4 results' operands, both kept k-major in LDS.
+constexpr int FN = 64, FK = 32;
+template <int KIND>
+constexpr int f32_rows() { return KIND == kDWGU || KIND == kDWDN ? 64 : 32; }
 
 template <int KIND>
 __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, int NT) {
   constexpr bool DW = KIND == kDWGU || KIND == kDWDN;
-  __shared__ __align__(16) float As[FK][FT + 4], Bs[FK][FT + 4];
-  __shared__ int toks[FT];
+  constexpr int BM = f32_rows<KIND>(), TM = BM / 16;
+  constexpr int NA = BM * FK / 4 / 256, NB = FN * FK / 4 / 256;  // 16-B loads a thread
+  __shared__ __align__(16) float As[FK][BM + 4], Bs[FK][FN + 4];
   const int H = o.H, I = o.I;
   const int Nout = KIND == kDU || KIND == kDWDN ? I : H;
   const int M = KIND == kDWGU ? 2 * I : H;
   int e = 0, row0, row1, m0 = 0;
-  const int nt = blockIdx.x % NT, n0 = nt * FT;
+  const int nt = blockIdx.x % NT, n0 = nt * FN;
   if constexpr (DW) {
     e = blockIdx.x / (MT * NT);
-    m0 = blockIdx.x / NT % MT * FT;
+    m0 = blockIdx.x / NT % MT * BM;
     const bool all = o.ident || o.rows == 0;  // no rows: the offsets may not exist
     row0 = all ? 0 : o.offsets[e];
     row1 = all ? o.rows : o.offsets[e + 1];
   } else if (o.ident) {
-    row0 = blockIdx.x / NT * FT;
-    row1 = min(row0 + FT, o.rows);
-  } else if (!find_row_tile(o.offsets, o.E, FT, blockIdx.x / NT, e, row0, row1)) {
+    row0 = blockIdx.x / NT * BM;
+    row1 = min(row0 + BM, o.rows);
+  } else if (!find_row_tile(o.offsets, o.E, BM, blockIdx.x / NT, e, row0, row1)) {
     return;  // uniform over the block
   }
   const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
@@ -963,95 +1029,128 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
   const float* wu = static_cast<const float*>(o.w_up) + (size_t)e * o.gu_stride;
   const float* wd = static_cast<const float*>(o.w_down) + (size_t)e * o.dn_stride;
   const int Kd = DW ? row1 - row0 : KIND == kDU ? H : 2 * I;
-  if (!DW && tid < FT) toks[tid] = row0 + tid < row1 ? o.row_tok[row0 + tid] : -1;
-  float acc[4][4] = {};
-  for (int k0 = 0; k0 < Kd; k0 += FK) {
-    if (DW && tid < FK) toks[tid] = k0 + tid < Kd ? o.row_tok[row0 + k0 + tid] : -1;
-    __syncthreads();
-    for (int i = tid; i < FT * FK; i += 256) {
+  const f32x4 zero = {0.0f, 0.0f, 0.0f, 0.0f};
+  auto ld4 = [](const float* p) { return *reinterpret_cast<const f32x4*>(p); };
+
+  f32x4 va[NA], vb[NB];
+  auto load = [&](int k0) {
+#pragma unroll
+    for (int u = 0; u < NA; ++u) {
+      const int i = tid + 256 * u;
+      va[u] = zero;
       if constexpr (DW) {
-        const int k = i / FT, c = i % FT, r = row0 + k0 + k, tok = toks[k];
-        float a = 0.0f, b = 0.0f;
-        if (k0 + k < Kd && tok >= 0) {
-          if (m0 + c < M)
-            a = KIND == kDWGU ? d_gu[(size_t)r * 2 * I + m0 + c] : d_out[(size_t)tok * H + m0 + c];
-          if (n0 + c < Nout)
-            b = KIND == kDWGU ? x[(size_t)tok * H + n0 + c] : hw[(size_t)r * I + n0 + c];
+        const int k = k0 + i / (BM / 4), c = m0 + i % (BM / 4) * 4, r = row0 + k;
+        if (k < Kd && c < M) {
+          const int tok = o.row_tok[r];
+          if (tok >= 0)
+            va[u] = ld4(KIND == kDWGU ? d_gu + (size_t)r * 2 * I + c : d_out + (size_t)tok * H + c);
         }
-        As[k][c] = a;
-        Bs[k][c] = b;
       } else {
-        const int r = i / FK, ka = i % FK;  // contraction lengths are multiples of 32
-        float a = 0.0f;
-        if (row0 + r < row1) {
-          if (KIND == kDU)
-            a = toks[r] >= 0 ? d_out[(size_t)toks[r] * H + k0 + ka] : 0.0f;
-          else
-            a = d_gu[(size_t)(row0 + r) * 2 * I + k0 + ka];
+        const int r = row0 + i / (FK / 4), k = k0 + i % (FK / 4) * 4;  // Kd is a multiple of 32
+        if (r < row1) {
+          if constexpr (KIND == kDU) {
+            const int tok = o.row_tok[r];
+            if (tok >= 0) va[u] = ld4(d_out + (size_t)tok * H + k);
+          } else {
+            va[u] = ld4(d_gu + (size_t)r * 2 * I + k);
+          }
         }
-        As[ka][r] = a;
-        const int k = i / FT, c = i % FT, kk = k0 + k;
-        float b = 0.0f;
-        if (n0 + c < Nout) {
-          if (KIND == kDU)
-            b = wd[(size_t)kk * I + n0 + c];
-          else
-            b = kk < I ? wg[(size_t)kk * H + n0 + c] : wu[(size_t)(kk - I) * H + n0 + c];
-        }
-        Bs[k][c] = b;
       }
     }
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const int i = tid + 256 * u, k = k0 + i / (FN / 4), c = n0 + i % (FN / 4) * 4;
+      vb[u] = zero;
+      if (k >= Kd || c >= Nout) continue;
+      if constexpr (KIND == kDU) {
+        vb[u] = ld4(wd + (size_t)k * I + c);
+      } else if constexpr (KIND == kDX) {
+        vb[u] = ld4(k < I ? wg + (size_t)k * H + c : wu + (size_t)(k - I) * H + c);
+      } else {
+        const int r = row0 + k, tok = o.row_tok[r];
+        if (tok >= 0)
+          vb[u] = ld4(KIND == kDWGU ? x + (size_t)tok * H + c : hw + (size_t)r * I + c);
+      }
+    }
+  };
+  float acc[TM][4] = {};
+  if (Kd > 0) load(0);
+  for (int k0 = 0; k0 < Kd; k0 += FK) {
+#pragma unroll
+    for (int u = 0; u < NA; ++u) {
+      const int i = tid + 256 * u;
+      if constexpr (DW) {
+        *reinterpret_cast<f32x4*>(&As[i / (BM / 4)][i % (BM / 4) * 4]) = va[u];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) As[i % (FK / 4) * 4 + j][i / (FK / 4)] = va[u][j];
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < NB; ++u) {
+      const int i = tid + 256 * u;
+      *reinterpret_cast<f32x4*>(&Bs[i / (FN / 4)][i % (FN / 4) * 4]) = vb[u];
+    }
     __syncthreads();
+    if (k0 + FK < Kd) load(k0 + FK);
 #pragma unroll
     for (int k = 0; k < FK; ++k) {
-      const float4 a = *reinterpret_cast<const float4*>(&As[k][4 * tr]);
-      const float4 b = *reinterpret_cast<const float4*>(&Bs[k][4 * tc]);
-      const float av[4] = {a.x, a.y, a.z, a.w}, bv[4] = {b.x, b.y, b.z, b.w};
+      const f32x4 b = ld4(&Bs[k][4 * tc]);
 #pragma unroll
-      for (int i = 0; i < 4; ++i)
+      for (int i = 0; i < TM; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(av[i], bv[j], acc[i][j]);
+        for (int j = 0; j < 4; ++j) acc[i][j] = fmaf(As[k][TM * tr + i], b[j], acc[i][j]);
     }
     __syncthreads();
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int rl = 4 * tr + i, row = row0 + rl;
-    float dot = 0.0f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-      const int col = n0 + 4 * tc + j;
-      if (col >= Nout) continue;
-      const float v = acc[i][j];
-      if constexpr (KIND == kDU) {
-        if (row >= row1) continue;
-        const bool live = toks[rl] >= 0;
+  for (int i = 0; i < TM; ++i) {
+    const int rl = TM * tr + i, row = row0 + rl, col = n0 + 4 * tc;
+    const bool in = col < Nout;  // four columns are inside or outside together
+    const f32x4 v = {acc[i][0], acc[i][1], acc[i][2], acc[i][3]};
+    if constexpr (KIND == kDU) {
+      float dot = 0.0f;
+      if (row < row1 && in) {
+        const bool live = o.row_tok[row] >= 0;
         const float w = o.ident ? 1.0f : o.topk_w[o.sorted_slots[row]];
-        float h, dg, du;
-        act_grad<false>(kept[(size_t)row * 2 * I + col], kept[(size_t)row * 2 * I + I + col], v, h,
-                        dg, du);
-        if (live) dot += v * h;
-        d_gu[(size_t)row * 2 * I + col] = live ? w * dg : 0.0f;
-        d_gu[(size_t)row * 2 * I + I + col] = live ? w * du : 0.0f;
-        hw[(size_t)row * I + col] = live ? w * h : 0.0f;
-      } else if constexpr (KIND == kDX) {
-        if (row < row1) static_cast<float*>(o.d_xs)[(size_t)row * H + col] = v;
-      } else {
-        const int m = m0 + rl;
-        if (m >= M) continue;
-        if constexpr (KIND == kDWGU) {
-          float* d = m < I ? static_cast<float*>(o.d_gate) + (size_t)m * H
-                           : static_cast<float*>(o.d_up) + (size_t)(m - I) * H;
-          d[(size_t)e * o.gu_stride + col] = v;
-        } else {
-          static_cast<float*>(o.d_down)[(size_t)e * o.dn_stride + (size_t)m * I + col] = v;
-        }
-      }
-    }
-    if (KIND == kDU && o.part) {
+        const f32x4 g = ld4(kept + (size_t)row * 2 * I + col);
+        const f32x4 u = ld4(kept + (size_t)row * 2 * I + I + col);
+        f32x4 og = zero, ou = zero, oh = zero;
+        if (live) {
 #pragma unroll
-      for (int s = 8; s > 0; s >>= 1) dot += __shfl_xor(dot, s, kWave);
-      if (tc == 0 && row < row1) o.part[(size_t)nt * o.rows + row] = dot;
+          for (int j = 0; j < 4; ++j) {
+            float h, dg, du;
+            act_grad<false>(g[j], u[j], v[j], h, dg, du);
+            dot += v[j] * h;
+            og[j] = w * dg;
+            ou[j] = w * du;
+            oh[j] = w * h;
+          }
+        }
+        *reinterpret_cast<f32x4*>(d_gu + (size_t)row * 2 * I + col) = og;
+        *reinterpret_cast<f32x4*>(d_gu + (size_t)row * 2 * I + I + col) = ou;
+        *reinterpret_cast<f32x4*>(hw + (size_t)row * I + col) = oh;
+      }
+      if (o.part) {
+#pragma unroll
+        for (int s = 8; s > 0; s >>= 1) dot += __shfl_xor(dot, s, kWave);
+        if (tc == 0 && row < row1) o.part[(size_t)nt * o.rows + row] = dot;
+      }
+    } else if constexpr (KIND == kDX) {
+      if (row < row1 && in)
+        *reinterpret_cast<f32x4*>(static_cast<float*>(o.d_xs) + (size_t)row * H + col) = v;
+    } else {
+      const int m = m0 + rl;
+      if (m < M && in) {
+        float* d;
+        if constexpr (KIND == kDWGU)
+          d = (m < I ? static_cast<float*>(o.d_gate) + (size_t)m * H
+                     : static_cast<float*>(o.d_up) + (size_t)(m - I) * H) +
+              (size_t)e * o.gu_stride;
+        else
+          d = static_cast<float*>(o.d_down) + (size_t)e * o.dn_stride + (size_t)m * I;
+        *reinterpret_cast<f32x4*>(d + col) = v;
+      }
     }
   }
 }
@@ -1061,39 +1160,77 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
 // of 4 waves a CU 484 / 277, waves of 64 x 128 496 / 269).
 typedef Tile<128, 256, 2, 4, 3, 2> RowsTile;
 typedef Tile<256, 256, 2, 4, 4, 1> WeightsTile;
+// DU and DX of small problems: 64 x 64, the contraction split over 8 single waves.
+typedef Tile<64, 64, 1, 1, 2, 1> FewTile;
+constexpr int kFewSplit = 8;
+// DW of small problems: 128 x 128, two blocks of 4 waves a CU.
+typedef Tile<128, 128, 2, 2, 3, 2> SmallWeightsTile;
 constexpr int kCUs = 256;
+
+template <int KIND, typename WT, typename TL, int KS>
+hipError_t launch_rows(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
+  const int NT = ((KIND == kDU ? a.I : a.H) + TL::BN - 1) / TL::BN;
+  const int blocks = tile_count_bound(a.ident, a.rows, a.T, a.E, TL::BM) * NT;
+  auto kf = grad_rows_kernel<KIND, WT, TL, KS>;
+  constexpr int lds = TL::template rows_lds<KS>();
+  static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
+  static const hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kf, dim3(blocks), dim3(64 * TL::NW * KS), lds, s, o, NT);
+  return hipGetLastError();
+}
+
+// Whether DU (N = I) or DX (N = H) takes the small form: while its blocks, one a CU,
+// are one and a half a CU at most.  The dense MLP (2816 x 2112) at 16 / 301 / 700 /
+// 1200 tokens, DU: 14 / 20 / 38 / 58 us, in the large form 28 / 46 / 48 / 48; DX 16 /
+// 26 / 52 / 98 and 36 / 49 / 51 / 53.  (128 x 128 tiles split over four groups of
+// four waves: DU 24 / 36 / 38 / 40.)
+bool small_rows(const FfnGradArgs& a, int N) {
+  return tile_count_bound(a.ident, a.rows, a.T, a.E, FewTile::BM) *
+             ((N + FewTile::BN - 1) / FewTile::BN) <= kCUs * 3 / 2;
+}
+
+template <int KIND, typename WT, typename TL>
+hipError_t launch_weights(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
+  const int N = KIND == kDWDN ? a.I : a.H, M = KIND == kDWGU ? 2 * a.I : a.H;
+  const int NT = (N + TL::BN - 1) / TL::BN, MT = (M + TL::BM - 1) / TL::BM;
+  const int tiles = o.E * MT * NT;
+  auto kf = grad_weights_kernel<KIND, WT, TL>;
+  constexpr int lds = TL::RING + TL::NW * TL::WAVE_STAGING;
+  static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
+  static const hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
+  const int most = kCUs * TL::BLOCKS, blocks = tiles < most ? (tiles + 7) / 8 * 8 : most;
+  hipLaunchKernelGGL(kf, dim3(blocks), dim3(64 * TL::NW), lds, s, o, MT, NT);
+  return hipGetLastError();
+}
 
 template <int KIND, typename WT>
 hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   constexpr bool DW = KIND == kDWGU || KIND == kDWDN;
-  typedef typename std::conditional<DW, WeightsTile, RowsTile>::type TL;
   const int N = KIND == kDU || KIND == kDWDN ? a.I : a.H;
   const int M = KIND == kDWGU ? 2 * a.I : a.H;
-  const int bm = a.bf16 ? TL::BM : FT, bn = a.bf16 ? TL::BN : FT;
-  const int NT = (N + bn - 1) / bn, MT = (M + bm - 1) / bm;
-  const int tiles = DW ? o.E * MT * NT : tile_count_bound(a.ident, a.rows, a.T, a.E, bm) * NT;
-  if (tiles == 0) return hipSuccess;
   if (!a.bf16) {
+    constexpr int BM = f32_rows<KIND>();
+    const int NT = (N + FN - 1) / FN, MT = (M + BM - 1) / BM;
+    const int tiles = DW ? o.E * MT * NT : tile_count_bound(a.ident, a.rows, a.T, a.E, BM) * NT;
+    if (tiles == 0) return hipSuccess;
     hipLaunchKernelGGL(grad_gemm_f32_kernel<KIND>, dim3(tiles), dim3(256), 0, s, o, MT, NT);
-  } else if constexpr (DW) {
-    auto kf = grad_weights_kernel<KIND, WT, TL>;
-    constexpr int lds = TL::RING + TL::NW * TL::WAVE_STAGING;
-    static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
-    static const hipError_t attr = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (attr != hipSuccess) return attr;
-    const int most = kCUs * TL::BLOCKS, blocks = tiles < most ? (tiles + 7) / 8 * 8 : most;
-    hipLaunchKernelGGL(kf, dim3(blocks), dim3(64 * TL::NW), lds, s, o, MT, NT);
-  } else {
-    auto kf = grad_rows_kernel<KIND, WT, TL>;
-    constexpr int lds = TL::ROWS_LDS;
-    static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
-    static const hipError_t attr = hipFuncSetAttribute(
-        reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
-    if (attr != hipSuccess) return attr;
-    hipLaunchKernelGGL(kf, dim3(tiles), dim3(64 * TL::NW), lds, s, o, NT);
+    return hipGetLastError();
   }
-  return hipGetLastError();
+  if constexpr (DW) {
+    const int tiles = o.E * ((M + WeightsTile::BM - 1) / WeightsTile::BM) *
+                      ((N + WeightsTile::BN - 1) / WeightsTile::BN);
+    // Up to half as many large tiles as CUs: the dense MLP's DWDN (99 tiles) at 301 / 4096
+    // tokens 14.0 / 93 -> 10.7 / 63 us; its DWGU (187) 16.6 / 106, with small ones 16.0 / 121.
+    if (tiles <= kCUs / 2) return launch_weights<KIND, WT, SmallWeightsTile>(a, o, s);
+    return launch_weights<KIND, WT, WeightsTile>(a, o, s);
+  } else {
+    if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit>(a, o, s);
+    return launch_rows<KIND, WT, RowsTile, 1>(a, o, s);
+  }
 }
 
 template <typename XT, typename ST>
@@ -1106,8 +1243,10 @@ void launch_combine_grad(const FfnGradArgs& a, int parts, hipStream_t s) {
 
 }  // namespace
 
+// Partial sums of d_topk_w: DU's column tiles, those of its widest grid.
 int ffn_grad_parts(int I, bool bf16) {
-  return bf16 ? (I + RowsTile::BN - 1) / RowsTile::BN : (I + FT - 1) / FT;
+  const int n = bf16 ? FewTile::BN : FN;
+  return (I + n - 1) / n;
 }
 
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
@@ -1133,7 +1272,8 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
       if (e != hipSuccess) return e;
     }
     if (!a.ident && (a.d_x || a.d_topk_w)) {
-      const int parts = ffn_grad_parts(a.I, a.bf16);
+      const int pn = !a.bf16 ? FN : small_rows(a, a.I) ? FewTile::BN : RowsTile::BN;
+      const int parts = (a.I + pn - 1) / pn;
       if (!a.bf16) launch_combine_grad<float, float>(a, parts, s);
       else if (a.xs_bf16) launch_combine_grad<bf16, bf16>(a, parts, s);
       else launch_combine_grad<bf16, float>(a, parts, s);
