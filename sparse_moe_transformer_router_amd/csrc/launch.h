@@ -349,7 +349,7 @@ struct FfnGradArgs {
 int ffn_grad_parts(int I, bool bf16);
 hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s);
 
-// Backward passes of the layer's norms (norms_grad.hip), in norms_grad_blocks(T)
+// Backward passes of the layer's norms (norms_grad.hip), in norms_grad_blocks
 // blocks whose sums over tokens a last kernel adds.
 struct PreNormGradArgs {
   int T, H;
@@ -389,7 +389,7 @@ struct PostNormGradArgs {
   float* ws_part;        // [blocks,3,H]
   double* ws_scalar;     // [blocks]
 };
-int norms_grad_blocks(int T);
+int norms_grad_blocks(int T, int H);
 hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s);
 hipError_t launch_post_norms_grad(const PostNormGradArgs& a, hipStream_t s);
 

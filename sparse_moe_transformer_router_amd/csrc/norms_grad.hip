@@ -9,14 +9,20 @@
 //            added on the way out.  One pair of row sums: x^2 and e x.
 //   behind   s = n(dn) g1 + n(moe) g2, o = n(s) g3, out = (o + x) layer_scalar.
 //            Row sums: dn^2 and moe^2; then s^2 and e3 s; then e1 n1 and e2 n2.
-// A block takes one row at a time, a thread 8 of its columns (hidden <= 8192), so
-// that its sums over tokens (d_g) stay in registers; each block writes them once
-// and a second kernel adds the blocks in order.
+// A group of threads takes a row, a thread 8 of its columns (hidden <= 8192), and a
+// block as many groups as fit 512 threads (one of up to 1024 past hidden 4096), so that the sums over tokens (d_g) stay in
+// registers; a block adds its groups' and writes them once, and a second kernel adds
+// the blocks in order.  A row's loads are issued before the row before it is worked
+// on.  Bound by memory.
 #include "common.h"
 #include "launch.h"
 
 namespace moe {
 namespace {
+
+// Blocks of a backward pass at most, one a CU (post-norms at 4096 tokens 48 us, with
+// two a CU 52: the blocks' sums are written and read again).
+constexpr int kNormsBlocks = 256;
 
 __device__ __forceinline__ void ld8(const float* p, float v[8]) {
   const f32x4* q = reinterpret_cast<const f32x4*>(p);
@@ -44,97 +50,177 @@ __device__ __forceinline__ void st8(bf16* p, const float v[8]) {
   *reinterpret_cast<bf16x8*>(p) = b;
 }
 
-// Sums of a and b over the block, to every thread.  red: 2 x 16 floats that no
-// thread still reads from an earlier call (callers alternate two of them).
-__device__ __forceinline__ void block_sum2(float& a, float& b, float* red) {
-  a = wave_sum(a);
-  b = wave_sum(b);
-  const int wave = threadIdx.x / kWave, nw = blockDim.x / kWave;
-  if (lane_id() == 0) {
-    red[wave] = a;
-    red[16 + wave] = b;
-  }
-  __syncthreads();
-  a = b = 0.0f;
-  for (int w = 0; w < nw; ++w) {
-    a += red[w];
-    b += red[16 + w];
-  }
+// 8 values as loaded.
+template <typename T> struct Raw8 { uint4 u[sizeof(T) / 2]; };
+template <typename T>
+__device__ __forceinline__ Raw8<T> ld_raw(const T* p) {
+  Raw8<T> r;
+#pragma unroll
+  for (int i = 0; i < (int)sizeof(T) / 2; ++i) r.u[i] = reinterpret_cast<const uint4*>(p)[i];
+  return r;
+}
+template <typename T>
+__device__ __forceinline__ void widen(const Raw8<T>& r, float v[8]) {
+  ld8(reinterpret_cast<const T*>(&r), v);
 }
 
-template <typename XT>
-__global__ __launch_bounds__(1024) void pre_grad_kernel(
-    int T, int H, float eps, float scalar, const XT* __restrict__ x, const float* __restrict__ g1,
-    const float* __restrict__ g2, const uint8_t* __restrict__ mask, const XT* __restrict__ d_xd,
-    const XT* __restrict__ d_xm, const XT* __restrict__ d_add, const XT* __restrict__ d_out,
-    XT* __restrict__ d_x, float* __restrict__ part) {
-  __shared__ float red[2][32];
-  const int c = threadIdx.x * 8;
+// Sum over the wave, in every lane: within rows of 16 lanes, then across them, on the
+// vector unit's own lane moves (a shuffle goes through LDS: six of them in a row took
+// a third of a row's time).
+template <int CTRL, int ROWS>
+__device__ __forceinline__ float dpp_add(float v) {
+  return v + __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(v), CTRL, ROWS, 0xf,
+                                                        false));
+}
+__device__ __forceinline__ float wave_total(float v) {
+  v = dpp_add<0x111, 0xf>(v);  // row_shr:1, 2, 4, 8
+  v = dpp_add<0x112, 0xf>(v);
+  v = dpp_add<0x114, 0xf>(v);
+  v = dpp_add<0x118, 0xf>(v);
+  v = dpp_add<0x142, 0xa>(v);  // row_bcast:15 into rows 1 and 3
+  v = dpp_add<0x143, 0xc>(v);  // row_bcast:31 into rows 2 and 3
+  return __int_as_float(__builtin_amdgcn_readlane(__float_as_int(v), 63));
+}
+
+// Sums of the N values over the threads of a group (nw waves, this one the w-th of
+// group g), to each of them.  red: 16 x N floats that no thread still reads from an
+// earlier call (callers alternate two of them).
+template <int N>
+__device__ __forceinline__ void group_sums(float (&v)[N], float* red, int g, int w, int nw) {
+#pragma unroll
+  for (int i = 0; i < N; ++i) {
+    v[i] = wave_total(v[i]);
+    if (lane_id() == 0) red[(g * nw + w) * N + i] = v[i];
+  }
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < N; ++i) v[i] = 0.0f;
+  for (int k = 0; k < nw; ++k)
+#pragma unroll
+    for (int i = 0; i < N; ++i) v[i] += red[(g * nw + k) * N + i];
+}
+
+// Adds the groups' sums s (N arrays of H) in order; group 0 writes them to part.
+template <int N>
+__device__ __forceinline__ void write_sums(float (&s)[N][8], int H, int c, bool on, int g,
+                                           int groups, float* lds, float* __restrict__ part) {
+  for (int k = 1; k < groups; ++k) {
+    __syncthreads();
+    if (g == k && on)
+#pragma unroll
+      for (int i = 0; i < N; ++i) st8(lds + i * H + c, s[i]);
+    __syncthreads();
+    if (g == 0 && on)
+#pragma unroll
+      for (int i = 0; i < N; ++i) {
+        float v[8];
+        ld8(lds + i * H + c, v);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] += v[j];
+      }
+  }
+  if (g == 0 && on)
+#pragma unroll
+    for (int i = 0; i < N; ++i) st8(part + i * H + c, s[i]);
+}
+
+template <typename XT, int MAXT>
+__global__ __launch_bounds__(MAXT) void pre_grad_kernel(
+    int T, int H, int groups, float eps, float scalar, const XT* __restrict__ x,
+    const float* __restrict__ g1, const float* __restrict__ g2, const uint8_t* __restrict__ mask,
+    const XT* __restrict__ d_xd, const XT* __restrict__ d_xm, const XT* __restrict__ d_add,
+    const XT* __restrict__ d_out, XT* __restrict__ d_x, float* __restrict__ part) {
+  constexpr int R = MAXT > 512 ? 1 : 2;  // rows that a group works on at a time
+  extern __shared__ __align__(16) float lds[];
+  __shared__ __align__(16) float red[2][2 * R * 16];
+  const int nt = blockDim.x / groups, nw = nt / kWave;  // threads, waves a group
+  const int g = threadIdx.x / nt, c = threadIdx.x % nt * 8, w = threadIdx.x % nt / kWave;
   const bool on = c < H;
-  float w1[8] = {}, w2[8] = {}, s1[8] = {}, s2[8] = {};
+  float w1[8] = {}, w2[8] = {}, s[2][8] = {};
   if (on) {
     ld8(g1 + c, w1);
     ld8(g2 + c, w2);
   }
-  int flip = 0;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+  const int step = gridDim.x * groups * R;
+  auto live = [&](int t) { return on && t < T && !(mask && !mask[t]); };
+  struct Row { Raw8<XT> x, a, b, z, o; } next[R];
+  auto load = [&](int t, Row& r) {
+    if (!live(t)) return;
     const size_t at = (size_t)t * H + c;
-    if (mask && !mask[t]) {  // uniform over the block
-      const float z[8] = {};
-      if (on) st8(d_x + at, z);
-      continue;
-    }
-    float v[8] = {}, a[8] = {}, b[8] = {}, o[8] = {}, ss = 0.0f, es = 0.0f;
-    if (on) {
-      ld8(x + at, v);
-      ld8(d_xd + at, a);
-      ld8(d_xm + at, b);
-      if (d_out) ld8(d_out + at, o);
+    r.x = ld_raw(x + at);
+    r.a = ld_raw(d_xd + at);
+    r.b = ld_raw(d_xm + at);
+    if (d_add) r.z = ld_raw(d_add + at);
+    if (d_out) r.o = ld_raw(d_out + at);
+  };
+  int flip = 0;
+  const int mine = (blockIdx.x * groups + g) * R;
 #pragma unroll
-      for (int j = 0; j < 8; ++j) o[j] *= scalar;
-      if (d_add) {
-        float z[8];
-        ld8(d_add + at, z);
+  for (int i = 0; i < R; ++i) load(mine + i, next[i]);
+  for (int t0 = blockIdx.x * groups * R; t0 < T; t0 += step) {  // the same for every group
+    const int t = t0 + g * R;
+    float v[R][8], a[R][8], b[R][8], o[R][8], sum[2 * R];
 #pragma unroll
-        for (int j = 0; j < 8; ++j) o[j] += z[j];
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) v[i][j] = a[i][j] = b[i][j] = o[i][j] = 0.0f;
+      if (live(t + i)) {
+        widen(next[i].x, v[i]);
+        widen(next[i].a, a[i]);
+        widen(next[i].b, b[i]);
+        if (d_out) widen(next[i].o, o[i]);
+#pragma unroll
+        for (int j = 0; j < 8; ++j) o[i][j] *= scalar;
+        if (d_add) {
+          float z[8];
+          widen(next[i].z, z);
+#pragma unroll
+          for (int j = 0; j < 8; ++j) o[i][j] += z[j];
+        }
+      }
+      load(t + step + i, next[i]);
+      sum[2 * i] = sum[2 * i + 1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        sum[2 * i] += v[i][j] * v[i][j];
+        sum[2 * i + 1] += (a[i][j] * w1[j] + b[i][j] * w2[j]) * v[i][j];
       }
     }
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      ss += v[j] * v[j];
-      es += (a[j] * w1[j] + b[j] * w2[j]) * v[j];
-    }
-    block_sum2(ss, es, red[flip]);
+    group_sums(sum, red[flip], g, w, nw);
     flip ^= 1;
-    const float r = 1.0f / sqrtf(ss / (float)H + eps);
-    const float m = r * es / (float)H;  // mean(e n)
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float n = v[j] * r;
-      s1[j] += a[j] * n;
-      s2[j] += b[j] * n;
-      o[j] += r * (a[j] * w1[j] + b[j] * w2[j] - n * m);
+    for (int i = 0; i < R; ++i) {
+      const float r = 1.0f / sqrtf(sum[2 * i] / (float)H + eps);
+      const float m = r * sum[2 * i + 1] / (float)H;  // mean(e n)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n = v[i][j] * r;
+        s[0][j] += a[i][j] * n;
+        s[1][j] += b[i][j] * n;
+        o[i][j] += r * (a[i][j] * w1[j] + b[i][j] * w2[j] - n * m);
+      }
+      // zeros where the token does not count
+      if (on && t + i < T) st8(d_x + (size_t)(t + i) * H + c, o[i]);
     }
-    if (on) st8(d_x + at, o);
   }
-  if (on) {
-    st8(part + (size_t)blockIdx.x * 2 * H + c, s1);
-    st8(part + ((size_t)blockIdx.x * 2 + 1) * H + c, s2);
-  }
+  write_sums<2>(s, H, c, on, g, groups, lds, part + (size_t)blockIdx.x * 2 * H);
 }
 
-template <typename XT, typename YT>
-__global__ __launch_bounds__(1024) void post_grad_kernel(
-    int T, int H, float eps, float scalar, const XT* __restrict__ x, const YT* __restrict__ dn,
-    const YT* __restrict__ moe_sum, const float* __restrict__ g1, const float* __restrict__ g2,
-    const float* __restrict__ g3, const uint8_t* __restrict__ mask, const XT* __restrict__ d_out,
-    XT* __restrict__ d_dn, XT* __restrict__ d_moe, float* __restrict__ part,
-    double* __restrict__ part_scalar) {
-  __shared__ float red[2][32];
+template <typename XT, typename YT, int MAXT>
+__global__ __launch_bounds__(MAXT) void post_grad_kernel(
+    int T, int H, int groups, float eps, float scalar, const XT* __restrict__ x,
+    const YT* __restrict__ dn, const YT* __restrict__ moe_sum, const float* __restrict__ g1,
+    const float* __restrict__ g2, const float* __restrict__ g3, const uint8_t* __restrict__ mask,
+    const XT* __restrict__ d_out, XT* __restrict__ d_dn, XT* __restrict__ d_moe,
+    float* __restrict__ part, double* __restrict__ part_scalar) {
+  constexpr int R = MAXT > 512 ? 1 : 2;
+  extern __shared__ __align__(16) float lds[];
+  __shared__ __align__(16) float red[2][2 * R * 16];
   __shared__ double dred[16];
-  const int c = threadIdx.x * 8;
+  const int nt = blockDim.x / groups, nw = nt / kWave;
+  const int g = threadIdx.x / nt, c = threadIdx.x % nt * 8, w = threadIdx.x % nt / kWave;
   const bool on = c < H;
-  float w1[8] = {}, w2[8] = {}, w3[8] = {}, s1[8] = {}, s2[8] = {}, s3[8] = {};
+  float w1[8] = {}, w2[8] = {}, w3[8] = {}, sg[3][8] = {};
   double ds = 0.0;
   if (on) {
     ld8(g1 + c, w1);
@@ -142,115 +228,136 @@ __global__ __launch_bounds__(1024) void post_grad_kernel(
     ld8(g3 + c, w3);
   }
   const float inv = 1.0f / (float)H;
-  int flip = 0;
-  for (int t = blockIdx.x; t < T; t += gridDim.x) {
+  const int step = gridDim.x * groups * R;
+  auto live = [&](int t) { return on && t < T && !(mask && !mask[t]); };
+  struct Row { Raw8<YT> a, b; Raw8<XT> d, x; } next[R];
+  auto load = [&](int t, Row& r) {
+    if (!live(t)) return;
     const size_t at = (size_t)t * H + c;
-    if (mask && !mask[t]) {
-      const float z[8] = {};
-      if (on) {
-        st8(d_dn + at, z);
-        st8(d_moe + at, z);
+    r.a = ld_raw(dn + at);
+    r.b = ld_raw(moe_sum + at);
+    r.d = ld_raw(d_out + at);
+    if (part_scalar) r.x = ld_raw(x + at);
+  };
+  int flip = 0;
+  const int mine = (blockIdx.x * groups + g) * R;
+#pragma unroll
+  for (int i = 0; i < R; ++i) load(mine + i, next[i]);
+  for (int t0 = blockIdx.x * groups * R; t0 < T; t0 += step) {
+    const int t = t0 + g * R;
+    float a[R][8], b[R][8], d[R][8], xv[R][8], s[R][8], sum[2 * R], r1[R], r2[R];
+#pragma unroll
+    for (int i = 0; i < R; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) a[i][j] = b[i][j] = d[i][j] = xv[i][j] = 0.0f;
+      if (live(t + i)) {
+        widen(next[i].a, a[i]);
+        widen(next[i].b, b[i]);
+        widen(next[i].d, d[i]);
+        if (part_scalar) widen(next[i].x, xv[i]);
       }
-      continue;
-    }
-    float a[8] = {}, b[8] = {}, d[8] = {}, xv[8] = {};
-    if (on) {
-      ld8(dn + at, a);
-      ld8(moe_sum + at, b);
-      ld8(d_out + at, d);
-      if (part_scalar) ld8(x + at, xv);
-    }
-    float sa = 0.0f, sb = 0.0f;
+      load(t + step + i, next[i]);
+      sum[2 * i] = sum[2 * i + 1] = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      sa += a[j] * a[j];
-      sb += b[j] * b[j];
+      for (int j = 0; j < 8; ++j) {
+        sum[2 * i] += a[i][j] * a[i][j];
+        sum[2 * i + 1] += b[i][j] * b[i][j];
+      }
     }
-    block_sum2(sa, sb, red[flip]);
+    group_sums(sum, red[flip], g, w, nw);
     flip ^= 1;
-    const float r1 = 1.0f / sqrtf(sa * inv + eps), r2 = 1.0f / sqrtf(sb * inv + eps);
-    float s[8], e3[8], ss = 0.0f, es = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] *= r1;  // n1, n2 from here on
-      b[j] *= r2;
-      s[j] = a[j] * w1[j] + b[j] * w2[j];
-      e3[j] = d[j] * scalar * w3[j];
-      ss += s[j] * s[j];
-      es += e3[j] * s[j];
+    for (int i = 0; i < R; ++i) {
+      r1[i] = 1.0f / sqrtf(sum[2 * i] * inv + eps);
+      r2[i] = 1.0f / sqrtf(sum[2 * i + 1] * inv + eps);
+      sum[2 * i] = sum[2 * i + 1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[i][j] *= r1[i];  // n1, n2 from here on
+        b[i][j] *= r2[i];
+        s[i][j] = a[i][j] * w1[j] + b[i][j] * w2[j];
+        sum[2 * i] += s[i][j] * s[i][j];
+        sum[2 * i + 1] += d[i][j] * w3[j] * s[i][j];
+      }
     }
-    block_sum2(ss, es, red[flip]);
+    group_sums(sum, red[flip], g, w, nw);
     flip ^= 1;
-    const float r3 = 1.0f / sqrtf(ss * inv + eps), m3 = r3 * es * inv;
-    float ea = 0.0f, eb = 0.0f;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      const float n3 = s[j] * r3;
-      s3[j] += d[j] * scalar * n3;
-      if (part_scalar) ds += (double)d[j] * (double)(n3 * w3[j] + xv[j]);
-      const float dsj = r3 * (e3[j] - n3 * m3);
-      s1[j] += dsj * a[j];
-      s2[j] += dsj * b[j];
-      s[j] = dsj;
-      ea += dsj * w1[j] * a[j];
-      eb += dsj * w2[j] * b[j];
+    for (int i = 0; i < R; ++i) {
+      const float r3 = 1.0f / sqrtf(sum[2 * i] * inv + eps), m3 = r3 * sum[2 * i + 1] * inv;
+      const float rs = r3 * scalar;
+      float row = 0.0f;  // of 8 products; the rows add up in fp64
+      sum[2 * i] = sum[2 * i + 1] = 0.0f;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const float n3 = s[i][j] * r3;
+        sg[2][j] += d[i][j] * n3;
+        row += d[i][j] * (n3 * w3[j] + xv[i][j]);
+        const float dsj = rs * (d[i][j] * w3[j] - n3 * m3);
+        sg[0][j] += dsj * a[i][j];
+        sg[1][j] += dsj * b[i][j];
+        s[i][j] = dsj * w1[j];  // e1, and e2 in d's place
+        d[i][j] = dsj * w2[j];
+        sum[2 * i] += s[i][j] * a[i][j];
+        sum[2 * i + 1] += d[i][j] * b[i][j];
+      }
+      ds += (double)row;
     }
-    block_sum2(ea, eb, red[flip]);
+    group_sums(sum, red[flip], g, w, nw);
     flip ^= 1;
-    const float m1 = ea * inv, m2 = eb * inv;
 #pragma unroll
-    for (int j = 0; j < 8; ++j) {
-      a[j] = r1 * (s[j] * w1[j] - a[j] * m1);
-      b[j] = r2 * (s[j] * w2[j] - b[j] * m2);
-    }
-    if (on) {
-      st8(d_dn + at, a);
-      st8(d_moe + at, b);
+    for (int i = 0; i < R; ++i) {
+      const float m1 = sum[2 * i] * inv, m2 = sum[2 * i + 1] * inv;
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        a[i][j] = r1[i] * (s[i][j] - a[i][j] * m1);
+        b[i][j] = r2[i] * (d[i][j] - b[i][j] * m2);
+      }
+      if (on && t + i < T) {
+        st8(d_dn + (size_t)(t + i) * H + c, a[i]);
+        st8(d_moe + (size_t)(t + i) * H + c, b[i]);
+      }
     }
   }
-  if (on) {
-    float* p = part + (size_t)blockIdx.x * 3 * H + c;
-    st8(p, s1);
-    st8(p + H, s2);
-    st8(p + 2 * (size_t)H, s3);
-  }
+#pragma unroll
+  for (int j = 0; j < 8; ++j) sg[2][j] *= scalar;
+  write_sums<3>(sg, H, c, on, g, groups, lds, part + (size_t)blockIdx.x * 3 * H);
   if (part_scalar) {
     ds = wave_sum(ds);
     if (lane_id() == 0) dred[threadIdx.x / kWave] = ds;
     __syncthreads();
     if (threadIdx.x == 0) {
       double v = 0.0;
-      for (int w = 0; w < (int)blockDim.x / kWave; ++w) v += dred[w];
+      for (int i = 0; i < (int)blockDim.x / kWave; ++i) v += dred[i];
       part_scalar[blockIdx.x] = v;
     }
   }
 }
 
-// out_i[c] = sum over blocks of part[block][i][c], in order within a lane's run of
-// blocks, the 16 runs in order.  A block takes 16 columns of n arrays end to end.
-__global__ __launch_bounds__(256) void sum_parts_kernel(int nb, int n, int H,
-                                                        const float* __restrict__ part,
-                                                        float* o1, float* o2, float* o3,
-                                                        const double* __restrict__ part_scalar,
-                                                        float* d_scalar) {
-  __shared__ float red[16][17];
-  const int tc = threadIdx.x % 16, tr = threadIdx.x / 16;
-  if ((int)blockIdx.x == n * H / 16) {  // the block past the columns: the scalar
-    __shared__ double dred[256];
+// out_i[c] = sum over blocks of part[block][i][c]: 16 lanes' runs of blocks, each in
+// order, added in order.  A block takes 64 columns of the n arrays end to end (H is a
+// multiple of 64); the one past the columns adds the scalar's parts.
+__global__ __launch_bounds__(1024) void sum_parts_kernel(int nb, int n, int H,
+                                                         const float* __restrict__ part,
+                                                         float* o1, float* o2, float* o3,
+                                                         const double* __restrict__ part_scalar,
+                                                         float* d_scalar) {
+  const int tc = threadIdx.x % 64, tr = threadIdx.x / 64;
+  if ((int)blockIdx.x == n * H / 64) {
     double v = 0.0;
-    for (int b = threadIdx.x; b < nb; b += 256) v += part_scalar[b];
-    dred[threadIdx.x] = v;
-    __syncthreads();
-    if (threadIdx.x == 0) {
-      v = 0.0;
-      for (int i = 0; i < 256; ++i) v += dred[i];
-      *d_scalar = (float)v;
+    if (threadIdx.x < 64) {
+      for (int b = threadIdx.x; b < nb; b += 64) v += part_scalar[b];
+      v = wave_sum(v);
+      if (threadIdx.x == 0) *d_scalar = (float)v;
     }
     return;
   }
-  const int col = blockIdx.x * 16 + tc;
+  __shared__ float red[16][64];
+  const int col = blockIdx.x * 64 + tc;
+  const float* p = part + col;
   float v = 0.0f;
-  for (int b = tr; b < nb; b += 16) v += part[(size_t)b * n * H + col];
+#pragma unroll 8
+  for (int b = tr; b < nb; b += 16) v += p[(size_t)b * n * H];
   red[tr][tc] = v;
   __syncthreads();
   if (tr == 0) {
@@ -262,50 +369,60 @@ __global__ __launch_bounds__(256) void sum_parts_kernel(int nb, int n, int H,
   }
 }
 
+// Threads of a row's group, groups of a block, LDS of a block that adds n arrays.
 int threads_of(int H) { return (H / 8 + kWave - 1) / kWave * kWave; }
+int groups_of(int H) { return threads_of(H) > 512 ? 1 : 512 / threads_of(H); }
+size_t lds_of(int H, int n) { return groups_of(H) > 1 ? (size_t)n * H * 4 : 0; }
+int blocks_of(int T, int H) {
+  const int rows = groups_of(H) * (threads_of(H) > 512 ? 1 : 2), b = (T + rows - 1) / rows;
+  return b < kNormsBlocks ? b : kNormsBlocks;
+}
 
 }  // namespace
 
-int norms_grad_blocks(int T) { return T < 512 ? T : 512; }
-
-hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s) {
-  const int nb = norms_grad_blocks(a.T);
-  if (nb > 0) {
-    if (a.bf16)
-      hipLaunchKernelGGL(pre_grad_kernel<bf16>, dim3(nb), dim3(threads_of(a.H)), 0, s, a.T, a.H,
-                         a.eps, a.scalar, static_cast<const bf16*>(a.x), a.g1, a.g2, a.mask,
-                         static_cast<const bf16*>(a.d_xd), static_cast<const bf16*>(a.d_xm),
-                         static_cast<const bf16*>(a.d_add), static_cast<const bf16*>(a.d_out),
-                         static_cast<bf16*>(a.d_x), a.ws_part);
-    else
-      hipLaunchKernelGGL(pre_grad_kernel<float>, dim3(nb), dim3(threads_of(a.H)), 0, s, a.T, a.H,
-                         a.eps, a.scalar, static_cast<const float*>(a.x), a.g1, a.g2, a.mask,
-                         static_cast<const float*>(a.d_xd), static_cast<const float*>(a.d_xm),
-                         static_cast<const float*>(a.d_add), static_cast<const float*>(a.d_out),
-                         static_cast<float*>(a.d_x), a.ws_part);
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
-  hipLaunchKernelGGL(sum_parts_kernel, dim3(2 * a.H / 16), dim3(256), 0, s, nb, 2, a.H, a.ws_part,
-                     a.d_g1, a.d_g2, nullptr, nullptr, nullptr);
-  return hipGetLastError();
-}
+int norms_grad_blocks(int T, int H) { return blocks_of(T, H); }
 
 namespace {
 
+template <typename XT>
+void launch_pre(const PreNormGradArgs& a, int nb, hipStream_t s) {
+  auto kf = threads_of(a.H) > 512 ? pre_grad_kernel<XT, 1024> : pre_grad_kernel<XT, 512>;
+  hipLaunchKernelGGL(kf, dim3(nb), dim3(threads_of(a.H) * groups_of(a.H)),
+                     lds_of(a.H, 2), s, a.T, a.H, groups_of(a.H), a.eps, a.scalar,
+                     static_cast<const XT*>(a.x), a.g1, a.g2, a.mask,
+                     static_cast<const XT*>(a.d_xd), static_cast<const XT*>(a.d_xm),
+                     static_cast<const XT*>(a.d_add), static_cast<const XT*>(a.d_out),
+                     static_cast<XT*>(a.d_x), a.ws_part);
+}
+
 template <typename XT, typename YT>
 void launch_post(const PostNormGradArgs& a, int nb, hipStream_t s) {
-  hipLaunchKernelGGL((post_grad_kernel<XT, YT>), dim3(nb), dim3(threads_of(a.H)), 0, s, a.T, a.H,
-                     a.eps, a.scalar, static_cast<const XT*>(a.x), static_cast<const YT*>(a.dn),
-                     static_cast<const YT*>(a.moe_sum), a.g1, a.g2, a.g3, a.mask,
-                     static_cast<const XT*>(a.d_out), static_cast<XT*>(a.d_dn),
+  auto kf = threads_of(a.H) > 512 ? post_grad_kernel<XT, YT, 1024> : post_grad_kernel<XT, YT, 512>;
+  hipLaunchKernelGGL(kf, dim3(nb),
+                     dim3(threads_of(a.H) * groups_of(a.H)), lds_of(a.H, 3), s, a.T, a.H,
+                     groups_of(a.H), a.eps, a.scalar, static_cast<const XT*>(a.x),
+                     static_cast<const YT*>(a.dn), static_cast<const YT*>(a.moe_sum), a.g1, a.g2,
+                     a.g3, a.mask, static_cast<const XT*>(a.d_out), static_cast<XT*>(a.d_dn),
                      static_cast<XT*>(a.d_moe), a.ws_part, a.d_scalar ? a.ws_scalar : nullptr);
 }
 
 }  // namespace
 
+hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s) {
+  const int nb = blocks_of(a.T, a.H);
+  if (nb > 0) {
+    if (a.bf16) launch_pre<bf16>(a, nb, s);
+    else launch_pre<float>(a, nb, s);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(sum_parts_kernel, dim3(2 * a.H / 64), dim3(1024), 0, s, nb, 2, a.H, a.ws_part,
+                     a.d_g1, a.d_g2, nullptr, nullptr, nullptr);
+  return hipGetLastError();
+}
+
 hipError_t launch_post_norms_grad(const PostNormGradArgs& a, hipStream_t s) {
-  const int nb = norms_grad_blocks(a.T);
+  const int nb = blocks_of(a.T, a.H);
   if (nb > 0) {
     if (!a.bf16) launch_post<float, float>(a, nb, s);
     else if (a.y_bf16) launch_post<bf16, bf16>(a, nb, s);
@@ -313,7 +430,7 @@ hipError_t launch_post_norms_grad(const PostNormGradArgs& a, hipStream_t s) {
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(sum_parts_kernel, dim3(3 * a.H / 16 + (a.d_scalar ? 1 : 0)), dim3(256), 0, s,
+  hipLaunchKernelGGL(sum_parts_kernel, dim3(3 * a.H / 64 + (a.d_scalar ? 1 : 0)), dim3(1024), 0, s,
                      nb, 3, a.H, a.ws_part, a.d_g1, a.d_g2, a.d_g3, a.ws_scalar, a.d_scalar);
   return hipGetLastError();
 }
