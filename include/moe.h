@@ -252,8 +252,8 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
  * moe_router_grad, and gemma4_pre_norms_grad, which adds the router's and the
  * residual's gradient of x to its own.  Then moe_grad_norm and moe_grad_clip.
  * token_mask and T == 0 are as in the router's training calls above; sums run in
- * fp32 or more in an order fixed by the sizes; no output may overlap an input
- * unless it says so.
+ * fp32 or more in an order fixed by the sizes and the dispatch; no output may
+ * overlap an input or another output unless it says so.
  *
  * moe_expert_ffn_keep: moe_expert_ffn, with the projections as an output: row r
  * of gate_up [T*K, 2I] (act dtype) belongs to slot sorted_slots[r] of expert e
@@ -278,8 +278,8 @@ int moe_expert_ffn_keep(const moe_dims* dims, int32_t T, const void* x, const vo
  * where act_dtype is), overwritten, zero for an expert without rows.  Each output
  * may be NULL (not wanted), not all.  A slot that the dispatch dropped has a zero
  * in d_topk_w and takes part in nothing.  bf16 path: v, <v, h> and every sum in
- * fp32; [d_gate, d_up], w h and the slots' parts of d_x are rounded to bf16 in
- * between.  Workspace of its own size, as is every call's below that has one. */
+ * fp32; [d_gate, d_up], w h and, where slot_dtype is MOE_BF16, the slots' parts of
+ * d_x are rounded to bf16 in between.  Workspace of its own size, as is every call's below that has one. */
 size_t moe_expert_ffn_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
 int moe_expert_ffn_grad(const moe_dims* dims, int32_t T, const void* x, const void* w_gate_up,
                         const void* w_down, const float* topk_w, const int32_t* expert_offsets,
@@ -368,7 +368,8 @@ int moe_grad_norm(int32_t n, const moe_tensor* grads, float max_norm, float* nor
 
 /* out[i] = grads[i] * norm[1], norm as moe_grad_norm left it on the device; out
  * NULL: in place.  An out tensor may have another dtype than its gradient; it is
- * its gradient (same address and dtype) or overlaps nothing in either list. */
+ * its gradient (same address and dtype) or overlaps nothing in either list.  In
+ * place, no two tensors of the list overlap. */
 int moe_grad_clip(int32_t n, const moe_tensor* grads, const float* norm, const moe_tensor* out,
                   void* stream);
 

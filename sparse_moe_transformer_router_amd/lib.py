@@ -490,6 +490,7 @@ class GradList:
         for (_, end, i), (start, _, j) in zip(spans, spans[1:]):
             if start < end:
                 raise ValueError(f"tensors {i} and {j} overlap")
+        self.spans = spans
         self.n = len(self.tensors)
         self.array = (MoeTensor * self.n)(*[
             (t.data_ptr(), t.numel(), MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32)
@@ -523,11 +524,29 @@ def moe_grad_norm(grads: GradList, max_norm, norm, ws, stream=None):
                               _stream(stream, dev)))
 
 
+def _check_out(grads: GradList, out: GradList):
+    """out's tensors are their gradients or overlap none of them."""
+    if out.n != grads.n:
+        raise ValueError(f"out has {out.n} tensors, grads {grads.n}")
+    a, b = grads.spans, out.spans
+    if not a or not b or a[-1][1] <= b[0][0] or b[-1][1] <= a[0][0]:
+        return
+    i = j = 0
+    while i < len(a) and j < len(b):  # both ascending, neither overlapping itself
+        if a[i][0] < b[j][1] and b[j][0] < a[i][1] and not (
+                a[i] == b[j] and grads.tensors[a[i][2]].dtype == out.tensors[b[j][2]].dtype):
+            raise ValueError(f"out tensor {b[j][2]} overlaps gradient {a[i][2]}")
+        if a[i][1] <= b[j][1]:
+            i += 1
+        else:
+            j += 1
+
+
 def moe_grad_clip(grads: GradList, norm, out: Optional[GradList] = None, stream=None):
     """out (None: grads themselves) = grads * norm[1]."""
     dev = _device()
-    if out is not None and out.n != grads.n:
-        raise ValueError(f"out has {out.n} tensors, grads {grads.n}")
+    if out is not None and out is not grads:
+        _check_out(grads, out)
     _check(_lib.moe_grad_clip(grads.n, grads._on(dev),
                               _arg("norm", norm, torch.float32, 2, dev),
                               None if out is None else out._on(dev), _stream(stream, dev)))
