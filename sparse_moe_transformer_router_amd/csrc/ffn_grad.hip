@@ -16,9 +16,9 @@
 // Four grouped matrix products of 2 (S H I) to 4 (S H I) operations each, S rows.
 //
 // d_w comes from <v, h>, not from <d, W_d h>: it needs no expert output kept.
-// Rows are the expert-sorted slots of the dispatch; row_tok maps a row to its
-// token, -1 where the token does not count: such a row enters every product as
-// zeros, whatever its token's data hold.
+// Rows are the expert-sorted slots of the dispatch (the dense MLP's: the tokens).  A
+// row whose token does not count enters every product as zeros, whatever its token's
+// data hold.
 #include <type_traits>
 
 #include "common.h"
@@ -52,31 +52,6 @@ __device__ __forceinline__ void act_grad(float z, float up, float v, float& h, f
   h = gelu * up;
   dg = v * up * slope;
   du = v * gelu;
-}
-
-// Row r of the sorted order -> its token, -1 if the token does not count, and that
-// token's byte offset in a bf16 [T, H], kNowhere if it does not; slot -> its row.  A
-// slot that the dispatch dropped keeps whatever the workspace held: readers of
-// slot_row check that sorted_slots points back.
-__global__ __launch_bounds__(256) void rows_kernel(int rows, int ident, int E, int K,
-                                                   const int32_t* __restrict__ offsets,
-                                                   const int32_t* __restrict__ sorted_slots,
-                                                   const uint8_t* __restrict__ mask,
-                                                   unsigned row_bytes,
-                                                   int32_t* __restrict__ row_tok,
-                                                   unsigned* __restrict__ row_off,
-                                                   int32_t* __restrict__ slot_row) {
-  const int r = blockIdx.x * 256 + threadIdx.x;
-  if (r >= (ident ? rows : offsets[E])) return;
-  int tok = r;
-  if (!ident) {
-    const int slot = sorted_slots[r];
-    slot_row[slot] = r;
-    tok = slot / K;
-  }
-  if (mask && !mask[tok]) tok = -1;
-  row_tok[r] = tok;
-  row_off[r] = tok < 0 ? kNowhere : (unsigned)tok * row_bytes;
 }
 
 // d_x[t] = sum over t's slots (k ascending) of their rows of d_xs, in fp32;
@@ -141,9 +116,10 @@ __global__ __launch_bounds__(256) void combine_grad_kernel(
 struct Operands {
   int T, H, I, E, K, rows, ident;
   const int32_t* offsets;
-  const int32_t* row_tok;
-  const unsigned* row_off;
   const int32_t* sorted_slots;
+  const uint8_t* mask;
+  unsigned* row_off;    // row -> its token's byte offset in x and d_out, or kNowhere
+  int32_t* slot_row;    // slot -> its row
   const float* topk_w;
   const void* x;        // [T, H]
   const void* d_out;    // [T, H]
@@ -160,6 +136,24 @@ struct Operands {
   void* d_up;
   void* d_down;         // DWDN: group 0's [H, I]
 };
+
+// The token of a row, -1 if it does not count.
+__device__ __forceinline__ int token_of(const Operands& o, int row) {
+  const int tok = o.ident ? row : o.sorted_slots[row] / o.K;
+  return o.mask && !o.mask[tok] ? -1 : tok;
+}
+
+// DU writes the tables that the later kernels read, a row tile's by its first block.  A
+// slot that the dispatch dropped keeps whatever the workspace held: readers of slot_row
+// check that sorted_slots points back.
+__device__ __forceinline__ void write_tables(const Operands& o, int row0, int row1,
+                                             unsigned row_bytes) {
+  for (int r = row0 + threadIdx.x; r < row1; r += blockDim.x) {
+    const int tok = token_of(o, r);
+    o.row_off[r] = tok < 0 ? kNowhere : (unsigned)tok * row_bytes;
+    if (!o.ident) o.slot_row[o.sorted_slots[r]] = r;
+  }
+}
 
 // ---------------------------------------------------------------------------
 // bf16: tiles on v_mfma_f32_32x32x16_bf16
@@ -277,6 +271,16 @@ __device__ __forceinline__ void buffer_copy16(i32x4 buf, unsigned off, unsigned 
                : "v"(off), "s"(buf), "s"(m0)
                : "memory", "m0");
 }
+// `at`: bytes that all lanes add
+__device__ __forceinline__ void buffer_copy16(i32x4 buf, unsigned off, unsigned at,
+                                              unsigned lds) {
+  const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
+  const unsigned so = __builtin_amdgcn_readfirstlane(at);
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 4\n\tbuffer_load_dwordx4 %0, %1, %3 offen lds"
+               :
+               : "v"(off), "s"(buf), "s"(m0), "s"(so)
+               : "memory", "m0");
+}
 __device__ __forceinline__ void global_copy16(const void* base, unsigned off, unsigned lds) {
   const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1"
@@ -342,13 +346,12 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TL::TM][TL::TN]) {
 // in an epilogue that reads the kept projections and writes three times as much; the
 // second block of the CU multiplies meanwhile.
 template <int KIND, typename WT, typename TL, int KS>
-__global__ __launch_bounds__(64 * TL::NW * KS, (TL::BLOCKS * TL::NW * KS + 3) / 4) void
-grad_rows_kernel(Operands o, int NT) {
+__device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
+                                           unsigned char* smem) {
   constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, ST = TL::ST, WN = TL::WN;
   constexpr int TM = TL::TM, TN = TL::TN, NF = TL::NF, NMF = TL::NMF, WR = TL::WR, WC = TL::WC;
   constexpr int CA = TL::CA, LPW = TL::LPW;
   static_assert(KS == 1 || NW == 1, "groups of several waves would wait for each other");
-  extern __shared__ __align__(16) unsigned char smem[];
 
   const int H = o.H, I = o.I;
   const int Nout = KIND == kDU ? I : H;
@@ -362,7 +365,7 @@ grad_rows_kernel(Operands o, int NT) {
       row_tile_scan(o.offsets, o.E, BM, sc);
       R = sc.total;
     }
-    const int item = xcd_item(blockIdx.x, R * NT);
+    const int item = xcd_item(block, R * NT);
     if (item < 0) return;  // uniform over the block
     if (o.ident) {
       nt = item % NT;
@@ -382,16 +385,20 @@ grad_rows_kernel(Operands o, int NT) {
   const int wm = wave / WN, wn = wave % WN, fr = lane % 32, fq = lane / 32;
   const int n0 = nt * BN;
 
+  if (KIND == kDU && nt == 0) write_tables(o, row0, row1, 2u * (unsigned)H);
+
   // This lane's copies of a k-tile, CA of A and CB of B: byte offsets from bases
-  // that all lanes share.  A row past the tile reads a valid one, a token that does
-  // not count reads token 0: outputs dropped and replaced in the epilogue.
-  unsigned off[LPW];
-  const bf16 *pA, *pB, *pU = nullptr;
+  // that all lanes share.  A row past the tile and a token that does not count lie
+  // outside A's descriptor: zeros, and no traffic.
+  unsigned off[LPW], atA = 0;
+  const bf16 *pB, *pU = nullptr;
+  i32x4 bufA;
   if constexpr (KIND == kDU) {
-    pA = static_cast<const bf16*>(o.d_out);
+    bufA = buffer_of(o.d_out, (unsigned)o.T * 2u * (unsigned)H);
     pB = static_cast<const bf16*>(o.w_down) + (size_t)e * o.dn_stride;
   } else {
-    pA = static_cast<const bf16*>(o.d_gu) + (size_t)row0 * 2 * I;
+    bufA = buffer_of(static_cast<const bf16*>(o.d_gu) + (size_t)row0 * 2 * I,
+                     (unsigned)(row1 - row0) * 4u * (unsigned)I);
     pB = static_cast<const bf16*>(o.w_gate) + (size_t)e * o.gu_stride;
     pU = static_cast<const bf16*>(o.w_up) + (size_t)e * o.gu_stride;
   }
@@ -399,10 +406,13 @@ grad_rows_kernel(Operands o, int NT) {
   for (int j = 0; j < LPW; ++j) {
     if (j < CA) {
       const int r = 16 * (wave * CA + j) + lane / 4;
-      const int gr = row0 + r < row1 ? r : 0;
-      const unsigned at = KIND == kDU ? (unsigned)max(o.row_tok[row0 + gr], 0) * (unsigned)(2 * H)
-                                      : (unsigned)gr * (unsigned)(4 * I);
-      off[j] = at + rswz(r, lane % 4) * 16;
+      if constexpr (KIND == kDU) {
+        const int tok = row0 + r < row1 ? token_of(o, row0 + r) : -1;
+        off[j] = tok < 0 ? kNowhere : (unsigned)tok * (unsigned)(2 * H) + rswz(r, lane % 4) * 16;
+      } else {
+        off[j] = row0 + r < row1 ? (unsigned)r * (unsigned)(4 * I) + rswz(r, lane % 4) * 16
+                                 : kNowhere;
+      }
     } else {
       const int k = TL::SB * (wave * TL::CB + j - CA) + lane / TL::LB;
       const int c = n0 + cswz(k, lane % TL::LB / 2, BN) * 16 + (lane & 1) * 8;
@@ -412,19 +422,19 @@ grad_rows_kernel(Operands o, int NT) {
   // this group's k-tiles
   const int nk_all = (KIND == kDU ? H : 2 * I) / GK, first = grp * nk_all / KS;
   const int nk = (grp + 1) * nk_all / KS - first;
-  // pA, pB: the k-tile that is being copied; `turn` k-tiles before pB goes on to the
+  // atA, pB: the k-tile that is being copied; `turn` k-tiles before pB goes on to the
   // up rows
   int turn = KIND == kDX ? I / GK - first : -1;
-  pA += first * GK;
+  atA += first * GK * 2;
   if (KIND == kDX && turn <= 0) pB = pU + (size_t)(-turn) * GK * Nout;
   else pB += (size_t)first * GK * Nout;
   const unsigned ldsA = base + wave * CA * 1024, ldsB = base + TL::A_BYTES + wave * TL::CB * 1024;
   auto copy = [&](int j, unsigned st) {
-    if (j < CA) global_copy16(pA, off[j], ldsA + st + j * 1024);
+    if (j < CA) buffer_copy16(bufA, off[j], atA, ldsA + st + j * 1024);
     else global_copy16(pB, off[j], ldsB + st + (j - CA) * 1024);
   };
   auto copied = [&]() {
-    pA += GK;
+    atA += GK * 2;
     pB += (size_t)GK * Nout;
     if (KIND == kDX && --turn == 0) pB = pU;
   };
@@ -609,7 +619,7 @@ grad_rows_kernel(Operands o, int NT) {
         } else {
           float dot = 0.0f;
           if (row < row1 && col < I) {
-            const bool live = o.row_tok[row] >= 0;
+            const bool live = token_of(o, row) >= 0;
             const float w = o.ident ? 1.0f : o.topk_w[o.sorted_slots[row]];
             const bf16x8 g = *reinterpret_cast<const bf16x8*>(kept + (size_t)row * 2 * I + col);
             const bf16x8 u =
@@ -664,6 +674,13 @@ grad_rows_kernel(Operands o, int NT) {
   }
 }
 
+template <int KIND, typename WT, typename TL, int KS>
+__global__ __launch_bounds__(64 * TL::NW * KS, (TL::BLOCKS * TL::NW * KS + 3) / 4) void
+grad_rows_kernel(Operands o, int NT) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  rows_block<KIND, WT, TL, KS>(o, NT, blockIdx.x, smem);
+}
+
 // First tile of the weights' gradients (tpe an expert) that XCD x takes, x = 8: all
 // of them.  A tile costs its k-tiles and kTileEnds more for its ends; XCD x starts at
 // the first tile that x / 8 of the whole cost lies before.
@@ -713,8 +730,8 @@ __device__ __forceinline__ int first_tile(const Operands& o, int tpe, int x) {
 // the rows' tokens: x, d_out).  Both are copied through descriptors, whose range
 // check gives zeros for rows past the expert's and for tokens that do not count.
 template <int KIND, typename WT, typename TL>
-__global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void
-grad_weights_kernel(Operands o, int MT, int NT) {
+__device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT, int block,
+                                              int blocks, unsigned char* smem) {
   constexpr int ST = TL::ST, WN = TL::WN, NW = TL::NW;
   constexpr int TM = TL::TM, TN = TL::TN, NF = TL::NF, NMF = TL::NMF, WR = TL::WR, WC = TL::WC;
   constexpr int CA = TL::CA, CB = TL::CB, LPW = TL::LPW;
@@ -723,7 +740,6 @@ grad_weights_kernel(Operands o, int MT, int NT) {
   constexpr int NS = TM * TN * (F32 ? 4 : 2);  // stores of a tile's results a wave
   constexpr int KW = GK / NW;         // k rows that a wave copies of each operand
   static_assert(TL::SA * CA == KW && TL::SB * CB == KW && (KW & (KW - 1)) == 0, "k rows a wave");
-  extern __shared__ __align__(16) unsigned char smem[];
   const unsigned base = lds_offset(smem);
   const int H = o.H, I = o.I;
   const int M = KIND == kDWGU ? 2 * I : H, N = KIND == kDWGU ? H : I;
@@ -733,9 +749,9 @@ grad_weights_kernel(Operands o, int MT, int NT) {
   // This block's tiles: every nb-th of its XCD's range (neighbours share operands).
   // The ranges split the tiles by their k-tiles, not by their number: experts differ
   // by more than ten in their rows, sixteen of them together by a fifth.
-  const int nb = gridDim.x / 8;
-  const int end = first_tile(o, MT * NT, blockIdx.x % 8 + 1);
-  int c_it = first_tile(o, MT * NT, blockIdx.x % 8) + blockIdx.x / 8;
+  const int nb = blocks / 8;
+  const int end = first_tile(o, MT * NT, block % 8 + 1);
+  int c_it = first_tile(o, MT * NT, block % 8) + block / 8;
 
   const_int* offsets = (const_int*)o.offsets;
   const_int* row_off_tab = (const_int*)o.row_off;
@@ -1000,6 +1016,13 @@ grad_weights_kernel(Operands o, int MT, int NT) {
   }
 }
 
+template <int KIND, typename WT, typename TL>
+__global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_weights_kernel(Operands o, int MT,
+                                                                                 int NT) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  weights_block<KIND, WT, TL>(o, MT, NT, blockIdx.x, gridDim.x, smem);
+}
+
 // ---------------------------------------------------------------------------
 // fp32 (debug path): BM x 64 tiles on the vector ALUs
 // ---------------------------------------------------------------------------
@@ -1010,32 +1033,42 @@ template <int KIND>
 constexpr int f32_rows() { return KIND == kDWGU || KIND == kDWDN ? 64 : 32; }
 
 template <int KIND>
-__global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, int NT) {
+__device__ __forceinline__ void gemm_f32(const Operands& o, int block, int MT, int NT,
+                                         float (*As)[68], float (*Bs)[FN + 4]) {
   constexpr bool DW = KIND == kDWGU || KIND == kDWDN;
   constexpr int BM = f32_rows<KIND>(), TM = BM / 16;
   constexpr int NA = BM * FK / 4 / 256, NB = FN * FK / 4 / 256;  // 16-B loads a thread
-  __shared__ __align__(16) float As[FK][BM + 4], Bs[FK][FN + 4];
   const int H = o.H, I = o.I;
   const int Nout = KIND == kDU || KIND == kDWDN ? I : H;
   const int M = KIND == kDWGU ? 2 * I : H;
   int e = 0, row0, row1, m0 = 0;
-  const int nt = blockIdx.x % NT, n0 = nt * FN;
+  const int nt = block % NT, n0 = nt * FN;
   if constexpr (DW) {
-    e = blockIdx.x / (MT * NT);
-    m0 = blockIdx.x / NT % MT * BM;
+    e = block / (MT * NT);
+    m0 = block / NT % MT * BM;
     const bool all = o.ident || o.rows == 0;  // no rows: the offsets may not exist
     row0 = all ? 0 : o.offsets[e];
     row1 = all ? o.rows : o.offsets[e + 1];
   } else if (o.ident) {
-    row0 = blockIdx.x / NT * BM;
+    row0 = block / NT * BM;
     row1 = min(row0 + BM, o.rows);
-  } else if (!find_row_tile(o.offsets, o.E, BM, blockIdx.x / NT, e, row0, row1)) {
+  } else if (!find_row_tile(o.offsets, o.E, BM, block / NT, e, row0, row1)) {
     return;  // uniform over the block
   }
   const int tid = threadIdx.x, tr = tid / 16, tc = tid % 16;
   const float* d_out = static_cast<const float*>(o.d_out);
   const float* x = static_cast<const float*>(o.x);
   const float* kept = static_cast<const float*>(o.kept);
+  if (KIND == kDU && nt == 0) write_tables(o, row0, row1, 4u * (unsigned)H);
+  auto row_of = [&](const float* p, unsigned off) {  // a token's
+    return reinterpret_cast<const float*>(reinterpret_cast<const char*>(p) + off);
+  };
+  int toks[NA];  // DU: the tokens of this thread's rows
+#pragma unroll
+  for (int u = 0; u < NA && KIND == kDU; ++u) {
+    const int r = row0 + (threadIdx.x + 256 * u) / (FK / 4);
+    toks[u] = r < row1 ? token_of(o, r) : -1;
+  }
   float* d_gu = static_cast<float*>(o.d_gu);
   float* hw = static_cast<float*>(o.hw);
   const float* wg = static_cast<const float*>(o.w_gate) + (size_t)e * o.gu_stride;
@@ -1054,16 +1087,15 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
       if constexpr (DW) {
         const int k = k0 + i / (BM / 4), c = m0 + i % (BM / 4) * 4, r = row0 + k;
         if (k < Kd && c < M) {
-          const int tok = o.row_tok[r];
-          if (tok >= 0)
-            va[u] = ld4(KIND == kDWGU ? d_gu + (size_t)r * 2 * I + c : d_out + (size_t)tok * H + c);
+          const unsigned off = o.row_off[r];
+          if (off != kNowhere)
+            va[u] = ld4(KIND == kDWGU ? d_gu + (size_t)r * 2 * I + c : row_of(d_out, off) + c);
         }
       } else {
         const int r = row0 + i / (FK / 4), k = k0 + i % (FK / 4) * 4;  // Kd is a multiple of 32
         if (r < row1) {
           if constexpr (KIND == kDU) {
-            const int tok = o.row_tok[r];
-            if (tok >= 0) va[u] = ld4(d_out + (size_t)tok * H + k);
+            if (toks[u] >= 0) va[u] = ld4(d_out + (size_t)toks[u] * H + k);
           } else {
             va[u] = ld4(d_gu + (size_t)r * 2 * I + k);
           }
@@ -1080,9 +1112,10 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
       } else if constexpr (KIND == kDX) {
         vb[u] = ld4(k < I ? wg + (size_t)k * H + c : wu + (size_t)(k - I) * H + c);
       } else {
-        const int r = row0 + k, tok = o.row_tok[r];
-        if (tok >= 0)
-          vb[u] = ld4(KIND == kDWGU ? x + (size_t)tok * H + c : hw + (size_t)r * I + c);
+        const int r = row0 + k;
+        const unsigned off = o.row_off[r];
+        if (off != kNowhere)
+          vb[u] = ld4(KIND == kDWGU ? row_of(x, off) + c : hw + (size_t)r * I + c);
       }
     }
   };
@@ -1124,7 +1157,7 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
     if constexpr (KIND == kDU) {
       float dot = 0.0f;
       if (row < row1 && in) {
-        const bool live = o.row_tok[row] >= 0;
+        const bool live = token_of(o, row) >= 0;
         const float w = o.ident ? 1.0f : o.topk_w[o.sorted_slots[row]];
         const f32x4 g = ld4(kept + (size_t)row * 2 * I + col);
         const f32x4 u = ld4(kept + (size_t)row * 2 * I + I + col);
@@ -1168,6 +1201,22 @@ __global__ __launch_bounds__(256) void grad_gemm_f32_kernel(Operands o, int MT, 
   }
 }
 
+__global__ __launch_bounds__(256) void grad_du_f32_kernel(Operands o, int NT) {
+  __shared__ __align__(16) float As[FK][68], Bs[FK][FN + 4];
+  gemm_f32<kDU>(o, blockIdx.x, 0, NT, As, Bs);
+}
+
+// The other three, which need DU alone, in one launch.
+struct F32Tiles { int dx, dwgu, end; };  // first block behind DX's, behind DWGU's, of all
+__global__ __launch_bounds__(256) void grad_rest_f32_kernel(Operands o, F32Tiles n) {
+  __shared__ __align__(16) float As[FK][68], Bs[FK][FN + 4];
+  const int NH = (o.H + FN - 1) / FN, NI = (o.I + FN - 1) / FN;
+  const int b = blockIdx.x;
+  if (b < n.dx) gemm_f32<kDX>(o, b, 0, NH, As, Bs);
+  else if (b < n.dwgu) gemm_f32<kDWGU>(o, b - n.dx, (2 * o.I + 63) / 64, NH, As, Bs);
+  else gemm_f32<kDWDN>(o, b - n.dwgu, NH, NI, As, Bs);
+}
+
 // DU and DX: 128 x 256, two blocks of 8 waves a CU; DW: 256 x 256, one block of 8
 // waves, four stages (4096 tokens, DWGU / DWDN: 471 / 261 us; 128 x 256 in two blocks
 // of 4 waves a CU 484 / 277, waves of 64 x 128 496 / 269).
@@ -1179,6 +1228,25 @@ constexpr int kFewSplit = 8;
 // DW of small problems: 128 x 128, two blocks of 4 waves a CU.
 typedef Tile<128, 128, 2, 2, 3, 2> SmallWeightsTile;
 constexpr int kCUs = 256;
+
+
+// The dense MLP's DX, DWGU and DWDN in one launch: DX's blocks in the small form, then a
+// large tile a block.
+struct RestBlocks { int dx, gu, end; };  // behind DX's, behind DWGU's, all; multiples of 8
+template <typename WT>
+__global__ __launch_bounds__(512, 2) void grad_rest_kernel(Operands o, RestBlocks n) {
+  extern __shared__ __align__(16) unsigned char smem[];
+  constexpr int BM = WeightsTile::BM, BN = WeightsTile::BN;
+  const int b = blockIdx.x;
+  if (b < n.dx)
+    rows_block<kDX, bf16, FewTile, kFewSplit>(o, (o.H + FewTile::BN - 1) / FewTile::BN, b, smem);
+  else if (b < n.gu)
+    weights_block<kDWGU, WT, WeightsTile>(o, (2 * o.I + BM - 1) / BM, (o.H + BN - 1) / BN, b - n.dx,
+                                          n.gu - n.dx, smem);
+  else
+    weights_block<kDWDN, WT, WeightsTile>(o, (o.H + BM - 1) / BM, (o.I + BN - 1) / BN, b - n.gu,
+                                          n.end - n.gu, smem);
+}
 
 template <int KIND, typename WT, typename TL, int KS>
 hipError_t launch_rows(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
@@ -1225,14 +1293,6 @@ hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   constexpr bool DW = KIND == kDWGU || KIND == kDWDN;
   const int N = KIND == kDU || KIND == kDWDN ? a.I : a.H;
   const int M = KIND == kDWGU ? 2 * a.I : a.H;
-  if (!a.bf16) {
-    constexpr int BM = f32_rows<KIND>();
-    const int NT = (N + FN - 1) / FN, MT = (M + BM - 1) / BM;
-    const int tiles = DW ? o.E * MT * NT : tile_count_bound(a.ident, a.rows, a.T, a.E, BM) * NT;
-    if (tiles == 0) return hipSuccess;
-    hipLaunchKernelGGL(grad_gemm_f32_kernel<KIND>, dim3(tiles), dim3(256), 0, s, o, MT, NT);
-    return hipGetLastError();
-  }
   if constexpr (DW) {
     const int tiles = o.E * ((M + WeightsTile::BM - 1) / WeightsTile::BM) *
                       ((N + WeightsTile::BN - 1) / WeightsTile::BN);
@@ -1244,6 +1304,64 @@ hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
     if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit>(a, o, s);
     return launch_rows<KIND, WT, RowsTile, 1>(a, o, s);
   }
+}
+
+hipError_t launch_f32(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
+  const int RT = a.rows > 0 ? tile_count_bound(a.ident, a.rows, a.T, a.E, f32_rows<kDX>()) : 0;
+  const int NH = (a.H + FN - 1) / FN, NI = (a.I + FN - 1) / FN;
+  if (RT > 0) {
+    hipLaunchKernelGGL(grad_du_f32_kernel, dim3(RT * NI), dim3(256), 0, s, o, NI);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  F32Tiles n;
+  n.dx = a.d_x ? RT * NH : 0;
+  n.dwgu = n.dx + (a.d_gate ? o.E * ((2 * a.I + 63) / 64) * NH : 0);
+  n.end = n.dwgu + (a.d_down ? o.E * NH * NI : 0);
+  if (n.end == 0) return hipSuccess;
+  hipLaunchKernelGGL(grad_rest_f32_kernel, dim3(n.end), dim3(256), 0, s, o, n);
+  return hipGetLastError();
+}
+
+template <typename WT>
+hipError_t launch_rest(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
+  typedef WeightsTile W;
+  auto eights = [](int n) { return (n + 7) / 8 * 8; };
+  auto over = [](int n, int d) { return (n + d - 1) / d; };
+  RestBlocks n;
+  n.dx = eights(over(a.rows, FewTile::BM) * over(a.H, FewTile::BN));
+  n.gu = n.dx + (a.d_gate ? eights(over(2 * a.I, W::BM) * over(a.H, W::BN)) : 0);
+  n.end = n.gu + (a.d_down ? eights(over(a.H, W::BM) * over(a.I, W::BN)) : 0);
+  auto kf = grad_rest_kernel<WT>;
+  constexpr int wlds = W::RING + W::NW * W::WAVE_STAGING, rlds = FewTile::rows_lds<kFewSplit>();
+  constexpr int lds = wlds > rlds ? wlds : rlds;
+  static_assert(lds <= 160 * 1024 && W::NW == 8 && kFewSplit * FewTile::NW == 8, "one block shape");
+  static const hipError_t attr = hipFuncSetAttribute(
+      reinterpret_cast<const void*>(kf), hipFuncAttributeMaxDynamicSharedMemorySize, lds);
+  if (attr != hipSuccess) return attr;
+  hipLaunchKernelGGL(kf, dim3(n.end), dim3(512), lds, s, o, n);
+  return hipGetLastError();
+}
+
+hipError_t launch_bf16(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
+  hipError_t e;
+  if (a.rows > 0) {
+    if ((e = launch_gemm<kDU, bf16>(a, o, s)) != hipSuccess) return e;
+    if (a.ident && a.d_x && (a.d_gate || a.d_down) && small_rows(a, a.H))
+      return a.wgrad_bf16 ? launch_rest<bf16>(a, o, s) : launch_rest<float>(a, o, s);
+    if (a.d_x) {
+      e = a.ident || a.xs_bf16 ? launch_gemm<kDX, bf16>(a, o, s) : launch_gemm<kDX, float>(a, o, s);
+      if (e != hipSuccess) return e;
+    }
+  }
+  const bool b = a.wgrad_bf16;
+  if (a.d_gate && (e = b ? launch_gemm<kDWGU, bf16>(a, o, s) : launch_gemm<kDWGU, float>(a, o, s)) !=
+                      hipSuccess)
+    return e;
+  if (a.d_down && (e = b ? launch_gemm<kDWDN, bf16>(a, o, s) : launch_gemm<kDWDN, float>(a, o, s)) !=
+                      hipSuccess)
+    return e;
+  return hipSuccess;
 }
 
 template <typename XT, typename ST>
@@ -1266,42 +1384,22 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   Operands o{};
   o.T = a.T; o.H = a.H; o.I = a.I; o.E = a.ident ? 1 : a.E; o.K = a.K;
   o.rows = a.rows; o.ident = a.ident;
-  o.offsets = a.offsets; o.row_tok = a.ws_row_tok;
-  o.row_off = a.ws_row_off; o.sorted_slots = a.sorted_slots;
+  o.offsets = a.offsets; o.sorted_slots = a.sorted_slots; o.mask = a.mask;
+  o.row_off = a.ws_row_off; o.slot_row = a.ws_slot_row;
   o.topk_w = a.topk_w; o.x = a.x; o.d_out = a.d_out; o.kept = a.kept;
   o.w_gate = a.w_gate; o.w_up = a.w_up; o.w_down = a.w_down;
   o.gu_stride = a.gu_stride; o.dn_stride = a.dn_stride;
   o.d_gu = a.ws_d_gu; o.hw = a.ws_hw; o.part = a.d_topk_w ? a.ws_part : nullptr;
   o.d_xs = a.ident ? a.d_x : a.ws_d_xs;
   o.d_gate = a.d_gate; o.d_up = a.d_up; o.d_down = a.d_down;
-  hipError_t e;
-  if (a.rows > 0) {
-    hipLaunchKernelGGL(rows_kernel, dim3((a.rows + 255) / 256), dim3(256), 0, s, a.rows,
-                       (int)a.ident, a.E, a.K, a.offsets, a.sorted_slots, a.mask,
-                       2u * (unsigned)a.H, a.ws_row_tok, a.ws_row_off, a.ws_slot_row);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if ((e = launch_gemm<kDU, bf16>(a, o, s)) != hipSuccess) return e;
-    if (a.d_x) {
-      e = a.ident || a.xs_bf16 ? launch_gemm<kDX, bf16>(a, o, s) : launch_gemm<kDX, float>(a, o, s);
-      if (e != hipSuccess) return e;
-    }
-    if (!a.ident && (a.d_x || a.d_topk_w)) {
-      const int pn = !a.bf16 ? FN : small_rows(a, a.I) ? FewTile::BN : RowsTile::BN;
-      const int parts = (a.I + pn - 1) / pn;
-      if (!a.bf16) launch_combine_grad<float, float>(a, parts, s);
-      else if (a.xs_bf16) launch_combine_grad<bf16, bf16>(a, parts, s);
-      else launch_combine_grad<bf16, float>(a, parts, s);
-      if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-  }
-  const bool b = a.bf16 && a.wgrad_bf16;
-  if (a.d_gate && (e = b ? launch_gemm<kDWGU, bf16>(a, o, s) : launch_gemm<kDWGU, float>(a, o, s)) !=
-                      hipSuccess)
-    return e;
-  if (a.d_down && (e = b ? launch_gemm<kDWDN, bf16>(a, o, s) : launch_gemm<kDWDN, float>(a, o, s)) !=
-                      hipSuccess)
-    return e;
-  return hipSuccess;
+  hipError_t e = a.bf16 ? launch_bf16(a, o, s) : launch_f32(a, o, s);
+  if (e != hipSuccess || a.ident || a.rows == 0 || !(a.d_x || a.d_topk_w)) return e;
+  const int pn = !a.bf16 ? FN : small_rows(a, a.I) ? FewTile::BN : RowsTile::BN;
+  const int parts = (a.I + pn - 1) / pn;
+  if (!a.bf16) launch_combine_grad<float, float>(a, parts, s);
+  else if (a.xs_bf16) launch_combine_grad<bf16, bf16>(a, parts, s);
+  else launch_combine_grad<bf16, float>(a, parts, s);
+  return hipGetLastError();
 }
 
 }  // namespace moe

@@ -338,7 +338,6 @@ struct FfnGradArgs {
   void* d_gate;                  // or nullptr (with d_up)
   void* d_up;
   void* d_down;                  // or nullptr
-  int32_t* ws_row_tok;           // [rows]
   unsigned* ws_row_off;          // [rows + 32]
   int32_t* ws_slot_row;          // [rows]
   void* ws_d_gu;                 // [rows,2I]

@@ -189,13 +189,12 @@ B128Layout b128_layout(const moe_dims* d, long long T) {
 }
 
 // Backward pass of the gated block over `rows` rows of width I.
-struct FfnGradLayout { size_t row_tok, row_off, slot_row, d_gu, hw, d_xs, part, total; };
+struct FfnGradLayout { size_t row_off, slot_row, d_gu, hw, d_xs, part, total; };
 FfnGradLayout ffn_grad_layout(const moe_dims* d, long long rows, long long I, bool experts) {
   FfnGradLayout L{};
   const bool bf = d->act_dtype == MOE_BF16;
   const size_t act = dtype_size(d->act_dtype), S = (size_t)rows;
   size_t o = 0;
-  L.row_tok = region(o, 4 * S);
   L.row_off = region(o, 4 * (S + 32));
   L.slot_row = region(o, experts ? 4 * S : 0);
   L.d_gu = region(o, act * S * 2 * I);
@@ -562,7 +561,7 @@ int check_wgrad(const moe_dims* d, int32_t dt) {
 }
 
 void set_ffn_grad_ws(moe::FfnGradArgs& a, const FfnGradLayout& L, void* ws) {
-  a.ws_row_tok = at<int32_t>(ws, L.row_tok); a.ws_row_off = at<unsigned>(ws, L.row_off);
+  a.ws_row_off = at<unsigned>(ws, L.row_off);
   a.ws_slot_row = at<int32_t>(ws, L.slot_row);
   a.ws_d_gu = at<void>(ws, L.d_gu); a.ws_hw = at<void>(ws, L.hw);
   a.ws_d_xs = at<void>(ws, L.d_xs); a.ws_part = at<float>(ws, L.part);
