@@ -10,6 +10,7 @@ from __future__ import annotations
 
 import ctypes
 import os
+import weakref
 from typing import Optional
 
 import torch
@@ -491,6 +492,7 @@ class GradList:
             if start < end:
                 raise ValueError(f"tensors {i} and {j} overlap")
         self.spans = spans
+        self.fits = None  # the list whose gradients it was found to be outputs of
         self.n = len(self.tensors)
         self.array = (MoeTensor * self.n)(*[
             (t.data_ptr(), t.numel(), MOE_BF16 if t.dtype == torch.bfloat16 else MOE_F32)
@@ -545,8 +547,9 @@ def _check_out(grads: GradList, out: GradList):
 def moe_grad_clip(grads: GradList, norm, out: Optional[GradList] = None, stream=None):
     """out (None: grads themselves) = grads * norm[1]."""
     dev = _device()
-    if out is not None and out is not grads:
+    if out is not None and out is not grads and (out.fits is None or out.fits() is not grads):
         _check_out(grads, out)
+        out.fits = weakref.ref(grads)
     _check(_lib.moe_grad_clip(grads.n, grads._on(dev),
                               _arg("norm", norm, torch.float32, 2, dev),
                               None if out is None else out._on(dev), _stream(stream, dev)))
