@@ -288,11 +288,18 @@ __device__ __forceinline__ void global_copy16(const void* base, unsigned off, un
                : "v"(off), "s"(base), "s"(m0)
                : "memory", "m0");
 }
+template <bool PAST>
 __device__ __forceinline__ void buffer_store16(i32x4 buf, unsigned off, i32x4 v) {
-  asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1"
-               :
-               : "v"(v), "v"(off), "s"(buf)
-               : "memory");
+  if constexpr (PAST)  // past the caches
+    asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, 0 offen nt\n\ts_nop 1"
+                 :
+                 : "v"(v), "v"(off), "s"(buf)
+                 : "memory");
+  else
+    asm volatile("s_nop 4\n\tbuffer_store_dwordx4 %0, %1, %2, 0 offen\n\ts_nop 1"
+                 :
+                 : "v"(v), "v"(off), "s"(buf)
+                 : "memory");
 }
 
 // Fragment offsets of a wave within a stage.
@@ -729,7 +736,10 @@ __device__ __forceinline__ int first_tile(const Operands& o, int tpe, int x) {
 // An operand is "regular" (rows of the sorted order: d_gu, w h) or "gathered" (by
 // the rows' tokens: x, d_out).  Both are copied through descriptors, whose range
 // check gives zeros for rows past the expert's and for tokens that do not count.
-template <int KIND, typename WT, typename TL>
+// PAST: the results go past the caches, where they would be written back while later
+// kernels read (gradients of 1.5 GB, the next call's DU at 64 / 4096 tokens 96 / 280 us
+// against 154 / 313).
+template <int KIND, typename WT, typename TL, bool PAST>
 __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT, int block,
                                               int blocks, unsigned char* smem) {
   constexpr int ST = TL::ST, WN = TL::WN, NW = TL::NW;
@@ -984,7 +994,7 @@ __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT,
             const i32x4 v = {__float_as_int(acc[i][j][4 * q]), __float_as_int(acc[i][j][4 * q + 1]),
                              __float_as_int(acc[i][j][4 * q + 2]),
                              __float_as_int(acc[i][j][4 * q + 3])};
-            buffer_store16(buf, at, v);
+            buffer_store16<PAST>(buf, at, v);
           }
         } else {
           // 32 rows of SJ x 32 columns through the wave's own LDS, 16-B chunk q of row r
@@ -1005,7 +1015,7 @@ __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT,
               const int rr = RPS * h + lane / CPR, ch = lane % CPR;
               const i32x4 v = *reinterpret_cast<const i32x4*>(stg + place(rr, ch));
               const int cc = c - 32 * (SJ - 1) + ch * 8;
-              buffer_store16(buf, n0 + cc < N ? rr * ldo + cc * 2u : kNowhere, v);
+              buffer_store16<PAST>(buf, n0 + cc < N ? rr * ldo + cc * 2u : kNowhere, v);
             }
             asm volatile("" ::: "memory");
           }
@@ -1016,11 +1026,11 @@ __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT,
   }
 }
 
-template <int KIND, typename WT, typename TL>
+template <int KIND, typename WT, typename TL, bool PAST>
 __global__ __launch_bounds__(64 * TL::NW, TL::WAVES_EU) void grad_weights_kernel(Operands o, int MT,
                                                                                  int NT) {
   extern __shared__ __align__(16) unsigned char smem[];
-  weights_block<KIND, WT, TL>(o, MT, NT, blockIdx.x, gridDim.x, smem);
+  weights_block<KIND, WT, TL, PAST>(o, MT, NT, blockIdx.x, gridDim.x, smem);
 }
 
 // ---------------------------------------------------------------------------
@@ -1241,11 +1251,11 @@ __global__ __launch_bounds__(512, 2) void grad_rest_kernel(Operands o, RestBlock
   if (b < n.dx)
     rows_block<kDX, bf16, FewTile, kFewSplit>(o, (o.H + FewTile::BN - 1) / FewTile::BN, b, smem);
   else if (b < n.gu)
-    weights_block<kDWGU, WT, WeightsTile>(o, (2 * o.I + BM - 1) / BM, (o.H + BN - 1) / BN, b - n.dx,
-                                          n.gu - n.dx, smem);
+    weights_block<kDWGU, WT, WeightsTile, false>(o, (2 * o.I + BM - 1) / BM, (o.H + BN - 1) / BN,
+                                                 b - n.dx, n.gu - n.dx, smem);
   else
-    weights_block<kDWDN, WT, WeightsTile>(o, (o.H + BM - 1) / BM, (o.I + BN - 1) / BN, b - n.gu,
-                                          n.end - n.gu, smem);
+    weights_block<kDWDN, WT, WeightsTile, false>(o, (o.H + BM - 1) / BM, (o.I + BN - 1) / BN,
+                                                 b - n.gu, n.end - n.gu, smem);
 }
 
 template <int KIND, typename WT, typename TL, int KS>
@@ -1272,12 +1282,12 @@ bool small_rows(const FfnGradArgs& a, int N) {
              ((N + FewTile::BN - 1) / FewTile::BN) <= kCUs * 3 / 2;
 }
 
-template <int KIND, typename WT, typename TL>
+template <int KIND, typename WT, typename TL, bool PAST>
 hipError_t launch_weights(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   const int N = KIND == kDWDN ? a.I : a.H, M = KIND == kDWGU ? 2 * a.I : a.H;
   const int NT = (N + TL::BN - 1) / TL::BN, MT = (M + TL::BM - 1) / TL::BM;
   const int tiles = o.E * MT * NT;
-  auto kf = grad_weights_kernel<KIND, WT, TL>;
+  auto kf = grad_weights_kernel<KIND, WT, TL, PAST>;
   constexpr int lds = TL::RING + TL::NW * TL::WAVE_STAGING;
   static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
   static const hipError_t attr = hipFuncSetAttribute(
@@ -1298,12 +1308,36 @@ hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
                       ((N + WeightsTile::BN - 1) / WeightsTile::BN);
     // Up to half as many large tiles as CUs: the dense MLP's DWDN (99 tiles) at 301 / 4096
     // tokens 14.0 / 93 -> 10.7 / 63 us; its DWGU (187) 16.6 / 106, with small ones 16.0 / 121.
-    if (tiles <= kCUs / 2) return launch_weights<KIND, WT, SmallWeightsTile>(a, o, s);
-    return launch_weights<KIND, WT, WeightsTile>(a, o, s);
+    if (tiles <= kCUs / 2) return launch_weights<KIND, WT, SmallWeightsTile, false>(a, o, s);
+    // All three gradients, a quarter of the last cache or more: past it.  512 tokens x 2,
+    // 2816 x 704, the whole call with 8 / 16 / 32 experts (95 / 190 / 381 MB) 95 / 120 / 223
+    // us, through the caches 98 / 155 / 250; the dense MLP (36 MB) at 4096 tokens 366 and 363,
+    // and who reads them next finds them there.
+    const long long bytes = (long long)o.E * 3 * o.I * o.H * sizeof(WT);
+    if (bytes >= 64 << 20) return launch_weights<KIND, WT, WeightsTile, true>(a, o, s);
+    return launch_weights<KIND, WT, WeightsTile, false>(a, o, s);
   } else {
     if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit>(a, o, s);
     return launch_rows<KIND, WT, RowsTile, 1>(a, o, s);
   }
+}
+
+template <typename XT, typename ST>
+void launch_combine_grad(const FfnGradArgs& a, int parts, hipStream_t s) {
+  hipLaunchKernelGGL((combine_grad_kernel<XT, ST>), dim3(a.T), dim3(256), 0, s, a.T, a.H, a.K, a.E,
+                     parts, (long long)a.rows, a.offsets, a.sorted_slots, a.ws_slot_row,
+                     static_cast<const ST*>(a.ws_d_xs), a.ws_part, static_cast<XT*>(a.d_x),
+                     a.d_topk_w);
+}
+
+hipError_t launch_combine(const FfnGradArgs& a, hipStream_t s) {
+  if (a.ident || a.rows == 0 || !(a.d_x || a.d_topk_w)) return hipSuccess;
+  const int pn = !a.bf16 ? FN : small_rows(a, a.I) ? FewTile::BN : RowsTile::BN;
+  const int parts = (a.I + pn - 1) / pn;
+  if (!a.bf16) launch_combine_grad<float, float>(a, parts, s);
+  else if (a.xs_bf16) launch_combine_grad<bf16, bf16>(a, parts, s);
+  else launch_combine_grad<bf16, float>(a, parts, s);
+  return hipGetLastError();
 }
 
 hipError_t launch_f32(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
@@ -1318,9 +1352,12 @@ hipError_t launch_f32(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   n.dx = a.d_x ? RT * NH : 0;
   n.dwgu = n.dx + (a.d_gate ? o.E * ((2 * a.I + 63) / 64) * NH : 0);
   n.end = n.dwgu + (a.d_down ? o.E * NH * NI : 0);
-  if (n.end == 0) return hipSuccess;
-  hipLaunchKernelGGL(grad_rest_f32_kernel, dim3(n.end), dim3(256), 0, s, o, n);
-  return hipGetLastError();
+  if (n.end > 0) {
+    hipLaunchKernelGGL(grad_rest_f32_kernel, dim3(n.end), dim3(256), 0, s, o, n);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  return launch_combine(a, s);
 }
 
 template <typename WT>
@@ -1353,6 +1390,9 @@ hipError_t launch_bf16(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
       e = a.ident || a.xs_bf16 ? launch_gemm<kDX, bf16>(a, o, s) : launch_gemm<kDX, float>(a, o, s);
       if (e != hipSuccess) return e;
     }
+    // behind DX, whose results are in the caches still: 51 us at 4096 tokens, at the
+    // end 80
+    if ((e = launch_combine(a, s)) != hipSuccess) return e;
   }
   const bool b = a.wgrad_bf16;
   if (a.d_gate && (e = b ? launch_gemm<kDWGU, bf16>(a, o, s) : launch_gemm<kDWGU, float>(a, o, s)) !=
@@ -1362,14 +1402,6 @@ hipError_t launch_bf16(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
                       hipSuccess)
     return e;
   return hipSuccess;
-}
-
-template <typename XT, typename ST>
-void launch_combine_grad(const FfnGradArgs& a, int parts, hipStream_t s) {
-  hipLaunchKernelGGL((combine_grad_kernel<XT, ST>), dim3(a.T), dim3(256), 0, s, a.T, a.H, a.K, a.E,
-                     parts, (long long)a.rows, a.offsets, a.sorted_slots, a.ws_slot_row,
-                     static_cast<const ST*>(a.ws_d_xs), a.ws_part, static_cast<XT*>(a.d_x),
-                     a.d_topk_w);
 }
 
 }  // namespace
@@ -1392,14 +1424,7 @@ hipError_t launch_ffn_grad(const FfnGradArgs& a, hipStream_t s) {
   o.d_gu = a.ws_d_gu; o.hw = a.ws_hw; o.part = a.d_topk_w ? a.ws_part : nullptr;
   o.d_xs = a.ident ? a.d_x : a.ws_d_xs;
   o.d_gate = a.d_gate; o.d_up = a.d_up; o.d_down = a.d_down;
-  hipError_t e = a.bf16 ? launch_bf16(a, o, s) : launch_f32(a, o, s);
-  if (e != hipSuccess || a.ident || a.rows == 0 || !(a.d_x || a.d_topk_w)) return e;
-  const int pn = !a.bf16 ? FN : small_rows(a, a.I) ? FewTile::BN : RowsTile::BN;
-  const int parts = (a.I + pn - 1) / pn;
-  if (!a.bf16) launch_combine_grad<float, float>(a, parts, s);
-  else if (a.xs_bf16) launch_combine_grad<bf16, bf16>(a, parts, s);
-  else launch_combine_grad<bf16, float>(a, parts, s);
-  return hipGetLastError();
+  return a.bf16 ? launch_bf16(a, o, s) : launch_f32(a, o, s);
 }
 
 }  // namespace moe

@@ -11,8 +11,8 @@
 // adds its chunks' squares in fp64 (an fp32 square overflows from 2^64 on and
 // vanishes below 2^-75) and writes one partial sum, added in order by a last block:
 // results repeat bit for bit.
-// A layer's 780M bf16 gradients: the norm 283 us (1.56 GB read, 5.5 TB/s), the
-// clipping 565 us (3.12 GB, 5.5 TB/s; a large copy reaches 4.85).
+// A layer's 780M bf16 gradients: the norm 248 us (1.56 GB read, 6.3 TB/s), the
+// clipping 572 us (3.12 GB, 5.5 TB/s; a large copy reaches 4.85).
 #include "common.h"
 #include "launch.h"
 #include "moe.h"
@@ -26,6 +26,10 @@ constexpr int kTable = 128;              // tensors a launch
 // / 24.2; 64M: 69 and 60.
 constexpr int kChunk = 16384, kSmallChunk = 2048;
 constexpr long long kSmallList = 1 << 23;
+// Lists whose results go past the caches: from 64 MB of bf16 on, a quarter of the last
+// cache.  780M elements: the clipping 572 us (565 through the caches), the next norm 248
+// (283).
+constexpr long long kPastList = 1 << 25;
 constexpr int kThreads = 256;
 constexpr int kNormBlocks = 2048;        // blocks of a norm launch at most
 
@@ -120,7 +124,9 @@ __global__ __launch_bounds__(kThreads) void norm_end_kernel(int nparts, float ma
   }
 }
 
-template <typename S, typename D>
+typedef unsigned u32x4 __attribute__((ext_vector_type(4)));
+
+template <bool PAST, typename S, typename D>
 __device__ __forceinline__ void chunk_scale(const S* p, D* q, int n, float coef) {
   if (aligned16(p) && aligned16(q)) {
     const int nv = n / 8;
@@ -133,8 +139,11 @@ __device__ __forceinline__ void chunk_scale(const S* p, D* q, int n, float coef)
 #pragma unroll
       for (int j = 0; j < 8; ++j) o[j] = from_f32<D>(to_f32(v[j]) * coef);
 #pragma unroll
-      for (int j = 0; j < (int)sizeof(D) / 2; ++j)
-        reinterpret_cast<uint4*>(q + 8 * (size_t)i)[j] = reinterpret_cast<uint4*>(o)[j];
+      for (int j = 0; j < (int)sizeof(D) / 2; ++j) {
+        u32x4* to = reinterpret_cast<u32x4*>(q + 8 * (size_t)i) + j;
+        if constexpr (PAST) __builtin_nontemporal_store(reinterpret_cast<u32x4*>(o)[j], to);
+        else *to = reinterpret_cast<u32x4*>(o)[j];
+      }
     }
     for (int i = nv * 8 + threadIdx.x; i < n; i += kThreads)
       q[i] = from_f32<D>(to_f32(p[i]) * coef);
@@ -144,7 +153,9 @@ __device__ __forceinline__ void chunk_scale(const S* p, D* q, int n, float coef)
 }
 
 // Chunks from the last to the first: the norm's pass read the last ones last, so
-// they are the likeliest to be in the caches still.
+// they are the likeliest to be in the caches still.  PAST: the results go past the
+// caches, where they would be written back while a later kernel reads.
+template <bool PAST>
 __global__ __launch_bounds__(kThreads) void clip_kernel(const Table t,
                                                         const float* __restrict__ norm) {
   const float coef = norm[1];
@@ -156,21 +167,22 @@ __global__ __launch_bounds__(kThreads) void clip_kernel(const Table t,
     const int n = (int)min((long long)t.chunk, t.numel[i] - at);
     if (t.src_bf16[i]) {
       const bf16* p = static_cast<const bf16*>(t.src[i]) + at;
-      if (t.dst_bf16[i]) chunk_scale(p, static_cast<bf16*>(t.dst[i]) + at, n, coef);
-      else chunk_scale(p, static_cast<float*>(t.dst[i]) + at, n, coef);
+      if (t.dst_bf16[i]) chunk_scale<PAST>(p, static_cast<bf16*>(t.dst[i]) + at, n, coef);
+      else chunk_scale<PAST>(p, static_cast<float*>(t.dst[i]) + at, n, coef);
     } else {
       const float* p = static_cast<const float*>(t.src[i]) + at;
-      if (t.dst_bf16[i]) chunk_scale(p, static_cast<bf16*>(t.dst[i]) + at, n, coef);
-      else chunk_scale(p, static_cast<float*>(t.dst[i]) + at, n, coef);
+      if (t.dst_bf16[i]) chunk_scale<PAST>(p, static_cast<bf16*>(t.dst[i]) + at, n, coef);
+      else chunk_scale<PAST>(p, static_cast<float*>(t.dst[i]) + at, n, coef);
     }
   }
 }
 
-int chunk_of(int n, const moe_tensor* t) {
+long long elements(int n, const moe_tensor* t) {
   long long total = 0;
   for (int i = 0; i < n; ++i) total += t[i].numel;
-  return total < kSmallList ? kSmallChunk : kChunk;
+  return total;
 }
+int chunk_of(long long total) { return total < kSmallList ? kSmallChunk : kChunk; }
 
 // The next tensors of a list, from `at` on, as a launch's table: at most kTable
 // tensors with elements (the callers hold them to 2^40 elements, 2^26 chunks).
@@ -193,7 +205,7 @@ void fill(Table& tb, int n, const moe_tensor* t, const moe_tensor* out, int chun
 }  // namespace
 
 long long grad_norm_parts(int n, const moe_tensor* t) {
-  const int chunk = chunk_of(n, t);
+  const int chunk = chunk_of(elements(n, t));
   long long parts = 0;
   int at = 0;
   while (at < n) {
@@ -206,7 +218,7 @@ long long grad_norm_parts(int n, const moe_tensor* t) {
 
 hipError_t launch_grad_norm(int n, const moe_tensor* t, float max_norm, float* norm,
                             double* ws_part, hipStream_t s) {
-  const int chunk = chunk_of(n, t);
+  const int chunk = chunk_of(elements(n, t));
   int parts = 0, at = 0;
   while (at < n) {
     Table tb;
@@ -225,14 +237,16 @@ hipError_t launch_grad_norm(int n, const moe_tensor* t, float max_norm, float* n
 
 hipError_t launch_grad_clip(int n, const moe_tensor* t, const float* norm, const moe_tensor* out,
                             hipStream_t s) {
-  const int chunk = chunk_of(n, t);
+  const long long total = elements(n, t);
+  const int chunk = chunk_of(total);
+  auto kf = total < kPastList ? clip_kernel<false> : clip_kernel<true>;
   int at = 0;
   while (at < n) {
     Table tb;
     fill(tb, n, t, out, chunk, at);
     const int chunks = tb.first[tb.n];
     if (chunks == 0) continue;
-    hipLaunchKernelGGL(clip_kernel, dim3(chunks < 8192 ? chunks : 8192), dim3(kThreads), 0, s, tb,
+    hipLaunchKernelGGL(kf, dim3(chunks < 8192 ? chunks : 8192), dim3(kThreads), 0, s, tb,
                        norm);
     hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
