@@ -281,12 +281,19 @@ __device__ __forceinline__ void buffer_copy16(i32x4 buf, unsigned off, unsigned 
                : "v"(off), "s"(buf), "s"(m0), "s"(so)
                : "memory", "m0");
 }
+template <bool ONCE>
 __device__ __forceinline__ void global_copy16(const void* base, unsigned off, unsigned lds) {
   const unsigned m0 = __builtin_amdgcn_readfirstlane(lds);
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1"
-               :
-               : "v"(off), "s"(base), "s"(m0)
-               : "memory", "m0");
+  if constexpr (ONCE)  // leaves the caches first
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1 nt"
+                 :
+                 : "v"(off), "s"(base), "s"(m0)
+                 : "memory", "m0");
+  else
+    asm volatile("s_mov_b32 m0, %2\n\ts_nop 3\n\tglobal_load_lds_dwordx4 %0, %1"
+                 :
+                 : "v"(off), "s"(base), "s"(m0)
+                 : "memory", "m0");
 }
 template <bool PAST>
 __device__ __forceinline__ void buffer_store16(i32x4 buf, unsigned off, i32x4 v) {
@@ -349,10 +356,14 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TL::TM][TL::TN]) {
 // in LDS, always in the same order.
 // The experts' 128 x 256 tiles at 4096 tokens (256 rows an expert on average, so three
 // row tiles with their last ones half empty, neighbours on one XCD for their weights):
-// DU 305 us, 426 TFLOP/s, DX 390 us, 667 TFLOP/s.  DU's contraction of 88 k-tiles ends
-// in an epilogue that reads the kept projections and writes three times as much; the
-// second block of the CU multiplies meanwhile.
-template <int KIND, typename WT, typename TL, int KS>
+// DU 283 us, 459 TFLOP/s, DX 388 us, 670 TFLOP/s, the matrix units busy for 0.27 and
+// 0.41 of the time; a wave's LDS reads take nearly as long as its products, and the
+// weights (1.5 GB for the two) come from memory once.  DU's contraction of 88 k-tiles
+// ends in an epilogue that reads the kept projections and writes 1.5 times as much; the
+// second block of the CU multiplies meanwhile.  At 64 tokens the weights bound both:
+// 90 and 128 us, 4.8 and 6.8 TB/s.
+// ONCE: the weights' copies do not stay in the caches.
+template <int KIND, typename WT, typename TL, int KS, bool ONCE>
 __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
                                            unsigned char* smem) {
   constexpr int BM = TL::BM, BN = TL::BN, NW = TL::NW, ST = TL::ST, WN = TL::WN;
@@ -438,7 +449,7 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
   const unsigned ldsA = base + wave * CA * 1024, ldsB = base + TL::A_BYTES + wave * TL::CB * 1024;
   auto copy = [&](int j, unsigned st) {
     if (j < CA) buffer_copy16(bufA, off[j], atA, ldsA + st + j * 1024);
-    else global_copy16(pB, off[j], ldsB + st + (j - CA) * 1024);
+    else global_copy16<ONCE>(pB, off[j], ldsB + st + (j - CA) * 1024);
   };
   auto copied = [&]() {
     atA += GK * 2;
@@ -681,11 +692,11 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
   }
 }
 
-template <int KIND, typename WT, typename TL, int KS>
+template <int KIND, typename WT, typename TL, int KS, bool ONCE>
 __global__ __launch_bounds__(64 * TL::NW * KS, (TL::BLOCKS * TL::NW * KS + 3) / 4) void
 grad_rows_kernel(Operands o, int NT) {
   extern __shared__ __align__(16) unsigned char smem[];
-  rows_block<KIND, WT, TL, KS>(o, NT, blockIdx.x, smem);
+  rows_block<KIND, WT, TL, KS, ONCE>(o, NT, blockIdx.x, smem);
 }
 
 // First tile of the weights' gradients (tpe an expert) that XCD x takes, x = 8: all
@@ -1216,7 +1227,8 @@ __global__ __launch_bounds__(256) void grad_du_f32_kernel(Operands o, int NT) {
   gemm_f32<kDU>(o, blockIdx.x, 0, NT, As, Bs);
 }
 
-// The other three, which need DU alone, in one launch.
+// The other three, which need DU alone, in one launch (100 tokens, 12 experts of 320 x
+// 224: 21 us, one after another 36).
 struct F32Tiles { int dx, dwgu, end; };  // first block behind DX's, behind DWGU's, of all
 __global__ __launch_bounds__(256) void grad_rest_f32_kernel(Operands o, F32Tiles n) {
   __shared__ __align__(16) float As[FK][68], Bs[FK][FN + 4];
@@ -1241,7 +1253,7 @@ constexpr int kCUs = 256;
 
 
 // The dense MLP's DX, DWGU and DWDN in one launch: DX's blocks in the small form, then a
-// large tile a block.
+// large tile a block.  2816 x 2112 at 301 tokens 42 us; one after another 26 + 17 + 11.
 struct RestBlocks { int dx, gu, end; };  // behind DX's, behind DWGU's, all; multiples of 8
 template <typename WT>
 __global__ __launch_bounds__(512, 2) void grad_rest_kernel(Operands o, RestBlocks n) {
@@ -1249,7 +1261,8 @@ __global__ __launch_bounds__(512, 2) void grad_rest_kernel(Operands o, RestBlock
   constexpr int BM = WeightsTile::BM, BN = WeightsTile::BN;
   const int b = blockIdx.x;
   if (b < n.dx)
-    rows_block<kDX, bf16, FewTile, kFewSplit>(o, (o.H + FewTile::BN - 1) / FewTile::BN, b, smem);
+    rows_block<kDX, bf16, FewTile, kFewSplit, false>(o, (o.H + FewTile::BN - 1) / FewTile::BN, b,
+                                                     smem);
   else if (b < n.gu)
     weights_block<kDWGU, WT, WeightsTile, false>(o, (2 * o.I + BM - 1) / BM, (o.H + BN - 1) / BN,
                                                  b - n.dx, n.gu - n.dx, smem);
@@ -1258,11 +1271,11 @@ __global__ __launch_bounds__(512, 2) void grad_rest_kernel(Operands o, RestBlock
                                                  b - n.gu, n.end - n.gu, smem);
 }
 
-template <int KIND, typename WT, typename TL, int KS>
+template <int KIND, typename WT, typename TL, int KS, bool ONCE>
 hipError_t launch_rows(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   const int NT = ((KIND == kDU ? a.I : a.H) + TL::BN - 1) / TL::BN;
   const int blocks = tile_count_bound(a.ident, a.rows, a.T, a.E, TL::BM) * NT;
-  auto kf = grad_rows_kernel<KIND, WT, TL, KS>;
+  auto kf = grad_rows_kernel<KIND, WT, TL, KS, ONCE>;
   constexpr int lds = TL::template rows_lds<KS>();
   static_assert(TL::BLOCKS * lds <= 160 * 1024, "LDS");
   static const hipError_t attr = hipFuncSetAttribute(
@@ -1317,8 +1330,14 @@ hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
     if (bytes >= 64 << 20) return launch_weights<KIND, WT, WeightsTile, true>(a, o, s);
     return launch_weights<KIND, WT, WeightsTile, false>(a, o, s);
   } else {
-    if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit>(a, o, s);
-    return launch_rows<KIND, WT, RowsTile, 1>(a, o, s);
+    if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit, false>(a, o, s);
+    // Up to 32 rows an expert on average most have one row tile, which reads the weights
+    // alone.  26B-A4B at 64 / 256 / 512 / 1024 / 4096 tokens, DU 90 / 107 / 130 / 152 / 329
+    // us, with copies that stay 95 / 115 / 136 / 154 / 292; DX 129 / 166 / 188 / 231 / 494
+    // and 147 / 182 / 197 / 227 / 386.
+    if (!a.ident && (long long)a.rows <= 32LL * a.E)
+      return launch_rows<KIND, WT, RowsTile, 1, true>(a, o, s);
+    return launch_rows<KIND, WT, RowsTile, 1, false>(a, o, s);
   }
 }
 
@@ -1384,6 +1403,7 @@ hipError_t launch_bf16(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   hipError_t e;
   if (a.rows > 0) {
     if ((e = launch_gemm<kDU, bf16>(a, o, s)) != hipSuccess) return e;
+    // (small enough for the small form: few blocks, which would leave CUs without work)
     if (a.ident && a.d_x && (a.d_gate || a.d_down) && small_rows(a, a.H))
       return a.wgrad_bf16 ? launch_rest<bf16>(a, o, s) : launch_rest<float>(a, o, s);
     if (a.d_x) {

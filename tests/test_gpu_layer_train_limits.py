@@ -136,3 +136,16 @@ def test_clip_refuses_outputs_that_overlap():
         with pytest.raises(ValueError):
             lib.moe_grad_clip(plan, norm, out)
     torch.cuda.synchronize()
+
+
+@pytest.mark.parametrize("tokens", [100, 300, 1500])
+def test_many_experts(tokens):
+    """Few rows an expert and more, unevenly: one row tile of an expert or several, gradients
+    that the caches do not hold (64 experts, 201 MB of them)."""
+    note(f"moe_expert_ffn_grad of {tokens} tokens, 64 experts")
+    s = Experts(tokens, 1024, 64, 4, 512, seed=24, pad=0.1, skew=True)
+    s.forward()
+    s.backward()
+    torch.cuda.synchronize()
+    assert int(s.cnt.max()) > (128 if tokens > 200 else 32)
+    s.check()
