@@ -858,7 +858,8 @@ __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT,
       if constexpr (SG == 2) {
         at = lane < 32 ? row_off[(2 * g) & (KW - 1)] : row_off[(2 * g + 1) & (KW - 1)];
       } else {
-        const unsigned lo = lane & 16 ? row_off[(4 * g + 1) & (KW - 1)] : row_off[(4 * g) & (KW - 1)];
+        const unsigned lo =
+            lane & 16 ? row_off[(4 * g + 1) & (KW - 1)] : row_off[(4 * g) & (KW - 1)];
         const unsigned hi =
             lane & 16 ? row_off[(4 * g + 3) & (KW - 1)] : row_off[(4 * g + 2) & (KW - 1)];
         at = lane & 32 ? hi : lo;
@@ -1011,7 +1012,9 @@ __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT,
           // 32 rows of SJ x 32 columns through the wave's own LDS, 16-B chunk q of row r
           // at q ^ f(r), so that 4 SJ lanes store 64 SJ B of a row
           constexpr int SJ = TL::SJ, CPR = 4 * SJ, RPS = 64 / CPR;
-          auto place = [](int r, int q) { return r * (CPR * 16) + (q ^ (r / (4 / SJ) % CPR)) * 16; };
+          auto place = [](int r, int q) {
+            return r * (CPR * 16) + (q ^ (r / (4 / SJ) % CPR)) * 16;
+          };
           unsigned char* stg = smem + TL::RING + wave * TL::WAVE_STAGING;
 #pragma unroll
           for (int q = 0; q < 4; ++q) {
@@ -1415,13 +1418,12 @@ hipError_t launch_bf16(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
     if ((e = launch_combine(a, s)) != hipSuccess) return e;
   }
   const bool b = a.wgrad_bf16;
-  if (a.d_gate && (e = b ? launch_gemm<kDWGU, bf16>(a, o, s) : launch_gemm<kDWGU, float>(a, o, s)) !=
-                      hipSuccess)
-    return e;
-  if (a.d_down && (e = b ? launch_gemm<kDWDN, bf16>(a, o, s) : launch_gemm<kDWDN, float>(a, o, s)) !=
-                      hipSuccess)
-    return e;
-  return hipSuccess;
+  if (a.d_gate) {
+    e = b ? launch_gemm<kDWGU, bf16>(a, o, s) : launch_gemm<kDWGU, float>(a, o, s);
+    if (e != hipSuccess) return e;
+  }
+  if (!a.d_down) return hipSuccess;
+  return b ? launch_gemm<kDWDN, bf16>(a, o, s) : launch_gemm<kDWDN, float>(a, o, s);
 }
 
 }  // namespace

@@ -135,7 +135,7 @@ struct GateUpArgs {
   const int32_t* offsets;      // [E+1] (unused when ident)
   const int32_t* sorted_slots; // [rows] (unused when ident)
   void* h;                     // [rows, N] act dtype, sorted order
-  void* keep;                  // [rows, 2N] act dtype or nullptr: the gate projections, then the up ones
+  void* keep;                  // [rows, 2N] act dtype or nullptr: gate's projections, then up's
   // Weights below bf16: w_gate / w_up hold codes; int8 and E4M3 rows n of
   // group e are scaled by the fp32 s_gate / s_up[e * s_stride + n]; MXFP4
   // rows carry E8M0 block scales at s_gate / s_up + e * s_stride + n * (H /

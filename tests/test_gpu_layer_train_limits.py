@@ -117,7 +117,7 @@ def test_clip():
     assert abs(float(norm[0]) - want) <= 2.0 ** -23 * want
     assert abs(float(norm[1]) - 0.25) <= 2.0 ** -22
     # 0.125, 2 and 1 to one rounding of the factor and one of the product
-    assert ((a[:-1] - 0.125).abs().max() <= 0.125 * 2.0 ** -7) and abs(float(a[-1]) - 2) <= 2.0 ** -6
+    assert (a[:-1] - 0.125).abs().max() <= 0.125 * 2.0 ** -7 and abs(float(a[-1]) - 2) <= 2.0 ** -6
     assert ((b - 1).abs() <= 2.0 ** -21).all()
 
 
