@@ -191,11 +191,11 @@ struct Tile {
   static constexpr int F32_PITCH = BN + 4, BF_PITCH = BN + 8;
   static constexpr int STAGED = WR * F32_PITCH * 4 > BM * BF_PITCH * 2 ? WR * F32_PITCH * 4
                                                                        : BM * BF_PITCH * 2;
-  // (and, with the contraction split over KS groups, their sums on the way)
+  // (with the contraction split over KS groups, the fp32 of all of them)
   template <int KS>
   static constexpr int rows_lds() {
-    const int sums = KS / 2 * BM * F32_PITCH * 4, most = KS * RING > STAGED ? KS * RING : STAGED;
-    return most > sums ? most : sums;
+    const int staged = KS > 1 ? KS * BM * F32_PITCH * 4 : STAGED;
+    return KS * RING > staged ? KS * RING : staged;
   }
   // LDS through which a wave's results leave: 32 rows of SJ 32-column sub-tiles
   static constexpr int SJ = BLOCKS * (RING + NW * 4096) <= 160 * 1024 ? 2 : 1;
@@ -560,47 +560,11 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
   else if (nv == 1) run(std::integral_constant<int, 1>{});
   else run(std::integral_constant<int, 0>{});
 
-  // the groups' sums: the upper half of them to LDS, the lower half adds, and again
-#pragma unroll
-  for (int half = KS / 2; half > 0; half /= 2) {
-    float* part = reinterpret_cast<float*>(smem) +
-                  (size_t)(grp % half) * BM * TL::F32_PITCH + (wm * WR + fr) * TL::F32_PITCH +
-                  wn * WC + 4 * fq;
-    if (grp >= half && grp < 2 * half) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (i < nv)
-              *reinterpret_cast<f32x4*>(part + i * 32 * TL::F32_PITCH + j * 32 + 8 * q) =
-                  f32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
-                        acc[i][j][4 * q + 3]};
-    }
-    __syncthreads();
-    if (grp < half) {
-#pragma unroll
-      for (int i = 0; i < TM; ++i)
-#pragma unroll
-        for (int j = 0; j < TN; ++j)
-#pragma unroll
-          for (int q = 0; q < 4; ++q)
-            if (i < nv) {
-              const f32x4 v =
-                  *reinterpret_cast<const f32x4*>(part + i * 32 * TL::F32_PITCH + j * 32 + 8 * q);
-#pragma unroll
-              for (int r = 0; r < 4; ++r) acc[i][j][4 * q + r] += v[r];
-            }
-    }
-    __syncthreads();
-  }
-
-  // Epilogue through LDS (the ring's, free now), so that whole rows are read and
-  // written in 16-B pieces.
+  // Epilogue through LDS (the rings', free now), so that whole rows are read and
+  // written in 16-B pieces; the groups' sums meet there, always in the same order.
   const int tid = threadIdx.x;
   constexpr int F32_PITCH = TL::F32_PITCH, BF_PITCH = TL::BF_PITCH;
-  constexpr bool F32 = KIND == kDU || std::is_same<WT, float>::value;
+  constexpr bool F32 = KIND == kDU || std::is_same<WT, float>::value || KS > 1;
   if constexpr (F32) {
     float* stg = reinterpret_cast<float*>(smem);
     const bf16* kept = static_cast<const bf16*>(o.kept);
@@ -609,7 +573,8 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
     constexpr int LPR = BN / 8, RPI = 64 * NW * KS / LPR;  // lanes a row, rows an iteration
     static_assert(LPR <= kWave && WR % RPI == 0, "rows of the epilogue");
     for (int pass = 0; pass < TL::WM; ++pass) {
-      if (grp == 0 && wm == pass) {
+      if (wm == pass) {
+        float* to = stg + (grp * BM + fr) * F32_PITCH + wn * WC + 4 * fq;
 #pragma unroll
         for (int i = 0; i < TM; ++i)
 #pragma unroll
@@ -618,8 +583,7 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
             for (int q = 0; q < 4; ++q) {
               const f32x4 v = {acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2],
                                acc[i][j][4 * q + 3]};
-              *reinterpret_cast<f32x4*>(stg + (i * 32 + fr) * F32_PITCH + wn * WC + j * 32 +
-                                        8 * q + 4 * fq) = v;
+              *reinterpret_cast<f32x4*>(to + i * 32 * F32_PITCH + j * 32 + 8 * q) = v;
             }
       }
       __syncthreads();
@@ -627,12 +591,30 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
       for (int it = 0; it < WR / RPI; ++it) {
         const int rl = it * RPI + tid / LPR, c = (tid % LPR) * 8;
         const int row = row0 + pass * WR + rl, col = n0 + c;
+        f32x4 va[2];  // the row's eight columns
+        auto sums = [&]() {
+          const f32x4* from = reinterpret_cast<const f32x4*>(stg + rl * F32_PITCH + c);
+          va[0] = from[0];
+          va[1] = from[1];
+#pragma unroll
+          for (int g = 1; g < KS; ++g) {
+            va[0] += from[g * (BM * F32_PITCH / 4)];
+            va[1] += from[g * (BM * F32_PITCH / 4) + 1];
+          }
+        };
         if constexpr (KIND == kDX) {
           if (row < row1 && col < Nout) {
-            const float* v = stg + rl * F32_PITCH + c;
-            float* d = static_cast<float*>(o.d_xs) + (size_t)row * H + col;
-            *reinterpret_cast<f32x4*>(d) = *reinterpret_cast<const f32x4*>(v);
-            *reinterpret_cast<f32x4*>(d + 4) = *reinterpret_cast<const f32x4*>(v + 4);
+            sums();
+            WT* d = static_cast<WT*>(o.d_xs) + (size_t)row * H + col;
+            if constexpr (std::is_same<WT, float>::value) {
+              *reinterpret_cast<f32x4*>(d) = va[0];
+              *reinterpret_cast<f32x4*>(d + 4) = va[1];
+            } else {
+              bf16x8 v;
+#pragma unroll
+              for (int j = 0; j < 8; ++j) v[j] = (bf16)va[j / 4][j % 4];
+              *reinterpret_cast<bf16x8*>(d) = v;
+            }
           }
         } else {
           float dot = 0.0f;
@@ -643,10 +625,11 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
             const bf16x8 u =
                 *reinterpret_cast<const bf16x8*>(kept + (size_t)row * 2 * I + I + col);
             bf16x8 og, ou, oh;
+            sums();
 #pragma unroll
             for (int j = 0; j < 8; ++j) {
               float h, dg, du;
-              const float v = stg[rl * F32_PITCH + c + j];
+              const float v = va[j / 4][j % 4];
               act_grad<true>((float)g[j], (float)u[j], v, h, dg, du);
               dot += v * h;
               og[j] = (bf16)(live ? w * dg : 0.0f);
@@ -670,7 +653,7 @@ __device__ __forceinline__ void rows_block(const Operands& o, int NT, int block,
   } else {
     bf16* stg = reinterpret_cast<bf16*>(smem);
 #pragma unroll
-    for (int i = 0; i < TM && grp == 0; ++i)
+    for (int i = 0; i < TM; ++i)
 #pragma unroll
       for (int j = 0; j < TN; ++j)
 #pragma unroll
