@@ -149,3 +149,46 @@ def test_many_experts(tokens):
     torch.cuda.synchronize()
     assert int(s.cnt.max()) > (128 if tokens > 200 else 32)
     s.check()
+
+
+def test_calls_at_once():
+    """The same calls of two sizes on two streams at a time, each with its own workspace:
+    the bits of one after another."""
+    g = torch.Generator(device="cuda").manual_seed(25)
+    sets = []
+    for i, (n, st) in enumerate(((700, torch.cuda.Stream()), (90, torch.cuda.Stream()))):
+        e, m, v = Experts(n, 320, 6, 3, 224, seed=i), Dense(n, 320, 288, seed=i), Norms(n, 320)
+        for s in (e, m, v):
+            s.forward()
+        grads = [torch.randn(k, generator=g, device="cuda") for k in (5000 * n, 77, 12345)]
+        plan, out = lib.grad_list(grads), [torch.empty_like(t) for t in grads]
+        sets.append((st, e, m, v, plan, lib.grad_list(out), torch.empty(2, device="cuda"),
+                     lib.grad_norm_workspace(plan)))
+
+    def run(st, e, m, v, plan, to, norm, ws):
+        for s in (e, m, v):
+            s.backward(st)
+        lib.moe_grad_norm(plan, 0.5, norm, ws, st)
+        lib.moe_grad_clip(plan, norm, to, st)
+
+    def results(st, e, m, v, plan, to, norm, ws):
+        return [*e.outputs().values(), *m.outputs().values(), *v.results(), *to.tensors, norm]
+
+    torch.cuda.synchronize()
+    want = []
+    for s in sets:
+        run(*s)
+        torch.cuda.synchronize()
+        want.append([t.clone() for t in results(*s)])
+    for _ in range(5):
+        for s in sets:
+            for t in results(*s):
+                t.fill_(float("nan"))
+        torch.cuda.synchronize()
+        note("training calls on two streams at once")
+        for _ in range(3):
+            for s in sets:
+                run(*s)
+        torch.cuda.synchronize()
+        for s, w in zip(sets, want):
+            assert all(torch.equal(a, b) for a, b in zip(results(*s), w))
