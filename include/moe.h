@@ -228,11 +228,11 @@ int moe_balance_loss_grad(const moe_dims* dims, int32_t T, const float* logits,
  * d_topk_w [T,K] and d_logits [T,E] (fp32; either may be NULL for zero, not
  * both), those of its inputs: d_x [T,H] act dtype (NULL: not wanted),
  * d_router_w [E,H], d_router_scale [H], d_per_expert_scale [E],
- * d_pre_norm_gain [H] (exactly when pre_norm_gain is given), all fp32, all
- * overwritten.  The picks are constants; x, the parameters, logits and
- * topk_idx are the forward call's.  Where a logit is -inf (an expert switched
- * off), d_logits counts as 0, whatever it holds, and a pick takes part in
- * nothing.  No output may overlap an input. */
+ * d_pre_norm_gain [H] (exactly when pre_norm_gain is given; the gain's gradient
+ * through the router alone), all fp32, all overwritten.  The picks are constants;
+ * x, the parameters, logits and topk_idx are the forward call's.  Where a logit is
+ * -inf (an expert switched off), d_logits counts as 0, whatever it holds, and a
+ * pick takes part in nothing.  No output may overlap an input. */
 int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float* router_w,
                     const float* router_scale, const float* per_expert_scale,
                     const float* pre_norm_gain, const float* logits, const int32_t* topk_idx,
@@ -251,6 +251,10 @@ int moe_router_grad(const moe_dims* dims, int32_t T, const void* x, const float*
  * (which also gives the routing weights' gradient), the balance loss's calls,
  * moe_router_grad, and gemma4_pre_norms_grad, which adds the router's and the
  * residual's gradient of x to its own.  Then moe_grad_norm and moe_grad_clip.
+ * One sum is the caller's, no call here makes it: g_pre2 feeds the experts and
+ * the router, so its gradient is gemma4_pre_norms_grad's d_g_pre2 plus
+ * moe_router_grad's d_pre_norm_gain.  Both calls overwrite: give them a buffer
+ * each and add the two before the norm and the clipping.
  * token_mask and T == 0 are as in the router's training calls above; sums run in
  * fp32 or more in an order fixed by the sizes and the dispatch; no output may
  * overlap an input or another output unless it says so.
@@ -279,7 +283,8 @@ int moe_expert_ffn_keep(const moe_dims* dims, int32_t T, const void* x, const vo
  * may be NULL (not wanted), not all.  A slot that the dispatch dropped has a zero
  * in d_topk_w and takes part in nothing.  bf16 path: v, <v, h> and every sum in
  * fp32; [d_gate, d_up], w h and, where slot_dtype is MOE_BF16, the slots' parts of
- * d_x are rounded to bf16 in between.  Workspace of its own size, as is every call's below that has one. */
+ * d_x are rounded to bf16 in between.  Workspace of its own size, as is every
+ * call's below that has one. */
 size_t moe_expert_ffn_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
 int moe_expert_ffn_grad(const moe_dims* dims, int32_t T, const void* x, const void* w_gate_up,
                         const void* w_down, const float* topk_w, const int32_t* expert_offsets,
@@ -325,9 +330,10 @@ int gemma4_post_norms(const moe_dims* dims, int32_t T, const void* x, const void
 /* Backward pass of gemma4_pre_norms, from d_xd and d_xm: d_x = the norms' gradient
  * + d_x_add (another branch's gradient of x, the router's; NULL: none) +
  * layer_scalar * d_out (the residual's; d_out NULL: none), all [T,H] act dtype;
- * d_g_pre, d_g_pre2 [H] fp32.  A token that does not count gets a zero row of
- * d_x whatever d_x_add and d_out hold.  d_x may be any of the [T,H] inputs (each
- * row is read before it is written). */
+ * d_g_pre, d_g_pre2 [H] fp32, overwritten (d_g_pre2 without the router's part,
+ * moe_router_grad's d_pre_norm_gain, which is the caller's to add).  A token that
+ * does not count gets a zero row of d_x whatever d_x_add and d_out hold.  d_x may
+ * be any of the [T,H] inputs (each row is read before it is written). */
 size_t gemma4_norms_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);
 int gemma4_pre_norms_grad(const moe_dims* dims, int32_t T, const void* x, const float* g_pre,
                           const float* g_pre2, const uint8_t* token_mask, const void* d_xd,

@@ -447,7 +447,9 @@ def gemma4_post_norms(d, T, x, y_slots, dn, g_post1, g_post2, g_post, layer_scal
 
 def gemma4_pre_norms_grad(d, T, x, g_pre, g_pre2, token_mask, d_xd, d_xm, d_x_add, d_out,
                           layer_scalar, d_x, d_g_pre, d_g_pre2, ws, stream=None):
-    """Backward pass of gemma4_pre_norms, plus d_x_add and layer_scalar * d_out."""
+    """Backward pass of gemma4_pre_norms, plus d_x_add and layer_scalar * d_out.  The
+    gradient of g_pre2 is d_g_pre2 plus moe_router_grad's d_pre_norm_gain: both calls
+    overwrite, the sum is the caller's."""
     n, H, a, f32, dev = T * d.hidden, d.hidden, _act(d), torch.float32, _device()
     _check(_lib.gemma4_pre_norms_grad(
         ctypes.byref(d), T, _arg("x", x, a, n, dev), _arg("g_pre", g_pre, f32, H, dev),
