@@ -32,8 +32,8 @@
  *   - T = 0 is a valid no-op.
  *   - No call allocates device memory.  Calls that need scratch take a
  *     workspace `ws` of at least moe_workspace_size() bytes, 256-byte aligned;
- *     moe_balance_loss, moe_router_grad, moe_expert_ffn_b128 and
- *     moe_linear_b128 have size functions of their own.
+ *     calls with a size function of their own (it stands above them, or below
+ *     moe_workspace_size) need that many instead.
  *     Two calls in flight must not share a workspace.
  *   - Pointers must be 16-byte aligned.
  *   - Preconditions that are not checked: inputs are finite; topk_idx given to
@@ -146,9 +146,11 @@ typedef struct gemma4_ffn_weights {
 } gemma4_ffn_weights;
 
 /* Bytes of workspace sufficient for T <= max_tokens: for every call below that
- * has no size function of its own, and for each of the three that follow.  A
- * buffer of the largest of them serves all.  Returns 0 if the dimensions are
- * unsupported (moe_last_error() says why). */
+ * has no size function of its own, and for each of the three that follow.
+ * moe_expert_ffn_grad, gemma4_dense_mlp_grad, the norms' backward passes,
+ * moe_grad_norm and moe_linear_b128 have theirs beside them.  A buffer of the
+ * largest of the sizes of the calls that a program makes serves them all.
+ * Returns 0 if the dimensions are unsupported (moe_last_error() says why). */
 size_t moe_workspace_size(const moe_dims* dims, int32_t max_tokens);
 size_t moe_balance_loss_workspace_size(const moe_dims* dims, int32_t max_tokens);
 size_t moe_router_grad_workspace_size(const moe_dims* dims, int32_t max_tokens);

@@ -56,15 +56,14 @@ class MoeError(RuntimeError):
         self.code = code
 
 
-# Size functions of the workspaces: of the calls named, of all others ("layer").
+# Size functions of the workspaces: of the calls named, of all others that have none of
+# their own ("layer").  A default workspace serves the first four.
 _WS_SIZES = {"layer": "moe_workspace_size", "balance_loss": "moe_balance_loss_workspace_size",
              "router_grad": "moe_router_grad_workspace_size",
              "expert_ffn_b128": "moe_expert_ffn_b128_workspace_size"}
-
-
-# Size functions of the calls whose workspace is asked for by a function of its own.
-_OWN_WS_SIZES = ("moe_expert_ffn_grad_workspace_size", "gemma4_dense_mlp_grad_workspace_size",
-                 "gemma4_norms_grad_workspace_size")
+_WS_SIZES_ALL = {**_WS_SIZES, "expert_ffn_grad": "moe_expert_ffn_grad_workspace_size",
+                 "dense_mlp_grad": "gemma4_dense_mlp_grad_workspace_size",
+                 "norms_grad": "gemma4_norms_grad_workspace_size"}
 
 
 def _load():
@@ -74,7 +73,7 @@ def _load():
     L = ctypes.CDLL(LIB_PATH)
     P, I32, SZ = ctypes.c_void_p, ctypes.c_int32, ctypes.c_size_t
     D = ctypes.POINTER(MoeDims)
-    for f in _WS_SIZES.values():
+    for f in _WS_SIZES_ALL.values():
         getattr(L, f).argtypes = [D, I32]
         getattr(L, f).restype = SZ
     L.moe_last_error.argtypes = []
@@ -93,9 +92,6 @@ def _load():
     L.moe_linear_b128.argtypes = [I32, I32, I32] + [P] * 4 + [I32, P, SZ, P]
     L.moe_expert_ffn_b128.argtypes = [D, I32] + [P] * 10 + [SZ, P]
     TN = ctypes.POINTER(MoeTensor)
-    for f in _OWN_WS_SIZES:
-        getattr(L, f).argtypes = [D, I32]
-        getattr(L, f).restype = SZ
     L.moe_grad_norm_workspace_size.argtypes = [I32, TN]
     L.moe_grad_norm_workspace_size.restype = SZ
     L.moe_expert_ffn_keep.argtypes = [D, I32] + [P] * 9 + [SZ, P]
@@ -231,14 +227,14 @@ def last_error() -> str:
 
 
 def workspace_size(d: MoeDims, max_tokens: int, calls=tuple(_WS_SIZES)) -> int:
-    """Bytes that serve the calls named (any of "layer", "balance_loss", "router_grad",
-    "expert_ffn_b128", where "layer" is every call but the other three), all of
-    them by default."""
+    """Bytes that serve the calls named: any of "layer", "balance_loss", "router_grad",
+    "expert_ffn_b128" (all four by default), "expert_ffn_grad", "dense_mlp_grad" and
+    "norms_grad", where "layer" is every call that has no size function of its own."""
     need = 0
     for c in calls:
-        if c not in _WS_SIZES:
-            raise ValueError(f"calls names {c!r}, expected some of {tuple(_WS_SIZES)}")
-        n = getattr(_lib, _WS_SIZES[c])(ctypes.byref(d), max_tokens)
+        if c not in _WS_SIZES_ALL:
+            raise ValueError(f"calls names {c!r}, expected some of {tuple(_WS_SIZES_ALL)}")
+        n = getattr(_lib, _WS_SIZES_ALL[c])(ctypes.byref(d), max_tokens)
         if n == 0:
             raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
         need = max(need, n)
@@ -336,26 +332,19 @@ def _dtype(*tensors):
     return MOE_BF16 if kinds == {torch.bfloat16} else MOE_F32
 
 
-def _own_workspace(size, d, max_tokens, device):
-    n = getattr(_lib, size)(ctypes.byref(d), max_tokens)
-    if n == 0:
-        raise MoeError(MOE_ERR_UNSUPPORTED, last_error())
-    return torch.empty(n, dtype=torch.uint8, device=device)
-
-
 def expert_ffn_grad_workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
     """A uint8 device buffer of moe_expert_ffn_grad_workspace_size bytes."""
-    return _own_workspace("moe_expert_ffn_grad_workspace_size", d, max_tokens, device)
+    return workspace(d, max_tokens, device, ("expert_ffn_grad",))
 
 
 def dense_mlp_grad_workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
     """A uint8 device buffer of gemma4_dense_mlp_grad_workspace_size bytes."""
-    return _own_workspace("gemma4_dense_mlp_grad_workspace_size", d, max_tokens, device)
+    return workspace(d, max_tokens, device, ("dense_mlp_grad",))
 
 
 def norms_grad_workspace(d: MoeDims, max_tokens: int, device="cuda") -> torch.Tensor:
     """A uint8 device buffer of gemma4_norms_grad_workspace_size bytes."""
-    return _own_workspace("gemma4_norms_grad_workspace_size", d, max_tokens, device)
+    return workspace(d, max_tokens, device, ("norms_grad",))
 
 
 def moe_expert_ffn_keep(d, T, x, w_gate_up, w_down, topk_w, offsets, sorted_slots, gate_up,
