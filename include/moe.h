@@ -182,9 +182,10 @@ int moe_router(const moe_dims* dims, int32_t T, const void* x, const float* rout
  * output for token t), moe_combine on those slots times topk_w, moe_balance_loss
  * on the logits and the picks, moe_balance_loss_grad for the loss's gradient in
  * the logits, and moe_router_grad with that gradient and the routing weights'.
- * Two steps are the caller's, no call here makes them: d_topk_w[t,k] = sum_h
- * d_out[t,h] y_slots[t,k,h], d_out the gradient of the layer's output, and the
- * slots' product with topk_w before moe_combine.
+ * Two steps of this form are the caller's: d_topk_w[t,k] = sum_h d_out[t,h]
+ * y_slots[t,k,h], d_out the gradient of the layer's output, and the slots' product
+ * with topk_w before moe_combine.  With the calls of the next section neither is:
+ * moe_expert_ffn_keep takes topk_w, moe_expert_ffn_grad gives d_topk_w.
  * token_mask: uint8 [T], 0 for a token that does not count (padding), or NULL
  * when all do; the rows of such tokens in every [T, ...] input may hold
  * anything, NaN too, and their rows of every [T, ...] gradient are zero.
