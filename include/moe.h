@@ -42,7 +42,8 @@
  *     is missing from sorted_slots, expert_offsets[E] falls short of T*K,
  *     and its y_slots row is left unwritten); the
  *     offsets / sorted_slots given to moe_expert_ffn are moe_dispatch's output
- *     for the same topk_idx.
+ *     for the same topk_idx; outputs overlap nothing that their call does not
+ *     name.
  *   - Results are deterministic: no floating-point atomics; the same inputs
  *     give the same bits on every run.
  *
@@ -378,7 +379,10 @@ int moe_grad_norm(int32_t n, const moe_tensor* grads, float max_norm, float* nor
 /* out[i] = grads[i] * norm[1], norm as moe_grad_norm left it on the device; out
  * NULL: in place.  An out tensor may have another dtype than its gradient; it is
  * its gradient (same address and dtype) or overlaps nothing in either list.  In
- * place, no two tensors of the list overlap. */
+ * place, no two tensors of the list overlap, so none is listed twice.  Neither is
+ * checked here: an element with two places in the lists would be scaled by blocks
+ * that run at once.  (The Python binding, whose lists outlive a call, refuses both
+ * when a list or a pair of them is first used.) */
 int moe_grad_clip(int32_t n, const moe_tensor* grads, const float* norm, const moe_tensor* out,
                   void* stream);
 

@@ -497,7 +497,9 @@ class GradList:
 
 def grad_list(tensors) -> GradList:
     """The gradients (contiguous, fp32 or bf16, of any sizes, none overlapping another)
-    that moe_grad_norm and moe_grad_clip take."""
+    that moe_grad_norm and moe_grad_clip take.  One that overlaps another, or is listed
+    twice, is refused here, also in a list that is only measured, where the library's
+    own call would count it twice."""
     return GradList(tensors)
 
 

@@ -1,5 +1,8 @@
 """Sums of the layer's training step that one call alone does not show: the second
-pre-norm's gain, whose gradient has two parts."""
+pre-norm's gain, whose gradient has two parts, and a gradient that a list names twice."""
+import ctypes
+import math
+
 import pytest
 import torch
 
@@ -7,6 +10,11 @@ from tests.gpu_util import F32_TOL, note, rel_max_err
 from tests.test_gpu_layer_step import Layer
 
 pytestmark = pytest.mark.gpu
+
+if torch.cuda.is_available():
+    from sparse_moe_transformer_router_amd import lib
+else:
+    lib = None
 
 
 @pytest.mark.parametrize("T", [5, 150])
@@ -23,3 +31,22 @@ def test_second_pre_norms_gain_has_two_parts(T):
     assert rel_max_err(both.numpy(), want) <= F32_TOL
     for part in (router, both - router):
         assert rel_max_err(part.numpy(), want) > 100 * F32_TOL
+
+
+def test_a_gradient_listed_twice_counts_twice():
+    """moe_grad_norm itself takes such a list (the binding's lists hold a tensor once)."""
+    a = torch.randn(5000, device="cuda")
+    b = torch.randn(33, device="cuda").bfloat16()
+    t = (lib.MoeTensor * 3)((a.data_ptr(), a.numel(), lib.MOE_F32),
+                            (b.data_ptr(), b.numel(), lib.MOE_BF16),
+                            (a.data_ptr(), a.numel(), lib.MOE_F32))
+    L = lib.raw()
+    norm = torch.empty(2, device="cuda")
+    ws = torch.empty(L.moe_grad_norm_workspace_size(3, t), dtype=torch.uint8, device="cuda")
+    note("norm of a list that names a gradient twice")
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    assert L.moe_grad_norm(3, t, 1.0, norm.data_ptr(), ws.data_ptr(), ws.numel(),
+                           stream) == lib.MOE_OK
+    torch.cuda.synchronize()
+    want = math.sqrt(2 * float(a.double().square().sum()) + float(b.double().square().sum()))
+    assert abs(float(norm[0]) - want) <= 1.01 * 2.0 ** -24 * want
