@@ -1,5 +1,6 @@
 """Sums of the layer's training step that one call alone does not show: the second
-pre-norm's gain, whose gradient has two parts, and a gradient that a list names twice."""
+pre-norm's gain, whose gradient has two parts, the clipped gradients of a whole step, and a
+gradient that a list names twice."""
 import ctypes
 import math
 
@@ -31,6 +32,30 @@ def test_second_pre_norms_gain_has_two_parts(T):
     assert rel_max_err(both.numpy(), want) <= F32_TOL
     for part in (router, both - router):
         assert rel_max_err(part.numpy(), want) > 100 * F32_TOL
+
+
+@pytest.mark.parametrize("bf16", [False, True], ids=["f32", "bf16"])
+@pytest.mark.parametrize("T", [5, 150, 700])
+def test_clipped_gradients_of_a_step(T, bf16):
+    """Each clipped value against its gradient times the factor: off by half a step of its
+    type and the product's rounding, relative to itself (below the smallest normal number
+    half a step of the subnormal ones)."""
+    s = Layer(T, T, bf16)
+    note(f"clipped gradients of a step, T={T} bf16={bf16}")
+    s.run()
+    torch.cuda.synchronize()
+    norm = math.sqrt(sum(float(v.double().square().sum()) for v in s.grads.tensors))
+    coef = min(1.0, 1.0 / (norm + 1e-6))
+    assert coef < 0.9  # it clips
+    assert abs(float(s.norm[1]) - coef) <= 4 * 2.0 ** -24 * coef
+    for a, b in zip(s.clipped, s.grads.tensors):
+        e = b.double() * float(s.norm[1])
+        half = torch.finfo(a.dtype).eps / 2
+        assert ((a.double() - e).abs()
+                <= (1.01 * half + 2.0 ** -24) * e.abs() + 2.0 ** -134).all()
+    total = math.sqrt(sum(float(v.double().square().sum()) for v in s.clipped))
+    # at most a rounding of the norm, the quotient and each value
+    assert abs(total - 1.0) <= (2.0 ** -8 if bf16 else 1e-6)
 
 
 def test_a_gradient_listed_twice_counts_twice():
