@@ -1308,12 +1308,18 @@ hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
     // Up to half as many large tiles as CUs: the dense MLP's DWDN (99 tiles) at 301 / 4096
     // tokens 14.0 / 93 -> 10.7 / 63 us; its DWGU (187) 16.6 / 106, with small ones 16.0 / 121.
     if (tiles <= kCUs / 2) return launch_weights<KIND, WT, SmallWeightsTile, false>(a, o, s);
-    // All three gradients, a quarter of the last cache or more: past it.  512 tokens x 2,
-    // 2816 x 704, the whole call with 8 / 16 / 32 experts (95 / 190 / 381 MB) 95 / 120 / 223
-    // us, through the caches 98 / 155 / 250; the dense MLP (36 MB) at 4096 tokens 366 and 363,
-    // and who reads them next finds them there.
-    const long long bytes = (long long)o.E * 3 * o.I * o.H * sizeof(WT);
-    if (bytes >= 64 << 20) return launch_weights<KIND, WT, WeightsTile, true>(a, o, s);
+    // All three gradients in bf16, a quarter of the last cache or more: past it.  512 tokens
+    // x 2, 2816 x 704, the call alone with 8 / 16 / 32 experts (95 / 190 / 381 MB) 91 / 106 /
+    // 192 us, through the caches 93 / 137 / 201; with the norm and the clipping of them
+    // behind it, which find up to 190 MB in the caches, 145 / 228 / 387 and 143 / 223 / 409.
+    // The dense MLP (36 MB) at 4096 tokens 346 and 351, with both 373 and 371.
+    // fp32 ones go through the caches, which join a store's 32-byte pieces of a row to lines;
+    // past them each is written by itself: 512 tokens x 8 with 16 / 32 experts (DWGU + DWDN)
+    // 141 and 424 / 225 and 833 us, 26B-A4B at 64 / 4096 tokens 582 and 3471 / 1062 and 3285.
+    if constexpr (std::is_same<WT, bf16>::value) {
+      const long long bytes = (long long)o.E * 3 * o.I * o.H * sizeof(WT);
+      if (bytes >= 64 << 20) return launch_weights<KIND, WT, WeightsTile, true>(a, o, s);
+    }
     return launch_weights<KIND, WT, WeightsTile, false>(a, o, s);
   } else {
     if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit, false>(a, o, s);
