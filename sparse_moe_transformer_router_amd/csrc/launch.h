@@ -388,7 +388,7 @@ struct PostNormGradArgs {
   float* ws_part;        // [blocks,3,H]
   double* ws_scalar;     // [blocks]
 };
-int norms_grad_blocks(int T, int H);
+int norms_grad_blocks(int T, int H, bool y_bf16);  // at most, of either
 hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s);
 hipError_t launch_post_norms_grad(const PostNormGradArgs& a, hipStream_t s);
 

@@ -208,7 +208,7 @@ FfnGradLayout ffn_grad_layout(const moe_dims* d, long long rows, long long I, bo
 struct NormsGradLayout { size_t scalar, part, total; };
 NormsGradLayout norms_grad_layout(const moe_dims* d, long long T) {
   NormsGradLayout L{};
-  const size_t nb = (size_t)moe::norms_grad_blocks((int)T, d->hidden);
+  const size_t nb = (size_t)moe::norms_grad_blocks((int)T, d->hidden, d->slot_dtype == MOE_BF16);
   size_t o = 0;
   L.scalar = region(o, 8 * nb);
   L.part = region(o, 4 * nb * 3 * d->hidden);

@@ -9,15 +9,19 @@
 //            added on the way out.  One pair of row sums: x^2 and e x.
 //   behind   s = n(dn) g1 + n(moe) g2, o = n(s) g3, out = (o + x) layer_scalar.
 //            Row sums: dn^2 and moe^2; then s^2 and e3 s; then e1 n1 and e2 n2.
-// A group of threads takes two rows at a time (past hidden 4096 one), a thread 8 of
-// their columns (hidden <= 8192), and a block as many groups as fit 512 threads (one
-// of up to 1024 past hidden 4096).  The sums over tokens (d_g) stay in registers; a
-// block adds its groups' and writes them once, and a second kernel adds the blocks in
-// order.  The next rows' loads are issued before these are worked on.
+// A group of threads takes two rows at a time (one past hidden 4096, and behind the
+// branches where the slots are fp32), a thread 8 of their columns (hidden <= 8192), and
+// a block as many groups as fit 512 threads (one of up to 1024 past hidden 4096).  The
+// sums over tokens (d_g) stay in registers; a block adds its groups' and writes them
+// once, and a second kernel adds the blocks in order.  The next rows' loads are issued
+// before these are worked on.
 // 4096 bf16 tokens of 2816, behind the branches: 138 MB in 46 + 5 us, 3.0 TB/s (one row
-// at a time 49 + 5): the three row sums one after another, each a wait for the whole
-// group, are not covered by the one block that a CU's registers hold.  333 tokens
-// before them: 6.9 + 3.4 us, two launches' latency.
+// at a time 48 + 5): the three row sums one after another, each a wait for the whole
+// group, are not covered by the one block that a CU's registers hold.  With fp32 slots
+// 184 MB in 52 + 5 us, all fp32 277 MB in 63 + 5.  Before them 138 MB in 32 + 5 us, 333
+// tokens 6.9 + 3.4 us, two launches' latency.  Past hidden 4096 a thread has 128
+// registers, and the kernel behind the branches spills 116 to 200 bytes of its rows: 4096
+// tokens of 5632, bf16 / fp32 slots / fp32 170 / 216 / 296 us (before them 60 / - / 119).
 #include "common.h"
 #include "launch.h"
 
@@ -210,6 +214,15 @@ __global__ __launch_bounds__(MAXT) void pre_grad_kernel(
   write_sums<2>(s, H, c, on, g, groups, lds, part + (size_t)blockIdx.x * 2 * H);
 }
 
+// Rows that a group of post_grad_kernel works on at a time.  Two of fp32 slots are more
+// than its registers hold (60 and 124 bytes a thread spilled with bf16 and fp32
+// activations): 4096 tokens of 2816, one / two rows, bf16 slots 48.4 / 46.0 us, fp32 slots
+// 51.9 / 65.8, all fp32 63.0 / 105.
+template <typename YT>
+__host__ __device__ constexpr int post_rows(int threads) {
+  return threads > 512 || sizeof(YT) > 2 ? 1 : 2;
+}
+
 template <typename XT, typename YT, int MAXT>
 __global__ __launch_bounds__(MAXT) void post_grad_kernel(
     int T, int H, int groups, float eps, float scalar, const XT* x,
@@ -217,7 +230,7 @@ __global__ __launch_bounds__(MAXT) void post_grad_kernel(
     const float* __restrict__ g2, const float* __restrict__ g3, const uint8_t* __restrict__ mask,
     const XT* d_out, XT* d_dn, XT* d_moe,
     float* __restrict__ part, double* __restrict__ part_scalar) {
-  constexpr int R = MAXT > 512 ? 1 : 2;
+  constexpr int R = post_rows<YT>(MAXT);
   extern __shared__ __align__(16) float lds[];
   __shared__ __align__(16) float red[2][2 * R * 16];
   __shared__ double dred[16];
@@ -377,14 +390,21 @@ __global__ __launch_bounds__(1024) void sum_parts_kernel(int nb, int n, int H,
 int threads_of(int H) { return (H / 8 + kWave - 1) / kWave * kWave; }
 int groups_of(int H) { return threads_of(H) > 512 ? 1 : 512 / threads_of(H); }
 size_t lds_of(int H, int n) { return groups_of(H) > 1 ? (size_t)n * H * 4 : 0; }
-int blocks_of(int T, int H) {
-  const int rows = groups_of(H) * (threads_of(H) > 512 ? 1 : 2), b = (T + rows - 1) / rows;
+int blocks_of(int T, int H, int rows) {  // of groups that take so many rows at a time
+  const int n = groups_of(H) * rows, b = (T + n - 1) / n;
   return b < kNormsBlocks ? b : kNormsBlocks;
+}
+int pre_blocks(int T, int H) { return blocks_of(T, H, threads_of(H) > 512 ? 1 : 2); }
+int post_blocks(int T, int H, bool y_bf16) {
+  return blocks_of(T, H, y_bf16 ? post_rows<bf16>(threads_of(H)) : post_rows<float>(threads_of(H)));
 }
 
 }  // namespace
 
-int norms_grad_blocks(int T, int H) { return blocks_of(T, H); }
+int norms_grad_blocks(int T, int H, bool y_bf16) {
+  const int a = pre_blocks(T, H), b = post_blocks(T, H, y_bf16);
+  return a > b ? a : b;
+}
 
 namespace {
 
@@ -413,7 +433,7 @@ void launch_post(const PostNormGradArgs& a, int nb, hipStream_t s) {
 }  // namespace
 
 hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s) {
-  const int nb = blocks_of(a.T, a.H);
+  const int nb = pre_blocks(a.T, a.H);
   if (nb > 0) {
     if (a.bf16) launch_pre<bf16>(a, nb, s);
     else launch_pre<float>(a, nb, s);
@@ -426,7 +446,7 @@ hipError_t launch_pre_norms_grad(const PreNormGradArgs& a, hipStream_t s) {
 }
 
 hipError_t launch_post_norms_grad(const PostNormGradArgs& a, hipStream_t s) {
-  const int nb = blocks_of(a.T, a.H);
+  const int nb = post_blocks(a.T, a.H, a.bf16 && a.y_bf16);
   if (nb > 0) {
     if (!a.bf16) launch_post<float, float>(a, nb, s);
     else if (a.y_bf16) launch_post<bf16, bf16>(a, nb, s);
