@@ -497,6 +497,7 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void grouped_gemm_kernel(
             g *= sg[j];
             u *= su[j];
           }
+          // the down projection's operand, rounded once from fp32
           stg[r * kGuStride + c] = (bf16)(gelu_tanh(g) * u);
         }
     }
@@ -513,7 +514,9 @@ __global__ __launch_bounds__(64 * WM * WN, 1) void grouped_gemm_kernel(
         *reinterpret_cast<uint4*>(hout + (size_t)(row0 + r) * Nout + col) =
             *reinterpret_cast<const uint4*>(stg + r * kGuStride + ch * 8);
     }
-    // KEEP: the projections themselves leave the same way, gate then up
+    // KEEP: the projections themselves leave the same way, gate then up, in bf16: half of
+    // the bytes to write and keep (92 MB at 4096 tokens of 26B-A4B); h is made of the fp32
+    // ones
     if constexpr (KEEP) {
 #pragma unroll
       for (int part = 0; part < 2; ++part) {

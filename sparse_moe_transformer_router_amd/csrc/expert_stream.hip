@@ -245,8 +245,9 @@ __global__ __launch_bounds__(64 * WK) void gate_up_stream_kernel(
       for (int r = 0; r < 4; ++r) {
         const int row = row0 + 16 * mb + 4 * fg + r;
         if (row < row1 && nvalid) {
+          // the down projection's operand, rounded once from fp32
           h[(size_t)row * N + n] = (bf16)(gelu_tanh(g[r]) * u[r]);
-          if constexpr (KEEP) {
+          if constexpr (KEEP) {  // kept in bf16, half of the bytes; h is made of the fp32 ones
             keep[(size_t)row * 2 * N + n] = (bf16)g[r];
             keep[(size_t)row * 2 * N + N + n] = (bf16)u[r];
           }
