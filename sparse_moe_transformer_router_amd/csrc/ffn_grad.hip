@@ -366,9 +366,11 @@ __device__ __forceinline__ void clear(f32x16 (&acc)[TL::TM][TL::TN]) {
 // in LDS, always in the same order.
 // The experts' 128 x 256 tiles at 4096 tokens (256 rows an expert on average, so three
 // row tiles with their last ones half empty, neighbours on one XCD for their weights):
-// DU 283 us, 459 TFLOP/s, DX 388 us, 670 TFLOP/s, the matrix units busy for 0.27 and
+// DU 284 us, 457 TFLOP/s, DX 391 us, 664 TFLOP/s, the matrix units busy for 0.27 and
 // 0.41 of the time; a wave's LDS reads take nearly as long as its products, and the
-// weights (1.5 GB for the two) come from memory once.  DU's contraction of 88 k-tiles
+// weights (1.5 GB for the two) come from memory once.  (Kernel times here and below are
+// of a trace of the call alone; they differ by up to 5 % from card to card, and those
+// compared with each other are of one card.)  DU's contraction of 88 k-tiles
 // ends in an epilogue that reads the kept projections and writes 1.5 times as much; the
 // second block of the CU multiplies meanwhile.  At 64 tokens the weights bound both:
 // 90 and 128 us, 4.8 and 6.8 TB/s.
@@ -743,8 +745,8 @@ __device__ __forceinline__ int first_tile(const Operands& o, int tpe, int x) {
 // the rows' tokens: x, d_out).  Both are copied through descriptors, whose range
 // check gives zeros for rows past the expert's and for tokens that do not count.
 // PAST: the results go past the caches, where they would be written back while later
-// kernels read (gradients of 1.5 GB, the next call's DU at 64 / 4096 tokens 96 / 280 us
-// against 154 / 313).
+// kernels read (gradients of 1.5 GB, the next call's DU at 64 / 4096 tokens 90 / 284 us
+// against 93 / 298).
 template <int KIND, typename WT, typename TL, bool PAST>
 __device__ __forceinline__ void weights_block(const Operands& o, int MT, int NT, int block,
                                               int blocks, unsigned char* smem) {
@@ -1238,8 +1240,8 @@ __global__ __launch_bounds__(256) void grad_rest_f32_kernel(Operands o, F32Tiles
 }
 
 // DU and DX: 128 x 256, two blocks of 8 waves a CU; DW: 256 x 256, one block of 8
-// waves, four stages (4096 tokens, DWGU / DWDN: 471 / 261 us; 128 x 256 in two blocks
-// of 4 waves a CU 484 / 277, waves of 64 x 128 496 / 269).
+// waves, four stages (26B-A4B at 64 / 4096 tokens, DWGU + DWDN 298 / 745 us; 128 x 256 in
+// two blocks of 4 waves a CU 473 / 939, waves of 64 x 128 303 / 744).
 typedef Tile<128, 256, 2, 4, 3, 2> RowsTile;
 typedef Tile<256, 256, 2, 4, 4, 1> WeightsTile;
 // DU and DX of small problems: 64 x 64, the contraction split over 8 single waves.
@@ -1336,9 +1338,9 @@ hipError_t launch_gemm(const FfnGradArgs& a, const Operands& o, hipStream_t s) {
   } else {
     if (small_rows(a, N)) return launch_rows<KIND, WT, FewTile, kFewSplit, false>(a, o, s);
     // Up to 32 rows an expert on average most have one row tile, which reads the weights
-    // alone.  26B-A4B at 64 / 256 / 512 / 1024 / 4096 tokens, DU 90 / 107 / 130 / 152 / 329
-    // us, with copies that stay 95 / 115 / 136 / 154 / 292; DX 129 / 166 / 188 / 231 / 494
-    // and 147 / 182 / 197 / 227 / 386.
+    // alone.  26B-A4B at 64 / 256 / 512 / 1024 / 4096 tokens, DU 90 / 107 / 136 / 157 / 335
+    // us, with copies that stay 95 / 116 / 136 / 154 / 289; DX 128 / 167 / 190 / 231 / 496
+    // and 149 / 182 / 197 / 230 / 380.
     if (!a.ident && (long long)a.rows <= 32LL * a.E)
       return launch_rows<KIND, WT, RowsTile, 1, true>(a, o, s);
     return launch_rows<KIND, WT, RowsTile, 1, false>(a, o, s);
