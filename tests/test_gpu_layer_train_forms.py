@@ -1,6 +1,8 @@
 """Forms of the gated block's backward pass that its sizes and types choose: fp32 weight
 gradients of bf16 weights where a block goes through many large tiles, bf16 slots in every
 tile, many experts; against fp64, at the bounds of tests/test_gpu_ffn_train.py."""
+import ctypes
+
 import pytest
 import torch
 
@@ -126,3 +128,29 @@ def test_the_same_bits_again():
             s.backward()
             torch.cuda.synchronize()
             assert all(torch.equal(v, want[k]) for k, v in s.outputs().items())
+
+
+@pytest.mark.parametrize("bf16", [True, False], ids=["bf16", "f32"])
+def test_no_tokens_and_no_inputs(bf16):
+    """T = 0 through the library's own calls, every input NULL: the gradients of what sums
+    over tokens are zeros."""
+    L, t = lib.raw(), lib.MOE_BF16 if bf16 else lib.MOE_F32
+    d = ctypes.byref(lib.dims(128, 5, 2, 96, 64, 1e-6, t, lib.MOE_F32))
+    nan = lambda *s: torch.full(s, float("nan"), device="cuda")  # noqa: E731
+    gu, dn, gate, up, down = nan(5, 192, 128), nan(5, 128, 96), nan(64, 128), nan(64, 128), \
+        nan(128, 64)
+    g = [nan(128) for _ in range(5)]
+    scalar = nan(1)
+    p = lambda v: v.data_ptr()  # noqa: E731
+    stream = ctypes.c_void_p(torch.cuda.current_stream().cuda_stream)
+    note(f"no tokens, no inputs, bf16={bf16}")
+    assert L.moe_expert_ffn_grad(d, 0, *[None] * 11, lib.MOE_F32, p(gu), p(dn), None, 0,
+                                 stream) == lib.MOE_OK
+    assert L.gemma4_dense_mlp_grad(d, 0, *[None] * 8, lib.MOE_F32, p(gate), p(up), p(down), None,
+                                   0, stream) == lib.MOE_OK
+    assert L.gemma4_post_norms_grad(d, 0, *[None] * 6, 0.5, *[None] * 4, p(g[0]), p(g[1]), p(g[2]),
+                                    p(scalar), None, 0, stream) == lib.MOE_OK
+    assert L.gemma4_pre_norms_grad(d, 0, *[None] * 8, 0.5, None, p(g[3]), p(g[4]), None, 0,
+                                   stream) == lib.MOE_OK
+    torch.cuda.synchronize()
+    assert all((v == 0).all() for v in (gu, dn, gate, up, down, *g, scalar))
