@@ -6,8 +6,12 @@ tokens: route (router + dispatch) -> expert gate_up -> expert down -> combine,
 each a call into libmoe (the C ABI) on the current stream.  The workload is the 26B-A4B
 layer's experts (128 experts, top-8, hidden 2816, expert intermediate 704,
 bf16 weights, fp32 router) at a decode batch of 64 tokens; batches of 1, 8 and
-32 and a 4096-token prefill are measured the same way and reported in the same
-line.
+32 and a 4096-token prefill are measured the same way.
+
+Standard output is one JSON line: the headline, its roofline and baseline, and the
+time and rate of every other leg.  The whole record (22 KB: kernel times, shares of
+the peaks, expert loads, clocks) goes to standard error before it, as one line that
+starts with "bench record: ".
 
 Inputs are seeded and synthetic: x ~ N(0,1) bf16, gate_up / down ~ N(0, 0.02)
 bf16, router weight N(0, 0.02) fp32, router_scale = 1, per_expert_scale ~
@@ -19,7 +23,7 @@ would hold one copy of the weights a small batch touches, so the steps rotate
 over several weight copies and several input batches: every step streams its
 experts from HBM.
 
-Also reported in the same line: the tiny fp32 configuration (16 tokens,
+Also measured: the tiny fp32 configuration (16 tokens,
 hidden 64, 8 experts, top-2); the whole FFN block (pre-norms, router on the
 normed input, experts, gated dense MLP of width 2112, five norms, residual,
 layer scalar) at 2048 tokens; and a stack of 30 independently seeded blocks
@@ -1039,6 +1043,30 @@ def traffic_from_profile():
     return rec.get("bytes_per_launch") if rec.get("kernel_src_sha256") == sha else None
 
 
+# What of the record the line holds as it is; of the legs it holds brief().
+HEADLINE = ("metric", "value", "unit", "n_gpus", "steps", "warmup", "clock_warmup", "ms_per_step",
+            "higher_is_better", "scaling", "vs_baseline", "dtype", "data", "config", "roofline",
+            "cpu_baseline", "achievable")
+
+
+def brief(leg):
+    """Times and rates of a leg and of the legs inside it, to five digits; {} if none."""
+    if "tokens_per_s" in leg:
+        return {k: float(f"{leg[k]:.5g}") for k in ("ms_per_step", "ms", "tokens_per_s")
+                if k in leg}
+    inside = {k: brief(v) for k, v in leg.items() if isinstance(v, dict)}
+    return {k: v for k, v in inside.items() if v}
+
+
+def short_line(record):
+    """The line of standard output: readers that keep the last few thousand characters of
+    it find it whole."""
+    line = {k: record[k] for k in HEADLINE}
+    legs = brief({k: v for k, v in record.items()
+                  if k not in HEADLINE and k != "cpu_oracle_other_configs"})
+    return {**line, "legs": legs}
+
+
 def main():
     args = parse()
     world = int(os.environ.get("WORLD_SIZE", "1"))
@@ -1177,7 +1205,7 @@ def main():
         done("cpu baselines")
 
     achieved = head["gate_up_gbs"]
-    line = {
+    record = {
         "metric": METRIC,
         "value": head["tokens_per_s"],
         "unit": "tokens/s",
@@ -1216,7 +1244,8 @@ def main():
         "stack": stack,
         "cpu_oracle_other_configs": cpu_configs,
     }
-    print(json.dumps(line), flush=True)
+    print("bench record: " + json.dumps(record), file=sys.stderr, flush=True)
+    print(json.dumps(short_line(record)), flush=True)
 
 
 if __name__ == "__main__":
