@@ -82,7 +82,7 @@ typedef enum moe_status {
   MOE_ERR_HIP = -4           /* a HIP launch reported an error */
 } moe_status;
 
-/* Storage formats of expert weights below bf16 (batches of up to 256 tokens):
+/* Storage formats of expert weights below bf16:
  *   MOE_W_INT8   int8 codes, one fp32 scale per output channel;
  *   MOE_W_FP8    E4M3 codes (OCP 8-bit floating point: bias 7, no
  *                infinities, largest finite 448), one fp32 scale per output

@@ -14,9 +14,6 @@
 
 namespace {
 
-// Quantized experts run on the weight-streaming kernels only, which pay up to
-// about 16 rows per expert (256 tokens at top-8 of 128 experts).
-
 thread_local std::string g_err;
 
 int fail(int code, const char* fmt, ...) {
